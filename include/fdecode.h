@@ -247,6 +247,132 @@ FD_API fd_status fd_attend(const float* q, int32_t n_q, int32_t causal, const fd
                            int32_t max_seq_len, int32_t D, float scale, int32_t n_splits, void* workspace,
                            size_t workspace_bytes, void* stream, int32_t* backend);
 
+/* ------------------------------------------------------------------ rotating append
+ *
+ * New rows of every sequence into a KV cache, their keys (and the queries)
+ * rotated by position on the way.  The sources name appending to paged caches
+ * ("FlashDecoding and split-KV", section "Walking through it") without a
+ * format; these calls are this library's reading, and what stands before
+ * fd_decode, fd_decode_rows, fd_prefill or fd_decode_kv4 in a serving loop.
+ *
+ * A pair (a, b) of channels of a q or k row at position p turns into
+ *     a cos[p, i] - b sin[p, i],   b cos[p, i] + a sin[p, i],
+ * in fp32, for the rot_dim / 2 pairs i of the first rot_dim channels: (i, i +
+ * rot_dim / 2), or (2i, 2i + 1) when interleaved.  The other channels, and v,
+ * are taken as they are.  k and v are rounded once to the cache's type; q comes
+ * out in fp32 as [B, Hq, n, D], which the attention calls take.
+ *
+ * Every sequence brings n rows; with new_lens, only the last new_lens[b] of them
+ * are tokens (the convention of fd_decode_rows, whose rows are the last ones of
+ * the sequence), and the padding rows before them are neither read nor written,
+ * in q_out too.  Token j of sequence b goes to place L_b + j of its cache, L_b being
+ * the length before the call (seq_lens is read, not updated).  Its row of the
+ * tables is that place, or positions[b, i] of its row i when given (a tree of drafts, a
+ * sequence whose positions do not start at zero).
+ */
+typedef struct fd_new_rows {
+  fd_dtype dtype;               /* of q, k and v: FD_BF16 or FD_F32 */
+  const void* q;                /* [B, n, Hq, D] by strides; unused when Hq = 0 */
+  const void* k;                /* [B, n, Hkv, D] by strides */
+  const void* v;
+  int64_t q_stride[3];          /* elements from batch to batch, row to row, head to head; the D */
+  int64_t k_stride[3];          /*   channels of a head are contiguous.  Bases and strides are */
+  int64_t v_stride[3];          /*   multiples of 16 bytes; a stride may be 0 (a broadcast input) */
+  const int32_t* new_lens;      /* [B] rows that are tokens, or NULL (= n); clamped to [0, n] */
+  const int32_t* positions;     /* [B, n] or NULL */
+  const float* cos;             /* [max_pos, rot_dim / 2]; may be NULL when rot_dim = 0 */
+  const float* sin;
+  int32_t max_pos;              /* rows of the tables */
+  int32_t rot_dim;              /* 0 (no rotation) or a multiple of 32 up to D */
+  int32_t interleaved;          /* 0 or 1 */
+} fd_new_rows;
+
+/*
+ * Append into a bf16 or fp32 cache (kv->k and kv->v are written).
+ *   seq_lens / max_seq_len  lengths BEFORE the append, or NULL (= every L_b is
+ *             max_seq_len); the cache must hold max_seq_len + n tokens, and without
+ *             `positions` so must the tables.
+ *   workspace at least 256 bytes, zero-filled once: its first word is the
+ *             error word that fd_workspace_status reads; nothing else of it is used,
+ *             so a call may share it with any other.  A page outside [0, num_pages)
+ *             (that k and v row is not written) or a position outside [0, max_pos)
+ *             (nor is that q row) is reported as FD_ERR_BAD_INDEX.
+ * One launch.  Two sequences of one call must not bring tokens to the same place
+ * of the same page: which of the two stays is not defined.
+ */
+FD_API fd_status fd_append_rope(const fd_new_rows* rows, const fd_kv_desc* kv, float* q_out, int32_t B, int32_t n,
+                                int32_t Hq, int32_t Hkv, const int32_t* seq_lens, int32_t max_seq_len, int32_t D,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------ 4-bit KV cache
+ *
+ * e2m1 codes (sign, two exponent bits, one mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4,
+ * 6) with one e4m3 scale for every sixteen consecutive channels of a token:
+ *     value = code * scale * 2^exp,     exp = k_exp for K, v_exp for V.
+ * Writing x: y = x * 2^-exp; scale = the largest |y| of the sixteen / 6, rounded to
+ * nearest (even) and held to 448; code = y / scale rounded to nearest (even) and
+ * held to 6 in size (0 where the scale is 0).  An infinity so becomes 6 * 448 * 2^exp; a NaN
+ * makes the scale, and with it the sixteen values, NaN.
+ *
+ * The unit of storage is the block of sixteen consecutive tokens of one KV head,
+ * fd_kv4_block_bytes(D) = 18 D bytes:
+ *     K codes  [16 tokens][D / 2], two channels a byte, the even one in the low
+ *              nibble; 16-byte chunk c of row t sits at chunk c ^ ((t / 2) % 4) for
+ *              D = 128, c ^ ((t / 4) % 2) for D = 64;
+ *     V codes  [D][8], two tokens a byte, the even one in the low nibble;
+ *     K scales [16][D / 16];   V scales [D / 16][16].
+ * Contiguous: [B, Hkv, capacity / 16] blocks.  Paged: [num_pages, Hkv, page_size /
+ * 16] blocks.  kv must be 16-byte aligned.  Bytes of a block that no token was
+ * written to are read but never reach a result.
+ */
+typedef struct fd_kv4_desc {
+  fd_kv_layout layout;
+  void* kv;
+  int64_t capacity;             /* contiguous: tokens per sequence, a multiple of 16 */
+  const int32_t* block_table;   /* paged only: [B, max_pages_per_seq] */
+  int32_t max_pages_per_seq;
+  int32_t page_size;            /* a multiple of 16 */
+  int32_t num_pages;
+  int32_t k_exp, v_exp;         /* in [-64, 64] */
+} fd_kv4_desc;
+
+/* 18 D for D = 64 or 128, else 0. */
+FD_API int32_t fd_kv4_block_bytes(int32_t D);
+
+/*
+ * fd_append_rope into a 4-bit cache.  The sixteen channels of a scale are taken
+ * after the rotation.  A block is written by one sequence at a time: besides
+ * the rule above, two sequences of one call must not bring tokens to the same
+ * block.  A page outside [0, num_pages) leaves out the block's tokens.
+ */
+FD_API fd_status fd_append_rope_kv4(const fd_new_rows* rows, const fd_kv4_desc* kv, float* q_out, int32_t B, int32_t n,
+                                    int32_t Hq, int32_t Hkv, const int32_t* seq_lens, int32_t max_seq_len, int32_t D,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Rows of a 4-bit cache as bf16 or fp32 values: for every sequence the tokens
+ * t = starts[b] + i, i < n, that lie below L_b, to row i of k_out and v_out [B, Hkv,
+ * n, D] (16-byte aligned).  Rows at or past L_b are left as they were.  starts NULL
+ * = 0; starts and lengths are clamped to [0, max_seq_len].  bf16 holds every value exactly
+ * (fp32 too).  A page outside the pool leaves its rows out and is reported as
+ * FD_ERR_BAD_INDEX.  Workspace as for fd_append_rope.
+ */
+FD_API fd_status fd_kv4_read(const fd_kv4_desc* kv, void* k_out, void* v_out, fd_dtype dtype, int32_t B, int32_t n,
+                             int32_t Hkv, const int32_t* starts, const int32_t* seq_lens, int32_t max_seq_len,
+                             int32_t D, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Decode attention over a 4-bit cache, 1 <= n_q <= 64 query rows per (batch,
+ * head): fd_decode_rows (n_q = 1: fd_decode) on the cache's values, with the same layouts of
+ * q, out and lse, the same masking, lengths and split arguments, and a workspace of
+ * fd_workspace_bytes(B, Hq * n_q, Hkv, D, n_splits, 0) bytes.  A page outside the pool
+ * counts as keys with score 0 and value 0, and is reported as FD_ERR_BAD_INDEX.
+ */
+FD_API fd_status fd_decode_kv4(const float* q, int32_t n_q, int32_t causal, const fd_kv4_desc* kv, float* out,
+                               float* lse, int32_t B, int32_t Hq, int32_t Hkv, const int32_t* seq_lens,
+                               int32_t max_seq_len, int32_t D, float scale, int32_t n_splits, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
 /*
  * Split step only ("fd_split" of the walkthrough), with n_splits > 0 splits
  * per sequence of fd_split_size(max_seq_len, n_splits) tokens each.  Writes:

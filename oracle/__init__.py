@@ -7,3 +7,4 @@ CUDA library or its Python binding.  See ``fd_oracle`` for what it computes.
 
 from .fd_oracle import *  # noqa: F401,F403
 from .fd_oracle import __all__  # noqa: F401
+from . import kv4_oracle as kv4  # noqa: F401

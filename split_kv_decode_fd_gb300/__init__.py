@@ -9,13 +9,21 @@ from .fdecode import (  # noqa: F401
     FD_SPLITS_AUTO,
     FdError,
     HostDecoder,
+    Kv4Desc,
     KvDesc,
+    NewRows,
     Workspace,
     combine,
     decode,
     decode_host,
     decode_rows,
     append_decode,
+    append_rope,
+    append_rope_kv4,
+    decode_kv4,
+    kv4_block_bytes,
+    kv4_cache,
+    kv4_read,
     prefill,
     attend,
     attend_backend,

@@ -11,6 +11,7 @@
 
 #include "../../include/fdecode.h"
 #include "fd_internal.h"
+#include "fd_kv4.h"
 #include "fd_prefill.h"
 #include "fd_split.cuh"
 
@@ -779,3 +780,219 @@ extern "C" fd_status fd_static_status(void* stream) {
   // the workspace header
   return fd_workspace_status(base, kHeaderBytes, stream);
 }
+
+// --------------------------------------------------------------------------
+// The 4-bit cache and the rotating append.
+namespace {
+
+fd_status check_kv4(const fd_kv4_desc* kv, int B, int Hkv, int D, int64_t max_len, Kv4View* out) {
+  if (!kv || !kv->kv || !aligned16(kv->kv)) return FD_ERR_INVALID_ARG;
+  if (max_len < 0) return FD_ERR_INVALID_ARG;
+  if (kv->k_exp < -kKv4MaxExp || kv->k_exp > kKv4MaxExp || kv->v_exp < -kKv4MaxExp || kv->v_exp > kKv4MaxExp)
+    return FD_ERR_INVALID_ARG;
+  const int64_t tiles = (int64_t)B * Hkv * ((max_len + kPlanTile - 1) / kPlanTile);
+  if (tiles >= ((int64_t)1 << 31) / kMaxGroupBf16) return FD_ERR_UNSUPPORTED;
+  Kv4View v;
+  std::memset(&v, 0, sizeof(v));
+  v.kv = static_cast<uint8_t*>(kv->kv);
+  v.Hkv = Hkv;
+  v.k_exp = kv->k_exp;
+  v.v_exp = kv->v_exp;
+  if (kv->layout == FD_KV_CONTIGUOUS) {
+    if (kv->capacity < 1 || kv->capacity % kKv4Tokens != 0 || kv->capacity < max_len) return FD_ERR_INVALID_ARG;
+    if (kv->capacity > INT32_MAX) return FD_ERR_UNSUPPORTED;
+    v.cap_blocks = kv->capacity / kKv4Tokens;
+  } else if (kv->layout == FD_KV_PAGED) {
+    if (!kv->block_table || kv->page_size < kKv4Tokens || kv->page_size % kKv4Tokens != 0 || kv->num_pages < 1 ||
+        kv->max_pages_per_seq < 1)
+      return FD_ERR_INVALID_ARG;
+    if ((int64_t)kv->max_pages_per_seq * kv->page_size < max_len) return FD_ERR_INVALID_ARG;
+    v.paged = 1;
+    v.block_table = kv->block_table;
+    v.page_size = kv->page_size;
+    v.max_pages = kv->max_pages_per_seq;
+    v.num_pages = kv->num_pages;
+  } else {
+    return FD_ERR_INVALID_ARG;
+  }
+  *out = v;
+  return FD_OK;
+}
+
+bool strides16(const void* p, const int64_t (&s)[3], int es) {
+  if (!aligned16(p)) return false;
+  for (const int64_t x : s)
+    if (x < 0 || x * es % 16 != 0) return false;
+  return true;
+}
+
+// The arguments that both appends share; fills `out`.
+fd_status check_rows(const fd_new_rows* rows, float* q_out, int B, int n, int Hq, int Hkv, const int32_t* seq_lens,
+                     int max_seq_len, int D, void* workspace, size_t workspace_bytes, NewRows* out) {
+  if (!rows || B < 1 || n < 1 || Hkv < 1 || Hq < 0 || max_seq_len < 0) return FD_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return FD_ERR_UNSUPPORTED;
+  if (rows->dtype != FD_F32 && rows->dtype != FD_BF16) return FD_ERR_UNSUPPORTED;
+  const int es = rows->dtype == FD_F32 ? 4 : 2;
+  if (!rows->k || !rows->v || !strides16(rows->k, rows->k_stride, es) || !strides16(rows->v, rows->v_stride, es))
+    return FD_ERR_INVALID_ARG;
+  if (Hq > 0 && (!rows->q || !q_out || !aligned16(q_out) || !strides16(rows->q, rows->q_stride, es)))
+    return FD_ERR_INVALID_ARG;
+  if (rows->rot_dim < 0 || rows->rot_dim > D || (rows->interleaved != 0 && rows->interleaved != 1))
+    return FD_ERR_INVALID_ARG;
+  if (rows->rot_dim % 32 != 0) return FD_ERR_UNSUPPORTED;
+  const int64_t last = (int64_t)max_seq_len + n;
+  if (last > INT32_MAX) return FD_ERR_UNSUPPORTED;
+  if (rows->rot_dim > 0) {
+    if (!rows->cos || !rows->sin || !aligned16(rows->cos) || !aligned16(rows->sin) || rows->max_pos < 1)
+      return FD_ERR_INVALID_ARG;
+    if (!rows->positions && last > rows->max_pos) return FD_ERR_INVALID_ARG;
+  }
+  if ((int64_t)B * n * ((int64_t)Hq + 2 * (int64_t)Hkv) > INT32_MAX) return FD_ERR_UNSUPPORTED;
+  if (!workspace || !aligned16(workspace)) return FD_ERR_INVALID_ARG;
+  if (workspace_bytes < kHeaderBytes) return FD_ERR_WORKSPACE_TOO_SMALL;
+  NewRows r;
+  std::memset(&r, 0, sizeof(r));
+  r.q = rows->q;
+  r.k = rows->k;
+  r.v = rows->v;
+  for (int i = 0; i < 3; ++i) {
+    r.qs[i] = rows->q_stride[i];
+    r.ks[i] = rows->k_stride[i];
+    r.vs[i] = rows->v_stride[i];
+  }
+  r.new_lens = rows->new_lens;
+  r.positions = rows->positions;
+  r.cos = rows->cos;
+  r.sin = rows->sin;
+  r.max_pos = rows->max_pos;
+  r.rot = rows->rot_dim;
+  r.interleaved = rows->interleaved;
+  r.seq_lens = seq_lens;
+  r.max_len = max_seq_len;
+  r.B = B;
+  r.n = n;
+  r.Hq = Hq;
+  r.q_out = q_out;
+  r.err = reinterpret_cast<unsigned*>(workspace);
+  *out = r;
+  return FD_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int32_t fd_kv4_block_bytes(int32_t D) { return D == 64 || D == 128 ? kv4_block_bytes(D) : 0; }
+
+fd_status fd_append_rope(const fd_new_rows* rows, const fd_kv_desc* kv, float* q_out, int32_t B, int32_t n, int32_t Hq,
+                         int32_t Hkv, const int32_t* seq_lens, int32_t max_seq_len, int32_t D, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  NewRows r;
+  fd_status st = check_rows(rows, q_out, B, n, Hq, Hkv, seq_lens, max_seq_len, D, workspace, workspace_bytes, &r);
+  if (st != FD_OK) return st;
+  if ((st = check_kv(kv, B, Hkv, max_seq_len + n)) != FD_OK) return st;
+  KvView v;
+  std::memset(&v, 0, sizeof(v));
+  v.k = const_cast<void*>(kv->k);
+  v.v = const_cast<void*>(kv->v);
+  v.block_table = kv->block_table;
+  v.capacity = kv->capacity;
+  v.Hkv = Hkv;
+  v.paged = kv->layout == FD_KV_PAGED;
+  v.page_size = kv->page_size;
+  v.max_pages = kv->max_pages_per_seq;
+  v.num_pages = kv->num_pages;
+  return launch_append(D, rows->dtype == FD_F32, kv->dtype == FD_F32, r, v, (cudaStream_t)stream) == cudaSuccess
+             ? FD_OK
+             : FD_ERR_CUDA;
+}
+
+fd_status fd_append_rope_kv4(const fd_new_rows* rows, const fd_kv4_desc* kv, float* q_out, int32_t B, int32_t n,
+                             int32_t Hq, int32_t Hkv, const int32_t* seq_lens, int32_t max_seq_len, int32_t D,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+  NewRows r;
+  fd_status st = check_rows(rows, q_out, B, n, Hq, Hkv, seq_lens, max_seq_len, D, workspace, workspace_bytes, &r);
+  if (st != FD_OK) return st;
+  Kv4View v;
+  if ((st = check_kv4(kv, B, Hkv, D, (int64_t)max_seq_len + n, &v)) != FD_OK) return st;
+  return launch_append_kv4(D, rows->dtype == FD_F32, r, v, (cudaStream_t)stream) == cudaSuccess ? FD_OK : FD_ERR_CUDA;
+}
+
+fd_status fd_kv4_read(const fd_kv4_desc* kv, void* k_out, void* v_out, fd_dtype dtype, int32_t B, int32_t n,
+                      int32_t Hkv, const int32_t* starts, const int32_t* seq_lens, int32_t max_seq_len, int32_t D,
+                      void* workspace, size_t workspace_bytes, void* stream) {
+  if (B < 1 || n < 1 || Hkv < 1 || !k_out || !v_out || !aligned16(k_out) || !aligned16(v_out))
+    return FD_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return FD_ERR_UNSUPPORTED;
+  if (dtype != FD_F32 && dtype != FD_BF16) return FD_ERR_UNSUPPORTED;
+  if (!workspace || !aligned16(workspace)) return FD_ERR_INVALID_ARG;
+  if (workspace_bytes < kHeaderBytes) return FD_ERR_WORKSPACE_TOO_SMALL;
+  Kv4View v;
+  fd_status st = check_kv4(kv, B, Hkv, D, max_seq_len, &v);
+  if (st != FD_OK) return st;
+  Kv4Read r;
+  r.k_out = k_out;
+  r.v_out = v_out;
+  r.starts = starts;
+  r.seq_lens = seq_lens;
+  r.max_len = max_seq_len;
+  r.B = B;
+  // rows past max_seq_len do not exist
+  r.n = n;
+  r.err = reinterpret_cast<unsigned*>(workspace);
+  return launch_kv4_read(D, dtype == FD_F32, r, v, (cudaStream_t)stream) == cudaSuccess ? FD_OK : FD_ERR_CUDA;
+}
+
+fd_status fd_decode_kv4(const float* q, int32_t n_q, int32_t causal, const fd_kv4_desc* kv, float* out, float* lse,
+                        int32_t B, int32_t Hq, int32_t Hkv, const int32_t* seq_lens, int32_t max_seq_len, int32_t D,
+                        float scale, int32_t n_splits, void* workspace, size_t workspace_bytes, void* stream) {
+  if (n_q < 1 || n_q > 64 || (causal != 0 && causal != 1)) return FD_ERR_INVALID_ARG;
+  if (Hq < 1 || (int64_t)Hq * n_q > ((int64_t)1 << 24)) return FD_ERR_INVALID_ARG;
+  Hq *= n_q;  // rows are served as virtual heads
+  fd_status st = check_shape(B, Hq, Hkv, D);
+  if (st != FD_OK) return st;
+  if ((Hq / n_q) % Hkv != 0) return FD_ERR_INVALID_ARG;
+  if (!q || !out || !workspace || !aligned16(q) || !aligned16(out) || !aligned16(workspace))
+    return FD_ERR_INVALID_ARG;
+  if (n_splits < 0 || n_splits > 65535) return FD_ERR_INVALID_ARG;
+  Kv4View v;
+  if ((st = check_kv4(kv, B, Hkv, D, max_seq_len, &v)) != FD_OK) return st;
+  fd_kv_desc as;  // what the shared parameters read of a cache
+  std::memset(&as, 0, sizeof(as));
+  as.layout = kv->layout;
+  as.dtype = FD_BF16;
+  as.block_table = kv->block_table;
+  as.page_size = kv->page_size;
+  as.max_pages_per_seq = kv->max_pages_per_seq;
+  as.num_pages = kv->num_pages;
+  const Groups gr = make_groups(Hq, Hkv, kMaxGroupBf16);
+  const int64_t pairs = (int64_t)B * gr.hv;
+  int sms = 0;
+  if (n_splits == 0) {
+    if (!sm_count(&sms)) return FD_ERR_CUDA;
+    n_splits = fallback_splits(B, gr.hv, max_seq_len, sms);
+    if (B <= FD_AUTO_MAX_BATCH && pairs <= kMaxFusedPairs)  // as many states as the balanced plan's workspace holds
+      n_splits = (int)std::max<int64_t>(1, std::min<int64_t>(n_splits, (sms + pairs) * gr.gpad / ((int64_t)B * Hq)));
+  }
+  const WsLayout w = ws_layout(B, Hq, Hkv, D, n_splits, sms, kMaxGroupBf16);
+  if (workspace_bytes < w.total) return FD_ERR_WORKSPACE_TOO_SMALL;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  SplitParams p = base_params(q, &as, B, Hq, Hkv, seq_lens, max_seq_len, scale);
+  p.n_q = n_q;
+  p.causal = causal;
+  p.out = out;
+  p.lse = lse;
+  p.o_part = reinterpret_cast<float*>(ws + w.o);
+  p.m_part = reinterpret_cast<float*>(ws + w.m);
+  p.l_part = reinterpret_cast<float*>(ws + w.l);
+  p.err = reinterpret_cast<unsigned*>(ws + w.err);
+  p.n_splits = n_splits;
+  p.split_tokens = max_seq_len > 0 ? explicit_split_size(max_seq_len, n_splits) : kSplitAlign;
+  const dim3 grid((unsigned)pairs, (unsigned)n_splits, 1);
+  cudaStream_t s = (cudaStream_t)stream;
+  if (launch_kv4_split(D, v, p, grid, s) != cudaSuccess) return FD_ERR_CUDA;
+  const cudaError_t e = launch_combine(D, p.o_part, p.m_part, p.l_part, out, lse, B * Hq, n_splits, s);
+  return e == cudaSuccess ? FD_OK : FD_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -18,6 +18,7 @@ import numpy as np
 __all__ = [
     "FdError", "KvDesc", "library_path", "load_library", "workspace_bytes", "split_size", "plan_pieces",
     "Workspace", "decode", "decode_rows", "append_decode", "prefill", "attend", "attend_backend", "decode_host", "HostDecoder", "decode_static", "static_status", "split_partial", "combine", "workspace_status",
+    "NewRows", "Kv4Desc", "append_rope", "append_rope_kv4", "kv4_block_bytes", "kv4_cache", "kv4_read", "decode_kv4",
 ]
 
 FD_OK, FD_ERR_INVALID_ARG, FD_ERR_UNSUPPORTED, FD_ERR_WORKSPACE_TOO_SMALL = 0, 1, 2, 3
@@ -53,6 +54,43 @@ class KvDesc(ctypes.Structure):
     ]
 
 
+class NewRows(ctypes.Structure):
+    """``fd_new_rows``: the rows an append brings."""
+
+    _fields_ = [
+        ("dtype", ctypes.c_int),
+        ("q", ctypes.c_void_p),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("q_stride", ctypes.c_int64 * 3),
+        ("k_stride", ctypes.c_int64 * 3),
+        ("v_stride", ctypes.c_int64 * 3),
+        ("new_lens", ctypes.c_void_p),
+        ("positions", ctypes.c_void_p),
+        ("cos", ctypes.c_void_p),
+        ("sin", ctypes.c_void_p),
+        ("max_pos", ctypes.c_int32),
+        ("rot_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+    ]
+
+
+class Kv4Desc(ctypes.Structure):
+    """``fd_kv4_desc``: a 4-bit cache."""
+
+    _fields_ = [
+        ("layout", ctypes.c_int),
+        ("kv", ctypes.c_void_p),
+        ("capacity", ctypes.c_int64),
+        ("block_table", ctypes.c_void_p),
+        ("max_pages_per_seq", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32),
+        ("k_exp", ctypes.c_int32),
+        ("v_exp", ctypes.c_int32),
+    ]
+
+
 def library_path() -> str:
     return os.environ.get("FDECODE_LIB", os.path.join(_HERE, "libfdecode.so"))
 
@@ -69,7 +107,7 @@ def load_library(path: Optional[str] = None):
                                "`python split_kv_decode_fd_gb300/build.py`")
         lib = ctypes.CDLL(path)
         c_i32, c_i64, c_sz, vp, f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_float
-        kvp = ctypes.POINTER(KvDesc)
+        kvp, kv4p = ctypes.POINTER(KvDesc), ctypes.POINTER(Kv4Desc)
         sig = {
             "fd_workspace_bytes": (c_sz, [c_i32, c_i32, c_i32, c_i32, c_i32, c_i32]),
             "fd_workspace_init": (ctypes.c_int, [vp, c_sz, vp]),
@@ -99,6 +137,15 @@ def load_library(path: Optional[str] = None):
             "fd_status_string": (ctypes.c_char_p, [ctypes.c_int]),
             "fd_version": (c_i32, []),
             "fd_debug_stall": (None, [c_i32, c_i64]),
+            "fd_kv4_block_bytes": (c_i32, [c_i32]),
+            "fd_append_rope": (ctypes.c_int, [ctypes.POINTER(NewRows), kvp, vp, c_i32, c_i32, c_i32, c_i32, vp, c_i32,
+                                              c_i32, vp, c_sz, vp]),
+            "fd_append_rope_kv4": (ctypes.c_int, [ctypes.POINTER(NewRows), kv4p, vp, c_i32, c_i32, c_i32, c_i32, vp,
+                                                  c_i32, c_i32, vp, c_sz, vp]),
+            "fd_kv4_read": (ctypes.c_int, [kv4p, vp, vp, ctypes.c_int, c_i32, c_i32, c_i32, vp, vp, c_i32, c_i32, vp,
+                                           c_sz, vp]),
+            "fd_decode_kv4": (ctypes.c_int, [vp, c_i32, c_i32, kv4p, vp, vp, c_i32, c_i32, c_i32, vp, c_i32, c_i32,
+                                             f32, c_i32, vp, c_sz, vp]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -562,3 +609,270 @@ def workspace_status(workspace: Optional[Workspace] = None, device=None, stream=
     if ws.buf is None:
         return FD_OK
     return int(_lib().fd_workspace_status(ws.buf.data_ptr(), ws.buf.numel(), _stream_handle(ws.buf.device, stream)))
+
+
+# ------------------------------------------------------------------ rotating append, 4-bit cache
+def _opt(t, name, dtype, device, shape=None):
+    """Pointer of an optional contiguous tensor on ``device``; None without one."""
+    if t is None:
+        return None
+    _need_cuda(t, name, dtype)
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _scratch(workspace, device, nbytes):
+    """The workspace's buffer.  It is not made during a stream capture: its first
+    zero-fill would then run only with the graph."""
+    ws = workspace or _default_workspace(device)
+    buf = ws.buf
+    if buf is None or buf.numel() < nbytes or buf.device != device:
+        if _torch().cuda.is_current_stream_capturing():
+            raise RuntimeError("the workspace is too small and cannot grow during a stream capture: run the call once "
+                               "before the capture, or pass a Workspace that has been used at this size")
+        buf = ws.get(nbytes, device)
+    return buf
+
+
+def _launch(device, fn, where, *args):
+    """Call ``fn`` with ``device`` current (the library launches on the current device)."""
+    torch = _torch()
+    if device.index == torch.cuda.current_device():
+        st = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args)
+    if st != FD_OK:
+        raise FdError(st, where)
+
+
+def kv4_block_bytes(D: int) -> int:
+    """Bytes of one block (sixteen tokens of one KV head) of a 4-bit cache."""
+    n = int(_lib().fd_kv4_block_bytes(int(D)))
+    if n == 0:
+        raise FdError(FD_ERR_UNSUPPORTED, "fd_kv4_block_bytes")
+    return n
+
+
+def kv4_cache(n, Hkv, tokens, D, device="cuda"):
+    """A zeroed 4-bit cache: uint8 ``[n, Hkv, tokens / 16, 18 * D]``.
+
+    Contiguous caches hold ``n`` sequences of ``tokens`` tokens, paged ones ``n`` pages.
+    """
+    if tokens % 16:
+        raise ValueError("tokens must be a multiple of 16")
+    return _torch().zeros((n, Hkv, tokens // 16, kv4_block_bytes(D)), dtype=_torch().uint8, device=device)
+
+
+def _kv4_desc(kv4, block_table, B, k_exp, v_exp):
+    """Descriptor, Hkv, D and tokens per sequence of a 4-bit cache tensor."""
+    torch = _torch()
+    _need_cuda(kv4, "kv4", torch.uint8)
+    if kv4.dim() != 4 or kv4.shape[3] not in (18 * 64, 18 * 128):
+        raise ValueError("kv4 must be uint8 [n, Hkv, tokens / 16, 18 * D] with D = 64 or 128")
+    d = Kv4Desc()
+    d.kv = kv4.data_ptr()
+    d.k_exp, d.v_exp = int(k_exp), int(v_exp)
+    tokens = kv4.shape[2] * 16
+    if block_table is None:
+        if kv4.shape[0] != B:
+            raise ValueError(f"a contiguous kv4 must hold {B} sequences, got {kv4.shape[0]}")
+        d.layout = FD_KV_CONTIGUOUS
+        d.capacity = tokens
+    else:
+        d.block_table = _opt(block_table, "block_table", torch.int32, kv4.device)
+        if block_table.dim() != 2 or block_table.shape[0] != B:
+            raise ValueError(f"block_table must be [{B}, max_pages]")
+        d.layout = FD_KV_PAGED
+        d.max_pages_per_seq = block_table.shape[1]
+        d.page_size = tokens
+        d.num_pages = kv4.shape[0]
+        tokens *= block_table.shape[1]
+    return d, kv4.shape[1], kv4.shape[3] // 18, tokens
+
+
+def _head_rows(t, name, B, n, D, device, dtype):
+    """Strides of ``t`` [B, n, heads, D], whose channels are contiguous."""
+    if not isinstance(t, _torch().Tensor) or not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 4 or t.shape[0] != B or t.shape[1] != n or t.shape[3] != D:
+        raise ValueError(f"{name} must be [{B}, {n}, heads, {D}], got {tuple(t.shape)}")
+    st = t.stride()
+    if st[3] != 1:
+        raise ValueError(f"the channels of {name} must be contiguous")
+    return st[0], st[1], st[2]
+
+
+def _append_args(k_new, v_new, Hkv, D, tokens, device, cos, sin, q, q_out, rot_dim, interleaved, positions, new_lens,
+                 seq_lens, max_seq_len):
+    torch = _torch()
+    if not isinstance(k_new, torch.Tensor) or k_new.dim() != 4:
+        raise ValueError("k_new must be [B, n, Hkv, D]")
+    B, n = k_new.shape[0], k_new.shape[1]
+    dt = {torch.bfloat16: FD_BF16, torch.float32: FD_F32}.get(k_new.dtype)
+    if dt is None:
+        raise ValueError(f"unsupported dtype of the new rows {k_new.dtype}")
+    r = NewRows()
+    r.dtype = dt
+    r.k_stride[:] = _head_rows(k_new, "k_new", B, n, D, device, k_new.dtype)
+    r.v_stride[:] = _head_rows(v_new, "v_new", B, n, D, device, k_new.dtype)
+    if k_new.shape[2] != Hkv or v_new.shape[2] != Hkv:
+        raise ValueError(f"k_new and v_new must have the cache's {Hkv} heads")
+    r.k, r.v = k_new.data_ptr(), v_new.data_ptr()
+    Hq = 0
+    if q is not None:
+        r.q_stride[:] = _head_rows(q, "q", B, n, D, device, k_new.dtype)
+        Hq = q.shape[2]
+        r.q = q.data_ptr()
+        if q_out is None:
+            # rows that new_lens leaves out are not written: they start as zeros
+            make = torch.empty if new_lens is None and positions is None else torch.zeros
+            q_out = make((B, Hq, n, D), dtype=torch.float32, device=device)
+        else:
+            _opt(q_out, "q_out", torch.float32, device, (B, Hq, n, D))
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin come together")
+    if cos is not None:
+        if cos.dim() != 2 or cos.shape != sin.shape:
+            raise ValueError("cos and sin must be [max_pos, rot_dim / 2]")
+        r.cos, r.sin = _opt(cos, "cos", torch.float32, device), _opt(sin, "sin", torch.float32, device)
+        r.max_pos, r.rot_dim = cos.shape[0], 2 * cos.shape[1]
+    if rot_dim is not None and rot_dim != r.rot_dim:
+        raise ValueError(f"rot_dim {rot_dim} does not fit tables of {r.rot_dim // 2} pairs")
+    r.interleaved = int(bool(interleaved))
+    r.new_lens = _opt(new_lens, "new_lens", torch.int32, device, (B,))
+    r.positions = _opt(positions, "positions", torch.int32, device, (B, n))
+    lens = _opt(seq_lens, "seq_lens", torch.int32, device, (B,))
+    if max_seq_len is None:
+        max_seq_len = tokens - n
+    return r, B, n, Hq, lens, int(max_seq_len), q_out
+
+
+def append_rope(k_new, v_new, k, v, cos=None, sin=None, *, q=None, q_out=None, rot_dim=None, interleaved=False,
+                positions=None, new_lens=None, seq_lens=None, max_seq_len=None, block_table=None,
+                workspace: Optional[Workspace] = None, stream=None):
+    """``fd_append_rope``: rotate ``q`` and ``k_new`` by position, write ``k_new`` and ``v_new`` into the cache.
+
+    ``k_new``, ``v_new`` ``[B, n, Hkv, D]`` and ``q`` ``[B, n, Hq, D]`` (optional), bf16 or fp32, may be
+    strided views (slices of one fused projection); ``k``, ``v`` are the cache as in ``decode`` (bf16 or fp32),
+    written in place.  ``cos``, ``sin`` fp32 ``[max_pos, rot_dim / 2]`` (None: no rotation).  Token ``j`` of sequence
+    ``b`` goes to place ``seq_lens[b] + j``; with ``new_lens`` ``[B]`` only the last ``new_lens[b]`` of the ``n``
+    rows are tokens.  ``seq_lens`` and ``max_seq_len`` are the lengths before the append.  ``positions``
+    ``[B, n]`` int32 replaces the places as rows of the tables.  Returns the rotated queries, fp32 ``[B, Hq, n, D]`` (``q_out`` if given,
+    whose padding rows keep their contents; None without ``q``).
+    """
+    kv = _kv_desc(k, v, block_table)
+    device = k.device
+    if k.dim() != 4 or v.device != device:
+        raise ValueError("k and v must be 4-d and on one device")
+    tokens = k.shape[2]
+    if block_table is not None:
+        if block_table.device != device or block_table.dim() != 2 or block_table.shape[0] != k_new.shape[0]:
+            raise ValueError("block_table must be [B, max_pages] on the cache's device")
+        tokens *= block_table.shape[1]
+    elif k.shape[0] != k_new.shape[0]:
+        raise ValueError(f"a contiguous cache must hold {k_new.shape[0]} sequences, got {k.shape[0]}")
+    r, B, n, Hq, lens, max_seq_len, q_out = _append_args(k_new, v_new, k.shape[1], k.shape[3], tokens, device, cos, sin,
+                                                         q, q_out, rot_dim, interleaved, positions, new_lens, seq_lens,
+                                                         max_seq_len)
+    buf = _scratch(workspace, device, 256)
+    _launch(device, _lib().fd_append_rope, "fd_append_rope", ctypes.byref(r), ctypes.byref(kv),
+            q_out.data_ptr() if q_out is not None else None, B, n, Hq, k.shape[1], lens, max_seq_len, k.shape[3],
+            buf.data_ptr(), buf.numel(), _stream_handle(device, stream))
+    return q_out
+
+
+def append_rope_kv4(k_new, v_new, kv4, cos=None, sin=None, *, k_exp=0, v_exp=0, q=None, q_out=None, rot_dim=None,
+                    interleaved=False, positions=None, new_lens=None, seq_lens=None, max_seq_len=None,
+                    block_table=None, workspace: Optional[Workspace] = None, stream=None):
+    """``fd_append_rope_kv4``: ``append_rope`` into a 4-bit cache (see ``kv4_cache``), written in place."""
+    if not isinstance(k_new, _torch().Tensor) or k_new.dim() != 4:
+        raise ValueError("k_new must be [B, n, Hkv, D]")
+    kv, Hkv, D, tokens = _kv4_desc(kv4, block_table, k_new.shape[0], k_exp, v_exp)
+    device = kv4.device
+    r, B, n, Hq, lens, max_seq_len, q_out = _append_args(k_new, v_new, Hkv, D, tokens, device, cos, sin, q, q_out,
+                                                         rot_dim, interleaved, positions, new_lens, seq_lens,
+                                                         max_seq_len)
+    buf = _scratch(workspace, device, 256)
+    _launch(device, _lib().fd_append_rope_kv4, "fd_append_rope_kv4", ctypes.byref(r), ctypes.byref(kv),
+            q_out.data_ptr() if q_out is not None else None, B, n, Hq, Hkv, lens, max_seq_len, D, buf.data_ptr(),
+            buf.numel(), _stream_handle(device, stream))
+    return q_out
+
+
+def kv4_read(kv4, n, *, starts=None, seq_lens=None, max_seq_len=None, block_table=None, k_exp=0, v_exp=0, dtype=None,
+             k_out=None, v_out=None, workspace: Optional[Workspace] = None, stream=None):
+    """``fd_kv4_read``: tokens ``starts[b] + i``, ``i < n``, of a 4-bit cache as values ``[B, Hkv, n, D]``.
+
+    ``dtype`` bf16 (default) or fp32.  Rows at or past ``seq_lens[b]`` keep the contents of ``k_out`` and
+    ``v_out`` (zeros when they are made here).  Returns ``(k_out, v_out)``.
+    """
+    torch = _torch()
+    B = kv4.shape[0] if block_table is None else block_table.shape[0]
+    kv, Hkv, D, tokens = _kv4_desc(kv4, block_table, B, k_exp, v_exp)
+    device = kv4.device
+    if dtype is None:
+        dtype = torch.bfloat16 if k_out is None else k_out.dtype
+    dt = {torch.bfloat16: FD_BF16, torch.float32: FD_F32}.get(dtype)
+    if dt is None:
+        raise ValueError(f"unsupported dtype {dtype}")
+    shape = (B, Hkv, int(n), D)
+    if k_out is None:
+        k_out = torch.zeros(shape, dtype=dtype, device=device)
+    if v_out is None:
+        v_out = torch.zeros(shape, dtype=dtype, device=device)
+    if max_seq_len is None:
+        max_seq_len = tokens
+    buf = _scratch(workspace, device, 256)
+    _launch(device, _lib().fd_kv4_read, "fd_kv4_read", ctypes.byref(kv), _opt(k_out, "k_out", dtype, device, shape),
+            _opt(v_out, "v_out", dtype, device, shape), dt, B, int(n), Hkv,
+            _opt(starts, "starts", torch.int32, device, (B,)), _opt(seq_lens, "seq_lens", torch.int32, device, (B,)),
+            int(max_seq_len), D, buf.data_ptr(), buf.numel(), _stream_handle(device, stream))
+    return k_out, v_out
+
+
+def decode_kv4(q, kv4, *, k_exp=0, v_exp=0, causal=True, seq_lens=None, max_seq_len=None, block_table=None, scale=None,
+               n_splits=FD_SPLITS_AUTO, out=None, lse=None, return_lse=True, workspace: Optional[Workspace] = None,
+               stream=None):
+    """``fd_decode_kv4``: decode attention over a 4-bit cache.
+
+    q ``[B, Hq, D]`` or ``[B, Hq, n_q, D]`` fp32 (``n_q`` up to 64 rows, masked as in ``decode_rows``); ``kv4`` as made by
+    ``kv4_cache``.  Returns ``(out, lse)`` shaped like q and q without its last axis.
+    """
+    torch = _torch()
+    _need_cuda(q, "q", torch.float32)
+    if q.dim() not in (3, 4):
+        raise ValueError("q must be [B, Hq, D] or [B, Hq, n_q, D]")
+    shape = tuple(q.shape)
+    B, Hq = shape[0], shape[1]
+    n_q = shape[2] if len(shape) == 4 else 1
+    kv, Hkv, D, tokens = _kv4_desc(kv4, block_table, B, k_exp, v_exp)
+    device = q.device
+    if D != shape[-1]:
+        raise ValueError("head_dim of q and kv4 differ")
+    if kv4.device != device:
+        raise ValueError("q and kv4 must be on one device")
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.float32, device=device)
+    else:
+        _opt(out, "out", torch.float32, device, shape)
+    if lse is not None:
+        _opt(lse, "lse", torch.float32, device, shape[:-1])
+    elif return_lse:
+        lse = torch.empty(shape[:-1], dtype=torch.float32, device=device)
+    buf = _scratch(workspace, device, workspace_bytes(B, Hq * n_q, Hkv, D, n_splits))
+    _launch(device, _lib().fd_decode_kv4, "fd_decode_kv4", q.data_ptr(), n_q, int(bool(causal)), ctypes.byref(kv),
+            out.data_ptr(), lse.data_ptr() if lse is not None else None, B, Hq, Hkv,
+            _opt(seq_lens, "seq_lens", torch.int32, device, (B,)),
+            int(max_seq_len) if max_seq_len is not None else tokens, D, float(scale), int(n_splits), buf.data_ptr(),
+            buf.numel(), _stream_handle(device, stream))
+    return out, lse
