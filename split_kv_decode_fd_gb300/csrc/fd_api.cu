@@ -970,9 +970,7 @@ fd_status fd_decode_kv4(const float* q, int32_t n_q, int32_t causal, const fd_kv
   int sms = 0;
   if (n_splits == 0) {
     if (!sm_count(&sms)) return FD_ERR_CUDA;
-    n_splits = fallback_splits(B, gr.hv, max_seq_len, sms);
-    if (B <= FD_AUTO_MAX_BATCH && pairs <= kMaxFusedPairs)  // as many states as the balanced plan's workspace holds
-      n_splits = (int)std::max<int64_t>(1, std::min<int64_t>(n_splits, (sms + pairs) * gr.gpad / ((int64_t)B * Hq)));
+    if (B > FD_AUTO_MAX_BATCH || pairs > kMaxFusedPairs) n_splits = fallback_splits(B, gr.hv, max_seq_len, sms);
   }
   const WsLayout w = ws_layout(B, Hq, Hkv, D, n_splits, sms, kMaxGroupBf16);
   if (workspace_bytes < w.total) return FD_ERR_WORKSPACE_TOO_SMALL;
@@ -986,11 +984,16 @@ fd_status fd_decode_kv4(const float* q, int32_t n_q, int32_t causal, const fd_kv
   p.m_part = reinterpret_cast<float*>(ws + w.m);
   p.l_part = reinterpret_cast<float*>(ws + w.l);
   p.err = reinterpret_cast<unsigned*>(ws + w.err);
+  p.counters = pairs <= kMaxFusedPairs ? reinterpret_cast<int*>(ws + w.counters) : nullptr;
   p.n_splits = n_splits;
-  p.split_tokens = max_seq_len > 0 ? explicit_split_size(max_seq_len, n_splits) : kSplitAlign;
-  const dim3 grid((unsigned)pairs, (unsigned)n_splits, 1);
   cudaStream_t s = (cudaStream_t)stream;
+  dim3 grid((unsigned)sms, 1, 1);
+  if (n_splits != 0) {
+    p.split_tokens = max_seq_len > 0 ? explicit_split_size(max_seq_len, n_splits) : kSplitAlign;
+    grid = dim3((unsigned)pairs, (unsigned)n_splits, 1);
+  }
   if (launch_kv4_split(D, v, p, grid, s) != cudaSuccess) return FD_ERR_CUDA;
+  if (p.counters) return FD_OK;
   const cudaError_t e = launch_combine(D, p.o_part, p.m_part, p.l_part, out, lse, B * Hq, n_splits, s);
   return e == cudaSuccess ? FD_OK : FD_ERR_CUDA;
 }

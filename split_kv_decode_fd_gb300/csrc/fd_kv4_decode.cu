@@ -1,130 +1,917 @@
-// fd_kv4_decode.cu -- decode attention over a 4-bit cache: partial states of
-// the explicit plan.
+// fd_kv4_decode.cu -- decode attention over a 4-bit cache on the tcgen05 tensor
+// cores.
 //
-// One CTA per (b, virtual KV head, split): 128 keys at a time, lane = key for
-// q.k, then lane = channel for p.V, with an online softmax per head.
+// A piece of work is a run of keys of one (sequence, KV head) and the up to 16
+// query heads (or heads x rows) of its group; the balanced plan of fd_plan.h
+// gives every SM's CTA an equal share of pieces.  Per tile of 128 keys:
+//
+//     S^T[key, head] = K[key, :] . q[head, :]        M = 128 keys, K = D
+//     p = exp2(S - m),  l += p                       thread = key
+//     O^T[d, head] += V^T[d, :] . p[:, head]         M = 128 channels, K = 128 keys
+//
+// Both products take their A operand (K, V^T) from tensor memory as fp16, where a
+// lane is a row: the thread that owns the row widens its codes in registers
+// and stores them there.  code * scale has six significant bits and is exact in
+// fp16.  The B operands are small: q (once per piece) and p (per tile) in shared
+// memory, each as the sum of two fp16 numbers, hi and lo, that sit in columns of
+// their own; so the products are exact and accumulate in fp32.
+//
+// What bounds it: 9/16 byte per element from HBM (18 KB per tile for D = 128,
+// 0.41 us of an SM's share of the copy rate) against the widening, about one
+// issue slot for two elements.  The MMAs cost no issue slots here (mma.sync costs
+// as many as the widening: measured 8.4 slots for a 16x8x16 step), and with heads
+// on the N axis their time does not grow with the group.
+//
+// Sixteen warps:
+//   0      walks the plan, announces pieces, copies tiles (one bulk copy for a
+//          contiguous run, one per block when paged) into a ring of stages;
+//   1      one thread issues the MMAs: S(g), then O of tile g - 1;
+//   2, 3   q of the next piece: scaled to the fp16 range by a power of two per
+//          head, split hi / lo, written in the B layout;
+//   4-7    K: lane = key;   8-11  V: lane = channel;
+//   12-15  softmax: lane = key; at the end of a piece lane = channel.
+// Every mbarrier wait is bounded; a wait that runs out raises the error word and
+// the CTA still counts its pieces, so that the workspace stays valid.
+#include <cuda_fp16.h>
+
+#include <atomic>
+
 #include "fd_internal.h"
 #include "fd_kv4.cuh"
 #include "fd_split.cuh"
+#include "fd_tcgen05.cuh"
 
 namespace fdk {
 namespace {
 
-constexpr int kTile = 128;
-constexpr int kHeads = kMaxGroupBf16;
+constexpr int kTile = kPlanTile;                       // keys per tile: the M of S^T
+constexpr int kTileBlocks = kTile / kKv4Tokens;
+constexpr int kDescs = 4;                              // pieces announced ahead
+constexpr int kThreads = 512;
+// p is held in fp16: the reference of the exponent lies kRefDown below the
+// running maximum and moves when a score exceeds that maximum by kTau, so p <=
+// 2^(kRefDown + kTau) = 2^15, and the smallest fp16 number stands for 2^-33 of the
+// maximum's weight.
+constexpr float kRefDown = 9.f, kTau = 6.f;
 
-template <int D>
-__global__ void __launch_bounds__(128) fd_kv4_split_kernel(const Kv4View kv, const SplitParams p) {
-  __shared__ float q[kHeads][D];
-  __shared__ float pr[kHeads][kTile];
-  __shared__ float red[4];
-  __shared__ int64_t blocks[kTile / kKv4Tokens];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int32_t pair = blockIdx.x, s = blockIdx.y;
-  const int32_t b = pair / p.hv, vkv = pair % p.hv;
-  Groups gr;
-  gr.g = p.g;
-  gr.gpad = p.gpad;
-  gr.nsub = p.nsub;
-  gr.hv = p.hv;
-  int32_t head0, nh;
-  vkv_heads(gr, vkv, &head0, &nh);
-  const int32_t kvh = kv_head_of_vkv(gr, vkv);
-  const int32_t L = p.seq_lens ? clamp_len(__ldg(p.seq_lens + b), p.max_len) : p.max_len;
-  const int64_t lo = (int64_t)s * p.split_tokens;
-  const int32_t t_end = (int32_t)(lo + p.split_tokens < L ? lo + p.split_tokens : L);
-  const RowLimits lim{head0, nh, L, p.n_q, p.causal};
-  const float up = p.qk_scale * pow2i(kv.k_exp);
-  for (int i = tid; i < nh * D; i += 128) q[i / D][i % D] = p.q[((size_t)b * p.Hq + head0) * D + i] * up;
-  float m[kHeads], l[kHeads], o[kHeads];
-  for (int h = 0; h < kHeads; ++h) {
-    m[h] = -INFINITY;
-    l[h] = 0.f;
-    o[h] = 0.f;
+// Tensor-memory columns: K and V (two buffers each), S (two), O.
+constexpr uint32_t kColK = 0, kColV = 128, kColS = 256, kColO = 320;
+
+struct KvPiece {
+  int32_t b, vkv, tok_begin, tok_end, slot, len, npieces, first;
+};
+
+template <int D, int G>
+struct K4 {
+  static constexpr int kHalf = G <= 8 ? 8 : 16;   // heads as columns: hi, then lo
+  static constexpr int kN = 2 * kHalf;
+  static constexpr int kStageBytes = kTileBlocks * kv4_block_bytes(D);
+  static constexpr int kStages = D == 128 ? 8 : 14;
+  static constexpr int kVWarps = D / 32;
+  static constexpr int kQBytes = kN * D * 2;
+  static constexpr int kPBytes = kN * kTile * 2;
+  // byte offsets from a 1024-aligned base
+  static constexpr int kQOff = 0;
+  static constexpr int kPOff = kQOff + 2 * kQBytes;
+  static constexpr int kStageOff = kPOff + 2 * kPBytes;
+  static constexpr int kVsOff = kStageOff + kStages * kStageBytes;   // V scales as fp16: [4 warps][2][128]
+  static constexpr int kRedOff = kVsOff + 4 * 2 * kTile * 2;         // [4 warps][G] maxima or sums
+  static constexpr int kMergeOff = kRedOff + 4 * 16 * 4;             // merge scratch: [4 warps][128]
+  static constexpr int kMetaOff = kMergeOff + 4 * 128 * 4;           // per q buffer: factor[16], limit[16], least limit
+  static constexpr int kMetaBytes = 16 * 8 + 16;
+  static constexpr int kDescOff = kMetaOff + 2 * kMetaBytes;
+  static constexpr int kLenOff = kDescOff + kDescs * (int)sizeof(KvPiece);
+  static constexpr int kPreOff = kLenOff + (kAutoMaxBatch + 4) * 4;
+  static constexpr int kBarOff = kPreOff + (kAutoMaxBatch + 4) * 4;
+  static constexpr int kBars = 2 * kStages + 2 * kDescs + 2 * 5 + 4 + 1;
+  static constexpr int kFlagOff = kBarOff + kBars * 8;
+  static constexpr int kSmem = kFlagOff + 16 + 1024;
+  static_assert(kSmem <= 232448 && kSmem > 118784, "one CTA per SM: each takes all of tensor memory");
+  static_assert(kStageOff % 128 == 0 && kQBytes % 1024 == 0 && kPBytes % 1024 == 0, "operand alignment");
+  static_assert(kDescOff % 16 == 0 && kBarOff % 8 == 0, "alignment");
+};
+
+struct Kv4Params {
+  SplitParams p;
+  Kv4View kv;
+};
+
+// Byte offset of fp16 element (n, k) of a B operand: rows n of 64 k (128 bytes,
+// swizzled), column blocks of N rows.
+template <int N>
+__device__ __forceinline__ uint32_t b_off(int n, int k) {
+  return (uint32_t)(k >> 6) * (N * 128) + (uint32_t)n * 128 + (((uint32_t)(k >> 3) & 7u) ^ ((uint32_t)n & 7u)) * 16 +
+         ((uint32_t)k & 7u) * 2;
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// Eight codes times their scales (pairs of them: s[0] for the first two codes ...).
+__device__ __forceinline__ void widen8(uint32_t w, uint32_t s0, uint32_t s1, uint32_t s2, uint32_t s3, uint32_t* out) {
+  out[0] = hmul2(e2m1x2_f16x2<0>(w), s0);
+  out[1] = hmul2(e2m1x2_f16x2<1>(w), s1);
+  out[2] = hmul2(e2m1x2_f16x2<2>(w), s2);
+  out[3] = hmul2(e2m1x2_f16x2<3>(w), s3);
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void sts16(uint32_t at, uint32_t v) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"((unsigned short)v) : "memory");
+}
+__device__ __forceinline__ void sts128u(uint32_t at, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// (x0, x1) = hi + lo in fp16, as packed pairs (x0 in the low half).
+__device__ __forceinline__ void split_f16x2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(x0, x1);
+  const float2 f = __half22float2(h);
+  const __half2 r = __floats2half2_rn(x0 - f.x, x1 - f.y);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// Barrier of the four softmax warps that counts raised predicates.
+__device__ __forceinline__ uint32_t softmax_vote(bool pred) {
+  uint32_t n;
+  __syncwarp();
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.popc.u32 %0, 1, 128, p;\n\t}"
+               : "=r"(n)
+               : "r"((uint32_t)pred)
+               : "memory");
+  return n;
+}
+__device__ __forceinline__ void softmax_sync() { named_barrier(1, 128); }
+
+// Waits of one warp (all lanes together): false when the CTA aborts or the limit passes.
+struct Waiter {
+  volatile int* abort_flag;
+  unsigned long long limit;
+  __device__ __forceinline__ bool one(uint64_t* bar, uint32_t parity) const {
+    return mbar_try_wait(bar, parity) || (!*abort_flag && mbar_wait_for(bar, parity, limit));
   }
-  for (int32_t t0 = (int32_t)(lo < L ? lo : L); t0 < t_end; t0 += kTile) {
-    __syncthreads();
-    if (tid < kTile / kKv4Tokens) {
-      blocks[tid] = -1;
-      if (t0 + 16 * tid < t_end) {
-        blocks[tid] = kv4_block_index(kv, b, kvh, t0 + 16 * tid);
-        if (blocks[tid] < 0) raise_error(p.err, kErrBadIndex);
-      }
+  __device__ __forceinline__ bool warp(uint64_t* bar, uint32_t parity) const {
+    return __all_sync(0xffffffffu, one(bar, parity));
+  }
+};
+
+template <int D, int G>
+__global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_constant__ Kv4Params pp) {
+  using C = K4<D, G>;
+  constexpr int H = C::kHalf, N = C::kN;
+  const SplitParams& p = pp.p;
+  const Kv4View& kv = pp.kv;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_addr(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
+  uint64_t* empty = full + C::kStages;
+  uint64_t* desc_full = empty + C::kStages;
+  uint64_t* desc_empty = desc_full + kDescs;
+  uint64_t* k_ready = desc_empty + kDescs;  // [2] each of the tile's buffers
+  uint64_t* s_full = k_ready + 2;           // [2] S is there; K's buffer is free
+  uint64_t* p_ready = s_full + 2;           // [2]
+  uint64_t* v_ready = p_ready + 2;          // [2]
+  uint64_t* pv_done = v_ready + 2;          // [2] V's and p's buffers are free
+  uint64_t* q_ready = pv_done + 2;          // [2]
+  uint64_t* q_free = q_ready + 2;           // [2]
+  uint64_t* drain = q_free + 2;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kFlagOff);
+  volatile int* last_flag = abort_flag + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kFlagOff + 8);
+  KvPiece* descs = reinterpret_cast<KvPiece*>(smem + C::kDescOff);
+  int32_t* lens = reinterpret_cast<int32_t*>(smem + C::kLenOff);
+  int32_t* pre = reinterpret_cast<int32_t*>(smem + C::kPreOff);
+
+  if (tid == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(empty + s, 4 + C::kVWarps);
     }
-    __syncthreads();
-    const int32_t t = t0 + tid;
-    const int64_t idx = blocks[tid / 16];
-    const bool in = t < t_end;
-    float sc[kHeads];
-    for (int h = 0; h < kHeads; ++h) sc[h] = 0.f;
-    if (in && idx >= 0) {
-      const uint8_t* blk = kv.kv + idx * kv4_block_bytes(D);
-      for (int c = 0; c < D / 16; ++c) {
-        const int at = (tid & 15) * (D / 2) + (((c >> 1) ^ kv4_swizzle(D, tid & 15)) << 4) + (c & 1) * 8;
-        const uint2 w = *reinterpret_cast<const uint2*>(blk + at);
-        const float f = e4m3_f32(blk[kv4_ks_off(D) + (tid & 15) * (D / 16) + c]);
-        const uint32_t x[8] = {e2m1x2_f16x2<0>(w.x), e2m1x2_f16x2<1>(w.x), e2m1x2_f16x2<2>(w.x), e2m1x2_f16x2<3>(w.x),
-                               e2m1x2_f16x2<0>(w.y), e2m1x2_f16x2<1>(w.y), e2m1x2_f16x2<2>(w.y), e2m1x2_f16x2<3>(w.y)};
+    for (int s = 0; s < kDescs; ++s) {
+      mbar_init(desc_full + s, 1);
+      mbar_init(desc_empty + s, 1 + 2 + 4 + C::kVWarps + 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(k_ready + i, 4);
+      mbar_init(s_full + i, 1);
+      mbar_init(p_ready + i, 4);
+      mbar_init(v_ready + i, C::kVWarps);
+      mbar_init(pv_done + i, 1);
+      mbar_init(q_ready + i, 2);
+      mbar_init(q_free + i, 1 + 4);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) tmem_alloc_all(smem_addr(tmem_slot));
+  pdl_launch_dependents();
+  if (p.seq_lens != nullptr) pdl_wait();
+  CtaTiles tl;
+  tl.pre = pre;
+  tl.ln = lens;
+  tl.ul = p.max_len;
+  tl.ut = ceil_div(p.max_len, kPlanTile);
+  tl.uniform = 1;
+  if (p.n_splits == 0 && p.seq_lens != nullptr) {
+    tl.uniform = 0;
+    for (int b = tid; b < p.B; b += kThreads) lens[b] = clamp_len(__ldg(p.seq_lens + b), p.max_len);
+    cta_sync();
+    if (warp == 0) {
+      const int per = ceil_div(p.B, 32);
+      const int lo = lane * per;
+      const int hi = lo + per < p.B ? lo + per : p.B;
+      int sum = 0;
+      for (int b = lo; b < hi; ++b) sum += (int)pair_units(ceil_div(lens[b], kPlanTile), kPieceUnits);
+      int incl = sum;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float2 k2 = __half22float2(*reinterpret_cast<const __half2*>(&x[j]));
-          for (int h = 0; h < nh; ++h)
-            sc[h] = fmaf(k2.y * f, q[h][16 * c + 2 * j + 1], fmaf(k2.x * f, q[h][16 * c + 2 * j], sc[h]));
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
+      }
+      int run = incl - sum;
+      for (int b = lo; b < hi; ++b) {
+        pre[b] = run;
+        run += (int)pair_units(ceil_div(lens[b], kPlanTile), kPieceUnits);
+      }
+      if (lane == 31) pre[p.B] = incl;
+    }
+  }
+  tmem_fence_before();
+  cta_sync();
+  tmem_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int64_t total = (int64_t)p.hv * tl.prefix(p.B);
+  const Waiter wait{abort_flag, wait_limit(p)};
+  bool ok = true;
+
+  // Every role but the producer takes the announced pieces in order.
+  const auto next_piece = [&](uint32_t e, KvPiece& pc) {
+    const uint32_t sl = e % kDescs;
+    // not `wait.warp`: pieces are still announced after an abort
+    const bool got = __all_sync(0xffffffffu, mbar_wait_for(desc_full + sl, (e / kDescs) & 1, wait.limit));
+    if (got) pc = descs[sl];
+    __syncwarp();
+    if (got && lane == 0) mbar_arrive(desc_empty + sl);
+    return got && pc.b >= 0;
+  };
+  const auto tiles_of = [](const KvPiece& pc) { return ceil_div(pc.tok_end - pc.tok_begin, kTile); };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    Groups gr;
+    gr.g = p.g;
+    gr.gpad = p.gpad;
+    gr.nsub = p.nsub;
+    gr.hv = p.hv;
+    const uint64_t stream_policy = policy_evict_first();
+    const int32_t grid_used = p.n_splits == 0 ? balanced_ctas(total, (int32_t)gridDim.x) : 0;
+    PieceIter pieces(p, tl, total);
+    Piece pc;
+    uint32_t it = 0, e = 0, stalled = 0xffffffffu;
+    bool live = true;  // the other roles still take pieces
+    pdl_wait();
+    const auto announce = [&](const KvPiece& d) {
+      const uint32_t sl = e % kDescs;
+      bool r = true;
+      if (lane == 0) {
+        r = mbar_wait_for(desc_empty + sl, ((e / kDescs) & 1) ^ 1, wait.limit);
+        if (r) {
+          descs[sl] = d;
+          mbar_arrive(desc_full + sl);
+        }
+      }
+      ++e;
+      return (bool)__shfl_sync(0xffffffffu, r, 0);
+    };
+    while (live && pieces.next(pc)) {
+      KvPiece d;
+      d.b = pc.b;
+      d.vkv = pc.vkv;
+      d.tok_begin = pc.tok_begin;
+      d.tok_end = pc.tok_end;
+      d.slot = pc.slot;
+      d.len = pc.len;
+      d.npieces = p.n_splits;
+      d.first = 0;
+      if (p.n_splits == 0) {
+        int32_t last;
+        balanced_pair_ctas(tl, p.hv, total, grid_used, pc.b, pc.vkv, &d.first, &last);
+        d.npieces = last - d.first + 1;
+      }
+      live = announce(d);
+      if (!live) break;
+      if (!ok) continue;
+      const int32_t kvh = kv_head_of_vkv(gr, pc.vkv);
+      const uint8_t* base = kv.kv;
+      if (!kv.paged)
+        base += (((int64_t)pc.b * kv.Hkv + kvh) * kv.cap_blocks + pc.tok_begin / kKv4Tokens) * kv4_block_bytes(D);
+      // Paged: lane j holds the block number of block j of four tiles; the next
+      // four tiles' table entries are in flight meanwhile.
+      const int32_t blk0 = pc.tok_begin / kKv4Tokens, blk1 = ceil_div(pc.tok_end, kKv4Tokens);
+      const int32_t ppb = kv.paged ? kv.page_size / kKv4Tokens : 1;
+      const int32_t* trow = kv.paged ? kv.block_table + (size_t)pc.b * kv.max_pages : nullptr;
+      const auto page_of = [&](int32_t blk) { return blk < blk1 ? __ldg(trow + blk / ppb) : 0; };
+      int32_t cur = 0, nxt = 0;
+      if (kv.paged) {
+        cur = page_of(blk0 + lane);
+        nxt = page_of(blk0 + 32 + lane);
+      }
+      const int32_t n = tiles_of(d);
+      for (int32_t j = 0; j < n; ++j, ++it) {
+        const uint32_t st = it % C::kStages;
+        const int32_t nblk = blk1 - (blk0 + j * kTileBlocks) < kTileBlocks ? blk1 - (blk0 + j * kTileBlocks) : kTileBlocks;
+        const bool stall = p.stall_it >= 0 && it == (uint32_t)p.stall_it;
+        if (!wait.warp(empty + st, ((it / C::kStages) & 1) ^ 1)) {
+          ok = false;
+          break;
+        }
+        if (stall) {
+          stalled = it;
+          continue;
+        }
+        uint8_t* dst = smem + C::kStageOff + st * C::kStageBytes;
+        if (!kv.paged) {
+          if (lane == 0) {
+            const uint32_t bytes = (uint32_t)nblk * kv4_block_bytes(D);
+            mbar_arrive_expect_tx(full + st, bytes);
+            const uint8_t* src = base + (int64_t)j * C::kStageBytes;
+            asm volatile(
+                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+                    smem_addr(dst)),
+                "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_addr(full + st)), "l"(stream_policy)
+                : "memory");
+          }
+        } else {
+          const int k = lane - (j & 3) * kTileBlocks;  // this lane's block of the tile
+          const bool mine = k >= 0 && k < nblk;
+          const bool bad = mine && (cur < 0 || cur >= kv.num_pages);
+          if (bad) {
+            // keys of score 0 and value 0 in its place
+            raise_error(p.err, kErrBadIndex);
+            for (int i = 0; i < kv4_block_bytes(D); i += 16)
+              sts128u(smem_addr(dst) + k * kv4_block_bytes(D) + i, make_uint4(0, 0, 0, 0));
+            // before a later copy into this stage
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          }
+          __syncwarp();
+          const uint32_t copies = __popc(__ballot_sync(0xffffffffu, mine && !bad));
+          if (lane == 0) mbar_arrive_expect_tx(full + st, copies * kv4_block_bytes(D));
+          __syncwarp();
+          if (mine && !bad) {
+            const int32_t blk = blk0 + j * kTileBlocks + k;
+            const int64_t idx = ((int64_t)cur * kv.Hkv + kvh) * ppb + blk % ppb;
+            bulk_load(dst + k * kv4_block_bytes(D), kv.kv + idx * kv4_block_bytes(D), kv4_block_bytes(D), full + st);
+          }
+          if ((j & 3) == 3) {
+            cur = nxt;
+            nxt = page_of(blk0 + (j + 5) * kTileBlocks + lane);
+          }
         }
       }
     }
-    for (int h = 0; h < nh; ++h) {
-      const float v = in && t < lim(h) ? sc[h] : -INFINITY;
-      const float wm = warp_max(v);
-      if (lane == 0) red[warp] = wm;
-      __syncthreads();
-      const float mn = fmaxf(fmaxf(m[h], fmaxf(red[0], red[1])), fmaxf(red[2], red[3]));
-      const float ref = mn == -INFINITY ? 0.f : mn;
-      const float e = exp2f(v - ref), alpha = exp2f(m[h] - ref);
-      pr[h][tid] = e;
-      const float ws = warp_sum(e);
-      __syncthreads();
-      if (lane == 0) red[warp] = ws;
-      __syncthreads();
-      l[h] = fmaf(l[h], alpha, (red[0] + red[1]) + (red[2] + red[3]));
-      o[h] *= alpha;
-      m[h] = mn;
-      __syncthreads();
+    if (live) {
+      KvPiece d;
+      d.b = -1;
+      live = announce(d);
     }
-    if (tid < D) {
-      const int n = t_end - t0 < kTile ? t_end - t0 : kTile;
-      for (int j = 0; j < n; ++j) {
-        if (blocks[j / 16] < 0) continue;
-        const uint8_t* blk = kv.kv + blocks[j / 16] * kv4_block_bytes(D);
-        const uint32_t byte = blk[kv4_v_off(D) + tid * 8 + (j & 15) / 2];
-        const uint32_t x = e2m1x2_f16x2<0>(j & 1 ? byte >> 4 : byte & 15);
-        const float v = __half2float(__ushort_as_half((unsigned short)(x & 0xffff))) *
-                        e4m3_f32(blk[kv4_vs_off(D) + (tid / 16) * 16 + (j & 15)]);
-        for (int h = 0; h < nh; ++h) o[h] = fmaf(pr[h][j], v, o[h]);
+    if (!ok || !live) {
+      raise_error(p.err, kErrTimeout);
+      *abort_flag = 1;
+    }
+    // stay until the copies in flight have landed
+    if (lane == 0) {
+      const uint32_t n = it < (uint32_t)C::kStages ? it : (uint32_t)C::kStages;
+      for (uint32_t j = it - n; j < it; ++j)
+        if (j != stalled && !mbar_wait_for(full + j % C::kStages, (j / C::kStages) & 1, wait.limit))
+          raise_error(p.err, kErrTimeout);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issue
+    constexpr uint32_t idesc = f16_instr_desc(kTile, N);
+    uint32_t g = 0, e = 0, f = 0;  // tiles, pieces, pieces with tiles
+    int32_t j_prev = -1;           // number within its piece of the tile whose O is owed
+    const auto issue_o = [&](uint32_t gt, int32_t j) {
+      const uint32_t buf = gt & 1, ph = (gt >> 1) & 1;
+      if (!wait.warp(v_ready + buf, ph) || !wait.warp(p_ready + buf, ph)) return false;
+      tmem_fence_after();
+      if (lane == 0) {
+        const uint32_t ps = sbase + C::kPOff + buf * C::kPBytes;
+#pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk)
+          mma_ts(tmem + kColO, tmem + kColV + buf * 64 + kk * 8, b_desc(ps + (kk >> 2) * (N * 128) + (kk & 3) * 32), idesc,
+                 j > 0 || kk > 0);
+        mma_commit(smem_addr(pv_done + buf));
+      }
+      __syncwarp();
+      return true;
+    };
+    KvPiece pc;
+    for (; next_piece(e, pc); ++e) {
+      const int32_t n = tiles_of(pc);
+      if (!ok || n == 0) continue;
+      const uint32_t qb = f & 1;
+      if (!wait.warp(q_ready + qb, (f >> 1) & 1)) ok = false;
+      for (int32_t j = 0; ok && j < n; ++j, ++g) {
+        const uint32_t buf = g & 1;
+        if (!wait.warp(k_ready + buf, (g >> 1) & 1)) {
+          ok = false;
+          break;
+        }
+        tmem_fence_after();
+        if (lane == 0) {
+          const uint32_t qs = sbase + C::kQOff + qb * C::kQBytes;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_ts(tmem + kColS + buf * 32, tmem + kColK + buf * 64 + kk * 8,
+                   b_desc(qs + (kk >> 2) * (N * 128) + (kk & 3) * 32), idesc, kk > 0);
+          mma_commit(smem_addr(s_full + buf));
+          if (j == n - 1) mma_commit(smem_addr(q_free + qb));
+        }
+        __syncwarp();
+        if (g > 0 && !issue_o(g - 1, j_prev)) {
+          ok = false;
+          break;
+        }
+        j_prev = j;
+      }
+      ++f;
+    }
+    if (ok && g > 0 && !issue_o(g - 1, j_prev)) ok = false;
+    if (!ok) {
+      raise_error(p.err, kErrTimeout);
+      *abort_flag = 1;
+    }
+    // every MMA has finished before tensor memory goes back
+    if (lane == 0) {
+      mma_commit(smem_addr(drain));
+      if (!mbar_wait_for(drain, 0, wait.limit)) raise_error(p.err, kErrTimeout);
+    }
+  } else if (warp < 4) {
+    // ------------------------------------------------------------ q
+    Groups gr;
+    gr.g = p.g;
+    gr.gpad = p.gpad;
+    gr.nsub = p.nsub;
+    gr.hv = p.hv;
+    uint32_t e = 0, f = 0;
+    KvPiece pc;
+    pdl_wait();
+    for (; next_piece(e, pc); ++e) {
+      if (!ok || tiles_of(pc) == 0) continue;
+      const uint32_t qb = f & 1;
+      if (f >= 2 && !wait.warp(q_free + qb, ((f >> 1) & 1) ^ 1)) {
+        ok = false;
+        continue;
+      }
+      int32_t head0, nh;
+      vkv_heads(gr, pc.vkv, &head0, &nh);
+      const RowLimits rl{head0, nh, pc.len, p.n_q, p.causal};
+      float* factor = reinterpret_cast<float*>(smem + C::kMetaOff + qb * C::kMetaBytes);
+      int32_t* limit = reinterpret_cast<int32_t*>(factor + 16);
+      const uint32_t qs = sbase + C::kQOff + qb * C::kQBytes;
+      constexpr int E = D / 32;
+      for (int h = warp - 2; h < H; h += 2) {
+        float x[E];
+        float big = 0.f;
+#pragma unroll
+        for (int i = 0; i < E; ++i) x[i] = 0.f;
+        if (h < nh) {
+          load_slice<D>(p.q + ((size_t)pc.b * p.Hq + head0 + h) * D + lane * E, x);
+#pragma unroll
+          for (int i = 0; i < E; ++i) big = fmaxf(big, fabsf(x[i]));
+        }
+        big = warp_max(big);
+        // 2^e <= big < 2^(e + 1): q times 2^(13 - e) fills fp16's range
+        int ex = (int)((__float_as_uint(big) >> 23) & 0xffu) - 127;
+        if (big == 0.f || ex > 127) ex = 13;
+        ex = ex < -80 ? -80 : (ex > 80 ? 80 : ex);
+        const float up = pow2i(13 - ex);
+#pragma unroll
+        for (int i = 0; i < E; i += 2) {
+          uint32_t hi, lo;
+          split_f16x2(x[i] * up, x[i + 1] * up, hi, lo);
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(qs + b_off<N>(h, lane * E + i)), "r"(hi) : "memory");
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(qs + b_off<N>(H + h, lane * E + i)), "r"(lo) : "memory");
+        }
+        if (lane == 0) {
+          factor[h] = h < nh ? p.qk_scale * pow2i(kv.k_exp) * pow2i(ex - 13) : 0.f;
+          limit[h] = h < nh ? rl(h) : 0x7fffffff;
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_ready + qb);
+      ++f;
+    }
+    if (!ok) {
+      raise_error(p.err, kErrTimeout);
+      *abort_flag = 1;
+    }
+  } else if (warp < 8) {
+    // ------------------------------------------------------------ K
+    const int quad = warp - 4;
+    const int row = lane & 15;
+    const uint32_t krow = (uint32_t)(quad * 2 + (lane >> 4)) * kv4_block_bytes(D);
+    const uint32_t sw = kv4_swizzle(D, row);
+    const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+    uint32_t g = 0, e = 0;
+    KvPiece pc;
+    for (; next_piece(e, pc); ++e) {
+      const int32_t n = ok ? tiles_of(pc) : 0;
+      for (int32_t j = 0; j < n; ++j, ++g) {
+        const uint32_t st = g % C::kStages, buf = g & 1;
+        if (!wait.warp(full + st, (g / C::kStages) & 1) || (g >= 2 && !wait.warp(s_full + buf, ((g >> 1) & 1) ^ 1))) {
+          ok = false;
+          break;
+        }
+        tmem_fence_after();
+        const uint32_t base = sbase + C::kStageOff + st * C::kStageBytes + krow;
+        // scales: D / 16 bytes a row
+        uint32_t sc[D / 32];
+        if constexpr (D == 128) {
+          const uint2 b = lds64u(base + kv4_ks_off(D) + row * 8);
+          sc[0] = e4m3x2_f16x2(b.x);
+          sc[1] = e4m3x2_f16x2(b.x >> 16);
+          sc[2] = e4m3x2_f16x2(b.y);
+          sc[3] = e4m3x2_f16x2(b.y >> 16);
+        } else {
+          const uint32_t b = lds32u(base + kv4_ks_off(D) + row * 4);
+          sc[0] = e4m3x2_f16x2(b);
+          sc[1] = e4m3x2_f16x2(b >> 16);
+        }
+        uint4 w[D / 32];
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) w[c] = lds128u(base + row * (D / 2) + ((c ^ sw) << 4));
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          const uint32_t a = __byte_perm(sc[c], 0, 0x1010), b = __byte_perm(sc[c], 0, 0x3232);
+          uint32_t r[16];
+          widen8(w[c].x, a, a, a, a, r);
+          widen8(w[c].y, a, a, a, a, r + 4);
+          widen8(w[c].z, b, b, b, b, r + 8);
+          widen8(w[c].w, b, b, b, b, r + 12);
+          tmem_store16(tmem + lanes + kColK + buf * 64 + c * 16, r);
+        }
+        tmem_wait_stores();
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(k_ready + buf);
+          mbar_arrive(empty + st);
+        }
       }
     }
-  }
-  const float vup = pow2i(kv.v_exp);
-  for (int h = 0; h < nh; ++h) {
-    const size_t i = ((size_t)b * p.Hq + head0 + h) * p.n_splits + s;
-    if (tid < D) p.o_part[i * D + tid] = o[h] * vup;
-    if (tid == 0) {
-      // The merge passes over states whose l is not above zero.  A NaN sum goes in as
-      // m = inf: the weight exp(inf - inf) then makes out and lse NaN, as the formula does.
-      p.m_part[i] = isnan(l[h]) ? INFINITY : m[h] == -INFINITY ? m[h] : m[h] * kLn2;
-      p.l_part[i] = isnan(l[h]) ? 1.f : l[h];
+    if (!ok) {
+      raise_error(p.err, kErrTimeout);
+      *abort_flag = 1;
+    }
+  } else if (warp < 12) {
+    // ------------------------------------------------------------ V
+    const int quad = warp - 8;
+    if (quad < C::kVWarps) {
+      const int d = quad * 32 + lane;
+      const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+      const uint32_t vs = sbase + C::kVsOff + quad * (2 * kTile * 2);
+      const int sblk = (lane >> 1) & 7, stok = sblk * 16 + (lane & 1) * 8;  // the scales that this lane converts
+      uint32_t g = 0, e = 0;
+      KvPiece pc;
+      for (; next_piece(e, pc); ++e) {
+        const int32_t n = ok ? tiles_of(pc) : 0;
+        for (int32_t j = 0; j < n; ++j, ++g) {
+          const uint32_t st = g % C::kStages, buf = g & 1;
+          if (!wait.warp(full + st, (g / C::kStages) & 1) || (g >= 2 && !wait.warp(pv_done + buf, ((g >> 1) & 1) ^ 1))) {
+            ok = false;
+            break;
+          }
+          tmem_fence_after();
+          const uint32_t base = sbase + C::kStageOff + st * C::kStageBytes;
+          {
+            // The warp's two groups of sixteen channels, 128 tokens: scales to fp16,
+            // 0 for tokens past the valid ones (0 * anything finite is 0, and codes are finite).
+            const uint2 b = lds64u(base + sblk * kv4_block_bytes(D) + kv4_vs_off(D) + (quad * 2 + (lane >> 4)) * 16 +
+                                   (lane & 1) * 8);
+            uint32_t x[4] = {e4m3x2_f16x2(b.x), e4m3x2_f16x2(b.x >> 16), e4m3x2_f16x2(b.y), e4m3x2_f16x2(b.y >> 16)};
+            const int32_t left = pc.tok_end - (pc.tok_begin + j * kTile) - stok;  // valid tokens of these eight
+            if (left < 8) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                if (left <= 2 * i) x[i] = 0;
+                if (left == 2 * i + 1) x[i] &= 0xffffu;
+              }
+            }
+            sts128u(vs + (lane >> 4) * (kTile * 2) + stok * 2, make_uint4(x[0], x[1], x[2], x[3]));
+          }
+          __syncwarp();
+          const uint32_t vsl = vs + (lane >> 4) * (kTile * 2);
+#pragma unroll
+          for (int c = 0; c < kTileBlocks / 2; ++c) {
+            uint32_t r[16];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int blk = 2 * c + i;
+              const uint2 w = lds64u(base + blk * kv4_block_bytes(D) + kv4_v_off(D) + d * 8);
+              const uint4 s0 = lds128u(vsl + blk * 32), s1 = lds128u(vsl + blk * 32 + 16);
+              widen8(w.x, s0.x, s0.y, s0.z, s0.w, r + 8 * i);
+              widen8(w.y, s1.x, s1.y, s1.z, s1.w, r + 8 * i + 4);
+            }
+            tmem_store16(tmem + lanes + kColV + buf * 64 + c * 16, r);
+          }
+          tmem_wait_stores();
+          tmem_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(v_ready + buf);
+            mbar_arrive(empty + st);
+          }
+        }
+      }
+      if (!ok) {
+        raise_error(p.err, kErrTimeout);
+        *abort_flag = 1;
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int quad = warp - 12;
+    const int key = quad * 32 + lane;  // of the tile; the channel at the end of a piece
+    const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+    float* red = reinterpret_cast<float*>(smem + C::kRedOff);
+    float* scratch = reinterpret_cast<float*>(smem + C::kMergeOff) + quad * 128;
+    Groups gr;
+    gr.g = p.g;
+    gr.gpad = p.gpad;
+    gr.nsub = p.nsub;
+    gr.hv = p.hv;
+    const bool balanced = p.n_splits == 0, fused = p.counters != nullptr;
+    const float vup = pow2i(kv.v_exp);
+    pdl_wait();  // before the first write
+    // Balanced plan: sequences with no keys own no tile; CTA b % grid writes their outputs.
+    if (balanced) {
+      for (int32_t b = blockIdx.x; b < p.B; b += gridDim.x) {
+        if (tl.len(b) != 0) continue;
+        for (int i = tid - 384; i < p.Hq * D; i += 128) p.out[(size_t)b * p.Hq * D + i] = 0.f;
+        if (p.lse)
+          for (int i = tid - 384; i < p.Hq; i += 128) p.lse[(size_t)b * p.Hq + i] = -INFINITY;
+      }
+    }
+    uint32_t g = 0, e = 0, f = 0;
+    KvPiece pc;
+    for (;; ++e) {
+      const bool more = next_piece(e, pc);
+      if (softmax_vote(!more) != 0) break;  // together: the last piece, or a wait that ran out
+      int32_t head0, nh;
+      vkv_heads(gr, pc.vkv, &head0, &nh);
+      const int32_t n = tiles_of(pc);
+      float mr[G], l[G], fac[G];
+      int32_t lim[G];
+#pragma unroll
+      for (int h = 0; h < G; ++h) {
+        mr[h] = -INFINITY;
+        l[h] = 0.f;
+        fac[h] = 0.f;
+        lim[h] = 0;
+      }
+      bool run = ok && n > 0;
+      if (run) {
+        const uint32_t qb = f & 1;
+        const bool got = wait.warp(q_ready + qb, (f >> 1) & 1);
+        if (softmax_vote(!got) != 0) {
+          ok = run = false;
+        } else {
+          const float* factor = reinterpret_cast<const float*>(smem + C::kMetaOff + qb * C::kMetaBytes);
+          const int32_t* limit = reinterpret_cast<const int32_t*>(factor + 16);
+#pragma unroll
+          for (int h = 0; h < G; ++h) {
+            fac[h] = factor[h];
+            lim[h] = limit[h];
+            if (h >= nh) mr[h] = 0.f;  // idle columns: S = 0, p = 1, never published
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(q_free + qb);
+          ++f;
+        }
+      }
+      int32_t lim_min = 0x7fffffff;
+#pragma unroll
+      for (int h = 0; h < G; ++h) lim_min = min(lim_min, lim[h]);
+      for (int32_t j = 0; run && j < n; ++j, ++g) {
+        const uint32_t buf = g & 1;
+        const int32_t t0 = pc.tok_begin + j * kTile, t = t0 + key;
+        const bool got = wait.warp(s_full + buf, (g >> 1) & 1);
+        tmem_fence_after();
+        float s[N];
+        const bool whole = t0 + kTile <= lim_min && t0 + kTile <= pc.tok_end;
+        bool up = false;
+        if (got) {
+#pragma unroll
+          for (int c = 0; c < N; c += 16) tmem_load16(tmem + lanes + kColS + buf * 32 + c, s + c);
+#pragma unroll
+          for (int h = 0; h < G; ++h) {
+            s[h] = (s[h] + s[H + h]) * fac[h];
+            if (!whole && (t >= lim[h] || t >= pc.tok_end)) s[h] = -INFINITY;
+            up |= s[h] - mr[h] > kRefDown + kTau;
+          }
+        }
+        // one vote a warp for a score above its reference, 24 for a wait that ran out
+        const bool any_up = __any_sync(0xffffffffu, up);
+        const uint32_t votes = softmax_vote(got ? any_up && lane == 0 : lane >= 8);
+        if (votes >= 24) {
+          ok = run = false;
+          break;
+        }
+        if (votes != 0) {
+          // the reference moves: maxima of the tile, then l and O on the new one
+#pragma unroll
+          for (int h = 0; h < G; ++h) {
+            const float mx = warp_max(s[h]);
+            if (lane == 0) red[quad * 16 + h] = mx;
+          }
+          softmax_sync();
+          float alpha[G];
+#pragma unroll
+          for (int h = 0; h < G; ++h) {
+            const float mx = fmaxf(fmaxf(red[h], red[16 + h]), fmaxf(red[32 + h], red[48 + h])) - kRefDown;
+            const float mn = fmaxf(mr[h], mx);
+            alpha[h] = mn == -INFINITY ? 1.f : ex2(mr[h] - mn);
+            mr[h] = mn;
+            l[h] *= alpha[h];
+          }
+          bool moved = true;
+          if (j > 0) {
+            moved = wait.warp(pv_done + ((g - 1) & 1), ((g - 1) >> 1) & 1);
+            if (moved) {
+              tmem_fence_after();
+              float o[16];
+#pragma unroll
+              for (int c = 0; c < N; c += 16) {
+                tmem_load16(tmem + lanes + kColO + c, o);
+                uint32_t r[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) r[i] = __float_as_uint((c + i) % H < G ? o[i] * alpha[(c + i) % H % G] : o[i]);
+                tmem_store16(tmem + lanes + kColO + c, r);
+              }
+              tmem_wait_stores();
+            }
+          }
+          if (softmax_vote(!moved) != 0) {  // red is free again, too
+            ok = run = false;
+            break;
+          }
+        }
+        // p's buffer: O of tile g - 2 has been computed
+        const bool free_p = g < 2 || wait.warp(pv_done + buf, ((g >> 1) & 1) ^ 1);
+        if (free_p) {
+          const uint32_t ps = sbase + C::kPOff + buf * C::kPBytes;
+          float x[G < 2 ? 2 : G];
+#pragma unroll
+          for (int h = 0; h < G; ++h) {
+            const float ref = mr[h] == -INFINITY ? 0.f : mr[h];
+            x[h] = ex2(s[h] - ref);
+            l[h] += x[h];
+          }
+          if constexpr (G == 1) x[1] = 0.f;
+#pragma unroll
+          for (int h = 0; h < G; h += 2) {
+            uint32_t hi, lo;
+            split_f16x2(x[h], x[h + 1], hi, lo);
+            sts16(ps + b_off<N>(h, key), hi);
+            sts16(ps + b_off<N>(H + h, key), lo);
+            if (G > 1) {
+              sts16(ps + b_off<N>(h + 1, key), hi >> 16);
+              sts16(ps + b_off<N>(H + h + 1, key), lo >> 16);
+            }
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        } else {
+          *abort_flag = 1;  // seen by this group at its next wait
+        }
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_ready + buf);
+      }
+      // ---- end of the piece: sums over the keys, O by channel
+      if (run) {
+        const uint32_t gl = g - 1;
+        const bool got = wait.warp(pv_done + (gl & 1), (gl >> 1) & 1);
+        if (softmax_vote(!got) != 0) ok = run = false;
+      }
+      float o[N];
+#pragma unroll
+      for (int c = 0; c < N; ++c) o[c] = 0.f;
+      if (run) {
+        tmem_fence_after();
+#pragma unroll
+        for (int c = 0; c < N; c += 16) tmem_load16(tmem + lanes + kColO + c, o + c);
+        tmem_fence_before();
+      }
+#pragma unroll
+      for (int h = 0; h < G; ++h) {
+        const float ls = warp_sum(l[h]);
+        if (lane == 0) red[quad * 16 + h] = ls;
+      }
+      softmax_sync();
+      const int32_t pair = pc.b * p.hv + pc.vkv;
+      const bool final_here = fused && pc.npieces == 1;
+#pragma unroll
+      for (int h = 0; h < G; ++h) {
+        if (h >= nh) break;
+        const float L = (red[h] + red[16 + h]) + (red[32 + h] + red[48 + h]);
+        const float acc = (o[h] + o[H + h]) * vup;
+        const size_t row = (size_t)pc.b * p.Hq + head0 + h;
+        if (final_here) {
+          if (key < D) p.out[row * D + key] = L == 0.f ? 0.f : acc / L;
+          if (p.lse && key == 0) p.lse[row] = L == 0.f ? -INFINITY : (mr[h] + log2f(L)) * kLn2;
+        } else {
+          const size_t i = balanced ? (size_t)pc.slot * p.gpad + h : row * p.n_splits + pc.slot;
+          if (key < D) p.o_part[i * D + key] = acc;
+          if (key == 0) {
+            // The merge passes over states whose l is not above zero.  A NaN sum goes in as
+            // m = inf: the weight exp(inf - inf) then makes out and lse NaN, as the formula does.
+            p.m_part[i] = isnan(L) ? INFINITY : (L == 0.f ? -INFINITY : mr[h] * kLn2);
+            p.l_part[i] = isnan(L) ? 1.f : L;
+          }
+        }
+      }
+      softmax_sync();  // the partials are written, red is read
+      if (fused && !final_here) {
+        if (tid == 384) *last_flag = atomic_add_acq_rel(p.counters + pair, 1) == pc.npieces - 1 ? 1 : 0;
+        softmax_sync();
+        if (*last_flag) {
+          const size_t base0 = balanced ? (size_t)(pair + pc.first) * p.gpad : ((size_t)pc.b * p.Hq + head0) * p.n_splits;
+          const size_t hs = balanced ? 1 : (size_t)p.n_splits, stride = balanced ? p.gpad : 1;
+          for (int h = quad; h < nh; h += 4) {
+            const GlobalPartials<D> src{p.o_part, p.m_part, p.l_part, base0 + h * hs, stride};
+            const size_t row = (size_t)pc.b * p.Hq + head0 + h;
+            merge_head<D>(src, balanced ? pc.npieces : p.n_splits, p.out + row * D, p.lse ? p.lse + row : nullptr, lane,
+                          scratch);
+          }
+          if (tid == 384) p.counters[pair] = 0;  // ready for the next call
+        }
+        softmax_sync();
+      }
+    }
+    if (!ok) {
+      raise_error(p.err, kErrTimeout);
+      *abort_flag = 1;
     }
   }
+  tmem_fence_before();
+  cta_sync();
+  if (warp == 1) {
+    tmem_fence_after();
+    tmem_free_all(tmem);
+  }
+}
+
+template <int D, int G>
+cudaError_t launch_t(const Kv4View& kv, const SplitParams& p, dim3 grid, cudaStream_t stream) {
+  using C = K4<D, G>;
+  static std::atomic<int> configured_device{-1};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (configured_device.load(std::memory_order_acquire) != dev) {
+    e = cudaFuncSetAttribute(fd_kv4_kernel<D, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    configured_device.store(dev, std::memory_order_release);
+  }
+  Kv4Params pp;
+  pp.p = p;
+  pp.kv = kv;
+  // Programmatic dependent launch: set-up overlaps the kernel before; every role
+  // waits for it before its first access to global memory.
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fd_kv4_kernel<D, G>, pp);
 }
 
 }  // namespace
 
 cudaError_t launch_kv4_split(int D, const Kv4View& kv, const SplitParams& p, dim3 grid, cudaStream_t stream) {
-  if (D == 128)
-    fd_kv4_split_kernel<128><<<grid, 128, 0, stream>>>(kv, p);
-  else
-    fd_kv4_split_kernel<64><<<grid, 128, 0, stream>>>(kv, p);
-  return cudaGetLastError();
+#define FD_CASE(DD, GG) \
+  if (D == DD && p.gpad == GG) return launch_t<DD, GG>(kv, p, grid, stream);
+  FD_CASE(128, 1) FD_CASE(128, 2) FD_CASE(128, 4) FD_CASE(128, 8) FD_CASE(128, 16)
+  FD_CASE(64, 1) FD_CASE(64, 2) FD_CASE(64, 4) FD_CASE(64, 8) FD_CASE(64, 16)
+#undef FD_CASE
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace fdk
