@@ -22,19 +22,27 @@
 // as many as the widening: measured 8.4 slots for a 16x8x16 step), and with heads
 // on the N axis their time does not grow with the group.
 //
-// Sixteen warps:
+// Twenty-eight warps:
 //   0      walks the plan, announces pieces, copies tiles (one bulk copy for a
 //          contiguous run, one per block when paged) into a ring of stages;
-//   1      one thread issues the MMAs: S(g), then O of tile g - 1;
-//   2, 3   q of the next piece: scaled to the fp16 range by a power of two per
+//   1, 2   one thread of each issues MMAs: S, and O (each MMA takes some 30
+//          cycles to issue, and a tile needs eight of each kind);
+//   3      q of the next piece: scaled to the fp16 range by a power of two per
 //          head, split hi / lo, written in the B layout;
-//   4-7    K: lane = key;   8-11  V: lane = channel;
-//   12-15  softmax: lane = key; at the end of a piece lane = channel.
+//   4-11   K, two groups of four warps: lane = key;
+//   12-19  V, two groups: lane = channel;
+//   20-27  softmax, two groups: lane = key; at the end of a piece lane = channel.
+// Group 0 of each role takes the even tiles and group 1 the odd ones, so that
+// a tile's latency (shared memory, conversions, tensor-memory stores, barriers)
+// may be two tiles long.  The softmax groups share nothing within a piece:
+// each has its reference, its sums and its O in tensor memory, and the two
+// states are joined at the piece's end.
 // Every mbarrier wait is bounded; a wait that runs out raises the error word and
 // the CTA still counts its pieces, so that the workspace stays valid.
 #include <cuda_fp16.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "fd_internal.h"
 #include "fd_kv4.cuh"
@@ -47,15 +55,24 @@ namespace {
 constexpr int kTile = kPlanTile;                       // keys per tile: the M of S^T
 constexpr int kTileBlocks = kTile / kKv4Tokens;
 constexpr int kDescs = 4;                              // pieces announced ahead
-constexpr int kThreads = 512;
+constexpr int kThreads = 896;
 // p is held in fp16: the reference of the exponent lies kRefDown below the
 // running maximum and moves when a score exceeds that maximum by kTau, so p <=
 // 2^(kRefDown + kTau) = 2^15, and the smallest fp16 number stands for 2^-33 of the
 // maximum's weight.
 constexpr float kRefDown = 9.f, kTau = 6.f;
 
-// Tensor-memory columns: K and V (two buffers each), S (two), O.
-constexpr uint32_t kColK = 0, kColV = 128, kColS = 256, kColO = 320;
+// Position in a ring of NB buffers: tile g is in buffer g % NB, its phase (g / NB) & 1.
+template <uint32_t NB>
+struct Ring {
+  uint32_t i = 0, ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++i == NB) {
+      i = 0;
+      ph ^= 1u;
+    }
+  }
+};
 
 struct KvPiece {
   int32_t b, vkv, tok_begin, tok_end, slot, len, npieces, first;
@@ -65,25 +82,33 @@ template <int D, int G>
 struct K4 {
   static constexpr int kHalf = G <= 8 ? 8 : 16;   // heads as columns: hi, then lo
   static constexpr int kN = 2 * kHalf;
+  // Buffers: K and V in tensor memory (64 columns each for D = 128), S there and p
+  // in shared memory.  With two of each, a group's next tile waited for the
+  // whole chain of its last one (S, softmax, O): 1125 cycles a tile, 128k tokens 43 us.
+  static constexpr uint32_t kKBufs = 3, kVBufs = G <= 8 ? 3 : 2, kSBufs = 4;
+  static constexpr uint32_t kColK = 0, kColV = kColK + kKBufs * (D / 2), kColS = kColV + kVBufs * (kTile / 2),
+                            kColO = kColS + kSBufs * kN;  // O: one per softmax group
+  static_assert(kColO + 2 * kN <= 512, "tensor memory");
   static constexpr int kStageBytes = kTileBlocks * kv4_block_bytes(D);
-  static constexpr int kStages = D == 128 ? 8 : 14;
+  static constexpr int kStages = D == 128 ? 8 : 12;
   static constexpr int kVWarps = D / 32;
   static constexpr int kQBytes = kN * D * 2;
   static constexpr int kPBytes = kN * kTile * 2;
   // byte offsets from a 1024-aligned base
   static constexpr int kQOff = 0;
   static constexpr int kPOff = kQOff + 2 * kQBytes;
-  static constexpr int kStageOff = kPOff + 2 * kPBytes;
-  static constexpr int kVsOff = kStageOff + kStages * kStageBytes;   // V scales as fp16: [4 warps][2][128]
-  static constexpr int kRedOff = kVsOff + 4 * 2 * kTile * 2;         // [4 warps][G] maxima or sums
-  static constexpr int kMergeOff = kRedOff + 4 * 16 * 4;             // merge scratch: [4 warps][128]
-  static constexpr int kMetaOff = kMergeOff + 4 * 128 * 4;           // per q buffer: factor[16], limit[16], least limit
-  static constexpr int kMetaBytes = 16 * 8 + 16;
+  static constexpr int kStageOff = kPOff + kSBufs * kPBytes;
+  static constexpr int kVsOff = kStageOff + kStages * kStageBytes;   // V scales as fp16: [8 warps][2][128]
+  static constexpr int kRedOff = kVsOff + 8 * 2 * kTile * 2;         // [2 groups][4 warps][16] maxima or sums
+  static constexpr int kFacOff = kRedOff + 2 * 4 * 16 * 4;           // [2 groups][16] score factors
+  static constexpr int kJoinOff = kFacOff + 2 * 16 * 4;              // group 1's state: [16] m, [16] l, [G][D] O
+  static constexpr int kMetaOff = kJoinOff + 32 * 4 + G * D * 4;     // per q buffer: factor[16], least limit
+  static constexpr int kMetaBytes = 16 * 4 + 16;
   static constexpr int kDescOff = kMetaOff + 2 * kMetaBytes;
   static constexpr int kLenOff = kDescOff + kDescs * (int)sizeof(KvPiece);
   static constexpr int kPreOff = kLenOff + (kAutoMaxBatch + 4) * 4;
   static constexpr int kBarOff = kPreOff + (kAutoMaxBatch + 4) * 4;
-  static constexpr int kBars = 2 * kStages + 2 * kDescs + 2 * 5 + 4 + 1;
+  static constexpr int kBars = 2 * kStages + 2 * kDescs + 2 * kKBufs + 2 * kVBufs + 3 * kSBufs + 4 + 1;
   static constexpr int kFlagOff = kBarOff + kBars * 8;
   static constexpr int kSmem = kFlagOff + 16 + 1024;
   static_assert(kSmem <= 232448 && kSmem > 118784, "one CTA per SM: each takes all of tensor memory");
@@ -121,6 +146,11 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ uint32_t lds16u(uint32_t at) {
+  unsigned short v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
+  return v;
+}
 __device__ __forceinline__ void sts16(uint32_t at, uint32_t v) {
   asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"((unsigned short)v) : "memory");
 }
@@ -137,24 +167,89 @@ __device__ __forceinline__ void split_f16x2(float x0, float x1, uint32_t& hi, ui
   lo = *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// Barrier of the four softmax warps that counts raised predicates.
-__device__ __forceinline__ uint32_t softmax_vote(bool pred) {
+// Barrier of a softmax group (id 2 or 3, 128 threads) or of both (id 1, 256)
+// that counts raised predicates.
+__device__ __forceinline__ uint32_t vote(uint32_t id, uint32_t threads, bool pred) {
   uint32_t n;
   __syncwarp();
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.popc.u32 %0, 1, 128, p;\n\t}"
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.popc.u32 %0, %2, %3, p;\n\t}"
                : "=r"(n)
-               : "r"((uint32_t)pred)
+               : "r"((uint32_t)pred), "r"(id), "r"(threads)
                : "memory");
   return n;
 }
-__device__ __forceinline__ void softmax_sync() { named_barrier(1, 128); }
+
+// One lane of a converged warp, known as such to the compiler: the operands of
+// the MMAs then stay in uniform registers (with a lane test each MMA took 70
+// issue cycles to set up, 128k tokens 70 us against 52).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// Join of the partial states of one head by one warp: M = max m, weights
+// exp(m_k - M) over the states with l > 0, out = sum w O / L, lse = M + ln L.
+// State k is partial index base + k * stride.  Thirty-two states' weights at a
+// time, their O slices in batches of eight loads, in a fixed order.
+template <int D>
+__device__ __forceinline__ void join_states(const SplitParams& p, size_t base, size_t stride, int count, float* out,
+                                            float* lse, int lane) {
+  constexpr int E = D / 32;
+  float mx = -INFINITY;
+  for (int k = lane; k < count; k += 32)
+    if (__ldcg(p.l_part + base + k * stride) > 0.f) mx = fmaxf(mx, __ldcg(p.m_part + base + k * stride));
+  mx = warp_max(mx);
+  float acc[E], L = 0.f;
+#pragma unroll
+  for (int i = 0; i < E; ++i) acc[i] = 0.f;
+  if (mx != -INFINITY) {
+    for (int k0 = 0; k0 < count; k0 += 32) {
+      const int k = k0 + lane;
+      float w = 0.f;
+      if (k < count) {
+        const float l = __ldcg(p.l_part + base + k * stride);
+        if (l > 0.f) {
+          w = exp2f((__ldcg(p.m_part + base + k * stride) - mx) * kLog2e);
+          L = fmaf(w, l, L);
+        }
+      }
+      const int m = count - k0 < 32 ? count - k0 : 32;
+      for (int j0 = 0; j0 < m; j0 += 8) {
+        float v[8][E];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+#pragma unroll
+          for (int i = 0; i < E; ++i) v[j][i] = 0.f;
+          if (j0 + j < m) load_slice<D>(p.o_part + (base + (k0 + j0 + j) * stride) * D + lane * E, v[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float wj = __shfl_sync(0xffffffffu, w, (j0 + j) & 31);
+#pragma unroll
+          for (int i = 0; i < E; ++i) acc[i] = fmaf(wj, v[j][i], acc[i]);
+        }
+      }
+    }
+    L = warp_sum(L);
+  }
+#pragma unroll
+  for (int i = 0; i < E; ++i) out[lane * E + i] = mx == -INFINITY ? 0.f : acc[i] / L;
+  if (lse && lane == 0) *lse = mx == -INFINITY ? -INFINITY : mx + logf(L);
+}
+
+// The part of a wait that is not complete at once, out of the way of the tile loops.
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned long long limit) {
+  return !*abort_flag && mbar_wait_for(bar, parity, limit);
+}
 
 // Waits of one warp (all lanes together): false when the CTA aborts or the limit passes.
 struct Waiter {
   volatile int* abort_flag;
   unsigned long long limit;
   __device__ __forceinline__ bool one(uint64_t* bar, uint32_t parity) const {
-    return mbar_try_wait(bar, parity) || (!*abort_flag && mbar_wait_for(bar, parity, limit));
+    return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort_flag, limit);
   }
   __device__ __forceinline__ bool warp(uint64_t* bar, uint32_t parity) const {
     return __all_sync(0xffffffffu, one(bar, parity));
@@ -176,12 +271,14 @@ __global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_consta
   uint64_t* empty = full + C::kStages;
   uint64_t* desc_full = empty + C::kStages;
   uint64_t* desc_empty = desc_full + kDescs;
-  uint64_t* k_ready = desc_empty + kDescs;  // [2] each of the tile's buffers
-  uint64_t* s_full = k_ready + 2;           // [2] S is there; K's buffer is free
-  uint64_t* p_ready = s_full + 2;           // [2]
-  uint64_t* v_ready = p_ready + 2;          // [2]
-  uint64_t* pv_done = v_ready + 2;          // [2] V's and p's buffers are free
-  uint64_t* q_ready = pv_done + 2;          // [2]
+  uint64_t* k_ready = desc_empty + kDescs;  // [kKBufs] K is in tensor memory
+  uint64_t* k_free = k_ready + C::kKBufs;   // S of it has been computed
+  uint64_t* v_ready = k_free + C::kKBufs;   // [kVBufs]
+  uint64_t* v_free = v_ready + C::kVBufs;
+  uint64_t* s_full = v_free + C::kVBufs;    // [kSBufs]
+  uint64_t* p_ready = s_full + C::kSBufs;   // [kSBufs] p is there, and S has been read
+  uint64_t* p_free = p_ready + C::kSBufs;   // [kSBufs] O with it has been computed
+  uint64_t* q_ready = p_free + C::kSBufs;   // [2]
   uint64_t* q_free = q_ready + 2;           // [2]
   uint64_t* drain = q_free + 2;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kFlagOff);
@@ -198,18 +295,26 @@ __global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_consta
     }
     for (int s = 0; s < kDescs; ++s) {
       mbar_init(desc_full + s, 1);
-      mbar_init(desc_empty + s, 1 + 2 + 4 + C::kVWarps + 4);
+      mbar_init(desc_empty + s, 2 + 1 + 8 + 2 * C::kVWarps + 8);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (uint32_t i = 0; i < C::kKBufs; ++i) {
       mbar_init(k_ready + i, 4);
+      mbar_init(k_free + i, 1);
+    }
+    for (uint32_t i = 0; i < C::kVBufs; ++i) {
+      mbar_init(v_ready + i, C::kVWarps);
+      mbar_init(v_free + i, 1);
+    }
+    for (uint32_t i = 0; i < C::kSBufs; ++i) {
       mbar_init(s_full + i, 1);
       mbar_init(p_ready + i, 4);
-      mbar_init(v_ready + i, C::kVWarps);
-      mbar_init(pv_done + i, 1);
-      mbar_init(q_ready + i, 2);
-      mbar_init(q_free + i, 1 + 4);
+      mbar_init(p_free + i, 1);
     }
-    mbar_init(drain, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(q_ready + i, 1);
+      mbar_init(q_free + i, 1 + 8);
+    }
+    mbar_init(drain, 2);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -278,6 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_consta
     PieceIter pieces(p, tl, total);
     Piece pc;
     uint32_t it = 0, e = 0, stalled = 0xffffffffu;
+    Ring<C::kStages> st;
     bool live = true;  // the other roles still take pieces
     pdl_wait();
     const auto announce = [&](const KvPiece& d) {
@@ -327,11 +433,10 @@ __global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_consta
         nxt = page_of(blk0 + 32 + lane);
       }
       const int32_t n = tiles_of(d);
-      for (int32_t j = 0; j < n; ++j, ++it) {
-        const uint32_t st = it % C::kStages;
+      for (int32_t j = 0; j < n; ++j, ++it, st.next()) {
         const int32_t nblk = blk1 - (blk0 + j * kTileBlocks) < kTileBlocks ? blk1 - (blk0 + j * kTileBlocks) : kTileBlocks;
         const bool stall = p.stall_it >= 0 && it == (uint32_t)p.stall_it;
-        if (!wait.warp(empty + st, ((it / C::kStages) & 1) ^ 1)) {
+        if (!wait.warp(empty + st.i, st.ph ^ 1)) {
           ok = false;
           break;
         }
@@ -339,16 +444,16 @@ __global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_consta
           stalled = it;
           continue;
         }
-        uint8_t* dst = smem + C::kStageOff + st * C::kStageBytes;
+        uint8_t* dst = smem + C::kStageOff + st.i * C::kStageBytes;
         if (!kv.paged) {
           if (lane == 0) {
             const uint32_t bytes = (uint32_t)nblk * kv4_block_bytes(D);
-            mbar_arrive_expect_tx(full + st, bytes);
+            mbar_arrive_expect_tx(full + st.i, bytes);
             const uint8_t* src = base + (int64_t)j * C::kStageBytes;
             asm volatile(
                 "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
                     smem_addr(dst)),
-                "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_addr(full + st)), "l"(stream_policy)
+                "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_addr(full + st.i)), "l"(stream_policy)
                 : "memory");
           }
         } else {
@@ -365,12 +470,12 @@ __global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_consta
           }
           __syncwarp();
           const uint32_t copies = __popc(__ballot_sync(0xffffffffu, mine && !bad));
-          if (lane == 0) mbar_arrive_expect_tx(full + st, copies * kv4_block_bytes(D));
+          if (lane == 0) mbar_arrive_expect_tx(full + st.i, copies * kv4_block_bytes(D));
           __syncwarp();
           if (mine && !bad) {
             const int32_t blk = blk0 + j * kTileBlocks + k;
             const int64_t idx = ((int64_t)cur * kv.Hkv + kvh) * ppb + blk % ppb;
-            bulk_load(dst + k * kv4_block_bytes(D), kv.kv + idx * kv4_block_bytes(D), kv4_block_bytes(D), full + st);
+            bulk_load(dst + k * kv4_block_bytes(D), kv.kv + idx * kv4_block_bytes(D), kv4_block_bytes(D), full + st.i);
           }
           if ((j & 3) == 3) {
             cur = nxt;
@@ -395,67 +500,78 @@ __global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_consta
         if (j != stalled && !mbar_wait_for(full + j % C::kStages, (j / C::kStages) & 1, wait.limit))
           raise_error(p.err, kErrTimeout);
     }
-  } else if (warp == 1) {
+  } else if (warp < 3) {
     // ------------------------------------------------------------ MMA issue
+    // Every branch and operand here is uniform over the warp as the compiler sees it
+    // (votes and shuffles): only then do the MMAs take their operands from uniform
+    // registers as they are (18 cycles each to issue; 70 to 130 otherwise).
     constexpr uint32_t idesc = f16_instr_desc(kTile, N);
-    uint32_t g = 0, e = 0, f = 0;  // tiles, pieces, pieces with tiles
-    int32_t j_prev = -1;           // number within its piece of the tile whose O is owed
-    const auto issue_o = [&](uint32_t gt, int32_t j) {
-      const uint32_t buf = gt & 1, ph = (gt >> 1) & 1;
-      if (!wait.warp(v_ready + buf, ph) || !wait.warp(p_ready + buf, ph)) return false;
-      tmem_fence_after();
-      if (lane == 0) {
-        const uint32_t ps = sbase + C::kPOff + buf * C::kPBytes;
+    const uint32_t base = uniform(tmem), sb = uniform(sbase);
+    const bool is_s = uniform(warp) == 1;
+    // A eight columns on per K = 16 step, B 32 bytes on within a swizzled row, then
+    // the next column block
+    const auto issue = [&](uint32_t d, uint32_t a, uint32_t b, auto steps, uint32_t acc) {
 #pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk)
-          mma_ts(tmem + kColO, tmem + kColV + buf * 64 + kk * 8, b_desc(ps + (kk >> 2) * (N * 128) + (kk & 3) * 32), idesc,
-                 j > 0 || kk > 0);
-        mma_commit(smem_addr(pv_done + buf));
-      }
-      __syncwarp();
-      return true;
+      for (int kk = 0; kk < decltype(steps)::value; ++kk)
+        mma_ts(d, a + kk * 8, b_desc(b + (kk >> 2) * (N * 128) + (kk & 3) * 32), idesc, kk > 0 ? 1u : acc);
     };
-    KvPiece pc;
-    for (; next_piece(e, pc); ++e) {
-      const int32_t n = tiles_of(pc);
-      if (!ok || n == 0) continue;
-      const uint32_t qb = f & 1;
-      if (!wait.warp(q_ready + qb, (f >> 1) & 1)) ok = false;
+    uint32_t g = 0, f = 0;  // tiles, pieces with tiles
+    Ring<C::kKBufs> kr;
+    Ring<C::kVBufs> vr;
+    Ring<C::kSBufs> sr;
+    for (uint32_t e = 0;; ++e) {
+      KvPiece pc;
+      if (!__all_sync(0xffffffffu, next_piece(e, pc))) break;
+      const int32_t n = ok ? (int32_t)uniform(tiles_of(pc)) : 0;
+      if (n == 0) continue;
+      if (is_s && !wait.warp(q_ready + (f & 1), (f >> 1) & 1)) ok = false;
       for (int32_t j = 0; ok && j < n; ++j, ++g) {
-        const uint32_t buf = g & 1;
-        if (!wait.warp(k_ready + buf, (g >> 1) & 1)) {
-          ok = false;
-          break;
-        }
-        tmem_fence_after();
-        if (lane == 0) {
-          const uint32_t qs = sbase + C::kQOff + qb * C::kQBytes;
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_ts(tmem + kColS + buf * 32, tmem + kColK + buf * 64 + kk * 8,
-                   b_desc(qs + (kk >> 2) * (N * 128) + (kk & 3) * 32), idesc, kk > 0);
-          mma_commit(smem_addr(s_full + buf));
-          if (j == n - 1) mma_commit(smem_addr(q_free + qb));
+        if (is_s) {
+          // K is there, and the softmax has read what the S buffer held
+          if (!wait.warp(k_ready + kr.i, kr.ph) || (g >= C::kSBufs && !wait.warp(p_ready + sr.i, sr.ph ^ 1))) {
+            ok = false;
+            break;
+          }
+          tmem_fence_after();
+          const uint32_t qb = f & 1;
+          if (elect_one()) {
+            issue(base + C::kColS + sr.i * N, base + C::kColK + kr.i * (D / 2), sb + C::kQOff + qb * C::kQBytes,
+                  std::integral_constant<int, D / 16>{}, 0);
+            mma_commit(smem_addr(s_full + sr.i));
+            mma_commit(smem_addr(k_free + kr.i));
+            if (j == n - 1) mma_commit(smem_addr(q_free + qb));
+          }
+        } else {
+          if (!wait.warp(v_ready + vr.i, vr.ph) || !wait.warp(p_ready + sr.i, sr.ph)) {
+            ok = false;
+            break;
+          }
+          tmem_fence_after();
+          if (elect_one()) {
+            // the group's first tile of the piece starts its O
+            issue(base + C::kColO + (g & 1) * N, base + C::kColV + vr.i * (kTile / 2), sb + C::kPOff + sr.i * C::kPBytes,
+                  std::integral_constant<int, kTile / 16>{}, j > 1 ? 1u : 0u);
+            mma_commit(smem_addr(p_free + sr.i));
+            mma_commit(smem_addr(v_free + vr.i));
+          }
         }
         __syncwarp();
-        if (g > 0 && !issue_o(g - 1, j_prev)) {
-          ok = false;
-          break;
-        }
-        j_prev = j;
+        kr.next();
+        vr.next();
+        sr.next();
       }
       ++f;
     }
-    if (ok && g > 0 && !issue_o(g - 1, j_prev)) ok = false;
     if (!ok) {
       raise_error(p.err, kErrTimeout);
       *abort_flag = 1;
     }
     // every MMA has finished before tensor memory goes back
-    if (lane == 0) {
+    if (elect_one()) {
       mma_commit(smem_addr(drain));
       if (!mbar_wait_for(drain, 0, wait.limit)) raise_error(p.err, kErrTimeout);
     }
+    __syncwarp();
   } else if (warp < 4) {
     // ------------------------------------------------------------ q
     Groups gr;
@@ -477,36 +593,44 @@ __global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_consta
       vkv_heads(gr, pc.vkv, &head0, &nh);
       const RowLimits rl{head0, nh, pc.len, p.n_q, p.causal};
       float* factor = reinterpret_cast<float*>(smem + C::kMetaOff + qb * C::kMetaBytes);
-      int32_t* limit = reinterpret_cast<int32_t*>(factor + 16);
       const uint32_t qs = sbase + C::kQOff + qb * C::kQBytes;
-      constexpr int E = D / 32;
-      for (int h = warp - 2; h < H; h += 2) {
-        float x[E];
-        float big = 0.f;
+      constexpr int E = D / 32, kBatch = 8;
+#pragma unroll 1
+      for (int h0 = 0; h0 < H; h0 += kBatch) {
+        float x[kBatch][E];
 #pragma unroll
-        for (int i = 0; i < E; ++i) x[i] = 0.f;
-        if (h < nh) {
-          load_slice<D>(p.q + ((size_t)pc.b * p.Hq + head0 + h) * D + lane * E, x);
+        for (int k = 0; k < kBatch; ++k) {
 #pragma unroll
-          for (int i = 0; i < E; ++i) big = fmaxf(big, fabsf(x[i]));
+          for (int i = 0; i < E; ++i) x[k][i] = 0.f;
+          if (h0 + k < nh) load_slice<D>(p.q + ((size_t)pc.b * p.Hq + head0 + h0 + k) * D + lane * E, x[k]);
         }
-        big = warp_max(big);
-        // 2^e <= big < 2^(e + 1): q times 2^(13 - e) fills fp16's range
-        int ex = (int)((__float_as_uint(big) >> 23) & 0xffu) - 127;
-        if (big == 0.f || ex > 127) ex = 13;
-        ex = ex < -80 ? -80 : (ex > 80 ? 80 : ex);
-        const float up = pow2i(13 - ex);
 #pragma unroll
-        for (int i = 0; i < E; i += 2) {
-          uint32_t hi, lo;
-          split_f16x2(x[i] * up, x[i + 1] * up, hi, lo);
-          asm volatile("st.shared.u32 [%0], %1;" ::"r"(qs + b_off<N>(h, lane * E + i)), "r"(hi) : "memory");
-          asm volatile("st.shared.u32 [%0], %1;" ::"r"(qs + b_off<N>(H + h, lane * E + i)), "r"(lo) : "memory");
+        for (int k = 0; k < kBatch; ++k) {
+          const int h = h0 + k;
+          float big = 0.f;
+#pragma unroll
+          for (int i = 0; i < E; ++i) big = fmaxf(big, fabsf(x[k][i]));
+          big = warp_max(big);
+          // 2^e <= big < 2^(e + 1): q times 2^(13 - e) fills fp16's range
+          int ex = (int)((__float_as_uint(big) >> 23) & 0xffu) - 127;
+          if (big == 0.f || ex > 127) ex = 13;
+          ex = ex < -80 ? -80 : (ex > 80 ? 80 : ex);
+          const float up = pow2i(13 - ex);
+#pragma unroll
+          for (int i = 0; i < E; i += 2) {
+            uint32_t hi, lo;
+            split_f16x2(x[k][i] * up, x[k][i + 1] * up, hi, lo);
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(qs + b_off<N>(h, lane * E + i)), "r"(hi) : "memory");
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(qs + b_off<N>(H + h, lane * E + i)), "r"(lo) : "memory");
+          }
+          if (lane == 0) factor[h] = h < nh ? p.qk_scale * pow2i(kv.k_exp) * pow2i(ex - 13) : 0.f;
         }
-        if (lane == 0) {
-          factor[h] = h < nh ? p.qk_scale * pow2i(kv.k_exp) * pow2i(ex - 13) : 0.f;
-          limit[h] = h < nh ? rl(h) : 0x7fffffff;
-        }
+      }
+      {  // the fewest keys that a head of the piece sees
+        int32_t least = lane < nh ? rl(lane) : 0x7fffffff;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
+        if (lane == 0) *reinterpret_cast<int32_t*>(factor + 16) = least;
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
@@ -517,57 +641,46 @@ __global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_consta
       raise_error(p.err, kErrTimeout);
       *abort_flag = 1;
     }
-  } else if (warp < 8) {
+  } else if (warp < 12) {
     // ------------------------------------------------------------ K
-    const int quad = warp - 4;
+    const int quad = warp & 3;
+    const uint32_t group = (uint32_t)(warp - 4) >> 2;
     const int row = lane & 15;
     const uint32_t krow = (uint32_t)(quad * 2 + (lane >> 4)) * kv4_block_bytes(D);
     const uint32_t sw = kv4_swizzle(D, row);
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
     uint32_t g = 0, e = 0;
+    Ring<C::kStages> st;
+    Ring<C::kKBufs> kr;
     KvPiece pc;
     for (; next_piece(e, pc); ++e) {
       const int32_t n = ok ? tiles_of(pc) : 0;
-      for (int32_t j = 0; j < n; ++j, ++g) {
-        const uint32_t st = g % C::kStages, buf = g & 1;
-        if (!wait.warp(full + st, (g / C::kStages) & 1) || (g >= 2 && !wait.warp(s_full + buf, ((g >> 1) & 1) ^ 1))) {
+      for (int32_t j = 0; j < n; ++j, ++g, st.next(), kr.next()) {
+        if ((g & 1) != group) continue;
+        if (!wait.warp(full + st.i, st.ph) || (g >= C::kKBufs && !wait.warp(k_free + kr.i, kr.ph ^ 1))) {
           ok = false;
           break;
         }
         tmem_fence_after();
-        const uint32_t base = sbase + C::kStageOff + st * C::kStageBytes + krow;
-        // scales: D / 16 bytes a row
-        uint32_t sc[D / 32];
-        if constexpr (D == 128) {
-          const uint2 b = lds64u(base + kv4_ks_off(D) + row * 8);
-          sc[0] = e4m3x2_f16x2(b.x);
-          sc[1] = e4m3x2_f16x2(b.x >> 16);
-          sc[2] = e4m3x2_f16x2(b.y);
-          sc[3] = e4m3x2_f16x2(b.y >> 16);
-        } else {
-          const uint32_t b = lds32u(base + kv4_ks_off(D) + row * 4);
-          sc[0] = e4m3x2_f16x2(b);
-          sc[1] = e4m3x2_f16x2(b >> 16);
-        }
-        uint4 w[D / 32];
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) w[c] = lds128u(base + row * (D / 2) + ((c ^ sw) << 4));
-#pragma unroll
+        const uint32_t base = sbase + C::kStageOff + st.i * C::kStageBytes + krow;
+#pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
-          const uint32_t a = __byte_perm(sc[c], 0, 0x1010), b = __byte_perm(sc[c], 0, 0x3232);
+          const uint4 w = lds128u(base + row * (D / 2) + ((c ^ sw) << 4));
+          const uint32_t b2 = e4m3x2_f16x2(lds16u(base + kv4_ks_off(D) + row * (D / 16) + 2 * c));
+          const uint32_t s0 = __byte_perm(b2, 0, 0x1010), s1 = __byte_perm(b2, 0, 0x3232);
           uint32_t r[16];
-          widen8(w[c].x, a, a, a, a, r);
-          widen8(w[c].y, a, a, a, a, r + 4);
-          widen8(w[c].z, b, b, b, b, r + 8);
-          widen8(w[c].w, b, b, b, b, r + 12);
-          tmem_store16(tmem + lanes + kColK + buf * 64 + c * 16, r);
+          widen8(w.x, s0, s0, s0, s0, r);
+          widen8(w.y, s0, s0, s0, s0, r + 4);
+          widen8(w.z, s1, s1, s1, s1, r + 8);
+          widen8(w.w, s1, s1, s1, s1, r + 12);
+          tmem_store16(tmem + lanes + C::kColK + kr.i * (D / 2) + c * 16, r);
         }
         tmem_wait_stores();
         tmem_fence_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(k_ready + buf);
-          mbar_arrive(empty + st);
+          mbar_arrive(k_ready + kr.i);
+          mbar_arrive(empty + st.i);
         }
       }
     }
@@ -575,26 +688,29 @@ __global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_consta
       raise_error(p.err, kErrTimeout);
       *abort_flag = 1;
     }
-  } else if (warp < 12) {
+  } else if (warp < 20) {
     // ------------------------------------------------------------ V
-    const int quad = warp - 8;
+    const int quad = warp & 3;
+    const uint32_t group = (uint32_t)(warp - 12) >> 2;
     if (quad < C::kVWarps) {
       const int d = quad * 32 + lane;
       const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-      const uint32_t vs = sbase + C::kVsOff + quad * (2 * kTile * 2);
+      const uint32_t vs = sbase + C::kVsOff + (warp - 12) * (2 * kTile * 2);
       const int sblk = (lane >> 1) & 7, stok = sblk * 16 + (lane & 1) * 8;  // the scales that this lane converts
       uint32_t g = 0, e = 0;
+      Ring<C::kStages> st;
+      Ring<C::kVBufs> vr;
       KvPiece pc;
       for (; next_piece(e, pc); ++e) {
         const int32_t n = ok ? tiles_of(pc) : 0;
-        for (int32_t j = 0; j < n; ++j, ++g) {
-          const uint32_t st = g % C::kStages, buf = g & 1;
-          if (!wait.warp(full + st, (g / C::kStages) & 1) || (g >= 2 && !wait.warp(pv_done + buf, ((g >> 1) & 1) ^ 1))) {
+        for (int32_t j = 0; j < n; ++j, ++g, st.next(), vr.next()) {
+          if ((g & 1) != group) continue;
+          if (!wait.warp(full + st.i, st.ph) || (g >= C::kVBufs && !wait.warp(v_free + vr.i, vr.ph ^ 1))) {
             ok = false;
             break;
           }
           tmem_fence_after();
-          const uint32_t base = sbase + C::kStageOff + st * C::kStageBytes;
+          const uint32_t base = sbase + C::kStageOff + st.i * C::kStageBytes;
           {
             // The warp's two groups of sixteen channels, 128 tokens: scales to fp16,
             // 0 for tokens past the valid ones (0 * anything finite is 0, and codes are finite).
@@ -613,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_consta
           }
           __syncwarp();
           const uint32_t vsl = vs + (lane >> 4) * (kTile * 2);
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < kTileBlocks / 2; ++c) {
             uint32_t r[16];
 #pragma unroll
@@ -624,14 +740,14 @@ __global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_consta
               widen8(w.x, s0.x, s0.y, s0.z, s0.w, r + 8 * i);
               widen8(w.y, s1.x, s1.y, s1.z, s1.w, r + 8 * i + 4);
             }
-            tmem_store16(tmem + lanes + kColV + buf * 64 + c * 16, r);
+            tmem_store16(tmem + lanes + C::kColV + vr.i * (kTile / 2) + c * 16, r);
           }
           tmem_wait_stores();
           tmem_fence_before();
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive(v_ready + buf);
-            mbar_arrive(empty + st);
+            mbar_arrive(v_ready + vr.i);
+            mbar_arrive(empty + st.i);
           }
         }
       }
@@ -642,101 +758,103 @@ __global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_consta
     }
   } else {
     // ------------------------------------------------------------ softmax
-    const int quad = warp - 12;
+    const int quad = warp & 3;
+    const uint32_t group = (uint32_t)(warp - 20) >> 2;
+    const uint32_t bar = 2 + group;  // this group's barrier
     const int key = quad * 32 + lane;  // of the tile; the channel at the end of a piece
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-    float* red = reinterpret_cast<float*>(smem + C::kRedOff);
-    float* scratch = reinterpret_cast<float*>(smem + C::kMergeOff) + quad * 128;
+    float* red = reinterpret_cast<float*>(smem + C::kRedOff) + group * 64;
+    float* fac = reinterpret_cast<float*>(smem + C::kFacOff) + group * 16;
+    float* join = reinterpret_cast<float*>(smem + C::kJoinOff);
+    // This thread's key in row 0 of a p buffer; row n is 128 n bytes on, its
+    // 16-byte chunk turned by n % 8.
+    const uint32_t p_at = sbase + C::kPOff + b_off<N>(0, key);
     Groups gr;
     gr.g = p.g;
     gr.gpad = p.gpad;
     gr.nsub = p.nsub;
     gr.hv = p.hv;
     const bool balanced = p.n_splits == 0, fused = p.counters != nullptr;
-    const float vup = pow2i(kv.v_exp);
     pdl_wait();  // before the first write
     // Balanced plan: sequences with no keys own no tile; CTA b % grid writes their outputs.
     if (balanced) {
       for (int32_t b = blockIdx.x; b < p.B; b += gridDim.x) {
         if (tl.len(b) != 0) continue;
-        for (int i = tid - 384; i < p.Hq * D; i += 128) p.out[(size_t)b * p.Hq * D + i] = 0.f;
+        for (int i = tid - 640; i < p.Hq * D; i += 256) p.out[(size_t)b * p.Hq * D + i] = 0.f;
         if (p.lse)
-          for (int i = tid - 384; i < p.Hq; i += 128) p.lse[(size_t)b * p.Hq + i] = -INFINITY;
+          for (int i = tid - 640; i < p.Hq; i += 256) p.lse[(size_t)b * p.Hq + i] = -INFINITY;
       }
     }
     uint32_t g = 0, e = 0, f = 0;
+    Ring<C::kSBufs> sr, done;  // this tile's buffers, the group's last tile's
     KvPiece pc;
     for (;; ++e) {
       const bool more = next_piece(e, pc);
-      if (softmax_vote(!more) != 0) break;  // together: the last piece, or a wait that ran out
+      if (vote(1, 256, !more) != 0) break;  // together: the last piece, or a wait that ran out
       int32_t head0, nh;
       vkv_heads(gr, pc.vkv, &head0, &nh);
       const int32_t n = tiles_of(pc);
-      float mr[G], l[G], fac[G];
-      int32_t lim[G];
+      float mr[G], l[G];
 #pragma unroll
       for (int h = 0; h < G; ++h) {
-        mr[h] = -INFINITY;
+        // idle columns have S = 0 and never move their reference
+        mr[h] = h < nh ? -INFINITY : 0.f;
         l[h] = 0.f;
-        fac[h] = 0.f;
-        lim[h] = 0;
       }
       bool run = ok && n > 0;
+      int32_t lim_min = 0;
       if (run) {
         const uint32_t qb = f & 1;
         const bool got = wait.warp(q_ready + qb, (f >> 1) & 1);
-        if (softmax_vote(!got) != 0) {
-          ok = run = false;
-        } else {
-          const float* factor = reinterpret_cast<const float*>(smem + C::kMetaOff + qb * C::kMetaBytes);
-          const int32_t* limit = reinterpret_cast<const int32_t*>(factor + 16);
-#pragma unroll
-          for (int h = 0; h < G; ++h) {
-            fac[h] = factor[h];
-            lim[h] = limit[h];
-            if (h >= nh) mr[h] = 0.f;  // idle columns: S = 0, p = 1, never published
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(q_free + qb);
-          ++f;
-        }
+        const float* factor = reinterpret_cast<const float*>(smem + C::kMetaOff + qb * C::kMetaBytes);
+        lim_min = *reinterpret_cast<const int32_t*>(factor + 16);
+        if (quad == 0 && lane < 16) fac[lane] = factor[lane];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_free + qb);
+        ++f;
+        if (vote(bar, 128, !got) != 0) ok = run = false;
       }
-      int32_t lim_min = 0x7fffffff;
-#pragma unroll
-      for (int h = 0; h < G; ++h) lim_min = min(lim_min, lim[h]);
-      for (int32_t j = 0; run && j < n; ++j, ++g) {
-        const uint32_t buf = g & 1;
+      int32_t mine = 0;  // tiles of this group so far
+      for (int32_t j = 0; run && j < n; ++j, ++g, sr.next()) {
+        if ((g & 1) != group) continue;
         const int32_t t0 = pc.tok_begin + j * kTile, t = t0 + key;
-        const bool got = wait.warp(s_full + buf, (g >> 1) & 1);
+        const bool got = wait.warp(s_full + sr.i, sr.ph);
         tmem_fence_after();
-        float s[N];
-        const bool whole = t0 + kTile <= lim_min && t0 + kTile <= pc.tok_end;
+        float s[G < 2 ? 2 : G];
         bool up = false;
         if (got) {
+          const RowLimits rl{head0, nh, pc.len, p.n_q, p.causal};
+          const bool whole = t0 + kTile <= lim_min && t0 + kTile <= pc.tok_end;
+          {
+            float x[N];
 #pragma unroll
-          for (int c = 0; c < N; c += 16) tmem_load16(tmem + lanes + kColS + buf * 32 + c, s + c);
+            for (int c = 0; c < N; c += 16) tmem_load16(tmem + lanes + C::kColS + sr.i * N + c, x + c);
 #pragma unroll
-          for (int h = 0; h < G; ++h) {
-            s[h] = (s[h] + s[H + h]) * fac[h];
-            if (!whole && (t >= lim[h] || t >= pc.tok_end)) s[h] = -INFINITY;
-            up |= s[h] - mr[h] > kRefDown + kTau;
+            for (int h = 0; h < G; ++h) s[h] = (x[h] + x[H + h]) * fac[h];
           }
+          if (__builtin_expect(!whole, 0)) {
+#pragma unroll
+            for (int h = 0; h < G; ++h)
+              if (t >= pc.tok_end || (h < nh && t >= rl(h))) s[h] = -INFINITY;
+          }
+#pragma unroll
+          for (int h = 0; h < G; ++h) up |= s[h] - mr[h] > kRefDown + kTau;
         }
         // one vote a warp for a score above its reference, 24 for a wait that ran out
         const bool any_up = __any_sync(0xffffffffu, up);
-        const uint32_t votes = softmax_vote(got ? any_up && lane == 0 : lane >= 8);
+        const uint32_t votes = vote(bar, 128, got ? any_up && lane == 0 : lane >= 8);
         if (votes >= 24) {
           ok = run = false;
           break;
         }
-        if (votes != 0) {
+        if (__builtin_expect(votes != 0, 0)) {
           // the reference moves: maxima of the tile, then l and O on the new one
 #pragma unroll
           for (int h = 0; h < G; ++h) {
             const float mx = warp_max(s[h]);
             if (lane == 0) red[quad * 16 + h] = mx;
           }
-          softmax_sync();
+          named_barrier(bar, 128);
           float alpha[G];
 #pragma unroll
           for (int h = 0; h < G; ++h) {
@@ -747,48 +865,47 @@ __global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_consta
             l[h] *= alpha[h];
           }
           bool moved = true;
-          if (j > 0) {
-            moved = wait.warp(pv_done + ((g - 1) & 1), ((g - 1) >> 1) & 1);
+          if (mine > 0) {
+            moved = wait.warp(p_free + done.i, done.ph);  // O of this group's last tile
             if (moved) {
               tmem_fence_after();
-              float o[16];
 #pragma unroll
               for (int c = 0; c < N; c += 16) {
-                tmem_load16(tmem + lanes + kColO + c, o);
+                float o[16];
+                tmem_load16(tmem + lanes + C::kColO + group * N + c, o);
                 uint32_t r[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) r[i] = __float_as_uint((c + i) % H < G ? o[i] * alpha[(c + i) % H % G] : o[i]);
-                tmem_store16(tmem + lanes + kColO + c, r);
+                for (int i = 0; i < 16; ++i)
+                  r[i] = __float_as_uint((c + i) % H < G ? o[i] * alpha[(c + i) % H % G] : o[i]);
+                tmem_store16(tmem + lanes + C::kColO + group * N + c, r);
               }
               tmem_wait_stores();
             }
           }
-          if (softmax_vote(!moved) != 0) {  // red is free again, too
+          if (vote(bar, 128, !moved) != 0) {  // red is free again, too
             ok = run = false;
             break;
           }
         }
-        // p's buffer: O of tile g - 2 has been computed
-        const bool free_p = g < 2 || wait.warp(pv_done + buf, ((g >> 1) & 1) ^ 1);
-        if (free_p) {
-          const uint32_t ps = sbase + C::kPOff + buf * C::kPBytes;
-          float x[G < 2 ? 2 : G];
+        // p's buffer: O of what it held has been computed
+        if (g < C::kSBufs || wait.warp(p_free + sr.i, sr.ph ^ 1)) {
+          const uint32_t ps = p_at + sr.i * C::kPBytes;
 #pragma unroll
           for (int h = 0; h < G; ++h) {
-            const float ref = mr[h] == -INFINITY ? 0.f : mr[h];
-            x[h] = ex2(s[h] - ref);
-            l[h] += x[h];
+            s[h] = ex2(s[h] - (mr[h] == -INFINITY ? 0.f : mr[h]));
+            l[h] += s[h];
           }
-          if constexpr (G == 1) x[1] = 0.f;
+          if constexpr (G == 1) s[1] = 0.f;
 #pragma unroll
           for (int h = 0; h < G; h += 2) {
             uint32_t hi, lo;
-            split_f16x2(x[h], x[h + 1], hi, lo);
-            sts16(ps + b_off<N>(h, key), hi);
-            sts16(ps + b_off<N>(H + h, key), lo);
+            split_f16x2(s[h], s[h + 1], hi, lo);
+            const uint32_t a0 = ps ^ ((h & 7) << 4), a1 = ps ^ (((h + 1) & 7) << 4);
+            sts16(a0 + h * 128, hi);
+            sts16(a0 + (H + h) * 128, lo);
             if (G > 1) {
-              sts16(ps + b_off<N>(h + 1, key), hi >> 16);
-              sts16(ps + b_off<N>(H + h + 1, key), lo >> 16);
+              sts16(a1 + (h + 1) * 128, hi >> 16);
+              sts16(a1 + (H + h + 1) * 128, lo >> 16);
             }
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -797,67 +914,90 @@ __global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_consta
         }
         tmem_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_ready + buf);
+        if (lane == 0) mbar_arrive(p_ready + sr.i);
+        done = sr;
+        ++mine;
       }
       // ---- end of the piece: sums over the keys, O by channel
-      if (run) {
-        const uint32_t gl = g - 1;
-        const bool got = wait.warp(pv_done + (gl & 1), (gl >> 1) & 1);
-        if (softmax_vote(!got) != 0) ok = run = false;
-      }
-      float o[N];
+      float o[G];
 #pragma unroll
-      for (int c = 0; c < N; ++c) o[c] = 0.f;
-      if (run) {
-        tmem_fence_after();
+      for (int h = 0; h < G; ++h) o[h] = 0.f;
+      if (run && mine > 0) {
+        const bool got = wait.warp(p_free + done.i, done.ph);  // O of this group's last tile
+        if (vote(bar, 128, !got) != 0) {
+          ok = run = false;
+        } else {
+          tmem_fence_after();
+          float x[N];
 #pragma unroll
-        for (int c = 0; c < N; c += 16) tmem_load16(tmem + lanes + kColO + c, o + c);
-        tmem_fence_before();
+          for (int c = 0; c < N; c += 16) tmem_load16(tmem + lanes + C::kColO + group * N + c, x + c);
+#pragma unroll
+          for (int h = 0; h < G; ++h) o[h] = x[h] + x[H + h];
+          tmem_fence_before();
+        }
       }
 #pragma unroll
       for (int h = 0; h < G; ++h) {
         const float ls = warp_sum(l[h]);
         if (lane == 0) red[quad * 16 + h] = ls;
       }
-      softmax_sync();
-      const int32_t pair = pc.b * p.hv + pc.vkv;
-      const bool final_here = fused && pc.npieces == 1;
+      named_barrier(bar, 128);
 #pragma unroll
-      for (int h = 0; h < G; ++h) {
-        if (h >= nh) break;
-        const float L = (red[h] + red[16 + h]) + (red[32 + h] + red[48 + h]);
-        const float acc = (o[h] + o[H + h]) * vup;
-        const size_t row = (size_t)pc.b * p.Hq + head0 + h;
-        if (final_here) {
-          if (key < D) p.out[row * D + key] = L == 0.f ? 0.f : acc / L;
-          if (p.lse && key == 0) p.lse[row] = L == 0.f ? -INFINITY : (mr[h] + log2f(L)) * kLn2;
-        } else {
-          const size_t i = balanced ? (size_t)pc.slot * p.gpad + h : row * p.n_splits + pc.slot;
-          if (key < D) p.o_part[i * D + key] = acc;
+      for (int h = 0; h < G; ++h) l[h] = (red[h] + red[16 + h]) + (red[32 + h] + red[48 + h]);
+      if (group == 1) {
+#pragma unroll
+        for (int h = 0; h < G; ++h) {
           if (key == 0) {
-            // The merge passes over states whose l is not above zero.  A NaN sum goes in as
-            // m = inf: the weight exp(inf - inf) then makes out and lse NaN, as the formula does.
-            p.m_part[i] = isnan(L) ? INFINITY : (L == 0.f ? -INFINITY : mr[h] * kLn2);
-            p.l_part[i] = isnan(L) ? 1.f : L;
+            join[h] = mr[h];
+            join[16 + h] = l[h];
           }
+          if (key < D) join[32 + h * D + key] = o[h];
         }
       }
-      softmax_sync();  // the partials are written, red is read
-      if (fused && !final_here) {
-        if (tid == 384) *last_flag = atomic_add_acq_rel(p.counters + pair, 1) == pc.npieces - 1 ? 1 : 0;
-        softmax_sync();
-        if (*last_flag) {
-          const size_t base0 = balanced ? (size_t)(pair + pc.first) * p.gpad : ((size_t)pc.b * p.Hq + head0) * p.n_splits;
-          const size_t hs = balanced ? 1 : (size_t)p.n_splits, stride = balanced ? p.gpad : 1;
-          for (int h = quad; h < nh; h += 4) {
-            const GlobalPartials<D> src{p.o_part, p.m_part, p.l_part, base0 + h * hs, stride};
-            const size_t row = (size_t)pc.b * p.Hq + head0 + h;
-            merge_head<D>(src, balanced ? pc.npieces : p.n_splits, p.out + row * D, p.lse ? p.lse + row : nullptr, lane,
-                          scratch);
+      named_barrier(1, 256);
+      const int32_t pair = pc.b * p.hv + pc.vkv;
+      const bool final_here = fused && pc.npieces == 1;
+      if (group == 0) {
+        const float vup = pow2i(kv.v_exp);
+#pragma unroll
+        for (int h = 0; h < G; ++h) {
+          if (h >= nh) break;
+          // the groups' states on the larger reference; one without keys has l = 0
+          const float m1 = join[h], l1 = join[16 + h];
+          const float mm = fmaxf(mr[h], m1);
+          const float w0 = l[h] == 0.f ? 0.f : ex2(mr[h] - mm), w1 = l1 == 0.f ? 0.f : ex2(m1 - mm);
+          const float L = fmaf(w0, l[h], w1 * l1);
+          const float acc = key < D ? fmaf(w0, o[h], w1 * join[32 + h * D + key]) * vup : 0.f;
+          const size_t row = (size_t)pc.b * p.Hq + head0 + h;
+          if (final_here) {
+            if (key < D) p.out[row * D + key] = L == 0.f ? 0.f : acc / L;
+            if (p.lse && key == 0) p.lse[row] = L == 0.f ? -INFINITY : (mm + log2f(L)) * kLn2;
+          } else {
+            const size_t i = balanced ? (size_t)pc.slot * p.gpad + h : row * p.n_splits + pc.slot;
+            if (key < D) p.o_part[i * D + key] = acc;
+            if (key == 0) {
+              // The join passes over states whose l is not above zero.  A NaN sum goes in as
+              // m = inf: the weight exp(inf - inf) then makes out and lse NaN, as the formula does.
+              p.m_part[i] = isnan(L) ? INFINITY : (L == 0.f ? -INFINITY : mm * kLn2);
+              p.l_part[i] = isnan(L) ? 1.f : L;
+            }
           }
-          if (tid == 384) p.counters[pair] = 0;  // ready for the next call
         }
-        softmax_sync();
+        if (fused && !final_here) {
+          named_barrier(bar, 128);  // the group's partial stores come before the release
+          if (tid == 640) *last_flag = atomic_add_acq_rel(p.counters + pair, 1) == pc.npieces - 1 ? 1 : 0;
+        }
+      }
+      named_barrier(1, 256);  // `join` is read, last_flag is set
+      if (fused && !final_here && *last_flag) {
+        const size_t base0 = balanced ? (size_t)(pair + pc.first) * p.gpad : ((size_t)pc.b * p.Hq + head0) * p.n_splits;
+        const size_t hs = balanced ? 1 : (size_t)p.n_splits, stride = balanced ? p.gpad : 1;
+        for (int h = warp - 20; h < nh; h += 8) {
+          const size_t row = (size_t)pc.b * p.Hq + head0 + h;
+          join_states<D>(p, base0 + h * hs, stride, balanced ? pc.npieces : p.n_splits, p.out + row * D,
+                         p.lse ? p.lse + row : nullptr, lane);
+        }
+        if (tid == 640) p.counters[pair] = 0;  // ready for the next call
       }
     }
     if (!ok) {
