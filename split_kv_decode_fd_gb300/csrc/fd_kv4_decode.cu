@@ -61,6 +61,7 @@ constexpr int kThreads = 896;
 // 2^(kRefDown + kTau) = 2^15, and the smallest fp16 number stands for 2^-33 of the
 // maximum's weight.
 constexpr float kRefDown = 9.f, kTau = 6.f;
+constexpr float kNoRef = -1e30f;  // of a head that has seen no key: any score lies above it
 
 // Position in a ring of NB buffers: tile g is in buffer g % NB, its phase (g / NB) & 1.
 template <uint32_t NB>
@@ -72,6 +73,13 @@ struct Ring {
       ph ^= 1u;
     }
   }
+  __device__ __forceinline__ void skip() {  // two tiles on
+    i += 2;
+    if (i >= NB) {
+      i -= NB;
+      ph ^= 1u;
+    }
+  }
 };
 
 struct KvPiece {
@@ -80,8 +88,7 @@ struct KvPiece {
 
 template <int D, int G>
 struct K4 {
-  static constexpr int kHalf = G <= 8 ? 8 : 16;   // heads as columns: hi, then lo
-  static constexpr int kN = 2 * kHalf;
+  static constexpr int kN = G <= 8 ? 16 : 2 * G;  // columns: hi of the G heads, then lo; the rest is not used
   // Buffers: K and V in tensor memory (64 columns each for D = 128), S there and p
   // in shared memory.  With two of each, a group's next tile waited for the
   // whole chain of its last one (S, softmax, O): 1125 cycles a tile, 128k tokens 43 us.
@@ -90,7 +97,7 @@ struct K4 {
                             kColO = kColS + kSBufs * kN;  // O: one per softmax group
   static_assert(kColO + 2 * kN <= 512, "tensor memory");
   static constexpr int kStageBytes = kTileBlocks * kv4_block_bytes(D);
-  static constexpr int kStages = D == 128 ? 8 : 12;
+  static constexpr int kStages = D == 128 ? 8 : 16;  // a power of two
   static constexpr int kVWarps = D / 32;
   static constexpr int kQBytes = kN * D * 2;
   static constexpr int kPBytes = kN * kTile * 2;
@@ -129,13 +136,13 @@ __device__ __forceinline__ uint32_t b_off(int n, int k) {
          ((uint32_t)k & 7u) * 2;
 }
 
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
+__device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, __half2 b) {
+  const __half2 r = __hmul2(as_half2(a), b);
+  return *reinterpret_cast<const uint32_t*>(&r);
 }
-// Eight codes times their scales (pairs of them: s[0] for the first two codes ...).
-__device__ __forceinline__ void widen8(uint32_t w, uint32_t s0, uint32_t s1, uint32_t s2, uint32_t s3, uint32_t* out) {
+// Eight codes times their scales (s0 for the first two codes ...).
+__device__ __forceinline__ void widen8(uint32_t w, __half2 s0, __half2 s1, __half2 s2, __half2 s3, uint32_t* out) {
   out[0] = hmul2(e2m1x2_f16x2<0>(w), s0);
   out[1] = hmul2(e2m1x2_f16x2<1>(w), s1);
   out[2] = hmul2(e2m1x2_f16x2<2>(w), s2);
@@ -239,9 +246,26 @@ __device__ __forceinline__ void join_states(const SplitParams& p, size_t base, s
   if (lse && lane == 0) *lse = mx == -INFINITY ? -INFINITY : mx + logf(L);
 }
 
+// try_wait that lets the hardware suspend the warp for up to 20 us: with many
+// warps waiting at any time, polling took a fifth of the issue slots.
+__device__ __forceinline__ bool mbar_sleep_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity), "r"(20000u)
+      : "memory");
+  return ok != 0;
+}
+
 // The part of a wait that is not complete at once, out of the way of the tile loops.
 __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned long long limit) {
-  return !*abort_flag && mbar_wait_for(bar, parity, limit);
+  const unsigned long long t0 = global_ns();
+  while (!*abort_flag) {
+    if (mbar_sleep_wait(bar, parity)) return true;
+    if (global_ns() - t0 > limit) return false;
+  }
+  return false;
 }
 
 // Waits of one warp (all lanes together): false when the CTA aborts or the limit passes.
@@ -249,7 +273,7 @@ struct Waiter {
   volatile int* abort_flag;
   unsigned long long limit;
   __device__ __forceinline__ bool one(uint64_t* bar, uint32_t parity) const {
-    return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort_flag, limit);
+    return mbar_sleep_wait(bar, parity) || wait_slow(bar, parity, abort_flag, limit);
   }
   __device__ __forceinline__ bool warp(uint64_t* bar, uint32_t parity) const {
     return __all_sync(0xffffffffu, one(bar, parity));
@@ -259,7 +283,7 @@ struct Waiter {
 template <int D, int G>
 __global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_constant__ Kv4Params pp) {
   using C = K4<D, G>;
-  constexpr int H = C::kHalf, N = C::kN;
+  constexpr int N = C::kN;
   const SplitParams& p = pp.p;
   const Kv4View& kv = pp.kv;
   extern __shared__ uint8_t smem_raw[];
@@ -594,9 +618,9 @@ __global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_consta
       const RowLimits rl{head0, nh, pc.len, p.n_q, p.causal};
       float* factor = reinterpret_cast<float*>(smem + C::kMetaOff + qb * C::kMetaBytes);
       const uint32_t qs = sbase + C::kQOff + qb * C::kQBytes;
-      constexpr int E = D / 32, kBatch = 8;
+      constexpr int E = D / 32, kBatch = G < 8 ? G : 8;
 #pragma unroll 1
-      for (int h0 = 0; h0 < H; h0 += kBatch) {
+      for (int h0 = 0; h0 < G; h0 += kBatch) {
         float x[kBatch][E];
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
@@ -621,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_consta
             uint32_t hi, lo;
             split_f16x2(x[k][i] * up, x[k][i + 1] * up, hi, lo);
             asm volatile("st.shared.u32 [%0], %1;" ::"r"(qs + b_off<N>(h, lane * E + i)), "r"(hi) : "memory");
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(qs + b_off<N>(H + h, lane * E + i)), "r"(lo) : "memory");
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(qs + b_off<N>(G + h, lane * E + i)), "r"(lo) : "memory");
           }
           if (lane == 0) factor[h] = h < nh ? p.qk_scale * pow2i(kv.k_exp) * pow2i(ex - 13) : 0.f;
         }
@@ -649,25 +673,26 @@ __global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_consta
     const uint32_t krow = (uint32_t)(quad * 2 + (lane >> 4)) * kv4_block_bytes(D);
     const uint32_t sw = kv4_swizzle(D, row);
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-    uint32_t g = 0, e = 0;
-    Ring<C::kStages> st;
+    uint32_t g = group, e = 0, g1 = 0;  // this group's next tile, the end of the piece
     Ring<C::kKBufs> kr;
+    if (group) kr.next();
     KvPiece pc;
     for (; next_piece(e, pc); ++e) {
-      const int32_t n = ok ? tiles_of(pc) : 0;
-      for (int32_t j = 0; j < n; ++j, ++g, st.next(), kr.next()) {
-        if ((g & 1) != group) continue;
-        if (!wait.warp(full + st.i, st.ph) || (g >= C::kKBufs && !wait.warp(k_free + kr.i, kr.ph ^ 1))) {
+      if (ok) g1 += tiles_of(pc);
+      for (; g < g1; g += 2, kr.skip()) {
+        const uint32_t st = g % C::kStages;
+        if (!wait.warp(full + st, g / C::kStages & 1) || (g >= C::kKBufs && !wait.warp(k_free + kr.i, kr.ph ^ 1))) {
           ok = false;
           break;
         }
         tmem_fence_after();
-        const uint32_t base = sbase + C::kStageOff + st.i * C::kStageBytes + krow;
+        const uint32_t base = sbase + C::kStageOff + st * C::kStageBytes + krow;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           const uint4 w = lds128u(base + row * (D / 2) + ((c ^ sw) << 4));
           const uint32_t b2 = e4m3x2_f16x2(lds16u(base + kv4_ks_off(D) + row * (D / 16) + 2 * c));
-          const uint32_t s0 = __byte_perm(b2, 0, 0x1010), s1 = __byte_perm(b2, 0, 0x3232);
+          const __half2 sc = *reinterpret_cast<const __half2*>(&b2);
+          const __half2 s0 = __low2half2(sc), s1 = __high2half2(sc);
           uint32_t r[16];
           widen8(w.x, s0, s0, s0, s0, r);
           widen8(w.y, s0, s0, s0, s0, r + 4);
@@ -680,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_consta
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(k_ready + kr.i);
-          mbar_arrive(empty + st.i);
+          mbar_arrive(empty + st);
         }
       }
     }
@@ -697,27 +722,28 @@ __global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_consta
       const uint32_t lanes = (uint32_t)(quad * 32) << 16;
       const uint32_t vs = sbase + C::kVsOff + (warp - 12) * (2 * kTile * 2);
       const int sblk = (lane >> 1) & 7, stok = sblk * 16 + (lane & 1) * 8;  // the scales that this lane converts
-      uint32_t g = 0, e = 0;
-      Ring<C::kStages> st;
+      uint32_t g = group, e = 0, g1 = 0;
       Ring<C::kVBufs> vr;
+      if (group) vr.next();
       KvPiece pc;
       for (; next_piece(e, pc); ++e) {
-        const int32_t n = ok ? tiles_of(pc) : 0;
-        for (int32_t j = 0; j < n; ++j, ++g, st.next(), vr.next()) {
-          if ((g & 1) != group) continue;
-          if (!wait.warp(full + st.i, st.ph) || (g >= C::kVBufs && !wait.warp(v_free + vr.i, vr.ph ^ 1))) {
+        const uint32_t g0 = g1;
+        if (ok) g1 += tiles_of(pc);
+        for (; g < g1; g += 2, vr.skip()) {
+          const uint32_t st = g % C::kStages;
+          if (!wait.warp(full + st, g / C::kStages & 1) || (g >= C::kVBufs && !wait.warp(v_free + vr.i, vr.ph ^ 1))) {
             ok = false;
             break;
           }
           tmem_fence_after();
-          const uint32_t base = sbase + C::kStageOff + st.i * C::kStageBytes;
+          const uint32_t base = sbase + C::kStageOff + st * C::kStageBytes;
           {
             // The warp's two groups of sixteen channels, 128 tokens: scales to fp16,
             // 0 for tokens past the valid ones (0 * anything finite is 0, and codes are finite).
             const uint2 b = lds64u(base + sblk * kv4_block_bytes(D) + kv4_vs_off(D) + (quad * 2 + (lane >> 4)) * 16 +
                                    (lane & 1) * 8);
             uint32_t x[4] = {e4m3x2_f16x2(b.x), e4m3x2_f16x2(b.x >> 16), e4m3x2_f16x2(b.y), e4m3x2_f16x2(b.y >> 16)};
-            const int32_t left = pc.tok_end - (pc.tok_begin + j * kTile) - stok;  // valid tokens of these eight
+            const int32_t left = pc.tok_end - (pc.tok_begin + (int32_t)(g - g0) * kTile) - stok;  // valid tokens of these eight
             if (left < 8) {
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
@@ -737,8 +763,8 @@ __global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_consta
               const int blk = 2 * c + i;
               const uint2 w = lds64u(base + blk * kv4_block_bytes(D) + kv4_v_off(D) + d * 8);
               const uint4 s0 = lds128u(vsl + blk * 32), s1 = lds128u(vsl + blk * 32 + 16);
-              widen8(w.x, s0.x, s0.y, s0.z, s0.w, r + 8 * i);
-              widen8(w.y, s1.x, s1.y, s1.z, s1.w, r + 8 * i + 4);
+              widen8(w.x, as_half2(s0.x), as_half2(s0.y), as_half2(s0.z), as_half2(s0.w), r + 8 * i);
+              widen8(w.y, as_half2(s1.x), as_half2(s1.y), as_half2(s1.z), as_half2(s1.w), r + 8 * i + 4);
             }
             tmem_store16(tmem + lanes + C::kColV + vr.i * (kTile / 2) + c * 16, r);
           }
@@ -747,7 +773,7 @@ __global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_consta
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(v_ready + vr.i);
-            mbar_arrive(empty + st.i);
+            mbar_arrive(empty + st);
           }
         }
       }
@@ -785,8 +811,7 @@ __global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_consta
           for (int i = tid - 640; i < p.Hq; i += 256) p.lse[(size_t)b * p.Hq + i] = -INFINITY;
       }
     }
-    uint32_t g = 0, e = 0, f = 0;
-    Ring<C::kSBufs> sr, done;  // this tile's buffers, the group's last tile's
+    uint32_t g = group, e = 0, f = 0, g1 = 0;  // this group's next tile, the end of the piece
     KvPiece pc;
     for (;; ++e) {
       const bool more = next_piece(e, pc);
@@ -798,88 +823,81 @@ __global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_consta
 #pragma unroll
       for (int h = 0; h < G; ++h) {
         // idle columns have S = 0 and never move their reference
-        mr[h] = h < nh ? -INFINITY : 0.f;
+        mr[h] = h < nh ? kNoRef : 0.f;
         l[h] = 0.f;
       }
       bool run = ok && n > 0;
-      int32_t lim_min = 0;
+      int32_t whole_end = 0;  // keys below it are seen by every head
       if (run) {
         const uint32_t qb = f & 1;
         const bool got = wait.warp(q_ready + qb, (f >> 1) & 1);
         const float* factor = reinterpret_cast<const float*>(smem + C::kMetaOff + qb * C::kMetaBytes);
-        lim_min = *reinterpret_cast<const int32_t*>(factor + 16);
+        whole_end = min(pc.tok_end, *reinterpret_cast<const int32_t*>(factor + 16));
         if (quad == 0 && lane < 16) fac[lane] = factor[lane];
         __syncwarp();
         if (lane == 0) mbar_arrive(q_free + qb);
         ++f;
         if (vote(bar, 128, !got) != 0) ok = run = false;
       }
-      int32_t mine = 0;  // tiles of this group so far
-      for (int32_t j = 0; run && j < n; ++j, ++g, sr.next()) {
-        if ((g & 1) != group) continue;
-        const int32_t t0 = pc.tok_begin + j * kTile, t = t0 + key;
-        const bool got = wait.warp(s_full + sr.i, sr.ph);
+      const uint32_t g0 = g1;
+      if (run) g1 += n;
+      const uint32_t first = g;
+      for (; run && g < g1; g += 2) {
+        const uint32_t i = g % C::kSBufs, ph = g / C::kSBufs & 1;
+        const int32_t t0 = pc.tok_begin + (int32_t)(g - g0) * kTile;
+        const bool whole = t0 + kTile <= whole_end;
+        const bool got = wait.warp(s_full + i, ph);
         tmem_fence_after();
-        float s[G < 2 ? 2 : G];
-        bool up = false;
-        if (got) {
-          const RowLimits rl{head0, nh, pc.len, p.n_q, p.causal};
-          const bool whole = t0 + kTile <= lim_min && t0 + kTile <= pc.tok_end;
-          {
-            float x[N];
+        float s[2 * G], x[G < 2 ? 2 : G];
+        tmem_load<2 * G>(tmem + lanes + C::kColS + i * N, s);
 #pragma unroll
-            for (int c = 0; c < N; c += 16) tmem_load16(tmem + lanes + C::kColS + sr.i * N + c, x + c);
+        for (int h = 0; h < G; ++h) s[h] += s[G + h];
+        for (;;) {
+          // exponents relative to the references; almost always none lies too far above
+          bool up = false;
 #pragma unroll
-            for (int h = 0; h < G; ++h) s[h] = (x[h] + x[H + h]) * fac[h];
-          }
+          for (int h = 0; h < G; ++h) x[h] = fmaf(s[h], fac[h], -mr[h]);
           if (__builtin_expect(!whole, 0)) {
+            const RowLimits rl{head0, nh, pc.len, p.n_q, p.causal};
 #pragma unroll
             for (int h = 0; h < G; ++h)
-              if (t >= pc.tok_end || (h < nh && t >= rl(h))) s[h] = -INFINITY;
+              if (t0 + key >= pc.tok_end || (h < nh && t0 + key >= rl(h))) x[h] = -INFINITY;
           }
 #pragma unroll
-          for (int h = 0; h < G; ++h) up |= s[h] - mr[h] > kRefDown + kTau;
-        }
-        // one vote a warp for a score above its reference, 24 for a wait that ran out
-        const bool any_up = __any_sync(0xffffffffu, up);
-        const uint32_t votes = vote(bar, 128, got ? any_up && lane == 0 : lane >= 8);
-        if (votes >= 24) {
-          ok = run = false;
-          break;
-        }
-        if (__builtin_expect(votes != 0, 0)) {
-          // the reference moves: maxima of the tile, then l and O on the new one
+          for (int h = 0; h < G; ++h) up |= x[h] > kRefDown + kTau;
+          // one vote a warp for such a score, 24 for a wait that ran out
+          const bool any_up = __any_sync(0xffffffffu, up);
+          const uint32_t votes = vote(bar, 128, got ? any_up && lane == 0 : lane >= 8);
+          if (__builtin_expect(votes == 0, 1)) break;
+          bool moved = votes < 24;
+          if (moved) {
+            // the reference moves: maxima of the tile, then l and O on the new one
 #pragma unroll
-          for (int h = 0; h < G; ++h) {
-            const float mx = warp_max(s[h]);
-            if (lane == 0) red[quad * 16 + h] = mx;
-          }
-          named_barrier(bar, 128);
-          float alpha[G];
+            for (int h = 0; h < G; ++h) {
+              const float mx = warp_max(x[h] == -INFINITY ? -INFINITY : s[h] * fac[h]);
+              if (lane == 0) red[quad * 16 + h] = mx;
+            }
+            named_barrier(bar, 128);
+            float alpha[G];
 #pragma unroll
-          for (int h = 0; h < G; ++h) {
-            const float mx = fmaxf(fmaxf(red[h], red[16 + h]), fmaxf(red[32 + h], red[48 + h])) - kRefDown;
-            const float mn = fmaxf(mr[h], mx);
-            alpha[h] = mn == -INFINITY ? 1.f : ex2(mr[h] - mn);
-            mr[h] = mn;
-            l[h] *= alpha[h];
-          }
-          bool moved = true;
-          if (mine > 0) {
-            moved = wait.warp(p_free + done.i, done.ph);  // O of this group's last tile
-            if (moved) {
-              tmem_fence_after();
+            for (int h = 0; h < G; ++h) {
+              const float mx = fmaxf(fmaxf(red[h], red[16 + h]), fmaxf(red[32 + h], red[48 + h])) - kRefDown;
+              const float mn = fmaxf(mr[h], mx);
+              alpha[h] = ex2(mr[h] - mn);
+              mr[h] = mn;
+              l[h] *= alpha[h];
+            }
+            if (g != first) {
+              moved = wait.warp(p_free + (g - 2) % C::kSBufs, (g - 2) / C::kSBufs & 1);  // O of this group's last tile
+              if (moved) {
+                tmem_fence_after();
+                float o[2 * G];
+                tmem_load<2 * G>(tmem + lanes + C::kColO + group * N, o);
 #pragma unroll
-              for (int c = 0; c < N; c += 16) {
-                float o[16];
-                tmem_load16(tmem + lanes + C::kColO + group * N + c, o);
-                uint32_t r[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                  r[i] = __float_as_uint((c + i) % H < G ? o[i] * alpha[(c + i) % H % G] : o[i]);
-                tmem_store16(tmem + lanes + C::kColO + group * N + c, r);
+                for (int h = 0; h < 2 * G; ++h) o[h] *= alpha[h % G];
+                tmem_store<2 * G>(tmem + lanes + C::kColO + group * N, o);
+                tmem_wait_stores();
               }
-              tmem_wait_stores();
             }
           }
           if (vote(bar, 128, !moved) != 0) {  // red is free again, too
@@ -887,25 +905,25 @@ __global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_consta
             break;
           }
         }
+        if (!run) break;
         // p's buffer: O of what it held has been computed
-        if (g < C::kSBufs || wait.warp(p_free + sr.i, sr.ph ^ 1)) {
-          const uint32_t ps = p_at + sr.i * C::kPBytes;
+        if (g < C::kSBufs || wait.warp(p_free + i, ph ^ 1)) {
+          const uint32_t ps = p_at + i * C::kPBytes;
 #pragma unroll
           for (int h = 0; h < G; ++h) {
-            s[h] = ex2(s[h] - (mr[h] == -INFINITY ? 0.f : mr[h]));
-            l[h] += s[h];
+            x[h] = ex2(x[h]);
+            l[h] += x[h];
           }
-          if constexpr (G == 1) s[1] = 0.f;
+          if constexpr (G == 1) x[1] = 0.f;
 #pragma unroll
           for (int h = 0; h < G; h += 2) {
             uint32_t hi, lo;
-            split_f16x2(s[h], s[h + 1], hi, lo);
-            const uint32_t a0 = ps ^ ((h & 7) << 4), a1 = ps ^ (((h + 1) & 7) << 4);
-            sts16(a0 + h * 128, hi);
-            sts16(a0 + (H + h) * 128, lo);
+            split_f16x2(x[h], x[h + 1], hi, lo);
+            sts16((ps ^ ((h & 7) << 4)) + h * 128, hi);
+            sts16((ps ^ (((G + h) & 7) << 4)) + (G + h) * 128, lo);
             if (G > 1) {
-              sts16(a1 + (h + 1) * 128, hi >> 16);
-              sts16(a1 + (H + h + 1) * 128, lo >> 16);
+              sts16((ps ^ (((h + 1) & 7) << 4)) + (h + 1) * 128, hi >> 16);
+              sts16((ps ^ (((G + h + 1) & 7) << 4)) + (G + h + 1) * 128, lo >> 16);
             }
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -914,25 +932,22 @@ __global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_consta
         }
         tmem_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_ready + sr.i);
-        done = sr;
-        ++mine;
+        if (lane == 0) mbar_arrive(p_ready + i);
       }
       // ---- end of the piece: sums over the keys, O by channel
       float o[G];
 #pragma unroll
       for (int h = 0; h < G; ++h) o[h] = 0.f;
-      if (run && mine > 0) {
-        const bool got = wait.warp(p_free + done.i, done.ph);  // O of this group's last tile
+      if (run && g != first) {
+        const bool got = wait.warp(p_free + (g - 2) % C::kSBufs, (g - 2) / C::kSBufs & 1);  // O of this group's last tile
         if (vote(bar, 128, !got) != 0) {
           ok = run = false;
         } else {
           tmem_fence_after();
-          float x[N];
+          float x[2 * G];
+          tmem_load<2 * G>(tmem + lanes + C::kColO + group * N, x);
 #pragma unroll
-          for (int c = 0; c < N; c += 16) tmem_load16(tmem + lanes + C::kColO + group * N + c, x + c);
-#pragma unroll
-          for (int h = 0; h < G; ++h) o[h] = x[h] + x[H + h];
+          for (int h = 0; h < G; ++h) o[h] = x[h] + x[G + h];
           tmem_fence_before();
         }
       }
