@@ -55,7 +55,7 @@ namespace {
 constexpr int kTile = kPlanTile;                       // keys per tile: the M of S^T
 constexpr int kTileBlocks = kTile / kKv4Tokens;
 constexpr int kDescs = 4;                              // pieces announced ahead
-constexpr int kThreads = 896;
+constexpr int kSoftmax0 = 20;                          // first softmax warp
 // p is held in fp16: the reference of the exponent lies kRefDown below the
 // running maximum and moves when a score exceeds that maximum by kTau, so p <=
 // 2^(kRefDown + kTau) = 2^15, and the smallest fp16 number stands for 2^-33 of the
@@ -83,7 +83,9 @@ struct Ring {
 };
 
 struct KvPiece {
-  int32_t b, vkv, tok_begin, tok_end, slot, len, npieces, first;
+  int32_t b, vkv, tok_begin, tok_end, slot, len;
+  int32_t more;  // the CTA goes on after it
+  int32_t pad;
 };
 
 template <int D, int G>
@@ -92,10 +94,11 @@ struct K4 {
   // Buffers: K and V in tensor memory (64 columns each for D = 128), S there and p
   // in shared memory.  With two of each, a group's next tile waited for the
   // whole chain of its last one (S, softmax, O): 1125 cycles a tile, 128k tokens 43 us.
+  static constexpr int kSGroups = 2, kSThreads = 128 * kSGroups, kThreads = 32 * kSoftmax0 + kSThreads;
   static constexpr uint32_t kKBufs = 3, kVBufs = G <= 8 ? 3 : 2, kSBufs = 4;
   static constexpr uint32_t kColK = 0, kColV = kColK + kKBufs * (D / 2), kColS = kColV + kVBufs * (kTile / 2),
                             kColO = kColS + kSBufs * kN;  // O: one per softmax group
-  static_assert(kColO + 2 * kN <= 512, "tensor memory");
+  static_assert(kColO + kSGroups * kN <= 512, "tensor memory");
   static constexpr int kStageBytes = kTileBlocks * kv4_block_bytes(D);
   static constexpr int kStages = D == 128 ? 8 : 16;  // a power of two
   static constexpr int kVWarps = D / 32;
@@ -106,16 +109,18 @@ struct K4 {
   static constexpr int kPOff = kQOff + 2 * kQBytes;
   static constexpr int kStageOff = kPOff + kSBufs * kPBytes;
   static constexpr int kVsOff = kStageOff + kStages * kStageBytes;   // V scales as fp16: [8 warps][2][128]
-  static constexpr int kRedOff = kVsOff + 8 * 2 * kTile * 2;         // [2 groups][4 warps][16] maxima or sums
-  static constexpr int kFacOff = kRedOff + 2 * 4 * 16 * 4;           // [2 groups][16] score factors
-  static constexpr int kJoinOff = kFacOff + 2 * 16 * 4;              // group 1's state: [16] m, [16] l, [G][D] O
-  static constexpr int kMetaOff = kJoinOff + 32 * 4 + G * D * 4;     // per q buffer: factor[16], least limit
+  static constexpr int kRedOff = kVsOff + 8 * 2 * kTile * 2;          // [groups][4 warps][16] maxima or sums
+  static constexpr int kFacOff = kRedOff + kSGroups * 64 * 4;         // [groups][16] score factors
+  static constexpr int kEndOff = kFacOff + kSGroups * 16 * 4;         // a piece's end: see the softmax
+  static constexpr int kEndFloats = (2 * kSGroups + 2) * 16;
+  static constexpr int kJoinOff = kEndOff + kEndFloats * 4;           // the groups' O: [groups][G][D]
+  static constexpr int kMetaOff = kJoinOff + kSGroups * G * D * 4;    // per q buffer: factor[16], least limit
   static constexpr int kMetaBytes = 16 * 4 + 16;
   static constexpr int kDescOff = kMetaOff + 2 * kMetaBytes;
   static constexpr int kLenOff = kDescOff + kDescs * (int)sizeof(KvPiece);
   static constexpr int kPreOff = kLenOff + (kAutoMaxBatch + 4) * 4;
   static constexpr int kBarOff = kPreOff + (kAutoMaxBatch + 4) * 4;
-  static constexpr int kBars = 2 * kStages + 2 * kDescs + 2 * kKBufs + 2 * kVBufs + 3 * kSBufs + 4 + 1;
+  static constexpr int kBars = 2 * kStages + 2 * kDescs + 2 * kKBufs + 2 * kVBufs + 3 * kSBufs + 4 + 2;
   static constexpr int kFlagOff = kBarOff + kBars * 8;
   static constexpr int kSmem = kFlagOff + 16 + 1024;
   static_assert(kSmem <= 232448 && kSmem > 118784, "one CTA per SM: each takes all of tensor memory");
@@ -174,7 +179,26 @@ __device__ __forceinline__ void split_f16x2(float x0, float x1, uint32_t& hi, ui
   lo = *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// Barrier of a softmax group (id 2 or 3, 128 threads) or of both (id 1, 256)
+// Sums over the warp of G values a lane, G a power of two: sum h is in v[0] of
+// the lanes [h * 32 / G, (h + 1) * 32 / G).  Each step halves the values as well as
+// the lanes that a sum is spread over.
+template <int G>
+__device__ __forceinline__ void warp_sums(float (&v)[G], int lane) {
+  int off = 16;
+#pragma unroll
+  for (int n = G / 2; n > 0; n /= 2, off /= 2) {
+    const bool upper = lane & off;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float send = upper ? v[i] : v[i + n], keep = upper ? v[i + n] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, off);
+    }
+  }
+#pragma unroll
+  for (; off > 0; off /= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
+}
+
+// Barrier of a softmax group (ids from 2, 128 threads) or of all of them (id 1)
 // that counts raised predicates.
 __device__ __forceinline__ uint32_t vote(uint32_t id, uint32_t threads, bool pred) {
   uint32_t n;
@@ -193,6 +217,12 @@ __device__ __forceinline__ bool elect_one() {
   uint32_t r;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
   return r != 0;
+}
+// Largest of the warp's values; NaN is passed over, as fmaxf does.
+__device__ __forceinline__ float redux_max(float x) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
 }
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 
@@ -281,9 +311,10 @@ struct Waiter {
 };
 
 template <int D, int G>
-__global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_constant__ Kv4Params pp) {
+__global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __grid_constant__ Kv4Params pp) {
   using C = K4<D, G>;
   constexpr int N = C::kN;
+  constexpr uint32_t kSG = C::kSGroups;
   const SplitParams& p = pp.p;
   const Kv4View& kv = pp.kv;
   extern __shared__ uint8_t smem_raw[];
@@ -305,6 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_consta
   uint64_t* q_ready = p_free + C::kSBufs;   // [2]
   uint64_t* q_free = q_ready + 2;           // [2]
   uint64_t* drain = q_free + 2;
+  uint64_t* part_done = drain + 1;          // a piece's partial state is written
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kFlagOff);
   volatile int* last_flag = abort_flag + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kFlagOff + 8);
@@ -312,34 +344,22 @@ __global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_consta
   int32_t* lens = reinterpret_cast<int32_t*>(smem + C::kLenOff);
   int32_t* pre = reinterpret_cast<int32_t*>(smem + C::kPreOff);
 
-  if (tid == 0) {
-    for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(full + s, 1);
-      mbar_init(empty + s, 4 + C::kVWarps);
+  if (warp == 0) {  // arrivals that each barrier counts, one barrier a lane
+    constexpr uint32_t kV = C::kVWarps;
+    for (int i = lane; i < C::kBars; i += 32) {
+      uint64_t* at = full + i;
+      uint32_t n = 1;
+      if (at >= empty && at < desc_full) n = 4 + kV;
+      if (at >= desc_empty && at < k_ready) n = 2 + 1 + 8 + 2 * kV + 4 * C::kSGroups;
+      if (at >= k_ready && at < k_free) n = 4;
+      if (at >= v_ready && at < v_free) n = kV;
+      if (at >= p_ready && at < p_free) n = 4;
+      if (at >= q_free && at < drain) n = 1 + 4 * C::kSGroups;
+      if (at == drain) n = 2;
+      if (at == part_done) n = 4 * C::kSGroups;
+      mbar_init(at, n);
     }
-    for (int s = 0; s < kDescs; ++s) {
-      mbar_init(desc_full + s, 1);
-      mbar_init(desc_empty + s, 2 + 1 + 8 + 2 * C::kVWarps + 8);
-    }
-    for (uint32_t i = 0; i < C::kKBufs; ++i) {
-      mbar_init(k_ready + i, 4);
-      mbar_init(k_free + i, 1);
-    }
-    for (uint32_t i = 0; i < C::kVBufs; ++i) {
-      mbar_init(v_ready + i, C::kVWarps);
-      mbar_init(v_free + i, 1);
-    }
-    for (uint32_t i = 0; i < C::kSBufs; ++i) {
-      mbar_init(s_full + i, 1);
-      mbar_init(p_ready + i, 4);
-      mbar_init(p_free + i, 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(q_ready + i, 1);
-      mbar_init(q_free + i, 1 + 8);
-    }
-    mbar_init(drain, 2);
-    *abort_flag = 0;
+    if (lane == 0) *abort_flag = 0;
     fence_barrier_init();
   }
   if (warp == 1) tmem_alloc_all(smem_addr(tmem_slot));
@@ -353,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_consta
   tl.uniform = 1;
   if (p.n_splits == 0 && p.seq_lens != nullptr) {
     tl.uniform = 0;
-    for (int b = tid; b < p.B; b += kThreads) lens[b] = clamp_len(__ldg(p.seq_lens + b), p.max_len);
+    for (int b = tid; b < p.B; b += C::kThreads) lens[b] = clamp_len(__ldg(p.seq_lens + b), p.max_len);
     cta_sync();
     if (warp == 0) {
       const int per = ceil_div(p.B, 32);
@@ -393,6 +413,29 @@ __global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_consta
     if (got && lane == 0) mbar_arrive(desc_empty + sl);
     return got && pc.b >= 0;
   };
+  // Pieces of the piece's sequence over all CTAs, and the first CTA that holds one.
+  const auto pieces_of = [&](const KvPiece& pc, int32_t& first) {
+    first = 0;
+    if (p.n_splits != 0) return p.n_splits;
+    int32_t last;
+    balanced_pair_ctas(tl, p.hv, total, balanced_ctas(total, (int32_t)gridDim.x), pc.b, pc.vkv, &first, &last);
+    return last - first + 1;
+  };
+  // Count the piece (one thread); true for the last of its sequence.
+  const auto arrive_last = [&](const KvPiece& pc, int32_t npieces) {
+    return atomic_add_acq_rel(p.counters + pc.b * p.hv + pc.vkv, 1) == npieces - 1;
+  };
+  // Join the sequence's states: heads first, first + step, ...; one warp each.
+  const auto join_piece = [&](const KvPiece& pc, int32_t head0, int32_t nh, int32_t npieces, int32_t first, int h0,
+                              int step) {
+    const bool balanced = p.n_splits == 0;
+    const size_t base = balanced ? (size_t)(pc.b * p.hv + pc.vkv + first) * p.gpad : ((size_t)pc.b * p.Hq + head0) * p.n_splits;
+    const size_t hs = balanced ? 1 : (size_t)p.n_splits, stride = balanced ? p.gpad : 1;
+    for (int h = h0; h < nh; h += step) {
+      const size_t row = (size_t)pc.b * p.Hq + head0 + h;
+      join_states<D>(p, base + h * hs, stride, npieces, p.out + row * D, p.lse ? p.lse + row : nullptr, lane);
+    }
+  };
   const auto tiles_of = [](const KvPiece& pc) { return ceil_div(pc.tok_end - pc.tok_begin, kTile); };
 
   if (warp == 0) {
@@ -403,7 +446,6 @@ __global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_consta
     gr.nsub = p.nsub;
     gr.hv = p.hv;
     const uint64_t stream_policy = policy_evict_first();
-    const int32_t grid_used = p.n_splits == 0 ? balanced_ctas(total, (int32_t)gridDim.x) : 0;
     PieceIter pieces(p, tl, total);
     Piece pc;
     uint32_t it = 0, e = 0, stalled = 0xffffffffu;
@@ -431,13 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_consta
       d.tok_end = pc.tok_end;
       d.slot = pc.slot;
       d.len = pc.len;
-      d.npieces = p.n_splits;
-      d.first = 0;
-      if (p.n_splits == 0) {
-        int32_t last;
-        balanced_pair_ctas(tl, p.hv, total, grid_used, pc.b, pc.vkv, &d.first, &last);
-        d.npieces = last - d.first + 1;
-      }
+      d.more = pieces.more() ? 1 : 0;
       live = announce(d);
       if (!live) break;
       if (!ok) continue;
@@ -543,6 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_consta
     Ring<C::kKBufs> kr;
     Ring<C::kVBufs> vr;
     Ring<C::kSBufs> sr;
+    uint32_t sg = 0;  // the softmax group of tile g
     for (uint32_t e = 0;; ++e) {
       KvPiece pc;
       if (!__all_sync(0xffffffffu, next_piece(e, pc))) break;
@@ -573,8 +610,8 @@ __global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_consta
           tmem_fence_after();
           if (elect_one()) {
             // the group's first tile of the piece starts its O
-            issue(base + C::kColO + (g & 1) * N, base + C::kColV + vr.i * (kTile / 2), sb + C::kPOff + sr.i * C::kPBytes,
-                  std::integral_constant<int, kTile / 16>{}, j > 1 ? 1u : 0u);
+            issue(base + C::kColO + sg * N, base + C::kColV + vr.i * (kTile / 2), sb + C::kPOff + sr.i * C::kPBytes,
+                  std::integral_constant<int, kTile / 16>{}, j >= (int32_t)kSG ? 1u : 0u);
             mma_commit(smem_addr(p_free + sr.i));
             mma_commit(smem_addr(v_free + vr.i));
           }
@@ -583,6 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_consta
         kr.next();
         vr.next();
         sr.next();
+        if (++sg == kSG) sg = 0;
       }
       ++f;
     }
@@ -603,16 +641,10 @@ __global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_consta
     gr.gpad = p.gpad;
     gr.nsub = p.nsub;
     gr.hv = p.hv;
-    uint32_t e = 0, f = 0;
-    KvPiece pc;
-    pdl_wait();
-    for (; next_piece(e, pc); ++e) {
-      if (!ok || tiles_of(pc) == 0) continue;
+    uint32_t f = 0, parts = 0;
+    const auto prepare = [&](const KvPiece& pc) {
       const uint32_t qb = f & 1;
-      if (f >= 2 && !wait.warp(q_free + qb, ((f >> 1) & 1) ^ 1)) {
-        ok = false;
-        continue;
-      }
+      if (f >= 2 && !wait.warp(q_free + qb, ((f >> 1) & 1) ^ 1)) return false;
       int32_t head0, nh;
       vkv_heads(gr, pc.vkv, &head0, &nh);
       const RowLimits rl{head0, nh, pc.len, p.n_q, p.causal};
@@ -660,6 +692,37 @@ __global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_consta
       __syncwarp();
       if (lane == 0) mbar_arrive(q_ready + qb);
       ++f;
+      return true;
+    };
+    // The pieces that the CTA goes on after are counted here, so that the softmax
+    // warps need not wait for the atomic; their joins, too, are off its way.
+    const auto finish = [&](const KvPiece& pc) {
+      int32_t head0, nh, first;
+      vkv_heads(gr, pc.vkv, &head0, &nh);
+      const int32_t npieces = pieces_of(pc, first);
+      if (!__all_sync(0xffffffffu, mbar_wait_for(part_done, parts++ & 1, wait.limit))) {
+        ok = false;
+        return;
+      }
+      bool last = false;
+      if (lane == 0) last = arrive_last(pc, npieces);
+      last = __shfl_sync(0xffffffffu, last, 0);
+      if (!last) return;
+      join_piece(pc, head0, nh, npieces, first, 0, 1);
+      if (lane == 0) p.counters[pc.b * p.hv + pc.vkv] = 0;  // ready for the next call
+    };
+    pdl_wait();
+    KvPiece prev;
+    bool pending = false;
+    for (uint32_t e = 0;; ++e) {
+      KvPiece pc;
+      const bool got = next_piece(e, pc);
+      if (got && ok && tiles_of(pc) > 0 && !prepare(pc)) ok = false;
+      if (pending) finish(prev);
+      if (!got) break;
+      int32_t first;
+      pending = p.counters != nullptr && pc.more && pieces_of(pc, first) != 1;
+      prev = pc;
     }
     if (!ok) {
       raise_error(p.err, kErrTimeout);
@@ -785,12 +848,16 @@ __global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_consta
   } else {
     // ------------------------------------------------------------ softmax
     const int quad = warp & 3;
-    const uint32_t group = (uint32_t)(warp - 20) >> 2;
+    const uint32_t group = (uint32_t)(warp - kSoftmax0) >> 2;
+    const int st = tid - 32 * kSoftmax0;  // thread among the softmax warps
     const uint32_t bar = 2 + group;  // this group's barrier
     const int key = quad * 32 + lane;  // of the tile; the channel at the end of a piece
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
     float* red = reinterpret_cast<float*>(smem + C::kRedOff) + group * 64;
     float* fac = reinterpret_cast<float*>(smem + C::kFacOff) + group * 16;
+    // A piece's end.  Per group and head: the reference, then the weight of the group's
+    // state; the sum.  Per head: the joint reference and sum.  And the groups' O.
+    float* ends = reinterpret_cast<float*>(smem + C::kEndOff);
     float* join = reinterpret_cast<float*>(smem + C::kJoinOff);
     // This thread's key in row 0 of a p buffer; row n is 128 n bytes on, its
     // 16-byte chunk turned by n % 8.
@@ -806,16 +873,16 @@ __global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_consta
     if (balanced) {
       for (int32_t b = blockIdx.x; b < p.B; b += gridDim.x) {
         if (tl.len(b) != 0) continue;
-        for (int i = tid - 640; i < p.Hq * D; i += 256) p.out[(size_t)b * p.Hq * D + i] = 0.f;
+        for (int i = st; i < p.Hq * D; i += C::kSThreads) p.out[(size_t)b * p.Hq * D + i] = 0.f;
         if (p.lse)
-          for (int i = tid - 640; i < p.Hq; i += 256) p.lse[(size_t)b * p.Hq + i] = -INFINITY;
+          for (int i = st; i < p.Hq; i += C::kSThreads) p.lse[(size_t)b * p.Hq + i] = -INFINITY;
       }
     }
     uint32_t g = group, e = 0, f = 0, g1 = 0;  // this group's next tile, the end of the piece
     KvPiece pc;
     for (;; ++e) {
       const bool more = next_piece(e, pc);
-      if (vote(1, 256, !more) != 0) break;  // together: the last piece, or a wait that ran out
+      if (vote(1, C::kSThreads, !more) != 0) break;  // together: the last piece, or a wait that ran out
       int32_t head0, nh;
       vkv_heads(gr, pc.vkv, &head0, &nh);
       const int32_t n = tiles_of(pc);
@@ -841,8 +908,8 @@ __global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_consta
       }
       const uint32_t g0 = g1;
       if (run) g1 += n;
-      const uint32_t first = g;
-      for (; run && g < g1; g += 2) {
+      const uint32_t g_first = g;
+      for (; run && g < g1; g += kSG) {
         const uint32_t i = g % C::kSBufs, ph = g / C::kSBufs & 1;
         const int32_t t0 = pc.tok_begin + (int32_t)(g - g0) * kTile;
         const bool whole = t0 + kTile <= whole_end;
@@ -874,7 +941,7 @@ __global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_consta
             // the reference moves: maxima of the tile, then l and O on the new one
 #pragma unroll
             for (int h = 0; h < G; ++h) {
-              const float mx = warp_max(x[h] == -INFINITY ? -INFINITY : s[h] * fac[h]);
+              const float mx = redux_max(x[h] == -INFINITY ? -INFINITY : s[h] * fac[h]);
               if (lane == 0) red[quad * 16 + h] = mx;
             }
             named_barrier(bar, 128);
@@ -887,8 +954,8 @@ __global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_consta
               mr[h] = mn;
               l[h] *= alpha[h];
             }
-            if (g != first) {
-              moved = wait.warp(p_free + (g - 2) % C::kSBufs, (g - 2) / C::kSBufs & 1);  // O of this group's last tile
+            if (g != g_first) {
+              moved = wait.warp(p_free + (g - kSG) % C::kSBufs, (g - kSG) / C::kSBufs & 1);  // O of this group's last tile
               if (moved) {
                 tmem_fence_after();
                 float o[2 * G];
@@ -934,85 +1001,93 @@ __global__ void __launch_bounds__(kThreads, 1) fd_kv4_kernel(const __grid_consta
         __syncwarp();
         if (lane == 0) mbar_arrive(p_ready + i);
       }
-      // ---- end of the piece: sums over the keys, O by channel
-      float o[G];
-#pragma unroll
-      for (int h = 0; h < G; ++h) o[h] = 0.f;
-      if (run && g != first) {
-        const bool got = wait.warp(p_free + (g - 2) % C::kSBufs, (g - 2) / C::kSBufs & 1);  // O of this group's last tile
+      // ---- end of the piece: sums over the keys, O by channel, the groups joined.
+      // (Rolled loops over shared memory: code that runs once a piece is not in the
+      // instruction cache, and its length was what a piece's end took.)
+      if (run && g != g_first) {
+        const bool got = wait.warp(p_free + (g - kSG) % C::kSBufs, (g - kSG) / C::kSBufs & 1);  // O of the last tile
         if (vote(bar, 128, !got) != 0) {
           ok = run = false;
         } else {
           tmem_fence_after();
           float x[2 * G];
           tmem_load<2 * G>(tmem + lanes + C::kColO + group * N, x);
-#pragma unroll
-          for (int h = 0; h < G; ++h) o[h] = x[h] + x[G + h];
           tmem_fence_before();
-        }
-      }
+          if (key < D) {
 #pragma unroll
-      for (int h = 0; h < G; ++h) {
-        const float ls = warp_sum(l[h]);
-        if (lane == 0) red[quad * 16 + h] = ls;
-      }
-      named_barrier(bar, 128);
-#pragma unroll
-      for (int h = 0; h < G; ++h) l[h] = (red[h] + red[16 + h]) + (red[32 + h] + red[48 + h]);
-      if (group == 1) {
-#pragma unroll
-        for (int h = 0; h < G; ++h) {
-          if (key == 0) {
-            join[h] = mr[h];
-            join[16 + h] = l[h];
-          }
-          if (key < D) join[32 + h * D + key] = o[h];
-        }
-      }
-      named_barrier(1, 256);
-      const int32_t pair = pc.b * p.hv + pc.vkv;
-      const bool final_here = fused && pc.npieces == 1;
-      if (group == 0) {
-        const float vup = pow2i(kv.v_exp);
-#pragma unroll
-        for (int h = 0; h < G; ++h) {
-          if (h >= nh) break;
-          // the groups' states on the larger reference; one without keys has l = 0
-          const float m1 = join[h], l1 = join[16 + h];
-          const float mm = fmaxf(mr[h], m1);
-          const float w0 = l[h] == 0.f ? 0.f : ex2(mr[h] - mm), w1 = l1 == 0.f ? 0.f : ex2(m1 - mm);
-          const float L = fmaf(w0, l[h], w1 * l1);
-          const float acc = key < D ? fmaf(w0, o[h], w1 * join[32 + h * D + key]) * vup : 0.f;
-          const size_t row = (size_t)pc.b * p.Hq + head0 + h;
-          if (final_here) {
-            if (key < D) p.out[row * D + key] = L == 0.f ? 0.f : acc / L;
-            if (p.lse && key == 0) p.lse[row] = L == 0.f ? -INFINITY : (mm + log2f(L)) * kLn2;
-          } else {
-            const size_t i = balanced ? (size_t)pc.slot * p.gpad + h : row * p.n_splits + pc.slot;
-            if (key < D) p.o_part[i * D + key] = acc;
-            if (key == 0) {
-              // The join passes over states whose l is not above zero.  A NaN sum goes in as
-              // m = inf: the weight exp(inf - inf) then makes out and lse NaN, as the formula does.
-              p.m_part[i] = isnan(L) ? INFINITY : (L == 0.f ? -INFINITY : mm * kLn2);
-              p.l_part[i] = isnan(L) ? 1.f : L;
-            }
+            for (int h = 0; h < G; ++h) join[(group * G + h) * D + key] = x[h] + x[G + h];
           }
         }
-        if (fused && !final_here) {
-          named_barrier(bar, 128);  // the group's partial stores come before the release
-          if (tid == 640) *last_flag = atomic_add_acq_rel(p.counters + pair, 1) == pc.npieces - 1 ? 1 : 0;
+      } else if (key < D) {
+#pragma unroll
+        for (int h = 0; h < G; ++h) join[(group * G + h) * D + key] = 0.f;
+      }
+      warp_sums<G>(l, lane);
+      if (lane % (32 / G) == 0) red[quad * 16 + lane / (32 / G)] = l[0];
+      if (key == 0) {
+#pragma unroll
+        for (int h = 0; h < G; ++h) ends[group * 16 + h] = mr[h];
+      }
+      named_barrier(1, C::kSThreads);
+      if (st < G) {
+        // the groups' states on the largest reference; one without keys has l = 0
+        const float* reds = reinterpret_cast<const float*>(smem + C::kRedOff) + st;
+        float lk[kSG], mm = kNoRef, L = 0.f;
+#pragma unroll
+        for (int k = 0; k < kSG; ++k) {
+          lk[k] = (reds[k * 64] + reds[k * 64 + 16]) + (reds[k * 64 + 32] + reds[k * 64 + 48]);
+          mm = fmaxf(mm, ends[k * 16 + st]);
+        }
+#pragma unroll
+        for (int k = 0; k < kSG; ++k) {
+          const float w = lk[k] == 0.f ? 0.f : ex2(ends[k * 16 + st] - mm);
+          ends[k * 16 + st] = w;
+          L = fmaf(w, lk[k], L);
+        }
+        ends[kSG * 16 + st] = mm;
+        ends[(kSG + 1) * 16 + st] = L;
+      }
+      named_barrier(1, C::kSThreads);
+      int32_t first;
+      const int32_t npieces = pieces_of(pc, first);
+      const bool final_here = fused && npieces == 1;
+      const float vup = pow2i(kv.v_exp);
+#pragma unroll 1
+      for (int idx = st; idx < nh * D; idx += C::kSThreads) {
+        const int h = idx / D, d = idx % D;
+        float acc = 0.f;
+#pragma unroll
+        for (int k = 0; k < kSG; ++k) acc = fmaf(ends[k * 16 + h], join[(k * G + h) * D + d], acc);
+        acc *= vup;
+        const float mm = ends[kSG * 16 + h], L = ends[(kSG + 1) * 16 + h];
+        const size_t row = (size_t)pc.b * p.Hq + head0 + h;
+        if (final_here) {
+          p.out[row * D + d] = L == 0.f ? 0.f : acc / L;
+          if (p.lse && d == 0) p.lse[row] = L == 0.f ? -INFINITY : (mm + log2f(L)) * kLn2;
+        } else {
+          const size_t i = balanced ? (size_t)pc.slot * p.gpad + h : row * p.n_splits + pc.slot;
+          p.o_part[i * D + d] = acc;
+          if (d == 0) {
+            // The join passes over states whose l is not above zero.  A NaN sum goes in as
+            // m = inf: the weight exp(inf - inf) then makes out and lse NaN, as the formula does.
+            p.m_part[i] = isnan(L) ? INFINITY : (L == 0.f ? -INFINITY : mm * kLn2);
+            p.l_part[i] = isnan(L) ? 1.f : L;
+          }
         }
       }
-      named_barrier(1, 256);  // `join` is read, last_flag is set
-      if (fused && !final_here && *last_flag) {
-        const size_t base0 = balanced ? (size_t)(pair + pc.first) * p.gpad : ((size_t)pc.b * p.Hq + head0) * p.n_splits;
-        const size_t hs = balanced ? 1 : (size_t)p.n_splits, stride = balanced ? p.gpad : 1;
-        for (int h = warp - 20; h < nh; h += 8) {
-          const size_t row = (size_t)pc.b * p.Hq + head0 + h;
-          join_states<D>(p, base0 + h * hs, stride, balanced ? pc.npieces : p.n_splits, p.out + row * D,
-                         p.lse ? p.lse + row : nullptr, lane);
+      if (fused && !final_here) {
+        if (pc.more) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(part_done);
+        } else {
+          named_barrier(1, C::kSThreads);  // every thread's partial stores come before the release
+          if (st == 0) *last_flag = arrive_last(pc, npieces) ? 1 : 0;
+          named_barrier(1, C::kSThreads);
+          if (*last_flag) {
+            join_piece(pc, head0, nh, npieces, first, warp - kSoftmax0, 4 * kSG);
+            if (st == 0) p.counters[pc.b * p.hv + pc.vkv] = 0;  // ready for the next call
+          }
         }
-        if (tid == 640) p.counters[pair] = 0;  // ready for the next call
       }
     }
     if (!ok) {
@@ -1047,7 +1122,7 @@ cudaError_t launch_t(const Kv4View& kv, const SplitParams& p, dim3 grid, cudaStr
   // waits for it before its first access to global memory.
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
