@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
   int32_t* lens = reinterpret_cast<int32_t*>(smem + C::kLenOff);
   int32_t* pre = reinterpret_cast<int32_t*>(smem + C::kPreOff);
 
-  if (warp == 0) {  // arrivals that each barrier counts, one barrier a lane
+  if (warp == 3) {  // arrivals that each barrier counts, one barrier a lane
     constexpr uint32_t kV = C::kVWarps;
     for (int i = lane; i < C::kBars; i += 32) {
       uint64_t* at = full + i;
@@ -395,10 +395,17 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
       if (lane == 31) pre[p.B] = incl;
     }
   }
-  tmem_fence_before();
-  cta_sync();
-  tmem_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  // The producer (warp 0, which has the prefix sums) walks to its first piece
+  // before it meets the others here.
+  uint32_t tmem = 0;
+  if (warp != 0) {
+    tmem_fence_before();
+    cta_sync();
+    tmem_fence_after();
+    tmem = *tmem_slot;
+  } else {
+    __syncwarp();
+  }
   const int64_t total = (int64_t)p.hv * tl.prefix(p.B);
   const Waiter wait{abort_flag, wait_limit(p)};
   bool ok = true;
@@ -448,6 +455,8 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
     const uint64_t stream_policy = policy_evict_first();
     PieceIter pieces(p, tl, total);
     Piece pc;
+    bool have = pieces.next(pc);
+    cta_sync();
     uint32_t it = 0, e = 0, stalled = 0xffffffffu;
     Ring<C::kStages> st;
     bool live = true;  // the other roles still take pieces
@@ -465,7 +474,7 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
       ++e;
       return (bool)__shfl_sync(0xffffffffu, r, 0);
     };
-    while (live && pieces.next(pc)) {
+    for (; have; have = pieces.next(pc)) {
       KvPiece d;
       d.b = pc.b;
       d.vkv = pc.vkv;
@@ -481,16 +490,33 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
       const uint8_t* base = kv.kv;
       if (!kv.paged)
         base += (((int64_t)pc.b * kv.Hkv + kvh) * kv.cap_blocks + pc.tok_begin / kKv4Tokens) * kv4_block_bytes(D);
-      // Paged: lane j holds the block number of block j of four tiles; the next
-      // four tiles' table entries are in flight meanwhile.
+      // Paged: lane k has block k of four tiles at hand (its number in the pool, -1
+      // for a page outside it), and the table entry of its block of the next four
+      // is in flight.
       const int32_t blk0 = pc.tok_begin / kKv4Tokens, blk1 = ceil_div(pc.tok_end, kKv4Tokens);
+      int64_t cur = 0;
+      int32_t page = 0, rem = 0, at = 0;  // of the next four tiles: the page, the block in it, the table entry
       const int32_t ppb = kv.paged ? kv.page_size / kKv4Tokens : 1;
+      const int32_t step_q = 32 / ppb, step_r = 32 - step_q * ppb;  // thirty-two blocks on
       const int32_t* trow = kv.paged ? kv.block_table + (size_t)pc.b * kv.max_pages : nullptr;
-      const auto page_of = [&](int32_t blk) { return blk < blk1 ? __ldg(trow + blk / ppb) : 0; };
-      int32_t cur = 0, nxt = 0;
+      int32_t blk = blk0 + lane;
+      const auto load_page = [&] { page = blk < blk1 ? __ldg(trow + at) : 0; };
+      const auto take_page = [&] {
+        cur = page >= 0 && page < kv.num_pages ? ((int64_t)page * kv.Hkv + kvh) * ppb + rem : -1;
+        blk += 32;
+        at += step_q;
+        rem += step_r;
+        if (rem >= ppb) {
+          rem -= ppb;
+          ++at;
+        }
+        load_page();
+      };
       if (kv.paged) {
-        cur = page_of(blk0 + lane);
-        nxt = page_of(blk0 + 32 + lane);
+        at = blk / ppb;
+        rem = blk - at * ppb;
+        load_page();
+        take_page();
       }
       const int32_t n = tiles_of(d);
       for (int32_t j = 0; j < n; ++j, ++it, st.next()) {
@@ -519,7 +545,7 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
         } else {
           const int k = lane - (j & 3) * kTileBlocks;  // this lane's block of the tile
           const bool mine = k >= 0 && k < nblk;
-          const bool bad = mine && (cur < 0 || cur >= kv.num_pages);
+          const bool bad = mine && cur < 0;
           if (bad) {
             // keys of score 0 and value 0 in its place
             raise_error(p.err, kErrBadIndex);
@@ -532,15 +558,9 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
           const uint32_t copies = __popc(__ballot_sync(0xffffffffu, mine && !bad));
           if (lane == 0) mbar_arrive_expect_tx(full + st.i, copies * kv4_block_bytes(D));
           __syncwarp();
-          if (mine && !bad) {
-            const int32_t blk = blk0 + j * kTileBlocks + k;
-            const int64_t idx = ((int64_t)cur * kv.Hkv + kvh) * ppb + blk % ppb;
-            bulk_load(dst + k * kv4_block_bytes(D), kv.kv + idx * kv4_block_bytes(D), kv4_block_bytes(D), full + st.i);
-          }
-          if ((j & 3) == 3) {
-            cur = nxt;
-            nxt = page_of(blk0 + (j + 5) * kTileBlocks + lane);
-          }
+          if (mine && !bad)
+            bulk_load(dst + k * kv4_block_bytes(D), kv.kv + cur * kv4_block_bytes(D), kv4_block_bytes(D), full + st.i);
+          if ((j & 3) == 3) take_page();
         }
       }
     }
