@@ -112,10 +112,9 @@ struct K4 {
   static constexpr int kRedOff = kVsOff + 8 * 2 * kTile * 2;          // [groups][4 warps][16] maxima or sums
   static constexpr int kFacOff = kRedOff + kSGroups * 64 * 4;         // [groups][16] score factors
   static constexpr int kEndOff = kFacOff + kSGroups * 16 * 4;         // a piece's end: see the softmax
-  static constexpr int kEndFloats = (2 * kSGroups + 2) * 16;
-  static constexpr int kJoinOff = kEndOff + kEndFloats * 4;           // the groups' O: [groups][G][D]
+  static constexpr int kJoinOff = kEndOff + 16 * 10 * 4;          // the groups' O: [groups][G][D]
   static constexpr int kMetaOff = kJoinOff + kSGroups * G * D * 4;    // per q buffer: factor[16], least limit
-  static constexpr int kMetaBytes = 16 * 4 + 16;
+  static constexpr int kMetaBytes = 16 * 4 + 16;  // ... and the sequence's pieces, their first CTA
   static constexpr int kDescOff = kMetaOff + 2 * kMetaBytes;
   static constexpr int kLenOff = kDescOff + kDescs * (int)sizeof(KvPiece);
   static constexpr int kPreOff = kLenOff + (kAutoMaxBatch + 4) * 4;
@@ -496,9 +495,8 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
       const int32_t blk0 = pc.tok_begin / kKv4Tokens, blk1 = ceil_div(pc.tok_end, kKv4Tokens);
       int64_t cur = 0;
       int32_t page = 0, rem = 0, at = 0;  // of the next four tiles: the page, the block in it, the table entry
-      const int32_t ppb = kv.paged ? kv.page_size / kKv4Tokens : 1;
-      const int32_t step_q = 32 / ppb, step_r = 32 - step_q * ppb;  // thirty-two blocks on
-      const int32_t* trow = kv.paged ? kv.block_table + (size_t)pc.b * kv.max_pages : nullptr;
+      int32_t ppb = 1, step_q = 0, step_r = 0;  // blocks of a page; thirty-two blocks on
+      const int32_t* trow = kv.block_table + (size_t)pc.b * kv.max_pages;
       int32_t blk = blk0 + lane;
       const auto load_page = [&] { page = blk < blk1 ? __ldg(trow + at) : 0; };
       const auto take_page = [&] {
@@ -513,6 +511,9 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
         load_page();
       };
       if (kv.paged) {
+        ppb = kv.page_size / kKv4Tokens;
+        step_q = 32 / ppb;
+        step_r = 32 - step_q * ppb;
         at = blk / ppb;
         rem = blk - at * ppb;
         load_page();
@@ -706,7 +707,13 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
         int32_t least = lane < nh ? rl(lane) : 0x7fffffff;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
-        if (lane == 0) *reinterpret_cast<int32_t*>(factor + 16) = least;
+        if (lane == 0) {
+          int32_t first;
+          int32_t* meta = reinterpret_cast<int32_t*>(factor + 16);
+          meta[1] = pieces_of(pc, first);
+          meta[2] = first;
+          meta[0] = least;
+        }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
@@ -875,8 +882,8 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
     float* red = reinterpret_cast<float*>(smem + C::kRedOff) + group * 64;
     float* fac = reinterpret_cast<float*>(smem + C::kFacOff) + group * 16;
-    // A piece's end.  Per group and head: the reference, then the weight of the group's
-    // state; the sum.  Per head: the joint reference and sum.  And the groups' O.
+    // A piece's end.  Per head, the sums [groups][4 warps], then [16][groups]
+    // references; and the groups' O.
     float* ends = reinterpret_cast<float*>(smem + C::kEndOff);
     float* join = reinterpret_cast<float*>(smem + C::kJoinOff);
     // This thread's key in row 0 of a p buffer; row n is 128 n bytes on, its
@@ -913,19 +920,24 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
         mr[h] = h < nh ? kNoRef : 0.f;
         l[h] = 0.f;
       }
+      int32_t npieces = 0, first = 0;
       bool run = ok && n > 0;
       int32_t whole_end = 0;  // keys below it are seen by every head
       if (run) {
         const uint32_t qb = f & 1;
         const bool got = wait.warp(q_ready + qb, (f >> 1) & 1);
         const float* factor = reinterpret_cast<const float*>(smem + C::kMetaOff + qb * C::kMetaBytes);
-        whole_end = min(pc.tok_end, *reinterpret_cast<const int32_t*>(factor + 16));
+        const int32_t* meta = reinterpret_cast<const int32_t*>(factor + 16);
+        whole_end = min(pc.tok_end, meta[0]);
+        npieces = meta[1];
+        first = meta[2];
         if (quad == 0 && lane < 16) fac[lane] = factor[lane];
         __syncwarp();
         if (lane == 0) mbar_arrive(q_free + qb);
         ++f;
         if (vote(bar, 128, !got) != 0) ok = run = false;
       }
+      if (!run) npieces = pieces_of(pc, first);
       const uint32_t g0 = g1;
       if (run) g1 += n;
       const uint32_t g_first = g;
@@ -1043,43 +1055,24 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
         for (int h = 0; h < G; ++h) join[(group * G + h) * D + key] = 0.f;
       }
       warp_sums<G>(l, lane);
-      if (lane % (32 / G) == 0) red[quad * 16 + lane / (32 / G)] = l[0];
+      if (lane % (32 / G) == 0) ends[lane / (32 / G) * 8 + group * 4 + quad] = l[0];
       if (key == 0) {
 #pragma unroll
-        for (int h = 0; h < G; ++h) ends[group * 16 + h] = mr[h];
+        for (int h = 0; h < G; ++h) ends[128 + h * 2 + group] = mr[h];
       }
       named_barrier(1, C::kSThreads);
-      if (st < G) {
-        // the groups' states on the largest reference; one without keys has l = 0
-        const float* reds = reinterpret_cast<const float*>(smem + C::kRedOff) + st;
-        float lk[kSG], mm = kNoRef, L = 0.f;
-#pragma unroll
-        for (int k = 0; k < kSG; ++k) {
-          lk[k] = (reds[k * 64] + reds[k * 64 + 16]) + (reds[k * 64 + 32] + reds[k * 64 + 48]);
-          mm = fmaxf(mm, ends[k * 16 + st]);
-        }
-#pragma unroll
-        for (int k = 0; k < kSG; ++k) {
-          const float w = lk[k] == 0.f ? 0.f : ex2(ends[k * 16 + st] - mm);
-          ends[k * 16 + st] = w;
-          L = fmaf(w, lk[k], L);
-        }
-        ends[kSG * 16 + st] = mm;
-        ends[(kSG + 1) * 16 + st] = L;
-      }
-      named_barrier(1, C::kSThreads);
-      int32_t first;
-      const int32_t npieces = pieces_of(pc, first);
       const bool final_here = fused && npieces == 1;
-      const float vup = pow2i(kv.v_exp);
 #pragma unroll 1
       for (int idx = st; idx < nh * D; idx += C::kSThreads) {
         const int h = idx / D, d = idx % D;
-        float acc = 0.f;
-#pragma unroll
-        for (int k = 0; k < kSG; ++k) acc = fmaf(ends[k * 16 + h], join[(k * G + h) * D + d], acc);
-        acc *= vup;
-        const float mm = ends[kSG * 16 + h], L = ends[(kSG + 1) * 16 + h];
+        // the groups' states on the largest reference; one without keys has l = 0
+        const float4 la = reinterpret_cast<const float4*>(ends)[2 * h], lb = reinterpret_cast<const float4*>(ends)[2 * h + 1];
+        const float2 ms = reinterpret_cast<const float2*>(ends + 128)[h];
+        const float l0 = (la.x + la.y) + (la.z + la.w), l1 = (lb.x + lb.y) + (lb.z + lb.w), mm = fmaxf(ms.x, ms.y);
+        const float w0 = l0 == 0.f ? 0.f : ex2(ms.x - mm), w1 = l1 == 0.f ? 0.f : ex2(ms.y - mm);
+        const float L = fmaf(w0, l0, w1 * l1);
+        float acc = fmaf(w0, join[h * D + d], w1 * join[(G + h) * D + d]);
+        acc *= pow2i(kv.v_exp);
         const size_t row = (size_t)pc.b * p.Hq + head0 + h;
         if (final_here) {
           p.out[row * D + d] = L == 0.f ? 0.f : acc / L;
