@@ -947,15 +947,27 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
         const bool whole = t0 + kTile <= whole_end;
         const bool got = wait.warp(s_full + i, ph);
         tmem_fence_after();
-        float s[2 * G], x[G < 2 ? 2 : G];
-        tmem_load<2 * G>(tmem + lanes + C::kColS + i * N, s);
+        float x[G < 2 ? 2 : G];
+        const auto load_scores = [&] {  // hi + lo, not yet times their factors
+          if constexpr (G < 16) {
+            float s[2 * G];
+            tmem_load<2 * G>(tmem + lanes + C::kColS + i * N, s);
 #pragma unroll
-        for (int h = 0; h < G; ++h) s[h] += s[G + h];
+            for (int h = 0; h < G; ++h) x[h] = s[h] + s[G + h];
+          } else {
+            float lo[G];
+            tmem_load<G>(tmem + lanes + C::kColS + i * N, x);
+            tmem_load<G>(tmem + lanes + C::kColS + i * N + G, lo);
+#pragma unroll
+            for (int h = 0; h < G; ++h) x[h] += lo[h];
+          }
+        };
         for (;;) {
           // exponents relative to the references; almost always none lies too far above
           bool up = false;
+          load_scores();
 #pragma unroll
-          for (int h = 0; h < G; ++h) x[h] = fmaf(s[h], fac[h], -mr[h]);
+          for (int h = 0; h < G; ++h) x[h] = fmaf(x[h], fac[h], -mr[h]);
           if (__builtin_expect(!whole, 0)) {
             const RowLimits rl{head0, nh, pc.len, p.n_q, p.causal};
 #pragma unroll
@@ -971,13 +983,17 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
           bool moved = votes < 24;
           if (moved) {
             // the reference moves: maxima of the tile, then l and O on the new one
+            uint32_t seen = 0;
+#pragma unroll
+            for (int h = 0; h < G; ++h) seen |= (x[h] == -INFINITY ? 0u : 1u) << h;
+            load_scores();
 #pragma unroll
             for (int h = 0; h < G; ++h) {
-              const float mx = redux_max(x[h] == -INFINITY ? -INFINITY : s[h] * fac[h]);
+              const float mx = redux_max(seen >> h & 1 ? x[h] * fac[h] : -INFINITY);
               if (lane == 0) red[quad * 16 + h] = mx;
             }
             named_barrier(bar, 128);
-            float alpha[G];
+            float (&alpha)[G < 2 ? 2 : G] = x;
 #pragma unroll
             for (int h = 0; h < G; ++h) {
               const float mx = fmaxf(fmaxf(red[h], red[16 + h]), fmaxf(red[32 + h], red[48 + h])) - kRefDown;
@@ -990,11 +1006,16 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
               moved = wait.warp(p_free + (g - kSG) % C::kSBufs, (g - kSG) / C::kSBufs & 1);  // O of this group's last tile
               if (moved) {
                 tmem_fence_after();
-                float o[2 * G];
-                tmem_load<2 * G>(tmem + lanes + C::kColO + group * N, o);
 #pragma unroll
-                for (int h = 0; h < 2 * G; ++h) o[h] *= alpha[h % G];
-                tmem_store<2 * G>(tmem + lanes + C::kColO + group * N, o);
+                for (int part = 0; part < 2; ++part) {  // hi, lo
+                  constexpr int W = G < 2 ? 2 : G;
+                  if (G == 1 && part == 1) break;
+                  float o[W];
+                  tmem_load<W>(tmem + lanes + C::kColO + group * N + part * G, o);
+#pragma unroll
+                  for (int h = 0; h < W; ++h) o[h] *= alpha[h % G];
+                  tmem_store<W>(tmem + lanes + C::kColO + group * N + part * G, o);
+                }
                 tmem_wait_stores();
               }
             }
@@ -1042,13 +1063,18 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
           ok = run = false;
         } else {
           tmem_fence_after();
-          float x[2 * G];
-          tmem_load<2 * G>(tmem + lanes + C::kColO + group * N, x);
-          tmem_fence_before();
-          if (key < D) {
+          constexpr int W = G < 2 ? 2 : (G < 8 ? G : 8);
 #pragma unroll
-            for (int h = 0; h < G; ++h) join[(group * G + h) * D + key] = x[h] + x[G + h];
+          for (int h0 = 0; h0 < G; h0 += W) {
+            float hi[W], lo[W];
+            tmem_load<W>(tmem + lanes + C::kColO + group * N + h0, hi);
+            tmem_load<W>(tmem + lanes + C::kColO + group * N + G + h0, lo);
+            if (key < D) {
+#pragma unroll
+              for (int h = 0; h < W && h0 + h < G; ++h) join[(group * G + h0 + h) * D + key] = hi[h] + lo[h];
+            }
           }
+          tmem_fence_before();
         }
       } else if (key < D) {
 #pragma unroll
