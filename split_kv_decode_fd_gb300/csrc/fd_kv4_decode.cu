@@ -88,6 +88,11 @@ struct KvPiece {
   int32_t pad;
 };
 
+// A counted piece, from the q warp to the softmax warps.
+struct JoinPiece {
+  int32_t last, b, vkv, npieces, first;
+};
+
 template <int D, int G>
 struct K4 {
   static constexpr int kN = G <= 8 ? 16 : 2 * G;  // columns: hi of the G heads, then lo; the rest is not used
@@ -109,19 +114,20 @@ struct K4 {
   static constexpr int kPOff = kQOff + 2 * kQBytes;
   static constexpr int kStageOff = kPOff + kSBufs * kPBytes;
   static constexpr int kVsOff = kStageOff + kStages * kStageBytes;   // V scales as fp16: [8 warps][2][128]
-  static constexpr int kRedOff = kVsOff + 8 * 2 * kTile * 2;          // [groups][4 warps][16] maxima or sums
-  static constexpr int kFacOff = kRedOff + kSGroups * 64 * 4;         // [groups][16] score factors
-  static constexpr int kEndOff = kFacOff + kSGroups * 16 * 4;         // a piece's end: see the softmax
+  static constexpr int kRedOff = kVsOff + 8 * 2 * kTile * 2;          // [groups][16][4 warps] maxima, [16] references
+  static constexpr int kFacOff = kRedOff + kSGroups * 80 * 4;         // [groups][16] score factors, [16] limits
+  static constexpr int kEndOff = kFacOff + kSGroups * 32 * 4;         // a piece's end: see the softmax
   static constexpr int kJoinOff = kEndOff + 16 * 10 * 4;          // the groups' O: [groups][G][D]
-  static constexpr int kMetaOff = kJoinOff + kSGroups * G * D * 4;    // per q buffer: factor[16], least limit
-  static constexpr int kMetaBytes = 16 * 4 + 16;  // ... and the sequence's pieces, their first CTA
+  static constexpr int kMetaOff = kJoinOff + kSGroups * G * D * 4;    // per q buffer: factor[16], limit[16], least limit
+  static constexpr int kMetaBytes = 2 * 16 * 4 + 16;  // ... and the sequence's pieces, their first CTA
   static constexpr int kDescOff = kMetaOff + 2 * kMetaBytes;
   static constexpr int kLenOff = kDescOff + kDescs * (int)sizeof(KvPiece);
   static constexpr int kPreOff = kLenOff + (kAutoMaxBatch + 4) * 4;
   static constexpr int kBarOff = kPreOff + (kAutoMaxBatch + 4) * 4;
-  static constexpr int kBars = 2 * kStages + 2 * kDescs + 2 * kKBufs + 2 * kVBufs + 3 * kSBufs + 4 + 2;
+  static constexpr int kBars = 2 * kStages + 2 * kDescs + 2 * kKBufs + 2 * kVBufs + 3 * kSBufs + 4 + 3;
   static constexpr int kFlagOff = kBarOff + kBars * 8;
-  static constexpr int kSmem = kFlagOff + 16 + 1024;
+  static constexpr int kLastOff = kFlagOff + 16;                      // the piece to join: see JoinPiece
+  static constexpr int kSmem = kLastOff + 32 + 1024;
   static_assert(kSmem <= 232448 && kSmem > 118784, "one CTA per SM: each takes all of tensor memory");
   static_assert(kStageOff % 128 == 0 && kQBytes % 1024 == 0 && kPBytes % 1024 == 0, "operand alignment");
   static_assert(kDescOff % 16 == 0 && kBarOff % 8 == 0, "alignment");
@@ -178,11 +184,11 @@ __device__ __forceinline__ void split_f16x2(float x0, float x1, uint32_t& hi, ui
   lo = *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// Sums over the warp of G values a lane, G a power of two: sum h is in v[0] of
-// the lanes [h * 32 / G, (h + 1) * 32 / G).  Each step halves the values as well as
-// the lanes that a sum is spread over.
-template <int G>
-__device__ __forceinline__ void warp_sums(float (&v)[G], int lane) {
+// Reductions over the warp of G values a lane, G a power of two: result h is in
+// v[0] of the lanes [h * 32 / G, (h + 1) * 32 / G).  Each step halves the values as
+// well as the lanes that a result is spread over.
+template <int G, int NV, class Op>
+__device__ __forceinline__ void warp_reduce(float (&v)[NV], int lane, Op op) {
   int off = 16;
 #pragma unroll
   for (int n = G / 2; n > 0; n /= 2, off /= 2) {
@@ -190,11 +196,11 @@ __device__ __forceinline__ void warp_sums(float (&v)[G], int lane) {
 #pragma unroll
     for (int i = 0; i < n; ++i) {
       const float send = upper ? v[i] : v[i + n], keep = upper ? v[i + n] : v[i];
-      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, off);
+      v[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, off));
     }
   }
 #pragma unroll
-  for (; off > 0; off /= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
+  for (; off > 0; off /= 2) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], off));
 }
 
 // Barrier of a softmax group (ids from 2, 128 threads) or of all of them (id 1)
@@ -217,11 +223,9 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
   return r != 0;
 }
-// Largest of the warp's values; NaN is passed over, as fmaxf does.
-__device__ __forceinline__ float redux_max(float x) {
-  float r;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
-  return r;
+// Largest of the warp's values, none below zero; a NaN is the largest.
+__device__ __forceinline__ float warp_max_abs(float x) {
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(x))));
 }
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 
@@ -336,6 +340,7 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
   uint64_t* q_free = q_ready + 2;           // [2]
   uint64_t* drain = q_free + 2;
   uint64_t* part_done = drain + 1;          // a piece's partial state is written
+  uint64_t* join_known = part_done + 1;     // ... and counted: whether it was its sequence's last
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kFlagOff);
   volatile int* last_flag = abort_flag + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kFlagOff + 8);
@@ -432,16 +437,24 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
     return atomic_add_acq_rel(p.counters + pc.b * p.hv + pc.vkv, 1) == npieces - 1;
   };
   // Join the sequence's states: heads first, first + step, ...; one warp each.
-  const auto join_piece = [&](const KvPiece& pc, int32_t head0, int32_t nh, int32_t npieces, int32_t first, int h0,
-                              int step) {
+  const auto join_piece = [&](int32_t b, int32_t vkv, int32_t npieces, int32_t first, int h0, int step) {
+    Groups gr;
+    gr.g = p.g;
+    gr.gpad = p.gpad;
+    gr.nsub = p.nsub;
+    gr.hv = p.hv;
+    int32_t head0, nh;
+    vkv_heads(gr, vkv, &head0, &nh);
     const bool balanced = p.n_splits == 0;
-    const size_t base = balanced ? (size_t)(pc.b * p.hv + pc.vkv + first) * p.gpad : ((size_t)pc.b * p.Hq + head0) * p.n_splits;
+    const size_t base = balanced ? (size_t)(b * p.hv + vkv + first) * p.gpad : ((size_t)b * p.Hq + head0) * p.n_splits;
     const size_t hs = balanced ? 1 : (size_t)p.n_splits, stride = balanced ? p.gpad : 1;
     for (int h = h0; h < nh; h += step) {
-      const size_t row = (size_t)pc.b * p.Hq + head0 + h;
+      const size_t row = (size_t)b * p.Hq + head0 + h;
       join_states<D>(p, base + h * hs, stride, npieces, p.out + row * D, p.lse ? p.lse + row : nullptr, lane);
     }
+    if (h0 == 0 && lane == 0) p.counters[b * p.hv + vkv] = 0;  // ready for the next call
   };
+  JoinPiece* counted = reinterpret_cast<JoinPiece*>(smem + C::kLastOff);
   const auto tiles_of = [](const KvPiece& pc) { return ceil_div(pc.tok_end - pc.tok_begin, kTile); };
 
   if (warp == 0) {
@@ -671,45 +684,46 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
       const RowLimits rl{head0, nh, pc.len, p.n_q, p.causal};
       float* factor = reinterpret_cast<float*>(smem + C::kMetaOff + qb * C::kMetaBytes);
       const uint32_t qs = sbase + C::kQOff + qb * C::kQBytes;
-      constexpr int E = D / 32, kBatch = G < 8 ? G : 8;
+      constexpr int E = D / 32;
+      float x[E], nx[E];
+      const auto load_head = [&](int h) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) nx[i] = 0.f;
+        if (h < nh) load_slice<D>(p.q + ((size_t)pc.b * p.Hq + head0 + h) * D + lane * E, nx);
+      };
+      load_head(0);
 #pragma unroll 1
-      for (int h0 = 0; h0 < G; h0 += kBatch) {
-        float x[kBatch][E];
+      for (int h = 0; h < G; ++h) {
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
+        for (int i = 0; i < E; ++i) x[i] = nx[i];
+        if (h + 1 < G) load_head(h + 1);
+        float big = 0.f;
 #pragma unroll
-          for (int i = 0; i < E; ++i) x[k][i] = 0.f;
-          if (h0 + k < nh) load_slice<D>(p.q + ((size_t)pc.b * p.Hq + head0 + h0 + k) * D + lane * E, x[k]);
+        for (int i = 0; i < E; ++i) big = fmaxf(big, fabsf(x[i]));
+        big = warp_max_abs(big);
+        // 2^e <= big < 2^(e + 1): q times 2^(13 - e) fills fp16's range
+        int ex = (int)(__float_as_uint(big) >> 23) - 127;
+        if (big == 0.f || ex > 127) ex = 13;
+        ex = ex < -80 ? -80 : (ex > 80 ? 80 : ex);
+        const float up = pow2i(13 - ex);
+#pragma unroll
+        for (int i = 0; i < E; i += 2) {
+          uint32_t hi, lo;
+          split_f16x2(x[i] * up, x[i + 1] * up, hi, lo);
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(qs + b_off<N>(h, lane * E + i)), "r"(hi) : "memory");
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(qs + b_off<N>(G + h, lane * E + i)), "r"(lo) : "memory");
         }
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const int h = h0 + k;
-          float big = 0.f;
-#pragma unroll
-          for (int i = 0; i < E; ++i) big = fmaxf(big, fabsf(x[k][i]));
-          big = warp_max(big);
-          // 2^e <= big < 2^(e + 1): q times 2^(13 - e) fills fp16's range
-          int ex = (int)((__float_as_uint(big) >> 23) & 0xffu) - 127;
-          if (big == 0.f || ex > 127) ex = 13;
-          ex = ex < -80 ? -80 : (ex > 80 ? 80 : ex);
-          const float up = pow2i(13 - ex);
-#pragma unroll
-          for (int i = 0; i < E; i += 2) {
-            uint32_t hi, lo;
-            split_f16x2(x[k][i] * up, x[k][i + 1] * up, hi, lo);
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(qs + b_off<N>(h, lane * E + i)), "r"(hi) : "memory");
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(qs + b_off<N>(G + h, lane * E + i)), "r"(lo) : "memory");
-          }
-          if (lane == 0) factor[h] = h < nh ? p.qk_scale * pow2i(kv.k_exp) * pow2i(ex - 13) : 0.f;
-        }
+        if (lane == 0) factor[h] = h < nh ? p.qk_scale * pow2i(kv.k_exp) * pow2i(ex - 13) : 0.f;
       }
-      {  // the fewest keys that a head of the piece sees
-        int32_t least = lane < nh ? rl(lane) : 0x7fffffff;
+      {  // the keys that each head sees, and the fewest
+        const int32_t limit = lane < nh ? rl(lane) : 0x7fffffff;
+        if (lane < 16) reinterpret_cast<int32_t*>(factor + 16)[lane] = limit;
+        int32_t least = limit;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
         if (lane == 0) {
           int32_t first;
-          int32_t* meta = reinterpret_cast<int32_t*>(factor + 16);
+          int32_t* meta = reinterpret_cast<int32_t*>(factor + 32);
           meta[1] = pieces_of(pc, first);
           meta[2] = first;
           meta[0] = least;
@@ -722,21 +736,20 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
       return true;
     };
     // The pieces that the CTA goes on after are counted here, so that the softmax
-    // warps need not wait for the atomic; their joins, too, are off its way.
+    // warps need not wait for the atomic; they join a sequence at their next piece's end.
     const auto finish = [&](const KvPiece& pc) {
-      int32_t head0, nh, first;
-      vkv_heads(gr, pc.vkv, &head0, &nh);
-      const int32_t npieces = pieces_of(pc, first);
-      if (!__all_sync(0xffffffffu, mbar_wait_for(part_done, parts++ & 1, wait.limit))) {
-        ok = false;
-        return;
+      JoinPiece j;
+      j.b = pc.b;
+      j.vkv = pc.vkv;
+      j.npieces = pieces_of(pc, j.first);
+      const bool done = __all_sync(0xffffffffu, mbar_wait_for(part_done, parts++ & 1, wait.limit));
+      if (!done) ok = false;
+      if (lane == 0) {
+        j.last = done && arrive_last(pc, j.npieces) ? 1 : 0;
+        *counted = j;
+        mbar_arrive(join_known);
       }
-      bool last = false;
-      if (lane == 0) last = arrive_last(pc, npieces);
-      last = __shfl_sync(0xffffffffu, last, 0);
-      if (!last) return;
-      join_piece(pc, head0, nh, npieces, first, 0, 1);
-      if (lane == 0) p.counters[pc.b * p.hv + pc.vkv] = 0;  // ready for the next call
+      __syncwarp();
     };
     pdl_wait();
     KvPiece prev;
@@ -880,8 +893,9 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
     const uint32_t bar = 2 + group;  // this group's barrier
     const int key = quad * 32 + lane;  // of the tile; the channel at the end of a piece
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-    float* red = reinterpret_cast<float*>(smem + C::kRedOff) + group * 64;
-    float* fac = reinterpret_cast<float*>(smem + C::kFacOff) + group * 16;
+    float* red = reinterpret_cast<float*>(smem + C::kRedOff) + group * 80;
+    float* fac = reinterpret_cast<float*>(smem + C::kFacOff) + group * 32;
+    const int32_t* lims = reinterpret_cast<const int32_t*>(fac + 16);
     // A piece's end.  Per head, the sums [groups][4 warps], then [16][groups]
     // references; and the groups' O.
     float* ends = reinterpret_cast<float*>(smem + C::kEndOff);
@@ -906,10 +920,21 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
       }
     }
     uint32_t g = group, e = 0, f = 0, g1 = 0;  // this group's next tile, the end of the piece
+    bool owed = false;                         // the q warp counts the last piece
+    uint32_t joins = 0;
+    const auto join_owed = [&] {
+      const bool known = __all_sync(0xffffffffu, mbar_wait_for(join_known, joins++ & 1, wait.limit));
+      if (known && counted->last)
+        join_piece(counted->b, counted->vkv, counted->npieces, counted->first, warp - kSoftmax0, 4 * kSG);
+      ok = ok && known;
+    };
     KvPiece pc;
     for (;; ++e) {
       const bool more = next_piece(e, pc);
-      if (vote(1, C::kSThreads, !more) != 0) break;  // together: the last piece, or a wait that ran out
+      if (vote(1, C::kSThreads, !more) != 0) {  // together: the last piece, or a wait that ran out
+        if (owed) join_owed();
+        break;
+      }
       int32_t head0, nh;
       vkv_heads(gr, pc.vkv, &head0, &nh);
       const int32_t n = tiles_of(pc);
@@ -927,11 +952,11 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
         const uint32_t qb = f & 1;
         const bool got = wait.warp(q_ready + qb, (f >> 1) & 1);
         const float* factor = reinterpret_cast<const float*>(smem + C::kMetaOff + qb * C::kMetaBytes);
-        const int32_t* meta = reinterpret_cast<const int32_t*>(factor + 16);
+        const int32_t* meta = reinterpret_cast<const int32_t*>(factor + 32);
         whole_end = min(pc.tok_end, meta[0]);
         npieces = meta[1];
         first = meta[2];
-        if (quad == 0 && lane < 16) fac[lane] = factor[lane];
+        if (quad == 0) fac[lane] = factor[lane];  // factors, then limits
         __syncwarp();
         if (lane == 0) mbar_arrive(q_free + qb);
         ++f;
@@ -969,10 +994,10 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
 #pragma unroll
           for (int h = 0; h < G; ++h) x[h] = fmaf(x[h], fac[h], -mr[h]);
           if (__builtin_expect(!whole, 0)) {
-            const RowLimits rl{head0, nh, pc.len, p.n_q, p.causal};
+            const int32_t t = t0 + key < pc.tok_end ? t0 + key : 0x7fffffff;
 #pragma unroll
             for (int h = 0; h < G; ++h)
-              if (t0 + key >= pc.tok_end || (h < nh && t0 + key >= rl(h))) x[h] = -INFINITY;
+              if (t >= lims[h]) x[h] = -INFINITY;
           }
 #pragma unroll
           for (int h = 0; h < G; ++h) up |= x[h] > kRefDown + kTau;
@@ -988,16 +1013,19 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
             for (int h = 0; h < G; ++h) seen |= (x[h] == -INFINITY ? 0u : 1u) << h;
             load_scores();
 #pragma unroll
-            for (int h = 0; h < G; ++h) {
-              const float mx = redux_max(seen >> h & 1 ? x[h] * fac[h] : -INFINITY);
-              if (lane == 0) red[quad * 16 + h] = mx;
+            for (int h = 0; h < G; ++h) x[h] = seen >> h & 1 ? x[h] * fac[h] : -INFINITY;
+            warp_reduce<G>(x, lane, [](float a, float b) { return fmaxf(a, b); });
+            if (lane % (32 / G) == 0) red[lane / (32 / G) * 4 + quad] = x[0];
+            named_barrier(bar, 128);
+            if (key < G) {
+              const float4 m = reinterpret_cast<const float4*>(red)[key];
+              red[64 + key] = fmaxf(fmaxf(m.x, m.y), fmaxf(m.z, m.w)) - kRefDown;
             }
             named_barrier(bar, 128);
             float (&alpha)[G < 2 ? 2 : G] = x;
 #pragma unroll
             for (int h = 0; h < G; ++h) {
-              const float mx = fmaxf(fmaxf(red[h], red[16 + h]), fmaxf(red[32 + h], red[48 + h])) - kRefDown;
-              const float mn = fmaxf(mr[h], mx);
+              const float mn = fmaxf(mr[h], red[64 + h]);
               alpha[h] = ex2(mr[h] - mn);
               mr[h] = mn;
               l[h] *= alpha[h];
@@ -1080,7 +1108,7 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
 #pragma unroll
         for (int h = 0; h < G; ++h) join[(group * G + h) * D + key] = 0.f;
       }
-      warp_sums<G>(l, lane);
+      warp_reduce<G>(l, lane, [](float a, float b) { return a + b; });
       if (lane % (32 / G) == 0) ends[lane / (32 / G) * 8 + group * 4 + quad] = l[0];
       if (key == 0) {
 #pragma unroll
@@ -1114,6 +1142,8 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
           }
         }
       }
+      if (owed) join_owed();  // before the q warp hears of this piece
+      owed = fused && !final_here && pc.more;
       if (fused && !final_here) {
         if (pc.more) {
           __syncwarp();
@@ -1122,10 +1152,7 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
           named_barrier(1, C::kSThreads);  // every thread's partial stores come before the release
           if (st == 0) *last_flag = arrive_last(pc, npieces) ? 1 : 0;
           named_barrier(1, C::kSThreads);
-          if (*last_flag) {
-            join_piece(pc, head0, nh, npieces, first, warp - kSoftmax0, 4 * kSG);
-            if (st == 0) p.counters[pc.b * p.hv + pc.vkv] = 0;  // ready for the next call
-          }
+          if (*last_flag) join_piece(pc.b, pc.vkv, npieces, first, warp - kSoftmax0, 4 * kSG);
         }
       }
     }
