@@ -88,6 +88,22 @@ struct KvPiece {
   int32_t pad;
 };
 
+// Lengths and tile counts as in CtaTiles, with this kernel's charge for a piece:
+// its end and the next one's start take a CTA about as long as six tiles (16 ragged
+// sequences 35.9 us with the bf16 kernel's charge of 1.25 tiles, 33.2 so; 8 windows of 4
+// rows 69 and 44).
+constexpr int kKv4PieceUnits = 6 * kTileUnits;
+struct Kv4Tiles {
+  const int32_t* pre;
+  const int32_t* ln;
+  int32_t ut, ul;
+  int uniform;
+  FD_HD int32_t piece() const { return uniform ? 0 : kKv4PieceUnits; }
+  FD_HD int64_t prefix(int32_t b) const { return uniform ? (int64_t)b * pair_units(ut, 0) : pre[b]; }
+  FD_HD int32_t tiles(int32_t b) const { return uniform ? ut : ceil_div(ln[b], kPlanTile); }
+  FD_HD int32_t len(int32_t b) const { return uniform ? ul : ln[b]; }
+};
+
 // A counted piece, from the q warp to the softmax warps.
 struct JoinPiece {
   int32_t last, b, vkv, npieces, first;
@@ -369,7 +385,7 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
   if (warp == 1) tmem_alloc_all(smem_addr(tmem_slot));
   pdl_launch_dependents();
   if (p.seq_lens != nullptr) pdl_wait();
-  CtaTiles tl;
+  Kv4Tiles tl;
   tl.pre = pre;
   tl.ln = lens;
   tl.ul = p.max_len;
@@ -384,7 +400,7 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
       const int lo = lane * per;
       const int hi = lo + per < p.B ? lo + per : p.B;
       int sum = 0;
-      for (int b = lo; b < hi; ++b) sum += (int)pair_units(ceil_div(lens[b], kPlanTile), kPieceUnits);
+      for (int b = lo; b < hi; ++b) sum += (int)pair_units(ceil_div(lens[b], kPlanTile), kKv4PieceUnits);
       int incl = sum;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -394,7 +410,7 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
       int run = incl - sum;
       for (int b = lo; b < hi; ++b) {
         pre[b] = run;
-        run += (int)pair_units(ceil_div(lens[b], kPlanTile), kPieceUnits);
+        run += (int)pair_units(ceil_div(lens[b], kPlanTile), kKv4PieceUnits);
       }
       if (lane == 31) pre[p.B] = incl;
     }
@@ -465,9 +481,24 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
     gr.nsub = p.nsub;
     gr.hv = p.hv;
     const uint64_t stream_policy = policy_evict_first();
-    PieceIter pieces(p, tl, total);
+    const bool balanced = p.n_splits == 0;
+    const int32_t used = balanced ? balanced_ctas(total, (int32_t)gridDim.x) : 0;
+    const bool part = balanced && (int32_t)blockIdx.x < used;  // this CTA has a share of the plan
+    BalancedWalk<Kv4Tiles> walk(tl, p.B, p.hv, part ? total : 0, part ? used : 1, part ? (int32_t)blockIdx.x : 0);
     Piece pc;
-    bool have = pieces.next(pc);
+    bool have;
+    if (balanced) {
+      have = walk.next(pc);
+    } else {
+      have = true;
+      pc.b = blockIdx.x / p.hv;
+      pc.vkv = blockIdx.x % p.hv;
+      pc.slot = blockIdx.y;
+      pc.len = p.seq_lens ? clamp_len(__ldg(p.seq_lens + pc.b), p.max_len) : p.max_len;
+      const int64_t lo = (int64_t)pc.slot * p.split_tokens, hi = lo + p.split_tokens;
+      pc.tok_begin = (int32_t)(lo < pc.len ? lo : pc.len);
+      pc.tok_end = (int32_t)(hi < pc.len ? hi : pc.len);
+    }
     cta_sync();
     uint32_t it = 0, e = 0, stalled = 0xffffffffu;
     Ring<C::kStages> st;
@@ -486,7 +517,7 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
       ++e;
       return (bool)__shfl_sync(0xffffffffu, r, 0);
     };
-    for (; have; have = pieces.next(pc)) {
+    for (; have; have = balanced && walk.next(pc)) {
       KvPiece d;
       d.b = pc.b;
       d.vkv = pc.vkv;
@@ -494,7 +525,7 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
       d.tok_end = pc.tok_end;
       d.slot = pc.slot;
       d.len = pc.len;
-      d.more = pieces.more() ? 1 : 0;
+      d.more = balanced && !walk.done() ? 1 : 0;
       live = announce(d);
       if (!live) break;
       if (!ok) continue;

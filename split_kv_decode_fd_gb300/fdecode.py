@@ -8,8 +8,10 @@ CPU fallback: calls with CPU tensors raise, and a missing library raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
+import struct
 import threading
 from typing import Optional, Sequence
 
@@ -192,9 +194,15 @@ def plan_pieces(B, Hq, Hkv, seq_lens: Optional[Sequence[int]], max_seq_len, n_sp
 
 
 # ------------------------------------------------------------------ device
+_TORCH = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
 
 
 def _stream_handle(device, stream=None) -> int:
@@ -612,39 +620,74 @@ def workspace_status(workspace: Optional[Workspace] = None, device=None, stream=
 
 
 # ------------------------------------------------------------------ rotating append, 4-bit cache
-def _opt(t, name, dtype, device, shape=None):
-    """Pointer of an optional contiguous tensor on ``device``; None without one."""
-    if t is None:
-        return None
-    _need_cuda(t, name, dtype)
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+#
+# These calls take a few microseconds on the device, less than Python takes to ask a
+# tensor a dozen questions: the checks use the cheap ones (get_device() is -1 off the
+# GPU, dtypes are singletons), and structures are packed in one go.
+_ROWS = struct.Struct("@i4x3P9q4P3i4x")
+_KV = struct.Struct("@2i2PqP3i4x")
+_KV4 = struct.Struct("@i4xPqP5i4x")
+assert _ROWS.size == ctypes.sizeof(NewRows) and _KV.size == ctypes.sizeof(KvDesc) and _KV4.size == ctypes.sizeof(Kv4Desc)
+
+
+def _flat(t, name, dtype, index, shape=None):
+    """Pointer of a contiguous CUDA tensor of ``dtype`` on device ``index``."""
+    if not isinstance(t, _torch().Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (libfdecode has no CPU path)")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
-def _scratch(workspace, device, nbytes):
+def _opt(t, name, dtype, index, shape=None):
+    """Pointer of an optional tensor (see ``_flat``); 0 without one."""
+    return 0 if t is None else _flat(t, name, dtype, index, shape)
+
+
+def _index_of(t, name):
+    if not isinstance(t, _torch().Tensor) or t.get_device() < 0:
+        raise ValueError(f"{name} must be a CUDA tensor (libfdecode has no CPU path)")
+    return t.get_device()
+
+
+def _scratch(workspace, index, nbytes):
     """The workspace's buffer.  It is not made during a stream capture: its first
     zero-fill would then run only with the graph."""
-    ws = workspace or _default_workspace(device)
+    torch = _torch()
+    ws = workspace
+    if ws is None:
+        ws = _DEFAULT_WS.get(("cuda", index)) or _default_workspace(torch.device("cuda", index))
     buf = ws.buf
-    if buf is None or buf.numel() < nbytes or buf.device != device:
-        if _torch().cuda.is_current_stream_capturing():
+    if buf is None or buf.numel() < nbytes or buf.get_device() != index:
+        if torch.cuda.is_current_stream_capturing():
             raise RuntimeError("the workspace is too small and cannot grow during a stream capture: run the call once "
                                "before the capture, or pass a Workspace that has been used at this size")
-        buf = ws.get(nbytes, device)
+        buf = ws.get(nbytes, torch.device("cuda", index))
     return buf
 
 
-def _launch(device, fn, where, *args):
-    """Call ``fn`` with ``device`` current (the library launches on the current device)."""
+@functools.lru_cache(maxsize=256)
+def _decode_bytes(B, Hq, Hkv, D, n_splits, index):
+    """``workspace_bytes`` on device ``index``."""
+    with _torch().cuda.device(index):
+        return workspace_bytes(B, Hq, Hkv, D, n_splits)
+
+
+def _launch(index, stream, fn, where, *args):
+    """Call ``fn(*args, stream)`` with device ``index`` current (the library launches on the current device)."""
     torch = _torch()
-    if device.index == torch.cuda.current_device():
-        st = fn(*args)
+    s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if index == torch.cuda.current_device():
+        st = fn(*args, s)
     else:
-        with torch.cuda.device(device):
-            st = fn(*args)
+        with torch.cuda.device(index):
+            st = fn(*args, s)
     if st != FD_OK:
         raise FdError(st, where)
 
@@ -667,92 +710,91 @@ def kv4_cache(n, Hkv, tokens, D, device="cuda"):
     return _torch().zeros((n, Hkv, tokens // 16, kv4_block_bytes(D)), dtype=_torch().uint8, device=device)
 
 
+def _table(block_table, B, index):
+    """Pointer and row length of a block table of B sequences."""
+    at = _flat(block_table, "block_table", _torch().int32, index)
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"block_table must be [{B}, max_pages]")
+    return at, block_table.shape[1]
+
+
 def _kv4_desc(kv4, block_table, B, k_exp, v_exp):
-    """Descriptor, Hkv, D and tokens per sequence of a 4-bit cache tensor."""
-    torch = _torch()
-    _need_cuda(kv4, "kv4", torch.uint8)
+    """Descriptor, Hkv, D, tokens per sequence and device index of a 4-bit cache tensor."""
+    index = _index_of(kv4, "kv4")
+    at = _flat(kv4, "kv4", _torch().uint8, index)
     if kv4.dim() != 4 or kv4.shape[3] not in (18 * 64, 18 * 128):
         raise ValueError("kv4 must be uint8 [n, Hkv, tokens / 16, 18 * D] with D = 64 or 128")
-    d = Kv4Desc()
-    d.kv = kv4.data_ptr()
-    d.k_exp, d.v_exp = int(k_exp), int(v_exp)
-    tokens = kv4.shape[2] * 16
+    n, Hkv, blocks, size = kv4.shape
+    tokens = blocks * 16
     if block_table is None:
-        if kv4.shape[0] != B:
-            raise ValueError(f"a contiguous kv4 must hold {B} sequences, got {kv4.shape[0]}")
-        d.layout = FD_KV_CONTIGUOUS
-        d.capacity = tokens
+        if n != B:
+            raise ValueError(f"a contiguous kv4 must hold {B} sequences, got {n}")
+        d = _KV4.pack(FD_KV_CONTIGUOUS, at, tokens, 0, 0, 0, 0, int(k_exp), int(v_exp))
     else:
-        d.block_table = _opt(block_table, "block_table", torch.int32, kv4.device)
-        if block_table.dim() != 2 or block_table.shape[0] != B:
-            raise ValueError(f"block_table must be [{B}, max_pages]")
-        d.layout = FD_KV_PAGED
-        d.max_pages_per_seq = block_table.shape[1]
-        d.page_size = tokens
-        d.num_pages = kv4.shape[0]
-        tokens *= block_table.shape[1]
-    return d, kv4.shape[1], kv4.shape[3] // 18, tokens
+        table, pages = _table(block_table, B, index)
+        d = _KV4.pack(FD_KV_PAGED, at, 0, table, pages, tokens, n, int(k_exp), int(v_exp))
+        tokens *= pages
+    return Kv4Desc.from_buffer_copy(d), Hkv, size // 18, tokens, index
 
 
-def _head_rows(t, name, B, n, D, device, dtype):
+def _head_rows(t, name, B, n, heads, D, index, dtype):
     """Strides of ``t`` [B, n, heads, D], whose channels are contiguous."""
-    if not isinstance(t, _torch().Tensor) or not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be a CUDA tensor on {device}")
-    if t.dtype != dtype:
+    if not isinstance(t, _torch().Tensor) or t.get_device() != index:
+        raise ValueError(f"{name} must be a CUDA tensor on cuda:{index}")
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 4 or t.shape[0] != B or t.shape[1] != n or t.shape[3] != D:
-        raise ValueError(f"{name} must be [{B}, {n}, heads, {D}], got {tuple(t.shape)}")
+    shape = t.shape
+    if len(shape) != 4 or shape[0] != B or shape[1] != n or shape[3] != D:
+        raise ValueError(f"{name} must be [{B}, {n}, heads, {D}], got {tuple(shape)}")
+    if heads is not None and shape[2] != heads:
+        raise ValueError(f"{name} must have the cache's {heads} heads, got {shape[2]}")
     st = t.stride()
     if st[3] != 1:
         raise ValueError(f"the channels of {name} must be contiguous")
-    return st[0], st[1], st[2]
+    return st
 
 
-def _append_args(k_new, v_new, Hkv, D, tokens, device, cos, sin, q, q_out, rot_dim, interleaved, positions, new_lens,
-                 seq_lens, max_seq_len):
+def _append(fn, where, desc, k_new, v_new, Hkv, D, tokens, index, cos, sin, q, q_out, rot_dim, interleaved, positions,
+            new_lens, seq_lens, max_seq_len, workspace, stream):
     torch = _torch()
-    if not isinstance(k_new, torch.Tensor) or k_new.dim() != 4:
-        raise ValueError("k_new must be [B, n, Hkv, D]")
     B, n = k_new.shape[0], k_new.shape[1]
-    dt = {torch.bfloat16: FD_BF16, torch.float32: FD_F32}.get(k_new.dtype)
-    if dt is None:
-        raise ValueError(f"unsupported dtype of the new rows {k_new.dtype}")
-    r = NewRows()
-    r.dtype = dt
-    r.k_stride[:] = _head_rows(k_new, "k_new", B, n, D, device, k_new.dtype)
-    r.v_stride[:] = _head_rows(v_new, "v_new", B, n, D, device, k_new.dtype)
-    if k_new.shape[2] != Hkv or v_new.shape[2] != Hkv:
-        raise ValueError(f"k_new and v_new must have the cache's {Hkv} heads")
-    r.k, r.v = k_new.data_ptr(), v_new.data_ptr()
-    Hq = 0
+    dtype = k_new.dtype
+    dt = FD_BF16 if dtype is torch.bfloat16 else FD_F32 if dtype is torch.float32 else -1
+    if dt < 0:
+        raise ValueError(f"unsupported dtype of the new rows {dtype}")
+    ks = _head_rows(k_new, "k_new", B, n, Hkv, D, index, dtype)
+    vs = _head_rows(v_new, "v_new", B, n, Hkv, D, index, dtype)
+    Hq, qp, qo, qs = 0, 0, 0, (0, 0, 0)
     if q is not None:
-        r.q_stride[:] = _head_rows(q, "q", B, n, D, device, k_new.dtype)
-        Hq = q.shape[2]
-        r.q = q.data_ptr()
+        qs = _head_rows(q, "q", B, n, None, D, index, dtype)
+        Hq, qp = q.shape[2], q.data_ptr()
         if q_out is None:
-            # rows that new_lens leaves out are not written: they start as zeros
+            # rows that new_lens or a bad position leaves out are not written: they start as zeros
             make = torch.empty if new_lens is None and positions is None else torch.zeros
-            q_out = make((B, Hq, n, D), dtype=torch.float32, device=device)
+            q_out = make((B, Hq, n, D), dtype=torch.float32, device=q.device)
+            qo = q_out.data_ptr()
         else:
-            _opt(q_out, "q_out", torch.float32, device, (B, Hq, n, D))
+            qo = _flat(q_out, "q_out", torch.float32, index, (B, Hq, n, D))
     elif q_out is not None:
         raise ValueError("q_out without q")
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin come together")
+    cp = sp = max_pos = rot = 0
     if cos is not None:
         if cos.dim() != 2 or cos.shape != sin.shape:
             raise ValueError("cos and sin must be [max_pos, rot_dim / 2]")
-        r.cos, r.sin = _opt(cos, "cos", torch.float32, device), _opt(sin, "sin", torch.float32, device)
-        r.max_pos, r.rot_dim = cos.shape[0], 2 * cos.shape[1]
-    if rot_dim is not None and rot_dim != r.rot_dim:
-        raise ValueError(f"rot_dim {rot_dim} does not fit tables of {r.rot_dim // 2} pairs")
-    r.interleaved = int(bool(interleaved))
-    r.new_lens = _opt(new_lens, "new_lens", torch.int32, device, (B,))
-    r.positions = _opt(positions, "positions", torch.int32, device, (B, n))
-    lens = _opt(seq_lens, "seq_lens", torch.int32, device, (B,))
-    if max_seq_len is None:
-        max_seq_len = tokens - n
-    return r, B, n, Hq, lens, int(max_seq_len), q_out
+        cp, sp = _flat(cos, "cos", torch.float32, index), _flat(sin, "sin", torch.float32, index)
+        max_pos, rot = cos.shape[0], 2 * cos.shape[1]
+    if rot_dim is not None and rot_dim != rot:
+        raise ValueError(f"rot_dim {rot_dim} does not fit tables of {rot // 2} pairs")
+    rows = NewRows.from_buffer_copy(_ROWS.pack(
+        dt, qp, k_new.data_ptr(), v_new.data_ptr(), qs[0], qs[1], qs[2], ks[0], ks[1], ks[2], vs[0], vs[1], vs[2],
+        _opt(new_lens, "new_lens", torch.int32, index, (B,)), _opt(positions, "positions", torch.int32, index, (B, n)),
+        cp, sp, max_pos, rot, 1 if interleaved else 0))
+    buf = _scratch(workspace, index, 256)
+    _launch(index, stream, fn, where, rows, desc, qo, B, n, Hq, Hkv, _opt(seq_lens, "seq_lens", torch.int32, index, (B,)),
+            tokens - n if max_seq_len is None else int(max_seq_len), D, buf.data_ptr(), buf.numel())
+    return q_out
 
 
 def append_rope(k_new, v_new, k, v, cos=None, sin=None, *, q=None, q_out=None, rot_dim=None, interleaved=False,
@@ -765,28 +807,32 @@ def append_rope(k_new, v_new, k, v, cos=None, sin=None, *, q=None, q_out=None, r
     written in place.  ``cos``, ``sin`` fp32 ``[max_pos, rot_dim / 2]`` (None: no rotation).  Token ``j`` of sequence
     ``b`` goes to place ``seq_lens[b] + j``; with ``new_lens`` ``[B]`` only the last ``new_lens[b]`` of the ``n``
     rows are tokens.  ``seq_lens`` and ``max_seq_len`` are the lengths before the append.  ``positions``
-    ``[B, n]`` int32 replaces the places as rows of the tables.  Returns the rotated queries, fp32 ``[B, Hq, n, D]`` (``q_out`` if given,
-    whose padding rows keep their contents; None without ``q``).
+    ``[B, n]`` int32 replaces the places as rows of the tables.  Returns the rotated queries, fp32
+    ``[B, Hq, n, D]`` (``q_out`` if given, whose padding rows keep their contents; None without ``q``).
     """
-    kv = _kv_desc(k, v, block_table)
-    device = k.device
-    if k.dim() != 4 or v.device != device:
-        raise ValueError("k and v must be 4-d and on one device")
-    tokens = k.shape[2]
-    if block_table is not None:
-        if block_table.device != device or block_table.dim() != 2 or block_table.shape[0] != k_new.shape[0]:
-            raise ValueError("block_table must be [B, max_pages] on the cache's device")
-        tokens *= block_table.shape[1]
-    elif k.shape[0] != k_new.shape[0]:
-        raise ValueError(f"a contiguous cache must hold {k_new.shape[0]} sequences, got {k.shape[0]}")
-    r, B, n, Hq, lens, max_seq_len, q_out = _append_args(k_new, v_new, k.shape[1], k.shape[3], tokens, device, cos, sin,
-                                                         q, q_out, rot_dim, interleaved, positions, new_lens, seq_lens,
-                                                         max_seq_len)
-    buf = _scratch(workspace, device, 256)
-    _launch(device, _lib().fd_append_rope, "fd_append_rope", ctypes.byref(r), ctypes.byref(kv),
-            q_out.data_ptr() if q_out is not None else None, B, n, Hq, k.shape[1], lens, max_seq_len, k.shape[3],
-            buf.data_ptr(), buf.numel(), _stream_handle(device, stream))
-    return q_out
+    torch = _torch()
+    index = _index_of(k, "k")
+    if not isinstance(k_new, torch.Tensor) or k_new.dim() != 4:
+        raise ValueError("k_new must be [B, n, Hkv, D]")
+    if k.dim() != 4:
+        raise ValueError("k and v must be [B, Hkv, T, D] or [num_pages, Hkv, page, D]")
+    shape, dtype, B = k.shape, k.dtype, k_new.shape[0]
+    dt = FD_BF16 if dtype is torch.bfloat16 else FD_F32 if dtype is torch.float32 else -1
+    if dt < 0:
+        raise ValueError(f"unsupported KV dtype {dtype}")
+    at, vt = _flat(k, "k", dtype, index), _flat(v, "v", dtype, index, shape)
+    tokens = shape[2]
+    if block_table is None:
+        if shape[0] != B:
+            raise ValueError(f"a contiguous cache must hold {B} sequences, got {shape[0]}")
+        d = _KV.pack(FD_KV_CONTIGUOUS, dt, at, vt, tokens, 0, 0, 0, 0)
+    else:
+        table, pages = _table(block_table, B, index)
+        d = _KV.pack(FD_KV_PAGED, dt, at, vt, 0, table, pages, tokens, shape[0])
+        tokens *= pages
+    return _append(_lib().fd_append_rope, "fd_append_rope", KvDesc.from_buffer_copy(d), k_new, v_new, shape[1], shape[3],
+                   tokens, index, cos, sin, q, q_out, rot_dim, interleaved, positions, new_lens, seq_lens, max_seq_len,
+                   workspace, stream)
 
 
 def append_rope_kv4(k_new, v_new, kv4, cos=None, sin=None, *, k_exp=0, v_exp=0, q=None, q_out=None, rot_dim=None,
@@ -795,16 +841,9 @@ def append_rope_kv4(k_new, v_new, kv4, cos=None, sin=None, *, k_exp=0, v_exp=0, 
     """``fd_append_rope_kv4``: ``append_rope`` into a 4-bit cache (see ``kv4_cache``), written in place."""
     if not isinstance(k_new, _torch().Tensor) or k_new.dim() != 4:
         raise ValueError("k_new must be [B, n, Hkv, D]")
-    kv, Hkv, D, tokens = _kv4_desc(kv4, block_table, k_new.shape[0], k_exp, v_exp)
-    device = kv4.device
-    r, B, n, Hq, lens, max_seq_len, q_out = _append_args(k_new, v_new, Hkv, D, tokens, device, cos, sin, q, q_out,
-                                                         rot_dim, interleaved, positions, new_lens, seq_lens,
-                                                         max_seq_len)
-    buf = _scratch(workspace, device, 256)
-    _launch(device, _lib().fd_append_rope_kv4, "fd_append_rope_kv4", ctypes.byref(r), ctypes.byref(kv),
-            q_out.data_ptr() if q_out is not None else None, B, n, Hq, Hkv, lens, max_seq_len, D, buf.data_ptr(),
-            buf.numel(), _stream_handle(device, stream))
-    return q_out
+    desc, Hkv, D, tokens, index = _kv4_desc(kv4, block_table, k_new.shape[0], k_exp, v_exp)
+    return _append(_lib().fd_append_rope_kv4, "fd_append_rope_kv4", desc, k_new, v_new, Hkv, D, tokens, index, cos, sin,
+                   q, q_out, rot_dim, interleaved, positions, new_lens, seq_lens, max_seq_len, workspace, stream)
 
 
 def kv4_read(kv4, n, *, starts=None, seq_lens=None, max_seq_len=None, block_table=None, k_exp=0, v_exp=0, dtype=None,
@@ -815,26 +854,25 @@ def kv4_read(kv4, n, *, starts=None, seq_lens=None, max_seq_len=None, block_tabl
     ``v_out`` (zeros when they are made here).  Returns ``(k_out, v_out)``.
     """
     torch = _torch()
+    index = _index_of(kv4, "kv4")
     B = kv4.shape[0] if block_table is None else block_table.shape[0]
-    kv, Hkv, D, tokens = _kv4_desc(kv4, block_table, B, k_exp, v_exp)
-    device = kv4.device
+    desc, Hkv, D, tokens, index = _kv4_desc(kv4, block_table, B, k_exp, v_exp)
     if dtype is None:
         dtype = torch.bfloat16 if k_out is None else k_out.dtype
-    dt = {torch.bfloat16: FD_BF16, torch.float32: FD_F32}.get(dtype)
-    if dt is None:
+    dt = FD_BF16 if dtype is torch.bfloat16 else FD_F32 if dtype is torch.float32 else -1
+    if dt < 0:
         raise ValueError(f"unsupported dtype {dtype}")
-    shape = (B, Hkv, int(n), D)
+    n = int(n)
+    shape = (B, Hkv, n, D)
     if k_out is None:
-        k_out = torch.zeros(shape, dtype=dtype, device=device)
+        k_out = torch.zeros(shape, dtype=dtype, device=kv4.device)
     if v_out is None:
-        v_out = torch.zeros(shape, dtype=dtype, device=device)
-    if max_seq_len is None:
-        max_seq_len = tokens
-    buf = _scratch(workspace, device, 256)
-    _launch(device, _lib().fd_kv4_read, "fd_kv4_read", ctypes.byref(kv), _opt(k_out, "k_out", dtype, device, shape),
-            _opt(v_out, "v_out", dtype, device, shape), dt, B, int(n), Hkv,
-            _opt(starts, "starts", torch.int32, device, (B,)), _opt(seq_lens, "seq_lens", torch.int32, device, (B,)),
-            int(max_seq_len), D, buf.data_ptr(), buf.numel(), _stream_handle(device, stream))
+        v_out = torch.zeros(shape, dtype=dtype, device=kv4.device)
+    buf = _scratch(workspace, index, 256)
+    _launch(index, stream, _lib().fd_kv4_read, "fd_kv4_read", desc, _flat(k_out, "k_out", dtype, index, shape),
+            _flat(v_out, "v_out", dtype, index, shape), dt, B, n, Hkv, _opt(starts, "starts", torch.int32, index, (B,)),
+            _opt(seq_lens, "seq_lens", torch.int32, index, (B,)), tokens if max_seq_len is None else int(max_seq_len), D,
+            buf.data_ptr(), buf.numel())
     return k_out, v_out
 
 
@@ -847,32 +885,33 @@ def decode_kv4(q, kv4, *, k_exp=0, v_exp=0, causal=True, seq_lens=None, max_seq_
     ``kv4_cache``.  Returns ``(out, lse)`` shaped like q and q without its last axis.
     """
     torch = _torch()
-    _need_cuda(q, "q", torch.float32)
-    if q.dim() not in (3, 4):
+    index = _index_of(q, "q")
+    at = _flat(q, "q", torch.float32, index)
+    shape = q.shape
+    rank = len(shape)
+    if rank != 3 and rank != 4:
         raise ValueError("q must be [B, Hq, D] or [B, Hq, n_q, D]")
-    shape = tuple(q.shape)
     B, Hq = shape[0], shape[1]
-    n_q = shape[2] if len(shape) == 4 else 1
-    kv, Hkv, D, tokens = _kv4_desc(kv4, block_table, B, k_exp, v_exp)
-    device = q.device
+    n_q = shape[2] if rank == 4 else 1
+    desc, Hkv, D, tokens, on = _kv4_desc(kv4, block_table, B, k_exp, v_exp)
     if D != shape[-1]:
         raise ValueError("head_dim of q and kv4 differ")
-    if kv4.device != device:
+    if on != index:
         raise ValueError("q and kv4 must be on one device")
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
     if out is None:
-        out = torch.empty(shape, dtype=torch.float32, device=device)
+        out = torch.empty_like(q)
+        op = out.data_ptr()
     else:
-        _opt(out, "out", torch.float32, device, shape)
+        op = _flat(out, "out", torch.float32, index, shape)
+    lp = 0
     if lse is not None:
-        _opt(lse, "lse", torch.float32, device, shape[:-1])
+        lp = _flat(lse, "lse", torch.float32, index, shape[:-1])
     elif return_lse:
-        lse = torch.empty(shape[:-1], dtype=torch.float32, device=device)
-    buf = _scratch(workspace, device, workspace_bytes(B, Hq * n_q, Hkv, D, n_splits))
-    _launch(device, _lib().fd_decode_kv4, "fd_decode_kv4", q.data_ptr(), n_q, int(bool(causal)), ctypes.byref(kv),
-            out.data_ptr(), lse.data_ptr() if lse is not None else None, B, Hq, Hkv,
-            _opt(seq_lens, "seq_lens", torch.int32, device, (B,)),
-            int(max_seq_len) if max_seq_len is not None else tokens, D, float(scale), int(n_splits), buf.data_ptr(),
-            buf.numel(), _stream_handle(device, stream))
+        lse = torch.empty(shape[:-1], dtype=torch.float32, device=q.device)
+        lp = lse.data_ptr()
+    n_splits = int(n_splits)
+    buf = _scratch(workspace, index, _decode_bytes(B, Hq * n_q, Hkv, D, n_splits, index))
+    _launch(index, stream, _lib().fd_decode_kv4, "fd_decode_kv4", at, n_q, 1 if causal else 0, desc, op, lp, B, Hq, Hkv,
+            _opt(seq_lens, "seq_lens", torch.int32, index, (B,)), tokens if max_seq_len is None else int(max_seq_len), D,
+            1.0 / math.sqrt(D) if scale is None else float(scale), n_splits, buf.data_ptr(), buf.numel())
     return out, lse
