@@ -61,7 +61,7 @@ constexpr int kSoftmax0 = 20;                          // first softmax warp
 // 2^(kRefDown + kTau) = 2^15, and the smallest fp16 number stands for 2^-33 of the
 // maximum's weight.
 constexpr float kRefDown = 9.f, kTau = 6.f;
-constexpr float kNoRef = -1e30f;  // of a head that has seen no key: any score lies above it
+constexpr float kNoRef = -3.402823466e38f;  // of a head that has seen no key: no score lies below it
 
 // Position in a ring of NB buffers: tile g is in buffer g % NB, its phase (g / NB) & 1.
 template <uint32_t NB>
@@ -308,11 +308,12 @@ __device__ __forceinline__ bool mbar_sleep_wait(uint64_t* bar, uint32_t parity) 
 }
 
 // The part of a wait that is not complete at once, out of the way of the tile loops.
+// One that runs out ends the CTA's others.
 __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned long long limit) {
   const unsigned long long t0 = global_ns();
   while (!*abort_flag) {
     if (mbar_sleep_wait(bar, parity)) return true;
-    if (global_ns() - t0 > limit) return false;
+    if (global_ns() - t0 > limit) *abort_flag = 1;
   }
   return false;
 }
@@ -428,13 +429,15 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
   }
   const int64_t total = (int64_t)p.hv * tl.prefix(p.B);
   const Waiter wait{abort_flag, wait_limit(p)};
+  // Pieces are announced, counted and joined after an abort, too, or the workspace's
+  // counters would be left set: these waits outlast the one that ran out.
+  const unsigned long long patience = 4 * wait.limit;
   bool ok = true;
 
   // Every role but the producer takes the announced pieces in order.
   const auto next_piece = [&](uint32_t e, KvPiece& pc) {
     const uint32_t sl = e % kDescs;
-    // not `wait.warp`: pieces are still announced after an abort
-    const bool got = __all_sync(0xffffffffu, mbar_wait_for(desc_full + sl, (e / kDescs) & 1, wait.limit));
+    const bool got = __all_sync(0xffffffffu, mbar_wait_for(desc_full + sl, (e / kDescs) & 1, patience));
     if (got) pc = descs[sl];
     __syncwarp();
     if (got && lane == 0) mbar_arrive(desc_empty + sl);
@@ -508,7 +511,7 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
       const uint32_t sl = e % kDescs;
       bool r = true;
       if (lane == 0) {
-        r = mbar_wait_for(desc_empty + sl, ((e / kDescs) & 1) ^ 1, wait.limit);
+        r = mbar_wait_for(desc_empty + sl, ((e / kDescs) & 1) ^ 1, patience);
         if (r) {
           descs[sl] = d;
           mbar_arrive(desc_full + sl);
@@ -726,16 +729,18 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
 #pragma unroll 1
       for (int h = 0; h < G; ++h) {
 #pragma unroll
-        for (int i = 0; i < E; ++i) x[i] = nx[i];
+        for (int i = 0; i < E; ++i) x[i] = nx[i] * p.qk_scale;
         if (h + 1 < G) load_head(h + 1);
         float big = 0.f;
 #pragma unroll
         for (int i = 0; i < E; ++i) big = fmaxf(big, fabsf(x[i]));
         big = warp_max_abs(big);
-        // 2^e <= big < 2^(e + 1): q times 2^(13 - e) fills fp16's range
+        // 2^e <= big < 2^(e + 1): q times 2^(13 - e) fills fp16's range.  The factor of a
+        // score is then a power of two, so the product with it is exact: its difference
+        // from a reference may be fused, and is never above zero for the largest score.
         int ex = (int)(__float_as_uint(big) >> 23) - 127;
         if (big == 0.f || ex > 127) ex = 13;
-        ex = ex < -80 ? -80 : (ex > 80 ? 80 : ex);
+        ex = ex < -80 ? -80 : ex;  // 2^(13 - ex) is a float
         const float up = pow2i(13 - ex);
 #pragma unroll
         for (int i = 0; i < E; i += 2) {
@@ -744,7 +749,7 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
           asm volatile("st.shared.u32 [%0], %1;" ::"r"(qs + b_off<N>(h, lane * E + i)), "r"(hi) : "memory");
           asm volatile("st.shared.u32 [%0], %1;" ::"r"(qs + b_off<N>(G + h, lane * E + i)), "r"(lo) : "memory");
         }
-        if (lane == 0) factor[h] = h < nh ? p.qk_scale * pow2i(kv.k_exp) * pow2i(ex - 13) : 0.f;
+        if (lane == 0) factor[h] = h < nh ? pow2i(kv.k_exp) * pow2i(ex - 13) : 0.f;
       }
       {  // the keys that each head sees, and the fewest
         const int32_t limit = lane < nh ? rl(lane) : 0x7fffffff;
@@ -773,7 +778,7 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
       j.b = pc.b;
       j.vkv = pc.vkv;
       j.npieces = pieces_of(pc, j.first);
-      const bool done = __all_sync(0xffffffffu, mbar_wait_for(part_done, parts++ & 1, wait.limit));
+      const bool done = __all_sync(0xffffffffu, mbar_wait_for(part_done, parts++ & 1, patience));
       if (!done) ok = false;
       if (lane == 0) {
         j.last = done && arrive_last(pc, j.npieces) ? 1 : 0;
@@ -813,7 +818,7 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
     KvPiece pc;
     for (; next_piece(e, pc); ++e) {
       if (ok) g1 += tiles_of(pc);
-      for (; g < g1; g += 2, kr.skip()) {
+      for (; ok && g < g1; g += 2, kr.skip()) {
         const uint32_t st = g % C::kStages;
         if (!wait.warp(full + st, g / C::kStages & 1) || (g >= C::kKBufs && !wait.warp(k_free + kr.i, kr.ph ^ 1))) {
           ok = false;
@@ -863,7 +868,7 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
       for (; next_piece(e, pc); ++e) {
         const uint32_t g0 = g1;
         if (ok) g1 += tiles_of(pc);
-        for (; g < g1; g += 2, vr.skip()) {
+        for (; ok && g < g1; g += 2, vr.skip()) {
           const uint32_t st = g % C::kStages;
           if (!wait.warp(full + st, g / C::kStages & 1) || (g >= C::kVBufs && !wait.warp(v_free + vr.i, vr.ph ^ 1))) {
             ok = false;
@@ -954,7 +959,7 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
     bool owed = false;                         // the q warp counts the last piece
     uint32_t joins = 0;
     const auto join_owed = [&] {
-      const bool known = __all_sync(0xffffffffu, mbar_wait_for(join_known, joins++ & 1, wait.limit));
+      const bool known = __all_sync(0xffffffffu, mbar_wait_for(join_known, joins++ & 1, patience));
       if (known && counted->last)
         join_piece(counted->b, counted->vkv, counted->npieces, counted->first, warp - kSoftmax0, 4 * kSG);
       ok = ok && known;
@@ -1018,7 +1023,7 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
             for (int h = 0; h < G; ++h) x[h] += lo[h];
           }
         };
-        for (;;) {
+        for (bool again = false;; again = true) {
           // exponents relative to the references; almost always none lies too far above
           bool up = false;
           load_scores();
@@ -1029,6 +1034,13 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
 #pragma unroll
             for (int h = 0; h < G; ++h)
               if (t >= lims[h]) x[h] = -INFINITY;
+          }
+          if (__builtin_expect(again, 0)) {
+            // Once is enough.  Scores of 2^27 and more are further apart than kTau: a reference
+            // that was rounded down by more than that stays, and the exponent is cut.
+#pragma unroll
+            for (int h = 0; h < G; ++h) x[h] = x[h] > kRefDown + kTau ? kRefDown + kTau : x[h];
+            break;
           }
 #pragma unroll
           for (int h = 0; h < G; ++h) up |= x[h] > kRefDown + kTau;
@@ -1050,13 +1062,14 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
             named_barrier(bar, 128);
             if (key < G) {
               const float4 m = reinterpret_cast<const float4*>(red)[key];
-              red[64 + key] = fmaxf(fmaxf(m.x, m.y), fmaxf(m.z, m.w)) - kRefDown;
+              const float top = fmaxf(fmaxf(m.x, m.y), fmaxf(m.z, m.w)) - kRefDown;
+              red[64 + key] = top == INFINITY ? NAN : top;  // a score past the range of floats shows as NaN
             }
             named_barrier(bar, 128);
             float (&alpha)[G < 2 ? 2 : G] = x;
 #pragma unroll
             for (int h = 0; h < G; ++h) {
-              const float mn = fmaxf(mr[h], red[64 + h]);
+              const float mn = red[64 + h] <= mr[h] ? mr[h] : red[64 + h];
               alpha[h] = ex2(mr[h] - mn);
               mr[h] = mn;
               l[h] *= alpha[h];
@@ -1107,7 +1120,7 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         } else {
-          *abort_flag = 1;  // seen by this group at its next wait
+          raise_error(p.err, kErrTimeout);  // the abort ends this group at its next wait
         }
         tmem_fence_before();
         __syncwarp();
