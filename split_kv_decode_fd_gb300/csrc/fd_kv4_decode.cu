@@ -184,9 +184,6 @@ __device__ __forceinline__ uint32_t lds16u(uint32_t at) {
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
   return v;
 }
-__device__ __forceinline__ void sts16(uint32_t at, uint32_t v) {
-  asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"((unsigned short)v) : "memory");
-}
 __device__ __forceinline__ void sts128u(uint32_t at, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
@@ -536,18 +533,25 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
       const uint8_t* base = kv.kv;
       if (!kv.paged)
         base += (((int64_t)pc.b * kv.Hkv + kvh) * kv.cap_blocks + pc.tok_begin / kKv4Tokens) * kv4_block_bytes(D);
-      // Paged: lane k has block k of four tiles at hand (its number in the pool, -1
+      // Paged: lane k has block k of four tiles at hand (its number in the pool, kNoBlock
       // for a page outside it), and the table entry of its block of the next four
-      // is in flight.
+      // is in flight.  Blocks of a tile that follow one another in the pool go in one
+      // copy: an SM starts one in some 90 cycles, whichever warp asks, so that pages of
+      // sixteen tokens are bound by it (524288 tokens of 8 heads 162 us, of a
+      // contiguous cache 121; sixteen-byte copies by a warp's lanes took 182).
       const int32_t blk0 = pc.tok_begin / kKv4Tokens, blk1 = ceil_div(pc.tok_end, kKv4Tokens);
-      int64_t cur = 0;
+      constexpr uint32_t kNoBlock = 0xffffffffu;  // a pool has fewer: 2^32 blocks are 4.9 TB
+      uint32_t cur = 0, firsts = 0, bads = 0;     // of four tiles: blocks that start a copy, blocks outside the pool
       int32_t page = 0, rem = 0, at = 0;  // of the next four tiles: the page, the block in it, the table entry
       int32_t ppb = 1, step_q = 0, step_r = 0;  // blocks of a page; thirty-two blocks on
       const int32_t* trow = kv.block_table + (size_t)pc.b * kv.max_pages;
       int32_t blk = blk0 + lane;
       const auto load_page = [&] { page = blk < blk1 ? __ldg(trow + at) : 0; };
       const auto take_page = [&] {
-        cur = page >= 0 && page < kv.num_pages ? ((int64_t)page * kv.Hkv + kvh) * ppb + rem : -1;
+        cur = page >= 0 && page < kv.num_pages ? ((uint32_t)page * (uint32_t)kv.Hkv + kvh) * ppb + rem : kNoBlock;
+        const uint32_t before = __shfl_up_sync(0xffffffffu, cur, 1);
+        firsts = __ballot_sync(0xffffffffu, lane % kTileBlocks == 0 || cur != before + 1);
+        bads = __ballot_sync(0xffffffffu, cur == kNoBlock && blk < blk1);
         blk += 32;
         at += step_q;
         rem += step_r;
@@ -591,23 +595,31 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
                 : "memory");
           }
         } else {
-          const int k = lane - (j & 3) * kTileBlocks;  // this lane's block of the tile
-          const bool mine = k >= 0 && k < nblk;
-          const bool bad = mine && cur < 0;
-          if (bad) {
+          const int k0 = (j & 3) * kTileBlocks;
+          const uint32_t valid = (1u << nblk) - 1, bad = bads >> k0 & valid;
+          const int k = lane - k0;  // this lane's block of the tile
+          uint32_t starts = firsts >> k0 & valid;
+          if (__builtin_expect(bad != 0, 0)) {
             // keys of score 0 and value 0 in its place
-            raise_error(p.err, kErrBadIndex);
-            for (int i = 0; i < kv4_block_bytes(D); i += 16)
-              sts128u(smem_addr(dst) + k * kv4_block_bytes(D) + i, make_uint4(0, 0, 0, 0));
-            // before a later copy into this stage
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            if (k >= 0 && k < kTileBlocks && bad >> k & 1) {
+              raise_error(p.err, kErrBadIndex);
+              for (int i = 0; i < kv4_block_bytes(D); i += 16)
+                sts128u(smem_addr(dst) + k * kv4_block_bytes(D) + i, make_uint4(0, 0, 0, 0));
+              // before a later copy into this stage
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            }
+            starts = (starts | bad << 1) & valid & ~bad;  // a block after a bad one starts a copy
+            __syncwarp();
           }
+          const uint8_t* from = kv.kv + (uint64_t)cur * kv4_block_bytes(D);
+          if (starts == valid) {  // one a block: a constant size is quicker to issue
+            if (k >= 0 && k < nblk) bulk_load(dst + k * kv4_block_bytes(D), from, kv4_block_bytes(D), full + st.i);
+          } else if (k >= 0 && k < kTileBlocks && starts >> k & 1) {
+            const uint32_t stops = starts | bad | ~valid;  // the next copy, a bad block, the tile's end
+            bulk_load(dst + k * kv4_block_bytes(D), from, __ffs(stops >> (k + 1)) * kv4_block_bytes(D), full + st.i);
+          }
+          if (lane == 0) mbar_arrive_expect_tx(full + st.i, __popc(valid & ~bad) * kv4_block_bytes(D));
           __syncwarp();
-          const uint32_t copies = __popc(__ballot_sync(0xffffffffu, mine && !bad));
-          if (lane == 0) mbar_arrive_expect_tx(full + st.i, copies * kv4_block_bytes(D));
-          __syncwarp();
-          if (mine && !bad)
-            bulk_load(dst + k * kv4_block_bytes(D), kv.kv + cur * kv4_block_bytes(D), kv4_block_bytes(D), full + st.i);
           if ((j & 3) == 3) take_page();
         }
       }
@@ -633,16 +645,9 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
     // Every branch and operand here is uniform over the warp as the compiler sees it
     // (votes and shuffles): only then do the MMAs take their operands from uniform
     // registers as they are (18 cycles each to issue; 70 to 130 otherwise).
-    constexpr uint32_t idesc = f16_instr_desc(kTile, N);
+    constexpr uint32_t s_desc = f16_instr_desc(kTile, N), o_desc = f16_instr_desc(kTile, N, true);
     const uint32_t base = uniform(tmem), sb = uniform(sbase);
     const bool is_s = uniform(warp) == 1;
-    // A eight columns on per K = 16 step, B 32 bytes on within a swizzled row, then
-    // the next column block
-    const auto issue = [&](uint32_t d, uint32_t a, uint32_t b, auto steps, uint32_t acc) {
-#pragma unroll
-      for (int kk = 0; kk < decltype(steps)::value; ++kk)
-        mma_ts(d, a + kk * 8, b_desc(b + (kk >> 2) * (N * 128) + (kk & 3) * 32), idesc, kk > 0 ? 1u : acc);
-    };
     uint32_t g = 0, f = 0;  // tiles, pieces with tiles
     Ring<C::kKBufs> kr;
     Ring<C::kVBufs> vr;
@@ -664,8 +669,13 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
           tmem_fence_after();
           const uint32_t qb = f & 1;
           if (elect_one()) {
-            issue(base + C::kColS + sr.i * N, base + C::kColK + kr.i * (D / 2), sb + C::kQOff + qb * C::kQBytes,
-                  std::integral_constant<int, D / 16>{}, 0);
+            // A is eight columns on per K = 16 step, B 32 bytes within a swizzled row, then
+            // the next column block
+            const uint32_t d = base + C::kColS + sr.i * N, a = base + C::kColK + kr.i * (D / 2),
+                           b = sb + C::kQOff + qb * C::kQBytes;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              mma_ts(d, a + kk * 8, b_desc(b + (kk >> 2) * (N * 128) + (kk & 3) * 32), s_desc, kk > 0);
             mma_commit(smem_addr(s_full + sr.i));
             mma_commit(smem_addr(k_free + kr.i));
             if (j == n - 1) mma_commit(smem_addr(q_free + qb));
@@ -678,8 +688,11 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
           tmem_fence_after();
           if (elect_one()) {
             // the group's first tile of the piece starts its O
-            issue(base + C::kColO + sg * N, base + C::kColV + vr.i * (kTile / 2), sb + C::kPOff + sr.i * C::kPBytes,
-                  std::integral_constant<int, kTile / 16>{}, j >= (int32_t)kSG ? 1u : 0u);
+            const uint32_t d = base + C::kColO + sg * N, a = base + C::kColV + vr.i * (kTile / 2),
+                           b = sb + C::kPOff + sr.i * C::kPBytes;
+#pragma unroll
+            for (int kk = 0; kk < kTile / 16; ++kk)
+              mma_ts(d, a + kk * 8, b_desc_n<16 * kTile>(b + kk * 256), o_desc, kk > 0 || j >= (int32_t)kSG);
             mma_commit(smem_addr(p_free + sr.i));
             mma_commit(smem_addr(v_free + vr.i));
           }
@@ -936,9 +949,8 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
     // references; and the groups' O.
     float* ends = reinterpret_cast<float*>(smem + C::kEndOff);
     float* join = reinterpret_cast<float*>(smem + C::kJoinOff);
-    // This thread's key in row 0 of a p buffer; row n is 128 n bytes on, its
-    // 16-byte chunk turned by n % 8.
-    const uint32_t p_at = sbase + C::kPOff + b_off<N>(0, key);
+    // This thread's key in a p buffer: eight columns, the next eight 16 * kTile bytes on.
+    const uint32_t p_at = sbase + C::kPOff + key * 16;
     Groups gr;
     gr.g = p.g;
     gr.gpad = p.gpad;
@@ -1106,17 +1118,23 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
             x[h] = ex2(x[h]);
             l[h] += x[h];
           }
-          if constexpr (G == 1) x[1] = 0.f;
-#pragma unroll
-          for (int h = 0; h < G; h += 2) {
+          uint32_t w[G < 2 ? 1 : G];  // columns of hi, then of lo, in pairs
+          if constexpr (G == 1) {
             uint32_t hi, lo;
-            split_f16x2(x[h], x[h + 1], hi, lo);
-            sts16((ps ^ ((h & 7) << 4)) + h * 128, hi);
-            sts16((ps ^ (((G + h) & 7) << 4)) + (G + h) * 128, lo);
-            if (G > 1) {
-              sts16((ps ^ (((h + 1) & 7) << 4)) + (h + 1) * 128, hi >> 16);
-              sts16((ps ^ (((G + h + 1) & 7) << 4)) + (G + h + 1) * 128, lo >> 16);
-            }
+            split_f16x2(x[0], 0.f, hi, lo);
+            w[0] = hi | lo << 16;
+          } else {
+#pragma unroll
+            for (int h = 0; h < G; h += 2) split_f16x2(x[h], x[h + 1], w[h / 2], w[(G + h) / 2]);
+          }
+          if constexpr (G == 1) {
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(ps), "r"(w[0]) : "memory");
+          } else if constexpr (G == 2) {
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(ps), "r"(w[0]), "r"(w[1]) : "memory");
+          } else {
+#pragma unroll
+            for (int c = 0; c < G; c += 4)
+              sts128u(ps + c / 4 * (16 * kTile), make_uint4(w[c], w[c + 1], w[c + 2], w[c + 3]));
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         } else {

@@ -15,9 +15,19 @@ __device__ __forceinline__ uint64_t b_desc(uint32_t saddr) {
   return ((uint64_t)kHi << 32) | ((saddr >> 4) & 0x3FFFu);
 }
 
-// Instruction descriptor of kind::f16: fp32 accumulator, A and B fp16, both K-major.
-__host__ __device__ constexpr uint32_t f16_instr_desc(int M, int N) {
-  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+// The same of an N-major B operand without a swizzle: 16 bytes hold eight n of one
+// k, consecutive k are 16 bytes apart (bits 16-29: distance of eight k / 16), the next
+// eight n `n_stride` bytes on (bits 32-45).
+template <int NStride>
+__device__ __forceinline__ uint64_t b_desc_n(uint32_t saddr) {
+  constexpr uint32_t kHi = ((uint32_t)NStride >> 4) | (1u << 14);
+  return ((uint64_t)kHi << 32) | ((128u >> 4) << 16) | ((saddr >> 4) & 0x3FFFu);
+}
+
+// Instruction descriptor of kind::f16: fp32 accumulator, A and B fp16, A K-major, B
+// K-major or (bit 16) N-major.
+__host__ __device__ constexpr uint32_t f16_instr_desc(int M, int N, bool b_n_major = false) {
+  return (1u << 4) | ((b_n_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
 // D[tmem] (+)= A[tmem] B: 128 rows, 16 of K.
