@@ -245,44 +245,56 @@ __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xf
 // Join of the partial states of one head by one warp: M = max m, weights
 // exp(m_k - M) over the states with l > 0, out = sum w O / L, lse = M + ln L.
 // State k is partial index base + k * stride.  Thirty-two states' weights at a
-// time, their O slices in batches of eight loads, in a fixed order.
+// time, their O slices in batches of eight loads, in a fixed order.  The first
+// thirty-two states' m and l and the first batch are asked for at once: one
+// trip to L2 for few states (16 heads of 9 states on 8 warps TIME_J).
 template <int D>
 __device__ __forceinline__ void join_states(const SplitParams& p, size_t base, size_t stride, int count, float* out,
                                             float* lse, int lane) {
   constexpr int E = D / 32;
-  float mx = -INFINITY;
-  for (int k = lane; k < count; k += 32)
+  float v[8][E];
+  const auto load_batch = [&](int k0) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+#pragma unroll
+      for (int i = 0; i < E; ++i) v[j][i] = 0.f;
+      if (k0 + j < count) load_slice<D>(p.o_part + (base + (k0 + j) * stride) * D + lane * E, v[j]);
+    }
+  };
+  float m = -INFINITY, l = 0.f;
+  if (lane < count) {
+    m = __ldcg(p.m_part + base + lane * stride);
+    l = __ldcg(p.l_part + base + lane * stride);
+  }
+  load_batch(0);
+  float mx = l > 0.f ? m : -INFINITY;
+  for (int k = lane + 32; k < count; k += 32)
     if (__ldcg(p.l_part + base + k * stride) > 0.f) mx = fmaxf(mx, __ldcg(p.m_part + base + k * stride));
   mx = warp_max(mx);
   float acc[E], L = 0.f;
 #pragma unroll
   for (int i = 0; i < E; ++i) acc[i] = 0.f;
   if (mx != -INFINITY) {
-    for (int k0 = 0; k0 < count; k0 += 32) {
-      const int k = k0 + lane;
-      float w = 0.f;
-      if (k < count) {
-        const float l = __ldcg(p.l_part + base + k * stride);
-        if (l > 0.f) {
-          w = exp2f((__ldcg(p.m_part + base + k * stride) - mx) * kLog2e);
-          L = fmaf(w, l, L);
+#pragma unroll 1
+    for (int k0 = 0; k0 < count; k0 += 8) {
+      if (k0 > 0) {
+        if (k0 % 32 == 0) {
+          l = 0.f;
+          if (k0 + lane < count) {
+            m = __ldcg(p.m_part + base + (k0 + lane) * stride);
+            l = __ldcg(p.l_part + base + (k0 + lane) * stride);
+          }
         }
+        load_batch(k0);
       }
-      const int m = count - k0 < 32 ? count - k0 : 32;
-      for (int j0 = 0; j0 < m; j0 += 8) {
-        float v[8][E];
+      float w = 0.f;
+      if (l > 0.f) w = exp2f((m - mx) * kLog2e);
+      if (k0 % 32 == 0) L = fmaf(w, l, L);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < 8; ++j) {
+        const float wj = __shfl_sync(0xffffffffu, w, (k0 + j) & 31);
 #pragma unroll
-          for (int i = 0; i < E; ++i) v[j][i] = 0.f;
-          if (j0 + j < m) load_slice<D>(p.o_part + (base + (k0 + j0 + j) * stride) * D + lane * E, v[j]);
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float wj = __shfl_sync(0xffffffffu, w, (j0 + j) & 31);
-#pragma unroll
-          for (int i = 0; i < E; ++i) acc[i] = fmaf(wj, v[j][i], acc[i]);
-        }
+        for (int i = 0; i < E; ++i) acc[i] = fmaf(wj, v[j][i], acc[i]);
       }
     }
     L = warp_sum(L);
@@ -732,18 +744,21 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
       float* factor = reinterpret_cast<float*>(smem + C::kMetaOff + qb * C::kMetaBytes);
       const uint32_t qs = sbase + C::kQOff + qb * C::kQBytes;
       constexpr int E = D / 32;
-      float x[E], nx[E];
-      const auto load_head = [&](int h) {
+      // Four heads' loads at a time, one group ahead (one head ahead: 16 heads took 10000
+      // cycles before the first S).
+      constexpr int kAtOnce = G < 4 ? G : 4;
+      float x[kAtOnce][E], nx[kAtOnce][E];
+      const auto load_heads = [&](int h0, float (&to)[kAtOnce][E]) {
 #pragma unroll
-        for (int i = 0; i < E; ++i) nx[i] = 0.f;
-        if (h < nh) load_slice<D>(p.q + ((size_t)pc.b * p.Hq + head0 + h) * D + lane * E, nx);
+        for (int a = 0; a < kAtOnce; ++a) {
+#pragma unroll
+          for (int i = 0; i < E; ++i) to[a][i] = 0.f;
+          if (h0 + a < nh) load_slice<D>(p.q + ((size_t)pc.b * p.Hq + head0 + h0 + a) * D + lane * E, to[a]);
+        }
       };
-      load_head(0);
-#pragma unroll 1
-      for (int h = 0; h < G; ++h) {
+      const auto put_head = [&](int h, float (&x)[E]) {
 #pragma unroll
-        for (int i = 0; i < E; ++i) x[i] = nx[i] * p.qk_scale;
-        if (h + 1 < G) load_head(h + 1);
+        for (int i = 0; i < E; ++i) x[i] *= p.qk_scale;
         float big = 0.f;
 #pragma unroll
         for (int i = 0; i < E; ++i) big = fmaxf(big, fabsf(x[i]));
@@ -763,6 +778,17 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
           asm volatile("st.shared.u32 [%0], %1;" ::"r"(qs + b_off<N>(G + h, lane * E + i)), "r"(lo) : "memory");
         }
         if (lane == 0) factor[h] = h < nh ? pow2i(kv.k_exp) * pow2i(ex - 13) : 0.f;
+      };
+      load_heads(0, x);
+#pragma unroll 1
+      for (int h0 = 0; h0 < G; h0 += kAtOnce) {
+        if (h0 + kAtOnce < G) load_heads(h0 + kAtOnce, nx);
+#pragma unroll
+        for (int a = 0; a < kAtOnce; ++a) {
+          put_head(h0 + a, x[a]);
+#pragma unroll
+          for (int i = 0; i < E; ++i) x[a][i] = nx[a][i];
+        }
       }
       {  // the keys that each head sees, and the fewest
         const int32_t limit = lane < nh ? rl(lane) : 0x7fffffff;
