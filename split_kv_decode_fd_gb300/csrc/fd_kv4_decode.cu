@@ -300,7 +300,11 @@ __device__ __forceinline__ void join_states(const SplitParams& p, size_t base, s
     L = warp_sum(L);
   }
 #pragma unroll
-  for (int i = 0; i < E; ++i) out[lane * E + i] = mx == -INFINITY ? 0.f : acc[i] / L;
+  for (int i = 0; i < E; ++i) acc[i] = mx == -INFINITY ? 0.f : acc[i] / L;
+  if constexpr (E == 4)
+    *reinterpret_cast<float4*>(out + lane * E) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+  else
+    *reinterpret_cast<float2*>(out + lane * E) = make_float2(acc[0], acc[1]);
   if (lse && lane == 0) *lse = mx == -INFINITY ? -INFINITY : mx + logf(L);
 }
 
@@ -1205,23 +1209,29 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
       named_barrier(1, C::kSThreads);
       const bool final_here = fused && npieces == 1;
 #pragma unroll 1
-      for (int idx = st; idx < nh * D; idx += C::kSThreads) {
-        const int h = idx / D, d = idx % D;
+      for (int idx = st; idx < nh * (D / 4); idx += C::kSThreads) {
+        const int h = idx / (D / 4), d = idx % (D / 4) * 4;
         // the groups' states on the largest reference; one without keys has l = 0
         const float4 la = reinterpret_cast<const float4*>(ends)[2 * h], lb = reinterpret_cast<const float4*>(ends)[2 * h + 1];
         const float2 ms = reinterpret_cast<const float2*>(ends + 128)[h];
+        const float4 oa = *reinterpret_cast<const float4*>(join + h * D + d);
+        const float4 ob = *reinterpret_cast<const float4*>(join + (G + h) * D + d);
         const float l0 = (la.x + la.y) + (la.z + la.w), l1 = (lb.x + lb.y) + (lb.z + lb.w), mm = fmaxf(ms.x, ms.y);
         const float w0 = l0 == 0.f ? 0.f : ex2(ms.x - mm), w1 = l1 == 0.f ? 0.f : ex2(ms.y - mm);
-        const float L = fmaf(w0, l0, w1 * l1);
-        float acc = fmaf(w0, join[h * D + d], w1 * join[(G + h) * D + d]);
-        acc *= pow2i(kv.v_exp);
+        const float L = fmaf(w0, l0, w1 * l1), up = pow2i(kv.v_exp);
+        float4 acc = make_float4(fmaf(w0, oa.x, w1 * ob.x) * up, fmaf(w0, oa.y, w1 * ob.y) * up,
+                                 fmaf(w0, oa.z, w1 * ob.z) * up, fmaf(w0, oa.w, w1 * ob.w) * up);
         const size_t row = (size_t)pc.b * p.Hq + head0 + h;
         if (final_here) {
-          p.out[row * D + d] = L == 0.f ? 0.f : acc / L;
+          acc.x = L == 0.f ? 0.f : acc.x / L;
+          acc.y = L == 0.f ? 0.f : acc.y / L;
+          acc.z = L == 0.f ? 0.f : acc.z / L;
+          acc.w = L == 0.f ? 0.f : acc.w / L;
+          *reinterpret_cast<float4*>(p.out + row * D + d) = acc;
           if (p.lse && d == 0) p.lse[row] = L == 0.f ? -INFINITY : (mm + log2f(L)) * kLn2;
         } else {
           const size_t i = balanced ? (size_t)pc.slot * p.gpad + h : row * p.n_splits + pc.slot;
-          p.o_part[i * D + d] = acc;
+          *reinterpret_cast<float4*>(p.o_part + i * D + d) = acc;
           if (d == 0) {
             // The join passes over states whose l is not above zero.  A NaN sum goes in as
             // m = inf: the weight exp(inf - inf) then makes out and lse NaN, as the formula does.
