@@ -89,16 +89,17 @@ struct KvPiece {
 };
 
 // Lengths and tile counts as in CtaTiles, with this kernel's charge for a piece:
-// its end and the next one's start take a CTA about as long as six tiles (16 ragged
-// sequences 35.9 us with the bf16 kernel's charge of 1.25 tiles, 33.2 so; 8 windows of 4
-// rows 69 and 44).
-constexpr int kKv4PieceUnits = 6 * kTileUnits;
+// its end and the next one's start take a CTA about as long as four tiles, with 16
+// heads as long as seven of its longer tiles (16 ragged sequences 35.9 us with the bf16
+// kernel's charge of 1.25 tiles, 31.7 so; 64 paged sequences of 8 heads a group 111 us,
+// with a charge of six 114; 8 windows of 4 rows 34.4, with a charge of four 36.1).
+template <int Units>
 struct Kv4Tiles {
   const int32_t* pre;
   const int32_t* ln;
   int32_t ut, ul;
   int uniform;
-  FD_HD int32_t piece() const { return uniform ? 0 : kKv4PieceUnits; }
+  FD_HD int32_t piece() const { return uniform ? 0 : Units; }
   FD_HD int64_t prefix(int32_t b) const { return uniform ? (int64_t)b * pair_units(ut, 0) : pre[b]; }
   FD_HD int32_t tiles(int32_t b) const { return uniform ? ut : ceil_div(ln[b], kPlanTile); }
   FD_HD int32_t len(int32_t b) const { return uniform ? ul : ln[b]; }
@@ -120,6 +121,7 @@ struct K4 {
   static constexpr uint32_t kColK = 0, kColV = kColK + kKBufs * (D / 2), kColS = kColV + kVBufs * (kTile / 2),
                             kColO = kColS + kSBufs * kN;  // O: one per softmax group
   static_assert(kColO + kSGroups * kN <= 512, "tensor memory");
+  static constexpr int kPieceUnits = (G == 16 ? 7 : 4) * kTileUnits;
   static constexpr int kStageBytes = kTileBlocks * kv4_block_bytes(D);
   static constexpr int kStages = D == 128 ? 8 : 16;  // a power of two
   static constexpr int kVWarps = D / 32;
@@ -235,10 +237,6 @@ __device__ __forceinline__ bool elect_one() {
   uint32_t r;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
   return r != 0;
-}
-// Largest of the warp's values, none below zero; a NaN is the largest.
-__device__ __forceinline__ float warp_max_abs(float x) {
-  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(x))));
 }
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 
@@ -399,7 +397,7 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
   if (warp == 1) tmem_alloc_all(smem_addr(tmem_slot));
   pdl_launch_dependents();
   if (p.seq_lens != nullptr) pdl_wait();
-  Kv4Tiles tl;
+  Kv4Tiles<C::kPieceUnits> tl;
   tl.pre = pre;
   tl.ln = lens;
   tl.ul = p.max_len;
@@ -414,7 +412,7 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
       const int lo = lane * per;
       const int hi = lo + per < p.B ? lo + per : p.B;
       int sum = 0;
-      for (int b = lo; b < hi; ++b) sum += (int)pair_units(ceil_div(lens[b], kPlanTile), kKv4PieceUnits);
+      for (int b = lo; b < hi; ++b) sum += (int)pair_units(ceil_div(lens[b], kPlanTile), C::kPieceUnits);
       int incl = sum;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -424,7 +422,7 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
       int run = incl - sum;
       for (int b = lo; b < hi; ++b) {
         pre[b] = run;
-        run += (int)pair_units(ceil_div(lens[b], kPlanTile), kKv4PieceUnits);
+        run += (int)pair_units(ceil_div(lens[b], kPlanTile), C::kPieceUnits);
       }
       if (lane == 31) pre[p.B] = incl;
     }
@@ -500,7 +498,7 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
     const bool balanced = p.n_splits == 0;
     const int32_t used = balanced ? balanced_ctas(total, (int32_t)gridDim.x) : 0;
     const bool part = balanced && (int32_t)blockIdx.x < used;  // this CTA has a share of the plan
-    BalancedWalk<Kv4Tiles> walk(tl, p.B, p.hv, part ? total : 0, part ? used : 1, part ? (int32_t)blockIdx.x : 0);
+    BalancedWalk<Kv4Tiles<C::kPieceUnits>> walk(tl, p.B, p.hv, part ? total : 0, part ? used : 1, part ? (int32_t)blockIdx.x : 0);
     Piece pc;
     bool have;
     if (balanced) {
@@ -747,51 +745,60 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
       const RowLimits rl{head0, nh, pc.len, p.n_q, p.causal};
       float* factor = reinterpret_cast<float*>(smem + C::kMetaOff + qb * C::kMetaBytes);
       const uint32_t qs = sbase + C::kQOff + qb * C::kQBytes;
-      constexpr int E = D / 32;
-      // Four heads' loads at a time, one group ahead (one head ahead: 16 heads took 10000
-      // cycles before the first S).
-      constexpr int kAtOnce = G < 4 ? G : 4;
-      float x[kAtOnce][E], nx[kAtOnce][E];
-      const auto load_heads = [&](int h0, float (&to)[kAtOnce][E]) {
+      // A lane holds eight channels, so a pass of the warp takes 256 / D heads; two passes'
+      // loads at a time, one pair of passes ahead (one head a pass and one ahead: 16 heads
+      // took 10000 cycles before the first S).
+      constexpr int kLanes = D / 8, kHeads = 32 / kLanes;
+      const int c8 = lane % kLanes * 8, hl = lane / kLanes;
+      float x[2][8], nx[2][8];
+      const auto load_heads = [&](int h0, float (&to)[2][8]) {
 #pragma unroll
-        for (int a = 0; a < kAtOnce; ++a) {
-#pragma unroll
-          for (int i = 0; i < E; ++i) to[a][i] = 0.f;
-          if (h0 + a < nh) load_slice<D>(p.q + ((size_t)pc.b * p.Hq + head0 + h0 + a) * D + lane * E, to[a]);
+        for (int a = 0; a < 2; ++a) {
+          const int h = h0 + a * kHeads + hl;
+          float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
+          if (h < nh) {
+            const float4* row = reinterpret_cast<const float4*>(p.q + ((size_t)pc.b * p.Hq + head0 + h) * D + c8);
+            lo = __ldcg(row);
+            hi = __ldcg(row + 1);
+          }
+          to[a][0] = lo.x; to[a][1] = lo.y; to[a][2] = lo.z; to[a][3] = lo.w;
+          to[a][4] = hi.x; to[a][5] = hi.y; to[a][6] = hi.z; to[a][7] = hi.w;
         }
       };
-      const auto put_head = [&](int h, float (&x)[E]) {
+      const auto put_heads = [&](int h, float (&x)[8]) {
+        uint32_t big = 0;  // a NaN is the largest
 #pragma unroll
-        for (int i = 0; i < E; ++i) x[i] *= p.qk_scale;
-        float big = 0.f;
+        for (int i = 0; i < 8; ++i) {
+          x[i] *= p.qk_scale;
+          big = max(big, __float_as_uint(fabsf(x[i])));
+        }
 #pragma unroll
-        for (int i = 0; i < E; ++i) big = fmaxf(big, fabsf(x[i]));
-        big = warp_max_abs(big);
+        for (int o = kLanes / 2; o > 0; o /= 2) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
         // 2^e <= big < 2^(e + 1): q times 2^(13 - e) fills fp16's range.  The factor of a
         // score is then a power of two, so the product with it is exact: its difference
         // from a reference may be fused, and is never above zero for the largest score.
-        int ex = (int)(__float_as_uint(big) >> 23) - 127;
-        if (big == 0.f || ex > 127) ex = 13;
+        int ex = (int)(big >> 23) - 127;
+        if (big == 0 || ex > 127) ex = 13;
         ex = ex < -80 ? -80 : ex;  // 2^(13 - ex) is a float
         const float up = pow2i(13 - ex);
+        uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int i = 0; i < E; i += 2) {
-          uint32_t hi, lo;
-          split_f16x2(x[i] * up, x[i + 1] * up, hi, lo);
-          asm volatile("st.shared.u32 [%0], %1;" ::"r"(qs + b_off<N>(h, lane * E + i)), "r"(hi) : "memory");
-          asm volatile("st.shared.u32 [%0], %1;" ::"r"(qs + b_off<N>(G + h, lane * E + i)), "r"(lo) : "memory");
+        for (int i = 0; i < 4; ++i) split_f16x2(x[2 * i] * up, x[2 * i + 1] * up, hi[i], lo[i]);
+        if (G % kHeads == 0 || h < G) {
+          sts128u(qs + b_off<N>(h, c8), make_uint4(hi[0], hi[1], hi[2], hi[3]));
+          sts128u(qs + b_off<N>(G + h, c8), make_uint4(lo[0], lo[1], lo[2], lo[3]));
+          if (c8 == 0) factor[h] = h < nh ? pow2i(kv.k_exp) * pow2i(ex - 13) : 0.f;
         }
-        if (lane == 0) factor[h] = h < nh ? pow2i(kv.k_exp) * pow2i(ex - 13) : 0.f;
       };
       load_heads(0, x);
 #pragma unroll 1
-      for (int h0 = 0; h0 < G; h0 += kAtOnce) {
-        if (h0 + kAtOnce < G) load_heads(h0 + kAtOnce, nx);
+      for (int h0 = 0; h0 < G; h0 += 2 * kHeads) {
+        if (h0 + 2 * kHeads < G) load_heads(h0 + 2 * kHeads, nx);
 #pragma unroll
-        for (int a = 0; a < kAtOnce; ++a) {
-          put_head(h0 + a, x[a]);
+        for (int a = 0; a < 2; ++a) {
+          if (h0 + a * kHeads < G) put_heads(h0 + a * kHeads + hl, x[a]);
 #pragma unroll
-          for (int i = 0; i < E; ++i) x[a][i] = nx[a][i];
+          for (int i = 0; i < 8; ++i) x[a][i] = nx[a][i];
         }
       }
       {  // the keys that each head sees, and the fewest
