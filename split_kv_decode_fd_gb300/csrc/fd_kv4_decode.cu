@@ -61,6 +61,11 @@ constexpr int kSoftmax0 = 20;                          // first softmax warp
 // 2^(kRefDown + kTau) = 2^15, and the smallest fp16 number stands for 2^-33 of the
 // maximum's weight.
 constexpr float kRefDown = 9.f, kTau = 6.f;
+// Tiles of a group whose O products add up in tensor memory before their sum moves to
+// fp32 adds in shared memory.  An MMA's add drops bits instead of rounding, some 2^-25.6
+// of the sum each and all one way: with 27 tiles in a row the outputs of 128k tokens were
+// 4.2e-6 off (2-norm), with four 8.1e-7.  It costs 0.5 us of 40, with 16 heads a group 5 of 57.
+constexpr uint32_t kFlush = 4;
 constexpr float kNoRef = -3.402823466e38f;  // of a head that has seen no key: no score lies below it
 
 // Position in a ring of NB buffers: tile g is in buffer g % NB, its phase (g / NB) & 1.
@@ -245,7 +250,7 @@ __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xf
 // State k is partial index base + k * stride.  Thirty-two states' weights at a
 // time, their O slices in batches of eight loads, in a fixed order.  The first
 // thirty-two states' m and l and the first batch are asked for at once: one
-// trip to L2 for few states (16 heads of 9 states on 8 warps TIME_J).
+// trip to L2 for few states (16 heads of 9 states on 8 warps took 14000 cycles with the loads one after another, 10000 so).
 template <int D>
 __device__ __forceinline__ void join_states(const SplitParams& p, size_t base, size_t stride, int count, float* out,
                                             float* lse, int lane) {
@@ -701,12 +706,12 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
           }
           tmem_fence_after();
           if (elect_one()) {
-            // the group's first tile of the piece starts its O
+            const bool fresh = j / (int32_t)kSG % (int32_t)kFlush == 0;  // a new sum
             const uint32_t d = base + C::kColO + sg * N, a = base + C::kColV + vr.i * (kTile / 2),
                            b = sb + C::kPOff + sr.i * C::kPBytes;
 #pragma unroll
             for (int kk = 0; kk < kTile / 16; ++kk)
-              mma_ts(d, a + kk * 8, b_desc_n<16 * kTile>(b + kk * 256), o_desc, kk > 0 || j >= (int32_t)kSG);
+              mma_ts(d, a + kk * 8, b_desc_n<16 * kTile>(b + kk * 256), o_desc, kk > 0 || !fresh);
             mma_commit(smem_addr(p_free + sr.i));
             mma_commit(smem_addr(v_free + vr.i));
           }
@@ -1051,7 +1056,30 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
       const uint32_t g0 = g1;
       if (run) g1 += n;
       const uint32_t g_first = g;
-      for (; run && g < g1; g += kSG) {
+      for (; run; g += kSG) {
+        const uint32_t jj = (g - g_first) / kSG;  // the group's tile
+        if (jj > 0 && (g >= g1 || jj % kFlush == 0)) {  // O of the last tiles joins the sums in shared memory
+          const bool got = wait.warp(p_free + (g - kSG) % C::kSBufs, (g - kSG) / C::kSBufs & 1);
+          if (vote(bar, 128, !got) != 0) {
+            ok = run = false;
+            break;
+          }
+          tmem_fence_after();
+          constexpr int W = G < 2 ? 2 : (G < 8 ? G : 8);
+#pragma unroll 1
+          for (int h0 = 0; h0 < G; h0 += W) {
+            float hi[W], lo[W];
+            tmem_load<W>(tmem + lanes + C::kColO + group * N + h0, hi);
+            tmem_load<W>(tmem + lanes + C::kColO + group * N + G + h0, lo);
+            if (key < D) {
+              float* sum = join + (group * G + h0) * D + key;
+#pragma unroll
+              for (int h = 0; h < W && h0 + h < G; ++h) sum[h * D] = (jj > kFlush ? sum[h * D] : 0.f) + (hi[h] + lo[h]);
+            }
+          }
+          tmem_fence_before();
+        }
+        if (g >= g1) break;
         const uint32_t i = g % C::kSBufs, ph = g / C::kSBufs & 1;
         const int32_t t0 = pc.tok_begin + (int32_t)(g - g0) * kTile;
         const bool whole = t0 + kTile <= whole_end;
@@ -1123,6 +1151,10 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
               mr[h] = mn;
               l[h] *= alpha[h];
             }
+            if (jj >= kFlush && key < D) {
+#pragma unroll
+              for (int h = 0; h < G; ++h) join[(group * G + h) * D + key] *= alpha[h];
+            }
             if (g != g_first) {
               moved = wait.warp(p_free + (g - kSG) % C::kSBufs, (g - kSG) / C::kSBufs & 1);  // O of this group's last tile
               if (moved) {
@@ -1184,26 +1216,7 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
       // ---- end of the piece: sums over the keys, O by channel, the groups joined.
       // (Rolled loops over shared memory: code that runs once a piece is not in the
       // instruction cache, and its length was what a piece's end took.)
-      if (run && g != g_first) {
-        const bool got = wait.warp(p_free + (g - kSG) % C::kSBufs, (g - kSG) / C::kSBufs & 1);  // O of the last tile
-        if (vote(bar, 128, !got) != 0) {
-          ok = run = false;
-        } else {
-          tmem_fence_after();
-          constexpr int W = G < 2 ? 2 : (G < 8 ? G : 8);
-#pragma unroll
-          for (int h0 = 0; h0 < G; h0 += W) {
-            float hi[W], lo[W];
-            tmem_load<W>(tmem + lanes + C::kColO + group * N + h0, hi);
-            tmem_load<W>(tmem + lanes + C::kColO + group * N + G + h0, lo);
-            if (key < D) {
-#pragma unroll
-              for (int h = 0; h < W && h0 + h < G; ++h) join[(group * G + h0 + h) * D + key] = hi[h] + lo[h];
-            }
-          }
-          tmem_fence_before();
-        }
-      } else if (key < D) {
+      if ((!run || g == g_first) && key < D) {
 #pragma unroll
         for (int h = 0; h < G; ++h) join[(group * G + h) * D + key] = 0.f;
       }
