@@ -367,6 +367,11 @@ FD_API fd_status fd_kv4_read(const fd_kv4_desc* kv, void* k_out, void* v_out, fd
  * q, out and lse, the same masking, lengths and split arguments, and a workspace of
  * fd_workspace_bytes(B, Hq * n_q, Hkv, D, n_splits, 0) bytes.  A page outside the pool
  * counts as keys with score 0 and value 0, and is reported as FD_ERR_BAD_INDEX.
+ * q and the softmax weights are held to 22 bits, products and sums in fp32.  Scores
+ * may have any size that fp32 holds.  A NaN key shows in the rows that see it; a NaN
+ * value of one of the last n_q tokens in every row of the window, those before the
+ * token too (its weight there is 0, and 0 * NaN is NaN), and of an older token in all
+ * rows, as it should.
  */
 FD_API fd_status fd_decode_kv4(const float* q, int32_t n_q, int32_t causal, const fd_kv4_desc* kv, float* out,
                                float* lse, int32_t B, int32_t Hq, int32_t Hkv, const int32_t* seq_lens,
@@ -479,7 +484,7 @@ FD_API int64_t fd_plan_pieces(int32_t B, int32_t Hq, int32_t Hkv, int32_t kv_dty
  * it issued land and exits, so the context stays usable.  With stage >= 0, the
  * kernels launched afterwards skip, in every CTA that reaches it, the copies of
  * stage number `stage` (split kernels: fd_decode and every call built on it,
- * fd_split_partial) or K/V tile copy number `stage` (fd_prefill, K and V
+ * fd_split_partial; fd_decode_kv4) or K/V tile copy number `stage` (fd_prefill, K and V
  * counted separately), so the waits for it run out; wait_limit_ns > 0 shortens
  * every wait of those kernels to that many nanoseconds (0 keeps the default).  The
  * call's output is then undefined and fd_workspace_status (or

@@ -14,29 +14,39 @@
 // and stores them there.  code * scale has six significant bits and is exact in
 // fp16.  The B operands are small: q (once per piece) and p (per tile) in shared
 // memory, each as the sum of two fp16 numbers, hi and lo, that sit in columns of
-// their own; so the products are exact and accumulate in fp32.
+// their own; so the products are exact, and they add up in fp32.  q is K-major in
+// swizzled rows; p is N-major, so that a key's thread stores its heads as they lie
+// in registers, eight columns a 16-byte store.
 //
 // What bounds it: 9/16 byte per element from HBM (18 KB per tile for D = 128,
-// 0.41 us of an SM's share of the copy rate) against the widening, about one
-// issue slot for two elements.  The MMAs cost no issue slots here (mma.sync costs
-// as many as the widening: measured 8.4 slots for a 16x8x16 step), and with heads
-// on the N axis their time does not grow with the group.
+// 790 cycles of an SM's share of the copy rate) against instruction issue: a tile is
+// 1300 instructions of widening (one conversion and one product for two elements) and,
+// with all waits and the softmax, some 3200, which is 800 of a scheduler's slots.  The
+// MMAs cost hardly any (mma.sync costs as many as the widening: measured 8.4 slots for
+// a 16x8x16 step), and with heads on the N axis their time does not grow with the group.
+// Measured, D = 128: 524288 tokens of 8 KV heads 121 us with 4 heads a group (5.0 TB/s, 74 %
+// of a copy's rate; 1020 cycles a tile), 130 with 8, 231 with 16 (the softmax of 16 heads
+// takes a group of warps 4600 cycles, registers spill).  A CTA's start takes 7000 cycles (lengths,
+// prefix sums, its place in the plan, q) and its end 4000 to 10000 (join), so that 131072
+// tokens take 40.5 us (3.7 TB/s), 16 ragged sequences of 1024 to 16384 tokens 32.
 //
 // Twenty-eight warps:
 //   0      walks the plan, announces pieces, copies tiles (one bulk copy for a
-//          contiguous run, one per block when paged) into a ring of stages;
-//   1, 2   one thread of each issues MMAs: S, and O (each MMA takes some 30
+//          contiguous run, one per run of blocks when paged) into a ring of stages;
+//   1, 2   one thread of each issues MMAs: S, and O (each MMA takes 18
 //          cycles to issue, and a tile needs eight of each kind);
 //   3      q of the next piece: scaled to the fp16 range by a power of two per
-//          head, split hi / lo, written in the B layout;
+//          head, split hi / lo, written in the B layout; it also counts the pieces
+//          that the CTA goes on after;
 //   4-11   K, two groups of four warps: lane = key;
 //   12-19  V, two groups: lane = channel;
 //   20-27  softmax, two groups: lane = key; at the end of a piece lane = channel.
 // Group 0 of each role takes the even tiles and group 1 the odd ones, so that
 // a tile's latency (shared memory, conversions, tensor-memory stores, barriers)
 // may be two tiles long.  The softmax groups share nothing within a piece:
-// each has its reference, its sums and its O in tensor memory, and the two
-// states are joined at the piece's end.
+// each has its reference, its sums and its O, and the two states are joined at the
+// piece's end.  More groups (64 registers a thread) were slower, and so was a
+// split of the registers between roles (setmaxnreg does not compile for them).
 // Every mbarrier wait is bounded; a wait that runs out raises the error word and
 // the CTA still counts its pieces, so that the workspace stays valid.
 #include <cuda_fp16.h>
@@ -120,7 +130,7 @@ struct K4 {
   static constexpr int kN = G <= 8 ? 16 : 2 * G;  // columns: hi of the G heads, then lo; the rest is not used
   // Buffers: K and V in tensor memory (64 columns each for D = 128), S there and p
   // in shared memory.  With two of each, a group's next tile waited for the
-  // whole chain of its last one (S, softmax, O): 1125 cycles a tile, 128k tokens 43 us.
+  // whole chain of its last one (S, softmax, O): 128k tokens 43 us, 41 so.
   static constexpr int kSGroups = 2, kSThreads = 128 * kSGroups, kThreads = 32 * kSoftmax0 + kSThreads;
   static constexpr uint32_t kKBufs = 3, kVBufs = G <= 8 ? 3 : 2, kSBufs = 4;
   static constexpr uint32_t kColK = 0, kColV = kColK + kKBufs * (D / 2), kColS = kColV + kVBufs * (kTile / 2),
