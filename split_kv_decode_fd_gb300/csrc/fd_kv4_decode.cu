@@ -24,9 +24,9 @@
 // with all waits and the softmax, some 3200, which is 800 of a scheduler's slots.  The
 // MMAs cost hardly any (mma.sync costs as many as the widening: measured 8.4 slots for
 // a 16x8x16 step), and with heads on the N axis their time does not grow with the group.
-// Measured, D = 128: 524288 tokens of 8 KV heads 121 us with 4 heads a group (5.0 TB/s, 74 %
-// of a copy's rate; 1020 cycles a tile), 130 with 8, 231 with 16 (the softmax of 16 heads
-// takes a group of warps 4600 cycles, registers spill).  A CTA's start takes 7000 cycles (lengths,
+// Measured, D = 128: 524288 tokens of 8 KV heads 124 us with 4 heads a group (4.9 TB/s, 72 %
+// of a copy's rate; 1050 cycles a tile), 135 with 8, 211 with 16 (the softmax of half the
+// heads takes a group of warps 1800 cycles).  A CTA's start takes 7000 cycles (lengths,
 // prefix sums, its place in the plan, q) and its end 4000 to 10000 (join), so that 131072
 // tokens take 40.5 us (3.7 TB/s), 16 ragged sequences of 1024 to 16384 tokens 32.
 //
@@ -40,9 +40,9 @@
 //          that the CTA goes on after;
 //   4-11   K, two groups of four warps: lane = key;
 //   12-19  V, two groups: lane = channel;
-//   20-27  softmax, two groups: lane = key; at the end of a piece lane = channel.
-// Group 0 of each role takes the even tiles and group 1 the odd ones, so that
-// a tile's latency (shared memory, conversions, tensor-memory stores, barriers)
+//   20-27  softmax, two groups: lane = key; lane = channel where O is taken.
+// Group 0 of each role takes the even tiles and group 1 the odd ones (with 16 heads the
+// softmax groups take half of the heads each), so that a tile's latency (shared memory, conversions, tensor-memory stores, barriers)
 // may be two tiles long.  The softmax groups share nothing within a piece:
 // each has its reference, its sums and its O, and the two states are joined at the
 // piece's end.  More groups (64 registers a thread) were slower, and so was a
@@ -74,7 +74,7 @@ constexpr float kRefDown = 9.f, kTau = 6.f;
 // Tiles of a group whose O products add up in tensor memory before their sum moves to
 // fp32 adds in shared memory.  An MMA's add drops bits instead of rounding, some 2^-25.6
 // of the sum each and all one way: with 27 tiles in a row the outputs of 128k tokens were
-// 4.2e-6 off (2-norm), with four 8.1e-7.  It costs 0.5 us of 40, with 16 heads a group 5 of 57.
+// 4.2e-6 off (2-norm), with four 8.1e-7.  It costs 0.5 us of 40.
 constexpr uint32_t kFlush = 4;
 constexpr float kNoRef = -3.402823466e38f;  // of a head that has seen no key: no score lies below it
 
@@ -104,17 +104,16 @@ struct KvPiece {
 };
 
 // Lengths and tile counts as in CtaTiles, with this kernel's charge for a piece:
-// its end and the next one's start take a CTA about as long as four tiles, with 16
-// heads as long as seven of its longer tiles (16 ragged sequences 35.9 us with the bf16
-// kernel's charge of 1.25 tiles, 31.7 so; 64 paged sequences of 8 heads a group 111 us,
-// with a charge of six 114; 8 windows of 4 rows 34.4, with a charge of four 36.1).
-template <int Units>
+// its end and the next one's start take a CTA about as long as four tiles (16 ragged
+// sequences 35.9 us with the bf16 kernel's charge of 1.25 tiles, 32.2 so, 33.3 with
+// three; 64 paged sequences of 8 heads a group 113 us, with a charge of six 116).
+constexpr int kKv4PieceUnits = 4 * kTileUnits;
 struct Kv4Tiles {
   const int32_t* pre;
   const int32_t* ln;
   int32_t ut, ul;
   int uniform;
-  FD_HD int32_t piece() const { return uniform ? 0 : Units; }
+  FD_HD int32_t piece() const { return uniform ? 0 : kKv4PieceUnits; }
   FD_HD int64_t prefix(int32_t b) const { return uniform ? (int64_t)b * pair_units(ut, 0) : pre[b]; }
   FD_HD int32_t tiles(int32_t b) const { return uniform ? ut : ceil_div(ln[b], kPlanTile); }
   FD_HD int32_t len(int32_t b) const { return uniform ? ul : ln[b]; }
@@ -131,12 +130,18 @@ struct K4 {
   // Buffers: K and V in tensor memory (64 columns each for D = 128), S there and p
   // in shared memory.  With two of each, a group's next tile waited for the
   // whole chain of its last one (S, softmax, O): 128k tokens 43 us, 41 so.
+  // The softmax groups take alternate tiles, or, with 16 heads, whose scores, references
+  // and sums do not fit in a thread's 72 registers, half of the heads of each tile
+  // (131072 tokens of 4 KV heads 57.6 us by tiles, 48.6 by heads; 8 windows of 4 rows 37
+  // and 30.5).
+  static constexpr bool kByHead = G == 16;
+  static constexpr uint32_t kStep = kByHead ? 1 : 2;  // from one tile of a group to its next
+  static constexpr int kHeads = kByHead ? G / 2 : G;  // heads of a group
   static constexpr int kSGroups = 2, kSThreads = 128 * kSGroups, kThreads = 32 * kSoftmax0 + kSThreads;
   static constexpr uint32_t kKBufs = 3, kVBufs = G <= 8 ? 3 : 2, kSBufs = 4;
   static constexpr uint32_t kColK = 0, kColV = kColK + kKBufs * (D / 2), kColS = kColV + kVBufs * (kTile / 2),
-                            kColO = kColS + kSBufs * kN;  // O: one per softmax group
+                            kColO = kColS + kSBufs * kN;  // O: one per softmax group, or one of both
   static_assert(kColO + kSGroups * kN <= 512, "tensor memory");
-  static constexpr int kPieceUnits = (G == 16 ? 7 : 4) * kTileUnits;
   static constexpr int kStageBytes = kTileBlocks * kv4_block_bytes(D);
   static constexpr int kStages = D == 128 ? 8 : 16;  // a power of two
   static constexpr int kVWarps = D / 32;
@@ -360,7 +365,7 @@ template <int D, int G>
 __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __grid_constant__ Kv4Params pp) {
   using C = K4<D, G>;
   constexpr int N = C::kN;
-  constexpr uint32_t kSG = C::kSGroups;
+  constexpr uint32_t kSG = C::kSGroups, kStep = C::kStep;
   const SplitParams& p = pp.p;
   const Kv4View& kv = pp.kv;
   extern __shared__ uint8_t smem_raw[];
@@ -400,7 +405,7 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
       if (at >= desc_empty && at < k_ready) n = 2 + 1 + 8 + 2 * kV + 4 * C::kSGroups;
       if (at >= k_ready && at < k_free) n = 4;
       if (at >= v_ready && at < v_free) n = kV;
-      if (at >= p_ready && at < p_free) n = 4;
+      if (at >= p_ready && at < p_free) n = C::kByHead ? 8 : 4;
       if (at >= q_free && at < drain) n = 1 + 4 * C::kSGroups;
       if (at == drain) n = 2;
       if (at == part_done) n = 4 * C::kSGroups;
@@ -412,7 +417,7 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
   if (warp == 1) tmem_alloc_all(smem_addr(tmem_slot));
   pdl_launch_dependents();
   if (p.seq_lens != nullptr) pdl_wait();
-  Kv4Tiles<C::kPieceUnits> tl;
+  Kv4Tiles tl;
   tl.pre = pre;
   tl.ln = lens;
   tl.ul = p.max_len;
@@ -427,7 +432,7 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
       const int lo = lane * per;
       const int hi = lo + per < p.B ? lo + per : p.B;
       int sum = 0;
-      for (int b = lo; b < hi; ++b) sum += (int)pair_units(ceil_div(lens[b], kPlanTile), C::kPieceUnits);
+      for (int b = lo; b < hi; ++b) sum += (int)pair_units(ceil_div(lens[b], kPlanTile), kKv4PieceUnits);
       int incl = sum;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -437,7 +442,7 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
       int run = incl - sum;
       for (int b = lo; b < hi; ++b) {
         pre[b] = run;
-        run += (int)pair_units(ceil_div(lens[b], kPlanTile), C::kPieceUnits);
+        run += (int)pair_units(ceil_div(lens[b], kPlanTile), kKv4PieceUnits);
       }
       if (lane == 31) pre[p.B] = incl;
     }
@@ -513,7 +518,7 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
     const bool balanced = p.n_splits == 0;
     const int32_t used = balanced ? balanced_ctas(total, (int32_t)gridDim.x) : 0;
     const bool part = balanced && (int32_t)blockIdx.x < used;  // this CTA has a share of the plan
-    BalancedWalk<Kv4Tiles<C::kPieceUnits>> walk(tl, p.B, p.hv, part ? total : 0, part ? used : 1, part ? (int32_t)blockIdx.x : 0);
+    BalancedWalk<Kv4Tiles> walk(tl, p.B, p.hv, part ? total : 0, part ? used : 1, part ? (int32_t)blockIdx.x : 0);
     Piece pc;
     bool have;
     if (balanced) {
@@ -716,7 +721,7 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
           }
           tmem_fence_after();
           if (elect_one()) {
-            const bool fresh = j / (int32_t)kSG % (int32_t)kFlush == 0;  // a new sum
+            const bool fresh = j / (int32_t)kStep % (int32_t)kFlush == 0;  // a new sum
             const uint32_t d = base + C::kColO + sg * N, a = base + C::kColV + vr.i * (kTile / 2),
                            b = sb + C::kPOff + sr.i * C::kPBytes;
 #pragma unroll
@@ -730,7 +735,7 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
         kr.next();
         vr.next();
         sr.next();
-        if (++sg == kSG) sg = 0;
+        if (++sg == kStep) sg = 0;
       }
       ++f;
     }
@@ -994,15 +999,19 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
     const uint32_t bar = 2 + group;  // this group's barrier
     const int key = quad * 32 + lane;  // of the tile; the channel at the end of a piece
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+    constexpr int H = C::kHeads;
+    const int hb = C::kByHead ? (int)group * H : 0;  // this group's first head
+    const uint32_t o_col = C::kColO + (C::kByHead ? 0 : group * N) + hb;
     float* red = reinterpret_cast<float*>(smem + C::kRedOff) + group * 80;
     float* fac = reinterpret_cast<float*>(smem + C::kFacOff) + group * 32;
-    const int32_t* lims = reinterpret_cast<const int32_t*>(fac + 16);
+    const float* fac_h = fac + hb;
+    const int32_t* lims = reinterpret_cast<const int32_t*>(fac + 16) + hb;
     // A piece's end.  Per head, the sums [groups][4 warps], then [16][groups]
     // references; and the groups' O.
     float* ends = reinterpret_cast<float*>(smem + C::kEndOff);
     float* join = reinterpret_cast<float*>(smem + C::kJoinOff);
     // This thread's key in a p buffer: eight columns, the next eight 16 * kTile bytes on.
-    const uint32_t p_at = sbase + C::kPOff + key * 16;
+    const uint32_t p_at = sbase + C::kPOff + key * 16 + (C::kByHead ? group * (16 * kTile) : 0);
     Groups gr;
     gr.g = p.g;
     gr.gpad = p.gpad;
@@ -1019,7 +1028,7 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
           for (int i = st; i < p.Hq; i += C::kSThreads) p.lse[(size_t)b * p.Hq + i] = -INFINITY;
       }
     }
-    uint32_t g = group, e = 0, f = 0, g1 = 0;  // this group's next tile, the end of the piece
+    uint32_t g = C::kByHead ? 0 : group, e = 0, f = 0, g1 = 0;  // this group's next tile, the end of the piece
     bool owed = false;                         // the q warp counts the last piece
     uint32_t joins = 0;
     const auto join_owed = [&] {
@@ -1038,11 +1047,11 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
       int32_t head0, nh;
       vkv_heads(gr, pc.vkv, &head0, &nh);
       const int32_t n = tiles_of(pc);
-      float mr[G], l[G];
+      float mr[H], l[H];
 #pragma unroll
-      for (int h = 0; h < G; ++h) {
+      for (int h = 0; h < H; ++h) {
         // idle columns have S = 0 and never move their reference
-        mr[h] = h < nh ? kNoRef : 0.f;
+        mr[h] = hb + h < nh ? kNoRef : 0.f;
         l[h] = 0.f;
       }
       int32_t npieces = 0, first = 0;
@@ -1066,26 +1075,23 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
       const uint32_t g0 = g1;
       if (run) g1 += n;
       const uint32_t g_first = g;
-      for (; run; g += kSG) {
-        const uint32_t jj = (g - g_first) / kSG;  // the group's tile
+      float* sums = join + (C::kByHead ? hb : (int)group * G) * D + key;  // this thread's channel of O
+      for (; run; g += kStep) {
+        const uint32_t jj = (g - g_first) / kStep;  // the group's tile
         if (jj > 0 && (g >= g1 || jj % kFlush == 0)) {  // O of the last tiles joins the sums in shared memory
-          const bool got = wait.warp(p_free + (g - kSG) % C::kSBufs, (g - kSG) / C::kSBufs & 1);
+          const bool got = wait.warp(p_free + (g - kStep) % C::kSBufs, (g - kStep) / C::kSBufs & 1);
           if (vote(bar, 128, !got) != 0) {
             ok = run = false;
             break;
           }
           tmem_fence_after();
-          constexpr int W = G < 2 ? 2 : (G < 8 ? G : 8);
-#pragma unroll 1
-          for (int h0 = 0; h0 < G; h0 += W) {
-            float hi[W], lo[W];
-            tmem_load<W>(tmem + lanes + C::kColO + group * N + h0, hi);
-            tmem_load<W>(tmem + lanes + C::kColO + group * N + G + h0, lo);
-            if (key < D) {
-              float* sum = join + (group * G + h0) * D + key;
+          constexpr int W = H < 2 ? 2 : H;
+          float hi[W], lo[W];
+          tmem_load<W>(tmem + lanes + o_col, hi);
+          tmem_load<W>(tmem + lanes + o_col + G, lo);
+          if (key < D) {
 #pragma unroll
-              for (int h = 0; h < W && h0 + h < G; ++h) sum[h * D] = (jj > kFlush ? sum[h * D] : 0.f) + (hi[h] + lo[h]);
-            }
+            for (int h = 0; h < H; ++h) sums[h * D] = (jj > kFlush ? sums[h * D] : 0.f) + (hi[h] + lo[h]);
           }
           tmem_fence_before();
         }
@@ -1095,19 +1101,19 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
         const bool whole = t0 + kTile <= whole_end;
         const bool got = wait.warp(s_full + i, ph);
         tmem_fence_after();
-        float x[G < 2 ? 2 : G];
+        float x[H < 2 ? 2 : H];
         const auto load_scores = [&] {  // hi + lo, not yet times their factors
           if constexpr (G < 16) {
             float s[2 * G];
             tmem_load<2 * G>(tmem + lanes + C::kColS + i * N, s);
 #pragma unroll
-            for (int h = 0; h < G; ++h) x[h] = s[h] + s[G + h];
+            for (int h = 0; h < H; ++h) x[h] = s[h] + s[G + h];
           } else {
-            float lo[G];
-            tmem_load<G>(tmem + lanes + C::kColS + i * N, x);
-            tmem_load<G>(tmem + lanes + C::kColS + i * N + G, lo);
+            float lo[H];
+            tmem_load<H>(tmem + lanes + C::kColS + i * N + hb, x);
+            tmem_load<H>(tmem + lanes + C::kColS + i * N + G + hb, lo);
 #pragma unroll
-            for (int h = 0; h < G; ++h) x[h] += lo[h];
+            for (int h = 0; h < H; ++h) x[h] += lo[h];
           }
         };
         for (bool again = false;; again = true) {
@@ -1115,22 +1121,22 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
           bool up = false;
           load_scores();
 #pragma unroll
-          for (int h = 0; h < G; ++h) x[h] = fmaf(x[h], fac[h], -mr[h]);
+          for (int h = 0; h < H; ++h) x[h] = fmaf(x[h], fac_h[h], -mr[h]);
           if (__builtin_expect(!whole, 0)) {
             const int32_t t = t0 + key < pc.tok_end ? t0 + key : 0x7fffffff;
 #pragma unroll
-            for (int h = 0; h < G; ++h)
+            for (int h = 0; h < H; ++h)
               if (t >= lims[h]) x[h] = -INFINITY;
           }
           if (__builtin_expect(again, 0)) {
             // Once is enough.  Scores of 2^27 and more are further apart than kTau: a reference
             // that was rounded down by more than that stays, and the exponent is cut.
 #pragma unroll
-            for (int h = 0; h < G; ++h) x[h] = x[h] > kRefDown + kTau ? kRefDown + kTau : x[h];
+            for (int h = 0; h < H; ++h) x[h] = x[h] > kRefDown + kTau ? kRefDown + kTau : x[h];
             break;
           }
 #pragma unroll
-          for (int h = 0; h < G; ++h) up |= x[h] > kRefDown + kTau;
+          for (int h = 0; h < H; ++h) up |= x[h] > kRefDown + kTau;
           // one vote a warp for such a score, 24 for a wait that ran out
           const bool any_up = __any_sync(0xffffffffu, up);
           const uint32_t votes = vote(bar, 128, got ? any_up && lane == 0 : lane >= 8);
@@ -1140,22 +1146,22 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
             // the reference moves: maxima of the tile, then l and O on the new one
             uint32_t seen = 0;
 #pragma unroll
-            for (int h = 0; h < G; ++h) seen |= (x[h] == -INFINITY ? 0u : 1u) << h;
+            for (int h = 0; h < H; ++h) seen |= (x[h] == -INFINITY ? 0u : 1u) << h;
             load_scores();
 #pragma unroll
-            for (int h = 0; h < G; ++h) x[h] = seen >> h & 1 ? x[h] * fac[h] : -INFINITY;
-            warp_reduce<G>(x, lane, [](float a, float b) { return fmaxf(a, b); });
-            if (lane % (32 / G) == 0) red[lane / (32 / G) * 4 + quad] = x[0];
+            for (int h = 0; h < H; ++h) x[h] = seen >> h & 1 ? x[h] * fac_h[h] : -INFINITY;
+            warp_reduce<H>(x, lane, [](float a, float b) { return fmaxf(a, b); });
+            if (lane % (32 / H) == 0) red[lane / (32 / H) * 4 + quad] = x[0];
             named_barrier(bar, 128);
-            if (key < G) {
+            if (key < H) {
               const float4 m = reinterpret_cast<const float4*>(red)[key];
               const float top = fmaxf(fmaxf(m.x, m.y), fmaxf(m.z, m.w)) - kRefDown;
               red[64 + key] = top == INFINITY ? NAN : top;  // a score past the range of floats shows as NaN
             }
             named_barrier(bar, 128);
-            float (&alpha)[G < 2 ? 2 : G] = x;
+            float (&alpha)[H < 2 ? 2 : H] = x;
 #pragma unroll
-            for (int h = 0; h < G; ++h) {
+            for (int h = 0; h < H; ++h) {
               const float mn = red[64 + h] <= mr[h] ? mr[h] : red[64 + h];
               alpha[h] = ex2(mr[h] - mn);
               mr[h] = mn;
@@ -1163,21 +1169,21 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
             }
             if (jj >= kFlush && key < D) {
 #pragma unroll
-              for (int h = 0; h < G; ++h) join[(group * G + h) * D + key] *= alpha[h];
+              for (int h = 0; h < H; ++h) sums[h * D] *= alpha[h];
             }
             if (g != g_first) {
-              moved = wait.warp(p_free + (g - kSG) % C::kSBufs, (g - kSG) / C::kSBufs & 1);  // O of this group's last tile
+              moved = wait.warp(p_free + (g - kStep) % C::kSBufs, (g - kStep) / C::kSBufs & 1);  // O of this group's last tile
               if (moved) {
                 tmem_fence_after();
 #pragma unroll
                 for (int part = 0; part < 2; ++part) {  // hi, lo
-                  constexpr int W = G < 2 ? 2 : G;
+                  constexpr int W = H < 2 ? 2 : H;
                   if (G == 1 && part == 1) break;
                   float o[W];
-                  tmem_load<W>(tmem + lanes + C::kColO + group * N + part * G, o);
+                  tmem_load<W>(tmem + lanes + o_col + part * G, o);
 #pragma unroll
-                  for (int h = 0; h < W; ++h) o[h] *= alpha[h % G];
-                  tmem_store<W>(tmem + lanes + C::kColO + group * N + part * G, o);
+                  for (int h = 0; h < W; ++h) o[h] *= alpha[h % H];
+                  tmem_store<W>(tmem + lanes + o_col + part * G, o);
                 }
                 tmem_wait_stores();
               }
@@ -1193,18 +1199,18 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
         if (g < C::kSBufs || wait.warp(p_free + i, ph ^ 1)) {
           const uint32_t ps = p_at + i * C::kPBytes;
 #pragma unroll
-          for (int h = 0; h < G; ++h) {
+          for (int h = 0; h < H; ++h) {
             x[h] = ex2(x[h]);
             l[h] += x[h];
           }
-          uint32_t w[G < 2 ? 1 : G];  // columns of hi, then of lo, in pairs
+          uint32_t w[H < 2 ? 1 : H];  // columns of hi, then of lo, in pairs
           if constexpr (G == 1) {
             uint32_t hi, lo;
             split_f16x2(x[0], 0.f, hi, lo);
             w[0] = hi | lo << 16;
           } else {
 #pragma unroll
-            for (int h = 0; h < G; h += 2) split_f16x2(x[h], x[h + 1], w[h / 2], w[(G + h) / 2]);
+            for (int h = 0; h < H; h += 2) split_f16x2(x[h], x[h + 1], w[h / 2], w[(H + h) / 2]);
           }
           if constexpr (G == 1) {
             asm volatile("st.shared.u32 [%0], %1;" ::"r"(ps), "r"(w[0]) : "memory");
@@ -1212,8 +1218,8 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
             asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(ps), "r"(w[0]), "r"(w[1]) : "memory");
           } else {
 #pragma unroll
-            for (int c = 0; c < G; c += 4)
-              sts128u(ps + c / 4 * (16 * kTile), make_uint4(w[c], w[c + 1], w[c + 2], w[c + 3]));
+            for (int c = 0; c < H; c += 4)  // hi, lo: G / 8 places on with 8 heads and more
+              sts128u(ps + c / 4 * (G / 8) * (16 * kTile), make_uint4(w[c], w[c + 1], w[c + 2], w[c + 3]));
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         } else {
@@ -1228,13 +1234,20 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
       // instruction cache, and its length was what a piece's end took.)
       if ((!run || g == g_first) && key < D) {
 #pragma unroll
-        for (int h = 0; h < G; ++h) join[(group * G + h) * D + key] = 0.f;
+        for (int h = 0; h < H; ++h) sums[h * D] = 0.f;
       }
-      warp_reduce<G>(l, lane, [](float a, float b) { return a + b; });
-      if (lane % (32 / G) == 0) ends[lane / (32 / G) * 8 + group * 4 + quad] = l[0];
+      warp_reduce<H>(l, lane, [](float a, float b) { return a + b; });
+      if (lane % (32 / H) == 0) {
+        float* to = ends + (hb + lane / (32 / H)) * 8 + quad;
+        to[C::kByHead ? 0 : group * 4] = l[0];
+        if (C::kByHead) to[4] = 0.f;
+      }
       if (key == 0) {
 #pragma unroll
-        for (int h = 0; h < G; ++h) ends[128 + h * 2 + group] = mr[h];
+        for (int h = 0; h < H; ++h) {
+          ends[128 + (hb + h) * 2 + (C::kByHead ? 0 : group)] = mr[h];
+          if (C::kByHead) ends[128 + (hb + h) * 2 + 1] = mr[h];
+        }
       }
       named_barrier(1, C::kSThreads);
       const bool final_here = fused && npieces == 1;
@@ -1245,7 +1258,7 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
         const float4 la = reinterpret_cast<const float4*>(ends)[2 * h], lb = reinterpret_cast<const float4*>(ends)[2 * h + 1];
         const float2 ms = reinterpret_cast<const float2*>(ends + 128)[h];
         const float4 oa = *reinterpret_cast<const float4*>(join + h * D + d);
-        const float4 ob = *reinterpret_cast<const float4*>(join + (G + h) * D + d);
+        const float4 ob = C::kByHead ? make_float4(0.f, 0.f, 0.f, 0.f) : *reinterpret_cast<const float4*>(join + (G + h) * D + d);
         const float l0 = (la.x + la.y) + (la.z + la.w), l1 = (lb.x + lb.y) + (lb.z + lb.w), mm = fmaxf(ms.x, ms.y);
         const float w0 = l0 == 0.f ? 0.f : ex2(ms.x - mm), w1 = l1 == 0.f ? 0.f : ex2(ms.y - mm);
         const float L = fmaf(w0, l0, w1 * l1), up = pow2i(kv.v_exp);
