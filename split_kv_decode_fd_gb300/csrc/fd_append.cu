@@ -194,7 +194,7 @@ __device__ __forceinline__ void query_row(const NewRows& r, int32_t b, int32_t i
 template <int D, class T, class C>
 __global__ void __launch_bounds__(256) fd_append_kernel(const NewRows r, const KvView kv, int32_t items) {
   constexpr int TPR = D / 16;
-  const int32_t item = (int32_t)((blockIdx.x * 256u + threadIdx.x) / TPR);
+  const int32_t item = (int32_t)(((int64_t)blockIdx.x * 256 + threadIdx.x) / TPR);
   const int s = threadIdx.x % TPR;
   if (item >= items) return;
   const int32_t heads = r.Hq + 2 * kv.Hkv;

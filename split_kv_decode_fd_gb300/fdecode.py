@@ -656,15 +656,26 @@ def _index_of(t, name):
     return t.get_device()
 
 
-def _scratch(workspace, index, nbytes):
-    """The workspace's buffer.  It is not made during a stream capture: its first
-    zero-fill would then run only with the graph."""
+def _made(make, shape, dtype, device, stream):
+    """A tensor for a call on ``stream``, filled there: a fill on the current stream could come after the call."""
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    with _torch().cuda.stream(stream):
+        return make(shape, dtype=dtype, device=device)
+
+
+def _scratch(workspace, index, nbytes, stream=None):
+    """The workspace's buffer, zero-filled on the call's stream.  It is not made during a
+    stream capture: its first zero-fill would then run only with the graph."""
     torch = _torch()
     ws = workspace
     if ws is None:
         ws = _DEFAULT_WS.get(("cuda", index)) or _default_workspace(torch.device("cuda", index))
     buf = ws.buf
     if buf is None or buf.numel() < nbytes or buf.get_device() != index:
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return _scratch(ws, index, nbytes)
         if torch.cuda.is_current_stream_capturing():
             raise RuntimeError("the workspace is too small and cannot grow during a stream capture: run the call once "
                                "before the capture, or pass a Workspace that has been used at this size")
@@ -771,7 +782,7 @@ def _append(fn, where, desc, k_new, v_new, Hkv, D, tokens, index, cos, sin, q, q
         if q_out is None:
             # rows that new_lens or a bad position leaves out are not written: they start as zeros
             make = torch.empty if new_lens is None and positions is None else torch.zeros
-            q_out = make((B, Hq, n, D), dtype=torch.float32, device=q.device)
+            q_out = _made(make, (B, Hq, n, D), torch.float32, q.device, stream)
             qo = q_out.data_ptr()
         else:
             qo = _flat(q_out, "q_out", torch.float32, index, (B, Hq, n, D))
@@ -791,7 +802,7 @@ def _append(fn, where, desc, k_new, v_new, Hkv, D, tokens, index, cos, sin, q, q
         dt, qp, k_new.data_ptr(), v_new.data_ptr(), qs[0], qs[1], qs[2], ks[0], ks[1], ks[2], vs[0], vs[1], vs[2],
         _opt(new_lens, "new_lens", torch.int32, index, (B,)), _opt(positions, "positions", torch.int32, index, (B, n)),
         cp, sp, max_pos, rot, 1 if interleaved else 0))
-    buf = _scratch(workspace, index, 256)
+    buf = _scratch(workspace, index, 256, stream)
     _launch(index, stream, fn, where, rows, desc, qo, B, n, Hq, Hkv, _opt(seq_lens, "seq_lens", torch.int32, index, (B,)),
             tokens - n if max_seq_len is None else int(max_seq_len), D, buf.data_ptr(), buf.numel())
     return q_out
@@ -865,10 +876,10 @@ def kv4_read(kv4, n, *, starts=None, seq_lens=None, max_seq_len=None, block_tabl
     n = int(n)
     shape = (B, Hkv, n, D)
     if k_out is None:
-        k_out = torch.zeros(shape, dtype=dtype, device=kv4.device)
+        k_out = _made(torch.zeros, shape, dtype, kv4.device, stream)
     if v_out is None:
-        v_out = torch.zeros(shape, dtype=dtype, device=kv4.device)
-    buf = _scratch(workspace, index, 256)
+        v_out = _made(torch.zeros, shape, dtype, kv4.device, stream)
+    buf = _scratch(workspace, index, 256, stream)
     _launch(index, stream, _lib().fd_kv4_read, "fd_kv4_read", desc, _flat(k_out, "k_out", dtype, index, shape),
             _flat(v_out, "v_out", dtype, index, shape), dt, B, n, Hkv, _opt(starts, "starts", torch.int32, index, (B,)),
             _opt(seq_lens, "seq_lens", torch.int32, index, (B,)), tokens if max_seq_len is None else int(max_seq_len), D,
@@ -899,7 +910,7 @@ def decode_kv4(q, kv4, *, k_exp=0, v_exp=0, causal=True, seq_lens=None, max_seq_
     if on != index:
         raise ValueError("q and kv4 must be on one device")
     if out is None:
-        out = torch.empty_like(q)
+        out = _made(torch.empty, shape, torch.float32, q.device, stream)
         op = out.data_ptr()
     else:
         op = _flat(out, "out", torch.float32, index, shape)
@@ -907,10 +918,10 @@ def decode_kv4(q, kv4, *, k_exp=0, v_exp=0, causal=True, seq_lens=None, max_seq_
     if lse is not None:
         lp = _flat(lse, "lse", torch.float32, index, shape[:-1])
     elif return_lse:
-        lse = torch.empty(shape[:-1], dtype=torch.float32, device=q.device)
+        lse = _made(torch.empty, shape[:-1], torch.float32, q.device, stream)
         lp = lse.data_ptr()
     n_splits = int(n_splits)
-    buf = _scratch(workspace, index, _decode_bytes(B, Hq * n_q, Hkv, D, n_splits, index))
+    buf = _scratch(workspace, index, _decode_bytes(B, Hq * n_q, Hkv, D, n_splits, index), stream)
     _launch(index, stream, _lib().fd_decode_kv4, "fd_decode_kv4", at, n_q, 1 if causal else 0, desc, op, lp, B, Hq, Hkv,
             _opt(seq_lens, "seq_lens", torch.int32, index, (B,)), tokens if max_seq_len is None else int(max_seq_len), D,
             1.0 / math.sqrt(D) if scale is None else float(scale), n_splits, buf.data_ptr(), buf.numel())

@@ -177,6 +177,40 @@ def test_steps_replayed_on_another_stream(page):
     assert fd.workspace_status(one["ws"]) == 0 and fd.workspace_status(two["ws"]) == 0
 
 
+def test_outputs_and_workspaces_are_made_on_the_streams_of_the_calls():
+    """Calls on a stream of their own while the current one is busy: nothing that they make waits for it."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    B, n, Hq, Hkv, D, cap = 2, 5, 4, 2, 64, 64
+    x = torch.randn((B, n, Hq + 2 * Hkv, D), generator=g, device="cuda")
+    new = torch.tensor([5, 2], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([10, 20], dtype=torch.int32, device="cuda")
+    ends = lens + new
+    kv = fd.kv4_cache(B, Hkv, cap, D)
+    k, v = (torch.zeros((B, Hkv, cap, D), device="cuda") for _ in range(2))
+
+    def calls(stream):
+        ws = [fd.Workspace() for _ in range(4)] if stream is not None else [None] * 4
+        how = dict(q=x[:, :, :Hq], new_lens=new, seq_lens=lens, max_seq_len=cap - n, stream=stream)
+        rows = x[:, :, Hq:Hq + Hkv], x[:, :, Hq + Hkv:]
+        q = fd.append_rope_kv4(*rows, kv, workspace=ws[0], **how)
+        q2 = fd.append_rope(*rows, k, v, workspace=ws[1], **how)
+        ko, vo = fd.kv4_read(kv, cap, seq_lens=ends, workspace=ws[2], stream=stream)
+        out, lse = fd.decode_kv4(q, kv, seq_lens=ends, max_seq_len=cap, workspace=ws[3], stream=stream)
+        return (q, q2, ko, vo, out, lse), ws
+
+    want, _ = calls(None)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)
+    got, ws = calls(s)
+    s.synchronize()
+    early = [t.cpu() for t in want]  # waits for the current stream
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b.cpu()) for a, b in zip(early, got))
+    assert all(fd.workspace_status(w) == 0 for w in ws)
+    assert got[0][1, :, :3].abs().max() == 0 and got[0][1, :, 3:].abs().min() > 0
+
+
 def test_decode_of_pages_past_32_bits():
     c = Case(2, 8, 2, 128, [500, 70], page=16, seed=14)
     want = [t.clone() for t in c.run()]
