@@ -119,7 +119,8 @@ struct Kv4Tiles {
   FD_HD int32_t len(int32_t b) const { return uniform ? ul : ln[b]; }
 };
 
-// A counted piece, from the q warp to the softmax warps.
+// A piece to count, from the softmax warps to the O warp; whether it was its sequence's
+// last, from the O warp back.
 struct JoinPiece {
   int32_t last, b, vkv, npieces, first;
 };
@@ -164,8 +165,8 @@ struct K4 {
   static constexpr int kBarOff = kPreOff + (kAutoMaxBatch + 4) * 4;
   static constexpr int kBars = 2 * kStages + 2 * kDescs + 2 * kKBufs + 2 * kVBufs + 3 * kSBufs + 4 + 3;
   static constexpr int kFlagOff = kBarOff + kBars * 8;
-  static constexpr int kLastOff = kFlagOff + 16;                      // the piece to join: see JoinPiece
-  static constexpr int kSmem = kLastOff + 32 + 1024;
+  static constexpr int kLastOff = kFlagOff + 16;                      // two JoinPieces in turn
+  static constexpr int kSmem = kLastOff + 48 + 1024;
   static_assert(kSmem <= 232448 && kSmem > 118784, "one CTA per SM: each takes all of tensor memory");
   static_assert(kStageOff % 128 == 0 && kQBytes % 1024 == 0 && kPBytes % 1024 == 0, "operand alignment");
   static_assert(kDescOff % 16 == 0 && kBarOff % 8 == 0, "alignment");
@@ -361,6 +362,105 @@ struct Waiter {
   }
 };
 
+// Copies of every second tile j, j + 2, ... of a paged piece, by one warp; tile j is the
+// CTA's tile g.  Returns how many it dealt with: a wait for a free stage may run out.
+// An SM's warp starts a bulk copy in some 90 cycles, and pages of sixteen tokens need eight
+// a tile, so two warps take turns (524288 tokens of 8 heads TIME_C; one warp's lanes with
+// 16-byte copies took 182).  Blocks of a tile that follow one another in the pool go in one.
+template <int D, int kStages>
+__device__ __noinline__ int32_t copy_paged(const Kv4View& kv, unsigned* err, uint8_t* stages, uint64_t* full, Waiter wait,
+                                           int32_t stall_it, int32_t b, int32_t kvh, int32_t tok_begin, int32_t tok_end,
+                                           uint32_t g, int32_t j) {
+  constexpr int kBytes = kv4_block_bytes(D);
+  const int lane = threadIdx.x & 31;
+  uint64_t* empty = full + kStages;
+  const uint8_t* pool = kv.kv;
+  const int32_t n = ceil_div(tok_end - tok_begin, kTile), num_pages = kv.num_pages, Hkv = kv.Hkv;
+  const int32_t blk0 = tok_begin / kKv4Tokens, blk1 = ceil_div(tok_end, kKv4Tokens);
+  // Lane k has block k of this warp's next four tiles at hand (its number in the pool, kNoBlock
+  // for a page outside it), and the table entry of its block of the four after is in flight.
+  constexpr uint32_t kNoBlock = 0xffffffffu;  // a pool has fewer: 2^32 blocks are 4.9 TB
+  uint32_t cur = 0, firsts = 0, bads = 0;     // of four tiles: blocks that start a copy, blocks outside the pool
+  const int32_t* trow = kv.block_table + (size_t)b * kv.max_pages;
+  int32_t blk = blk0 + (j + 2 * (lane / kTileBlocks)) * kTileBlocks + lane % kTileBlocks;
+  // the entry's place in the table, the block in the page; sixty-four blocks on
+  const int32_t ppb = kv.page_size / kKv4Tokens, step_q = 64 / ppb, step_r = 64 - step_q * ppb;
+  int32_t at = blk / ppb, rem = blk - at * ppb, page = 0;
+  const auto load_page = [&] { page = blk < blk1 ? __ldg(trow + at) : 0; };
+  const auto take_page = [&] {
+    cur = page >= 0 && page < num_pages ? ((uint32_t)page * (uint32_t)Hkv + kvh) * ppb + rem : kNoBlock;
+    const uint32_t before = __shfl_up_sync(0xffffffffu, cur, 1);
+    firsts = __ballot_sync(0xffffffffu, lane % kTileBlocks == 0 || cur != before + 1);
+    bads = __ballot_sync(0xffffffffu, cur == kNoBlock && blk < blk1);
+    blk += 64;
+    at += step_q;
+    rem += step_r;
+    if (rem >= ppb) {
+      rem -= ppb;
+      ++at;
+    }
+    load_page();
+  };
+  load_page();
+  take_page();
+  int32_t done = 0;
+  for (; j < n; j += 2, g += 2, ++done) {
+    const int32_t left = blk1 - (blk0 + j * kTileBlocks), nblk = left < kTileBlocks ? left : kTileBlocks;
+    const uint32_t st = g % kStages;
+    if (!wait.warp(empty + st, ((g / kStages) & 1) ^ 1)) break;
+    if (g != (uint32_t)stall_it) {
+      uint8_t* dst = stages + st * (kTileBlocks * kBytes);
+      const int k0 = (done & 3) * kTileBlocks;
+      const uint32_t valid = (1u << nblk) - 1, bad = bads >> k0 & valid;
+      const int k = lane - k0;  // this lane's block of the tile
+      uint32_t starts = firsts >> k0 & valid;
+      if (__builtin_expect(bad != 0, 0)) {
+        // keys of score 0 and value 0 in its place
+        if (k >= 0 && k < kTileBlocks && bad >> k & 1) {
+          raise_error(err, kErrBadIndex);
+          for (int i = 0; i < kBytes; i += 16) sts128u(smem_addr(dst) + k * kBytes + i, make_uint4(0, 0, 0, 0));
+          // before a later copy into this stage
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        starts = (starts | bad << 1) & valid & ~bad;  // a block after a bad one starts a copy
+        __syncwarp();
+      }
+      const uint8_t* from = pool + (uint64_t)cur * kBytes;
+      if (starts == valid) {  // one a block: a constant size is quicker to issue
+        if (k >= 0 && k < nblk) bulk_load(dst + k * kBytes, from, kBytes, full + st);
+      } else if (k >= 0 && k < kTileBlocks && starts >> k & 1) {
+        const uint32_t stops = starts | bad | ~valid;  // the next copy, a bad block, the tile's end
+        bulk_load(dst + k * kBytes, from, __ffs(stops >> (k + 1)) * kBytes, full + st);
+      }
+      if (lane == 0) mbar_arrive_expect_tx(full + st, __popc(valid & ~bad) * kBytes);
+      __syncwarp();
+    }
+    if ((done & 3) == 3) take_page();
+  }
+  return done;
+}
+
+// The tiles that a warp copied last: bit i of `mine` is tile last - i.
+struct Copied {
+  uint32_t last = 0, mine = 0;
+  // `count` tiles g, g + step, ...
+  __device__ __forceinline__ void add(uint32_t g, uint32_t step, int32_t count) {
+    if (count <= 0) return;
+    const uint32_t to = g + step * (uint32_t)(count - 1), by = to - last, span = to - g;
+    mine = (by < 32 ? mine << by : 0u) | ((step == 1 ? 0xffffffffu : 0x55555555u) & (span < 31 ? (2u << span) - 1 : 0xffffffffu));
+    last = to;
+  }
+  // Stay until those in flight have landed; `end` tiles were copied by all warps.
+  template <int kStages>
+  __device__ __forceinline__ void land(uint64_t* full, uint32_t end, int32_t stall_it, unsigned long long limit, unsigned* err) const {
+    for (uint32_t i = 0; i < (uint32_t)kStages && i <= last; ++i) {
+      const uint32_t g = last - i;
+      if (!(mine >> i & 1) || g + kStages < end || g == (uint32_t)stall_it) continue;
+      if (!mbar_wait_for(full + g % kStages, (g / kStages) & 1, limit)) raise_error(err, kErrTimeout);
+    }
+  }
+};
+
 template <int D, int G>
 __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __grid_constant__ Kv4Params pp) {
   using C = K4<D, G>;
@@ -534,8 +634,9 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
       pc.tok_end = (int32_t)(hi < pc.len ? hi : pc.len);
     }
     cta_sync();
-    uint32_t it = 0, e = 0, stalled = 0xffffffffu;
-    Ring<C::kStages> st;
+    uint32_t it = 0, e = 0;  // tiles, pieces
+    Ring<C::kStages> st;  // of a contiguous cache
+    Copied copied;
     bool live = true;  // the other roles still take pieces
     pdl_wait();
     const auto announce = [&](const KvPiece& d) {
@@ -563,100 +664,38 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
       live = announce(d);
       if (!live) break;
       if (!ok) continue;
-      const int32_t kvh = kv_head_of_vkv(gr, pc.vkv);
-      const uint8_t* base = kv.kv;
-      if (!kv.paged)
-        base += (((int64_t)pc.b * kv.Hkv + kvh) * kv.cap_blocks + pc.tok_begin / kKv4Tokens) * kv4_block_bytes(D);
-      // Paged: lane k has block k of four tiles at hand (its number in the pool, kNoBlock
-      // for a page outside it), and the table entry of its block of the next four
-      // is in flight.  Blocks of a tile that follow one another in the pool go in one
-      // copy: an SM starts one in some 90 cycles, whichever warp asks, so that pages of
-      // sixteen tokens are bound by it (524288 tokens of 8 heads 162 us, of a
-      // contiguous cache 121; sixteen-byte copies by a warp's lanes took 182).
-      const int32_t blk0 = pc.tok_begin / kKv4Tokens, blk1 = ceil_div(pc.tok_end, kKv4Tokens);
-      constexpr uint32_t kNoBlock = 0xffffffffu;  // a pool has fewer: 2^32 blocks are 4.9 TB
-      uint32_t cur = 0, firsts = 0, bads = 0;     // of four tiles: blocks that start a copy, blocks outside the pool
-      int32_t page = 0, rem = 0, at = 0;  // of the next four tiles: the page, the block in it, the table entry
-      int32_t ppb = 1, step_q = 0, step_r = 0;  // blocks of a page; thirty-two blocks on
-      const int32_t* trow = kv.block_table + (size_t)pc.b * kv.max_pages;
-      int32_t blk = blk0 + lane;
-      const auto load_page = [&] { page = blk < blk1 ? __ldg(trow + at) : 0; };
-      const auto take_page = [&] {
-        cur = page >= 0 && page < kv.num_pages ? ((uint32_t)page * (uint32_t)kv.Hkv + kvh) * ppb + rem : kNoBlock;
-        const uint32_t before = __shfl_up_sync(0xffffffffu, cur, 1);
-        firsts = __ballot_sync(0xffffffffu, lane % kTileBlocks == 0 || cur != before + 1);
-        bads = __ballot_sync(0xffffffffu, cur == kNoBlock && blk < blk1);
-        blk += 32;
-        at += step_q;
-        rem += step_r;
-        if (rem >= ppb) {
-          rem -= ppb;
-          ++at;
-        }
-        load_page();
-      };
-      if (kv.paged) {
-        ppb = kv.page_size / kKv4Tokens;
-        step_q = 32 / ppb;
-        step_r = 32 - step_q * ppb;
-        at = blk / ppb;
-        rem = blk - at * ppb;
-        load_page();
-        take_page();
+      const int32_t kvh = kv_head_of_vkv(gr, pc.vkv), n = tiles_of(d);
+      if (kv.paged) {  // the even tiles; the q warp copies the odd ones
+        const int32_t mine = (n + 1) / 2;
+        const int32_t done = copy_paged<D, C::kStages>(kv, p.err, smem + C::kStageOff, full, wait, p.stall_it, pc.b, kvh,
+                                                       pc.tok_begin, pc.tok_end, it, 0);
+        copied.add(it, 2, done);
+        if (done != mine) ok = false;
+        it += n;
+        continue;
       }
-      const int32_t n = tiles_of(d);
+      const uint8_t* base =
+          kv.kv + (((int64_t)pc.b * kv.Hkv + kvh) * kv.cap_blocks + pc.tok_begin / kKv4Tokens) * kv4_block_bytes(D);
+      const int32_t blocks = ceil_div(pc.tok_end, kKv4Tokens) - pc.tok_begin / kKv4Tokens;
+      const uint32_t it0 = it;
       for (int32_t j = 0; j < n; ++j, ++it, st.next()) {
-        const int32_t nblk = blk1 - (blk0 + j * kTileBlocks) < kTileBlocks ? blk1 - (blk0 + j * kTileBlocks) : kTileBlocks;
-        const bool stall = p.stall_it >= 0 && it == (uint32_t)p.stall_it;
+        const int32_t nblk = blocks - j * kTileBlocks < kTileBlocks ? blocks - j * kTileBlocks : kTileBlocks;
         if (!wait.warp(empty + st.i, st.ph ^ 1)) {
           ok = false;
           break;
         }
-        if (stall) {
-          stalled = it;
-          continue;
-        }
-        uint8_t* dst = smem + C::kStageOff + st.i * C::kStageBytes;
-        if (!kv.paged) {
-          if (lane == 0) {
-            const uint32_t bytes = (uint32_t)nblk * kv4_block_bytes(D);
-            mbar_arrive_expect_tx(full + st.i, bytes);
-            const uint8_t* src = base + (int64_t)j * C::kStageBytes;
-            asm volatile(
-                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
-                    smem_addr(dst)),
-                "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_addr(full + st.i)), "l"(stream_policy)
-                : "memory");
-          }
-        } else {
-          const int k0 = (j & 3) * kTileBlocks;
-          const uint32_t valid = (1u << nblk) - 1, bad = bads >> k0 & valid;
-          const int k = lane - k0;  // this lane's block of the tile
-          uint32_t starts = firsts >> k0 & valid;
-          if (__builtin_expect(bad != 0, 0)) {
-            // keys of score 0 and value 0 in its place
-            if (k >= 0 && k < kTileBlocks && bad >> k & 1) {
-              raise_error(p.err, kErrBadIndex);
-              for (int i = 0; i < kv4_block_bytes(D); i += 16)
-                sts128u(smem_addr(dst) + k * kv4_block_bytes(D) + i, make_uint4(0, 0, 0, 0));
-              // before a later copy into this stage
-              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            }
-            starts = (starts | bad << 1) & valid & ~bad;  // a block after a bad one starts a copy
-            __syncwarp();
-          }
-          const uint8_t* from = kv.kv + (uint64_t)cur * kv4_block_bytes(D);
-          if (starts == valid) {  // one a block: a constant size is quicker to issue
-            if (k >= 0 && k < nblk) bulk_load(dst + k * kv4_block_bytes(D), from, kv4_block_bytes(D), full + st.i);
-          } else if (k >= 0 && k < kTileBlocks && starts >> k & 1) {
-            const uint32_t stops = starts | bad | ~valid;  // the next copy, a bad block, the tile's end
-            bulk_load(dst + k * kv4_block_bytes(D), from, __ffs(stops >> (k + 1)) * kv4_block_bytes(D), full + st.i);
-          }
-          if (lane == 0) mbar_arrive_expect_tx(full + st.i, __popc(valid & ~bad) * kv4_block_bytes(D));
-          __syncwarp();
-          if ((j & 3) == 3) take_page();
+        if (lane == 0 && it != (uint32_t)p.stall_it) {
+          const uint32_t bytes = (uint32_t)nblk * kv4_block_bytes(D);
+          mbar_arrive_expect_tx(full + st.i, bytes);
+          const uint8_t* src = base + (int64_t)j * C::kStageBytes;
+          asm volatile(
+              "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+                  sbase + C::kStageOff + st.i * C::kStageBytes),
+              "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_addr(full + st.i)), "l"(stream_policy)
+              : "memory");
         }
       }
+      copied.add(it0, 1, (int32_t)(it - it0));
     }
     if (live) {
       KvPiece d;
@@ -667,13 +706,7 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
       raise_error(p.err, kErrTimeout);
       *abort_flag = 1;
     }
-    // stay until the copies in flight have landed
-    if (lane == 0) {
-      const uint32_t n = it < (uint32_t)C::kStages ? it : (uint32_t)C::kStages;
-      for (uint32_t j = it - n; j < it; ++j)
-        if (j != stalled && !mbar_wait_for(full + j % C::kStages, (j / C::kStages) & 1, wait.limit))
-          raise_error(p.err, kErrTimeout);
-    }
+    if (lane == 0) copied.land<C::kStages>(full, ok && live ? it : 0, p.stall_it, wait.limit, p.err);
   } else if (warp < 3) {
     // ------------------------------------------------------------ MMA issue
     // Every branch and operand here is uniform over the warp as the compiler sees it
@@ -687,10 +720,30 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
     Ring<C::kVBufs> vr;
     Ring<C::kSBufs> sr;
     uint32_t sg = 0;  // the softmax group of tile g
+    // The O warp counts the pieces that the CTA goes on after, so that the softmax warps need
+    // not wait for the atomic: they join a sequence at their next piece's end.  Their first p
+    // of that piece comes later than the end of the last.
+    bool due = false;
+    uint32_t parts = 0;
+    const auto count_piece = [&] {
+      const bool done = __all_sync(0xffffffffu, mbar_wait_for(part_done, parts & 1, patience));
+      if (!done) ok = false;
+      if (lane == 0) {
+        JoinPiece& j = counted[parts & 1];
+        j.last = done && j.npieces != 1 &&
+                 atomic_add_acq_rel(p.counters + j.b * p.hv + j.vkv, 1) == j.npieces - 1;
+        mbar_arrive(join_known);
+      }
+      __syncwarp();
+      ++parts;
+    };
     for (uint32_t e = 0;; ++e) {
       KvPiece pc;
-      if (!__all_sync(0xffffffffu, next_piece(e, pc))) break;
-      const int32_t n = ok ? (int32_t)uniform(tiles_of(pc)) : 0;
+      const bool got = __all_sync(0xffffffffu, next_piece(e, pc));
+      const int32_t n = got && ok ? (int32_t)uniform(tiles_of(pc)) : 0;
+      if (due) count_piece();
+      if (!got) break;
+      due = !is_s && p.counters != nullptr && uniform(pc.more) != 0;
       if (n == 0) continue;
       if (is_s && !wait.warp(q_ready + (f & 1), (f >> 1) & 1)) ok = false;
       for (int32_t j = 0; ok && j < n; ++j, ++g) {
@@ -756,7 +809,8 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
     gr.gpad = p.gpad;
     gr.nsub = p.nsub;
     gr.hv = p.hv;
-    uint32_t f = 0, parts = 0;
+    uint32_t f = 0, it = 0;
+    Copied copied;
     const auto prepare = [&](const KvPiece& pc) {
       const uint32_t qb = f & 1;
       if (f >= 2 && !wait.warp(q_free + qb, ((f >> 1) & 1) ^ 1)) return false;
@@ -841,39 +895,24 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
       ++f;
       return true;
     };
-    // The pieces that the CTA goes on after are counted here, so that the softmax
-    // warps need not wait for the atomic; they join a sequence at their next piece's end.
-    const auto finish = [&](const KvPiece& pc) {
-      JoinPiece j;
-      j.b = pc.b;
-      j.vkv = pc.vkv;
-      j.npieces = pieces_of(pc, j.first);
-      const bool done = __all_sync(0xffffffffu, mbar_wait_for(part_done, parts++ & 1, patience));
-      if (!done) ok = false;
-      if (lane == 0) {
-        j.last = done && arrive_last(pc, j.npieces) ? 1 : 0;
-        *counted = j;
-        mbar_arrive(join_known);
-      }
-      __syncwarp();
-    };
     pdl_wait();
-    KvPiece prev;
-    bool pending = false;
-    for (uint32_t e = 0;; ++e) {
-      KvPiece pc;
-      const bool got = next_piece(e, pc);
-      if (got && ok && tiles_of(pc) > 0 && !prepare(pc)) ok = false;
-      if (pending) finish(prev);
-      if (!got) break;
-      int32_t first;
-      pending = p.counters != nullptr && pc.more && pieces_of(pc, first) != 1;
-      prev = pc;
+    KvPiece pc;
+    for (uint32_t e = 0; next_piece(e, pc); ++e) {
+      const int32_t n = tiles_of(pc);
+      if (ok && n > 0 && !prepare(pc)) ok = false;
+      if (ok && kv.paged && n > 1) {  // the odd tiles
+        const int32_t done = copy_paged<D, C::kStages>(kv, p.err, smem + C::kStageOff, full, wait, p.stall_it, pc.b,
+                                                       kv_head_of_vkv(gr, pc.vkv), pc.tok_begin, pc.tok_end, it + 1, 1);
+        copied.add(it + 1, 2, done);
+        if (done != n / 2) ok = false;
+      }
+      it += n;
     }
     if (!ok) {
       raise_error(p.err, kErrTimeout);
       *abort_flag = 1;
     }
+    if (lane == 0) copied.land<C::kStages>(full, ok ? it : 0, p.stall_it, wait.limit, p.err);
   } else if (warp < 12) {
     // ------------------------------------------------------------ K
     const int quad = warp & 3;
@@ -1029,12 +1068,12 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
       }
     }
     uint32_t g = C::kByHead ? 0 : group, e = 0, f = 0, g1 = 0;  // this group's next tile, the end of the piece
-    bool owed = false;                         // the q warp counts the last piece
+    bool owed = false;                         // the O warp counts the last piece
     uint32_t joins = 0;
     const auto join_owed = [&] {
-      const bool known = __all_sync(0xffffffffu, mbar_wait_for(join_known, joins++ & 1, patience));
-      if (known && counted->last)
-        join_piece(counted->b, counted->vkv, counted->npieces, counted->first, warp - kSoftmax0, 4 * kSG);
+      const bool known = __all_sync(0xffffffffu, mbar_wait_for(join_known, joins & 1, patience));
+      const JoinPiece& j = counted[joins++ & 1];
+      if (known && j.last) join_piece(j.b, j.vkv, j.npieces, j.first, warp - kSoftmax0, 4 * kSG);
       ok = ok && known;
     };
     KvPiece pc;
@@ -1283,18 +1322,17 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
           }
         }
       }
-      if (owed) join_owed();  // before the q warp hears of this piece
-      owed = fused && !final_here && pc.more;
-      if (fused && !final_here) {
-        if (pc.more) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(part_done);
-        } else {
-          named_barrier(1, C::kSThreads);  // every thread's partial stores come before the release
-          if (st == 0) *last_flag = arrive_last(pc, npieces) ? 1 : 0;
-          named_barrier(1, C::kSThreads);
-          if (*last_flag) join_piece(pc.b, pc.vkv, npieces, first, warp - kSoftmax0, 4 * kSG);
-        }
+      if (owed) join_owed();
+      owed = fused && pc.more;
+      if (owed) {
+        if (st == 0) counted[joins & 1] = JoinPiece{0, pc.b, pc.vkv, npieces, first};
+        __syncwarp();
+        if (lane == 0) mbar_arrive(part_done);
+      } else if (fused && !final_here) {
+        named_barrier(1, C::kSThreads);  // every thread's partial stores come before the release
+        if (st == 0) *last_flag = arrive_last(pc, npieces) ? 1 : 0;
+        named_barrier(1, C::kSThreads);
+        if (*last_flag) join_piece(pc.b, pc.vkv, npieces, first, warp - kSoftmax0, 4 * kSG);
       }
     }
     if (!ok) {
