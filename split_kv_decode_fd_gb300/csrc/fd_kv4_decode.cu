@@ -31,13 +31,13 @@
 // tokens take 40.5 us (3.7 TB/s), 16 ragged sequences of 1024 to 16384 tokens 32.
 //
 // Twenty-eight warps:
-//   0      walks the plan, announces pieces, copies tiles (one bulk copy for a
-//          contiguous run, one per run of blocks when paged) into a ring of stages;
+//   0      walks the plan, announces pieces, copies tiles into a ring of stages: all of
+//          a contiguous cache (one bulk copy each), the even ones of a paged one;
 //   1, 2   one thread of each issues MMAs: S, and O (each MMA takes 18
-//          cycles to issue, and a tile needs eight of each kind);
+//          cycles to issue, and a tile needs eight of each kind); the latter also
+//          counts the pieces that the CTA goes on after;
 //   3      q of the next piece: scaled to the fp16 range by a power of two per
-//          head, split hi / lo, written in the B layout; it also counts the pieces
-//          that the CTA goes on after;
+//          head, split hi / lo, written in the B layout; the odd tiles of a paged cache;
 //   4-11   K, two groups of four warps: lane = key;
 //   12-19  V, two groups: lane = channel;
 //   20-27  softmax, two groups: lane = key; lane = channel where O is taken.
@@ -364,11 +364,12 @@ struct Waiter {
 
 // Copies of every second tile j, j + 2, ... of a paged piece, by one warp; tile j is the
 // CTA's tile g.  Returns how many it dealt with: a wait for a free stage may run out.
-// An SM's warp starts a bulk copy in some 90 cycles, and pages of sixteen tokens need eight
-// a tile, so two warps take turns (524288 tokens of 8 heads TIME_C; one warp's lanes with
-// 16-byte copies took 182).  Blocks of a tile that follow one another in the pool go in one.
+// A warp starts a bulk copy in some 90 cycles, and pages of sixteen tokens need eight
+// a tile, so two warps take turns (524288 tokens of 8 heads 127 us, with one warp 168, with one
+// warp's lanes and 16-byte copies 182; 64 sequences of 512 to 16384 tokens 105, 114 with one).
+// Blocks of a tile that follow one another in the pool go in one copy.
 template <int D, int kStages>
-__device__ __noinline__ int32_t copy_paged(const Kv4View& kv, unsigned* err, uint8_t* stages, uint64_t* full, Waiter wait,
+__device__ __forceinline__ int32_t copy_paged(const Kv4View& kv, unsigned* err, uint8_t* stages, uint64_t* full, Waiter wait,
                                            int32_t stall_it, int32_t b, int32_t kvh, int32_t tok_begin, int32_t tok_end,
                                            uint32_t g, int32_t j) {
   constexpr int kBytes = kv4_block_bytes(D);
