@@ -790,6 +790,7 @@ fd_status check_kv4(const fd_kv4_desc* kv, int B, int Hkv, int D, int64_t max_le
   if (max_len < 0) return FD_ERR_INVALID_ARG;
   if (kv->k_exp < -kKv4MaxExp || kv->k_exp > kKv4MaxExp || kv->v_exp < -kKv4MaxExp || kv->v_exp > kKv4MaxExp)
     return FD_ERR_INVALID_ARG;
+  if (max_len > INT32_MAX - 2 * kPlanTile) return FD_ERR_UNSUPPORTED;  // a tile's end is an int32
   const int64_t tiles = (int64_t)B * Hkv * ((max_len + kPlanTile - 1) / kPlanTile);
   if (tiles >= ((int64_t)1 << 31) / kMaxGroupBf16) return FD_ERR_UNSUPPORTED;
   Kv4View v;
