@@ -360,6 +360,11 @@ struct Waiter {
   __device__ __forceinline__ bool warp(uint64_t* bar, uint32_t parity) const {
     return __all_sync(0xffffffffu, one(bar, parity));
   }
+  // Two barriers, one vote.  (The phase before a barrier's first counts as complete: a
+  // buffer that nothing has used yet is free.)
+  __device__ __forceinline__ bool both(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb) const {
+    return __all_sync(0xffffffffu, one(a, pa) && one(b, pb));
+  }
 };
 
 // Copies of every second tile j, j + 2, ... of a paged piece, by one warp; tile j is the
@@ -750,7 +755,7 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
       for (int32_t j = 0; ok && j < n; ++j, ++g) {
         if (is_s) {
           // K is there, and the softmax has read what the S buffer held
-          if (!wait.warp(k_ready + kr.i, kr.ph) || (g >= C::kSBufs && !wait.warp(p_ready + sr.i, sr.ph ^ 1))) {
+          if (!wait.both(k_ready + kr.i, kr.ph, p_ready + sr.i, sr.ph ^ 1)) {
             ok = false;
             break;
           }
@@ -769,7 +774,7 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
             if (j == n - 1) mma_commit(smem_addr(q_free + qb));
           }
         } else {
-          if (!wait.warp(v_ready + vr.i, vr.ph) || !wait.warp(p_ready + sr.i, sr.ph)) {
+          if (!wait.both(v_ready + vr.i, vr.ph, p_ready + sr.i, sr.ph)) {
             ok = false;
             break;
           }
@@ -930,7 +935,7 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
       if (ok) g1 += tiles_of(pc);
       for (; ok && g < g1; g += 2, kr.skip()) {
         const uint32_t st = g % C::kStages;
-        if (!wait.warp(full + st, g / C::kStages & 1) || (g >= C::kKBufs && !wait.warp(k_free + kr.i, kr.ph ^ 1))) {
+        if (!wait.both(full + st, g / C::kStages & 1, k_free + kr.i, kr.ph ^ 1)) {
           ok = false;
           break;
         }
@@ -980,7 +985,7 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
         if (ok) g1 += tiles_of(pc);
         for (; ok && g < g1; g += 2, vr.skip()) {
           const uint32_t st = g % C::kStages;
-          if (!wait.warp(full + st, g / C::kStages & 1) || (g >= C::kVBufs && !wait.warp(v_free + vr.i, vr.ph ^ 1))) {
+          if (!wait.both(full + st, g / C::kStages & 1, v_free + vr.i, vr.ph ^ 1)) {
             ok = false;
             break;
           }
