@@ -18,9 +18,8 @@
 //     where they go, but after the length that says whether they are padding (55 %
 //     live of 8192 tokens: 36.8 us, 32.0 when padding is not loaded).
 // Measured: 8192 tokens into bf16 48 us (5.6 TB/s, 83 % of a copy's rate), the
-// same into 4 bits 51.6 us, 96 tokens 2.4 us (bf16) and 6.2 us (4 bits: the
-// length, the block number, the block's old nibbles, then two barriers, one
-// after another), a read-back of 16384 tokens 29.7 us (5.8 TB/s, 85 %).
+// same into 4 bits 51.6 us, 96 tokens 2.4 us (bf16) and 3.1 us (4 bits), a read-back
+// of 16384 tokens 29.7 us (5.8 TB/s, 85 %).
 #include "../../include/fdecode.h"
 #include "fd_kv4.cuh"
 
@@ -348,6 +347,80 @@ __global__ void __launch_bounds__(D) fd_append_kv4_kernel(const NewRows r, const
   *reinterpret_cast<uint2*>(blk + kv4_v_off(D) + tid * 8) = make_uint2(w[0], w[1]);
 }
 
+// The largest size of the sixteen lanes' values, NaN if one is.
+__device__ __forceinline__ float amax16(float v) {
+  float m = fabsf(v);
+#pragma unroll
+  for (int o = 8; o > 0; o /= 2) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return m;
+}
+__device__ __forceinline__ float load1(const float* p) { return __ldg(p); }
+__device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+
+// The same for few tokens a sequence: a CTA of D threads takes a (sequence, KV head)
+// and its tokens one after another, a channel a thread; the bytes are the same.  Above,
+// eight threads would quantise a lone token, sixteen channels each, while the others wait.
+// 1, 2, 3, 4, 8 tokens of 96 sequences: 3.1, 4.9, 6.1, 7.5, 13.9 us; above 5.9, 7.9, 7.7,
+// 7.7, 8.7.  Of one sequence: 2.6, 3.6, 4.7, 5.7, 9.4; above 4.8 to 5.0.
+constexpr int32_t kFewRows = 3;
+template <int D, class T>
+__global__ void __launch_bounds__(D) fd_append_kv4_few_kernel(const NewRows r, const Kv4View kv, int32_t kv_ctas) {
+  constexpr int TPR = D / 16;
+  const int d = threadIdx.x;
+  if ((int32_t)blockIdx.x >= kv_ctas) {
+    const int64_t item = (int64_t)(blockIdx.x - kv_ctas) * 16 + d / TPR;
+    if (item >= (int64_t)r.B * r.n * r.Hq) return;
+    const int32_t tok = (int32_t)(item / r.Hq), h = (int32_t)(item - (int64_t)tok * r.Hq);
+    query_row<D, T>(r, tok / r.n, tok % r.n, h, d % TPR);
+    return;
+  }
+  const int32_t b = blockIdx.x / kv.Hkv, h = blockIdx.x % kv.Hkv;
+  // this channel's pair, and its place in it
+  const int half = r.rot / 2;
+  const bool turned = d < r.rot, second = r.interleaved ? d & 1 : d >= half;
+  const int pair = r.interleaved ? d / 2 : (second ? d - half : d);
+  const int other = !turned ? d : r.interleaved ? d ^ 1 : (second ? d - half : d + half);
+  const float kdown = pow2i(-kv.k_exp), vdown = pow2i(-kv.v_exp);
+#pragma unroll 1
+  for (int32_t i = 0; i < r.n; ++i) {
+    if (padding(r, b, i)) continue;
+    const T* krow = static_cast<const T*>(r.k) + (int64_t)b * r.ks[0] + (int64_t)i * r.ks[1] + (int64_t)h * r.ks[2];
+    const T* vrow = static_cast<const T*>(r.v) + (int64_t)b * r.vs[0] + (int64_t)i * r.vs[1] + (int64_t)h * r.vs[2];
+    float k = load1(krow + d), v = load1(vrow + d);
+    const float o = load1(krow + other);
+    const Place pl = place_of(r, b, i);
+    if (!pl.live) continue;
+    const int64_t idx = kv4_block_index(kv, b, h, pl.t);
+    if (idx < 0) {
+      if (d == 0) atomicOr(r.err, kErrBadIndex);
+      continue;
+    }
+    if (turned) {
+      const int64_t at = (int64_t)pl.pos * half + pair;
+      const float c = __ldg(r.cos + at), sn = __ldg(r.sin + at);
+      k = second ? fmaf(k, c, o * sn) : fmaf(k, c, -(o * sn));
+    }
+    uint8_t* blk = kv.kv + idx * kv4_block_bytes(D);
+    const int tt = pl.t % kKv4Tokens;
+    uint8_t* vbyte = blk + kv4_v_off(D) + d * 8 + (tt >> 1);
+    const uint32_t old = *vbyte;
+    k *= kdown;
+    v *= vdown;
+    const uint32_t bk = f32_e4m3(__fdiv_rn(amax16(k), 6.f)), bv = f32_e4m3(__fdiv_rn(amax16(v), 6.f));
+    const float sk = e4m3_f32(bk), sv = e4m3_f32(bv);
+    const float qk = sk == 0.f ? copysignf(0.f, k) : __fdiv_rn(k, sk);
+    const float qv = sv == 0.f ? copysignf(0.f, v) : __fdiv_rn(v, sv);
+    const uint32_t code = f32_e2m1x2(qv, 0.f);
+    *vbyte = (uint8_t)(tt & 1 ? (old & 0x0fu) | code << 4 : (old & 0xf0u) | code);
+    const uint32_t two = f32_e2m1x2(qk, __shfl_down_sync(0xffffffffu, qk, 1));
+    if ((d & 1) == 0) blk[tt * (D / 2) + (((d >> 5) ^ kv4_swizzle(D, tt)) << 4) + ((d & 31) >> 1)] = (uint8_t)two;
+    if (d % 16 == 0) {
+      blk[kv4_ks_off(D) + tt * (D / 16) + d / 16] = (uint8_t)bk;
+      blk[kv4_vs_off(D) + d / 16 * 16 + tt] = (uint8_t)bv;
+    }
+  }
+}
+
 // ------------------------------------------------------------------ read-back
 template <class O>
 __device__ __forceinline__ void store_values(O* out, uint32_t lo, uint32_t hi, float scale) {
@@ -424,10 +497,14 @@ cudaError_t append_t(bool cache_f32, const NewRows& r, const KvView& kv, cudaStr
 
 template <int D, class T>
 cudaError_t append_kv4_t(const NewRows& r, const Kv4View& kv, cudaStream_t stream) {
-  const int32_t nblk = blocks_touched(r.n);
+  const int32_t nblk = r.n <= kFewRows ? 1 : blocks_touched(r.n);
   const int64_t kv_ctas = (int64_t)r.B * kv.Hkv * nblk;
   const int64_t ctas = kv_ctas + ((int64_t)r.B * r.n * r.Hq + 15) / 16;
   if (ctas > INT32_MAX) return cudaErrorInvalidValue;
+  if (r.n <= kFewRows) {
+    fd_append_kv4_few_kernel<D, T><<<(unsigned)ctas, D, 0, stream>>>(r, kv, (int32_t)kv_ctas);
+    return cudaGetLastError();
+  }
   fd_append_kv4_kernel<D, T><<<(unsigned)ctas, D, 0, stream>>>(r, kv, nblk, (int32_t)kv_ctas);
   return cudaGetLastError();
 }

@@ -55,6 +55,13 @@ __device__ __forceinline__ uint32_t f32_e2m1x8(const float (&v)[8]) {
   return r;
 }
 
+// Two values to codes: a in the low nibble of a byte, b in the high one.
+__device__ __forceinline__ uint32_t f32_e2m1x2(float a, float b) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 x;\n\tcvt.rn.satfinite.e2m1x2.f32 x, %2, %1;\n\tmov.b32 %0, {x, x, x, x};\n\t}" : "=r"(r) : "f"(a), "f"(b));
+  return r & 0xffu;
+}
+
 // The larger of two, NaN if one is.
 __device__ __forceinline__ float max_nan(float a, float b) {
   float d;

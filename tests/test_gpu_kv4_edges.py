@@ -104,6 +104,37 @@ def test_rows_at_16_byte_addresses(D, dtype, rot):
     assert torch.equal(got[0][3], got[0][4]) and got[0][0].abs().sum() > 0 and got[0][5].abs().sum() > 0
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rot,interleaved", [(0, False), (64, False), (64, True), (32, False), (32, True)])
+@pytest.mark.parametrize("page", [0, 16])
+def test_tokens_one_by_one_give_the_bytes_of_all_at_once(D, dtype, rot, interleaved, page):
+    g = torch.Generator(device="cuda").manual_seed(D + rot + page)
+    B, n, Hq, Hkv, cap = 3, 38, 4, 2, 64
+    x = torch.randn((B, n, Hq + 2 * Hkv, D), generator=g, device="cuda").to(dtype)
+    x[1, 5, :, 16:32] = 0.0
+    x[2, 7, Hq, 3] = float("nan")
+    x[0, 30, Hq + Hkv, 40] = float("inf")
+    table = torch.randperm(B * cap // page, generator=g, device="cuda").view(B, -1).int() if page else None
+    ang = torch.rand((cap, rot // 2), generator=g, device="cuda")
+    cos, sin = (ang.cos(), ang.sin()) if rot else (None, None)
+    got = []
+    for step in (n, 1, 2, 3):
+        kv = fd.kv4_cache(B * cap // page if page else B, Hkv, page or cap, D)
+        lens = torch.tensor([0, 11, 25], dtype=torch.int32, device="cuda")
+        q = []
+        for at in range(0, n, step):
+            y = x[:, at:at + step]
+            q.append(fd.append_rope_kv4(y[:, :, Hq:Hq + Hkv], y[:, :, Hq + Hkv:], kv, cos, sin, q=y[:, :, :Hq], k_exp=1,
+                                        v_exp=-2, interleaved=interleaved, seq_lens=lens,
+                                        max_seq_len=cap - y.shape[1], block_table=table))
+            lens += y.shape[1]
+        got.append((kv, torch.cat(q, 2)))
+    assert fd.workspace_status() == 0
+    for kv, q in got[1:]:
+        assert torch.equal(kv, got[0][0]) and torch.equal(q.view(torch.int32), got[0][1].view(torch.int32))
+
+
 def test_two_captured_graphs_share_a_workspace():
     a = Case(3, 8, 2, 128, [900, 33, 512], page=16, seed=3)
     b = Case(5, 32, 2, 64, [2000, 1, 700, 0, 64], seed=4)
