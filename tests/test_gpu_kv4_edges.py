@@ -119,7 +119,7 @@ def test_tokens_one_by_one_give_the_bytes_of_all_at_once(D, dtype, rot, interlea
     ang = torch.rand((cap, rot // 2), generator=g, device="cuda")
     cos, sin = (ang.cos(), ang.sin()) if rot else (None, None)
     got = []
-    for step in (n, 1, 2, 3):
+    for step in (n, 1, 2, 3, 4, 5):
         kv = fd.kv4_cache(B * cap // page if page else B, Hkv, page or cap, D)
         lens = torch.tensor([0, 11, 25], dtype=torch.int32, device="cuda")
         q = []
