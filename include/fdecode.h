@@ -367,8 +367,9 @@ FD_API fd_status fd_kv4_read(const fd_kv4_desc* kv, void* k_out, void* v_out, fd
  * q, out and lse, the same masking, lengths and split arguments, and a workspace of
  * fd_workspace_bytes(B, Hq * n_q, Hkv, D, n_splits, 0) bytes.  A page outside the pool
  * counts as keys with score 0 and value 0, and is reported as FD_ERR_BAD_INDEX.
- * q and the softmax weights are held to 22 bits, products and sums in fp32.  Scores
- * may have any size that fp32 holds.  A NaN key shows in the rows that see it; a NaN
+ * q is held to 22 bits of each head's largest channel, a softmax weight to 22 bits of
+ * itself down to 2^-23 of the largest and to 2^-45 of the largest below; products and sums
+ * are fp32.  Scores may have any size that fp32 holds.  A NaN key shows in the rows that see it; a NaN
  * value of one of the last n_q tokens in every row of the window, those before the
  * token too (its weight there is 0, and 0 * NaN is NaN), and of an older token in all
  * rows, as it should.

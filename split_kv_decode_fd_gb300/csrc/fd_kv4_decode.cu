@@ -68,9 +68,12 @@ constexpr int kDescs = 4;                              // pieces announced ahead
 constexpr int kSoftmax0 = 20;                          // first softmax warp
 // p is held in fp16: the reference of the exponent lies kRefDown below the
 // running maximum and moves when a score exceeds that maximum by kTau, so p <=
-// 2^(kRefDown + kTau) = 2^15, and the smallest fp16 number stands for 2^-33 of the
-// maximum's weight.
+// 2^(kRefDown + kTau) = 2^15.  Its lower half is held kLoUp times up, in the same range: the
+// smallest fp16 number there stands for 2^-44 of the maximum's weight, and p has its 22 bits
+// down to 2^-23 of it.  (Not scaled, a weight below 2^-34 was 0 in O and not in l: 131072 such keys
+// put out 8e-6 off.)
 constexpr float kRefDown = 9.f, kTau = 6.f;
+constexpr float kLoUp = 2048.f, kLoDown = 1.f / kLoUp;
 // Tiles of a group whose O products add up in tensor memory before their sum moves to
 // fp32 adds in shared memory.  An MMA's add drops bits instead of rounding, some 2^-25.6
 // of the sum each and all one way: with 27 tiles in a row the outputs of 128k tokens were
@@ -211,11 +214,19 @@ __device__ __forceinline__ void sts128u(uint32_t at, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
-// (x0, x1) = hi + lo in fp16, as packed pairs (x0 in the low half).
-__device__ __forceinline__ void split_f16x2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+// (x0, x1) = hi + lo / up in fp16, as packed pairs (x0 in the low half).  kPacked: the
+// difference and its product two at a time, the same numbers (8 heads a group, 64 paged sequences
+// 104.8 us against 107.1; 16 heads, 524288 tokens 217.7 against 209.0).
+template <bool kPacked>
+__device__ __forceinline__ void split_f16x2(float x0, float x1, uint32_t& hi, uint32_t& lo, float up = 1.f) {
   const __half2 h = __floats2half2_rn(x0, x1);
   const float2 f = __half22float2(h);
-  const __half2 r = __floats2half2_rn(x0 - f.x, x1 - f.y);
+  float2 d;
+  if constexpr (kPacked)
+    d = fma2(fma2(f, make_float2(-1.f, -1.f), make_float2(x0, x1)), make_float2(up, up), make_float2(0.f, 0.f));
+  else
+    d = make_float2((x0 - f.x) * up, (x1 - f.y) * up);
+  const __half2 r = __floats2half2_rn(d.x, d.y);
   hi = *reinterpret_cast<const uint32_t*>(&h);
   lo = *reinterpret_cast<const uint32_t*>(&r);
 }
@@ -863,7 +874,7 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
         const float up = pow2i(13 - ex);
         uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) split_f16x2(x[2 * i] * up, x[2 * i + 1] * up, hi[i], lo[i]);
+        for (int i = 0; i < 4; ++i) split_f16x2<!C::kByHead>(x[2 * i] * up, x[2 * i + 1] * up, hi[i], lo[i]);
         if (G % kHeads == 0 || h < G) {
           sts128u(qs + b_off<N>(h, c8), make_uint4(hi[0], hi[1], hi[2], hi[3]));
           sts128u(qs + b_off<N>(G + h, c8), make_uint4(lo[0], lo[1], lo[2], lo[3]));
@@ -1136,7 +1147,7 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
           tmem_load<W>(tmem + lanes + o_col + G, lo);
           if (key < D) {
 #pragma unroll
-            for (int h = 0; h < H; ++h) sums[h * D] = (jj > kFlush ? sums[h * D] : 0.f) + (hi[h] + lo[h]);
+            for (int h = 0; h < H; ++h) sums[h * D] = (jj > kFlush ? sums[h * D] : 0.f) + fmaf(lo[h], kLoDown, hi[h]);
           }
           tmem_fence_before();
         }
@@ -1251,11 +1262,11 @@ __global__ void __launch_bounds__(K4<D, G>::kThreads, 1) fd_kv4_kernel(const __g
           uint32_t w[H < 2 ? 1 : H];  // columns of hi, then of lo, in pairs
           if constexpr (G == 1) {
             uint32_t hi, lo;
-            split_f16x2(x[0], 0.f, hi, lo);
+            split_f16x2<!C::kByHead>(x[0], 0.f, hi, lo, kLoUp);
             w[0] = hi | lo << 16;
           } else {
 #pragma unroll
-            for (int h = 0; h < H; h += 2) split_f16x2(x[h], x[h + 1], w[h / 2], w[(H + h) / 2]);
+            for (int h = 0; h < H; h += 2) split_f16x2<!C::kByHead>(x[h], x[h + 1], w[h / 2], w[(H + h) / 2], kLoUp);
           }
           if constexpr (G == 1) {
             asm volatile("st.shared.u32 [%0], %1;" ::"r"(ps), "r"(w[0]) : "memory");
