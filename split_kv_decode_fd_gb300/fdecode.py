@@ -254,17 +254,31 @@ class Workspace:
     states, and the prefill's item queue, all left at zero between calls: calls
     that may run at the same time (on different streams) need a Workspace each.
     The default one, used when none is passed, is shared per device.
+
+    A buffer that has been outgrown stays allocated as long as the Workspace does: a graph
+    captured with it holds its address.  Each is at least twice as large as the one before, so
+    together they take no more than twice the last one's bytes.
     """
 
     def __init__(self, device=None):
         self.device = device
         self.buf = None
+        self._outgrown = []
 
     def get(self, nbytes: int, device):
-        torch = _torch()
         if self.buf is None or self.buf.numel() < nbytes or self.buf.device != device:
-            self.buf = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
+            self._replace(nbytes, device)
         return self.buf
+
+    def _replace(self, nbytes, device):
+        old = self._outgrown + ([] if self.buf is None else [self.buf])
+        here = [b for b in old if b.device == device]
+        buf = next((b for b in here if b.numel() >= nbytes), None)
+        if buf is None:
+            least = max([128] + [b.numel() for b in here])
+            buf = _torch().zeros(max(nbytes, 2 * least), dtype=_torch().uint8, device=device)
+        self._outgrown = [b for b in old if b is not buf]
+        self.buf = buf
 
 
 _DEFAULT_WS = {}

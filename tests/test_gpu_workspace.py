@@ -1,0 +1,43 @@
+"""GPU tests of workspaces that grow, and of calls that share one."""
+
+import pytest
+import torch
+
+import split_kv_decode_fd_gb300 as fd
+
+from test_gpu_decode_kv4 import Case
+
+pytestmark = pytest.mark.gpu
+
+
+def bf16_run(c):
+    """fd_decode of a Case's queries over a bf16 cache."""
+    k, v = (torch.from_numpy(x).cuda().bfloat16() for x in (c.k, c.v))
+    q = c.q[:, :, 0].contiguous()
+    return lambda **kw: fd.decode(q, k, v, max_seq_len=c.cap, scale=c.scale, **kw)
+
+
+@pytest.mark.parametrize("four", [True, False])
+def test_a_captured_graph_outlives_its_workspaces_growth(four):
+    small, large = Case(2, 8, 2, 128, [900, 33], seed=1), Case(8, 32, 4, 128, [2000] * 8, seed=2)
+    run, run_large = (small.run, large.run) if four else (bf16_run(small), bf16_run(large))
+    lens = torch.tensor(small.lens, dtype=torch.int32, device="cuda")
+    more = torch.tensor(large.lens, dtype=torch.int32, device="cuda")
+    ws = fd.Workspace()
+    want = [t.clone() for t in run(workspace=ws, seq_lens=lens)]
+    out, lse = (torch.zeros_like(t) for t in want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(workspace=ws, seq_lens=lens, out=out, lse=lse)
+    size, at = ws.buf.numel(), ws.buf.data_ptr()
+    first = [t.clone() for t in run_large(workspace=ws, seq_lens=more)]
+    assert ws.buf.numel() > size
+    taken = [torch.full((size,), 0x5A, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    assert all(t.data_ptr() != at for t in taken)
+    for _ in range(3):
+        out.fill_(7.0)
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip((out, lse), want))
+        assert all(torch.equal(a, b) for a, b in zip(first, run_large(workspace=ws, seq_lens=more)))
+    assert all(bool((t == 0x5A).all()) for t in taken)
+    assert fd.workspace_status(ws) == 0
