@@ -624,13 +624,18 @@ def combine(o_part, m_part, l_part, *, out=None, lse=None, return_lse=True, stre
 
 
 def workspace_status(workspace: Optional[Workspace] = None, device=None, stream=None) -> int:
-    """Synchronise and return (then clear) the kernels' error word of a workspace (0 = no error)."""
+    """Synchronise and return (then clear) the kernels' error word of a workspace (0 = no error).
+
+    Errors that calls, or replays of graphs captured with them, raised in a buffer that the workspace has outgrown count too.
+    """
     torch = _torch()
     device = device or torch.device("cuda", torch.cuda.current_device())
     ws = workspace or _default_workspace(device)
     if ws.buf is None:
         return FD_OK
-    return int(_lib().fd_workspace_status(ws.buf.data_ptr(), ws.buf.numel(), _stream_handle(ws.buf.device, stream)))
+    handle = _stream_handle(ws.buf.device, stream)
+    return max(int(_lib().fd_workspace_status(b.data_ptr(), b.numel(), handle))
+               for b in [ws.buf] + ws._outgrown if b.device == ws.buf.device)
 
 
 # ------------------------------------------------------------------ rotating append, 4-bit cache

@@ -41,3 +41,30 @@ def test_a_captured_graph_outlives_its_workspaces_growth(four):
         assert all(torch.equal(a, b) for a, b in zip(first, run_large(workspace=ws, seq_lens=more)))
     assert all(bool((t == 0x5A).all()) for t in taken)
     assert fd.workspace_status(ws) == 0
+
+
+@pytest.mark.parametrize("default", [False, True])
+def test_errors_raised_before_a_workspace_grew_are_reported(default):
+    c = Case(2, 8, 2, 64, [300, 200], page=16, seed=3)
+    large = Case(64, 64, 4, 128, [40] * 64, seed=4)
+    ws = fd.Workspace()
+    how = {} if default else dict(workspace=ws)
+    of = [] if default else [ws]
+    assert fd.workspace_status(*of) == 0
+    table = c.table.clone()
+    table[1, 3] = 1 << 20
+    lens = torch.tensor([40, 48], dtype=torch.int32, device="cuda")
+    x = torch.zeros((2, 1, 2, 64), device="cuda", dtype=torch.bfloat16)
+    append = lambda: fd.append_rope_kv4(x, x, c.kv4, seq_lens=lens, max_seq_len=48, block_table=table, **how)  # noqa: E731
+    append()
+    assert fd.workspace_status(*of) == 4 and fd.workspace_status(*of) == 0
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        append()
+    append()
+    for n_splits, cause in ((7, lambda: None), (40, graph.replay)):
+        cause()
+        large.run(n_splits=n_splits, **how)
+        assert fd.workspace_status(*of) == 4 and fd.workspace_status(*of) == 0
+    graph.replay()
+    assert fd.workspace_status(*of) == 4 and fd.workspace_status(*of) == 0
