@@ -264,6 +264,7 @@ class Workspace:
         self.device = device
         self.buf = None
         self._outgrown = []
+        self._streams = set()  # handles of the streams that the caching allocator knows to use buf
 
     def get(self, nbytes: int, device):
         if self.buf is None or self.buf.numel() < nbytes or self.buf.device != device:
@@ -279,6 +280,7 @@ class Workspace:
             buf = _torch().zeros(max(nbytes, 2 * least), dtype=_torch().uint8, device=device)
         self._outgrown = [b for b in old if b is not buf]
         self.buf = buf
+        self._streams = set()
 
 
 _DEFAULT_WS = {}
@@ -684,22 +686,33 @@ def _made(make, shape, dtype, device, stream):
 
 
 def _scratch(workspace, index, nbytes, stream=None):
-    """The workspace's buffer, zero-filled on the call's stream.  It is not made during a
-    stream capture: its first zero-fill would then run only with the graph."""
+    """The workspace's buffer, zero-filled on the call's stream, and the stream's handle."""
     torch = _torch()
     ws = workspace
     if ws is None:
         ws = _DEFAULT_WS.get(("cuda", index)) or _default_workspace(torch.device("cuda", index))
     buf = ws.buf
     if buf is None or buf.numel() < nbytes or buf.get_device() != index:
-        if stream is not None:
+        if stream is None:
+            buf = _grown(ws, index, nbytes)
+        else:
             with torch.cuda.stream(stream):
-                return _scratch(ws, index, nbytes)
-        if torch.cuda.is_current_stream_capturing():
-            raise RuntimeError("the workspace is too small and cannot grow during a stream capture: run the call once "
-                               "before the capture, or pass a Workspace that has been used at this size")
-        buf = ws.get(nbytes, torch.device("cuda", index))
-    return buf
+                buf = _grown(ws, index, nbytes)
+    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if handle not in ws._streams:
+        # freed with the Workspace, the memory waits for what is still running there
+        buf.record_stream(torch.cuda.current_stream(index) if stream is None else stream)
+        ws._streams.add(handle)
+    return buf, handle
+
+
+def _grown(ws, index, nbytes):
+    """A larger buffer.  It is not made during a stream capture: its first zero-fill would then run only with the graph."""
+    torch = _torch()
+    if torch.cuda.is_current_stream_capturing():
+        raise RuntimeError("the workspace is too small and cannot grow during a stream capture: run the call once "
+                           "before the capture, or pass a Workspace that has been used at this size")
+    return ws.get(nbytes, torch.device("cuda", index))
 
 
 @functools.lru_cache(maxsize=256)
@@ -709,15 +722,14 @@ def _decode_bytes(B, Hq, Hkv, D, n_splits, index):
         return workspace_bytes(B, Hq, Hkv, D, n_splits)
 
 
-def _launch(index, stream, fn, where, *args):
-    """Call ``fn(*args, stream)`` with device ``index`` current (the library launches on the current device)."""
+def _launch(index, handle, fn, where, *args):
+    """Call ``fn(*args, handle)`` with device ``index`` current (the library launches on the current device)."""
     torch = _torch()
-    s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
     if index == torch.cuda.current_device():
-        st = fn(*args, s)
+        st = fn(*args, handle)
     else:
         with torch.cuda.device(index):
-            st = fn(*args, s)
+            st = fn(*args, handle)
     if st != FD_OK:
         raise FdError(st, where)
 
@@ -821,8 +833,8 @@ def _append(fn, where, desc, k_new, v_new, Hkv, D, tokens, index, cos, sin, q, q
         dt, qp, k_new.data_ptr(), v_new.data_ptr(), qs[0], qs[1], qs[2], ks[0], ks[1], ks[2], vs[0], vs[1], vs[2],
         _opt(new_lens, "new_lens", torch.int32, index, (B,)), _opt(positions, "positions", torch.int32, index, (B, n)),
         cp, sp, max_pos, rot, 1 if interleaved else 0))
-    buf = _scratch(workspace, index, 256, stream)
-    _launch(index, stream, fn, where, rows, desc, qo, B, n, Hq, Hkv, _opt(seq_lens, "seq_lens", torch.int32, index, (B,)),
+    buf, handle = _scratch(workspace, index, 256, stream)
+    _launch(index, handle, fn, where, rows, desc, qo, B, n, Hq, Hkv, _opt(seq_lens, "seq_lens", torch.int32, index, (B,)),
             tokens - n if max_seq_len is None else int(max_seq_len), D, buf.data_ptr(), buf.numel())
     return q_out
 
@@ -898,8 +910,8 @@ def kv4_read(kv4, n, *, starts=None, seq_lens=None, max_seq_len=None, block_tabl
         k_out = _made(torch.zeros, shape, dtype, kv4.device, stream)
     if v_out is None:
         v_out = _made(torch.zeros, shape, dtype, kv4.device, stream)
-    buf = _scratch(workspace, index, 256, stream)
-    _launch(index, stream, _lib().fd_kv4_read, "fd_kv4_read", desc, _flat(k_out, "k_out", dtype, index, shape),
+    buf, handle = _scratch(workspace, index, 256, stream)
+    _launch(index, handle, _lib().fd_kv4_read, "fd_kv4_read", desc, _flat(k_out, "k_out", dtype, index, shape),
             _flat(v_out, "v_out", dtype, index, shape), dt, B, n, Hkv, _opt(starts, "starts", torch.int32, index, (B,)),
             _opt(seq_lens, "seq_lens", torch.int32, index, (B,)), tokens if max_seq_len is None else int(max_seq_len), D,
             buf.data_ptr(), buf.numel())
@@ -940,8 +952,8 @@ def decode_kv4(q, kv4, *, k_exp=0, v_exp=0, causal=True, seq_lens=None, max_seq_
         lse = _made(torch.empty, shape[:-1], torch.float32, q.device, stream)
         lp = lse.data_ptr()
     n_splits = int(n_splits)
-    buf = _scratch(workspace, index, _decode_bytes(B, Hq * n_q, Hkv, D, n_splits, index), stream)
-    _launch(index, stream, _lib().fd_decode_kv4, "fd_decode_kv4", at, n_q, 1 if causal else 0, desc, op, lp, B, Hq, Hkv,
+    buf, handle = _scratch(workspace, index, _decode_bytes(B, Hq * n_q, Hkv, D, n_splits, index), stream)
+    _launch(index, handle, _lib().fd_decode_kv4, "fd_decode_kv4", at, n_q, 1 if causal else 0, desc, op, lp, B, Hq, Hkv,
             _opt(seq_lens, "seq_lens", torch.int32, index, (B,)), tokens if max_seq_len is None else int(max_seq_len), D,
             1.0 / math.sqrt(D) if scale is None else float(scale), n_splits, buf.data_ptr(), buf.numel())
     return out, lse

@@ -68,3 +68,24 @@ def test_errors_raised_before_a_workspace_grew_are_reported(default):
         assert fd.workspace_status(*of) == 4 and fd.workspace_status(*of) == 0
     graph.replay()
     assert fd.workspace_status(*of) == 4 and fd.workspace_status(*of) == 0
+
+
+def test_a_dropped_workspace_waits_for_the_streams_that_used_it():
+    """Its memory is not given out again while a call on another stream still writes there."""
+    c = Case(2, 8, 2, 128, [900, 333], page=16, seed=5)
+    lens = torch.tensor(c.lens, dtype=torch.int32, device="cuda")
+    ws = fd.Workspace()
+    want = [t.clone() for t in c.run(workspace=ws, seq_lens=lens)]
+    out, lse = (torch.zeros_like(t) for t in want)
+    size, at = ws.buf.numel(), ws.buf.data_ptr()
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(200_000_000)
+    c.run(workspace=ws, stream=s, seq_lens=lens, out=out, lse=lse)
+    del ws
+    taken = [torch.full((size,), 0x5A, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    assert not s.query() and all(t.data_ptr() != at for t in taken)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    assert all(bool((t == 0x5A).all()) for t in taken)
