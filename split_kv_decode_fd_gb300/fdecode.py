@@ -253,7 +253,10 @@ class Workspace:
     It holds the error word, the decode kernels' arrival counters and partial
     states, and the prefill's item queue, all left at zero between calls: calls
     that may run at the same time (on different streams) need a Workspace each.
-    The default one, used when none is passed, is shared per device.
+    The default one, used when none is passed, is shared per device; append_rope,
+    append_rope_kv4, kv4_read and decode_kv4 have one per stream.  A graph captured without a
+    Workspace takes the newest of these that is large enough: pass one to a graph that is
+    replayed beside other calls.
 
     A buffer that has been outgrown stays allocated as long as the Workspace does: a graph
     captured with it holds its address.  Each is at least twice as large as the one before, so
@@ -629,12 +632,23 @@ def workspace_status(workspace: Optional[Workspace] = None, device=None, stream=
     """Synchronise and return (then clear) the kernels' error word of a workspace (0 = no error).
 
     Errors that calls, or replays of graphs captured with them, raised in a buffer that the workspace has outgrown count too.
+    Without a workspace: the default ones of ``stream``, or of every stream of the device, which is then waited for.
     """
     torch = _torch()
     device = device or torch.device("cuda", torch.cuda.current_device())
-    ws = workspace or _default_workspace(device)
-    if ws.buf is None:
-        return FD_OK
+    if workspace is not None:
+        spaces = [workspace]
+    else:
+        index = torch.cuda.current_device() if device.index is None else device.index
+        handle = _stream_handle(device, stream)
+        own = [w for (i, h), w in list(_STREAM_WS.items()) if i == index and (stream is None or h == handle)]
+        if stream is None and own:
+            torch.cuda.synchronize(device)
+        spaces = [_default_workspace(device)] + own
+    return max([FD_OK] + [_word(ws, stream) for ws in spaces if ws.buf is not None])
+
+
+def _word(ws, stream):
     handle = _stream_handle(ws.buf.device, stream)
     return max(int(_lib().fd_workspace_status(b.data_ptr(), b.numel(), handle))
                for b in [ws.buf] + ws._outgrown if b.device == ws.buf.device)
@@ -685,20 +699,22 @@ def _made(make, shape, dtype, device, stream):
         return make(shape, dtype=dtype, device=device)
 
 
+_STREAM_WS = {}  # (device index, stream handle) -> Workspace
+
+
 def _scratch(workspace, index, nbytes, stream=None):
     """The workspace's buffer, zero-filled on the call's stream, and the stream's handle."""
     torch = _torch()
-    ws = workspace
-    if ws is None:
-        ws = _DEFAULT_WS.get(("cuda", index)) or _default_workspace(torch.device("cuda", index))
-    buf = ws.buf
+    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    ws = _STREAM_WS.get((index, handle)) if workspace is None else workspace
+    buf = None if ws is None else ws.buf
     if buf is None or buf.numel() < nbytes or buf.get_device() != index:
         if stream is None:
-            buf = _grown(ws, index, nbytes)
+            ws = _grown(ws, index, nbytes, handle)
         else:
             with torch.cuda.stream(stream):
-                buf = _grown(ws, index, nbytes)
-    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+                ws = _grown(ws, index, nbytes, handle)
+        buf = ws.buf
     if handle not in ws._streams:
         # freed with the Workspace, the memory waits for what is still running there
         buf.record_stream(torch.cuda.current_stream(index) if stream is None else stream)
@@ -706,13 +722,24 @@ def _scratch(workspace, index, nbytes, stream=None):
     return buf, handle
 
 
-def _grown(ws, index, nbytes):
-    """A larger buffer.  It is not made during a stream capture: its first zero-fill would then run only with the graph."""
+def _grown(ws, index, nbytes, handle):
+    """The Workspace with a larger buffer; the stream's own default if it is None.  No buffer is made during a stream
+    capture: its first zero-fill would then run only with the graph."""
     torch = _torch()
+    default = ws is None or ws is _STREAM_WS.get((index, handle))
     if torch.cuda.is_current_stream_capturing():
-        raise RuntimeError("the workspace is too small and cannot grow during a stream capture: run the call once "
-                           "before the capture, or pass a Workspace that has been used at this size")
-    return ws.get(nbytes, torch.device("cuda", index))
+        sized = [w for (i, _), w in list(_STREAM_WS.items())
+                 if default and i == index and w.buf is not None and w.buf.numel() >= nbytes]
+        if not sized:
+            raise RuntimeError("the workspace is too small and cannot grow during a stream capture: run the call once "
+                               "before the capture, or pass a Workspace that has been used at this size")
+        return sized[-1]
+    device = torch.device("cuda", index)
+    with _LOCK:  # two host threads may call on one stream
+        if ws is None:
+            ws = _STREAM_WS.setdefault((index, handle), Workspace(device))
+        ws.get(nbytes, device)
+    return ws
 
 
 @functools.lru_cache(maxsize=256)

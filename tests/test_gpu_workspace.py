@@ -89,3 +89,54 @@ def test_a_dropped_workspace_waits_for_the_streams_that_used_it():
     torch.cuda.synchronize()
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
     assert all(bool((t == 0x5A).all()) for t in taken)
+
+
+@pytest.mark.parametrize("given", [True, False])
+def test_calls_on_two_streams_without_a_workspace(given):
+    """Each stream has its own counters and partial states; errors of both are reported."""
+    cases = Case(3, 8, 2, 128, [9000, 33, 512], page=16, seed=6), Case(5, 32, 2, 64, [7000, 1, 700, 0, 64], seed=7)
+    lens = [torch.tensor(c.lens, dtype=torch.int32, device="cuda") for c in cases]
+    want = [[t.clone() for t in c.run(seq_lens=ln)] for c, ln in zip(cases, lens)]
+    outs = [[[torch.zeros_like(t) for t in w] for w in want] for _ in range(10)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for o in outs:
+        for c, ln, s, (out, lse) in zip(cases, lens, streams, o):
+            if given:
+                c.run(seq_lens=ln, out=out, lse=lse, stream=s)
+            else:
+                with torch.cuda.stream(s):
+                    c.run(seq_lens=ln, out=out, lse=lse)
+    torch.cuda.synchronize()
+    for o in outs:
+        for got, w in zip(o, want):
+            assert all(torch.equal(a, b) for a, b in zip(got, w))
+    assert fd.workspace_status() == 0
+    cases[0].table[0, 3] = -1
+    for s in streams:
+        torch.cuda.synchronize()
+        cases[0].run(seq_lens=lens[0], stream=s)
+        assert fd.workspace_status() == 4 and fd.workspace_status() == 0
+        cases[0].run(seq_lens=lens[0], stream=s)
+        assert fd.workspace_status(stream=s) == 4 and fd.workspace_status() == 0
+
+
+def test_a_capture_without_a_workspace_takes_one_that_calls_have_sized():
+    c = Case(3, 8, 2, 128, [900, 33, 512], page=16, seed=8)
+    lens = torch.tensor(c.lens, dtype=torch.int32, device="cuda")
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        want = [t.clone() for t in c.run(seq_lens=lens)]
+    s.synchronize()
+    out, lse = (torch.zeros_like(t) for t in want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.run(seq_lens=lens, out=out, lse=lse)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    with pytest.raises(RuntimeError, match="capture"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            c.run(n_splits=60000, seq_lens=lens, out=out, lse=lse)
+    assert fd.workspace_status() == 0
