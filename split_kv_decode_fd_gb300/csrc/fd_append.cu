@@ -451,8 +451,9 @@ __global__ void __launch_bounds__(D) fd_kv4_read_kernel(const Kv4Read r, const K
   const int32_t L = clamp_len(r.seq_lens ? __ldg(r.seq_lens + b) : r.max_len, r.max_len);
   const int32_t start = r.starts ? clamp_len(__ldg(r.starts + b), r.max_len) : 0;
   const int32_t end = L - start < r.n ? L : start + r.n;
-  const int32_t blk0 = (start / 16 + k) * 16;
-  if (blk0 >= end) return;
+  const uint32_t first = ((uint32_t)start / 16 + k) * 16;  // may pass the largest int32
+  if (first >= (uint32_t)end) return;
+  const int32_t blk0 = (int32_t)first;
   const int64_t idx = kv4_block_index(kv, b, h, blk0);
   if (idx < 0) {
     if (tid == 0) atomicOr(r.err, kErrBadIndex);
