@@ -938,7 +938,6 @@ fd_status fd_kv4_read(const fd_kv4_desc* kv, void* k_out, void* v_out, fd_dtype 
   r.seq_lens = seq_lens;
   r.max_len = max_seq_len;
   r.B = B;
-  // rows past max_seq_len do not exist
   r.n = n;
   r.err = reinterpret_cast<unsigned*>(workspace);
   return launch_kv4_read(D, dtype == FD_F32, r, v, (cudaStream_t)stream) == cudaSuccess ? FD_OK : FD_ERR_CUDA;

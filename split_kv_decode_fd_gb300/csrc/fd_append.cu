@@ -481,7 +481,8 @@ __global__ void __launch_bounds__(D) fd_kv4_read_kernel(const Kv4Read r, const K
   }
 }
 
-// Blocks of sixteen tokens that n consecutive tokens can touch.
+// Blocks of sixteen tokens that n consecutive tokens can touch; n is at most a cache's longest
+// sequence, so the sum fits.
 int32_t blocks_touched(int32_t n) { return (n + 14) / 16 + 1; }
 
 template <int D, class T>
@@ -528,7 +529,8 @@ cudaError_t launch_append_kv4(int D, bool rows_f32, const NewRows& r, const Kv4V
 }
 
 cudaError_t launch_kv4_read(int D, bool out_f32, const Kv4Read& r, const Kv4View& kv, cudaStream_t stream) {
-  const int32_t nblk = blocks_touched(r.n);
+  // r.n rows of the output may be more than there are tokens
+  const int32_t nblk = blocks_touched(r.n < r.max_len ? r.n : r.max_len);
   const int64_t ctas = (int64_t)r.B * kv.Hkv * nblk;
   if (ctas > INT32_MAX) return cudaErrorInvalidValue;
   const unsigned grid = (unsigned)ctas;

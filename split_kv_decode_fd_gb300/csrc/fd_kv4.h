@@ -91,7 +91,9 @@ struct Kv4Read {
 cudaError_t launch_kv4_read(int D, bool out_f32, const Kv4Read& r, const Kv4View& kv, cudaStream_t stream);
 
 struct SplitParams;
-// Partial states of every (virtual KV head, split) of the explicit plan.
+// Decode attention: the explicit plan (grid of virtual KV heads x splits) or the balanced one (one CTA
+// per SM).  With counters the last piece of a sequence joins its states into the output; without, the
+// states are left for launch_combine.
 cudaError_t launch_kv4_split(int D, const Kv4View& kv, const SplitParams& p, dim3 grid, cudaStream_t stream);
 
 }  // namespace fdk

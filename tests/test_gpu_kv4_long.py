@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import split_kv_decode_fd_gb300 as fd
+from split_kv_decode_fd_gb300 import fdecode as fdb
 
 pytestmark = pytest.mark.gpu
 PAGE = 1 << 20
@@ -44,3 +45,22 @@ def test_appends_up_to_the_end(D, n):
     fd.append_rope_kv4(x[:, :, :2], x[:, :, 2:], small, seq_lens=lens % PAGE)
     assert fd.workspace_status() == 0
     assert torch.equal(pool, small)
+
+
+@pytest.mark.parametrize("n", [4000, 2 ** 31 - 15, 2 ** 31 - 1])
+def test_a_read_of_more_rows_than_a_sequence_can_have(n):
+    """One head, so that only the rows of tokens that exist are within the output's memory."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    kv = torch.randint(0, 120, (1, 1, 8, 18 * 64), dtype=torch.uint8, device="cuda", generator=g)
+    lens, starts = (torch.tensor([x], dtype=torch.int32, device="cuda") for x in (100, 30))
+    ko, vo = (torch.full((80, 64), 3.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    desc = fdb.Kv4Desc(layout=fdb.FD_KV_CONTIGUOUS, kv=kv.data_ptr(), capacity=128)
+    assert fd.load_library().fd_kv4_read(desc, ko.data_ptr(), vo.data_ptr(), fdb.FD_BF16, 1, n, 1, starts.data_ptr(),
+                                         lens.data_ptr(), 128, 64, ws.data_ptr(), 256,
+                                         torch.cuda.current_stream().cuda_stream) == fdb.FD_OK
+    want = fd.kv4_read(kv, 70, starts=starts)
+    torch.cuda.synchronize()
+    for got, w in zip((ko, vo), want):
+        assert torch.equal(got[:70].view(torch.int16), w[0, 0].view(torch.int16))
+        assert bool((got[70:] == 3.0).all())
