@@ -919,7 +919,7 @@ def kv4_read(kv4, n, *, starts=None, seq_lens=None, max_seq_len=None, block_tabl
              k_out=None, v_out=None, workspace: Optional[Workspace] = None, stream=None):
     """``fd_kv4_read``: tokens ``starts[b] + i``, ``i < n``, of a 4-bit cache as values ``[B, Hkv, n, D]``.
 
-    ``dtype`` bf16 (default) or fp32.  Rows at or past ``seq_lens[b]`` keep the contents of ``k_out`` and
+    ``dtype`` bf16 or fp32: that of ``k_out`` or ``v_out`` if given, else bf16.  Rows at or past ``seq_lens[b]`` keep the contents of ``k_out`` and
     ``v_out`` (zeros when they are made here).  Returns ``(k_out, v_out)``.
     """
     torch = _torch()
@@ -927,7 +927,8 @@ def kv4_read(kv4, n, *, starts=None, seq_lens=None, max_seq_len=None, block_tabl
     B = kv4.shape[0] if block_table is None else block_table.shape[0]
     desc, Hkv, D, tokens, index = _kv4_desc(kv4, block_table, B, k_exp, v_exp)
     if dtype is None:
-        dtype = torch.bfloat16 if k_out is None else k_out.dtype
+        given = k_out if k_out is not None else v_out
+        dtype = torch.bfloat16 if given is None else given.dtype
     dt = FD_BF16 if dtype is torch.bfloat16 else FD_F32 if dtype is torch.float32 else -1
     if dt < 0:
         raise ValueError(f"unsupported dtype {dtype}")
