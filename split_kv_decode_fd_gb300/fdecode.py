@@ -850,9 +850,9 @@ def _append(fn, where, desc, k_new, v_new, Hkv, D, tokens, index, cos, sin, q, q
         raise ValueError("cos and sin come together")
     cp = sp = max_pos = rot = 0
     if cos is not None:
+        cp, sp = _flat(cos, "cos", torch.float32, index), _flat(sin, "sin", torch.float32, index)
         if cos.dim() != 2 or cos.shape != sin.shape:
             raise ValueError("cos and sin must be [max_pos, rot_dim / 2]")
-        cp, sp = _flat(cos, "cos", torch.float32, index), _flat(sin, "sin", torch.float32, index)
         max_pos, rot = cos.shape[0], 2 * cos.shape[1]
     if rot_dim is not None and rot_dim != rot:
         raise ValueError(f"rot_dim {rot_dim} does not fit tables of {rot // 2} pairs")
@@ -924,7 +924,11 @@ def kv4_read(kv4, n, *, starts=None, seq_lens=None, max_seq_len=None, block_tabl
     """
     torch = _torch()
     index = _index_of(kv4, "kv4")
-    B = kv4.shape[0] if block_table is None else block_table.shape[0]
+    for t, name in ((block_table, "block_table"), (k_out, "k_out"), (v_out, "v_out")):
+        if t is not None:
+            _index_of(t, name)
+    lead = kv4.shape if block_table is None else block_table.shape
+    B = lead[0] if lead else 0
     desc, Hkv, D, tokens, index = _kv4_desc(kv4, block_table, B, k_exp, v_exp)
     if dtype is None:
         given = k_out if k_out is not None else v_out

@@ -22,3 +22,29 @@ def test_one_given_output_says_the_type_of_both(dtype, given):
     got = fd.kv4_read(kv, 64, **{given: out})
     assert got[given == "v_out"] is out and all(x.dtype is dtype for x in got)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_what_is_no_tensor_is_refused_as_a_value():
+    kv = cache()
+    x = torch.zeros((2, 1, 2, 64), device="cuda")
+    q = torch.zeros((2, 4, 64), device="cuda")
+    k = torch.zeros((2, 2, 64, 64), device="cuda")
+    cos = torch.zeros((64, 16), device="cuda")
+    flat = torch.zeros((18 * 64,), dtype=torch.uint8, device="cuda")
+    for name, call in {
+        "block_table": lambda: fd.kv4_read(kv, 4, block_table=[[0, 1], [2, 3]]),
+        "k_out": lambda: fd.kv4_read(kv, 4, k_out=[1.0]),
+        "v_out": lambda: fd.kv4_read(kv, 4, v_out=3.0),
+        "kv4": lambda: fd.kv4_read(flat[0], 4),
+        "cos": lambda: fd.append_rope_kv4(x, x, kv, cos.tolist(), cos, seq_lens=None),
+        "sin": lambda: fd.append_rope(x, x, k, k.clone(), cos, "sin"),
+    }.items():
+        with pytest.raises(ValueError, match=name):
+            call()
+    for call in (lambda: fd.kv4_read(flat, 4), lambda: fd.decode_kv4(q, flat), lambda: fd.append_rope_kv4(x, x, flat)):
+        with pytest.raises(ValueError, match="kv4"):
+            call()
+    for call in (lambda: fd.decode_kv4(q, kv, block_table=(0, 1)), lambda: fd.append_rope_kv4(x, x, kv, block_table=7),
+                 lambda: fd.append_rope(x, x, k, k.clone(), block_table=[0])):
+        with pytest.raises(ValueError, match="block_table"):
+            call()
