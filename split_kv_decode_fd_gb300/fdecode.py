@@ -685,6 +685,14 @@ def _opt(t, name, dtype, index, shape=None):
     return 0 if t is None else _flat(t, name, dtype, index, shape)
 
 
+def _i32(x, name):
+    """x as the library's int32 (ctypes would keep the lowest 32 bits)."""
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name} must fit in 32 bits, got {x}")
+    return x
+
+
 def _index_of(t, name):
     if not isinstance(t, _torch().Tensor) or t.get_device() < 0:
         raise ValueError(f"{name} must be a CUDA tensor (libfdecode has no CPU path)")
@@ -826,7 +834,8 @@ def _head_rows(t, name, B, n, heads, D, index, dtype):
 def _append(fn, where, desc, k_new, v_new, Hkv, D, tokens, index, cos, sin, q, q_out, rot_dim, interleaved, positions,
             new_lens, seq_lens, max_seq_len, workspace, stream):
     torch = _torch()
-    B, n = k_new.shape[0], k_new.shape[1]
+    B, n = k_new.shape[0], _i32(k_new.shape[1], "n of k_new")
+    max_seq_len = _i32(tokens - n if max_seq_len is None else max_seq_len, "max_seq_len")
     dtype = k_new.dtype
     dt = FD_BF16 if dtype is torch.bfloat16 else FD_F32 if dtype is torch.float32 else -1
     if dt < 0:
@@ -862,7 +871,7 @@ def _append(fn, where, desc, k_new, v_new, Hkv, D, tokens, index, cos, sin, q, q
         cp, sp, max_pos, rot, 1 if interleaved else 0))
     buf, handle = _scratch(workspace, index, 256, stream)
     _launch(index, handle, fn, where, rows, desc, qo, B, n, Hq, Hkv, _opt(seq_lens, "seq_lens", torch.int32, index, (B,)),
-            tokens - n if max_seq_len is None else int(max_seq_len), D, buf.data_ptr(), buf.numel())
+            max_seq_len, D, buf.data_ptr(), buf.numel())
     return q_out
 
 
@@ -936,7 +945,8 @@ def kv4_read(kv4, n, *, starts=None, seq_lens=None, max_seq_len=None, block_tabl
     dt = FD_BF16 if dtype is torch.bfloat16 else FD_F32 if dtype is torch.float32 else -1
     if dt < 0:
         raise ValueError(f"unsupported dtype {dtype}")
-    n = int(n)
+    n = _i32(n, "n of the rows")
+    max_seq_len = _i32(tokens if max_seq_len is None else max_seq_len, "max_seq_len")
     shape = (B, Hkv, n, D)
     if k_out is None:
         k_out = _made(torch.zeros, shape, dtype, kv4.device, stream)
@@ -945,8 +955,7 @@ def kv4_read(kv4, n, *, starts=None, seq_lens=None, max_seq_len=None, block_tabl
     buf, handle = _scratch(workspace, index, 256, stream)
     _launch(index, handle, _lib().fd_kv4_read, "fd_kv4_read", desc, _flat(k_out, "k_out", dtype, index, shape),
             _flat(v_out, "v_out", dtype, index, shape), dt, B, n, Hkv, _opt(starts, "starts", torch.int32, index, (B,)),
-            _opt(seq_lens, "seq_lens", torch.int32, index, (B,)), tokens if max_seq_len is None else int(max_seq_len), D,
-            buf.data_ptr(), buf.numel())
+            _opt(seq_lens, "seq_lens", torch.int32, index, (B,)), max_seq_len, D, buf.data_ptr(), buf.numel())
     return k_out, v_out
 
 
@@ -983,9 +992,10 @@ def decode_kv4(q, kv4, *, k_exp=0, v_exp=0, causal=True, seq_lens=None, max_seq_
     elif return_lse:
         lse = _made(torch.empty, shape[:-1], torch.float32, q.device, stream)
         lp = lse.data_ptr()
-    n_splits = int(n_splits)
+    n_splits = _i32(n_splits, "n_splits")
+    max_seq_len = _i32(tokens if max_seq_len is None else max_seq_len, "max_seq_len")
     buf, handle = _scratch(workspace, index, _decode_bytes(B, Hq * n_q, Hkv, D, n_splits, index), stream)
     _launch(index, handle, _lib().fd_decode_kv4, "fd_decode_kv4", at, n_q, 1 if causal else 0, desc, op, lp, B, Hq, Hkv,
-            _opt(seq_lens, "seq_lens", torch.int32, index, (B,)), tokens if max_seq_len is None else int(max_seq_len), D,
+            _opt(seq_lens, "seq_lens", torch.int32, index, (B,)), max_seq_len, D,
             1.0 / math.sqrt(D) if scale is None else float(scale), n_splits, buf.data_ptr(), buf.numel())
     return out, lse

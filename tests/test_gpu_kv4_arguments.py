@@ -48,3 +48,29 @@ def test_what_is_no_tensor_is_refused_as_a_value():
                  lambda: fd.append_rope(x, x, k, k.clone(), block_table=[0])):
         with pytest.raises(ValueError, match="block_table"):
             call()
+
+
+def test_numbers_past_32_bits_are_refused():
+    """They are not cut down to their lowest 32 bits."""
+    kv = cache(1, 1, 1 << 20)
+    table = torch.zeros((1, 4097), dtype=torch.int32, device="cuda")  # 2^32 + 2^20 places
+    q = torch.ones((1, 2, 64), device="cuda")
+    x = torch.zeros((1, 1, 1, 64), device="cuda")
+    big = 2 ** 32 + 16
+    small = cache(1, 1, 64)
+    for name, call in [
+        ("max_seq_len", lambda: fd.decode_kv4(q, kv, block_table=table)),
+        ("max_seq_len", lambda: fd.kv4_read(kv, 4, block_table=table)),
+        ("max_seq_len", lambda: fd.append_rope_kv4(x, x, kv, block_table=table)),
+        ("max_seq_len", lambda: fd.decode_kv4(q, small, max_seq_len=big)),
+        ("max_seq_len", lambda: fd.decode_kv4(q, small, max_seq_len=-big)),
+        ("max_seq_len", lambda: fd.kv4_read(small, 4, max_seq_len=big)),
+        ("max_seq_len", lambda: fd.append_rope_kv4(x, x, small, max_seq_len=big)),
+        ("n_splits", lambda: fd.decode_kv4(q, small, n_splits=big)),
+        ("n ", lambda: fd.kv4_read(small, big, k_out=x[:, :, :, :], v_out=x)),
+        ("n ", lambda: fd.append_rope_kv4(x.expand(1, big, 1, 64), x.expand(1, big, 1, 64), small)),
+    ]:
+        with pytest.raises(ValueError, match=name):
+            call()
+    out, _ = fd.decode_kv4(q, kv, block_table=table, max_seq_len=1 << 20)
+    assert torch.isfinite(out).all() and fd.workspace_status() == 0
