@@ -828,6 +828,8 @@ def _head_rows(t, name, B, n, heads, D, index, dtype):
     st = t.stride()
     if st[3] != 1:
         raise ValueError(f"the channels of {name} must be contiguous")
+    if (st[0] | st[1] | st[2]) & 7:  # the stride of a single entry may be anything
+        st = tuple(s if size > 1 else 0 for s, size in zip(st, shape))
     return st
 
 

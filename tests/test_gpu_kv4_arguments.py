@@ -74,3 +74,26 @@ def test_numbers_past_32_bits_are_refused():
             call()
     out, _ = fd.decode_kv4(q, kv, block_table=table, max_seq_len=1 << 20)
     assert torch.isfinite(out).all() and fd.workspace_status() == 0
+
+
+@pytest.mark.parametrize("four", [True, False])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_strides_of_single_entries_do_not_matter(four, dtype):
+    """A dimension of one entry is never stepped along, whatever its stride."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn((1, 1, 1, 64), dtype=torch.float32, device="cuda", generator=g).to(dtype)
+    odd = x.as_strided((1, 1, 1, 64), (5, 3, 7, 1))
+    got = []
+    for rows in (x, odd):
+        if four:
+            kv = torch.zeros((1, 1, 2, 18 * 64), dtype=torch.uint8, device="cuda")
+            q = fd.append_rope_kv4(rows, rows, kv, q=rows)
+        else:
+            kv = torch.zeros((2, 1, 1, 32, 64), device="cuda")
+            q = fd.append_rope(rows, rows, kv[0], kv[1], q=rows)
+        got.append((q, kv))
+    assert fd.workspace_status() == 0
+    assert all(torch.equal(a, b) for a, b in zip(*got)) and bool((got[0][1] != 0).any())
+    with pytest.raises(fd.FdError):
+        two = torch.zeros(200, dtype=dtype, device="cuda").as_strided((1, 2, 1, 64), (5, 65, 7, 1))
+        fd.append_rope_kv4(two, two, torch.zeros((1, 1, 2, 18 * 64), dtype=torch.uint8, device="cuda"))
