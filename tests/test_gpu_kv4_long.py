@@ -64,3 +64,32 @@ def test_a_read_of_more_rows_than_a_sequence_can_have(n):
     for got, w in zip((ko, vo), want):
         assert torch.equal(got[:70].view(torch.int16), w[0, 0].view(torch.int16))
         assert bool((got[70:] == 3.0).all())
+
+
+@pytest.mark.parametrize("D,Hq,n_q", [(64, 4, 1), (128, 8, 2)])
+def test_decode_of_the_longest_sequence(D, Hq, n_q):
+    """2^31 - 257 tokens, one page 2047 times and a part of it, against 64 bits.
+
+    With F = 2^31 / 128 / 8 / (CTAs) sums of O over the tiles of a group and as many of the weights, each rounded by 2^-25
+    of a sum that |v| bounds, and scores within (2^-21 + D 2^-24) A: out is off by (2 (that) + 4 F 2^-24 + 2^-19) max |v|.
+    """
+    pool, table = one_page(D, 1)
+    pool[..., 16 * D:] = pool[..., 16 * D:] % 17 + 0x28  # scales of 1 / 8 to 1 / 2
+    g = torch.Generator(device="cuda").manual_seed(3)
+    q = torch.randn((1, Hq, n_q, D), device="cuda", generator=g) * 0.3
+    lens = torch.tensor([END], dtype=torch.int32, device="cuda")
+    out, lse = fd.decode_kv4(q, pool, seq_lens=lens, max_seq_len=END, block_table=table)
+    assert fd.workspace_status() == 0
+    k, v = (x[0, 0].double() for x in fd.kv4_read(pool, PAGE, dtype=torch.float32))
+    times = torch.full((n_q, PAGE), float(END // PAGE), dtype=torch.float64, device="cuda")
+    for i in range(n_q):
+        times[i, :END % PAGE - (n_q - 1 - i)] += 1
+    w = torch.exp(q[0].double() @ k.t() * D ** -0.5) * times
+    L = w.sum(-1, keepdim=True)
+    want, wl = w @ v / L, L[..., 0].log()
+    A = (q[0].double().abs() @ k.abs().amax(0)) * D ** -0.5
+    es = (2.0 ** -21 + D * 2.0 ** -24) * A
+    F = 2 ** 31 / 128 / 8 / torch.cuda.get_device_properties(0).multi_processor_count
+    far = 4 * F * 2.0 ** -24 + 2.0 ** -19
+    assert bool(((out[0] - want).abs() <= (2 * es[..., None] + far) * v.abs().max()).all())
+    assert bool(((lse[0] - wl).abs() <= es + far + 2.0 ** -22 * wl.abs()).all())
