@@ -13,13 +13,13 @@
 // shared memory for bf16 and fp32 caches.  Two things count:
 //   - whole 32-byte sectors a store.  fp32 rows in 16-byte stores sent each
 //     sector to L2 twice: 8192 tokens of 32 + 8 heads of 128 channels took 51.9 us,
-//     46.9 to 48.5 with 32-byte stores; a read-back of 16384 tokens 31.8, now 29.7.
+//     46.9 to 48.5 with 32-byte stores; a read-back of 32768 tokens 31.8, now 29.8.
 //   - rows are loaded before the chain of lengths, pages and positions that says
 //     where they go, but after the length that says whether they are padding (55 %
 //     live of 8192 tokens: 36.8 us, 32.0 when padding is not loaded).
-// Measured: 8192 tokens into bf16 48 us (5.6 TB/s, 83 % of a copy's rate), the
-// same into 4 bits 51.6 us, 96 tokens 2.4 us (bf16) and 3.1 us (4 bits), a read-back
-// of 16384 tokens 29.7 us (5.8 TB/s, 85 %).
+// Measured on the device: 8192 tokens into bf16 48 us (5.7 TB/s, 84 % of a copy's rate), the
+// same into 4 bits 52 us, 64 tokens into bf16 2.4 us, 96 into 4 bits 3.2 us, a read-back
+// of 32768 tokens of 8 heads to bf16 29.8 us (5.8 TB/s, 85 %).
 #include "../../include/fdecode.h"
 #include "fd_kv4.cuh"
 
@@ -360,8 +360,10 @@ __device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat
 // The same for few tokens a sequence: a CTA of D threads takes a (sequence, KV head)
 // and its tokens one after another, a channel a thread; the bytes are the same.  Above,
 // eight threads would quantise a lone token, sixteen channels each, while the others wait.
-// 1, 2, 3, 4, 8 tokens of 96 sequences: 3.1, 4.9, 6.1, 7.5, 13.9 us; above 5.9, 7.9, 7.7,
-// 7.7, 8.7.  Of one sequence: 2.6, 3.6, 4.7, 5.7, 9.4; above 4.8 to 5.0.
+// 1, 2, 3, 4, 8 tokens of 96 sequences: 3.2, 4.6, 5.9, 7.4, 12.8 us; above 5.9, 7.4, 7.7,
+// 7.7, 8.6.  Of one sequence: 2.6, 3.5, 4.4, 5.5, 9.4; above 4.9 to 5.0.  D = 64, 96 sequences: 3.0, 4.2,
+// 5.5, 6.5, 10.8 against 5.5, 6.3, 6.4, 6.4, 6.8; one: 2.4, 3.3, 4.3, 5.5, 9.2 against 4.6 to 4.9.  1500
+// sequences of 3 and 4 tokens, D = 128: 68 and 87 against 78 and 85.
 constexpr int32_t kFewRows = 3;
 template <int D, class T>
 __global__ void __launch_bounds__(D) fd_append_kv4_few_kernel(const NewRows r, const Kv4View kv, int32_t kv_ctas) {

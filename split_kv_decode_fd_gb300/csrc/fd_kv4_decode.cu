@@ -13,22 +13,24 @@
 // lane is a row: the thread that owns the row widens its codes in registers
 // and stores them there.  code * scale has six significant bits and is exact in
 // fp16.  The B operands are small: q (once per piece) and p (per tile) in shared
-// memory, each as the sum of two fp16 numbers, hi and lo, that sit in columns of
-// their own; so the products are exact, and they add up in fp32.  q is K-major in
+// memory, each as the sum of two fp16 numbers, hi and lo (p's lo held 2^11 times up), that
+// sit in columns of their own; so the products are exact, and they add up in fp32.  q is K-major in
 // swizzled rows; p is N-major, so that a key's thread stores its heads as they lie
 // in registers, eight columns a 16-byte store.
 //
-// What bounds it: 9/16 byte per element from HBM (18 KB per tile for D = 128,
-// 790 cycles of an SM's share of the copy rate) against instruction issue: a tile is
-// 1300 instructions of widening (one conversion and one product for two elements) and,
-// with all waits and the softmax, some 3200, which is 800 of a scheduler's slots.  The
+// What bounds it: 9/16 byte per element from HBM (18 KB per tile for D = 128, 414 ns or
+// 857 cycles of an SM's share of a copy's rate, at 2070 MHz) and, next to it, instruction issue:
+// a tile is 1300 instructions of widening (one conversion and one product for two elements) and,
+// with all waits and the softmax, some 3200, which is 800 of a scheduler's slots.  A tile
+// takes 1060 cycles with 4 heads a group, so each is busy for some 80 % of it.  The
 // MMAs cost hardly any (mma.sync costs as many as the widening: measured 8.4 slots for
 // a 16x8x16 step), and with heads on the N axis their time does not grow with the group.
-// Measured, D = 128: 524288 tokens of 8 KV heads 124 us with 4 heads a group (4.9 TB/s, 72 %
-// of a copy's rate; 1050 cycles a tile), 135 with 8, 211 with 16 (the softmax of half the
-// heads takes a group of warps 1800 cycles).  A CTA's start takes 7000 cycles (lengths,
-// prefix sums, its place in the plan, q) and its end 4000 to 10000 (join), so that 131072
-// tokens take 40.5 us (3.7 TB/s), 16 ragged sequences of 1024 to 16384 tokens 32.
+// Measured, D = 128, 8 KV heads, as the slope of the time from 131072 to 1048576 tokens: 1060 cycles
+// a tile with 4 heads a group (5.5 TB/s, 81 % of a copy's rate), 1160 with 8, 1810 with 16 (the
+// softmax of half the heads takes a group of warps that long); with pages of 16 tokens 1070 and 1160.
+// What does not grow with the length (launch, a CTA's start, join) is 13 us with 4 heads, 14 with
+// 8, 20 with 16, so that 131072 tokens take 40.5 us (3.7 TB/s), 524288 tokens 123 (4.9 TB/s, 72 %), 135
+// and 209, 16 ragged sequences of 1024 to 16384 tokens 32.5.
 //
 // Twenty-eight warps:
 //   0      walks the plan, announces pieces, copies tiles into a ring of stages: all of
@@ -77,7 +79,7 @@ constexpr float kLoUp = 2048.f, kLoDown = 1.f / kLoUp;
 // Tiles of a group whose O products add up in tensor memory before their sum moves to
 // fp32 adds in shared memory.  An MMA's add drops bits instead of rounding, some 2^-25.6
 // of the sum each and all one way: with 27 tiles in a row the outputs of 128k tokens were
-// 4.2e-6 off (2-norm), with four 8.1e-7.  It costs 0.5 us of 40.
+// 4.2e-6 off (2-norm), with four 7.7e-7.  It costs 0.5 us of 40.
 constexpr uint32_t kFlush = 4;
 constexpr float kNoRef = -3.402823466e38f;  // of a head that has seen no key: no score lies below it
 
@@ -381,7 +383,7 @@ struct Waiter {
 // Copies of every second tile j, j + 2, ... of a paged piece, by one warp; tile j is the
 // CTA's tile g.  Returns how many it dealt with: a wait for a free stage may run out.
 // A warp starts a bulk copy in some 90 cycles, and pages of sixteen tokens need eight
-// a tile, so two warps take turns (524288 tokens of 8 heads 127 us, with one warp 168, with one
+// a tile, so two warps take turns (524288 tokens of 8 heads 126 us, with one warp 168, with one
 // warp's lanes and 16-byte copies 182; 64 sequences of 512 to 16384 tokens 105, 114 with one).
 // Blocks of a tile that follow one another in the pool go in one copy.
 template <int D, int kStages>
