@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import split_kv_decode_fd_gb300 as fd
+from split_kv_decode_fd_gb300 import fdecode as fdb
 
 from test_gpu_decode_kv4 import Case
 
@@ -121,7 +122,8 @@ def test_calls_on_two_streams_without_a_workspace(given):
         assert fd.workspace_status(stream=s) == 4 and fd.workspace_status() == 0
 
 
-def test_a_capture_without_a_workspace_takes_one_that_calls_have_sized():
+def test_a_capture_without_a_workspace_takes_one_that_calls_have_sized(monkeypatch):
+    monkeypatch.setattr(fdb, "_STREAM_WS", {})
     c = Case(3, 8, 2, 128, [900, 33, 512], page=16, seed=8)
     lens = torch.tensor(c.lens, dtype=torch.int32, device="cuda")
     s = torch.cuda.Stream()
