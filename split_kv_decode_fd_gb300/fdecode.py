@@ -275,6 +275,7 @@ class Workspace:
         return self.buf
 
     def _replace(self, nbytes, device):
+        device = _torch().empty(0, dtype=_torch().uint8, device=device).device  # "cuda" has an index from here on
         old = self._outgrown + ([] if self.buf is None else [self.buf])
         here = [b for b in old if b.device == device]
         buf = next((b for b in here if b.numel() >= nbytes), None)
@@ -887,7 +888,8 @@ def append_rope(k_new, v_new, k, v, cos=None, sin=None, *, q=None, q_out=None, r
     written in place.  ``cos``, ``sin`` fp32 ``[max_pos, rot_dim / 2]`` (None: no rotation).  Token ``j`` of sequence
     ``b`` goes to place ``seq_lens[b] + j``; with ``new_lens`` ``[B]`` only the last ``new_lens[b]`` of the ``n``
     rows are tokens.  ``seq_lens`` and ``max_seq_len`` are the lengths before the append.  ``positions``
-    ``[B, n]`` int32 replaces the places as rows of the tables.  Returns the rotated queries, fp32
+    ``[B, n]`` int32 replaces the places as rows of the tables.  Without ``workspace`` the stream's own is taken (see
+    ``Workspace``).  Returns the rotated queries, fp32
     ``[B, Hq, n, D]`` (``q_out`` if given, whose padding rows keep their contents; None without ``q``).
     """
     torch = _torch()
@@ -967,7 +969,8 @@ def decode_kv4(q, kv4, *, k_exp=0, v_exp=0, causal=True, seq_lens=None, max_seq_
     """``fd_decode_kv4``: decode attention over a 4-bit cache.
 
     q ``[B, Hq, D]`` or ``[B, Hq, n_q, D]`` fp32 (``n_q`` up to 64 rows, masked as in ``decode_rows``); ``kv4`` as made by
-    ``kv4_cache``.  Returns ``(out, lse)`` shaped like q and q without its last axis.
+    ``kv4_cache``.  Calls that may run at the same time need a ``workspace`` each; without one, each stream has its own (see
+    ``Workspace``).  Returns ``(out, lse)`` shaped like q and q without its last axis.
     """
     torch = _torch()
     index = _index_of(q, "q")

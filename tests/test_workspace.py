@@ -38,3 +38,12 @@ def test_a_buffer_that_is_large_enough_is_used_again():
     assert ws.get(900, CPU) is a
     meta = ws.get(500, torch.device("meta"))
     assert ws.get(800, CPU) is a and ws.get(400, torch.device("meta")) is meta
+
+
+def test_a_device_without_an_index_is_the_same_device():
+    ws = fd.Workspace()
+    a = ws.get(1000, torch.device("cpu"))
+    for _ in range(3):
+        assert ws.get(1000, torch.device("cpu", 0)).numel() >= 1000
+    assert len({ws.get(1000, d).data_ptr() for d in (CPU, CPU)}) == 1 and a.numel() == 1000
+    assert len(ws._outgrown) <= 1
