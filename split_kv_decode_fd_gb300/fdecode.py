@@ -255,8 +255,8 @@ class Workspace:
     that may run at the same time (on different streams) need a Workspace each.
     The default one, used when none is passed, is shared per device; append_rope,
     append_rope_kv4, kv4_read and decode_kv4 have one per stream.  A graph captured without a
-    Workspace takes the newest of these that is large enough: pass one to a graph that is
-    replayed beside other calls.
+    Workspace takes the newest of these that is large enough, or else the device's: pass one to
+    a graph that is replayed beside other calls.
 
     A buffer that has been outgrown stays allocated as long as the Workspace does: a graph
     captured with it holds its address.  Each is at least twice as large as the one before, so
@@ -737,8 +737,9 @@ def _grown(ws, index, nbytes, handle):
     torch = _torch()
     default = ws is None or ws is _STREAM_WS.get((index, handle))
     if torch.cuda.is_current_stream_capturing():
-        sized = [w for (i, _), w in list(_STREAM_WS.items())
-                 if default and i == index and w.buf is not None and w.buf.numel() >= nbytes]
+        spaces = [_default_workspace(torch.device("cuda", index))] if default else []
+        spaces += [w for (i, _), w in list(_STREAM_WS.items()) if default and i == index]
+        sized = [w for w in spaces if w.buf is not None and w.buf.numel() >= nbytes]
         if not sized:
             raise RuntimeError("the workspace is too small and cannot grow during a stream capture: run the call once "
                                "before the capture, or pass a Workspace that has been used at this size")

@@ -142,3 +142,20 @@ def test_a_capture_without_a_workspace_takes_one_that_calls_have_sized(monkeypat
         with torch.cuda.graph(torch.cuda.CUDAGraph()):
             c.run(n_splits=60000, seq_lens=lens, out=out, lse=lse)
     assert fd.workspace_status() == 0
+
+
+def test_a_capture_without_a_workspace_may_take_the_devices(monkeypatch):
+    """Only calls that share one per device have run before."""
+    monkeypatch.setattr(fdb, "_STREAM_WS", {})
+    c = Case(2, 8, 2, 128, [60, 33], seed=9)
+    bf16_run(c)()
+    x = torch.randn((2, 1, 2, 128), device="cuda")
+    kv, want = (fd.kv4_cache(2, 2, 64, 128) for _ in range(2))
+    lens = torch.tensor([5, 9], dtype=torch.int32, device="cuda")
+    fd.append_rope_kv4(x, x, want, seq_lens=lens, workspace=fd.Workspace())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fd.append_rope_kv4(x, x, kv, seq_lens=lens)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(kv, want) and bool((kv != 0).any()) and fd.workspace_status() == 0
