@@ -379,6 +379,47 @@ FD_API fd_status fd_decode_kv4(const float* q, int32_t n_q, int32_t causal, cons
                                int32_t max_seq_len, int32_t D, float scale, int32_t n_splits, void* workspace,
                                size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------ trees of drafted tokens
+ *
+ * A step that checks several drafted tokens at once, arranged in a tree: each
+ * sequence brings n rows, and with new_lens only the last m_b = new_lens[b] of
+ * them are tokens (as in fd_append_rope): row n - m_b + j is token j.  Token 0 is
+ * usually the last accepted token and the root of the drafts.  The tokens' keys and
+ * values are the last m_b places of the sequence in the cache: with P_b = L_b - m_b,
+ * token j has place P_b + j (fd_append_rope, with the depths as `positions`, writes
+ * them there).  Places below 0 do not exist.
+ *
+ * fd_decode_tree attends them, fd_verify_tree says which stay, fd_keep_rows moves
+ * the rows of those together in the cache.
+ */
+#define FD_MAX_DRAFTS 64
+
+typedef struct fd_tree_desc {
+  const int32_t* parents;       /* row by row: the number of the token's parent, below its own, or -1 */
+  int64_t parents_stride;       /* elements from sequence to sequence; 0: one tree for all */
+  const int32_t* new_lens;      /* [B] or NULL (= n); clamped to [0, n] */
+  int32_t n;                    /* rows of every sequence, 1 to FD_MAX_DRAFTS */
+} fd_tree_desc;
+
+/*
+ * Attention of the drafted tokens: token j sees every place below P_b, its
+ * ancestors in the tree, and itself.  (With parents j - 1 this is fd_decode_rows with
+ * causal = 1.)
+ *   q    [B, Hq, n, D] fp32; out [B, Hq, n, D]; lse [B, Hq, n] or NULL.  Rows of
+ *        padding are not written.  A token that sees no place gives out = 0, lse = -inf.
+ *   seq_lens / max_seq_len  L_b, the drafts included, as in fd_decode.
+ *   workspace  zero-filled once, fd_tree_workspace_bytes(B, Hq, Hkv, D, n, 0) bytes.
+ * Keys and values that a token does not see may be anything, NaN included.  A
+ * parent that is not below its token counts as -1 and is reported as FD_ERR_BAD_INDEX
+ * by fd_workspace_status, and so is a page outside the pool, which leaves the
+ * sequence's output undefined.  One launch, and a second one that joins the states
+ * where a sequence may be longer than a tile of 128 keys.
+ */
+FD_API size_t fd_tree_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_t n, int32_t num_sms);
+FD_API fd_status fd_decode_tree(const float* q, const fd_tree_desc* tree, const fd_kv_desc* kv, float* out, float* lse,
+                                int32_t B, int32_t Hq, int32_t Hkv, const int32_t* seq_lens, int32_t max_seq_len,
+                                int32_t D, float scale, void* workspace, size_t workspace_bytes, void* stream);
+
 /*
  * Split step only ("fd_split" of the walkthrough), with n_splits > 0 splits
  * per sequence of fd_split_size(max_seq_len, n_splits) tokens each.  Writes:

@@ -12,6 +12,7 @@ from .fdecode import (  # noqa: F401
     Kv4Desc,
     KvDesc,
     NewRows,
+    TreeDesc,
     Workspace,
     combine,
     decode,
@@ -21,6 +22,7 @@ from .fdecode import (  # noqa: F401
     append_rope,
     append_rope_kv4,
     decode_kv4,
+    decode_tree,
     kv4_block_bytes,
     kv4_cache,
     kv4_read,

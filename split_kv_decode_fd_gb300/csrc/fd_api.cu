@@ -14,6 +14,7 @@
 #include "fd_kv4.h"
 #include "fd_prefill.h"
 #include "fd_split.cuh"
+#include "fd_tree.h"
 
 using namespace fdk;
 
@@ -996,6 +997,122 @@ fd_status fd_decode_kv4(const float* q, int32_t n_q, int32_t causal, const fd_kv
   if (p.counters) return FD_OK;
   const cudaError_t e = launch_combine(D, p.o_part, p.m_part, p.l_part, out, lse, B * Hq, n_splits, s);
   return e == cudaSuccess ? FD_OK : FD_ERR_CUDA;
+}
+
+}  // extern "C"
+
+// --------------------------------------------------------------------------
+// Trees of drafted tokens.
+namespace {
+
+// Blocks of rows and shares of keys of fd_decode_tree on `sms` SMs (fd_tree.h); tiles: 128-key tiles of all (b, KV
+// head) pairs, or an upper bound.
+struct TreeSplit {
+  int32_t rows, nsub, ranges;
+};
+TreeSplit tree_split(int Hq, int Hkv, int n, int sms, int64_t tiles) {
+  TreeSplit t;
+  t.rows = Hq / Hkv * n;
+  t.nsub = ceil_div(t.rows, kTreeRows);
+  int64_t r = (int64_t)kTreeCtas * sms / t.nsub;  // CTAs that run at once
+  if (r > tiles) r = tiles;
+  t.ranges = (int32_t)(r < 1 ? 1 : r);
+  return t;
+}
+
+struct TreeLayout {
+  size_t joins, o, m, l, total;
+};
+TreeLayout tree_layout(const TreeSplit& t, int D) {
+  const size_t states = t.ranges > 1 ? (size_t)2 * t.ranges * t.nsub * kTreeRows : 0;
+  TreeLayout w;
+  w.joins = kHeaderBytes + kCounterBytes;  // behind the counters, which other calls expect at zero
+  w.o = w.joins + align_up((size_t)t.ranges * sizeof(TreeJoin));
+  w.m = w.o + align_up(states * D * 4);
+  w.l = w.m + align_up(states * 4);
+  w.total = w.l + align_up(states * 4);
+  return w;
+}
+
+fd_status check_tree(const fd_tree_desc* tree, int B, TreeView* out) {
+  if (!tree || !tree->parents || tree->n < 1 || B < 1) return FD_ERR_INVALID_ARG;
+  if (tree->n > kMaxDrafts) return FD_ERR_UNSUPPORTED;
+  if (tree->parents_stride != 0 && tree->parents_stride < tree->n) return FD_ERR_INVALID_ARG;
+  out->parents = tree->parents;
+  out->parents_stride = tree->parents_stride;
+  out->new_lens = tree->new_lens;
+  out->n = tree->n;
+  return FD_OK;
+}
+
+KvView view_of(const fd_kv_desc* kv, int Hkv) {
+  KvView v;
+  std::memset(&v, 0, sizeof(v));
+  v.k = const_cast<void*>(kv->k);
+  v.v = const_cast<void*>(kv->v);
+  v.block_table = kv->block_table;
+  v.capacity = kv->capacity;
+  v.Hkv = Hkv;
+  v.paged = kv->layout == FD_KV_PAGED;
+  v.page_size = kv->page_size;
+  v.max_pages = kv->max_pages_per_seq;
+  v.num_pages = kv->num_pages;
+  return v;
+}
+
+static_assert(kMaxDrafts == FD_MAX_DRAFTS, "header and kernels agree");
+
+}  // namespace
+
+extern "C" {
+
+size_t fd_tree_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_t n, int32_t num_sms) {
+  if (check_shape(B, Hq, Hkv, D) != FD_OK || n < 1 || n > kMaxDrafts || (int64_t)Hq * n > ((int64_t)1 << 24)) return 0;
+  int sms = num_sms;
+  if (sms <= 0 && !sm_count(&sms)) return 0;
+  return tree_layout(tree_split(Hq, Hkv, n, sms, INT64_MAX), D).total;
+}
+
+fd_status fd_decode_tree(const float* q, const fd_tree_desc* tree, const fd_kv_desc* kv, float* out, float* lse,
+                         int32_t B, int32_t Hq, int32_t Hkv, const int32_t* seq_lens, int32_t max_seq_len, int32_t D,
+                         float scale, void* workspace, size_t workspace_bytes, void* stream) {
+  TreeParams p;
+  std::memset(&p, 0, sizeof(p));
+  fd_status st = check_tree(tree, B, &p.tree);
+  if (st != FD_OK) return st;
+  if ((st = check_shape(B, Hq, Hkv, D)) != FD_OK) return st;
+  if ((int64_t)Hq * tree->n > ((int64_t)1 << 24)) return FD_ERR_UNSUPPORTED;
+  if (!q || !out || !workspace || !aligned16(q) || !aligned16(out) || !aligned16(workspace)) return FD_ERR_INVALID_ARG;
+  if ((st = check_kv(kv, B, Hkv, max_seq_len)) != FD_OK) return st;
+  if (max_seq_len > INT32_MAX - 2 * kPlanTile) return FD_ERR_UNSUPPORTED;  // a tile's end is an int32
+  int sms = 0;
+  if (!sm_count(&sms)) return FD_ERR_CUDA;
+  const TreeSplit t = tree_split(Hq, Hkv, tree->n, sms, (int64_t)B * Hkv * ceil_div(max_seq_len, kPlanTile));
+  const TreeLayout w = tree_layout(t, D);
+  if (workspace_bytes < w.total) return FD_ERR_WORKSPACE_TOO_SMALL;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.q = q;
+  p.out = out;
+  p.lse = lse;
+  p.seq_lens = seq_lens;
+  p.kv = view_of(kv, Hkv);
+  p.joins = reinterpret_cast<TreeJoin*>(ws + w.joins);
+  p.o_part = reinterpret_cast<float*>(ws + w.o);
+  p.m_part = reinterpret_cast<float*>(ws + w.m);
+  p.l_part = reinterpret_cast<float*>(ws + w.l);
+  p.err = reinterpret_cast<unsigned*>(ws);
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.g = Hq / Hkv;
+  p.rows = t.rows;
+  p.nsub = t.nsub;
+  p.ranges = t.ranges;
+  p.max_len = max_seq_len;
+  p.qk_scale = (float)((double)scale * 1.4426950408889634);
+  p.wait_ns = (uint64_t)g_wait_ns.load(std::memory_order_relaxed);
+  p.stall_u = g_stall_it.load(std::memory_order_relaxed);
+  return launch_tree(D, kv->dtype == FD_F32, p, (cudaStream_t)stream) == cudaSuccess ? FD_OK : FD_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -1,0 +1,231 @@
+// fd_tree.cuh -- what the tree attention kernels share: what a row sees, the
+// walk over a share of the keys, and where a piece's states go.
+#pragma once
+
+#include "fd_device.cuh"
+#include "fd_tree.h"
+
+namespace fdk {
+
+// Cost units (kTileUnits = 4 a tile of 128 keys) that a piece costs a CTA besides its tiles.
+constexpr int kTreePieceUnits = 6;
+
+__device__ __forceinline__ int32_t tree_len(const TreeParams& p, int32_t b) {
+  return p.seq_lens ? clamp_len(__ldg(p.seq_lens + b), p.max_len) : p.max_len;
+}
+__device__ __forceinline__ int32_t tree_tokens(const TreeView& t, int32_t b) {
+  return t.new_lens ? clamp_len(__ldg(t.new_lens + b), t.n) : t.n;
+}
+
+// The ancestors of every token and itself, as words of bits: lane l of the warp
+// holds those of tokens l and l + 32.  Twice as far up in each round, as a chain of
+// 64 tokens would otherwise be 64 loads one after another.  A parent that is not
+// below its token counts as none and is reported; m: the sequence's tokens.
+struct Ancestors {
+  uint64_t lo, hi;
+  // token j's, for any j of any lane (a warp-collective call)
+  __device__ __forceinline__ uint64_t of(int32_t j) const {
+    const uint64_t a = __shfl_sync(0xffffffffu, lo, j & 31), b = __shfl_sync(0xffffffffu, hi, j & 31);
+    return j < 0 ? 0 : (j < 32 ? a : b);
+  }
+};
+__device__ __forceinline__ Ancestors tree_ancestors(const TreeView& t, int32_t b, int32_t m, unsigned* err) {
+  const int32_t lane = threadIdx.x & 31;
+  const int32_t* parents = t.parents + b * t.parents_stride + (t.n - m);
+  int32_t x[2];
+  Ancestors a;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int32_t j = lane + 32 * i;
+    x[i] = j < m ? __ldg(parents + j) : -1;
+    if (x[i] < -1 || x[i] >= j) {
+      if (x[i] != -1) atomicOr(err, kErrBadIndex);
+      x[i] = -1;
+    }
+  }
+  a.lo = lane < m ? 1ull << lane : 0;
+  a.hi = lane + 32 < m ? 1ull << (lane + 32) : 0;
+  while (__any_sync(0xffffffffu, x[0] >= 0 || x[1] >= 0)) {
+    const uint64_t up0 = a.of(x[0]), up1 = a.of(x[1]);
+    int32_t y[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int32_t s = __shfl_sync(0xffffffffu, x[0], x[i] & 31), l = __shfl_sync(0xffffffffu, x[1], x[i] & 31);
+      y[i] = x[i] < 0 ? -1 : (x[i] < 32 ? s : l);
+    }
+    a.lo |= up0;
+    a.hi |= up1;
+    x[0] = y[0];
+    x[1] = y[1];
+  }
+  return a;
+}
+
+// Bits [0, 128) of a tile of keys that starts at place t0: which of them a row sees
+// that sees every place below P, and place P + a for each bit a of `anc`.  The bits
+// of places at or past the sequence's end are 0, as anc has none there.
+struct TileMask {
+  uint32_t w[4];
+};
+__device__ __forceinline__ TileMask tile_mask(int32_t P, uint64_t anc, int32_t t0) {
+  TileMask t;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int32_t d = P - (t0 + 32 * i);  // where bit 0 of anc falls in this word
+    const uint32_t before = d <= 0 ? 0u : (d >= 32 ? 0xffffffffu : (1u << d) - 1u);
+    uint32_t own;
+    if (d >= 32 || d <= -64)
+      own = 0u;
+    else if (d >= 0)
+      own = (uint32_t)(anc << d);
+    else
+      own = (uint32_t)(anc >> -d);
+    t.w[i] = before | own;
+  }
+  return t;
+}
+
+// A run of keys of one (sequence, KV head).
+struct TreePiece {
+  int32_t b, h;
+  int32_t begin, end;  // places, `end` clipped to the length
+  int32_t len, m;      // the sequence's length and its tokens
+  int32_t slot;        // -1: the piece is the whole pair
+  int32_t last;        // of a piece that begins a pair: the last share that holds the pair
+};
+
+// The pieces of one share, walked by one warp (all lanes alike).  Sequences
+// without keys or without tokens cost nothing and have no piece.
+struct TreeWalk {
+  const TreeParams& p;
+  int64_t units;
+  int32_t used, range;
+  int64_t pos, end;
+  int32_t b, h, len, m, tiles;
+  int64_t v, u;  // first unit of the pair, units of a pair of its sequence
+
+  __device__ __forceinline__ bool uniform() const { return !p.seq_lens && !p.tree.new_lens; }
+  __device__ __forceinline__ int32_t piece_units() const { return p.seq_lens ? kTreePieceUnits : 0; }
+  __device__ __forceinline__ int64_t units_of(int32_t bb) const {
+    if (tree_tokens(p.tree, bb) == 0) return 0;
+    return pair_units(ceil_div(tree_len(p, bb), kPlanTile), piece_units());
+  }
+  __device__ __forceinline__ void load(int32_t bb) {
+    b = bb;
+    len = tree_len(p, bb);
+    m = tree_tokens(p.tree, bb);
+    tiles = m > 0 ? ceil_div(len, kPlanTile) : 0;
+    u = pair_units(tiles, piece_units());
+  }
+
+  __device__ __forceinline__ TreeWalk(const TreeParams& p_, int32_t range_) : p(p_), range(range_) {
+    const int lane = threadIdx.x & 31;
+    pos = end = 0;
+    b = h = 0;
+    v = 0;
+    if (uniform()) {
+      load(0);
+      units = (int64_t)p.B * p.Hkv * u;
+    } else {
+      int64_t sum = 0;
+      for (int32_t i = lane; i < p.B; i += 32) sum += units_of(i);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      units = sum * p.Hkv;
+    }
+    used = units > 0 ? balanced_ctas(units, p.ranges) : 0;
+    if (range >= used) return;
+    pos = range_begin(units, used, range);
+    end = range_begin(units, used, range + 1);
+    // the sequence that holds `pos`
+    if (uniform()) {
+      const int64_t i = div_floor(pos, u);
+      b = (int32_t)(i / p.Hkv);
+      h = (int32_t)(i % p.Hkv);
+      v = i * u;
+      return;
+    }
+    int64_t before = 0;
+    for (int32_t i0 = 0; i0 < p.B; i0 += 32) {
+      int64_t mine = i0 + lane < p.B ? units_of(i0 + lane) : 0;
+      int64_t incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, (before + incl) * p.Hkv > pos);
+      if (past) {
+        const int l = __ffs(past) - 1;
+        const int64_t start = before + __shfl_sync(0xffffffffu, incl - mine, l);
+        load(i0 + l);
+        h = (int32_t)div_floor(pos - start * p.Hkv, u);
+        v = start * p.Hkv + (int64_t)h * u;
+        return;
+      }
+      before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    pos = end;  // not reached: pos is below the units in all
+  }
+
+  // The next piece; false when none is left.
+  __device__ __forceinline__ bool next(TreePiece& pc) {
+    while (pos < end) {
+      const int64_t pend = v + u;
+      const int64_t stop = end < pend ? end : pend;
+      const int32_t lo = first_tile_at(pos, v, piece_units());
+      int32_t hi = first_tile_at(stop, v, piece_units());
+      hi = hi < tiles ? hi : tiles;
+      bool found = hi > lo;
+      if (found) {
+        pc.b = b;
+        pc.h = h;
+        pc.begin = lo * kPlanTile;
+        pc.end = hi < tiles ? hi * kPlanTile : len;
+        pc.len = len;
+        pc.m = m;
+        pc.slot = lo == 0 && hi == tiles ? -1 : 2 * range + (lo == 0 ? 1 : 0);
+        pc.last = cta_of_unit(units, used, v + piece_units() + (int64_t)kTileUnits * (tiles - 1));
+      }
+      pos = stop;
+      if (pos == pend) {
+        v = pend;
+        if (++h == p.Hkv) {
+          h = 0;
+          if (uniform()) {
+            ++b;
+          } else if (pos < end) {  // the walk ends inside the units in all, so a sequence with units follows
+            int32_t bb = b + 1;
+            load(bb);
+            while (u == 0 && bb < p.B - 1) load(++bb);
+          }
+        }
+      }
+      if (found) return true;
+    }
+    return false;
+  }
+};
+
+// Sequences without keys: no share holds them, and the rows of their tokens get
+// out = 0, lse = -inf from the CTAs of share b % ranges.
+template <int D, int Rows>
+__device__ __forceinline__ void tree_empty_rows(const TreeParams& p, int32_t range, int32_t sub, int tid, int threads) {
+  for (int32_t b = range; b < p.B; b += p.ranges) {
+    if (tree_len(p, b) != 0) continue;
+    const int32_t pad = p.tree.n - tree_tokens(p.tree, b);
+    const int32_t r0 = sub * Rows, r1 = r0 + Rows < p.rows ? r0 + Rows : p.rows;
+    for (int64_t i = tid; i < (int64_t)p.Hkv * (r1 - r0); i += threads) {
+      const int32_t row = r0 + (int32_t)(i % (r1 - r0));
+      if (row % p.tree.n < pad) continue;
+      const int64_t at = ((int64_t)b * p.Hkv + i / (r1 - r0)) * p.rows + row;
+#pragma unroll 1
+      for (int d = 0; d < D; d += 4) *reinterpret_cast<float4*>(p.out + at * D + d) = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (p.lse) p.lse[at] = -INFINITY;
+    }
+  }
+}
+
+constexpr float kTreeLn2 = 0.6931471805599453f;
+
+}  // namespace fdk

@@ -1,0 +1,73 @@
+// fd_tree.h -- a step with a tree of drafted tokens: parameters and launches of
+// the kernels that attend the drafts, decide which stay and move the rows of
+// those together in the cache.
+//
+// Every sequence b brings n rows of drafts; with new_lens only the last
+// m_b = new_lens[b] of them are tokens, and row n - m_b + j is token j.  The
+// tokens' keys and values are the last m_b places of the sequence: token j has
+// place P_b + j, P_b = L_b - m_b.  parents gives, row by row, the number of a
+// token's parent, which is below its own, or -1.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "fd_kv4.h"
+#include "fd_plan.h"
+
+namespace fdk {
+
+constexpr int kMaxDrafts = 64;  // rows of a window: an ancestor set is one 64-bit word
+
+struct TreeView {
+  const int32_t* parents;
+  int64_t parents_stride;    // elements from sequence to sequence (0: one tree for all)
+  const int32_t* new_lens;   // [B] or null (n)
+  int32_t n;
+};
+
+// Attention: the g * n rows of a KV head (head by head, token rows within a head,
+// as q [B, Hq, n, D] has them) share its keys and values.  They are cut into
+// `nsub` blocks of kTreeRows rows, and the keys of all (b, KV head) pairs into
+// `ranges` shares of equal cost (BalancedWalk's line of cost units): CTA
+// r * nsub + s takes share r for block s, so that the blocks of a KV head read the
+// same keys at the same time, from memory once and then from L2.
+//
+// A pair that lies within a share is finished there.  Otherwise its states go
+// to o_part, m_part (base 2) and l_part, and a second kernel joins them.  A
+// share has at most two unfinished pieces: one that goes on with a pair begun in
+// an earlier share (slot 2 r), and one that begins a pair (slot 2 r + 1, whose
+// place in joins says which pair it is and where it ends).  Their number does not
+// grow with the batch.
+struct TreeJoin {
+  int32_t b, h, last;  // sequence (-1: none), KV head, last share that holds the pair
+  int32_t pad;
+};
+
+struct TreeParams {
+  const float* q;              // [B, Hq, n, D]
+  float* out;                  // [B, Hq, n, D]
+  float* lse;                  // [B, Hq, n] natural log, or null
+  const int32_t* seq_lens;     // [B] or null (max_len)
+  KvView kv;
+  TreeView tree;
+  float* o_part;               // [2 ranges][nsub][kTreeRows][D]
+  float* m_part;               // [2 ranges][nsub][kTreeRows]
+  float* l_part;
+  TreeJoin* joins;             // [ranges]
+  unsigned* err;
+  int32_t B, Hq, Hkv, g;
+  int32_t rows;                // g * n
+  int32_t nsub, ranges;
+  int32_t max_len;
+  float qk_scale;              // scale * log2(e)
+  uint64_t wait_ns;            // limit of every wait (0: the default)
+  int32_t stall_u;             // testing hook: the copy that every CTA skips, or -1
+};
+
+constexpr int kTreeRows = 32;  // rows per CTA
+constexpr int kTreeCtas = 2;   // CTAs per SM
+
+cudaError_t launch_tree(int D, bool f32, const TreeParams& p, cudaStream_t stream);
+
+}  // namespace fdk

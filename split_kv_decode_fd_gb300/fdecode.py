@@ -21,6 +21,7 @@ __all__ = [
     "FdError", "KvDesc", "library_path", "load_library", "workspace_bytes", "split_size", "plan_pieces",
     "Workspace", "decode", "decode_rows", "append_decode", "prefill", "attend", "attend_backend", "decode_host", "HostDecoder", "decode_static", "static_status", "split_partial", "combine", "workspace_status",
     "NewRows", "Kv4Desc", "append_rope", "append_rope_kv4", "kv4_block_bytes", "kv4_cache", "kv4_read", "decode_kv4",
+    "TreeDesc", "decode_tree",
 ]
 
 FD_OK, FD_ERR_INVALID_ARG, FD_ERR_UNSUPPORTED, FD_ERR_WORKSPACE_TOO_SMALL = 0, 1, 2, 3
@@ -93,6 +94,17 @@ class Kv4Desc(ctypes.Structure):
     ]
 
 
+class TreeDesc(ctypes.Structure):
+    """``fd_tree_desc``: the drafted tokens of every sequence."""
+
+    _fields_ = [
+        ("parents", ctypes.c_void_p),
+        ("parents_stride", ctypes.c_int64),
+        ("new_lens", ctypes.c_void_p),
+        ("n", ctypes.c_int32),
+    ]
+
+
 def library_path() -> str:
     return os.environ.get("FDECODE_LIB", os.path.join(_HERE, "libfdecode.so"))
 
@@ -148,6 +160,9 @@ def load_library(path: Optional[str] = None):
                                            c_sz, vp]),
             "fd_decode_kv4": (ctypes.c_int, [vp, c_i32, c_i32, kv4p, vp, vp, c_i32, c_i32, c_i32, vp, c_i32, c_i32,
                                              f32, c_i32, vp, c_sz, vp]),
+            "fd_tree_workspace_bytes": (c_sz, [c_i32, c_i32, c_i32, c_i32, c_i32, c_i32]),
+            "fd_decode_tree": (ctypes.c_int, [vp, ctypes.POINTER(TreeDesc), kvp, vp, vp, c_i32, c_i32, c_i32, vp, c_i32,
+                                              c_i32, f32, vp, c_sz, vp]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -663,7 +678,9 @@ def _word(ws, stream):
 _ROWS = struct.Struct("@i4x3P9q4P3i4x")
 _KV = struct.Struct("@2i2PqP3i4x")
 _KV4 = struct.Struct("@i4xPqP5i4x")
-assert _ROWS.size == ctypes.sizeof(NewRows) and _KV.size == ctypes.sizeof(KvDesc) and _KV4.size == ctypes.sizeof(Kv4Desc)
+_TREE = struct.Struct("@PqPi4x")
+assert _TREE.size == ctypes.sizeof(TreeDesc) and _ROWS.size == ctypes.sizeof(NewRows)
+assert _KV.size == ctypes.sizeof(KvDesc) and _KV4.size == ctypes.sizeof(Kv4Desc)
 
 
 def _flat(t, name, dtype, index, shape=None):
@@ -797,6 +814,29 @@ def _table(block_table, B, index):
     return at, block_table.shape[1]
 
 
+def _cache_desc(k, v, block_table, B):
+    """Descriptor, Hkv, D, tokens per sequence and device index of a bf16 or fp32 cache."""
+    torch = _torch()
+    index = _index_of(k, "k")
+    if k.dim() != 4:
+        raise ValueError("k and v must be [B, Hkv, T, D] or [num_pages, Hkv, page, D]")
+    shape, dtype = k.shape, k.dtype
+    dt = FD_BF16 if dtype is torch.bfloat16 else FD_F32 if dtype is torch.float32 else -1
+    if dt < 0:
+        raise ValueError(f"unsupported KV dtype {dtype}")
+    at, vt = _flat(k, "k", dtype, index), _flat(v, "v", dtype, index, shape)
+    tokens = shape[2]
+    if block_table is None:
+        if shape[0] != B:
+            raise ValueError(f"a contiguous cache must hold {B} sequences, got {shape[0]}")
+        d = _KV.pack(FD_KV_CONTIGUOUS, dt, at, vt, tokens, 0, 0, 0, 0)
+    else:
+        table, pages = _table(block_table, B, index)
+        d = _KV.pack(FD_KV_PAGED, dt, at, vt, 0, table, pages, tokens, shape[0])
+        tokens *= pages
+    return KvDesc.from_buffer_copy(d), shape[1], shape[3], tokens, index
+
+
 def _kv4_desc(kv4, block_table, B, k_exp, v_exp):
     """Descriptor, Hkv, D, tokens per sequence and device index of a 4-bit cache tensor."""
     index = _index_of(kv4, "kv4")
@@ -893,29 +933,11 @@ def append_rope(k_new, v_new, k, v, cos=None, sin=None, *, q=None, q_out=None, r
     ``Workspace``).  Returns the rotated queries, fp32
     ``[B, Hq, n, D]`` (``q_out`` if given, whose padding rows keep their contents; None without ``q``).
     """
-    torch = _torch()
-    index = _index_of(k, "k")
-    if not isinstance(k_new, torch.Tensor) or k_new.dim() != 4:
+    if not isinstance(k_new, _torch().Tensor) or k_new.dim() != 4:
         raise ValueError("k_new must be [B, n, Hkv, D]")
-    if k.dim() != 4:
-        raise ValueError("k and v must be [B, Hkv, T, D] or [num_pages, Hkv, page, D]")
-    shape, dtype, B = k.shape, k.dtype, k_new.shape[0]
-    dt = FD_BF16 if dtype is torch.bfloat16 else FD_F32 if dtype is torch.float32 else -1
-    if dt < 0:
-        raise ValueError(f"unsupported KV dtype {dtype}")
-    at, vt = _flat(k, "k", dtype, index), _flat(v, "v", dtype, index, shape)
-    tokens = shape[2]
-    if block_table is None:
-        if shape[0] != B:
-            raise ValueError(f"a contiguous cache must hold {B} sequences, got {shape[0]}")
-        d = _KV.pack(FD_KV_CONTIGUOUS, dt, at, vt, tokens, 0, 0, 0, 0)
-    else:
-        table, pages = _table(block_table, B, index)
-        d = _KV.pack(FD_KV_PAGED, dt, at, vt, 0, table, pages, tokens, shape[0])
-        tokens *= pages
-    return _append(_lib().fd_append_rope, "fd_append_rope", KvDesc.from_buffer_copy(d), k_new, v_new, shape[1], shape[3],
-                   tokens, index, cos, sin, q, q_out, rot_dim, interleaved, positions, new_lens, seq_lens, max_seq_len,
-                   workspace, stream)
+    desc, Hkv, D, tokens, index = _cache_desc(k, v, block_table, k_new.shape[0])
+    return _append(_lib().fd_append_rope, "fd_append_rope", desc, k_new, v_new, Hkv, D, tokens, index, cos, sin, q, q_out,
+                   rot_dim, interleaved, positions, new_lens, seq_lens, max_seq_len, workspace, stream)
 
 
 def append_rope_kv4(k_new, v_new, kv4, cos=None, sin=None, *, k_exp=0, v_exp=0, q=None, q_out=None, rot_dim=None,
@@ -1004,4 +1026,68 @@ def decode_kv4(q, kv4, *, k_exp=0, v_exp=0, causal=True, seq_lens=None, max_seq_
     _launch(index, handle, _lib().fd_decode_kv4, "fd_decode_kv4", at, n_q, 1 if causal else 0, desc, op, lp, B, Hq, Hkv,
             _opt(seq_lens, "seq_lens", torch.int32, index, (B,)), max_seq_len, D,
             1.0 / math.sqrt(D) if scale is None else float(scale), n_splits, buf.data_ptr(), buf.numel())
+    return out, lse
+
+
+# ------------------------------------------------------------------ trees of drafted tokens
+@functools.lru_cache(maxsize=256)
+def _tree_bytes(B, Hq, Hkv, D, n, index):
+    """``fd_tree_workspace_bytes`` on device ``index``."""
+    with _torch().cuda.device(index):
+        nbytes = int(_lib().fd_tree_workspace_bytes(B, Hq, Hkv, D, n, 0))
+    if nbytes == 0:
+        raise FdError(FD_ERR_INVALID_ARG, "fd_tree_workspace_bytes")
+    return nbytes
+
+
+def _tree_desc(parents, new_lens, B, n, index):
+    """Descriptor of the drafts of B sequences; ``parents`` is ``[B, n]`` or, for one tree, ``[n]``."""
+    torch = _torch()
+    shape = (n,) if isinstance(parents, torch.Tensor) and parents.dim() == 1 else (B, n)
+    at = _flat(parents, "parents", torch.int32, index, shape)
+    return TreeDesc.from_buffer_copy(_TREE.pack(at, n if len(shape) == 2 else 0,
+                                                _opt(new_lens, "new_lens", torch.int32, index, (B,)), n))
+
+
+def decode_tree(q, k, v, parents, *, new_lens=None, seq_lens=None, max_seq_len=None, block_table=None, scale=None, out=None,
+                lse=None, return_lse=True, workspace: Optional[Workspace] = None, stream=None):
+    """``fd_decode_tree``: attention of a tree of drafted tokens over the cache that holds them in its last places.
+
+    q ``[B, Hq, n, D]`` fp32, ``n`` up to 64; ``k``, ``v`` are the cache as in ``decode`` (bf16 or fp32).  ``parents``
+    ``[B, n]`` int32 (or ``[n]``, one tree for all sequences) gives the number of each token's parent, below its own, or -1; a
+    token sees what comes before the drafts, its ancestors and itself.  ``new_lens`` ``[B]``: only the last ``new_lens[b]`` of the
+    ``n`` rows are tokens, numbered from 0 there.  ``seq_lens`` count the drafts.  Calls that may run at the same time
+    need a ``workspace`` each; without one, each stream has its own (see ``Workspace``).  Returns ``(out [B, Hq, n, D], lse
+    [B, Hq, n])``; padding rows keep what ``out`` and ``lse`` hold (zeros when they are made here).
+    """
+    torch = _torch()
+    index = _index_of(q, "q")
+    at = _flat(q, "q", torch.float32, index)
+    shape = q.shape
+    if len(shape) != 4:
+        raise ValueError("q must be [B, Hq, n, D]")
+    B, Hq, n, D = shape
+    desc, Hkv, kv_D, tokens, on = _cache_desc(k, v, block_table, B)
+    if kv_D != D:
+        raise ValueError("head_dim of q and k differ")
+    if on != index:
+        raise ValueError("q and k must be on one device")
+    tree = _tree_desc(parents, new_lens, B, n, index)
+    make = torch.empty if new_lens is None else torch.zeros
+    if out is None:
+        out = _made(make, shape, torch.float32, q.device, stream)
+        op = out.data_ptr()
+    else:
+        op = _flat(out, "out", torch.float32, index, shape)
+    lp = 0
+    if lse is not None:
+        lp = _flat(lse, "lse", torch.float32, index, shape[:-1])
+    elif return_lse:
+        lse = _made(make, shape[:-1], torch.float32, q.device, stream)
+        lp = lse.data_ptr()
+    max_seq_len = _i32(tokens if max_seq_len is None else max_seq_len, "max_seq_len")
+    buf, handle = _scratch(workspace, index, _tree_bytes(B, Hq, Hkv, D, n, index), stream)
+    _launch(index, handle, _lib().fd_decode_tree, "fd_decode_tree", at, tree, desc, op, lp, B, Hq, Hkv,
+            _opt(seq_lens, "seq_lens", torch.int32, index, (B,)), max_seq_len, D,
+            1.0 / math.sqrt(D) if scale is None else float(scale), buf.data_ptr(), buf.numel())
     return out, lse
