@@ -421,6 +421,56 @@ FD_API fd_status fd_decode_tree(const float* q, const fd_tree_desc* tree, const 
                                 int32_t D, float scale, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Which drafts stay.  The walk starts at token 0, which stays.  Where it stands at a
+ * token with the target's probabilities p and the draft's q (those of the word after the
+ * token), the token's children are asked in the order of their numbers: the child with word x and
+ * random number u stays, and the walk goes on there, if
+ *     u Z q(x) < r(x),    r = max(p - c q, 0),   c = 0, Z = 1 at first;
+ * when it does not, c grows by Z and Z becomes the sum of r.  That is the rule that
+ * keeps the target's distribution when the children are drawn from q one by one: r / Z is what is
+ * left of the target.  Without `draft` the children are given, not drawn: u Z < r(x), with
+ * r = p but 0 at refused words, and Z = 1 less their probabilities.  Where no child
+ * stays, the next token is the first word v with r(0) + ... + r(v) > u_0 * sum r (of p
+ * itself if nothing is left), u_0 being token 0's random number.
+ *   tokens     [B, n] int32 words of the drafts, row by row (token 0's is not used).
+ *   uniforms   [B, n] fp32 random numbers in [0, 1).
+ *   target     p of token j is V probabilities in FD_F32 or FD_BF16 (dtype) at element
+ *              b * target_stride[0] + (n - m_b + j) * target_stride[1]; draft likewise, or
+ *              NULL.  They need not be normalised to the last bit; what is not above 0, NaN too,
+ *              counts as 0.  Rows need no alignment beyond their type's (16 bytes are
+ *              faster).  The draft's rows of tokens without children are not read.
+ *   path       [B, n]: the numbers of the tokens that stay, token 0 first, then -1.
+ *   count      [B]: how many they are.   next_token [B].  A sequence without tokens gets 0 and -1,
+ *              and -1 stands for a target row without a positive probability.
+ *   Sums are held to about 48 bits, so that a random number that decides between two words or
+ *   on a child is one that is within some 2^-44 of the border before another outcome than that of exact sums is had.
+ *   workspace  at least 256 bytes, zero-filled once, of which only the error word is used.
+ * A child whose word is outside [0, V), or a token whose parent is not below it, is left out
+ * (FD_ERR_BAD_INDEX).  One launch.
+ */
+FD_API fd_status fd_verify_tree(const fd_tree_desc* tree, const int32_t* tokens, const float* uniforms,
+                                const void* target, const int64_t target_stride[2], const void* draft,
+                                const int64_t draft_stride[2], fd_dtype dtype, int32_t* path, int32_t* count,
+                                int32_t* next_token, int32_t B, int32_t V, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/*
+ * Rows that stay, moved together in a bf16 or fp32 cache: for every sequence b and j <
+ * counts[b], place starts[b] + j gets the keys and values that place starts[b] + index[b, j] held
+ * before the call.  index [B, n] int32 rises along a sequence (index[b, j] <
+ * index[b, j + 1], from 0).  counts NULL = n, else clamped to [0, n]; starts NULL = 0.  With
+ * fd_verify_tree: index = path, counts = count, starts = P_b (the lengths before the drafts).
+ *   max_seq_len  places at or past it are not touched; as in fd_decode.
+ * An entry that does not rise, or whose place lies at or past max_seq_len, ends the list
+ * there, for all heads alike: it and those after it are left out (a negative start: all).  A page outside the
+ * pool leaves out its rows.  Both are reported as FD_ERR_BAD_INDEX.  Two sequences of one call must
+ * not share pages that a row moves from or to.  Workspace as for fd_append_rope.  One launch.
+ */
+FD_API fd_status fd_keep_rows(const fd_kv_desc* kv, const int32_t* index, int32_t n, const int32_t* counts,
+                              const int32_t* starts, int32_t B, int32_t Hkv, int32_t max_seq_len, int32_t D,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Split step only ("fd_split" of the walkthrough), with n_splits > 0 splits
  * per sequence of fd_split_size(max_seq_len, n_splits) tokens each.  Writes:
  *   o_part [B, Hq, n_splits, D]  unnormalised sum_t exp(s_t - m_s) v_t

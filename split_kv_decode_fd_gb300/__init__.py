@@ -23,6 +23,8 @@ from .fdecode import (  # noqa: F401
     append_rope_kv4,
     decode_kv4,
     decode_tree,
+    keep_rows,
+    verify_tree,
     kv4_block_bytes,
     kv4_cache,
     kv4_read,

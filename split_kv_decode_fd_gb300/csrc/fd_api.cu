@@ -821,6 +821,21 @@ fd_status check_kv4(const fd_kv4_desc* kv, int B, int Hkv, int D, int64_t max_le
   return FD_OK;
 }
 
+KvView view_of(const fd_kv_desc* kv, int Hkv) {
+  KvView v;
+  std::memset(&v, 0, sizeof(v));
+  v.k = const_cast<void*>(kv->k);
+  v.v = const_cast<void*>(kv->v);
+  v.block_table = kv->block_table;
+  v.capacity = kv->capacity;
+  v.Hkv = Hkv;
+  v.paged = kv->layout == FD_KV_PAGED;
+  v.page_size = kv->page_size;
+  v.max_pages = kv->max_pages_per_seq;
+  v.num_pages = kv->num_pages;
+  return v;
+}
+
 bool strides16(const void* p, const int64_t (&s)[3], int es) {
   if (!aligned16(p)) return false;
   for (const int64_t x : s)
@@ -893,18 +908,8 @@ fd_status fd_append_rope(const fd_new_rows* rows, const fd_kv_desc* kv, float* q
   fd_status st = check_rows(rows, q_out, B, n, Hq, Hkv, seq_lens, max_seq_len, D, workspace, workspace_bytes, &r);
   if (st != FD_OK) return st;
   if ((st = check_kv(kv, B, Hkv, max_seq_len + n)) != FD_OK) return st;
-  KvView v;
-  std::memset(&v, 0, sizeof(v));
-  v.k = const_cast<void*>(kv->k);
-  v.v = const_cast<void*>(kv->v);
-  v.block_table = kv->block_table;
-  v.capacity = kv->capacity;
-  v.Hkv = Hkv;
-  v.paged = kv->layout == FD_KV_PAGED;
-  v.page_size = kv->page_size;
-  v.max_pages = kv->max_pages_per_seq;
-  v.num_pages = kv->num_pages;
-  return launch_append(D, rows->dtype == FD_F32, kv->dtype == FD_F32, r, v, (cudaStream_t)stream) == cudaSuccess
+  return launch_append(D, rows->dtype == FD_F32, kv->dtype == FD_F32, r, view_of(kv, Hkv), (cudaStream_t)stream) ==
+                 cudaSuccess
              ? FD_OK
              : FD_ERR_CUDA;
 }
@@ -1045,21 +1050,6 @@ fd_status check_tree(const fd_tree_desc* tree, int B, TreeView* out) {
   return FD_OK;
 }
 
-KvView view_of(const fd_kv_desc* kv, int Hkv) {
-  KvView v;
-  std::memset(&v, 0, sizeof(v));
-  v.k = const_cast<void*>(kv->k);
-  v.v = const_cast<void*>(kv->v);
-  v.block_table = kv->block_table;
-  v.capacity = kv->capacity;
-  v.Hkv = Hkv;
-  v.paged = kv->layout == FD_KV_PAGED;
-  v.page_size = kv->page_size;
-  v.max_pages = kv->max_pages_per_seq;
-  v.num_pages = kv->num_pages;
-  return v;
-}
-
 static_assert(kMaxDrafts == FD_MAX_DRAFTS, "header and kernels agree");
 
 }  // namespace
@@ -1113,6 +1103,66 @@ fd_status fd_decode_tree(const float* q, const fd_tree_desc* tree, const fd_kv_d
   p.wait_ns = (uint64_t)g_wait_ns.load(std::memory_order_relaxed);
   p.stall_u = g_stall_it.load(std::memory_order_relaxed);
   return launch_tree(D, kv->dtype == FD_F32, p, (cudaStream_t)stream) == cudaSuccess ? FD_OK : FD_ERR_CUDA;
+}
+
+fd_status fd_verify_tree(const fd_tree_desc* tree, const int32_t* tokens, const float* uniforms, const void* target,
+                         const int64_t target_stride[2], const void* draft, const int64_t draft_stride[2],
+                         fd_dtype dtype, int32_t* path, int32_t* count, int32_t* next_token, int32_t B, int32_t V,
+                         void* workspace, size_t workspace_bytes, void* stream) {
+  VerifyParams p;
+  std::memset(&p, 0, sizeof(p));
+  const fd_status st = check_tree(tree, B, &p.tree);
+  if (st != FD_OK) return st;
+  if (!tokens || !uniforms || !target || !target_stride || !path || !count || !next_token || V < 1)
+    return FD_ERR_INVALID_ARG;
+  if (draft && !draft_stride) return FD_ERR_INVALID_ARG;
+  if (dtype != FD_F32 && dtype != FD_BF16) return FD_ERR_UNSUPPORTED;
+  const uintptr_t es = dtype == FD_F32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(target) % es != 0 || reinterpret_cast<uintptr_t>(draft) % es != 0)
+    return FD_ERR_INVALID_ARG;
+  for (int i = 0; i < 2; ++i) {
+    if (target_stride[i] < 0 || (draft && draft_stride[i] < 0)) return FD_ERR_INVALID_ARG;
+    p.ts[i] = target_stride[i];
+    p.ds[i] = draft ? draft_stride[i] : 0;
+  }
+  if (V > INT32_MAX / 2 || B > INT32_MAX / 64) return FD_ERR_UNSUPPORTED;  // places and CTAs are int32
+  if (!workspace || !aligned16(workspace)) return FD_ERR_INVALID_ARG;
+  if (workspace_bytes < kHeaderBytes) return FD_ERR_WORKSPACE_TOO_SMALL;
+  p.tokens = tokens;
+  p.uniforms = uniforms;
+  p.target = target;
+  p.draft = draft;
+  p.path = path;
+  p.count = count;
+  p.next_token = next_token;
+  p.B = B;
+  p.V = V;
+  p.err = reinterpret_cast<unsigned*>(workspace);
+  return launch_verify(dtype == FD_F32, p, (cudaStream_t)stream) == cudaSuccess ? FD_OK : FD_ERR_CUDA;
+}
+
+fd_status fd_keep_rows(const fd_kv_desc* kv, const int32_t* index, int32_t n, const int32_t* counts,
+                       const int32_t* starts, int32_t B, int32_t Hkv, int32_t max_seq_len, int32_t D, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  if (!index || n < 1) return FD_ERR_INVALID_ARG;
+  if (n > INT32_MAX - (1 << 16)) return FD_ERR_UNSUPPORTED;  // entries are counted in int32, a chunk at a time
+  fd_status st = check_shape(B, Hkv, Hkv, D);
+  if (st != FD_OK) return st;
+  if ((st = check_kv(kv, B, Hkv, max_seq_len)) != FD_OK) return st;
+  if (!workspace || !aligned16(workspace)) return FD_ERR_INVALID_ARG;
+  if (workspace_bytes < kHeaderBytes) return FD_ERR_WORKSPACE_TOO_SMALL;
+  if ((int64_t)B * Hkv > INT32_MAX / 64) return FD_ERR_UNSUPPORTED;  // CTAs of the grid
+  KeepParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.kv = view_of(kv, Hkv);
+  p.index = index;
+  p.counts = counts;
+  p.starts = starts;
+  p.B = B;
+  p.n = n;
+  p.max_len = max_seq_len;
+  p.err = reinterpret_cast<unsigned*>(workspace);
+  return launch_keep(D * (kv->dtype == FD_F32 ? 4 : 2), p, (cudaStream_t)stream) == cudaSuccess ? FD_OK : FD_ERR_CUDA;
 }
 
 }  // extern "C"

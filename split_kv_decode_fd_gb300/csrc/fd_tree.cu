@@ -282,30 +282,14 @@ __global__ void __launch_bounds__(256) fd_tree_join_kernel(const TreeParams p) {
   if (p.lse && lane == 0) p.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * kTreeLn2;
 }
 
-template <class... A>
-cudaError_t start(void (*kernel)(A...), unsigned grid, int threads, size_t smem, cudaStream_t stream, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  // set-up overlaps the end of the kernel before (griddepcontrol.wait)
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 template <int D, class T>
 cudaError_t launch_core(const TreeParams& p, cudaStream_t stream) {
   const size_t smem = sizeof(CoreSmem<D>);
   cudaError_t e = cudaFuncSetAttribute(fd_tree_core_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  e = start(fd_tree_core_kernel<D, T>, (unsigned)(p.ranges * p.nsub), kCoreThreads, smem, stream, p);
+  e = launch_early(fd_tree_core_kernel<D, T>, (unsigned)(p.ranges * p.nsub), kCoreThreads, smem, stream, p);
   if (e != cudaSuccess || p.ranges == 1) return e;
-  return start(fd_tree_join_kernel<D, kRows>, (unsigned)(p.ranges * p.nsub * (kRows / 8)), 256, 0, stream, p);
+  return launch_early(fd_tree_join_kernel<D, kRows>, (unsigned)(p.ranges * p.nsub * (kRows / 8)), 256, 0, stream, p);
 }
 
 }  // namespace

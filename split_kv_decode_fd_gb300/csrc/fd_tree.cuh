@@ -228,4 +228,21 @@ __device__ __forceinline__ void tree_empty_rows(const TreeParams& p, int32_t ran
 
 constexpr float kTreeLn2 = 0.6931471805599453f;
 
+// A launch whose set-up overlaps the end of the kernel before: the kernel waits for that one
+// (griddepcontrol.wait) before its first access to memory.
+template <class... A>
+cudaError_t launch_early(void (*kernel)(A...), unsigned grid, int threads, size_t smem, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 }  // namespace fdk

@@ -70,4 +70,31 @@ constexpr int kTreeCtas = 2;   // CTAs per SM
 
 cudaError_t launch_tree(int D, bool f32, const TreeParams& p, cudaStream_t stream);
 
+// Which drafts stay (fd_verify_tree).
+struct VerifyParams {
+  TreeView tree;
+  const int32_t* tokens;     // [B, n]
+  const float* uniforms;     // [B, n]
+  const void* target;        // row of token j: target + b * ts[0] + (n - m + j) * ts[1]
+  const void* draft;         // likewise, or null
+  int64_t ts[2], ds[2];
+  int32_t* path;             // [B, n]
+  int32_t* count;            // [B]
+  int32_t* next_token;       // [B]
+  int32_t B, V;
+  unsigned* err;
+};
+cudaError_t launch_verify(bool f32, const VerifyParams& p, cudaStream_t stream);
+
+// Rows together (fd_keep_rows): place start + j gets the row of place start + index[j].
+struct KeepParams {
+  KvView kv;
+  const int32_t* index;      // [B, n]
+  const int32_t* counts;     // [B] or null (n)
+  const int32_t* starts;     // [B] or null (0)
+  int32_t B, n, max_len;
+  unsigned* err;
+};
+cudaError_t launch_keep(int row_bytes, const KeepParams& p, cudaStream_t stream);
+
 }  // namespace fdk

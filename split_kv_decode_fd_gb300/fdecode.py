@@ -21,7 +21,7 @@ __all__ = [
     "FdError", "KvDesc", "library_path", "load_library", "workspace_bytes", "split_size", "plan_pieces",
     "Workspace", "decode", "decode_rows", "append_decode", "prefill", "attend", "attend_backend", "decode_host", "HostDecoder", "decode_static", "static_status", "split_partial", "combine", "workspace_status",
     "NewRows", "Kv4Desc", "append_rope", "append_rope_kv4", "kv4_block_bytes", "kv4_cache", "kv4_read", "decode_kv4",
-    "TreeDesc", "decode_tree",
+    "TreeDesc", "decode_tree", "verify_tree", "keep_rows",
 ]
 
 FD_OK, FD_ERR_INVALID_ARG, FD_ERR_UNSUPPORTED, FD_ERR_WORKSPACE_TOO_SMALL = 0, 1, 2, 3
@@ -163,6 +163,10 @@ def load_library(path: Optional[str] = None):
             "fd_tree_workspace_bytes": (c_sz, [c_i32, c_i32, c_i32, c_i32, c_i32, c_i32]),
             "fd_decode_tree": (ctypes.c_int, [vp, ctypes.POINTER(TreeDesc), kvp, vp, vp, c_i32, c_i32, c_i32, vp, c_i32,
                                               c_i32, f32, vp, c_sz, vp]),
+            "fd_verify_tree": (ctypes.c_int, [ctypes.POINTER(TreeDesc), vp, vp, vp, ctypes.POINTER(c_i64 * 2), vp,
+                                              ctypes.POINTER(c_i64 * 2), ctypes.c_int, vp, vp, vp, c_i32, c_i32, vp, c_sz,
+                                              vp]),
+            "fd_keep_rows": (ctypes.c_int, [kvp, vp, c_i32, vp, vp, c_i32, c_i32, c_i32, c_i32, vp, c_sz, vp]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -1091,3 +1095,80 @@ def decode_tree(q, k, v, parents, *, new_lens=None, seq_lens=None, max_seq_len=N
             _opt(seq_lens, "seq_lens", torch.int32, index, (B,)), max_seq_len, D,
             1.0 / math.sqrt(D) if scale is None else float(scale), buf.data_ptr(), buf.numel())
     return out, lse
+
+
+_PAIR = ctypes.c_int64 * 2
+
+
+def _probs(t, name, B, n, V, dtype, index):
+    """Pointer and strides of ``t`` [B, n, V], whose last axis is contiguous."""
+    if not isinstance(t, _torch().Tensor) or t.get_device() != index:
+        raise ValueError(f"{name} must be a CUDA tensor on cuda:{index}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != (B, n, V):
+        raise ValueError(f"{name} must have shape {(B, n, V)}, got {tuple(t.shape)}")
+    st = t.stride()
+    if st[2] != 1 and V != 1:
+        raise ValueError(f"the last axis of {name} must be contiguous")
+    return t.data_ptr(), _PAIR(st[0], st[1])
+
+
+def verify_tree(tokens, parents, target, uniforms, *, draft=None, new_lens=None, path=None, count=None, next_token=None,
+                workspace: Optional[Workspace] = None, stream=None):
+    """``fd_verify_tree``: which tokens of a drafted tree stay, and the token that follows them.
+
+    ``tokens`` ``[B, n]`` int32 (token 0 is the last one accepted), ``parents`` and ``new_lens`` as in ``decode_tree``;
+    ``target`` ``[B, n, V]`` are the target's probabilities after each token and ``draft`` those the children were drawn from
+    (None: the children are given, not drawn), fp32 or bf16, their last axis contiguous; ``uniforms`` ``[B, n]`` fp32 are
+    random numbers in [0, 1), a child's own for its acceptance and token 0's for the next token.  Returns ``(path [B, n],
+    count [B], next_token [B])``, int32: the numbers of the tokens that stay, -1 behind them; what ``keep_rows`` takes.
+    """
+    torch = _torch()
+    index = _index_of(target, "target")
+    if target.dim() != 3:
+        raise ValueError("target must be [B, n, V]")
+    B, n, V = target.shape
+    dtype = target.dtype
+    dt = FD_BF16 if dtype is torch.bfloat16 else FD_F32 if dtype is torch.float32 else -1
+    if dt < 0:
+        raise ValueError(f"unsupported dtype of probabilities {dtype}")
+    tp, ts = _probs(target, "target", B, n, V, dtype, index)
+    dp, ds = (0, None) if draft is None else _probs(draft, "draft", B, n, V, dtype, index)
+    int32 = torch.int32
+    at, up = _flat(tokens, "tokens", int32, index, (B, n)), _flat(uniforms, "uniforms", torch.float32, index, (B, n))
+    tree = _tree_desc(parents, new_lens, B, n, index)
+    made = []
+    for t, name, shape in ((path, "path", (B, n)), (count, "count", (B,)), (next_token, "next_token", (B,))):
+        if t is None:
+            t = _made(torch.empty, shape, int32, target.device, stream)
+            made.append((t, t.data_ptr()))
+        else:
+            made.append((t, _flat(t, name, int32, index, shape)))
+    (path, pp), (count, cp), (next_token, np_) = made
+    buf, handle = _scratch(workspace, index, 256, stream)
+    _launch(index, handle, _lib().fd_verify_tree, "fd_verify_tree", tree, at, up, tp, ts, dp, ds, dt, pp, cp, np_, B,
+            _i32(V, "V"), buf.data_ptr(), buf.numel())
+    return path, count, next_token
+
+
+def keep_rows(k, v, index, *, counts=None, starts=None, max_seq_len=None, block_table=None,
+              workspace: Optional[Workspace] = None, stream=None):
+    """``fd_keep_rows``: place ``starts[b] + j`` of a cache gets the row of place ``starts[b] + index[b, j]``, for ``j <
+    counts[b]``.
+
+    ``k``, ``v`` are the cache as in ``decode`` (bf16 or fp32), written in place; ``index`` ``[B, n]`` int32 rises along a
+    sequence.  ``counts`` ``[B]`` (None: n) and ``starts`` ``[B]`` (None: 0) int32.  After ``verify_tree``: its path, its
+    count and the lengths before the drafts.
+    """
+    torch = _torch()
+    if not isinstance(index, torch.Tensor) or index.dim() != 2:
+        raise ValueError("index must be [B, n]")
+    B, n = index.shape
+    desc, Hkv, D, tokens, on = _cache_desc(k, v, block_table, B)
+    at = _flat(index, "index", torch.int32, on)
+    max_seq_len = _i32(tokens if max_seq_len is None else max_seq_len, "max_seq_len")
+    buf, handle = _scratch(workspace, on, 256, stream)
+    _launch(on, handle, _lib().fd_keep_rows, "fd_keep_rows", desc, at, _i32(n, "n of the index"),
+            _opt(counts, "counts", torch.int32, on, (B,)), _opt(starts, "starts", torch.int32, on, (B,)), B, Hkv,
+            max_seq_len, D, buf.data_ptr(), buf.numel())
