@@ -1015,11 +1015,11 @@ namespace {
 struct TreeSplit {
   int32_t rows, nsub, ranges;
 };
-TreeSplit tree_split(int Hq, int Hkv, int n, int sms, int64_t tiles) {
+TreeSplit tree_split(int Hq, int Hkv, int n, bool f32, int sms, int64_t tiles) {
   TreeSplit t;
   t.rows = Hq / Hkv * n;
-  t.nsub = ceil_div(t.rows, kTreeRows);
-  int64_t r = (int64_t)kTreeCtas * sms / t.nsub;  // CTAs that run at once
+  t.nsub = ceil_div(t.rows, tree_rows(f32));
+  int64_t r = (int64_t)tree_ctas(f32) * sms / t.nsub;  // CTAs that run at once
   if (r > tiles) r = tiles;
   t.ranges = (int32_t)(r < 1 ? 1 : r);
   return t;
@@ -1028,8 +1028,8 @@ TreeSplit tree_split(int Hq, int Hkv, int n, int sms, int64_t tiles) {
 struct TreeLayout {
   size_t joins, o, m, l, total;
 };
-TreeLayout tree_layout(const TreeSplit& t, int D) {
-  const size_t states = t.ranges > 1 ? (size_t)2 * t.ranges * t.nsub * kTreeRows : 0;
+TreeLayout tree_layout(const TreeSplit& t, bool f32, int D) {
+  const size_t states = t.ranges > 1 ? (size_t)2 * t.ranges * t.nsub * tree_rows(f32) : 0;
   TreeLayout w;
   w.joins = kHeaderBytes + kCounterBytes;  // behind the counters, which other calls expect at zero
   w.o = w.joins + align_up((size_t)t.ranges * sizeof(TreeJoin));
@@ -1060,7 +1060,12 @@ size_t fd_tree_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t D, in
   if (check_shape(B, Hq, Hkv, D) != FD_OK || n < 1 || n > kMaxDrafts || (int64_t)Hq * n > ((int64_t)1 << 24)) return 0;
   int sms = num_sms;
   if (sms <= 0 && !sm_count(&sms)) return 0;
-  return tree_layout(tree_split(Hq, Hkv, n, sms, INT64_MAX), D).total;
+  size_t most = 0;  // the size must hold for either cache type
+  for (const bool f32 : {false, true}) {
+    const size_t a = tree_layout(tree_split(Hq, Hkv, n, f32, sms, INT64_MAX), f32, D).total;
+    most = a > most ? a : most;
+  }
+  return most;
 }
 
 fd_status fd_decode_tree(const float* q, const fd_tree_desc* tree, const fd_kv_desc* kv, float* out, float* lse,
@@ -1077,8 +1082,9 @@ fd_status fd_decode_tree(const float* q, const fd_tree_desc* tree, const fd_kv_d
   if (max_seq_len > INT32_MAX - 2 * kPlanTile) return FD_ERR_UNSUPPORTED;  // a tile's end is an int32
   int sms = 0;
   if (!sm_count(&sms)) return FD_ERR_CUDA;
-  const TreeSplit t = tree_split(Hq, Hkv, tree->n, sms, (int64_t)B * Hkv * ceil_div(max_seq_len, kPlanTile));
-  const TreeLayout w = tree_layout(t, D);
+  const bool f32 = kv->dtype == FD_F32;
+  const TreeSplit t = tree_split(Hq, Hkv, tree->n, f32, sms, (int64_t)B * Hkv * ceil_div(max_seq_len, kPlanTile));
+  const TreeLayout w = tree_layout(t, f32, D);
   if (workspace_bytes < w.total) return FD_ERR_WORKSPACE_TOO_SMALL;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.q = q;
@@ -1102,7 +1108,17 @@ fd_status fd_decode_tree(const float* q, const fd_tree_desc* tree, const fd_kv_d
   p.qk_scale = (float)((double)scale * 1.4426950408889634);
   p.wait_ns = (uint64_t)g_wait_ns.load(std::memory_order_relaxed);
   p.stall_u = g_stall_it.load(std::memory_order_relaxed);
-  return launch_tree(D, kv->dtype == FD_F32, p, (cudaStream_t)stream) == cudaSuccess ? FD_OK : FD_ERR_CUDA;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (f32) {
+    if (launch_tree_core(D, p, s) != cudaSuccess) return FD_ERR_CUDA;
+  } else {
+    CUtensorMap tk, tv;
+    if ((st = make_maps(kv, B, Hkv, D, &tk, &tv)) != FD_OK) return st;
+    if (launch_tree_mma(D, tk, tv, p, s) != cudaSuccess) return FD_ERR_CUDA;
+  }
+  // a sequence of one tile lies within a share
+  if (t.ranges == 1 || max_seq_len <= kPlanTile) return FD_OK;
+  return launch_tree_join(D, f32, p, s) == cudaSuccess ? FD_OK : FD_ERR_CUDA;
 }
 
 fd_status fd_verify_tree(const fd_tree_desc* tree, const int32_t* tokens, const float* uniforms, const void* target,

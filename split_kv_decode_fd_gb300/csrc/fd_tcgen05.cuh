@@ -1,6 +1,7 @@
-// fd_tcgen05.cuh -- the tcgen05 instructions of the 4-bit decode kernel: fp16
-// MMAs with A in tensor memory and B in shared memory, and moves between
-// registers and tensor memory (lane = row, one 32-bit column a register).
+// fd_tcgen05.cuh -- the tcgen05 instructions of the 4-bit decode kernel and of the
+// tree attention: fp16 and bf16 MMAs with A in tensor or shared memory and B in
+// shared memory, and moves between registers and tensor memory (lane = row, one
+// 32-bit column a register).
 #pragma once
 
 #include <stdint.h>
@@ -28,6 +29,26 @@ __device__ __forceinline__ uint64_t b_desc_n(uint32_t saddr) {
 // K-major or (bit 16) N-major.
 __host__ __device__ constexpr uint32_t f16_instr_desc(int M, int N, bool b_n_major = false) {
   return (1u << 4) | ((b_n_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// The same with A and B bf16.
+__host__ __device__ constexpr uint32_t bf16_instr_desc(int M, int N, bool b_n_major = false) {
+  return f16_instr_desc(M, N, b_n_major) | (1u << 7) | (1u << 10);
+}
+
+// The descriptor of an N-major B operand in rows (of K) of 128 bytes with the 128-byte
+// swizzle: eight rows are 1024 bytes apart, the next 64 n `n_stride` bytes on.
+__device__ __forceinline__ uint64_t b_desc_rows(uint32_t saddr, uint32_t n_stride) {
+  return b_desc(saddr) | ((uint64_t)(n_stride >> 4) << 16);
+}
+
+// D[tmem] (+)= A[smem] B: 128 rows, 16 of K; A's descriptor is as b_desc's.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
 }
 
 // D[tmem] (+)= A[tmem] B: 128 rows, 16 of K.

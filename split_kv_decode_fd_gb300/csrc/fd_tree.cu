@@ -1,4 +1,4 @@
-// fd_tree.cu -- attention of a tree of drafted tokens on CUDA cores, and the join
+// fd_tree.cu -- attention of a tree of drafted tokens over an fp32 cache, and the join
 // of the states that the shares of a sequence leave.
 //
 // A row sees the places before the drafts, its token's ancestors and itself:
@@ -7,14 +7,12 @@
 //
 // A CTA serves 32 rows of a KV head from tiles of 64 keys in shared memory, and
 // each thread two rows: four keys a row for q . k, D / 16 channels a row for p . V.
-#include <cuda_bf16.h>
-
 #include "fd_tree.cuh"
 
 namespace fdk {
 namespace {
 
-constexpr int kRows = kTreeRows;
+constexpr int kRows = kTreeRowsCore;
 constexpr int kKeys = 64;
 constexpr int kCoreThreads = 256;
 
@@ -30,13 +28,9 @@ struct CoreSmem {
 };
 
 __device__ __forceinline__ float4 load4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-  const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
-  return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
-}
 
-template <int D, class T>
-__global__ void __launch_bounds__(kCoreThreads, kTreeCtas) fd_tree_core_kernel(const TreeParams p) {
+template <int D>
+__global__ void __launch_bounds__(kCoreThreads, kTreeCtasCore) fd_tree_core_kernel(const TreeParams p) {
   using S = CoreSmem<D>;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   S& s = *reinterpret_cast<S*>(smem_raw);
@@ -100,8 +94,8 @@ __global__ void __launch_bounds__(kCoreThreads, kTreeCtas) fd_tree_core_kernel(c
             at = ((int64_t)pc.b * p.Hkv + pc.h) * p.kv.capacity + t;
           }
           if (at >= 0) {
-            x = load4(static_cast<const T*>(p.kv.k) + at * D + c);
-            y = load4(static_cast<const T*>(p.kv.v) + at * D + c);
+            x = load4(static_cast<const float*>(p.kv.k) + at * D + c);
+            y = load4(static_cast<const float*>(p.kv.v) + at * D + c);
           }
         }
         *reinterpret_cast<float4*>(s.k + r * S::kStride + c) = x;
@@ -282,21 +276,29 @@ __global__ void __launch_bounds__(256) fd_tree_join_kernel(const TreeParams p) {
   if (p.lse && lane == 0) p.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * kTreeLn2;
 }
 
-template <int D, class T>
+template <int D>
 cudaError_t launch_core(const TreeParams& p, cudaStream_t stream) {
-  const size_t smem = sizeof(CoreSmem<D>);
-  cudaError_t e = cudaFuncSetAttribute(fd_tree_core_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const cudaError_t e = allow_smem<fd_tree_core_kernel<D>>((int)sizeof(CoreSmem<D>));
   if (e != cudaSuccess) return e;
-  e = launch_early(fd_tree_core_kernel<D, T>, (unsigned)(p.ranges * p.nsub), kCoreThreads, smem, stream, p);
-  if (e != cudaSuccess || p.ranges == 1) return e;
-  return launch_early(fd_tree_join_kernel<D, kRows>, (unsigned)(p.ranges * p.nsub * (kRows / 8)), 256, 0, stream, p);
+  return launch_early(fd_tree_core_kernel<D>, (unsigned)(p.ranges * p.nsub), kCoreThreads, sizeof(CoreSmem<D>), stream, p);
+}
+
+template <int D, int Rows>
+cudaError_t launch_join(const TreeParams& p, cudaStream_t stream) {
+  return launch_early(fd_tree_join_kernel<D, Rows>, (unsigned)(p.ranges * p.nsub * (Rows / 8)), 256, 0, stream, p);
 }
 
 }  // namespace
 
-cudaError_t launch_tree(int D, bool f32, const TreeParams& p, cudaStream_t stream) {
-  if (D == 128) return f32 ? launch_core<128, float>(p, stream) : launch_core<128, __nv_bfloat16>(p, stream);
-  if (D == 64) return f32 ? launch_core<64, float>(p, stream) : launch_core<64, __nv_bfloat16>(p, stream);
+cudaError_t launch_tree_core(int D, const TreeParams& p, cudaStream_t stream) {
+  if (D == 128) return launch_core<128>(p, stream);
+  if (D == 64) return launch_core<64>(p, stream);
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_tree_join(int D, bool f32, const TreeParams& p, cudaStream_t stream) {
+  if (D == 128) return f32 ? launch_join<128, kTreeRowsCore>(p, stream) : launch_join<128, kTreeRowsMma>(p, stream);
+  if (D == 64) return f32 ? launch_join<64, kTreeRowsCore>(p, stream) : launch_join<64, kTreeRowsMma>(p, stream);
   return cudaErrorInvalidValue;
 }
 

@@ -2,6 +2,8 @@
 // walk over a share of the keys, and where a piece's states go.
 #pragma once
 
+#include <atomic>
+
 #include "fd_device.cuh"
 #include "fd_tree.h"
 
@@ -227,6 +229,20 @@ __device__ __forceinline__ void tree_empty_rows(const TreeParams& p, int32_t ran
 }
 
 constexpr float kTreeLn2 = 0.6931471805599453f;
+
+// Lets a kernel take `bytes` of dynamic shared memory, once per device.
+template <auto Kernel>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 // A launch whose set-up overlaps the end of the kernel before: the kernel waits for that one
 // (griddepcontrol.wait) before its first access to memory.

@@ -9,6 +9,7 @@
 // token's parent, which is below its own, or -1.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -28,7 +29,7 @@ struct TreeView {
 
 // Attention: the g * n rows of a KV head (head by head, token rows within a head,
 // as q [B, Hq, n, D] has them) share its keys and values.  They are cut into
-// `nsub` blocks of kTreeRows rows, and the keys of all (b, KV head) pairs into
+// `nsub` blocks of tree_rows() rows, and the keys of all (b, KV head) pairs into
 // `ranges` shares of equal cost (BalancedWalk's line of cost units): CTA
 // r * nsub + s takes share r for block s, so that the blocks of a KV head read the
 // same keys at the same time, from memory once and then from L2.
@@ -51,8 +52,8 @@ struct TreeParams {
   const int32_t* seq_lens;     // [B] or null (max_len)
   KvView kv;
   TreeView tree;
-  float* o_part;               // [2 ranges][nsub][kTreeRows][D]
-  float* m_part;               // [2 ranges][nsub][kTreeRows]
+  float* o_part;               // [2 ranges][nsub][tree_rows()][D]
+  float* m_part;               // [2 ranges][nsub][tree_rows()]
   float* l_part;
   TreeJoin* joins;             // [ranges]
   unsigned* err;
@@ -65,10 +66,17 @@ struct TreeParams {
   int32_t stall_u;             // testing hook: the copy that every CTA skips, or -1
 };
 
-constexpr int kTreeRows = 32;  // rows per CTA
-constexpr int kTreeCtas = 2;   // CTAs per SM
+// Rows per CTA and CTAs per SM: fp32 caches on CUDA cores, bf16 ones on tensor cores.
+constexpr int kTreeRowsCore = 32, kTreeCtasCore = 2;
+constexpr int kTreeRowsMma = 128;
+constexpr int tree_rows(bool f32) { return f32 ? kTreeRowsCore : kTreeRowsMma; }
+constexpr int tree_ctas(bool f32) { return f32 ? kTreeCtasCore : 1; }
 
-cudaError_t launch_tree(int D, bool f32, const TreeParams& p, cudaStream_t stream);
+cudaError_t launch_tree_core(int D, const TreeParams& p, cudaStream_t stream);
+cudaError_t launch_tree_mma(int D, const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p,
+                            cudaStream_t stream);
+// Joins what either left.
+cudaError_t launch_tree_join(int D, bool f32, const TreeParams& p, cudaStream_t stream);
 
 // Which drafts stay (fd_verify_tree).
 struct VerifyParams {

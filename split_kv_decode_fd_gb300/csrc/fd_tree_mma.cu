@@ -1,0 +1,652 @@
+// fd_tree_mma.cu -- attention of a tree of drafted tokens over a bf16 cache on the
+// 5th-generation tensor cores.
+//
+// The rows of a KV head's group (heads x tokens, up to 128 a CTA) are the rows of
+// both products: S = Q K^T (128 x 128 keys, over D) and O = P V (128 x D, over the 128
+// keys of a tile).  The work is bound by reading the cache as long as the products
+// take less time than the tile's bytes, and the rows of one CTA come free with it.
+//
+// Precision: K and V are exact in bf16.  q and p (fp32) are cut into three bf16
+// numbers of eight bits each by truncation, which is exact, so all products are, and
+// fp32 sums are what rounds: S sums its small parts first, and O is taken out of
+// tensor memory every tile and added up in registers, since the adds of the matrix
+// unit drop bits.  Six products of 8 k-steps make 3072 cycles a tile of 128 channels, and a
+// tile's 64 KB at an SM's share of the memory rate some 3000.
+//
+// Ten warps:
+//   0-3  softmax, thread = row: reads S, masks, keeps the running max and sum, writes P
+//        over S; cuts q at the start of a piece.
+//   4-7  sums, thread = row: O of each tile times what the max has moved by; writes the
+//        rows at the end of a piece.
+//   8    copies: walks the share, announces its pieces, brings q (by bulk copies) and the K and V
+//        tiles (16-row x 128-byte boxes, 128-byte swizzle) through one ring of slots
+//        in the order of their use: q, K0, K1, V0, K2, V1, ... , V(n-1).
+//   9    products, one thread: S(j+1) before O(j), so that the tensor core works on S while
+//        the softmax of the tile before runs.
+#include <atomic>
+
+#include "fd_tcgen05.cuh"
+#include "fd_tree.cuh"
+
+namespace fdk {
+namespace {
+
+constexpr int kRows = kTreeRowsMma;
+constexpr int kKeys = kPlanTile;
+constexpr int kThreads = 320;
+constexpr int kParts = 3;                 // bf16 numbers that q and p are cut into
+constexpr int kCopyWarp = 8, kMmaWarp = 9;
+// Tensor memory: two S / P buffers and O.  P takes 8 columns for each part of 16 keys, 192 in
+// all, and S the last 128 of them: a chunk of P never reaches an unread chunk of S.
+constexpr uint32_t kBuf = 192, kSOff = 64, kOCol = 384;
+
+template <int D>
+struct Layout {
+  static constexpr int kNB = D / 64;                          // 128-byte column blocks of a row
+  static constexpr uint32_t kBlock = 16384;                   // [128 rows][128 bytes]
+  static constexpr uint32_t kTile = kNB * kBlock;             // a K or V tile, one part of q
+  static constexpr uint32_t kRing = kParts * kTile;           // q first
+  static constexpr uint32_t kSlots = D == 128 ? 4 : 8;
+  static constexpr uint32_t kMisc = kRing + kSlots * kTile;
+  static constexpr uint32_t kQRowsPerSlot = kTile / (D * 4);  // fp32 rows of q
+  static constexpr uint32_t kBytes = kMisc + 2048 + 1024;     // 1024: the base is aligned up
+  static_assert(kBytes <= 232448, "shared memory");
+};
+
+// Behind the ring.
+struct Misc {
+  uint64_t kv_full[8], kv_empty[8];
+  uint64_t s_full[2], p_full[2], o_empty[2];
+  uint64_t piece_full[2], piece_empty[2];
+  uint64_t o_full, q_ready, fin_full, fin_empty, drain;
+  uint32_t tmem;
+  volatile int abort;
+  TreePiece piece[2];
+  float m[2][kRows];      // running max of the last tiles
+  float l[kRows];         // a piece's sums
+  uint64_t unfit[4];      // tokens whose values are not finite, as the softmax warps met them
+};
+static_assert(sizeof(Misc) <= 2048, "Misc");
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// Pairs of floats in one register pair: the packed arithmetic rounds each as the scalar one does.
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
+  return d;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// The upper 16 bits of both, x's in the low half: their bf16 truncations.
+__device__ __forceinline__ uint32_t trunc2(float x, float y) {
+  return __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+}
+__device__ __forceinline__ float trunc1(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
+
+// x and y as sums of three bf16 numbers each, exactly (24 bits = 3 x 8).
+__device__ __forceinline__ void cut3(float x, float y, uint32_t (&w)[kParts]) {
+  w[0] = trunc2(x, y);
+  float a, b;
+  unpack2(sub2(pack2(x, y), pack2(trunc1(x), trunc1(y))), a, b);
+  w[1] = trunc2(a, b);
+  float c, d;
+  unpack2(sub2(pack2(a, b), pack2(trunc1(a), trunc1(b))), c, d);
+  w[2] = trunc2(c, d);
+}
+
+// Waits of all roles: false when the CTA gives up or the limit runs out.
+struct Waits {
+  Misc* s;
+  unsigned long long limit;
+  bool ok = true;
+  __device__ __forceinline__ void on(uint64_t* bar, uint32_t parity) {
+    if (ok && !mbar_try_wait(bar, parity)) ok = !s->abort && mbar_wait_for(bar, parity, limit);
+  }
+  // The warp's lanes alike.
+  __device__ __forceinline__ bool all() {
+    ok = __all_sync(0xffffffffu, ok);
+    return ok;
+  }
+};
+
+// Uses of the ring: slot u % n in phase u / n.
+template <uint32_t N>
+struct Ring {
+  uint32_t slot = 0, phase = 0;
+  __device__ __forceinline__ void next(uint32_t by = 1) {
+    slot += by;
+    if (slot >= N) {
+      slot -= N;
+      phase ^= 1u;
+    }
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    fd_tree_mma_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+                       const __grid_constant__ TreeParams p) {
+  using Lay = Layout<D>;
+  constexpr uint32_t kSlots = Lay::kSlots, kBlock = Lay::kBlock, kTile = Lay::kTile;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Misc& s = *reinterpret_cast<Misc*>(smem + Lay::kMisc);
+  const uint32_t sq = smem_addr(smem), ring = sq + Lay::kRing;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int32_t range = blockIdx.x / p.nsub, sub = blockIdx.x % p.nsub;
+  const int32_t row0 = sub * kRows;
+  const int32_t live = p.rows - row0 < kRows ? p.rows - row0 : kRows;
+  const uint32_t nq = ((uint32_t)live + Lay::kQRowsPerSlot - 1) / Lay::kQRowsPerSlot;
+
+  if (tid == 0) {
+    for (uint32_t i = 0; i < kSlots; ++i) {
+      mbar_init(s.kv_full + i, 1);
+      mbar_init(s.kv_empty + i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(s.s_full + i, 1);
+      mbar_init(s.p_full + i, 4);
+      mbar_init(s.o_empty + i, 4);
+      mbar_init(s.piece_full + i, 1);
+      mbar_init(s.piece_empty + i, 9);
+    }
+    mbar_init(&s.o_full, 1);
+    mbar_init(&s.q_ready, 4);
+    mbar_init(&s.fin_full, 4);
+    mbar_init(&s.fin_empty, 4);
+    mbar_init(&s.drain, 1);
+    s.abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == kCopyWarp && lane == 0) {
+    prefetch_tensormap(&tmap_k);
+    prefetch_tensormap(&tmap_v);
+  }
+  if (warp == kMmaWarp) tmem_alloc_all(smem_addr(&s.tmem));
+  pdl_launch_dependents();
+  tmem_fence_before();
+  cta_sync();
+  tmem_fence_after();
+  const uint32_t tmem = s.tmem;
+  pdl_wait();
+  Waits w{&s, p.wait_ns ? (unsigned long long)p.wait_ns : kWaitLimitNs};
+
+  // The next piece, for a warp of the softmax or of the sums; false at the end.
+  auto take = [&](uint32_t e, TreePiece& pc) -> bool {
+    w.on(s.piece_full + (e & 1), (e >> 1) & 1);
+    if (!w.all()) return false;
+    pc = s.piece[e & 1];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(s.piece_empty + (e & 1));
+    return pc.b >= 0;
+  };
+
+  if (warp == kCopyWarp) {
+    // ------------------------------------------------------------ copies
+    uint32_t u = 0, stalled = 0xffffffffu;
+    Ring<kSlots> r;
+    if (lane == 0 && sub == 0) p.joins[range].b = -1;
+    TreeWalk walk(p, range);
+    const uint64_t once = policy_evict_first();
+    const bool shared_keys = p.nsub > 1;  // other CTAs read them too: they stay in L2
+    for (uint32_t e = 0;; ++e) {
+      TreePiece pc;
+      if (!walk.next(pc)) pc.b = -1;
+      if (e >= 2) w.on(s.piece_empty + (e & 1), ((e >> 1) - 1) & 1);
+      if (!w.all()) break;
+      if (lane == 0) {
+        s.piece[e & 1] = pc;
+        mbar_arrive(s.piece_full + (e & 1));
+        if (pc.b >= 0 && sub == 0 && pc.slot >= 0 && pc.begin == 0) p.joins[range] = TreeJoin{pc.b, pc.h, pc.last, 0};
+      }
+      if (pc.b < 0) break;
+      // q's rows lie side by side
+      const float* q = p.q + (((int64_t)pc.b * p.Hkv + pc.h) * p.rows + row0) * D;
+      for (uint32_t i = 0; i < nq && w.ok; ++i, ++u, r.next()) {
+        w.on(s.kv_empty + r.slot, r.phase ^ 1u);
+        if (!w.all()) break;
+        if (p.stall_u >= 0 && u == (uint32_t)p.stall_u) {
+          stalled = u;
+          continue;
+        }
+        if (lane == 0) {
+          const int32_t left = live - (int32_t)(i * Lay::kQRowsPerSlot);
+          const uint32_t rows = left < (int32_t)Lay::kQRowsPerSlot ? (uint32_t)left : Lay::kQRowsPerSlot;
+          mbar_arrive_expect_tx(s.kv_full + r.slot, rows * D * 4);
+          bulk_load(smem + Lay::kRing + r.slot * kTile, q + (size_t)i * Lay::kQRowsPerSlot * D, rows * D * 4,
+                    s.kv_full + r.slot);
+        }
+      }
+      const int32_t n = ceil_div(pc.end - pc.begin, kKeys);
+      // Lane l brings rows [16 l, 16 l + 16) of a tile, one run of a page.  Pages of the tile whose K comes next and of
+      // the one after (a lookup takes a while), of the last tile whose K has gone, and of the one before that.
+      const int32_t* table = p.kv.paged ? p.kv.block_table + (int64_t)pc.b * p.kv.max_pages : nullptr;
+      const int32_t t_lane = pc.begin + 16 * lane;
+      auto lookup = [&](int32_t j) -> int32_t {
+        const int32_t t = t_lane + j * kKeys;
+        return lane < 8 && j < n && t < pc.end ? __ldg(table + t / p.kv.page_size) : -2;
+      };
+      auto brings = [&](int32_t j) { return lane < 8 && t_lane + j * kKeys < pc.end; };
+      int32_t page_next = 0, page_after = 0, page_last = 0, page_before = 0;
+      if (table) {
+        page_next = lookup(0);
+        page_after = lookup(1);
+      }
+      for (int32_t i = 0; i < 2 * n && w.ok; ++i, ++u, r.next()) {
+        // the i-th copy: K0, then K(j), V(j - 1), and V(n - 1)
+        const bool is_v = i == 2 * n - 1 || (i > 0 && i % 2 == 0);
+        const int32_t j = i == 2 * n - 1 ? n - 1 : is_v ? i / 2 - 1 : (i + 1) / 2;
+        bool mine = brings(j);
+        int32_t z = pc.b * p.Hkv + pc.h, row = t_lane + j * kKeys;
+        if (table) {
+          z = !is_v ? page_next : i == 2 * n - 1 ? page_last : page_before;
+          if (mine && (z < 0 || z >= p.kv.num_pages)) {
+            atomicOr(p.err, kErrBadIndex);
+            mine = false;
+          }
+          z = z * p.Hkv + pc.h;
+          row %= p.kv.page_size;
+        }
+        w.on(s.kv_empty + r.slot, r.phase ^ 1u);
+        if (!w.all()) break;
+        if (p.stall_u >= 0 && u == (uint32_t)p.stall_u) {
+          stalled = u;
+        } else {
+          const unsigned issue = __ballot_sync(0xffffffffu, mine);
+          if (lane == 0) mbar_arrive_expect_tx(s.kv_full + r.slot, (uint32_t)__popc(issue) * Lay::kNB * 2048u);
+          __syncwarp();
+          if (mine) {
+            uint8_t* dst = smem + Lay::kRing + r.slot * kTile + lane * 2048;
+            const CUtensorMap* map = is_v ? &tmap_v : &tmap_k;
+#pragma unroll
+            for (int blk = 0; blk < Lay::kNB; ++blk) {
+              if (table || shared_keys)
+                tma_load_3d(dst + blk * kBlock, map, s.kv_full + r.slot, blk * 64, row, z);
+              else
+                tma_load_3d_hint(dst + blk * kBlock, map, s.kv_full + r.slot, blk * 64, row, z, once);
+            }
+          }
+        }
+        if (table && !is_v) {
+          page_before = page_last;
+          page_last = page_next;
+          page_next = page_after;
+          page_after = lookup(j + 2);
+        }
+      }
+      if (!w.ok) break;
+    }
+    if (!w.ok) s.abort = 1;
+    // do not leave while copies may still be landing
+    if (lane == 0) {
+      if (!w.ok) atomicOr(p.err, kErrTimeout);
+      const uint32_t first = u > kSlots ? u - kSlots : 0;
+      for (uint32_t i = first; i < u; ++i)
+        if (i != stalled && !mbar_wait_for(s.kv_full + i % kSlots, (i / kSlots) & 1, w.limit)) atomicOr(p.err, kErrTimeout);
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ products
+    if (lane == 0) {
+      constexpr uint32_t idS = bf16_instr_desc(kRows, kKeys), idO = bf16_instr_desc(kRows, D, true);
+      Ring<kSlots> r;
+      uint32_t g = 0, f = 0;  // tiles and pieces so far
+      auto issue_s = [&](uint32_t col, uint32_t slot) {
+        // the small parts of q first: their sums lose least
+#pragma unroll
+        for (int part = kParts - 1; part >= 0; --part) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = (uint32_t)(k >> 2) * kBlock + (uint32_t)(k & 3) * 32u;
+            mma_ss(tmem + col, b_desc(sq + (uint32_t)part * kTile + off), b_desc(ring + slot * kTile + off), idS,
+                   part != kParts - 1 || k != 0);
+          }
+        }
+      };
+      auto issue_o = [&](uint32_t col, uint32_t slot) {
+#pragma unroll
+        for (int part = kParts - 1; part >= 0; --part) {
+#pragma unroll
+          for (int k = 0; k < kKeys / 16; ++k)
+            mma_ts(tmem + kOCol, tmem + col + (uint32_t)k * (8u * kParts) + (uint32_t)part * 8u,
+                   b_desc_rows(ring + slot * kTile + (uint32_t)k * 2048u, kBlock), idO, part != kParts - 1 || k != 0);
+        }
+      };
+      for (uint32_t e = 0; w.ok; ++e) {
+        w.on(s.piece_full + (e & 1), (e >> 1) & 1);
+        if (!w.ok) break;
+        const TreePiece pc = s.piece[e & 1];
+        mbar_arrive(s.piece_empty + (e & 1));
+        if (pc.b < 0) break;
+        w.on(&s.q_ready, f & 1);
+        if (!w.ok) break;
+        for (uint32_t i = 0; i < nq; ++i, r.next()) mbar_arrive(s.kv_empty + r.slot);
+        const uint32_t n = (uint32_t)ceil_div(pc.end - pc.begin, kKeys);
+        for (uint32_t j = 0; j <= n; ++j) {
+          if (j < n) {
+            const uint32_t t = g + j;
+            w.on(s.kv_full + r.slot, r.phase);
+            if (!w.ok) break;
+            tmem_fence_after();
+            issue_s((t & 1) * kBuf + kSOff, r.slot);
+            mma_commit(smem_addr(s.s_full + (t & 1)));
+            mma_commit(smem_addr(s.kv_empty + r.slot));
+            r.next();
+          }
+          if (j > 0) {
+            const uint32_t t = g + j - 1;
+            w.on(s.kv_full + r.slot, r.phase);
+            w.on(s.p_full + (t & 1), (t >> 1) & 1);
+            if (t > 0) w.on(s.o_empty + ((t - 1) & 1), ((t - 1) >> 1) & 1);
+            if (!w.ok) break;
+            tmem_fence_after();
+            issue_o((t & 1) * kBuf, r.slot);
+            mma_commit(smem_addr(&s.o_full));
+            mma_commit(smem_addr(s.kv_empty + r.slot));
+            r.next();
+          }
+        }
+        g += n;
+        ++f;
+      }
+      if (!w.ok) {
+        s.abort = 1;
+        atomicOr(p.err, kErrTimeout);
+      }
+      // every product has completed before tensor memory is given back
+      mma_commit(smem_addr(&s.drain));
+      if (!mbar_wait_for(&s.drain, 0, w.limit)) atomicOr(p.err, kErrTimeout);
+    }
+  } else if (warp < 4) {
+    // ------------------------------------------------------------ softmax
+    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    const int32_t row = warp * 32 + lane;  // of the block = lane of tensor memory
+    // A scale of either sign, or 0, goes into q, so that scores rise with S.
+    const float f = p.qk_scale == 0.f ? 1.f : fabsf(p.qk_scale);
+    const uint32_t flip = p.qk_scale < 0.f ? 0x80000000u : 0u, keepq = p.qk_scale == 0.f ? 0u : 0xffffffffu;
+    const uint64_t f2 = pack2(f, f);
+    uint32_t g = 0, u = 0;
+    TreePiece pc;
+    for (uint32_t e = 0; take(e, pc); ++e) {
+      const int32_t n = ceil_div(pc.end - pc.begin, kKeys), P = pc.len - pc.m;
+      // q: three bf16 parts of the row in the swizzled layout of an MMA operand.  The products of the piece before
+      // have read theirs: its last S has been seen.  A lane starts at a 16-byte chunk of its own, off the others' banks.
+      for (uint32_t i = 0; i < nq; ++i) w.on(s.kv_full + (u + i) % kSlots, ((u + i) / kSlots) & 1);
+      {
+        constexpr uint32_t kC = D / 4;  // fp32 chunks of a row
+        const uint32_t from = ring + ((u + (uint32_t)row / Lay::kQRowsPerSlot) % kSlots) * kTile +
+                              ((uint32_t)row % Lay::kQRowsPerSlot) * (D * 4);
+#pragma unroll 4
+        for (uint32_t i = 0; i < kC; ++i) {
+          const uint32_t c = (i + (uint32_t)lane) % kC;
+          uint4 x = make_uint4(0u, 0u, 0u, 0u);
+          if (row < live) x = lds128u(from + c * 16u);
+          uint32_t a[kParts], b[kParts];
+          cut3(__uint_as_float((x.x & keepq) ^ flip), __uint_as_float((x.y & keepq) ^ flip), a);
+          cut3(__uint_as_float((x.z & keepq) ^ flip), __uint_as_float((x.w & keepq) ^ flip), b);
+          const uint32_t c8 = c >> 1;   // chunk of eight bf16
+          const uint32_t to = sq + (c8 >> 3) * kBlock + (uint32_t)row * 128u + (((c8 ^ (uint32_t)row) & 7u) << 4) + (c & 1u) * 8u;
+#pragma unroll
+          for (int part = 0; part < kParts; ++part) sts64(to + (uint32_t)part * kTile, a[part], b[part]);
+        }
+      }
+      fence_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.q_ready);
+      uint64_t anc = 0, unfit = 0;
+      if (pc.end > P) {
+        const Ancestors all = tree_ancestors(p.tree, pc.b, pc.m, p.err);
+        anc = all.of((row0 + row) % p.tree.n - (p.tree.n - pc.m));
+      }
+      float m = -INFINITY, l = 0.f;
+      for (int32_t j = 0; j < n; ++j) {
+        const uint32_t t = g + (uint32_t)j, buf = t & 1;
+        const int32_t t0 = pc.begin + j * kKeys;
+        const uint32_t at = tmem + buf * kBuf + lanes;
+        w.on(s.s_full + buf, (t >> 1) & 1);
+        tmem_fence_after();
+        float x[kKeys];
+        {
+          uint32_t* xr = reinterpret_cast<uint32_t*>(x);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) TmemRow<32>::load(at + kSOff + 32u * c, xr + 32 * c);
+          tmem_wait_loads();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) TmemRow<32>::tie(xr + 32 * c);
+        }
+        if (t0 + kKeys > P) {
+          const TileMask mask = tile_mask(P, anc, t0);
+#pragma unroll
+          for (int c = 0; c < kKeys; ++c) x[c] = mask.w[c >> 5] >> (c & 31) & 1u ? x[c] : -INFINITY;
+        }
+        float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < kKeys; c += 8)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) top4[i] = max3(top4[i], x[c + 2 * i], x[c + 2 * i + 1]);
+        const float top = max3(fmaxf(top4[0], top4[1]), top4[2], top4[3]);
+        const float mn = fmaxf(m, top == -INFINITY ? -INFINITY : top * f);
+        const float alpha = m == mn ? 1.f : ex2(m - mn);  // 0 from -inf
+        const float base = mn == -INFINITY ? 0.f : mn;
+        const uint64_t base2 = pack2(-base, -base);
+        uint64_t sum2[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
+#pragma unroll
+        for (int c = 0; c < kKeys / 16; ++c) {
+          uint32_t a[8 * kParts];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float y0, y1;
+            unpack2(fma2(pack2(x[16 * c + 2 * i], x[16 * c + 2 * i + 1]), f2, base2), y0, y1);
+            y0 = ex2(y0);
+            y1 = ex2(y1);
+            sum2[i & 1] = add2(sum2[i & 1], pack2(y0, y1));
+            uint32_t part[kParts];
+            cut3(y0, y1, part);
+#pragma unroll
+            for (int k = 0; k < kParts; ++k) a[8 * k + i] = part[k];
+          }
+          TmemRow<16>::store(at + (uint32_t)c * 24u, a);
+          TmemRow<8>::store(at + (uint32_t)c * 24u + 16u, a + 16);
+        }
+        float s0, s1, s2, s3;
+        unpack2(sum2[0], s0, s1);
+        unpack2(sum2[1], s2, s3);
+        l = fmaf(l, alpha, (s0 + s1) + (s2 + s3));
+        m = mn;
+        // the sums of two tiles ago have read their max
+        if (t >= 2) w.on(s.o_empty + buf, ((t - 2) >> 1) & 1);
+        s.m[buf][row] = m;
+        if (t0 + kKeys > P) {
+          // V's rows at or past the length may hold anything, and so may those of the drafts, which not every
+          // row sees: 0 * NaN is not 0.  Values that are no numbers become 0 here and are added to the rows that
+          // see them at the end.
+          const uint32_t uv = u + nq + (uint32_t)(j == n - 1 ? 2 * n - 1 : 2 * j + 2), slot = uv % kSlots;
+          w.on(s.kv_full + slot, (uv / kSlots) & 1);
+          constexpr int kChunks = D / 8;
+          const int32_t first = P > t0 ? P - t0 : 0, end = pc.len - t0 < kKeys ? pc.len - t0 : kKeys;
+          for (int32_t i = row; i < (kKeys - first) * kChunks; i += 128) {
+            const int32_t v_row = first + i / kChunks;
+            const uint32_t c = (uint32_t)(i % kChunks);
+            const uint32_t a = ring + slot * kTile + (c >> 3) * kBlock + (uint32_t)v_row * 128u + ((c & 7u) << 4);
+            if (v_row >= end) {
+              sts128(a, 0u, 0u, 0u, 0u);
+              continue;
+            }
+            const uint4 v = lds128u(a);
+            uint32_t v4[4] = {v.x, v.y, v.z, v.w};
+            bool any = false;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if ((v4[k] & 0x7f80u) == 0x7f80u) v4[k] &= 0xffff0000u, any = true;
+              if ((v4[k] & 0x7f800000u) == 0x7f800000u) v4[k] &= 0x0000ffffu, any = true;
+            }
+            if (any) {
+              sts128(a, v4[0], v4[1], v4[2], v4[3]);
+              unfit |= 1ull << (t0 + v_row - P);
+            }
+          }
+          fence_async();
+        }
+        tmem_wait_stores();
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s.p_full + buf);
+      }
+      if (e >= 1) w.on(&s.fin_empty, (e - 1) & 1);
+      s.l[row] = l;
+      unfit = ((uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(unfit >> 32)) << 32) |
+              __reduce_or_sync(0xffffffffu, (uint32_t)unfit);
+      if (lane == 0) s.unfit[warp] = unfit;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.fin_full);
+      g += (uint32_t)n;
+      u += nq + 2 * (uint32_t)n;
+      if (!w.all()) break;
+    }
+    if (!w.ok) {
+      s.abort = 1;
+      atomicOr(p.err, kErrTimeout);
+    }
+  } else {
+    // ------------------------------------------------------------ sums
+    const uint32_t at = tmem + kOCol + ((uint32_t)((warp - 4) * 32) << 16);
+    const int32_t row = (warp - 4) * 32 + lane;
+    tree_empty_rows<D, kRows>(p, range, sub, row, kRows);
+    uint32_t g = 0;
+    TreePiece pc;
+    for (uint32_t e = 0; take(e, pc); ++e) {
+      const int32_t n = ceil_div(pc.end - pc.begin, kKeys);
+      uint64_t acc[D / 2];
+#pragma unroll
+      for (int i = 0; i < D / 2; ++i) acc[i] = 0;
+      float m = -INFINITY;
+      for (int32_t j = 0; j < n; ++j) {
+        const uint32_t t = g + (uint32_t)j, buf = t & 1;
+        w.on(s.p_full + buf, (t >> 1) & 1);
+        const float mn = s.m[buf][row];
+        const float alpha = m == mn ? 1.f : ex2(m - mn);
+        m = mn;
+        const uint64_t alpha2 = pack2(alpha, alpha);
+        w.on(&s.o_full, t & 1);
+        tmem_fence_after();
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          float o[32];
+          tmem_load<32>(at + 32u * c, o);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[16 * c + i] = fma2(acc[16 * c + i], alpha2, pack2(o[2 * i], o[2 * i + 1]));
+        }
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s.o_empty + buf);
+      }
+      g += (uint32_t)n;
+      w.on(&s.fin_full, e & 1);
+      const float l = s.l[row];
+      uint64_t unfit = s.unfit[0] | s.unfit[1] | s.unfit[2] | s.unfit[3];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.fin_empty);
+      const bool writes = row < live && (row0 + row) % p.tree.n >= p.tree.n - pc.m;
+      float o[D];
+#pragma unroll
+      for (int i = 0; i < D / 2; ++i) unpack2(acc[i], o[2 * i], o[2 * i + 1]);
+      if (unfit) {
+        const Ancestors all = tree_ancestors(p.tree, pc.b, pc.m, p.err);
+        unfit &= all.of((row0 + row) % p.tree.n - (p.tree.n - pc.m));
+        while (unfit) {
+          const int32_t place = pc.len - pc.m + __ffsll((long long)unfit) - 1;
+          unfit &= unfit - 1;
+          int64_t v_row = ((int64_t)pc.b * p.Hkv + pc.h) * p.kv.capacity + place;
+          if (p.kv.paged) {
+            const int32_t page = __ldg(p.kv.block_table + (int64_t)pc.b * p.kv.max_pages + place / p.kv.page_size);
+            if (page < 0 || page >= p.kv.num_pages) continue;
+            v_row = ((int64_t)page * p.Hkv + pc.h) * p.kv.page_size + place % p.kv.page_size;
+          }
+          const uint32_t* v = static_cast<const uint32_t*>(p.kv.v) + v_row * (D / 2);
+#pragma unroll
+          for (int i = 0; i < D / 2; ++i) {
+            const uint32_t x = __ldg(v + i);
+            if ((x & 0x7f80u) == 0x7f80u) o[2 * i] += bf16_lo(x);
+            if ((x & 0x7f800000u) == 0x7f800000u) o[2 * i + 1] += bf16_hi(x);
+          }
+        }
+      }
+      if (writes && w.ok) {
+        const int64_t out = ((int64_t)pc.b * p.Hkv + pc.h) * p.rows + row0 + row;
+        const int64_t state = ((int64_t)pc.slot * p.nsub + sub) * kRows + row;
+        float* to = pc.slot < 0 ? p.out + out * D : p.o_part + state * D;
+        const float inv = pc.slot >= 0 ? 1.f : (l == 0.f ? 0.f : 1.f / l);
+#pragma unroll
+        for (int i = 0; i < D; i += 4)
+          *reinterpret_cast<float4*>(to + i) = make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv);
+        if (pc.slot >= 0) {
+          p.m_part[state] = m;
+          p.l_part[state] = l;
+        } else if (p.lse) {
+          p.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l)) * kTreeLn2;
+        }
+      }
+      if (!w.all()) break;
+    }
+    if (!w.ok) {
+      s.abort = 1;
+      atomicOr(p.err, kErrTimeout);
+    }
+  }
+  tmem_fence_before();
+  cta_sync();
+  if (warp == kMmaWarp) {
+    tmem_fence_after();
+    tmem_free_all(tmem);
+  }
+}
+
+template <int D>
+cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p, cudaStream_t stream) {
+  const cudaError_t e = allow_smem<fd_tree_mma_kernel<D>>((int)Layout<D>::kBytes);
+  if (e != cudaSuccess) return e;
+  return launch_early(fd_tree_mma_kernel<D>, (unsigned)(p.ranges * p.nsub), kThreads, Layout<D>::kBytes, stream, tk, tv, p);
+}
+
+}  // namespace
+
+cudaError_t launch_tree_mma(int D, const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p,
+                            cudaStream_t stream) {
+  if (D == 128) return launch<128>(tk, tv, p, stream);
+  if (D == 64) return launch<64>(tk, tv, p, stream);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace fdk
