@@ -1104,6 +1104,8 @@ fd_status fd_decode_tree(const float* q, const fd_tree_desc* tree, const fd_kv_d
   p.rows = t.rows;
   p.nsub = t.nsub;
   p.ranges = t.ranges;
+  p.join_pairs = (int64_t)B * Hkv <= t.ranges;
+  p.n_joins = p.join_pairs ? B * Hkv : t.ranges;
   p.max_len = max_seq_len;
   p.qk_scale = (float)((double)scale * 1.4426950408889634);
   p.wait_ns = (uint64_t)g_wait_ns.load(std::memory_order_relaxed);

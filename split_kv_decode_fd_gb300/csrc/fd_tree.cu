@@ -40,8 +40,7 @@ __global__ void __launch_bounds__(kCoreThreads, kTreeCtasCore) fd_tree_core_kern
   constexpr int kCols = D / 64;  // float4 of output a row and thread
   pdl_launch_dependents();
   pdl_wait();
-  tree_empty_rows<D, kRows>(p, range, sub, tid, kCoreThreads);
-  if (tid == 0 && sub == 0) p.joins[range].b = -1;
+  tree_no_rows<D, kRows>(p, range, sub, tid, kCoreThreads);  // thread 0 also says what its pieces leave to join
   TreeWalk walk(p, range);  // every warp walks; the pieces that count are those of warp 0
   for (;;) {
     if (warp == 0) {
@@ -50,7 +49,7 @@ __global__ void __launch_bounds__(kCoreThreads, kTreeCtasCore) fd_tree_core_kern
       if (lane == 0) {
         s.piece = pc;
         s.more = found;
-        if (found && sub == 0 && pc.slot >= 0 && pc.begin == 0) p.joins[range] = TreeJoin{pc.b, pc.h, pc.last, 0};
+        if (found && sub == 0) walk.say(pc);
       }
     }
     __syncthreads();
@@ -216,53 +215,65 @@ __global__ void __launch_bounds__(kCoreThreads, kTreeCtasCore) fd_tree_core_kern
   }
 }
 
-// Joins the states of the pair that begins in share f and goes on: a warp a row,
-// the weights of 32 shares at a time in its lanes.  With M the largest m,
+// Joins the states of a pair: a warp a row, the m and l of 32 shares at a time in its lanes.
+// With M the largest m so far,
 //     out = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k.
 template <int D, int Rows>
-__global__ void __launch_bounds__(256) fd_tree_join_kernel(const TreeParams p) {
-  constexpr int kPer = D / 32;  // channels a lane
+__global__ void __launch_bounds__(256, 4) fd_tree_join_kernel(const TreeParams p) {
+  constexpr int kPer = D / 32;   // channels a lane
+  constexpr int kAhead = 8;      // states whose O is on its way
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int32_t r = (int32_t)(w % Rows);
-  const int32_t sub = (int32_t)(w / Rows % p.nsub), f = (int32_t)(w / Rows / p.nsub);
-  if (f >= p.ranges) return;
+  const int32_t w = (int32_t)(blockIdx.x * 8 + (threadIdx.x >> 5));
+  const int32_t r = w % Rows, sub = w / Rows % p.nsub, f = w / Rows / p.nsub;
+  if (f >= p.n_joins) return;
   const TreeJoin j = p.joins[f];
   const int32_t row = sub * Rows + r;
   if (j.b < 0 || row >= p.rows || row % p.tree.n < p.tree.n - tree_tokens(p.tree, j.b)) return;
-  const int32_t count = j.last - f + 1;
-  auto state = [&](int32_t k) { return ((int64_t)(2 * (f + k) + (k == 0 ? 1 : 0)) * p.nsub + sub) * Rows + r; };
-  float M = -INFINITY;
-  for (int32_t k = lane; k < count; k += 32)
-    if (__ldcg(p.l_part + state(k)) != 0.f) M = fmaxf(M, __ldcg(p.m_part + state(k)));
-  M = warp_max(M);
-  float L = 0.f, acc[kPer] = {};
+  const int32_t count = j.last - j.first + 1;
+  auto state = [&](int32_t k) {
+    return ((int64_t)(2 * (j.first + k) + (k == 0 ? 1 : 0)) * p.nsub + sub) * Rows + r;
+  };
+  auto load = [&](int32_t k, float (&v)[kPer]) {
+    const float* o = p.o_part + state(k) * D + lane * kPer;
+    if constexpr (kPer == 4) {
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(o));
+      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+    } else {
+      const float2 x = __ldcg(reinterpret_cast<const float2*>(o));
+      v[0] = x.x, v[1] = x.y;
+    }
+  };
+  float M = -INFINITY, L = 0.f, acc[kPer] = {};
   for (int32_t k0 = 0; k0 < count; k0 += 32) {
-    float e = 0.f;
+    float l = 0.f, m = -INFINITY;
     if (k0 + lane < count) {
-      const float l = __ldcg(p.l_part + state(k0 + lane));
-      if (l != 0.f) {
-        e = exp2f(__ldcg(p.m_part + state(k0 + lane)) - M);
-        L = fmaf(e, l, L);
-      }
+      l = __ldcg(p.l_part + state(k0 + lane));
+      m = __ldcg(p.m_part + state(k0 + lane));
     }
     const int32_t stop = count - k0 < 32 ? count - k0 : 32;
-#pragma unroll 8
-    for (int32_t k = 0; k < stop; ++k) {
-      const float wk = __shfl_sync(0xffffffffu, e, k);
-      const float* o = p.o_part + state(k0 + k) * D + lane * kPer;
-      float v[kPer];
-      if constexpr (kPer == 4) {
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(o));
-        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-      } else {
-        const float2 x = __ldcg(reinterpret_cast<const float2*>(o));
-        v[0] = x.x, v[1] = x.y;
-      }
+    float v[kAhead][kPer];
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) acc[i] = fmaf(wk, v[i], acc[i]);
+    for (int i = 0; i < kAhead; ++i)
+      if (i < stop) load(k0 + i, v[i]);
+    const float top = fmaxf(M, warp_max(l != 0.f ? m : -INFINITY));
+    const float alpha = M == top ? 1.f : exp2f(M - top);
+    const float e = l != 0.f ? exp2f(m - top) : 0.f;  // a state that has seen nothing has l = 0
+    M = top;
+    L = fmaf(L, alpha, e * l);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) acc[i] *= alpha;
+    for (int32_t k = 0; k < stop; k += kAhead) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const float wk = __shfl_sync(0xffffffffu, e, k + i);
+        if (k + i < stop) {
+#pragma unroll
+          for (int c = 0; c < kPer; ++c) acc[c] = fmaf(wk, v[i][c], acc[c]);
+          if (k + i + kAhead < stop) load(k0 + k + i + kAhead, v[i]);
+        }
+      }
     }
   }
   L = warp_sum(L);
@@ -285,7 +296,7 @@ cudaError_t launch_core(const TreeParams& p, cudaStream_t stream) {
 
 template <int D, int Rows>
 cudaError_t launch_join(const TreeParams& p, cudaStream_t stream) {
-  return launch_early(fd_tree_join_kernel<D, Rows>, (unsigned)(p.ranges * p.nsub * (Rows / 8)), 256, 0, stream, p);
+  return launch_early(fd_tree_join_kernel<D, Rows>, (unsigned)(p.n_joins * p.nsub * (Rows / 8)), 256, 0, stream, p);
 }
 
 }  // namespace

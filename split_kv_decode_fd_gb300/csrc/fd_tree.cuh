@@ -93,44 +93,57 @@ struct TreePiece {
   int32_t begin, end;  // places, `end` clipped to the length
   int32_t len, m;      // the sequence's length and its tokens
   int32_t slot;        // -1: the piece is the whole pair
-  int32_t last;        // of a piece that begins a pair: the last share that holds the pair
+  int32_t tiles;       // of the pair
+  int64_t v;           // the pair's first cost unit
 };
 
 // The pieces of one share, walked by one warp (all lanes alike).  Sequences
-// without keys or without tokens cost nothing and have no piece.
+// without keys or without tokens cost nothing and have no piece.  Lane l holds length and
+// tokens of sequence base + l.
 struct TreeWalk {
   const TreeParams& p;
   int64_t units;
   int32_t used, range;
   int64_t pos, end;
   int32_t b, h, len, m, tiles;
-  int64_t v, u;  // first unit of the pair, units of a pair of its sequence
+  int64_t v;             // first unit of the pair
+  int32_t u;             // units of a pair of its sequence
+  int32_t base, my_len, my_m;
 
   __device__ __forceinline__ bool uniform() const { return !p.seq_lens && !p.tree.new_lens; }
   __device__ __forceinline__ int32_t piece_units() const { return p.seq_lens ? kTreePieceUnits : 0; }
-  __device__ __forceinline__ int64_t units_of(int32_t bb) const {
-    if (tree_tokens(p.tree, bb) == 0) return 0;
-    return pair_units(ceil_div(tree_len(p, bb), kPlanTile), piece_units());
+  __device__ __forceinline__ int32_t units_of(int32_t n, int32_t tokens) const {
+    return tokens > 0 ? (int32_t)pair_units(ceil_div(n, kPlanTile), piece_units()) : 0;
+  }
+  __device__ __forceinline__ void block(int32_t b0) {
+    const int32_t i = b0 + (int32_t)(threadIdx.x & 31);
+    base = b0;
+    my_len = i < p.B ? tree_len(p, i) : 0;
+    my_m = i < p.B ? tree_tokens(p.tree, i) : 0;
   }
   __device__ __forceinline__ void load(int32_t bb) {
+    if (!uniform() && (bb < base || bb >= base + 32)) block(bb & ~31);
     b = bb;
-    len = tree_len(p, bb);
-    m = tree_tokens(p.tree, bb);
+    len = uniform() ? p.max_len : __shfl_sync(0xffffffffu, my_len, bb & 31);
+    m = uniform() ? p.tree.n : __shfl_sync(0xffffffffu, my_m, bb & 31);
     tiles = m > 0 ? ceil_div(len, kPlanTile) : 0;
-    u = pair_units(tiles, piece_units());
+    u = units_of(len, m);
   }
 
   __device__ __forceinline__ TreeWalk(const TreeParams& p_, int32_t range_) : p(p_), range(range_) {
     const int lane = threadIdx.x & 31;
     pos = end = 0;
-    b = h = 0;
+    b = h = base = my_len = my_m = 0;
     v = 0;
     if (uniform()) {
       load(0);
       units = (int64_t)p.B * p.Hkv * u;
     } else {
       int64_t sum = 0;
-      for (int32_t i = lane; i < p.B; i += 32) sum += units_of(i);
+      for (int32_t i = (p.B - 1) & ~31; i >= 0; i -= 32) {  // the first block stays at hand
+        block(i);
+        sum += units_of(my_len, my_m);
+      }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       units = sum * p.Hkv;
@@ -142,14 +155,15 @@ struct TreeWalk {
     // the sequence that holds `pos`
     if (uniform()) {
       const int64_t i = div_floor(pos, u);
-      b = (int32_t)(i / p.Hkv);
-      h = (int32_t)(i % p.Hkv);
+      b = (int32_t)div_floor(i, p.Hkv);
+      h = (int32_t)(i - (int64_t)b * p.Hkv);
       v = i * u;
       return;
     }
     int64_t before = 0;
     for (int32_t i0 = 0; i0 < p.B; i0 += 32) {
-      int64_t mine = i0 + lane < p.B ? units_of(i0 + lane) : 0;
+      if (i0 != base) block(i0);
+      const int64_t mine = units_of(my_len, my_m);
       int64_t incl = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -159,10 +173,10 @@ struct TreeWalk {
       const unsigned past = __ballot_sync(0xffffffffu, (before + incl) * p.Hkv > pos);
       if (past) {
         const int l = __ffs(past) - 1;
-        const int64_t start = before + __shfl_sync(0xffffffffu, incl - mine, l);
+        const int64_t start = (before + __shfl_sync(0xffffffffu, incl - mine, l)) * p.Hkv;
         load(i0 + l);
-        h = (int32_t)div_floor(pos - start * p.Hkv, u);
-        v = start * p.Hkv + (int64_t)h * u;
+        h = (int32_t)div_floor(pos - start, u);
+        v = start + (int64_t)h * u;
         return;
       }
       before += __shfl_sync(0xffffffffu, incl, 31);
@@ -178,7 +192,7 @@ struct TreeWalk {
       const int32_t lo = first_tile_at(pos, v, piece_units());
       int32_t hi = first_tile_at(stop, v, piece_units());
       hi = hi < tiles ? hi : tiles;
-      bool found = hi > lo;
+      const bool found = hi > lo;
       if (found) {
         pc.b = b;
         pc.h = h;
@@ -187,7 +201,8 @@ struct TreeWalk {
         pc.len = len;
         pc.m = m;
         pc.slot = lo == 0 && hi == tiles ? -1 : 2 * range + (lo == 0 ? 1 : 0);
-        pc.last = cta_of_unit(units, used, v + piece_units() + (int64_t)kTileUnits * (tiles - 1));
+        pc.tiles = tiles;
+        pc.v = v;
       }
       pos = stop;
       if (pos == pend) {
@@ -207,15 +222,30 @@ struct TreeWalk {
     }
     return false;
   }
+
+  // Says of the pair that `pc` begins (if it does) whether it goes on, for the join; one lane.
+  __device__ __forceinline__ void say(const TreePiece& pc) const {
+    if (pc.begin != 0 || (pc.slot < 0 && !p.join_pairs)) return;
+    TreeJoin j{-1, pc.h, range, range};
+    if (pc.slot >= 0) {
+      j.b = pc.b;
+      j.last = cta_of_unit(units, used, pc.v + piece_units() + (int64_t)kTileUnits * (pc.tiles - 1));
+    }
+    p.joins[p.join_pairs ? (int64_t)pc.b * p.Hkv + pc.h : range] = j;
+  }
 };
 
-// Sequences without keys: no share holds them, and the rows of their tokens get
-// out = 0, lse = -inf from the CTAs of share b % ranges.
+// Sequences without keys or tokens: no share holds them.  The rows of their tokens get
+// out = 0, lse = -inf, and their pairs nothing to join, from the CTAs of share b % ranges.
 template <int D, int Rows>
-__device__ __forceinline__ void tree_empty_rows(const TreeParams& p, int32_t range, int32_t sub, int tid, int threads) {
+__device__ __forceinline__ void tree_no_rows(const TreeParams& p, int32_t range, int32_t sub, int tid, int threads) {
+  if (!p.join_pairs && sub == 0 && tid == 0) p.joins[range].b = -1;
   for (int32_t b = range; b < p.B; b += p.ranges) {
-    if (tree_len(p, b) != 0) continue;
-    const int32_t pad = p.tree.n - tree_tokens(p.tree, b);
+    const int32_t len = tree_len(p, b), m = tree_tokens(p.tree, b);
+    if (p.join_pairs && sub == 0 && (len == 0 || m == 0))
+      for (int32_t h = tid; h < p.Hkv; h += threads) p.joins[(int64_t)b * p.Hkv + h].b = -1;
+    if (len != 0) continue;
+    const int32_t pad = p.tree.n - m;
     const int32_t r0 = sub * Rows, r1 = r0 + Rows < p.rows ? r0 + Rows : p.rows;
     for (int64_t i = tid; i < (int64_t)p.Hkv * (r1 - r0); i += threads) {
       const int32_t row = r0 + (int32_t)(i % (r1 - r0));

@@ -37,12 +37,12 @@ struct TreeView {
 // A pair that lies within a share is finished there.  Otherwise its states go
 // to o_part, m_part (base 2) and l_part, and a second kernel joins them.  A
 // share has at most two unfinished pieces: one that goes on with a pair begun in
-// an earlier share (slot 2 r), and one that begins a pair (slot 2 r + 1, whose
-// place in joins says which pair it is and where it ends).  Their number does not
-// grow with the batch.
+// an earlier share (slot 2 r), and one that begins a pair (slot 2 r + 1).  Their number does not
+// grow with the batch.  Where a pair begins, joins says whether and how far it goes on: an
+// entry for each pair, or for each share where these are fewer.
 struct TreeJoin {
-  int32_t b, h, last;  // sequence (-1: none), KV head, last share that holds the pair
-  int32_t pad;
+  int32_t b, h;         // sequence (-1: nothing to join), KV head
+  int32_t first, last;  // shares that hold the pair
 };
 
 struct TreeParams {
@@ -55,11 +55,12 @@ struct TreeParams {
   float* o_part;               // [2 ranges][nsub][tree_rows()][D]
   float* m_part;               // [2 ranges][nsub][tree_rows()]
   float* l_part;
-  TreeJoin* joins;             // [ranges]
+  TreeJoin* joins;             // [n_joins]
   unsigned* err;
   int32_t B, Hq, Hkv, g;
   int32_t rows;                // g * n
   int32_t nsub, ranges;
+  int32_t n_joins, join_pairs; // join_pairs: an entry for each pair
   int32_t max_len;
   float qk_scale;              // scale * log2(e)
   uint64_t wait_ns;            // limit of every wait (0: the default)

@@ -13,7 +13,7 @@
 // unit drop bits.  Six products of 8 k-steps make 3072 cycles a tile of 128 channels, and a
 // tile's 64 KB at an SM's share of the memory rate some 3000.
 //
-// Ten warps:
+// Eleven warps:
 //   0-3  softmax, thread = row: reads S, masks, keeps the running max and sum, writes P
 //        over S; cuts q at the start of a piece.
 //   4-7  sums, thread = row: O of each tile times what the max has moved by; writes the
@@ -21,8 +21,8 @@
 //   8    copies: walks the share, announces its pieces, brings q (by bulk copies) and the K and V
 //        tiles (16-row x 128-byte boxes, 128-byte swizzle) through one ring of slots
 //        in the order of their use: q, K0, K1, V0, K2, V1, ... , V(n-1).
-//   9    products, one thread: S(j+1) before O(j), so that the tensor core works on S while
-//        the softmax of the tile before runs.
+//   9, 10  products, one thread of each: S, and O.  While the softmax of a tile runs, the tensor
+//        core has the S of the next and the O of the one before.
 #include <atomic>
 
 #include "fd_tcgen05.cuh"
@@ -33,9 +33,10 @@ namespace {
 
 constexpr int kRows = kTreeRowsMma;
 constexpr int kKeys = kPlanTile;
-constexpr int kThreads = 320;
+constexpr int kThreads = 352;
 constexpr int kParts = 3;                 // bf16 numbers that q and p are cut into
-constexpr int kCopyWarp = 8, kMmaWarp = 9;
+constexpr int kCopyWarp = 8, kSWarp = 9;  // and O: 10
+constexpr int kPBufs = 4;                // barriers of P and places for a tile's max
 // Tensor memory: two S / P buffers and O.  P takes 8 columns for each part of 16 keys, 192 in
 // all, and S the last 128 of them: a chunk of P never reaches an unread chunk of S.
 constexpr uint32_t kBuf = 192, kSOff = 64, kOCol = 384;
@@ -49,24 +50,24 @@ struct Layout {
   static constexpr uint32_t kSlots = D == 128 ? 4 : 8;
   static constexpr uint32_t kMisc = kRing + kSlots * kTile;
   static constexpr uint32_t kQRowsPerSlot = kTile / (D * 4);  // fp32 rows of q
-  static constexpr uint32_t kBytes = kMisc + 2048 + 1024;     // 1024: the base is aligned up
+  static constexpr uint32_t kBytes = kMisc + 3072;
   static_assert(kBytes <= 232448, "shared memory");
 };
 
 // Behind the ring.
 struct Misc {
   uint64_t kv_full[8], kv_empty[8];
-  uint64_t s_full[2], p_full[2], o_empty[2];
+  uint64_t s_full[2], p_empty[2], o_empty[2], p_full[kPBufs];
   uint64_t piece_full[2], piece_empty[2];
-  uint64_t o_full, q_ready, fin_full, fin_empty, drain;
+  uint64_t o_full, q_ready, fin_full, fin_empty, drain[2];
   uint32_t tmem;
   volatile int abort;
   TreePiece piece[2];
-  float m[2][kRows];      // running max of the last tiles
+  float m[kPBufs][kRows]; // running max of the last tiles
   float l[kRows];         // a piece's sums
   uint64_t unfit[4];      // tokens whose values are not finite, as the softmax warps met them
 };
-static_assert(sizeof(Misc) <= 2048, "Misc");
+static_assert(sizeof(Misc) <= 3072, "Misc");
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -108,6 +109,17 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, ui
 __device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
   asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
+// 32 bytes in one store where the address allows it: 16-byte stores of rows far apart send each sector to L2 twice.
+__device__ __forceinline__ void store32(float* to, const float* v) {
+  if ((reinterpret_cast<uintptr_t>(to) & 31) == 0) {
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+                 "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<float4*>(to)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(to)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  }
+}
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // The upper 16 bits of both, x's in the low half: their bf16 truncations.
@@ -126,6 +138,14 @@ __device__ __forceinline__ void cut3(float x, float y, uint32_t (&w)[kParts]) {
   unpack2(sub2(pack2(a, b), pack2(trunc1(a), trunc1(b))), c, d);
   w[2] = trunc2(c, d);
 }
+
+// One lane of a converged warp, known as such to the compiler.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 // Waits of all roles: false when the CTA gives up or the limit runs out.
 struct Waits {
@@ -161,8 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                        const __grid_constant__ TreeParams p) {
   using Lay = Layout<D>;
   constexpr uint32_t kSlots = Lay::kSlots, kBlock = Lay::kBlock, kTile = Lay::kTile;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   Misc& s = *reinterpret_cast<Misc*>(smem + Lay::kMisc);
   const uint32_t sq = smem_addr(smem), ring = sq + Lay::kRing;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -171,6 +190,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int32_t live = p.rows - row0 < kRows ? p.rows - row0 : kRows;
   const uint32_t nq = ((uint32_t)live + Lay::kQRowsPerSlot - 1) / Lay::kQRowsPerSlot;
 
+  if ((sq & 1023u) != 0) {  // the swizzle goes by address; no room is left to align here
+    if (tid == 0) atomicOr(p.err, kErrTimeout);
+    return;
+  }
   if (tid == 0) {
     for (uint32_t i = 0; i < kSlots; ++i) {
       mbar_init(s.kv_full + i, 1);
@@ -178,16 +201,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(s.s_full + i, 1);
-      mbar_init(s.p_full + i, 4);
+      mbar_init(s.p_empty + i, 1);
       mbar_init(s.o_empty + i, 4);
       mbar_init(s.piece_full + i, 1);
-      mbar_init(s.piece_empty + i, 9);
+      mbar_init(s.piece_empty + i, 10);
+      mbar_init(s.drain + i, 1);
     }
+    for (int i = 0; i < kPBufs; ++i) mbar_init(s.p_full + i, 4);
     mbar_init(&s.o_full, 1);
     mbar_init(&s.q_ready, 4);
     mbar_init(&s.fin_full, 4);
     mbar_init(&s.fin_empty, 4);
-    mbar_init(&s.drain, 1);
     s.abort = 0;
     fence_barrier_init();
   }
@@ -195,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tensormap(&tmap_k);
     prefetch_tensormap(&tmap_v);
   }
-  if (warp == kMmaWarp) tmem_alloc_all(smem_addr(&s.tmem));
+  if (warp == kSWarp) tmem_alloc_all(smem_addr(&s.tmem));
   pdl_launch_dependents();
   tmem_fence_before();
   cta_sync();
@@ -204,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
   Waits w{&s, p.wait_ns ? (unsigned long long)p.wait_ns : kWaitLimitNs};
 
-  // The next piece, for a warp of the softmax or of the sums; false at the end.
+  // The next piece, for a warp; false at the end.
   auto take = [&](uint32_t e, TreePiece& pc) -> bool {
     w.on(s.piece_full + (e & 1), (e >> 1) & 1);
     if (!w.all()) return false;
@@ -218,7 +242,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ copies
     uint32_t u = 0, stalled = 0xffffffffu;
     Ring<kSlots> r;
-    if (lane == 0 && sub == 0) p.joins[range].b = -1;
     TreeWalk walk(p, range);
     const uint64_t once = policy_evict_first();
     const bool shared_keys = p.nsub > 1;  // other CTAs read them too: they stay in L2
@@ -230,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) {
         s.piece[e & 1] = pc;
         mbar_arrive(s.piece_full + (e & 1));
-        if (pc.b >= 0 && sub == 0 && pc.slot >= 0 && pc.begin == 0) p.joins[range] = TreeJoin{pc.b, pc.h, pc.last, 0};
+        if (pc.b >= 0 && sub == 0) walk.say(pc);
       }
       if (pc.b < 0) break;
       // q's rows lie side by side
@@ -317,78 +340,88 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (uint32_t i = first; i < u; ++i)
         if (i != stalled && !mbar_wait_for(s.kv_full + i % kSlots, (i / kSlots) & 1, w.limit)) atomicOr(p.err, kErrTimeout);
     }
-  } else if (warp == kMmaWarp) {
+  } else if (warp >= kSWarp) {
     // ------------------------------------------------------------ products
-    if (lane == 0) {
-      constexpr uint32_t idS = bf16_instr_desc(kRows, kKeys), idO = bf16_instr_desc(kRows, D, true);
-      Ring<kSlots> r;
-      uint32_t g = 0, f = 0;  // tiles and pieces so far
-      auto issue_s = [&](uint32_t col, uint32_t slot) {
-        // the small parts of q first: their sums lose least
-#pragma unroll
-        for (int part = kParts - 1; part >= 0; --part) {
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = (uint32_t)(k >> 2) * kBlock + (uint32_t)(k & 3) * 32u;
-            mma_ss(tmem + col, b_desc(sq + (uint32_t)part * kTile + off), b_desc(ring + slot * kTile + off), idS,
-                   part != kParts - 1 || k != 0);
-          }
-        }
-      };
-      auto issue_o = [&](uint32_t col, uint32_t slot) {
-#pragma unroll
-        for (int part = kParts - 1; part >= 0; --part) {
-#pragma unroll
-          for (int k = 0; k < kKeys / 16; ++k)
-            mma_ts(tmem + kOCol, tmem + col + (uint32_t)k * (8u * kParts) + (uint32_t)part * 8u,
-                   b_desc_rows(ring + slot * kTile + (uint32_t)k * 2048u, kBlock), idO, part != kParts - 1 || k != 0);
-        }
-      };
-      for (uint32_t e = 0; w.ok; ++e) {
-        w.on(s.piece_full + (e & 1), (e >> 1) & 1);
-        if (!w.ok) break;
-        const TreePiece pc = s.piece[e & 1];
-        mbar_arrive(s.piece_empty + (e & 1));
-        if (pc.b < 0) break;
+    // Every branch and operand is uniform over the warp as the compiler sees it (votes and shuffles), so that the
+    // products take their operands from uniform registers as they are.
+    constexpr uint32_t idS = bf16_instr_desc(kRows, kKeys), idO = bf16_instr_desc(kRows, D, true);
+    const uint32_t base = uniform(tmem), q0 = uniform(sq), ring0 = uniform(ring);
+    const bool is_s = uniform((uint32_t)warp) == kSWarp;
+    Ring<kSlots> r;
+    uint32_t g = 0, f = 0;  // tiles and pieces so far
+    TreePiece pc;
+    for (uint32_t e = 0; take(e, pc); ++e) {
+      const uint32_t n = uniform((uint32_t)ceil_div(pc.end - pc.begin, kKeys));
+      if (is_s) {
         w.on(&s.q_ready, f & 1);
-        if (!w.ok) break;
-        for (uint32_t i = 0; i < nq; ++i, r.next()) mbar_arrive(s.kv_empty + r.slot);
-        const uint32_t n = (uint32_t)ceil_div(pc.end - pc.begin, kKeys);
-        for (uint32_t j = 0; j <= n; ++j) {
-          if (j < n) {
-            const uint32_t t = g + j;
-            w.on(s.kv_full + r.slot, r.phase);
-            if (!w.ok) break;
-            tmem_fence_after();
-            issue_s((t & 1) * kBuf + kSOff, r.slot);
+        if (!w.all()) break;
+        for (uint32_t i = 0; i < nq; ++i, r.next())
+          if (elect_one()) mbar_arrive(s.kv_empty + r.slot);
+        for (uint32_t j = 0; j < n; ++j) {
+          const uint32_t t = g + j;
+          w.on(s.kv_full + r.slot, r.phase);
+          if (t >= 2) w.on(s.p_empty + (t & 1), ((t - 2) >> 1) & 1);
+          if (!w.all()) break;
+          tmem_fence_after();
+          if (elect_one()) {
+            const uint32_t d = base + (t & 1) * kBuf + kSOff, k = ring0 + r.slot * kTile;
+            // the small parts of q first: their sums lose least
+#pragma unroll
+            for (int part = kParts - 1; part >= 0; --part) {
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) {
+                const uint32_t off = (uint32_t)(i >> 2) * kBlock + (uint32_t)(i & 3) * 32u;
+                mma_ss(d, b_desc(q0 + (uint32_t)part * kTile + off), b_desc(k + off), idS, part != kParts - 1 || i != 0);
+              }
+            }
             mma_commit(smem_addr(s.s_full + (t & 1)));
             mma_commit(smem_addr(s.kv_empty + r.slot));
-            r.next();
           }
-          if (j > 0) {
-            const uint32_t t = g + j - 1;
-            w.on(s.kv_full + r.slot, r.phase);
-            w.on(s.p_full + (t & 1), (t >> 1) & 1);
-            if (t > 0) w.on(s.o_empty + ((t - 1) & 1), ((t - 1) >> 1) & 1);
-            if (!w.ok) break;
-            tmem_fence_after();
-            issue_o((t & 1) * kBuf, r.slot);
-            mma_commit(smem_addr(&s.o_full));
-            mma_commit(smem_addr(s.kv_empty + r.slot));
-            r.next();
-          }
+          __syncwarp();
+          // K(j + 1), or what follows the piece
+          r.next(j + 1 < n ? (j == 0 ? 1 : 2) : (n == 1 ? 2 : 3));
         }
-        g += n;
-        ++f;
+      } else {
+        r.next(nq + (n == 1 ? 1 : 2));
+        for (uint32_t j = 0; j < n; ++j) {
+          const uint32_t t = g + j;
+          w.on(s.kv_full + r.slot, r.phase);
+          w.on(s.p_full + t % kPBufs, (t / kPBufs) & 1);
+          if (t > 0) w.on(s.o_empty + ((t - 1) & 1), ((t - 1) >> 1) & 1);
+          if (!w.all()) break;
+          tmem_fence_after();
+          if (elect_one()) {
+            const uint32_t a = base + (t & 1) * kBuf, v = ring0 + r.slot * kTile;
+#pragma unroll
+            for (int part = kParts - 1; part >= 0; --part) {
+#pragma unroll
+              for (int i = 0; i < kKeys / 16; ++i)
+                mma_ts(base + kOCol, a + (uint32_t)i * (8u * kParts) + (uint32_t)part * 8u,
+                       b_desc_rows(v + (uint32_t)i * 2048u, kBlock), idO, part != kParts - 1 || i != 0);
+            }
+            mma_commit(smem_addr(&s.o_full));
+            mma_commit(smem_addr(s.p_empty + (t & 1)));
+            mma_commit(smem_addr(s.kv_empty + r.slot));
+          }
+          __syncwarp();
+          r.next(j + 2 < n ? 2 : 1);  // V(j + 1), or what follows the piece
+        }
       }
-      if (!w.ok) {
-        s.abort = 1;
-        atomicOr(p.err, kErrTimeout);
-      }
-      // every product has completed before tensor memory is given back
-      mma_commit(smem_addr(&s.drain));
-      if (!mbar_wait_for(&s.drain, 0, w.limit)) atomicOr(p.err, kErrTimeout);
+      if (!w.ok) break;
+      g += n;
+      ++f;
     }
+    if (!w.ok) {
+      s.abort = 1;
+      atomicOr(p.err, kErrTimeout);
+    }
+    // every product has completed before tensor memory is given back
+    if (elect_one()) {
+      uint64_t* done = s.drain + (is_s ? 0 : 1);
+      mma_commit(smem_addr(done));
+      if (!mbar_wait_for(done, 0, w.limit)) atomicOr(p.err, kErrTimeout);
+    }
+    __syncwarp();
   } else if (warp < 4) {
     // ------------------------------------------------------------ softmax
     const uint32_t lanes = (uint32_t)(warp * 32) << 16;
@@ -404,22 +437,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       // q: three bf16 parts of the row in the swizzled layout of an MMA operand.  The products of the piece before
       // have read theirs: its last S has been seen.  A lane starts at a 16-byte chunk of its own, off the others' banks.
       for (uint32_t i = 0; i < nq; ++i) w.on(s.kv_full + (u + i) % kSlots, ((u + i) / kSlots) & 1);
-      {
-        constexpr uint32_t kC = D / 4;  // fp32 chunks of a row
+      if (row < live || e == 0) {  // rows that are none stay 0
+        constexpr uint32_t kC = D / 4, kStep = 8;  // fp32 chunks of a row, at a time
         const uint32_t from = ring + ((u + (uint32_t)row / Lay::kQRowsPerSlot) % kSlots) * kTile +
                               ((uint32_t)row % Lay::kQRowsPerSlot) * (D * 4);
-#pragma unroll 4
-        for (uint32_t i = 0; i < kC; ++i) {
-          const uint32_t c = (i + (uint32_t)lane) % kC;
-          uint4 x = make_uint4(0u, 0u, 0u, 0u);
-          if (row < live) x = lds128u(from + c * 16u);
-          uint32_t a[kParts], b[kParts];
-          cut3(__uint_as_float((x.x & keepq) ^ flip), __uint_as_float((x.y & keepq) ^ flip), a);
-          cut3(__uint_as_float((x.z & keepq) ^ flip), __uint_as_float((x.w & keepq) ^ flip), b);
-          const uint32_t c8 = c >> 1;   // chunk of eight bf16
-          const uint32_t to = sq + (c8 >> 3) * kBlock + (uint32_t)row * 128u + (((c8 ^ (uint32_t)row) & 7u) << 4) + (c & 1u) * 8u;
+#pragma unroll 1
+        for (uint32_t i0 = 0; i0 < kC; i0 += kStep) {
+          uint4 x[kStep];
 #pragma unroll
-          for (int part = 0; part < kParts; ++part) sts64(to + (uint32_t)part * kTile, a[part], b[part]);
+          for (uint32_t i = 0; i < kStep; ++i) {
+            x[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (row < live) x[i] = lds128u(from + ((i0 + i + (uint32_t)lane) % kC) * 16u);
+          }
+#pragma unroll
+          for (uint32_t i = 0; i < kStep; ++i) {
+            const uint32_t c = (i0 + i + (uint32_t)lane) % kC, c8 = c >> 1;  // c8: chunk of eight bf16
+            uint32_t a[kParts], b[kParts];
+            cut3(__uint_as_float((x[i].x & keepq) ^ flip), __uint_as_float((x[i].y & keepq) ^ flip), a);
+            cut3(__uint_as_float((x[i].z & keepq) ^ flip), __uint_as_float((x[i].w & keepq) ^ flip), b);
+            const uint32_t to = sq + (c8 >> 3) * kBlock + (uint32_t)row * 128u + (((c8 ^ (uint32_t)row) & 7u) << 4) + (c & 1u) * 8u;
+#pragma unroll
+            for (int part = 0; part < kParts; ++part) sts64(to + (uint32_t)part * kTile, a[part], b[part]);
+          }
         }
       }
       fence_async();
@@ -485,9 +524,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         unpack2(sum2[1], s2, s3);
         l = fmaf(l, alpha, (s0 + s1) + (s2 + s3));
         m = mn;
-        // the sums of two tiles ago have read their max
-        if (t >= 2) w.on(s.o_empty + buf, ((t - 2) >> 1) & 1);
-        s.m[buf][row] = m;
+        // the sums are past the tile that had this place: S of this one came after O of the tile before the last, which
+        // waited for the sums of the one before that
+        s.m[t % kPBufs][row] = m;
         if (t0 + kKeys > P) {
           // V's rows at or past the length may hold anything, and so may those of the drafts, which not every
           // row sees: 0 * NaN is not 0.  Values that are no numbers become 0 here and are added to the rows that
@@ -522,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_stores();
         tmem_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(s.p_full + buf);
+        if (lane == 0) mbar_arrive(s.p_full + t % kPBufs);
       }
       if (e >= 1) w.on(&s.fin_empty, (e - 1) & 1);
       s.l[row] = l;
@@ -543,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ sums
     const uint32_t at = tmem + kOCol + ((uint32_t)((warp - 4) * 32) << 16);
     const int32_t row = (warp - 4) * 32 + lane;
-    tree_empty_rows<D, kRows>(p, range, sub, row, kRows);
+    tree_no_rows<D, kRows>(p, range, sub, row, kRows);
     uint32_t g = 0;
     TreePiece pc;
     for (uint32_t e = 0; take(e, pc); ++e) {
@@ -554,8 +593,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = -INFINITY;
       for (int32_t j = 0; j < n; ++j) {
         const uint32_t t = g + (uint32_t)j, buf = t & 1;
-        w.on(s.p_full + buf, (t >> 1) & 1);
-        const float mn = s.m[buf][row];
+        w.on(s.p_full + t % kPBufs, (t / kPBufs) & 1);
+        const float mn = s.m[t % kPBufs][row];
         const float alpha = m == mn ? 1.f : ex2(m - mn);
         m = mn;
         const uint64_t alpha2 = pack2(alpha, alpha);
@@ -609,8 +648,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         float* to = pc.slot < 0 ? p.out + out * D : p.o_part + state * D;
         const float inv = pc.slot >= 0 ? 1.f : (l == 0.f ? 0.f : 1.f / l);
 #pragma unroll
-        for (int i = 0; i < D; i += 4)
-          *reinterpret_cast<float4*>(to + i) = make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv);
+        for (int i = 0; i < D; i += 8) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) o[i + k] *= inv;
+          store32(to + i, o + i);
+        }
         if (pc.slot >= 0) {
           p.m_part[state] = m;
           p.l_part[state] = l;
@@ -627,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tmem_fence_before();
   cta_sync();
-  if (warp == kMmaWarp) {
+  if (warp == kSWarp) {
     tmem_fence_after();
     tmem_free_all(tmem);
   }
