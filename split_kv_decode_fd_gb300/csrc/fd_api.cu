@@ -126,9 +126,10 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// 16-row x 128-byte boxes with the 128-byte swizzle, over the contiguous
+// Boxes of `rows` rows (16 if not given) x 128 bytes with the 128-byte swizzle, over the contiguous
 // cache [B*Hkv, T_cap, D] or the page pool [num_pages, Hkv, page_size, D].
-fd_status make_maps(const fd_kv_desc* kv, int B, int Hkv, int D, CUtensorMap* tk, CUtensorMap* tv) {
+fd_status make_maps(const fd_kv_desc* kv, int B, int Hkv, int D, CUtensorMap* tk, CUtensorMap* tv,
+                    cuuint32_t rows = 16) {
   auto encode = encode_fn();
   if (!encode) return FD_ERR_CUDA;
   const CUtensorMapDataType dt =
@@ -145,7 +146,7 @@ fd_status make_maps(const fd_kv_desc* kv, int B, int Hkv, int D, CUtensorMap* tk
     strides[0] = (cuuint64_t)D * es;
     strides[1] = (cuuint64_t)kv->capacity * D * es;
     box[0] = (cuuint32_t)(128 / es);
-    box[1] = 16;
+    box[1] = rows;
     box[2] = 1;
   } else {
     // the pool [num_pages, Hkv, page_size, D] as [num_pages * Hkv, page_size, D]
@@ -157,7 +158,7 @@ fd_status make_maps(const fd_kv_desc* kv, int B, int Hkv, int D, CUtensorMap* tk
     strides[0] = (cuuint64_t)D * es;
     strides[1] = (cuuint64_t)kv->page_size * D * es;
     box[0] = (cuuint32_t)(128 / es);
-    box[1] = 16;
+    box[1] = rows;
     box[2] = 1;
   }
   // Encoding costs a driver call per map; decode steps usually repeat the same
@@ -166,6 +167,7 @@ fd_status make_maps(const fd_kv_desc* kv, int B, int Hkv, int D, CUtensorMap* tk
   struct MapEntry {
     const void *k, *v;
     CUtensorMapDataType dt;
+    cuuint32_t rows;
     cuuint64_t dims[3], strides[2];
     CUtensorMap tk, tv;
     bool valid;
@@ -173,7 +175,7 @@ fd_status make_maps(const fd_kv_desc* kv, int B, int Hkv, int D, CUtensorMap* tk
   thread_local MapEntry cache[4];
   thread_local int next_slot = 0;
   for (const MapEntry& e : cache) {
-    if (e.valid && e.k == kv->k && e.v == kv->v && e.dt == dt && e.dims[0] == dims[0] && e.dims[1] == dims[1] &&
+    if (e.valid && e.k == kv->k && e.v == kv->v && e.dt == dt && e.rows == rows && e.dims[0] == dims[0] && e.dims[1] == dims[1] &&
         e.dims[2] == dims[2] && e.strides[0] == strides[0] && e.strides[1] == strides[1]) {
       *tk = e.tk;
       *tv = e.tv;
@@ -193,6 +195,7 @@ fd_status make_maps(const fd_kv_desc* kv, int B, int Hkv, int D, CUtensorMap* tk
   e.k = kv->k;
   e.v = kv->v;
   e.dt = dt;
+  e.rows = rows;
   for (int i = 0; i < 3; ++i) e.dims[i] = dims[i];
   for (int i = 0; i < 2; ++i) e.strides[i] = strides[i];
   e.tk = *tk;
@@ -1115,7 +1118,8 @@ fd_status fd_decode_tree(const float* q, const fd_tree_desc* tree, const fd_kv_d
     if (launch_tree_core(D, p, s) != cudaSuccess) return FD_ERR_CUDA;
   } else {
     CUtensorMap tk, tv;
-    if ((st = make_maps(kv, B, Hkv, D, &tk, &tv)) != FD_OK) return st;
+    p.box_rows = tree_box_rows(p.kv.paged ? kv->page_size : 64);
+    if ((st = make_maps(kv, B, Hkv, D, &tk, &tv, (cuuint32_t)p.box_rows)) != FD_OK) return st;
     if (launch_tree_mma(D, tk, tv, p, s) != cudaSuccess) return FD_ERR_CUDA;
   }
   // a sequence of one tile lies within a share

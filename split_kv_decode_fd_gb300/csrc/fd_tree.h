@@ -62,6 +62,7 @@ struct TreeParams {
   int32_t nsub, ranges;
   int32_t n_joins, join_pairs; // join_pairs: an entry for each pair
   int32_t max_len;
+  int32_t box_rows;            // rows that a copy of K or V brings (bf16 caches)
   float qk_scale;              // scale * log2(e)
   uint64_t wait_ns;            // limit of every wait (0: the default)
   int32_t stall_u;             // testing hook: the copy that every CTA skips, or -1
@@ -70,6 +71,8 @@ struct TreeParams {
 // Rows per CTA and CTAs per SM: fp32 caches on CUDA cores, bf16 ones on tensor cores.
 constexpr int kTreeRowsCore = 32, kTreeCtasCore = 2;
 constexpr int kTreeRowsMma = 128;
+// Rows of a copy: as many of 64, 32, 16 as lie in a page.  A copy takes a warp some 100 cycles to start.
+constexpr int tree_box_rows(int page) { return page % 64 == 0 ? 64 : page % 32 == 0 ? 32 : 16; }
 constexpr int tree_rows(bool f32) { return f32 ? kTreeRowsCore : kTreeRowsMma; }
 constexpr int tree_ctas(bool f32) { return f32 ? kTreeCtasCore : 1; }
 

@@ -13,15 +13,17 @@
 // unit drop bits.  Six products of 8 k-steps make 3072 cycles a tile of 128 channels, and a
 // tile's 64 KB at an SM's share of the memory rate some 3000.
 //
-// Eleven warps:
+// Twelve warps:
 //   0-3  softmax, thread = row: reads S, masks, keeps the running max and sum, writes P
 //        over S; cuts q at the start of a piece.
 //   4-7  sums, thread = row: O of each tile times what the max has moved by; writes the
 //        rows at the end of a piece.
-//   8    copies: walks the share, announces its pieces, brings q (by bulk copies) and the K and V
-//        tiles (16-row x 128-byte boxes, 128-byte swizzle) through one ring of slots
-//        in the order of their use: q, K0, K1, V0, K2, V1, ... , V(n-1).
-//   9, 10  products, one thread of each: S, and O.  While the softmax of a tile runs, the tensor
+//   8    walks the share, announces its pieces, copies q (its first 64 rows) and K;
+//   9    copies (the other rows of q and) V.  K and V have a ring of slots each, as only one warp may wait for a slot to
+//        be free: a barrier tells a phase from the one before, not from the one before that.  A warp starts a copy in
+//        some 100 cycles, so a copy brings up to 64 rows of a page and 64 channels (128-byte swizzle), and K and V have
+//        a warp each (with copies of 16 rows by one warp a tile took 4300 cycles);
+//   10, 11  products, one thread of each: S, and O.  While the softmax of a tile runs, the tensor
 //        core has the S of the next and the O of the one before.
 #include <atomic>
 
@@ -33,22 +35,27 @@ namespace {
 
 constexpr int kRows = kTreeRowsMma;
 constexpr int kKeys = kPlanTile;
-constexpr int kThreads = 352;
+constexpr int kThreads = 384;
 constexpr int kParts = 3;                 // bf16 numbers that q and p are cut into
-constexpr int kCopyWarp = 8, kSWarp = 9;  // and O: 10
+constexpr int kCopyK = 8, kCopyV = 9, kSWarp = 10;  // and O: 11
 constexpr int kPBufs = 4;                // barriers of P and places for a tile's max
 // Tensor memory: two S / P buffers and O.  P takes 8 columns for each part of 16 keys, 192 in
 // all, and S the last 128 of them: a chunk of P never reaches an unread chunk of S.
 constexpr uint32_t kBuf = 192, kSOff = 64, kOCol = 384;
 
-template <int D>
+// Rows: rows of q that are held, 64 or 128.  With 64, an operand's other rows are what follows in shared memory: the
+// products have rows that nobody reads, and the ring a slot more.
+template <int D, int Rows>
 struct Layout {
   static constexpr int kNB = D / 64;                          // 128-byte column blocks of a row
   static constexpr uint32_t kBlock = 16384;                   // [128 rows][128 bytes]
-  static constexpr uint32_t kTile = kNB * kBlock;             // a K or V tile, one part of q
-  static constexpr uint32_t kRing = kParts * kTile;           // q first
-  static constexpr uint32_t kSlots = D == 128 ? 4 : 8;
-  static constexpr uint32_t kMisc = kRing + kSlots * kTile;
+  static constexpr uint32_t kTile = kNB * kBlock;             // a K or V tile
+  static constexpr uint32_t kQBlock = Rows * 128u;            // a column block of a part of q
+  static constexpr uint32_t kQPart = kNB * kQBlock;
+  static constexpr uint32_t kRing = kParts * kQPart;          // q first
+  static constexpr uint32_t kK = D == 64 ? 4 : Rows == 64 ? 3 : 2, kV = D == 64 ? 4 : 2;  // slots
+  static constexpr uint32_t kVRing = kRing + kK * kTile;
+  static constexpr uint32_t kMisc = kVRing + kV * kTile;
   static constexpr uint32_t kQRowsPerSlot = kTile / (D * 4);  // fp32 rows of q
   static constexpr uint32_t kBytes = kMisc + 3072;
   static_assert(kBytes <= 232448, "shared memory");
@@ -56,7 +63,8 @@ struct Layout {
 
 // Behind the ring.
 struct Misc {
-  uint64_t kv_full[8], kv_empty[8];
+  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
+  uint64_t q_full[2][2];                               // of even and odd pieces, of each 64 rows
   uint64_t s_full[2], p_empty[2], o_empty[2], p_full[kPBufs];
   uint64_t piece_full[2], piece_empty[2];
   uint64_t o_full, q_ready, fin_full, fin_empty, drain[2];
@@ -175,51 +183,58 @@ struct Ring {
   }
 };
 
-template <int D>
+template <int D, int Rows>
 __global__ void __launch_bounds__(kThreads, 1)
     fd_tree_mma_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                        const __grid_constant__ TreeParams p) {
-  using Lay = Layout<D>;
-  constexpr uint32_t kSlots = Lay::kSlots, kBlock = Lay::kBlock, kTile = Lay::kTile;
+  using Lay = Layout<D, Rows>;
+  constexpr uint32_t kBlock = Lay::kBlock, kTile = Lay::kTile;
   extern __shared__ __align__(1024) uint8_t smem[];
   Misc& s = *reinterpret_cast<Misc*>(smem + Lay::kMisc);
-  const uint32_t sq = smem_addr(smem), ring = sq + Lay::kRing;
+  const uint32_t sq = smem_addr(smem), k_ring = sq + Lay::kRing, v_ring = sq + Lay::kVRing;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int32_t range = blockIdx.x / p.nsub, sub = blockIdx.x % p.nsub;
   const int32_t row0 = sub * kRows;
   const int32_t live = p.rows - row0 < kRows ? p.rows - row0 : kRows;
   const uint32_t nq = ((uint32_t)live + Lay::kQRowsPerSlot - 1) / Lay::kQRowsPerSlot;
+  const uint32_t warps = ((uint32_t)live + 31) / 32;  // of the softmax and of the sums that have rows
 
   if ((sq & 1023u) != 0) {  // the swizzle goes by address; no room is left to align here
     if (tid == 0) atomicOr(p.err, kErrTimeout);
     return;
   }
   if (tid == 0) {
-    for (uint32_t i = 0; i < kSlots; ++i) {
-      mbar_init(s.kv_full + i, 1);
-      mbar_init(s.kv_empty + i, 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(s.k_full + i, 1);
+      mbar_init(s.k_empty + i, 1);
+      mbar_init(s.v_full + i, 1);
+      mbar_init(s.v_empty + i, 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(s.s_full + i, 1);
+      for (int k = 0; k < 2; ++k) mbar_init(&s.q_full[i][k], 1);
       mbar_init(s.p_empty + i, 1);
-      mbar_init(s.o_empty + i, 4);
+      mbar_init(s.o_empty + i, warps);
       mbar_init(s.piece_full + i, 1);
-      mbar_init(s.piece_empty + i, 10);
+      mbar_init(s.piece_empty + i, 3 + 2 * warps);
       mbar_init(s.drain + i, 1);
     }
-    for (int i = 0; i < kPBufs; ++i) mbar_init(s.p_full + i, 4);
+    for (int i = 0; i < kPBufs; ++i) mbar_init(s.p_full + i, warps);
     mbar_init(&s.o_full, 1);
-    mbar_init(&s.q_ready, 4);
-    mbar_init(&s.fin_full, 4);
-    mbar_init(&s.fin_empty, 4);
+    mbar_init(&s.q_ready, warps);
+    mbar_init(&s.fin_full, warps);
+    mbar_init(&s.fin_empty, warps);
     s.abort = 0;
     fence_barrier_init();
   }
-  if (warp == kCopyWarp && lane == 0) {
-    prefetch_tensormap(&tmap_k);
-    prefetch_tensormap(&tmap_v);
-  }
+  if (warp == kCopyK && lane == 0) prefetch_tensormap(&tmap_k);
+  if (warp == kCopyV && lane == 0) prefetch_tensormap(&tmap_v);
   if (warp == kSWarp) tmem_alloc_all(smem_addr(&s.tmem));
+  if (warp < 4 && warp >= (int)warps && tid < Rows) {  // rows of q that are none are 0
+    for (uint32_t i = 0; i < kParts * Lay::kNB * 8u; ++i)
+      sts128(sq + (i >> 3) * Lay::kQBlock + (uint32_t)tid * 128u + (i & 7u) * 16u, 0u, 0u, 0u, 0u);
+    fence_async();
+  }
   pdl_launch_dependents();
   tmem_fence_before();
   cta_sync();
@@ -238,13 +253,78 @@ __global__ void __launch_bounds__(kThreads, 1)
     return pc.b >= 0;
   };
 
-  if (warp == kCopyWarp) {
-    // ------------------------------------------------------------ copies
-    uint32_t u = 0, stalled = 0xffffffffu;
-    Ring<kSlots> r;
+  // Copies of K or V, by one warp: lane l holds the place of the tile's rows [box l, box (l + 1)), a run of a page.
+  const int32_t box = p.box_rows, boxes = kKeys / box;
+  const bool shared_keys = p.nsub > 1;  // other CTAs read them too: they stay in L2
+  const uint64_t once = policy_evict_first();
+  auto page_of = [&](const TreePiece& pc, int32_t j) -> int32_t {
+    const int32_t t = pc.begin + j * kKeys + box * lane;
+    return p.kv.paged && lane < boxes && t < pc.end
+               ? __ldg(p.kv.block_table + (int64_t)pc.b * p.kv.max_pages + t / p.kv.page_size)
+               : -1;
+  };
+  auto copy = [&](const CUtensorMap* map, const TreePiece& pc, int32_t j, int32_t page, uint8_t* to, uint64_t* full) {
+    const int32_t t = pc.begin + j * kKeys + box * lane;
+    bool mine = lane < boxes && t < pc.end;
+    int32_t row = t, z = pc.b * p.Hkv + pc.h;
+    if (p.kv.paged) {
+      if (mine && (page < 0 || page >= p.kv.num_pages)) {
+        atomicOr(p.err, kErrBadIndex);
+        mine = false;
+      }
+      row = t % p.kv.page_size;
+      z = page * p.Hkv + pc.h;
+    }
+    uint32_t which = __ballot_sync(0xffffffffu, mine);
+    if (elect_one()) mbar_arrive_expect_tx(full, (uint32_t)(__popc(which) * box) * Lay::kNB * 128u);
+    for (; which; which &= which - 1) {
+      const int32_t i = __ffs(which) - 1;
+      const int32_t y = __shfl_sync(0xffffffffu, row, i), zz = __shfl_sync(0xffffffffu, z, i);
+      uint8_t* dst = to + (uint32_t)(i * box) * 128u;
+      if (elect_one()) {
+#pragma unroll
+        for (int blk = 0; blk < Lay::kNB; ++blk) {
+          if (p.kv.paged || shared_keys)
+            tma_load_3d(dst + blk * kBlock, map, full, blk * 64, y, zz);
+          else
+            tma_load_3d_hint(dst + blk * kBlock, map, full, blk * 64, y, zz, once);
+        }
+      }
+    }
+    __syncwarp();
+  };
+  // Rows [64 i, 64 (i + 1)) of the q of piece e, which lie side by side, into a slot.  They have barriers of their own, as
+  // the softmax waits for them without having waited for the slot's other uses; two, as q of the next piece may come
+  // before the softmax looks (not that of the one after: no ring has five slots).
+  auto copy_q = [&](const TreePiece& pc, uint32_t e, int32_t i, uint8_t* to, uint64_t* full) {
+    if (lane == 0) {
+      uint64_t* landed = &s.q_full[e & 1][i];
+      const int32_t first = i * (int32_t)Lay::kQRowsPerSlot;
+      const int32_t rows = live - first < (int32_t)Lay::kQRowsPerSlot ? live - first : (int32_t)Lay::kQRowsPerSlot;
+      mbar_arrive_expect_tx(landed, (uint32_t)rows * D * 4);
+      bulk_load(to, p.q + (((int64_t)pc.b * p.Hkv + pc.h) * p.rows + row0 + first) * D, (uint32_t)rows * D * 4, landed);
+      mbar_arrive(full);
+    }
+    __syncwarp();
+  };
+  // At the end of the work the products have waited for every copy.  A CTA that gives up must not leave while one may
+  // still be landing: its warp waits for the last use of each of its slots (`u` uses so far, of n slots; use `skipped` was
+  // not started).
+  auto leave = [&](uint64_t* full, uint32_t u, uint32_t n, uint32_t skipped, uint32_t i, uint32_t f) {
+    if (w.ok) return;
+    s.abort = 1;
+    if (lane != 0) return;
+    atomicOr(p.err, kErrTimeout);
+    for (uint32_t x = u > n ? u - n : 0; x < u; ++x)
+      if (x != skipped) mbar_wait_for(full + x % n, (x / n) & 1, w.limit);
+    for (uint32_t e = f > 2 ? f - 2 : 0; e < f; ++e) mbar_wait_for(&s.q_full[e & 1][i], (e >> 1) & 1, w.limit);
+  };
+
+  if (warp == kCopyK) {
+    // ------------------------------------------------------------ pieces, q, K
+    uint32_t u = 0, f = 0, skipped = 0xffffffffu;
+    Ring<Lay::kK> r;
     TreeWalk walk(p, range);
-    const uint64_t once = policy_evict_first();
-    const bool shared_keys = p.nsub > 1;  // other CTAs read them too: they stay in L2
     for (uint32_t e = 0;; ++e) {
       TreePiece pc;
       if (!walk.next(pc)) pc.b = -1;
@@ -256,142 +336,110 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (pc.b >= 0 && sub == 0) walk.say(pc);
       }
       if (pc.b < 0) break;
-      // q's rows lie side by side
-      const float* q = p.q + (((int64_t)pc.b * p.Hkv + pc.h) * p.rows + row0) * D;
-      for (uint32_t i = 0; i < nq && w.ok; ++i, ++u, r.next()) {
-        w.on(s.kv_empty + r.slot, r.phase ^ 1u);
-        if (!w.all()) break;
-        if (p.stall_u >= 0 && u == (uint32_t)p.stall_u) {
-          stalled = u;
-          continue;
-        }
-        if (lane == 0) {
-          const int32_t left = live - (int32_t)(i * Lay::kQRowsPerSlot);
-          const uint32_t rows = left < (int32_t)Lay::kQRowsPerSlot ? (uint32_t)left : Lay::kQRowsPerSlot;
-          mbar_arrive_expect_tx(s.kv_full + r.slot, rows * D * 4);
-          bulk_load(smem + Lay::kRing + r.slot * kTile, q + (size_t)i * Lay::kQRowsPerSlot * D, rows * D * 4,
-                    s.kv_full + r.slot);
-        }
-      }
       const int32_t n = ceil_div(pc.end - pc.begin, kKeys);
-      // Lane l brings rows [16 l, 16 l + 16) of a tile, one run of a page.  Pages of the tile whose K comes next and of
-      // the one after (a lookup takes a while), of the last tile whose K has gone, and of the one before that.
-      const int32_t* table = p.kv.paged ? p.kv.block_table + (int64_t)pc.b * p.kv.max_pages : nullptr;
-      const int32_t t_lane = pc.begin + 16 * lane;
-      auto lookup = [&](int32_t j) -> int32_t {
-        const int32_t t = t_lane + j * kKeys;
-        return lane < 8 && j < n && t < pc.end ? __ldg(table + t / p.kv.page_size) : -2;
-      };
-      auto brings = [&](int32_t j) { return lane < 8 && t_lane + j * kKeys < pc.end; };
-      int32_t page_next = 0, page_after = 0, page_last = 0, page_before = 0;
-      if (table) {
-        page_next = lookup(0);
-        page_after = lookup(1);
-      }
-      for (int32_t i = 0; i < 2 * n && w.ok; ++i, ++u, r.next()) {
-        // the i-th copy: K0, then K(j), V(j - 1), and V(n - 1)
-        const bool is_v = i == 2 * n - 1 || (i > 0 && i % 2 == 0);
-        const int32_t j = i == 2 * n - 1 ? n - 1 : is_v ? i / 2 - 1 : (i + 1) / 2;
-        bool mine = brings(j);
-        int32_t z = pc.b * p.Hkv + pc.h, row = t_lane + j * kKeys;
-        if (table) {
-          z = !is_v ? page_next : i == 2 * n - 1 ? page_last : page_before;
-          if (mine && (z < 0 || z >= p.kv.num_pages)) {
-            atomicOr(p.err, kErrBadIndex);
-            mine = false;
-          }
-          z = z * p.Hkv + pc.h;
-          row %= p.kv.page_size;
-        }
-        w.on(s.kv_empty + r.slot, r.phase ^ 1u);
+      int32_t page = page_of(pc, 0);
+      w.on(s.k_empty + r.slot, r.phase ^ 1u);
+      if (!w.all()) break;
+      copy_q(pc, e, 0, smem + Lay::kRing + r.slot * kTile, s.k_full + r.slot);
+      ++f;
+      ++u;
+      r.next();
+      for (int32_t j = 0; j < n; ++j, ++u, r.next()) {
+        const int32_t next = page_of(pc, j + 1);
+        w.on(s.k_empty + r.slot, r.phase ^ 1u);
         if (!w.all()) break;
-        if (p.stall_u >= 0 && u == (uint32_t)p.stall_u) {
-          stalled = u;
-        } else {
-          const unsigned issue = __ballot_sync(0xffffffffu, mine);
-          if (lane == 0) mbar_arrive_expect_tx(s.kv_full + r.slot, (uint32_t)__popc(issue) * Lay::kNB * 2048u);
-          __syncwarp();
-          if (mine) {
-            uint8_t* dst = smem + Lay::kRing + r.slot * kTile + lane * 2048;
-            const CUtensorMap* map = is_v ? &tmap_v : &tmap_k;
-#pragma unroll
-            for (int blk = 0; blk < Lay::kNB; ++blk) {
-              if (table || shared_keys)
-                tma_load_3d(dst + blk * kBlock, map, s.kv_full + r.slot, blk * 64, row, z);
-              else
-                tma_load_3d_hint(dst + blk * kBlock, map, s.kv_full + r.slot, blk * 64, row, z, once);
-            }
-          }
-        }
-        if (table && !is_v) {
-          page_before = page_last;
-          page_last = page_next;
-          page_next = page_after;
-          page_after = lookup(j + 2);
-        }
+        if (p.stall_u >= 0 && u == (uint32_t)p.stall_u)
+          skipped = u;  // testing hook
+        else
+          copy(&tmap_k, pc, j, page, smem + Lay::kRing + r.slot * kTile, s.k_full + r.slot);
+        page = next;
       }
       if (!w.ok) break;
     }
-    if (!w.ok) s.abort = 1;
-    // do not leave while copies may still be landing
-    if (lane == 0) {
-      if (!w.ok) atomicOr(p.err, kErrTimeout);
-      const uint32_t first = u > kSlots ? u - kSlots : 0;
-      for (uint32_t i = first; i < u; ++i)
-        if (i != stalled && !mbar_wait_for(s.kv_full + i % kSlots, (i / kSlots) & 1, w.limit)) atomicOr(p.err, kErrTimeout);
+    leave(s.k_full, u, Lay::kK, skipped, 0, f);
+  } else if (warp == kCopyV) {
+    // ------------------------------------------------------------ q, V
+    uint32_t u = 0, f = 0;
+    Ring<Lay::kV> r;
+    TreePiece pc;
+    for (uint32_t e = 0; take(e, pc); ++e) {
+      const int32_t n = ceil_div(pc.end - pc.begin, kKeys);
+      int32_t page = page_of(pc, 0);
+      if (nq == 2) {
+        w.on(s.v_empty + r.slot, r.phase ^ 1u);
+        if (!w.all()) break;
+        copy_q(pc, e, 1, smem + Lay::kVRing + r.slot * kTile, s.v_full + r.slot);
+        ++f;
+        ++u;
+        r.next();
+      }
+      for (int32_t j = 0; j < n; ++j, ++u, r.next()) {
+        const int32_t next = page_of(pc, j + 1);
+        w.on(s.v_empty + r.slot, r.phase ^ 1u);
+        if (!w.all()) break;
+        copy(&tmap_v, pc, j, page, smem + Lay::kVRing + r.slot * kTile, s.v_full + r.slot);
+        page = next;
+      }
+      if (!w.ok) break;
     }
+    leave(s.v_full, u, Lay::kV, 0xffffffffu, 1, f);
   } else if (warp >= kSWarp) {
     // ------------------------------------------------------------ products
     // Every branch and operand is uniform over the warp as the compiler sees it (votes and shuffles), so that the
     // products take their operands from uniform registers as they are.
     constexpr uint32_t idS = bf16_instr_desc(kRows, kKeys), idO = bf16_instr_desc(kRows, D, true);
-    const uint32_t base = uniform(tmem), q0 = uniform(sq), ring0 = uniform(ring);
+    const uint32_t base = uniform(tmem), q0 = uniform(sq), k0 = uniform(k_ring), v0 = uniform(v_ring);
     const bool is_s = uniform((uint32_t)warp) == kSWarp;
-    Ring<kSlots> r;
-    uint32_t g = 0, f = 0;  // tiles and pieces so far
+    Ring<Lay::kK> rk;
+    Ring<Lay::kV> rv;
+    uint32_t g = 0, f = 0, uv = 0;  // tiles, pieces and uses of V's slots so far
     TreePiece pc;
     for (uint32_t e = 0; take(e, pc); ++e) {
       const uint32_t n = uniform((uint32_t)ceil_div(pc.end - pc.begin, kKeys));
       if (is_s) {
         w.on(&s.q_ready, f & 1);
         if (!w.all()) break;
-        for (uint32_t i = 0; i < nq; ++i, r.next())
-          if (elect_one()) mbar_arrive(s.kv_empty + r.slot);
-        for (uint32_t j = 0; j < n; ++j) {
+        if (elect_one()) {  // the slots that q came in
+          mbar_arrive(s.k_empty + rk.slot);
+          if (nq == 2) mbar_arrive(s.v_empty + uv % Lay::kV);
+        }
+        __syncwarp();
+        rk.next();
+        uv += nq - 1 + n;
+        for (uint32_t j = 0; j < n; ++j, rk.next()) {
           const uint32_t t = g + j;
-          w.on(s.kv_full + r.slot, r.phase);
+          w.on(s.k_full + rk.slot, rk.phase);
           if (t >= 2) w.on(s.p_empty + (t & 1), ((t - 2) >> 1) & 1);
           if (!w.all()) break;
           tmem_fence_after();
           if (elect_one()) {
-            const uint32_t d = base + (t & 1) * kBuf + kSOff, k = ring0 + r.slot * kTile;
+            const uint32_t d = base + (t & 1) * kBuf + kSOff, k = k0 + rk.slot * kTile;
             // the small parts of q first: their sums lose least
 #pragma unroll
             for (int part = kParts - 1; part >= 0; --part) {
 #pragma unroll
               for (int i = 0; i < D / 16; ++i) {
-                const uint32_t off = (uint32_t)(i >> 2) * kBlock + (uint32_t)(i & 3) * 32u;
-                mma_ss(d, b_desc(q0 + (uint32_t)part * kTile + off), b_desc(k + off), idS, part != kParts - 1 || i != 0);
+                const uint32_t block = (uint32_t)(i >> 2), off = (uint32_t)(i & 3) * 32u;
+                mma_ss(d, b_desc(q0 + (uint32_t)part * Lay::kQPart + block * Lay::kQBlock + off),
+                       b_desc(k + block * kBlock + off), idS, part != kParts - 1 || i != 0);
               }
             }
             mma_commit(smem_addr(s.s_full + (t & 1)));
-            mma_commit(smem_addr(s.kv_empty + r.slot));
+            mma_commit(smem_addr(s.k_empty + rk.slot));
           }
           __syncwarp();
-          // K(j + 1), or what follows the piece
-          r.next(j + 1 < n ? (j == 0 ? 1 : 2) : (n == 1 ? 2 : 3));
         }
       } else {
-        r.next(nq + (n == 1 ? 1 : 2));
-        for (uint32_t j = 0; j < n; ++j) {
+        if (nq == 2) rv.next();
+        for (uint32_t j = 0; j < n; ++j, rv.next()) {
           const uint32_t t = g + j;
-          w.on(s.kv_full + r.slot, r.phase);
+          w.on(s.v_full + rv.slot, rv.phase);
           w.on(s.p_full + t % kPBufs, (t / kPBufs) & 1);
           if (t > 0) w.on(s.o_empty + ((t - 1) & 1), ((t - 1) >> 1) & 1);
           if (!w.all()) break;
           tmem_fence_after();
           if (elect_one()) {
-            const uint32_t a = base + (t & 1) * kBuf, v = ring0 + r.slot * kTile;
+            const uint32_t a = base + (t & 1) * kBuf, v = v0 + rv.slot * kTile;
 #pragma unroll
             for (int part = kParts - 1; part >= 0; --part) {
 #pragma unroll
@@ -401,10 +449,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             mma_commit(smem_addr(&s.o_full));
             mma_commit(smem_addr(s.p_empty + (t & 1)));
-            mma_commit(smem_addr(s.kv_empty + r.slot));
+            mma_commit(smem_addr(s.v_empty + rv.slot));
           }
           __syncwarp();
-          r.next(j + 2 < n ? 2 : 1);  // V(j + 1), or what follows the piece
         }
       }
       if (!w.ok) break;
@@ -422,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!mbar_wait_for(done, 0, w.limit)) atomicOr(p.err, kErrTimeout);
     }
     __syncwarp();
-  } else if (warp < 4) {
+  } else if (warp < (int)warps) {
     // ------------------------------------------------------------ softmax
     const uint32_t lanes = (uint32_t)(warp * 32) << 16;
     const int32_t row = warp * 32 + lane;  // of the block = lane of tensor memory
@@ -430,17 +477,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float f = p.qk_scale == 0.f ? 1.f : fabsf(p.qk_scale);
     const uint32_t flip = p.qk_scale < 0.f ? 0x80000000u : 0u, keepq = p.qk_scale == 0.f ? 0u : 0xffffffffu;
     const uint64_t f2 = pack2(f, f);
-    uint32_t g = 0, u = 0;
+    uint32_t g = 0, uk = 0, uv = 0;  // tiles and uses of the rings so far
     TreePiece pc;
     for (uint32_t e = 0; take(e, pc); ++e) {
       const int32_t n = ceil_div(pc.end - pc.begin, kKeys), P = pc.len - pc.m;
       // q: three bf16 parts of the row in the swizzled layout of an MMA operand.  The products of the piece before
       // have read theirs: its last S has been seen.  A lane starts at a 16-byte chunk of its own, off the others' banks.
-      for (uint32_t i = 0; i < nq; ++i) w.on(s.kv_full + (u + i) % kSlots, ((u + i) / kSlots) & 1);
-      if (row < live || e == 0) {  // rows that are none stay 0
+      for (uint32_t i = 0; i < nq; ++i) w.on(&s.q_full[e & 1][i], (e >> 1) & 1);
+      if (row < live || (e == 0 && row < Rows)) {  // rows that are none stay 0
         constexpr uint32_t kC = D / 4, kStep = 8;  // fp32 chunks of a row, at a time
-        const uint32_t from = ring + ((u + (uint32_t)row / Lay::kQRowsPerSlot) % kSlots) * kTile +
-                              ((uint32_t)row % Lay::kQRowsPerSlot) * (D * 4);
+        const uint32_t from = (row < (int32_t)Lay::kQRowsPerSlot ? k_ring + uk % Lay::kK * kTile : v_ring + uv % Lay::kV * kTile) +
+                              (uint32_t)row % Lay::kQRowsPerSlot * (D * 4);
 #pragma unroll 1
         for (uint32_t i0 = 0; i0 < kC; i0 += kStep) {
           uint4 x[kStep];
@@ -455,9 +502,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t a[kParts], b[kParts];
             cut3(__uint_as_float((x[i].x & keepq) ^ flip), __uint_as_float((x[i].y & keepq) ^ flip), a);
             cut3(__uint_as_float((x[i].z & keepq) ^ flip), __uint_as_float((x[i].w & keepq) ^ flip), b);
-            const uint32_t to = sq + (c8 >> 3) * kBlock + (uint32_t)row * 128u + (((c8 ^ (uint32_t)row) & 7u) << 4) + (c & 1u) * 8u;
+            const uint32_t to = sq + (c8 >> 3) * Lay::kQBlock + (uint32_t)row * 128u + (((c8 ^ (uint32_t)row) & 7u) << 4) + (c & 1u) * 8u;
 #pragma unroll
-            for (int part = 0; part < kParts; ++part) sts64(to + (uint32_t)part * kTile, a[part], b[part]);
+            for (int part = 0; part < kParts; ++part) sts64(to + (uint32_t)part * Lay::kQPart, a[part], b[part]);
           }
         }
       }
@@ -531,20 +578,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           // V's rows at or past the length may hold anything, and so may those of the drafts, which not every
           // row sees: 0 * NaN is not 0.  Values that are no numbers become 0 here and are added to the rows that
           // see them at the end.
-          const uint32_t uv = u + nq + (uint32_t)(j == n - 1 ? 2 * n - 1 : 2 * j + 2), slot = uv % kSlots;
-          w.on(s.kv_full + slot, (uv / kSlots) & 1);
+          const uint32_t use = uv + nq - 1 + (uint32_t)j, v = v_ring + use % Lay::kV * kTile;
+          // The slot's use before this one must have landed for the wait to tell them apart.  It is that of a tile
+          // whose O is done (S of this tile came after it), but for the first tile where q has a slot too: there it is the
+          // tile before.
+          if (nq == 2 && j == 0 && t > 0) w.on(s.p_empty + ((t - 1) & 1), ((t - 1) >> 1) & 1);
+          w.on(s.v_full + use % Lay::kV, (use / Lay::kV) & 1);
           constexpr int kChunks = D / 8;
           const int32_t first = P > t0 ? P - t0 : 0, end = pc.len - t0 < kKeys ? pc.len - t0 : kKeys;
-          for (int32_t i = row; i < (kKeys - first) * kChunks; i += 128) {
+          for (int32_t i = row; i < (kKeys - first) * kChunks; i += (int32_t)warps * 32) {
             const int32_t v_row = first + i / kChunks;
             const uint32_t c = (uint32_t)(i % kChunks);
-            const uint32_t a = ring + slot * kTile + (c >> 3) * kBlock + (uint32_t)v_row * 128u + ((c & 7u) << 4);
+            const uint32_t a = v + (c >> 3) * kBlock + (uint32_t)v_row * 128u + ((c & 7u) << 4);
             if (v_row >= end) {
               sts128(a, 0u, 0u, 0u, 0u);
               continue;
             }
-            const uint4 v = lds128u(a);
-            uint32_t v4[4] = {v.x, v.y, v.z, v.w};
+            const uint4 x4 = lds128u(a);
+            uint32_t v4[4] = {x4.x, x4.y, x4.z, x4.w};
             bool any = false;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -571,18 +622,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.fin_full);
       g += (uint32_t)n;
-      u += nq + 2 * (uint32_t)n;
+      uk += 1 + (uint32_t)n;
+      uv += nq - 1 + (uint32_t)n;
       if (!w.all()) break;
     }
     if (!w.ok) {
       s.abort = 1;
       atomicOr(p.err, kErrTimeout);
     }
-  } else {
+  } else if (warp >= 4 && warp < 4 + (int)warps) {
     // ------------------------------------------------------------ sums
     const uint32_t at = tmem + kOCol + ((uint32_t)((warp - 4) * 32) << 16);
     const int32_t row = (warp - 4) * 32 + lane;
-    tree_no_rows<D, kRows>(p, range, sub, row, kRows);
+    tree_no_rows<D, kRows>(p, range, sub, row, (int)warps * 32);
     uint32_t g = 0;
     TreePiece pc;
     for (uint32_t e = 0; take(e, pc); ++e) {
@@ -614,7 +666,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       g += (uint32_t)n;
       w.on(&s.fin_full, e & 1);
       const float l = s.l[row];
-      uint64_t unfit = s.unfit[0] | s.unfit[1] | s.unfit[2] | s.unfit[3];
+      uint64_t unfit = 0;
+      for (uint32_t i = 0; i < warps; ++i) unfit |= s.unfit[i];
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.fin_empty);
       const bool writes = row < live && (row0 + row) % p.tree.n >= p.tree.n - pc.m;
@@ -675,19 +728,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D>
+template <int D, int Rows>
 cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p, cudaStream_t stream) {
-  const cudaError_t e = allow_smem<fd_tree_mma_kernel<D>>((int)Layout<D>::kBytes);
+  constexpr uint32_t bytes = Layout<D, Rows>::kBytes;
+  const cudaError_t e = allow_smem<fd_tree_mma_kernel<D, Rows>>((int)bytes);
   if (e != cudaSuccess) return e;
-  return launch_early(fd_tree_mma_kernel<D>, (unsigned)(p.ranges * p.nsub), kThreads, Layout<D>::kBytes, stream, tk, tv, p);
+  return launch_early(fd_tree_mma_kernel<D, Rows>, (unsigned)(p.ranges * p.nsub), kThreads, bytes, stream, tk, tv, p);
 }
 
 }  // namespace
 
 cudaError_t launch_tree_mma(int D, const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p,
                             cudaStream_t stream) {
-  if (D == 128) return launch<128>(tk, tv, p, stream);
-  if (D == 64) return launch<64>(tk, tv, p, stream);
+  if (D == 128) return p.rows <= 64 ? launch<128, 64>(tk, tv, p, stream) : launch<128, 128>(tk, tv, p, stream);
+  if (D == 64) return launch<64, 128>(tk, tv, p, stream);
   return cudaErrorInvalidValue;
 }
 

@@ -100,6 +100,26 @@ class Case:
         assert el.size == 0 or el.max() <= 1.0, el.max()
 
 
+def exact_on_the_gpu(c):
+    """The oracle's formulas in 64 bits in torch, for cases that are large: out and lse (NaN in padding rows)."""
+    out, lse = (torch.full(x, math.nan, dtype=torch.float64, device="cuda") for x in (c.q.shape, c.q.shape[:3]))
+    for b, L in enumerate(c.lens):
+        m = c.n if c.new_lens is None else c.new_lens[b]
+        if m == 0:
+            continue
+        k, v = (torch.from_numpy(x[b, :, :L]).double().cuda() for x in (c.k_np, c.v_np))
+        sees = torch.ones((m, L), dtype=torch.bool)
+        tree = torch.from_numpy(oracle.tree.ancestors(c.parents_np[b, c.n - m:]))
+        first = max(0, L - m)
+        sees[:, first:] = tree[:, m - (L - first):]
+        q = c.q[b, :, c.n - m:].double().view(c.Hkv, -1, m, c.D)
+        x = torch.einsum("hgid,htd->hgit", q, k) * c.scale
+        x = x.masked_fill(~sees.cuda(), -math.inf)
+        out[b, :, c.n - m:] = torch.nan_to_num(torch.einsum("hgit,htd->hgid", torch.softmax(x, -1), v), 0.0).reshape(-1, m, c.D)
+        lse[b, :, c.n - m:] = torch.logsumexp(x, -1).reshape(-1, m)
+    return out, lse
+
+
 SHAPES = [  # B, Hq, Hkv, D, n, page
     (2, 4, 4, 128, 1, 0), (2, 4, 4, 64, 5, 16), (3, 8, 2, 128, 8, 16), (2, 8, 4, 64, 3, 0), (2, 24, 3, 128, 7, 48),
     (1, 32, 2, 128, 8, 0), (1, 32, 2, 64, 9, 32), (2, 10, 2, 128, 13, 0), (1, 3, 1, 64, 64, 16), (1, 34, 2, 128, 31, 64),
@@ -164,6 +184,29 @@ def test_one_tree_for_all_and_lengths_that_are_all_alike(cache):
 def test_sequences_cut_over_many_shares(B, Hkv, n, lens, cache):
     c = Case(B, 4 * Hkv, Hkv, 128, n, lens, cache=cache, page=16, seed=n)
     c.check(*c.run())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("page", [0, 16, 32])
+@pytest.mark.parametrize("g,n", [(1, 5), (2, 32), (2, 33), (2, 64), (3, 64), (8, 64)])
+@pytest.mark.parametrize("most", [130, 700, 6000])
+def test_many_pieces_and_blocks_of_rows(D, page, g, n, most):
+    """CTAs with many pieces, of one tile and of many, for one block of rows and for several."""
+    r = np.random.default_rng(most + n)
+    B, Hkv = (150, 2) if most < 1000 else (24, 2)
+    lens = r.integers(0, most, B).tolist()
+    c = Case(B, g * Hkv, Hkv, D, n, lens, page=page, seed=most + n, new_lens=[int(x) for x in r.integers(0, n + 1, B)])
+    for _ in range(3):
+        out, lse = c.run()
+    assert fd.workspace_status() == 0
+    ro, rl = exact_on_the_gpu(c)
+    live = ~torch.isnan(rl)
+    # scores of some units and values of a few, as in the bound above: 2 es vm + ... is below 1e-4 here
+    assert (out.double() - ro)[live].abs().max() < 1e-4
+    fin = live & torch.isfinite(rl)
+    assert torch.equal(torch.isneginf(lse[live]), torch.isneginf(rl[live])) and (lse.double() - rl)[fin].abs().max() < 1e-4
+    norm = (out.double() - ro)[live].norm() / ro[live].norm()
+    assert norm < 2e-6, norm  # rounding errors of fp32 sums, unbiased: some 4e-7
 
 
 @pytest.mark.parametrize("cache", ["bf16", "f32"])
