@@ -18,7 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfdecode.so")
 SOURCES = ["fd_api.cu", "fd_combine.cu", "fd_split_bf16.cu", "fd_split_f32.cu", "fd_prefill.cu",
-           "fd_append.cu", "fd_kv4_decode.cu", "fd_tree.cu", "fd_tree_mma.cu", "fd_verify.cu", "fd_keep.cu"]
+           "fd_append.cu", "fd_kv4_decode.cu", "fd_tree.cu", "fd_tree_mma.cu", "fd_tree_keys.cu", "fd_verify.cu", "fd_keep.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1016,12 +1016,13 @@ namespace {
 // Blocks of rows and shares of keys of fd_decode_tree on `sms` SMs (fd_tree.h); tiles: 128-key tiles of all (b, KV
 // head) pairs, or an upper bound.
 struct TreeSplit {
-  int32_t rows, nsub, ranges;
+  int32_t rows, block, nsub, ranges;
 };
 TreeSplit tree_split(int Hq, int Hkv, int n, bool f32, int sms, int64_t tiles) {
   TreeSplit t;
   t.rows = Hq / Hkv * n;
-  t.nsub = ceil_div(t.rows, tree_rows(f32));
+  t.block = tree_rows(f32, t.rows);
+  t.nsub = ceil_div(t.rows, t.block);
   int64_t r = (int64_t)tree_ctas(f32) * sms / t.nsub;  // CTAs that run at once
   if (r > tiles) r = tiles;
   t.ranges = (int32_t)(r < 1 ? 1 : r);
@@ -1031,8 +1032,8 @@ TreeSplit tree_split(int Hq, int Hkv, int n, bool f32, int sms, int64_t tiles) {
 struct TreeLayout {
   size_t joins, o, m, l, total;
 };
-TreeLayout tree_layout(const TreeSplit& t, bool f32, int D) {
-  const size_t states = t.ranges > 1 ? (size_t)2 * t.ranges * t.nsub * tree_rows(f32) : 0;
+TreeLayout tree_layout(const TreeSplit& t, int D) {
+  const size_t states = t.ranges > 1 ? (size_t)2 * t.ranges * t.nsub * t.block : 0;
   TreeLayout w;
   w.joins = kHeaderBytes + kCounterBytes;  // behind the counters, which other calls expect at zero
   w.o = w.joins + align_up((size_t)t.ranges * sizeof(TreeJoin));
@@ -1065,7 +1066,7 @@ size_t fd_tree_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t D, in
   if (sms <= 0 && !sm_count(&sms)) return 0;
   size_t most = 0;  // the size must hold for either cache type
   for (const bool f32 : {false, true}) {
-    const size_t a = tree_layout(tree_split(Hq, Hkv, n, f32, sms, INT64_MAX), f32, D).total;
+    const size_t a = tree_layout(tree_split(Hq, Hkv, n, f32, sms, INT64_MAX), D).total;
     most = a > most ? a : most;
   }
   return most;
@@ -1087,7 +1088,7 @@ fd_status fd_decode_tree(const float* q, const fd_tree_desc* tree, const fd_kv_d
   if (!sm_count(&sms)) return FD_ERR_CUDA;
   const bool f32 = kv->dtype == FD_F32;
   const TreeSplit t = tree_split(Hq, Hkv, tree->n, f32, sms, (int64_t)B * Hkv * ceil_div(max_seq_len, kPlanTile));
-  const TreeLayout w = tree_layout(t, f32, D);
+  const TreeLayout w = tree_layout(t, D);
   if (workspace_bytes < w.total) return FD_ERR_WORKSPACE_TOO_SMALL;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.q = q;
@@ -1120,11 +1121,12 @@ fd_status fd_decode_tree(const float* q, const fd_tree_desc* tree, const fd_kv_d
     CUtensorMap tk, tv;
     p.box_rows = tree_box_rows(p.kv.paged ? kv->page_size : 64);
     if ((st = make_maps(kv, B, Hkv, D, &tk, &tv, (cuuint32_t)p.box_rows)) != FD_OK) return st;
-    if (launch_tree_mma(D, tk, tv, p, s) != cudaSuccess) return FD_ERR_CUDA;
+    const cudaError_t e = t.block == kTreeRowsMma ? launch_tree_mma(D, tk, tv, p, s) : launch_tree_keys(D, t.block, tk, tv, p, s);
+    if (e != cudaSuccess) return FD_ERR_CUDA;
   }
   // a sequence of one tile lies within a share
   if (t.ranges == 1 || max_seq_len <= kPlanTile) return FD_OK;
-  return launch_tree_join(D, f32, p, s) == cudaSuccess ? FD_OK : FD_ERR_CUDA;
+  return launch_tree_join(D, t.block, p, s) == cudaSuccess ? FD_OK : FD_ERR_CUDA;
 }
 
 fd_status fd_verify_tree(const fd_tree_desc* tree, const int32_t* tokens, const float* uniforms, const void* target,

@@ -230,7 +230,9 @@ __global__ void __launch_bounds__(256, 4) fd_tree_join_kernel(const TreeParams p
   if (f >= p.n_joins) return;
   const TreeJoin j = p.joins[f];
   const int32_t row = sub * Rows + r;
-  if (j.b < 0 || row >= p.rows || row % p.tree.n < p.tree.n - tree_tokens(p.tree, j.b)) return;
+  // (a call that gave up may have left an entry of an earlier one)
+  if (j.b < 0 || j.b >= p.B || j.h < 0 || j.h >= p.Hkv || j.first < 0 || j.last < j.first || j.last >= p.ranges) return;
+  if (row >= p.rows || row % p.tree.n < p.tree.n - tree_tokens(p.tree, j.b)) return;
   const int32_t count = j.last - j.first + 1;
   auto state = [&](int32_t k) {
     return ((int64_t)(2 * (j.first + k) + (k == 0 ? 1 : 0)) * p.nsub + sub) * Rows + r;
@@ -307,9 +309,16 @@ cudaError_t launch_tree_core(int D, const TreeParams& p, cudaStream_t stream) {
   return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_tree_join(int D, bool f32, const TreeParams& p, cudaStream_t stream) {
-  if (D == 128) return f32 ? launch_join<128, kTreeRowsCore>(p, stream) : launch_join<128, kTreeRowsMma>(p, stream);
-  if (D == 64) return f32 ? launch_join<64, kTreeRowsCore>(p, stream) : launch_join<64, kTreeRowsMma>(p, stream);
+cudaError_t launch_tree_join(int D, int rows, const TreeParams& p, cudaStream_t stream) {
+  if (D == 128) {
+    if (rows == 32) return launch_join<128, 32>(p, stream);
+    if (rows == 64) return launch_join<128, 64>(p, stream);
+    if (rows == 128) return launch_join<128, 128>(p, stream);
+  } else if (D == 64) {
+    if (rows == 32) return launch_join<64, 32>(p, stream);
+    if (rows == 64) return launch_join<64, 64>(p, stream);
+    if (rows == 128) return launch_join<64, 128>(p, stream);
+  }
   return cudaErrorInvalidValue;
 }
 

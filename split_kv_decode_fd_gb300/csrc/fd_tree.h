@@ -68,19 +68,22 @@ struct TreeParams {
   int32_t stall_u;             // testing hook: the copy that every CTA skips, or -1
 };
 
-// Rows per CTA and CTAs per SM: fp32 caches on CUDA cores, bf16 ones on tensor cores.
+// Rows per CTA and CTAs per SM: fp32 caches on CUDA cores; bf16 ones on tensor cores, up to 64 rows of a KV head with the
+// keys on the rows of the products, more in blocks of 128 with the query rows there.
 constexpr int kTreeRowsCore = 32, kTreeCtasCore = 2;
 constexpr int kTreeRowsMma = 128;
+constexpr int tree_rows(bool f32, int rows) { return f32 || rows <= 32 ? 32 : rows <= 64 ? 64 : kTreeRowsMma; }
+constexpr int tree_ctas(bool f32) { return f32 ? kTreeCtasCore : 1; }
 // Rows of a copy: as many of 64, 32, 16 as lie in a page.  A copy takes a warp some 100 cycles to start.
 constexpr int tree_box_rows(int page) { return page % 64 == 0 ? 64 : page % 32 == 0 ? 32 : 16; }
-constexpr int tree_rows(bool f32) { return f32 ? kTreeRowsCore : kTreeRowsMma; }
-constexpr int tree_ctas(bool f32) { return f32 ? kTreeCtasCore : 1; }
 
 cudaError_t launch_tree_core(int D, const TreeParams& p, cudaStream_t stream);
 cudaError_t launch_tree_mma(int D, const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p,
                             cudaStream_t stream);
-// Joins what either left.
-cudaError_t launch_tree_join(int D, bool f32, const TreeParams& p, cudaStream_t stream);
+cudaError_t launch_tree_keys(int D, int rows, const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p,
+                             cudaStream_t stream);
+// Joins what any of them left; rows: those of a CTA.
+cudaError_t launch_tree_join(int D, int rows, const TreeParams& p, cudaStream_t stream);
 
 // Which drafts stay (fd_verify_tree).
 struct VerifyParams {

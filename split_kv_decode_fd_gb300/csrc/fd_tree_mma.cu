@@ -27,16 +27,14 @@
 //        core has the S of the next and the O of the one before.
 #include <atomic>
 
-#include "fd_tcgen05.cuh"
-#include "fd_tree.cuh"
+#include "fd_tree_tc.cuh"
 
 namespace fdk {
 namespace {
 
 constexpr int kRows = kTreeRowsMma;
 constexpr int kKeys = kPlanTile;
-constexpr int kThreads = 384;
-constexpr int kParts = 3;                 // bf16 numbers that q and p are cut into
+constexpr int kThreads = 352;
 constexpr int kCopyK = 8, kCopyV = 9, kSWarp = 10;  // and O: 11
 constexpr int kPBufs = 4;                // barriers of P and places for a tile's max
 // Tensor memory: two S / P buffers and O.  P takes 8 columns for each part of 16 keys, 192 in
@@ -77,112 +75,6 @@ struct Misc {
 };
 static_assert(sizeof(Misc) <= 3072, "Misc");
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-// Pairs of floats in one register pair: the packed arithmetic rounds each as the scalar one does.
-__device__ __forceinline__ uint64_t pack2(float x, float y) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
-  return d;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float& x, float& y) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
-__device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
-  asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
-}
-// 32 bytes in one store where the address allows it: 16-byte stores of rows far apart send each sector to L2 twice.
-__device__ __forceinline__ void store32(float* to, const float* v) {
-  if ((reinterpret_cast<uintptr_t>(to) & 31) == 0) {
-    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "f"(v[0]), "f"(v[1]), "f"(v[2]),
-                 "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
-                 : "memory");
-  } else {
-    reinterpret_cast<float4*>(to)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(to)[1] = make_float4(v[4], v[5], v[6], v[7]);
-  }
-}
-__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-// The upper 16 bits of both, x's in the low half: their bf16 truncations.
-__device__ __forceinline__ uint32_t trunc2(float x, float y) {
-  return __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
-}
-__device__ __forceinline__ float trunc1(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
-
-// x and y as sums of three bf16 numbers each, exactly (24 bits = 3 x 8).
-__device__ __forceinline__ void cut3(float x, float y, uint32_t (&w)[kParts]) {
-  w[0] = trunc2(x, y);
-  float a, b;
-  unpack2(sub2(pack2(x, y), pack2(trunc1(x), trunc1(y))), a, b);
-  w[1] = trunc2(a, b);
-  float c, d;
-  unpack2(sub2(pack2(a, b), pack2(trunc1(a), trunc1(b))), c, d);
-  w[2] = trunc2(c, d);
-}
-
-// One lane of a converged warp, known as such to the compiler.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-  return r != 0;
-}
-__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
-
-// Waits of all roles: false when the CTA gives up or the limit runs out.
-struct Waits {
-  Misc* s;
-  unsigned long long limit;
-  bool ok = true;
-  __device__ __forceinline__ void on(uint64_t* bar, uint32_t parity) {
-    if (ok && !mbar_try_wait(bar, parity)) ok = !s->abort && mbar_wait_for(bar, parity, limit);
-  }
-  // The warp's lanes alike.
-  __device__ __forceinline__ bool all() {
-    ok = __all_sync(0xffffffffu, ok);
-    return ok;
-  }
-};
-
-// Uses of the ring: slot u % n in phase u / n.
-template <uint32_t N>
-struct Ring {
-  uint32_t slot = 0, phase = 0;
-  __device__ __forceinline__ void next(uint32_t by = 1) {
-    slot += by;
-    if (slot >= N) {
-      slot -= N;
-      phase ^= 1u;
-    }
-  }
-};
-
 template <int D, int Rows>
 __global__ void __launch_bounds__(kThreads, 1)
     fd_tree_mma_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
@@ -216,7 +108,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(s.p_empty + i, 1);
       mbar_init(s.o_empty + i, warps);
       mbar_init(s.piece_full + i, 1);
-      mbar_init(s.piece_empty + i, 3 + 2 * warps);
+      mbar_init(s.piece_empty + i, 2 + 2 * warps);
       mbar_init(s.drain + i, 1);
     }
     for (int i = 0; i < kPBufs; ++i) mbar_init(s.p_full + i, warps);
@@ -241,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tmem_fence_after();
   const uint32_t tmem = s.tmem;
   pdl_wait();
-  Waits w{&s, p.wait_ns ? (unsigned long long)p.wait_ns : kWaitLimitNs};
+  Waits w{&s.abort, p.wait_ns ? (unsigned long long)p.wait_ns : kWaitLimitNs};
 
   // The next piece, for a warp; false at the end.
   auto take = [&](uint32_t e, TreePiece& pc) -> bool {
@@ -253,46 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     return pc.b >= 0;
   };
 
-  // Copies of K or V, by one warp: lane l holds the place of the tile's rows [box l, box (l + 1)), a run of a page.
-  const int32_t box = p.box_rows, boxes = kKeys / box;
-  const bool shared_keys = p.nsub > 1;  // other CTAs read them too: they stay in L2
-  const uint64_t once = policy_evict_first();
-  auto page_of = [&](const TreePiece& pc, int32_t j) -> int32_t {
-    const int32_t t = pc.begin + j * kKeys + box * lane;
-    return p.kv.paged && lane < boxes && t < pc.end
-               ? __ldg(p.kv.block_table + (int64_t)pc.b * p.kv.max_pages + t / p.kv.page_size)
-               : -1;
-  };
-  auto copy = [&](const CUtensorMap* map, const TreePiece& pc, int32_t j, int32_t page, uint8_t* to, uint64_t* full) {
-    const int32_t t = pc.begin + j * kKeys + box * lane;
-    bool mine = lane < boxes && t < pc.end;
-    int32_t row = t, z = pc.b * p.Hkv + pc.h;
-    if (p.kv.paged) {
-      if (mine && (page < 0 || page >= p.kv.num_pages)) {
-        atomicOr(p.err, kErrBadIndex);
-        mine = false;
-      }
-      row = t % p.kv.page_size;
-      z = page * p.Hkv + pc.h;
-    }
-    uint32_t which = __ballot_sync(0xffffffffu, mine);
-    if (elect_one()) mbar_arrive_expect_tx(full, (uint32_t)(__popc(which) * box) * Lay::kNB * 128u);
-    for (; which; which &= which - 1) {
-      const int32_t i = __ffs(which) - 1;
-      const int32_t y = __shfl_sync(0xffffffffu, row, i), zz = __shfl_sync(0xffffffffu, z, i);
-      uint8_t* dst = to + (uint32_t)(i * box) * 128u;
-      if (elect_one()) {
-#pragma unroll
-        for (int blk = 0; blk < Lay::kNB; ++blk) {
-          if (p.kv.paged || shared_keys)
-            tma_load_3d(dst + blk * kBlock, map, full, blk * 64, y, zz);
-          else
-            tma_load_3d_hint(dst + blk * kBlock, map, full, blk * 64, y, zz, once);
-        }
-      }
-    }
-    __syncwarp();
-  };
+  const TileCopy copy(p);
   // Rows [64 i, 64 (i + 1)) of the q of piece e, which lie side by side, into a slot.  They have barriers of their own, as
   // the softmax waits for them without having waited for the slot's other uses; two, as q of the next piece may come
   // before the softmax looks (not that of the one after: no ring has five slots).
@@ -307,16 +160,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   };
-  // At the end of the work the products have waited for every copy.  A CTA that gives up must not leave while one may
-  // still be landing: its warp waits for the last use of each of its slots (`u` uses so far, of n slots; use `skipped` was
-  // not started).
   auto leave = [&](uint64_t* full, uint32_t u, uint32_t n, uint32_t skipped, uint32_t i, uint32_t f) {
     if (w.ok) return;
     s.abort = 1;
     if (lane != 0) return;
     atomicOr(p.err, kErrTimeout);
-    for (uint32_t x = u > n ? u - n : 0; x < u; ++x)
-      if (x != skipped) mbar_wait_for(full + x % n, (x / n) & 1, w.limit);
+    land(full, u, n, skipped, w.limit);
     for (uint32_t e = f > 2 ? f - 2 : 0; e < f; ++e) mbar_wait_for(&s.q_full[e & 1][i], (e >> 1) & 1, w.limit);
   };
 
@@ -337,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (pc.b < 0) break;
       const int32_t n = ceil_div(pc.end - pc.begin, kKeys);
-      int32_t page = page_of(pc, 0);
+      int32_t page = copy.page_of(pc, 0);
       w.on(s.k_empty + r.slot, r.phase ^ 1u);
       if (!w.all()) break;
       copy_q(pc, e, 0, smem + Lay::kRing + r.slot * kTile, s.k_full + r.slot);
@@ -345,13 +194,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++u;
       r.next();
       for (int32_t j = 0; j < n; ++j, ++u, r.next()) {
-        const int32_t next = page_of(pc, j + 1);
+        const int32_t next = copy.page_of(pc, j + 1);
         w.on(s.k_empty + r.slot, r.phase ^ 1u);
         if (!w.all()) break;
         if (p.stall_u >= 0 && u == (uint32_t)p.stall_u)
           skipped = u;  // testing hook
         else
-          copy(&tmap_k, pc, j, page, smem + Lay::kRing + r.slot * kTile, s.k_full + r.slot);
+          copy.start<Lay::kNB>(&tmap_k, pc, j, page, smem + Lay::kRing + r.slot * kTile, s.k_full + r.slot);
         page = next;
       }
       if (!w.ok) break;
@@ -364,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     TreePiece pc;
     for (uint32_t e = 0; take(e, pc); ++e) {
       const int32_t n = ceil_div(pc.end - pc.begin, kKeys);
-      int32_t page = page_of(pc, 0);
+      int32_t page = copy.page_of(pc, 0);
       if (nq == 2) {
         w.on(s.v_empty + r.slot, r.phase ^ 1u);
         if (!w.all()) break;
@@ -374,16 +223,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         r.next();
       }
       for (int32_t j = 0; j < n; ++j, ++u, r.next()) {
-        const int32_t next = page_of(pc, j + 1);
+        const int32_t next = copy.page_of(pc, j + 1);
         w.on(s.v_empty + r.slot, r.phase ^ 1u);
         if (!w.all()) break;
-        copy(&tmap_v, pc, j, page, smem + Lay::kVRing + r.slot * kTile, s.v_full + r.slot);
+        copy.start<Lay::kNB>(&tmap_v, pc, j, page, smem + Lay::kVRing + r.slot * kTile, s.v_full + r.slot);
         page = next;
       }
       if (!w.ok) break;
     }
     leave(s.v_full, u, Lay::kV, 0xffffffffu, 1, f);
-  } else if (warp >= kSWarp) {
+  } else if (warp == kSWarp) {
     // ------------------------------------------------------------ products
     // Every branch and operand is uniform over the warp as the compiler sees it (votes and shuffles), so that the
     // products take their operands from uniform registers as they are.
@@ -392,29 +241,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool is_s = uniform((uint32_t)warp) == kSWarp;
     Ring<Lay::kK> rk;
     Ring<Lay::kV> rv;
-    uint32_t g = 0, f = 0, uv = 0;  // tiles, pieces and uses of V's slots so far
+    uint32_t g = 0, f = 0;  // tiles and pieces so far
     TreePiece pc;
     for (uint32_t e = 0; take(e, pc); ++e) {
       const uint32_t n = uniform((uint32_t)ceil_div(pc.end - pc.begin, kKeys));
-      if (is_s) {
-        w.on(&s.q_ready, f & 1);
-        if (!w.all()) break;
-        if (elect_one()) {  // the slots that q came in
-          mbar_arrive(s.k_empty + rk.slot);
-          if (nq == 2) mbar_arrive(s.v_empty + uv % Lay::kV);
-        }
-        __syncwarp();
-        rk.next();
-        uv += nq - 1 + n;
-        for (uint32_t j = 0; j < n; ++j, rk.next()) {
+      w.on(&s.q_ready, f & 1);
+      if (!w.all()) break;
+      if (elect_one()) {  // the slots that q came in
+        mbar_arrive(s.k_empty + rk.slot);
+        if (nq == 2) mbar_arrive(s.v_empty + rv.slot);
+      }
+      __syncwarp();
+      rk.next();
+      if (nq == 2) rv.next();
+      for (uint32_t j = 0; j <= n; ++j) {
+        if (j < n) {
           const uint32_t t = g + j;
           w.on(s.k_full + rk.slot, rk.phase);
-          if (t >= 2) w.on(s.p_empty + (t & 1), ((t - 2) >> 1) & 1);
           if (!w.all()) break;
           tmem_fence_after();
           if (elect_one()) {
             const uint32_t d = base + (t & 1) * kBuf + kSOff, k = k0 + rk.slot * kTile;
-            // the small parts of q first: their sums lose least
 #pragma unroll
             for (int part = kParts - 1; part >= 0; --part) {
 #pragma unroll
@@ -428,11 +275,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_commit(smem_addr(s.k_empty + rk.slot));
           }
           __syncwarp();
+          rk.next();
         }
-      } else {
-        if (nq == 2) rv.next();
-        for (uint32_t j = 0; j < n; ++j, rv.next()) {
-          const uint32_t t = g + j;
+        if (j > 0) {
+          const uint32_t t = g + j - 1;
           w.on(s.v_full + rv.slot, rv.phase);
           w.on(s.p_full + t % kPBufs, (t / kPBufs) & 1);
           if (t > 0) w.on(s.o_empty + ((t - 1) & 1), ((t - 1) >> 1) & 1);
@@ -452,6 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_commit(smem_addr(s.v_empty + rv.slot));
           }
           __syncwarp();
+          rv.next();
         }
       }
       if (!w.ok) break;
@@ -740,7 +587,7 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const TreeParam
 
 cudaError_t launch_tree_mma(int D, const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p,
                             cudaStream_t stream) {
-  if (D == 128) return p.rows <= 64 ? launch<128, 64>(tk, tv, p, stream) : launch<128, 128>(tk, tv, p, stream);
+  if (D == 128) return launch<128, 128>(tk, tv, p, stream);
   if (D == 64) return launch<64, 128>(tk, tv, p, stream);
   return cudaErrorInvalidValue;
 }
