@@ -1,15 +1,18 @@
 // fd_tree_keys.cu -- attention of a tree of drafted tokens over a bf16 cache, up to 64
 // rows a KV head: keys on the rows of the matrix products, query rows on their columns.
 //
-//     S^T = K Q^T   (128 keys x N rows, over D)       O^T = V^T P   (D x N rows, over 128 keys)
+//     S^T = K Q^T   (128 keys x rows, over D)       O^T = V^T P   (D x rows, over 128 keys)
 //
 // so that K and V are read from shared memory where they land, as the first operands, and a
 // product's work goes with the rows there are (N = 32 or 64), not with 128 (fd_tree_mma.cu).
 //
 // Precision: K and V are exact in bf16.  q and p (fp32) are cut into three bf16 numbers of eight
-// bits each by truncation, which is exact, so all products are, and fp32 sums are what rounds:
-// S sums its small parts first, and O is taken out of tensor memory every tile and added up in
-// registers, since the adds of the matrix unit drop bits.
+// bits each by truncation, which is exact, so all products are, and fp32 sums are what rounds.
+// The parts of q lie side by side as 3 N columns of one product, so that K is read once for
+// all of them, and their columns are added in registers, small parts first; of p the first two parts, and
+// the third is added to the columns of the second.  (A product for each part read 400 KB of shared memory a
+// tile, 3100 cycles of its bandwidth.)  O is taken out of tensor memory every tile, since
+// the adds of the matrix unit drop bits.
 //
 // A row's reference (what its scores are taken relative to) is the same for all keys, and moves only when a score of a
 // tile exceeds it by 2^kTau: a vote of the threads says so, and then the tile's maxima are found.
@@ -37,10 +40,10 @@ template <int D, int N>
 struct Layout {
   static constexpr int kNB = D / 64;                        // 128-byte column blocks of a row
   static constexpr uint32_t kTile = kNB * kTileBlock;       // a K or V tile
-  static constexpr uint32_t kQBlock = N * 128u;             // a column block of a part of q
-  static constexpr uint32_t kQPart = kNB * kQBlock;
+  static constexpr uint32_t kQPart = N * 128u;              // rows of a part of q in a column block
+  static constexpr uint32_t kQBlock = kParts * kQPart;
   static constexpr uint32_t kPPart = kKeys * N * 2u;        // a part of p: [N / 8][128 keys][8 rows]
-  static constexpr uint32_t kP = kParts * kQPart;           // q first
+  static constexpr uint32_t kP = kNB * kQBlock;             // q first
   static constexpr uint32_t kRing = kP + kParts * kPPart;
   static constexpr uint32_t kK = D == 64 ? 4 : N == 32 ? 3 : 2, kV = D == 64 ? 4 : 2;  // slots
   static constexpr uint32_t kVRing = kRing + kK * kTile;
@@ -55,14 +58,14 @@ template <int N>
 struct Misc {
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
   uint64_t q_full[2];                  // of even and odd pieces
-  uint64_t s_full[2], s_empty[2], o_full[2], o_empty[2], moves_full[kMoves];
+  uint64_t s_full[2], s_empty[2], o_full, o_empty, moves_full[kMoves];
   uint64_t piece_full[2], piece_empty[2];
   uint64_t p_full, p_empty, q_ready, fin_full, fin_empty, drain[2];
   uint32_t tmem;
   volatile int abort;
   TreePiece piece[2];
   alignas(16) float move[kMoves][N];   // what the sums so far are multiplied by; move[.][half] < 0: they are not
-  alignas(16) float ref[N];            // references, base 2
+  alignas(16) float ref[N];            // references, base 2, with the other sign
   float part[8][N / 2];                // by warp: maxima of a tile, sums of a piece
   uint64_t unfit[8];                   // tokens whose values are not finite, as the softmax warps met them
 };
@@ -132,13 +135,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(s.q_full + i, 1);
       mbar_init(s.s_full + i, 1);
       mbar_init(s.s_empty + i, 8);
-      mbar_init(s.o_full + i, 1);
-      mbar_init(s.o_empty + i, 4);
       mbar_init(s.piece_full + i, 1);
       mbar_init(s.piece_empty + i, 3 + 8 + 4);
       mbar_init(s.drain + i, 1);
     }
     for (int i = 0; i < kMoves; ++i) mbar_init(s.moves_full + i, 8);
+    mbar_init(&s.o_full, 1);
+    mbar_init(&s.o_empty, 4);
     mbar_init(&s.p_full, 8);
     mbar_init(&s.p_empty, 1);
     mbar_init(&s.q_ready, 8);
@@ -154,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tmem_fence_before();
   cta_sync();
   tmem_fence_after();
-  // Tensor memory: two buffers of S^T, then two of O^T, N columns each.
+  // Tensor memory: two buffers of S^T of 3 N columns (with one, K's slot waited for the softmax), then O^T, 2 N columns.
   const uint32_t tmem = s.tmem;
   pdl_wait();
   Waits w{&s.abort, p.wait_ns ? (unsigned long long)p.wait_ns : kWaitLimitNs};
@@ -251,7 +254,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ products
     // Every branch and operand is uniform over the warp as the compiler sees it (votes and shuffles), so that the
     // products take their operands from uniform registers as they are.
-    constexpr uint32_t idS = bf16_instr_desc(kKeys, N), idO = bf16_instr_desc(D, N, true) | kAlongRows;
+    constexpr uint32_t idS = bf16_instr_desc(kKeys, kParts * N), idO = bf16_instr_desc(D, 2 * N, true) | kAlongRows,
+                       idLast = bf16_instr_desc(D, N, true) | kAlongRows;
     const uint32_t base = uniform(tmem), q0 = uniform(sq), p0 = uniform(sp), k0 = uniform(k_ring), v0 = uniform(v_ring);
     const bool is_s = uniform((uint32_t)warp) == kSWarp;
     Ring<Lay::kK> rk;
@@ -273,17 +277,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!w.all()) break;
           tmem_fence_after();
           if (elect_one()) {
-            const uint32_t d = base + (t & 1) * N, k = k0 + rk.slot * kTile;
-            // the small parts of q first: their sums lose least
+            const uint32_t d = base + (t & 1) * (kParts * N), k = k0 + rk.slot * kTile;
 #pragma unroll
-            for (int part = kParts - 1; part >= 0; --part) {
-#pragma unroll
-              for (int i = 0; i < D / 16; ++i) {
-                const uint32_t block = (uint32_t)(i >> 2), off = (uint32_t)(i & 3) * 32u;
-                mma_ss(d, b_desc(k + block * kTileBlock + off),
-                       b_desc(q0 + (uint32_t)part * Lay::kQPart + block * Lay::kQBlock + off), idS,
-                       part != kParts - 1 || i != 0);
-              }
+            for (int i = 0; i < D / 16; ++i) {
+              const uint32_t block = (uint32_t)(i >> 2), off = (uint32_t)(i & 3) * 32u;
+              mma_ss(d, b_desc(k + block * kTileBlock + off), b_desc(q0 + block * Lay::kQBlock + off), idS, i != 0);
             }
             mma_commit(smem_addr(s.s_full + (t & 1)));
             mma_commit(smem_addr(s.k_empty + rk.slot));
@@ -295,20 +293,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t t = g + j;
           w.on(s.v_full + rv.slot, rv.phase);
           w.on(&s.p_full, t & 1);
-          if (t >= 2) w.on(s.o_empty + (t & 1), ((t - 2) >> 1) & 1);
+          if (t > 0) w.on(&s.o_empty, (t - 1) & 1);
           if (!w.all()) break;
           tmem_fence_after();
           if (elect_one()) {
-            const uint32_t d = base + (2 + (t & 1)) * N, v = v0 + rv.slot * kTile;
+            const uint32_t d = base + 2 * kParts * N, v = v0 + rv.slot * kTile;
 #pragma unroll
-            for (int part = kParts - 1; part >= 0; --part) {
+            for (int i = 0; i < kKeys / 16; ++i)
+              mma_ss(d, b_desc_rows(v + (uint32_t)i * 2048u, kTileBlock), b_desc_n<kKeys * 16>(p0 + (uint32_t)i * 256u), idO,
+                     i != 0);
 #pragma unroll
-              for (int i = 0; i < kKeys / 16; ++i)
-                mma_ss(d, b_desc_rows(v + (uint32_t)i * 2048u, kTileBlock),
-                       b_desc_n<kKeys * 16>(p0 + (uint32_t)part * Lay::kPPart + (uint32_t)i * 256u), idO,
-                       part != kParts - 1 || i != 0);
-            }
-            mma_commit(smem_addr(s.o_full + (t & 1)));
+            for (int i = 0; i < kKeys / 16; ++i)
+              mma_ss(d + N, b_desc_rows(v + (uint32_t)i * 2048u, kTileBlock),
+                     b_desc_n<kKeys * 16>(p0 + 2 * Lay::kPPart + (uint32_t)i * 256u), idLast, 1);
+            mma_commit(smem_addr(&s.o_full));
             mma_commit(smem_addr(&s.p_empty));
             mma_commit(smem_addr(s.v_empty + rv.slot));
           }
@@ -374,93 +372,129 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.q_ready);
-      Ancestors all{0, 0};
-      if (pc.end > P) all = tree_ancestors(p.tree, pc.b, pc.m, p.err);
-      uint64_t unfit = 0;
+      uint64_t anc = 0, unfit = 0;  // of the token of row r0 + lane: its ancestors and itself
+      if (pc.end > P) {
+        const Ancestors all = tree_ancestors(p.tree, pc.b, pc.m, p.err);
+        anc = all.of((row0 + r0 + lane) % p.tree.n - (p.tree.n - pc.m));
+      }
       // The references of the piece before have been read.
       if (e >= 1) w.on(&s.fin_empty, (e - 1) & 1);
-      if ((warp & 3) == 0 && lane < kHalf) s.ref[r0 + lane] = kNoRef;
+      if ((warp & 3) == 0 && lane < kHalf) s.ref[r0 + lane] = -kNoRef;
       group_or(false, id);
-      float l[kHalf];
+      uint64_t l[kHalf / 2];  // this key's sums of the rows, in pairs
 #pragma unroll
-      for (int i = 0; i < kHalf; ++i) l[i] = 0.f;
+      for (int i = 0; i < kHalf / 2; ++i) l[i] = 0;
       for (int32_t j = 0; j < n; ++j) {
         const uint32_t t = g + (uint32_t)j;
         const int32_t t0 = pc.begin + j * kKeys;
         const bool some_hidden = t0 + kKeys > P;
         w.on(s.s_full + (t & 1), (t >> 1) & 1);
         tmem_fence_after();
-        float x[kHalf];
-        tmem_load<kHalf>(tmem + (t & 1) * N + group * kHalf + ((uint32_t)((warp & 3) * 32) << 16), x);
+        uint64_t x[kHalf / 2];  // scores of two rows
+        {
+          const uint32_t at = tmem + (t & 1) * (kParts * N) + group * kHalf + ((uint32_t)((warp & 3) * 32) << 16);
+          uint32_t v0[kHalf], v1[kHalf];
+          TmemRow<kHalf>::load(at + 2 * N, v0);
+          TmemRow<kHalf>::load(at + N, v1);
+          tmem_wait_loads();
+          TmemRow<kHalf>::tie(v0);
+          TmemRow<kHalf>::tie(v1);
+          auto pair = [](const uint32_t* v) { return pack2(__uint_as_float(v[0]), __uint_as_float(v[1])); };
+#pragma unroll
+          for (int i = 0; i < kHalf / 2; ++i) x[i] = add2(pair(v0 + 2 * i), pair(v1 + 2 * i));
+          TmemRow<kHalf>::load(at, v0);
+          tmem_wait_loads();
+          TmemRow<kHalf>::tie(v0);
+#pragma unroll
+          for (int i = 0; i < kHalf / 2; ++i) x[i] = add2(x[i], pair(v0 + 2 * i));
+        }
         tmem_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(s.s_empty + (t & 1));
         if (some_hidden) {
           const int32_t a = t0 + key - P;  // the key's token
+          const bool drafted = a >= 0, none = a >= 64;
 #pragma unroll
-          for (int i = 0; i < kHalf; ++i) {
-            const uint64_t anc = all.of((row0 + r0 + i) % p.tree.n - (p.tree.n - pc.m));
-            if (a >= 0 && (a >= 64 || !(anc >> a & 1))) x[i] = -INFINITY;
+          for (int i = 0; i < kHalf; i += 2) {
+            float x0, x1;
+            unpack2(x[i / 2], x0, x1);
+            const uint64_t see0 = __shfl_sync(0xffffffffu, anc, i), see1 = __shfl_sync(0xffffffffu, anc, i + 1);
+            if (drafted && (none || !(see0 >> (a & 63) & 1))) x0 = -INFINITY;
+            if (drafted && (none || !(see1 >> (a & 63) & 1))) x1 = -INFINITY;
+            x[i / 2] = pack2(x0, x1);
           }
         }
-        // relative to the references; a NaN does not vote
-        float y[kHalf], top = -INFINITY;
+        // relative to the references (kept with the other sign); a NaN does not vote
+        uint64_t y[kHalf / 2];
+        const uint64_t f2 = pack2(f, f);
         auto relative = [&] {
 #pragma unroll
-          for (int i = 0; i < kHalf; i += 4) {
-            const float4 ref = lds128(smem_addr(s.ref + r0 + i));
-            y[i] = fmaf(x[i], f, -ref.x);
-            y[i + 1] = fmaf(x[i + 1], f, -ref.y);
-            y[i + 2] = fmaf(x[i + 2], f, -ref.z);
-            y[i + 3] = fmaf(x[i + 3], f, -ref.w);
+          for (int i = 0; i < kHalf / 2; i += 2) {
+            const float4 ref = lds128(smem_addr(s.ref + r0 + 2 * i));
+            y[i] = fma2(x[i], f2, pack2(ref.x, ref.y));
+            y[i + 1] = fma2(x[i + 1], f2, pack2(ref.z, ref.w));
           }
         };
         relative();
+        float top = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < kHalf; i += 2) top = max3(top, y[i], y[i + 1]);
+        for (int i = 0; i < kHalf / 2; ++i) {
+          float y0, y1;
+          unpack2(y[i], y0, y1);
+          top = max3(top, y0, y1);
+        }
         const bool moved = group_or(top > kTau, id);
         float* move = s.move[t % kMoves] + r0;
         if (moved) {
           // the tile's largest score of each row: of a warp's keys in lane i % kHalf, then of the four warps
+          float best[kHalf];
 #pragma unroll
-          for (int i = 0; i < kHalf; ++i) y[i] = x[i] * f;
-          const float best = across(y, [](float a, float b) { return fmaxf(a, b); });
-          if (lane < kHalf) s.part[warp][lane] = best;
+          for (int i = 0; i < kHalf / 2; ++i) {
+            float x0, x1;
+            unpack2(x[i], x0, x1);
+            best[2 * i] = x0 * f;
+            best[2 * i + 1] = x1 * f;
+          }
+          const float most = across(best, [](float a, float b) { return fmaxf(a, b); });
+          if (lane < kHalf) s.part[warp][lane] = most;
           group_or(false, id);
           if ((warp & 3) == 0 && lane < kHalf) {
-            float m = s.ref[r0 + lane];
-            const float old = m;
+            const float old = -s.ref[r0 + lane];
+            float m = old;
 #pragma unroll
             for (int i = 0; i < 4; ++i) m = fmaxf(m, s.part[4 * group + i][lane]);
-            s.ref[r0 + lane] = m;
+            s.ref[r0 + lane] = -m;
             move[lane] = old == m ? 1.f : ex2(old - m);
           }
           group_or(false, id);
           relative();
 #pragma unroll
-          for (int i = 0; i < kHalf; ++i) l[i] *= move[i];
+          for (int i = 0; i < kHalf / 2; ++i) l[i] = mul2(l[i], pack2(move[2 * i], move[2 * i + 1]));
         } else if ((warp & 3) == 0 && lane == 0) {
           move[0] = -1.f;
         }
+        uint32_t a[kParts][kHalf / 2];
+#pragma unroll
+        for (int i = 0; i < kHalf / 2; ++i) {
+          float e0, e1;
+          unpack2(y[i], e0, e1);
+          e0 = ex2(e0);
+          e1 = ex2(e1);
+          l[i] = add2(l[i], pack2(e0, e1));
+          uint32_t part[kParts];
+          cut3(e0, e1, part);
+#pragma unroll
+          for (int k = 0; k < kParts; ++k) a[k][i] = part[k];
+        }
         // P's place is free once O of the tile before has read it
         if (t > 0) w.on(&s.p_empty, (t - 1) & 1);
+        const uint32_t to = sp + (uint32_t)(r0 / 8) * (kKeys * 16u) + (uint32_t)key * 16u;
 #pragma unroll
-        for (int c = 0; c < kHalf / 8; ++c) {
-          uint32_t a[kParts][4];
+        for (int k = 0; k < kParts; ++k)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float e0 = ex2(y[8 * c + 2 * i]), e1 = ex2(y[8 * c + 2 * i + 1]);
-            l[8 * c + 2 * i] += e0;
-            l[8 * c + 2 * i + 1] += e1;
-            uint32_t part[kParts];
-            cut3(e0, e1, part);
-#pragma unroll
-            for (int k = 0; k < kParts; ++k) a[k][i] = part[k];
-          }
-          const uint32_t to = sp + (uint32_t)(r0 / 8 + c) * (kKeys * 16u) + (uint32_t)key * 16u;
-#pragma unroll
-          for (int k = 0; k < kParts; ++k) sts128(to + (uint32_t)k * Lay::kPPart, a[k][0], a[k][1], a[k][2], a[k][3]);
-        }
+          for (int c = 0; c < kHalf / 8; ++c)
+            sts128(to + (uint32_t)k * Lay::kPPart + (uint32_t)c * (kKeys * 16u), a[k][4 * c], a[k][4 * c + 1], a[k][4 * c + 2],
+                   a[k][4 * c + 3]);
         if (some_hidden) {
           // V's rows at or past the length may hold anything, and so may those of the drafts, which not every
           // row sees: 0 * NaN is not 0.  Values that are no numbers become 0 here and are added to the rows that
@@ -501,7 +535,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       g += (uint32_t)n;
       uk += 1 + (uint32_t)n;
       // the rows' sums over this warp's keys
-      const float sum = across(l, [](float a, float b) { return a + b; });
+      float mine[kHalf];
+#pragma unroll
+      for (int i = 0; i < kHalf / 2; ++i) unpack2(l[i], mine[2 * i], mine[2 * i + 1]);
+      const float sum = across(mine, [](float a, float b) { return a + b; });
       group_or(false, id);  // the maxima of the last tile have been read
       if (lane < kHalf) s.part[warp][lane] = sum;
       unfit = ((uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(unfit >> 32)) << 32) |
@@ -524,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kLanes = D / 4;
     const int32_t channel = (warp & 3) * kLanes + lane % kLanes;
     const bool holds = lane < kLanes;
-    const uint32_t at = tmem + 2 * N + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t at = tmem + 2 * kParts * N + ((uint32_t)((warp & 3) * 32) << 16);
     tree_no_rows<D, N>(p, range, sub, tid - kSums * 32, 128);
     uint32_t g = 0;
     TreePiece pc;
@@ -544,18 +581,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < kHalf; ++i) acc[h * kHalf + i] *= move[h * kHalf + i];
           }
         }
-        w.on(s.o_full + (t & 1), (t >> 1) & 1);
+        w.on(&s.o_full, t & 1);
         tmem_fence_after();
 #pragma unroll
         for (int c = 0; c < N; c += 32) {
-          float o[32];
-          tmem_load<32>(at + (t & 1) * N + (uint32_t)c, o);
+          float o[32], small[32];
+          tmem_load<32>(at + (uint32_t)(N + c), small);
+          tmem_load<32>(at + (uint32_t)c, o);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) acc[c + i] += o[i];
+          for (int i = 0; i < 32; ++i) acc[c + i] += o[i] + small[i];
         }
         tmem_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(s.o_empty + (t & 1));
+        if (lane == 0) mbar_arrive(&s.o_empty);
       }
       g += (uint32_t)n;
       w.on(&s.fin_full, e & 1);
@@ -565,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; k < N / 32; ++k) {
         const int32_t r = lane + 32 * k, of = r / kHalf, in = r % kHalf;
         l[k] = (s.part[4 * of][in] + s.part[4 * of + 1][in]) + (s.part[4 * of + 2][in] + s.part[4 * of + 3][in]);
-        m[k] = s.ref[r];
+        m[k] = -s.ref[r];
       }
       uint64_t unfit = 0;
       for (int i = 0; i < 8; ++i) unfit |= s.unfit[i];
@@ -573,6 +611,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&s.fin_empty);
       if (unfit) {
         const Ancestors all = tree_ancestors(p.tree, pc.b, pc.m, p.err);
+        uint64_t anc[N / 32];
+#pragma unroll
+        for (int k = 0; k < N / 32; ++k) anc[k] = all.of((row0 + lane + 32 * k) % p.tree.n - (p.tree.n - pc.m));
         for (uint64_t u = unfit; u; u &= u - 1) {
           const int32_t a = __ffsll((long long)u) - 1, place = pc.len - pc.m + a;
           int64_t v_row = ((int64_t)pc.b * p.Hkv + pc.h) * p.kv.capacity + place;
@@ -585,28 +626,34 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool bad = (bits & 0x7f800000u) == 0x7f800000u;
 #pragma unroll
           for (int i = 0; i < N; ++i) {
-            const uint64_t anc = all.of((row0 + i) % p.tree.n - (p.tree.n - pc.m));
-            if (bad && (anc >> a & 1)) acc[i] += __uint_as_float(bits);
+            const uint64_t see = __shfl_sync(0xffffffffu, anc[i / 32], i % 32);
+            if (bad && (see >> a & 1)) acc[i] += __uint_as_float(bits);
           }
         }
       }
+      // rows that are tokens' (a division for each of them, unrolled, was 64 KB of code to fetch: 15 us a piece)
       const int32_t pad = p.tree.n - pc.m;
+      uint32_t writes[N / 32];
+      float inv[N / 32];
+#pragma unroll
+      for (int k = 0; k < N / 32; ++k) {
+        const int32_t r = lane + 32 * k;
+        writes[k] = __ballot_sync(0xffffffffu, r < live && (row0 + r) % p.tree.n >= pad && w.ok);
+        inv[k] = pc.slot >= 0 ? 1.f : (l[k] == 0.f ? 0.f : 1.f / l[k]);
+      }
       const int64_t out = ((int64_t)pc.b * p.Hkv + pc.h) * p.rows + row0;
       const int64_t state = ((int64_t)pc.slot * p.nsub + sub) * N;
       float* to = (pc.slot < 0 ? p.out + out * D : p.o_part + state * D) + channel;
-      float inv[N / 32];
-#pragma unroll
-      for (int k = 0; k < N / 32; ++k) inv[k] = pc.slot >= 0 ? 1.f : (l[k] == 0.f ? 0.f : 1.f / l[k]);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const float x = acc[i] * __shfl_sync(0xffffffffu, inv[i / 32], i % 32);
-        if (holds && w.ok && i < live && (row0 + i) % p.tree.n >= pad) to[(int64_t)i * D] = x;
+        if (holds && (writes[i / 32] >> (i % 32) & 1u)) to[i * D] = x;
       }
       if (warp == kSums && w.ok) {
 #pragma unroll
         for (int k = 0; k < N / 32; ++k) {
           const int32_t r = lane + 32 * k;
-          if (r >= live || (row0 + r) % p.tree.n < pad) continue;
+          if (!(writes[k] >> lane & 1u)) continue;
           if (pc.slot >= 0) {
             p.m_part[state + r] = m[k];
             p.l_part[state + r] = l[k];
