@@ -12,10 +12,10 @@
 // the refused words, Z is 1 less their mass.  Where the walk ends, the next token is
 // the first v with r(0) + ... + r(v) > u_0 sum r.
 //
-// Sums decide on whole numbers, so they are held in about 48 bits: a thread sums in
-// pairs of floats with the errors of its additions (Knuth's two-sum), and threads are
-// joined in 64 bits.  (In 64 bits throughout, the conversions and additions of the
-// slow pipe would take longer than the loads.)
+// Sums decide on whole numbers, so they are held in about 48 bits, as pairs of floats with
+// the errors of their additions (Knuth's two-sum), from a thread's up to the cluster's.  An
+// instruction in 64 bits takes a warp 16 cycles of the SM's pipe for them, so only one warp of a CTA
+// walks the tree (when all sixteen did, 64 sequences of 131072 words took 131 us).
 //
 // A cluster takes a sequence, each of its CTAs a part of the vocabulary; CTAs exchange
 // their sums through shared memory and decide alike.  The numbers that decide on a child
@@ -28,9 +28,10 @@
 namespace fdk {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
+constexpr int kCtas = 4;        // CTAs an SM
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -41,11 +42,64 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// A sum as two floats, hi + lo.
+struct Sum {
+  float hi, lo;
+  __device__ __forceinline__ double value() const { return (double)hi + (double)lo; }
+  __device__ __forceinline__ bool positive() const { return hi + lo > 0.f; }
+};
+__device__ __forceinline__ void add(Sum& s, float hi, float lo) {
+  const float t = __fadd_rn(s.hi, hi), b = __fsub_rn(t, s.hi);
+  s.lo += __fadd_rn(__fsub_rn(s.hi, __fsub_rn(t, b)), __fsub_rn(hi, b)) + lo;
+  s.hi = t;
+}
+// The sum over the warp's lanes, the same in each: a step's partners add in one order.
+__device__ __forceinline__ Sum warp_sum(Sum s) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const Sum other{__shfl_xor_sync(0xffffffffu, s.hi, o), __shfl_xor_sync(0xffffffffu, s.lo, o)};
+    Sum low = lane & o ? other : s;
+    const Sum high = lane & o ? s : other;
+    add(low, high.hi, high.lo);
+    s = low;
+  }
+  return s;
+}
+__device__ __forceinline__ Sum minus(Sum a, const Sum& b) {
+  add(a, -b.hi, -b.lo);
+  return a;
+}
+// The sum over lanes 0 to this one.
+__device__ __forceinline__ Sum warp_upto(Sum s) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    Sum before{__shfl_up_sync(0xffffffffu, s.hi, o), __shfl_up_sync(0xffffffffu, s.lo, o)};
+    add(before, s.hi, s.lo);
+    if (lane >= o) s = before;
+  }
+  return s;
+}
+__device__ __forceinline__ Sum from_lane(const Sum& s, int lane) {
+  return Sum{__shfl_sync(0xffffffffu, s.hi, lane), __shfl_sync(0xffffffffu, s.lo, lane)};
+}
+// The lane that holds t when the lanes' sums lie end to end, the last with a sum if rounding leaves none (-1 if none
+// has), and the rest of t within it.
+__device__ __forceinline__ int holds(const Sum& own, Sum& t) {
+  const Sum upto = warp_upto(own);
+  const unsigned some = __ballot_sync(0xffffffffu, own.positive());
+  const unsigned over = __ballot_sync(0xffffffffu, minus(upto, t).positive()) & some;
+  const int l = over ? __ffs(over) - 1 : 31 - __clz(some);
+  if (l < 0) return -1;
+  t = minus(t, from_lane(minus(upto, own), l));
+  return l;
+}
 // `v` to the same place in the shared memory of CTA `rank`.
-__device__ __forceinline__ void store_remote(double* at, uint32_t rank, double v) {
-  asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\tst.shared::cluster.f64 [a], %2;\n\t}" ::"r"(
+__device__ __forceinline__ void store_remote(Sum* at, uint32_t rank, const Sum& v) {
+  asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\tst.shared::cluster.v2.f32 [a], {%2, %3};\n\t}" ::"r"(
                    smem_addr(at)),
-               "r"(rank), "d"(v)
+               "r"(rank), "f"(v.hi), "f"(v.lo)
                : "memory");
 }
 
@@ -63,12 +117,14 @@ __device__ __forceinline__ float at<__nv_bfloat16>(const __nv_bfloat16* row, int
   return __bfloat162float(row[i]);
 }
 
-// Group g of a row of V probabilities; zeros past its end.
+// Group g of a row of V probabilities: entries [g E - off, (g + 1) E - off), `off` making them 16-byte loads (entries
+// before or past the row are 0).  vec: they are.
 template <class T>
-__device__ __forceinline__ void load_group(const T* row, int32_t g, int32_t V, bool aligned, float (&x)[kGroup<T>]) {
+__device__ __forceinline__ void load_group(const T* row, int32_t g, int32_t V, int32_t off, bool vec, float (&x)[kGroup<T>]) {
   constexpr int E = kGroup<T>;
-  if (aligned && (g + 1) * E <= V) {
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>(row) + g);
+  const int32_t first = g * E - off;
+  if (vec && first >= 0 && first + E <= V) {
+    const uint4 w = __ldg(reinterpret_cast<const uint4*>(row + first));
     if constexpr (E == 4) {
       x[0] = __uint_as_float(w.x), x[1] = __uint_as_float(w.y), x[2] = __uint_as_float(w.z), x[3] = __uint_as_float(w.w);
     } else {
@@ -77,7 +133,7 @@ __device__ __forceinline__ void load_group(const T* row, int32_t g, int32_t V, b
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = g * E + e < V ? at(row, g * E + e) : 0.f;
+    for (int e = 0; e < E; ++e) x[e] = first + e >= 0 && first + e < V ? at(row, first + e) : 0.f;
   }
 }
 
@@ -85,8 +141,8 @@ __device__ __forceinline__ void load_group(const T* row, int32_t g, int32_t V, b
 template <class T, bool kDraft>
 struct Left {
   const T *p, *q;
-  int32_t V;
-  bool aligned;
+  int32_t V, off;
+  bool vec;                   // both rows are at the same place of 16 bytes
   float c_hi, c_lo;           // c as a sum of two floats
   const int32_t* refused;     // without a draft: words that are out, those of this CTA's part
   int32_t n_refused;
@@ -110,7 +166,7 @@ struct Left {
     }
     if constexpr (!kDraft) {
       for (int32_t i = 0; i < n_refused; ++i) {
-        const int32_t e = refused[i] - g * kGroup<T>;
+        const int32_t e = refused[i] - (g * kGroup<T> - off);
 #pragma unroll
         for (int k = 0; k < kGroup<T>; ++k)
           if (k == e) hi[k] = 0.f;
@@ -119,18 +175,18 @@ struct Left {
   }
 
   // The sum over groups [g0, g1), one warp; the same value in every lane.
-  __device__ __forceinline__ double sum(int32_t g0, int32_t g1) const {
+  __device__ __forceinline__ Sum sum(int32_t g0, int32_t g1) const {
     constexpr int E = kGroup<T>, kAhead = kGroupsAhead<T>;
     const int lane = threadIdx.x & 31;
-    float s = 0.f, err = 0.f;
+    Sum s{0.f, 0.f};
     for (int32_t g = g0 + lane; g < g1; g += 32 * kAhead) {
       float x[kAhead][E], y[kAhead][E] = {};
 #pragma unroll
       for (int a = 0; a < kAhead; ++a) {
         const int32_t ga = g + 32 * a;
         if (ga < g1) {
-          load_group(p, ga, V, aligned, x[a]);
-          if constexpr (kDraft) load_group(q, ga, V, aligned, y[a]);
+          load_group(p, ga, V, off, vec, x[a]);
+          if constexpr (kDraft) load_group(q, ga, V, off, vec, y[a]);
         } else {
 #pragma unroll
           for (int e = 0; e < E; ++e) x[a][e] = 0.f;
@@ -141,90 +197,68 @@ struct Left {
         float hi[E], lo[E];
         group(x[a], y[a], g + 32 * a, hi, lo);
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float t = __fadd_rn(s, hi[e]), b = __fsub_rn(t, s);
-          err += __fadd_rn(__fsub_rn(s, __fsub_rn(t, b)), __fsub_rn(hi[e], b)) + lo[e];
-          s = t;
-        }
+        for (int e = 0; e < E; ++e) add(s, hi[e], lo[e]);
       }
     }
-    double all = (double)s + (double)err;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-    return all;
+    return warp_sum(s);
   }
 
   // The first word of groups [g0, g1) up to which the sum is over t; the last with r > 0 if rounding leaves none.
-  __device__ __forceinline__ int32_t find(int32_t g0, int32_t g1, double t) const {
+  __device__ __forceinline__ int32_t find(int32_t g0, int32_t g1, Sum t) const {
     constexpr int E = kGroup<T>;
     const int lane = threadIdx.x & 31;
-    double before = 0.0;
-    int32_t last = -1;
+    int32_t word = -1;
     for (int32_t gb = g0; gb < g1; gb += 32) {
       const int32_t g = gb + lane;
       float x[E] = {}, y[E] = {}, hi[E], lo[E];
       if (g < g1) {
-        load_group(p, g, V, aligned, x);
-        if constexpr (kDraft) load_group(q, g, V, aligned, y);
+        load_group(p, g, V, off, vec, x);
+        if constexpr (kDraft) load_group(q, g, V, off, vec, y);
       }
       group(x, y, g, hi, lo);
-      double own = 0.0;
-      int32_t some = -1;
+      Sum own{0.f, 0.f};
+#pragma unroll
+      for (int e = 0; e < E; ++e) add(own, hi[e], lo[e]);
+      Sum rest = t;
+      const int l = holds(own, rest);
+      if (l < 0) continue;
+      const Sum all = warp_sum(own);
+      const bool here = minus(all, t).positive();  // t lies in these groups, not behind them
+      // the first of lane l's entries that goes over the rest, its last with r > 0 if rounding leaves none
+      int32_t mine = -1;
+      bool over = false;
+      Sum upto{0.f, 0.f};
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        own += (double)hi[e] + (double)lo[e];
-        if (hi[e] + lo[e] > 0.f) some = g * E + e;
-      }
-      double upto = own;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const double v = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += v;
-      }
-      const unsigned over = __ballot_sync(0xffffffffu, before + upto > t && some >= 0);
-      if (over) {
-        const int l = __ffs(over) - 1;
-        int32_t word = some;  // of lane l, if its own words do not reach t by rounding
-        double cum = before + (upto - own);
-#pragma unroll
-        for (int e = E - 1; e >= 0; --e) {
-          double c = cum;
-#pragma unroll
-          for (int k = 0; k <= e; ++k) c += (double)hi[k] + (double)lo[k];
-          if (c > t && hi[e] + lo[e] > 0.f) word = g * E + e;
+        add(upto, hi[e], lo[e]);
+        if (hi[e] + lo[e] > 0.f && !over) {
+          mine = g * E - off + e;
+          over = minus(upto, rest).positive();
         }
-        return __shfl_sync(0xffffffffu, word, l);
       }
-      const unsigned any = __ballot_sync(0xffffffffu, some >= 0);
-      if (any) last = __shfl_sync(0xffffffffu, some, 31 - __clz(any));
-      before += __shfl_sync(0xffffffffu, upto, 31);
+      word = __shfl_sync(0xffffffffu, mine, l);
+      if (here) return word;
+      t = minus(t, all);
     }
-    return last;
+    return word;
   }
 };
 
-// The part of `parts` that holds t when their sums lie end to end; the last with a sum if rounding leaves none.  t
-// becomes the rest within the part.
-__device__ __forceinline__ int32_t part_of(const double* parts, int32_t count, double& t) {
-  double before = 0.0, rest = 0.0;
-  int32_t last = -1;
-  for (int32_t i = 0; i < count; ++i) {
-    if (parts[i] > 0.0) {
-      last = i;
-      rest = t - before;
-      if (before + parts[i] > t) break;
-    }
-    before += parts[i];
-  }
-  t = rest;
-  return last;
-}
+// What the warp that walks tells the others.
+struct Order {
+  int32_t node;       // sum what is left at this token; -1: the walk has ended
+  float c_hi, c_lo;
+  int32_t n_refused;  // of the refused words of this CTA's part
+  int32_t part;       // the warp whose groups hold the next token, or -1
+};
 
 template <class T, bool kDraft>
-__global__ void __launch_bounds__(kThreads, 2) fd_verify_kernel(const VerifyParams v) {
+__global__ void __launch_bounds__(kThreads, kCtas) fd_verify_kernel(const VerifyParams v) {
   __shared__ int32_t s_parent[kMaxDrafts], s_token[kMaxDrafts], s_refused[kMaxDrafts];
   __shared__ float s_p[kMaxDrafts], s_q[kMaxDrafts], s_u[kMaxDrafts];
-  __shared__ double s_warp[kWarps], s_cta[2][kMaxCluster];
+  __shared__ Sum s_warp[kWarps], s_cta[2][kMaxCluster];
+  __shared__ Order s_order;
+  __shared__ Sum s_rest;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint32_t C;
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(C));
@@ -235,23 +269,26 @@ __global__ void __launch_bounds__(kThreads, 2) fd_verify_kernel(const VerifyPara
   const int32_t n = v.tree.n, m = tree_tokens(v.tree, b), pad = n - m;
   const T* target = static_cast<const T*>(v.target) + b * v.ts[0] + pad * v.ts[1];
   const T* draft = kDraft ? static_cast<const T*>(v.draft) + b * v.ds[0] + pad * v.ds[1] : nullptr;
-  if (tid < m) {
-    int32_t up = __ldg(v.tree.parents + b * v.tree.parents_stride + pad + tid);
-    const int32_t x = __ldg(v.tokens + (int64_t)b * n + pad + tid);
-    s_u[tid] = __ldg(v.uniforms + (int64_t)b * n + pad + tid);
-    const bool wrong = up < -1 || up >= tid;
-    const bool child = tid > 0 && !wrong && up >= 0 && x >= 0 && x < v.V;
-    if (wrong || (tid > 0 && up >= 0 && !child)) atomicOr(v.err, kErrBadIndex);
-    if (!child) up = -1;
-    s_parent[tid] = up;
+  if (tid < kMaxDrafts) {
+    int32_t up = -1, x = 0;
+    bool child = false;
+    if (tid < m) {
+      up = __ldg(v.tree.parents + b * v.tree.parents_stride + pad + tid);
+      x = __ldg(v.tokens + (int64_t)b * n + pad + tid);
+      s_u[tid] = __ldg(v.uniforms + (int64_t)b * n + pad + tid);
+      const bool wrong = up < -1 || up >= tid;
+      child = tid > 0 && !wrong && up >= 0 && x >= 0 && x < v.V;
+      if (wrong || (tid > 0 && up >= 0 && !child)) atomicOr(v.err, kErrBadIndex);
+    }
+    s_parent[tid] = child ? up : -1;
     s_token[tid] = x;
     s_p[tid] = child ? fmaxf(at(target + up * v.ts[1], x), 0.f) : 0.f;
-    if constexpr (kDraft) s_q[tid] = child ? at(draft + up * v.ds[1], x) : 0.f;
+    s_q[tid] = kDraft && child ? at(draft + up * v.ds[1], x) : 0.f;
   }
   int32_t* path = v.path + (int64_t)b * n;
   if (rank == 0 && tid < n) path[tid] = tid == 0 && m > 0 ? 0 : -1;
   cluster_sync();  // the tables are written, and every CTA of the cluster runs
-  if (m == 0) {  // the same in every CTA of the cluster
+  if (m == 0) {    // the same in every CTA of the cluster
     if (rank == 0 && tid == 0) {
       v.count[b] = 0;
       v.next_token[b] = -1;
@@ -259,140 +296,182 @@ __global__ void __launch_bounds__(kThreads, 2) fd_verify_kernel(const VerifyPara
     return;
   }
 
-  // groups of this CTA and of this warp
-  constexpr int E = kGroup<T>;
-  const int32_t groups = (v.V + E - 1) / E;
-  const int32_t per_cta = ceil_div(groups, (int32_t)C), per_warp = ceil_div(per_cta, kWarps);
-  const int32_t cta0 = min(groups, (int32_t)rank * per_cta), cta1 = min(groups, cta0 + per_cta);
-  const int32_t g0 = min(cta1, cta0 + warp * per_warp), g1 = min(cta1, g0 + per_warp);
-
   Left<T, kDraft> left;
   left.V = v.V;
   left.refused = s_refused;
-  left.n_refused = 0;
   int buf = 0;
-  // The mass of what is left, the parts of the warps and CTAs on the way
-  auto mass_of = [&](int32_t node, double c) -> double {
-    left.p = target + node * v.ts[1];
-    left.q = kDraft ? draft + node * v.ds[1] : nullptr;
-    left.aligned = ((reinterpret_cast<uintptr_t>(left.p) | (kDraft ? reinterpret_cast<uintptr_t>(left.q) : 0)) & 15) == 0;
-    left.c_hi = (float)c;
-    left.c_lo = (float)(c - (double)left.c_hi);
-    const double s = left.sum(g0, g1);
-    if (lane == 0) s_warp[warp] = s;
-    __syncthreads();
-    buf ^= 1;
-    if (tid < (int)C) {
-      double all = 0.0;
-      for (int i = 0; i < kWarps; ++i) all += s_warp[i];
-      store_remote(&s_cta[buf][rank], (uint32_t)tid, all);
-    }
-    cluster_sync();
-    double all = 0.0;
-    for (uint32_t i = 0; i < C; ++i) all += s_cta[buf][i];
-    return all;
-  };
+  int32_t g0 = 0, g1 = 0, cta0 = 0, cta1 = 0, per_warp = 0;  // groups of this warp and of this CTA
 
+  // The walk, by warp 0 of every CTA alike
   int32_t node = 0, count = 1;
   double c = 0.0, Z = 1.0;
-  bool summed = false;
-  for (bool on = true; on;) {
-    on = false;
-    c = 0.0;
-    Z = 1.0;
-    summed = false;
-    uint64_t children = __ballot_sync(0xffffffffu, lane < m && s_parent[lane] == node);
-    children |= (uint64_t)__ballot_sync(0xffffffffu, lane + 32 < m && s_parent[(lane + 32) & 63] == node) << 32;
-    uint64_t refused = 0;
-    while (children) {
-      const int32_t k = __ffsll((long long)children) - 1;
-      children &= children - 1;
-      bool stays;
-      if constexpr (kDraft) {
-        const double q = s_q[k];
-        const double r = fmax((double)s_p[k] - c * q, 0.0);
-        stays = (double)s_u[k] * Z * q < r;
-        if (!stays) {
-          c += Z;
-          Z = mass_of(node, c);
-          summed = true;
+  uint64_t children = 0, refused = 0;
+  bool fresh = true;      // at a token whose children have not been looked for
+  bool pending = false;   // a sum has been asked for, for the next child or for the end
+  bool last = false;      // ... for the end: no child is left
+  for (;;) {
+    if (warp == 0) {
+      if (pending) {
+        Sum s{0.f, 0.f};
+        if (lane < (int)C) s = s_cta[buf][lane];
+        Z = warp_sum(s).value();
+      }
+      bool sums = pending;  // Z and the sums are those of this token and c
+      pending = false;
+      Order o{-1, 0.f, 0.f, 0, -1};
+      for (;;) {
+        if (last) {
+          if (!(Z > 0.0) && (c != 0.0 || refused != 0)) {  // nothing left: the target itself
+            c = 0.0;
+            refused = 0;
+            o.node = node;
+          }
+          break;
         }
-      } else {
-        // a word that was refused before has nothing left
-        const bool again = __any_sync(0xffffffffu, (refused >> lane & 1 && s_token[lane] == s_token[k]) ||
-                                                       (refused >> (lane + 32) & 1 && s_token[lane + 32] == s_token[k]));
-        const double r = again ? 0.0 : (double)s_p[k];
-        stays = (double)s_u[k] * Z < r;
-        if (!stays) {
-          Z -= r;
-          refused |= 1ull << k;
+        if (fresh) {
+          children = __ballot_sync(0xffffffffu, s_parent[lane] == node);
+          children |= (uint64_t)__ballot_sync(0xffffffffu, s_parent[lane + 32] == node) << 32;
+          c = 0.0;
+          Z = 1.0;
+          refused = 0;
+          fresh = false;
+          sums = false;
+        }
+        if (children == 0) {
+          last = true;
+          if (sums) continue;
+          o.node = node;
+          break;
+        }
+        const int32_t k = __ffsll((long long)children) - 1;
+        children &= children - 1;
+        bool stays;
+        if constexpr (kDraft) {
+          const double q = s_q[k];
+          stays = (double)s_u[k] * Z * q < fmax((double)s_p[k] - c * q, 0.0);
+          if (!stays) {
+            c += Z;
+            o.node = node;
+            break;
+          }
+        } else {
+          // a word that was refused before has nothing left
+          const bool again = __any_sync(0xffffffffu, (refused >> lane & 1 && s_token[lane] == s_token[k]) ||
+                                                         (refused >> (lane + 32) & 1 && s_token[lane + 32] == s_token[k]));
+          const double r = again ? 0.0 : (double)s_p[k];
+          stays = (double)s_u[k] * Z < r;
+          if (!stays) {
+            Z -= r;
+            refused |= 1ull << k;
+          }
+        }
+        if (stays) {
+          if (rank == 0 && lane == 0) path[count] = k;
+          ++count;
+          node = k;
+          fresh = true;
         }
       }
-      if (stays) {
-        if (rank == 0 && tid == 0) path[count] = k;
-        ++count;
-        node = k;
-        on = true;
-        break;
-      }
-    }
-    if (!on && !kDraft) {
-      // the refused words of this CTA's part, for the sum
-      if (warp == 0) {
+      pending = o.node >= 0;
+      o.c_hi = (float)c;
+      o.c_lo = (float)(c - (double)o.c_hi);
+      if (!kDraft && pending) {
+        // the refused words, for those that have them in their part
         int32_t kept = 0;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int32_t x = s_token[lane + 32 * i];
-          const bool mine = (refused >> (lane + 32 * i) & 1) && x >= cta0 * E && x < cta1 * E;
-          const unsigned who = __ballot_sync(0xffffffffu, mine);
-          if (mine) s_refused[kept + __popc(who & ((1u << lane) - 1u))] = x;
+          const bool out = refused >> (lane + 32 * i) & 1;
+          const unsigned who = __ballot_sync(0xffffffffu, out);
+          if (out) s_refused[kept + __popc(who & ((1u << lane) - 1u))] = s_token[lane + 32 * i];
           kept += __popc(who);
         }
-        if (lane == 0) s_warp[0] = (double)kept;
+        o.n_refused = kept;
       }
-      __syncthreads();
-      left.n_refused = (int32_t)s_warp[0];
-      __syncthreads();
+      if (lane == 0) s_order = o;
+    }
+    __syncthreads();
+    const Order o = s_order;
+    if (o.node < 0) break;
+    left.p = target + o.node * v.ts[1];
+    left.q = kDraft ? draft + o.node * v.ds[1] : nullptr;
+    left.c_hi = o.c_hi;
+    left.c_lo = o.c_lo;
+    left.n_refused = o.n_refused;
+    constexpr int E = kGroup<T>;
+    const uint32_t byte = (uint32_t)(reinterpret_cast<uintptr_t>(left.p) & 15u);
+    left.vec = !kDraft || byte == (uint32_t)(reinterpret_cast<uintptr_t>(left.q) & 15u);
+    left.off = (int32_t)(byte / sizeof(T));
+    const int32_t groups = (v.V + left.off + E - 1) / E, per_cta = ceil_div(groups, (int32_t)C);
+    per_warp = ceil_div(per_cta, kWarps);
+    cta0 = min(groups, (int32_t)rank * per_cta);
+    cta1 = min(groups, cta0 + per_cta);
+    g0 = min(cta1, cta0 + warp * per_warp);
+    g1 = min(cta1, g0 + per_warp);
+    const Sum mine = left.sum(g0, g1);
+    if (lane == 0) s_warp[warp] = mine;
+    __syncthreads();
+    buf ^= 1;
+    if (warp == 0) {
+      Sum s{0.f, 0.f};
+      if (lane < kWarps) s = s_warp[lane];
+      s = warp_sum(s);
+      if (lane < (int)C) store_remote(&s_cta[buf][rank], (uint32_t)lane, s);
+    }
+    cluster_sync();
+  }
+
+  // The word at u_0 of what is left, by the CTA and the warp that have it
+  if (warp == 0) {
+    const double target_sum = (double)s_u[0] * Z;
+    Sum t{(float)target_sum, 0.f};
+    t.lo = (float)(target_sum - (double)t.hi);
+    const int owner = holds(lane < (int)C ? s_cta[buf][lane] : Sum{0.f, 0.f}, t);
+    const int w = holds(lane < kWarps ? s_warp[lane] : Sum{0.f, 0.f}, t);
+    if (lane == 0) {
+      s_order.part = owner == (int)rank ? w : -1;
+      s_rest = t;
+      if (rank == 0) v.count[b] = count;
+      if (owner < 0 ? rank == 0 : owner == (int)rank && w < 0) v.next_token[b] = -1;
     }
   }
-  if (!summed) Z = mass_of(node, c);
-  if (!(Z > 0.0)) {  // nothing left: the target itself
-    left.n_refused = 0;
-    Z = mass_of(node, 0.0);
-  }
-  int32_t word = -1;
-  double t = (double)s_u[0] * Z;
-  const int32_t owner = part_of(s_cta[buf], (int32_t)C, t);
-  if (owner == (int32_t)rank) {
-    const int32_t w = part_of(s_warp, kWarps, t);
-    if (w >= 0) {
-      // that warp's groups once more, a part to each warp
-      const int32_t h0 = min(cta1, cta0 + w * per_warp), h1 = min(cta1, h0 + per_warp);
-      const int32_t per = ceil_div(h1 - h0, kWarps);
-      const int32_t i0 = min(h1, h0 + warp * per), i1 = min(h1, i0 + per);
-      const double s = left.sum(i0, i1);
-      __syncthreads();
-      if (lane == 0) s_warp[warp] = s;
-      __syncthreads();
-      const int32_t mine = part_of(s_warp, kWarps, t);
-      if (mine == warp) {
-        word = left.find(i0, i1, t);
-        if (lane == 0) v.next_token[b] = word;
-      } else if (mine < 0 && tid == 0) {
-        v.next_token[b] = -1;
+  __syncthreads();
+  const int32_t w = s_order.part;
+  if (w >= 0) {
+    // that warp's groups once more, a part to each warp
+    const int32_t h0 = min(cta1, cta0 + w * per_warp), h1 = min(cta1, h0 + per_warp);
+    const int32_t per = ceil_div(h1 - h0, kWarps);
+    const int32_t i0 = min(h1, h0 + warp * per), i1 = min(h1, i0 + per);
+    const Sum mine = left.sum(i0, i1);
+    if (lane == 0) s_warp[warp] = mine;
+    __syncthreads();
+    if (warp == 0) {
+      Sum t = s_rest;
+      const int x = holds(lane < kWarps ? s_warp[lane] : Sum{0.f, 0.f}, t);
+      if (lane == 0) {
+        s_order.part = x;
+        s_rest = t;
+        if (x < 0) v.next_token[b] = -1;
       }
     }
-  } else if (owner < 0 && rank == 0 && tid == 0) {
-    v.next_token[b] = -1;
+    __syncthreads();
+    if (s_order.part == warp) {
+      const int32_t word = left.find(i0, i1, s_rest);
+      if (lane == 0) v.next_token[b] = word;
+    }
   }
-  if (rank == 0 && tid == 0) v.count[b] = count;
   if (C > 1) cluster_sync();  // no CTA leaves while another may write its shared memory
 }
 
 template <class T, bool kDraft>
 cudaError_t launch(const VerifyParams& v, cudaStream_t stream) {
+  // Parts of 1024 words at least, and no more CTAs than run at once.
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
   int cluster = 1;
-  while (cluster < kMaxCluster && (int64_t)cluster * 4096 < v.V) cluster *= 2;
+  while (cluster < kMaxCluster && (int64_t)cluster * 1024 < v.V && 2 * (int64_t)v.B * cluster <= kCtas * (int64_t)sms)
+    cluster *= 2;
   if ((int64_t)v.B * cluster > INT32_MAX) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(v.B * cluster));
