@@ -95,6 +95,21 @@ def test_a_list_that_does_not_rise_ends_there(n):
         c.check(index, want_counts=[stop, n], status=fd.fdecode.FD_ERR_BAD_INDEX)
 
 
+@pytest.mark.parametrize("cache,D", [("bf16", 128), ("bf16", 64), ("f32", 128)])
+@pytest.mark.parametrize("page", [0, 16])
+@pytest.mark.parametrize("n", [65, 700, 5000])
+def test_rows_from_behind_all_that_is_written(cache, D, page, n):
+    """The first rows stay where they are, the others come from behind: the list is shared."""
+    r = np.random.default_rng(n)
+    c = Case(3, 2, D, 3 * n + 90, cache=cache, page=page, seed=n)
+    index = np.stack([np.r_[np.arange(s), n + np.sort(r.permutation(2 * n)[:n - s])] for s in (0, 4, n)]).astype(np.int32)
+    c.check(index, starts=[5, 0, 80])
+    c.check(index, counts=[n, n - 1, n // 2], starts=[5, 0, 80])
+    index[0, n // 3] = 0  # the list ends there
+    index[1, n - 1] = 1 << 30
+    c.check(index, want_counts=[n // 3, n - 1, n], status=fd.fdecode.FD_ERR_BAD_INDEX)
+
+
 def test_places_past_the_end_and_before_the_start():
     bad = fd.fdecode.FD_ERR_BAD_INDEX
     c = Case(3, 2, 128, 64, seed=2)
