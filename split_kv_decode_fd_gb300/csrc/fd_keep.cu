@@ -8,7 +8,7 @@
 // of an earlier chunk has reached them.  Slices of different channels share nothing.
 //
 // The drafts of a step (up to 64 entries) are one chunk of whole rows in registers: bound by a chain
-// of loads (count, index, page, row).  Long lists go through shared memory, five chunks of 32 KB on their way
+// of loads (count, index, page, row).  Long lists go through shared memory, five chunks of 16 KB on their way
 // (loads may run ahead of the stores of earlier chunks).  Where the first row that moves comes from behind
 // the last place that is written, as when the latest part of a sequence stays, no row is both read and written: the CTAs
 // of a (sequence, KV head) share the list and take whole rows.  Otherwise each takes the whole list
@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kThreads) fd_keep_kernel(const KeepParams p) {
 }
 
 // ------------------------------------------------------------------ long lists
-constexpr int kLongLoads = 8, kStages = 6;
+constexpr int kLongLoads = 4, kStages = 6, kScan = 8;
 constexpr int kStageBytes = kThreads * kLongLoads * 16;
 
 // The cache rows of one (sequence, KV head) of K or V, in 16-byte pieces.
@@ -166,17 +166,16 @@ __device__ __forceinline__ void move_rows(const Rows& r, const int32_t* index, i
   }
 }
 
-// Wide: 16-byte pieces of a row; Narrow: of a slice.  CTAs of a (sequence, KV head): Wide / Narrow.
+// Wide: 16-byte pieces of a row; Narrow: of a slice.  parts: CTAs of a (sequence, KV head), Wide / Narrow at least.
 template <int Wide, int Narrow>
-__global__ void __launch_bounds__(kThreads) fd_keep_long_kernel(const KeepParams p) {
-  constexpr int kParts = Wide / Narrow;
+__global__ void __launch_bounds__(kThreads) fd_keep_long_kernel(const KeepParams p, int32_t parts) {
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ int32_t s_stop, s_moves;
   pdl_launch_dependents();
   pdl_wait();
   int64_t c = blockIdx.x;
-  const int32_t part = (int32_t)(c % kParts);
-  c /= kParts;
+  const int32_t part = (int32_t)(c % parts);
+  c /= parts;
   Rows r;
   r.base = static_cast<uint4*>(c % 2 ? p.kv.v : p.kv.k);
   c /= 2;
@@ -195,22 +194,31 @@ __global__ void __launch_bounds__(kThreads) fd_keep_long_kernel(const KeepParams
   if (threadIdx.x == 0) s_stop = s_moves = count;
   __syncthreads();
   int32_t bad = count, moves = count;
-  for (int32_t j0 = 0; j0 < count; j0 += 8 * kThreads) {
-    int32_t at[8], before[8];
+  const int32_t lead = (int32_t)((reinterpret_cast<uintptr_t>(index) / 4) & 3);  // index - lead is at a 16-byte boundary
+  for (int64_t j0 = -lead; j0 < count; j0 += 4 * kScan * kThreads) {
+    int32_t at[kScan][4], before[kScan];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int32_t j = j0 + i * kThreads + threadIdx.x;
-      at[i] = before[i] = -1;
-      if (j >= count) continue;
-      at[i] = __ldg(index + j);
-      if (j > 0) before[i] = __ldg(index + j - 1);
+    for (int i = 0; i < kScan; ++i) {
+      const int64_t j = j0 + 4 * (i * kThreads + (int32_t)threadIdx.x);
+      before[i] = j > 0 && j < count ? __ldg(index + j - 1) : -1;
+      if (j >= 0 && j + 4 <= count) {
+        const int4 w = __ldg(reinterpret_cast<const int4*>(index + j));
+        at[i][0] = w.x, at[i][1] = w.y, at[i][2] = w.z, at[i][3] = w.w;
+      } else {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) at[i][x] = j + x >= 0 && j + x < count ? __ldg(index + j + x) : -1;
+      }
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int32_t j = j0 + i * kThreads + threadIdx.x;
-      if (j >= count) continue;
-      if (at[i] <= before[i] || before[i] < -1 || start < 0 || (int64_t)start + at[i] >= p.max_len) bad = min(bad, j);
-      if (at[i] != j) moves = min(moves, j);
+    for (int i = 0; i < kScan; ++i) {
+      const int64_t j = j0 + 4 * (i * kThreads + (int32_t)threadIdx.x);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        if (j + x < 0 || j + x >= count) continue;
+        const int32_t prev = x > 0 ? at[i][x > 0 ? x - 1 : 0] : before[i];
+        if (at[i][x] <= prev || prev < -1 || start < 0 || (int64_t)start + at[i][x] >= p.max_len) bad = min(bad, (int32_t)j + x);
+        if (at[i][x] != j + x) moves = min(moves, (int32_t)j + x);
+      }
     }
   }
   if (bad < count) atomicMin(&s_stop, bad);
@@ -219,23 +227,24 @@ __global__ void __launch_bounds__(kThreads) fd_keep_long_kernel(const KeepParams
   const int32_t stop = s_stop, first = s_moves;
   if (stop < count && threadIdx.x == 0) atomicOr(p.err, kErrBadIndex);
   if (first >= stop) return;
-  if (kParts > 1 && __ldg(index + first) >= stop) {
+  if (parts > 1 && __ldg(index + first) >= stop) {
     // no row is both read and written
-    const int32_t per = (stop - first + kParts - 1) / kParts;
-    const int32_t j0 = first + part * per, j1 = stop - j0 < per ? stop : j0 + per;
-    if (j0 < j1) move_rows<Wide>(r, index, start, j0, j1, 0, smem_addr(ring), p.err);
-  } else {
+    const int32_t per = (stop - first + parts - 1) / parts;
+    const int64_t j0 = first + (int64_t)part * per, j1 = stop - j0 < per ? stop : j0 + per;
+    if (j0 < j1) move_rows<Wide>(r, index, start, (int32_t)j0, (int32_t)j1, 0, smem_addr(ring), p.err);
+  } else if (part < Wide / Narrow) {
     move_rows<Narrow>(r, index, start, first, stop, part * Narrow, smem_addr(ring), p.err);
   }
 }
 
 template <int Wide, int Narrow>
-cudaError_t launch_long(const KeepParams& p, cudaStream_t stream) {
-  const int64_t grid = (int64_t)p.B * p.kv.Hkv * 2 * (Wide / Narrow);
+cudaError_t launch_long(const KeepParams& p, int64_t parts, cudaStream_t stream) {
+  const int64_t grid = (int64_t)p.B * p.kv.Hkv * 2 * parts;
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
   const cudaError_t e = allow_smem<fd_keep_long_kernel<Wide, Narrow>>(kStages * kStageBytes);
   if (e != cudaSuccess) return e;
-  return launch_early(fd_keep_long_kernel<Wide, Narrow>, (unsigned)grid, kThreads, (size_t)kStages * kStageBytes, stream, p);
+  return launch_early(fd_keep_long_kernel<Wide, Narrow>, (unsigned)grid, kThreads, (size_t)kStages * kStageBytes, stream, p,
+                      (int32_t)parts);
 }
 
 template <int Wide>
@@ -244,7 +253,10 @@ cudaError_t launch_long(const KeepParams& p, cudaStream_t stream) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  return (int64_t)p.B * p.kv.Hkv * 2 < sms ? launch_long<Wide, 2>(p, stream) : launch_long<Wide, Wide>(p, stream);
+  const int64_t pairs = (int64_t)p.B * p.kv.Hkv * 2;
+  if (pairs >= sms) return launch_long<Wide, Wide>(p, 1, stream);
+  const int64_t parts = 2 * (int64_t)sms / pairs;  // two CTAs an SM
+  return launch_long<Wide, 2>(p, parts > Wide / 2 ? parts : Wide / 2, stream);
 }
 
 template <int Lanes, int Loads>
