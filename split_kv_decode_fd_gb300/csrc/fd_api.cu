@@ -1016,15 +1016,16 @@ namespace {
 // Blocks of rows and shares of keys of fd_decode_tree on `sms` SMs (fd_tree.h); tiles: 128-key tiles of all (b, KV
 // head) pairs, or an upper bound.
 struct TreeSplit {
-  int32_t rows, block, nsub, ranges;
+  int32_t rows, block, blocks, nsub, ranges;
 };
-TreeSplit tree_split(int Hq, int Hkv, int n, bool f32, int sms, int64_t tiles) {
+TreeSplit tree_split(int Hq, int Hkv, int n, int D, bool f32, int sms, int64_t tiles) {
   TreeSplit t;
   t.rows = Hq / Hkv * n;
   t.block = tree_rows(f32, t.rows);
-  t.nsub = ceil_div(t.rows, t.block);
-  int64_t r = (int64_t)tree_ctas(f32) * sms / t.nsub;  // CTAs that run at once
-  if (r > tiles) r = tiles;
+  t.blocks = f32 ? ceil_div(t.rows, t.block) : 1;  // (its own pairs)
+  t.nsub = f32 ? 1 : ceil_div(t.rows, t.block);
+  int64_t r = (int64_t)tree_ctas(f32, D) * sms / t.nsub;  // CTAs that run at once
+  if (r > tiles * t.blocks) r = tiles * t.blocks;
   t.ranges = (int32_t)(r < 1 ? 1 : r);
   return t;
 }
@@ -1066,7 +1067,7 @@ size_t fd_tree_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t D, in
   if (sms <= 0 && !sm_count(&sms)) return 0;
   size_t most = 0;  // the size must hold for either cache type
   for (const bool f32 : {false, true}) {
-    const size_t a = tree_layout(tree_split(Hq, Hkv, n, f32, sms, INT64_MAX), D).total;
+    const size_t a = tree_layout(tree_split(Hq, Hkv, n, D, f32, sms, (int64_t)1 << 40), D).total;
     most = a > most ? a : most;
   }
   return most;
@@ -1087,7 +1088,7 @@ fd_status fd_decode_tree(const float* q, const fd_tree_desc* tree, const fd_kv_d
   int sms = 0;
   if (!sm_count(&sms)) return FD_ERR_CUDA;
   const bool f32 = kv->dtype == FD_F32;
-  const TreeSplit t = tree_split(Hq, Hkv, tree->n, f32, sms, (int64_t)B * Hkv * ceil_div(max_seq_len, kPlanTile));
+  const TreeSplit t = tree_split(Hq, Hkv, tree->n, D, f32, sms, (int64_t)B * Hkv * ceil_div(max_seq_len, kPlanTile));
   const TreeLayout w = tree_layout(t, D);
   if (workspace_bytes < w.total) return FD_ERR_WORKSPACE_TOO_SMALL;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -1108,8 +1109,10 @@ fd_status fd_decode_tree(const float* q, const fd_tree_desc* tree, const fd_kv_d
   p.rows = t.rows;
   p.nsub = t.nsub;
   p.ranges = t.ranges;
-  p.join_pairs = (int64_t)B * Hkv <= t.ranges;
-  p.n_joins = p.join_pairs ? B * Hkv : t.ranges;
+  p.blocks = t.blocks;
+  p.join_pairs = (int64_t)B * Hkv * t.blocks <= t.ranges;
+  p.n_joins = p.join_pairs ? B * Hkv * t.blocks : t.ranges;
+  p.packed = f32;
   p.max_len = max_seq_len;
   p.qk_scale = (float)((double)scale * 1.4426950408889634);
   p.wait_ns = (uint64_t)g_wait_ns.load(std::memory_order_relaxed);

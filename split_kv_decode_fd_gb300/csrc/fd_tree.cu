@@ -5,8 +5,11 @@
 //     out = sum_t exp(x_t - m) v_t / sum_t exp(x_t - m),   x_t = scale q . k_t,
 // over what it sees, with the running m and sum of an online softmax.
 //
-// A CTA serves 32 rows of a KV head from tiles of 64 keys in shared memory, and
-// each thread two rows: four keys a row for q . k, D / 16 channels a row for p . V.
+// A CTA of four warps serves 32 rows of a KV head from tiles of 64 keys in shared
+// memory; a thread has four rows, of which it takes four keys for q . k and D / 16
+// channels for p . V: sixteen products for eight values read, so that both keep the
+// arithmetic busy rather than shared memory.  K and V have one buffer each: V's next tile
+// comes in under q . k, K's under p . V, and the other CTAs of the SM fill what is left.
 #include "fd_tree.cuh"
 
 namespace fdk {
@@ -14,34 +17,81 @@ namespace {
 
 constexpr int kRows = kTreeRowsCore;
 constexpr int kKeys = 64;
-constexpr int kCoreThreads = 256;
+constexpr int kCoreThreads = 128;
 
 template <int D>
 struct CoreSmem {
-  static constexpr int kStride = D + 4;  // rows of q and k: sixteen rows apart by 16 bytes in the banks
+  static constexpr int kStride = D + 4;     // rows of q and k: eight rows in a row of banks
+  static constexpr int kPStride = kRows + 4;
   float q[kRows * kStride];
   float k[kKeys * kStride];
   float v[kKeys * D];
-  float p[kRows * (kKeys + 4)];
+  float p[kKeys * kPStride];                // weights, key by key
   TreePiece piece;
   int32_t more;
 };
 
-__device__ __forceinline__ float4 load4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
+__device__ __forceinline__ void cp_async16(uint32_t to, const float* from, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void cp_async_wait_older() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
+
+// Rows [t0, t0 + 64) of K or V to shared memory.  Rows past the piece's end and those of pages that are none hold nothing
+// that counts: they come in as zeros.
+template <int D, int Stride>
+__device__ __forceinline__ void copy_tile(const TreeParams& p, const TreePiece& pc, const void* cache, int32_t t0, uint32_t to) {
+  constexpr int kStep = kCoreThreads / (D / 4);  // rows side by side
+  const int c = threadIdx.x % (D / 4) * 4, r0 = threadIdx.x / (D / 4);
+  const float* base = static_cast<const float*>(cache);
+  to += (uint32_t)(r0 * Stride + c) * 4;
+  if (t0 >= pc.end) {
+    // nothing
+  } else if (!p.kv.paged) {
+    const float* from = base + (((int64_t)pc.b * p.Hkv + pc.h) * p.kv.capacity + t0 + r0) * D + c;
+#pragma unroll
+    for (int i = 0; i < kKeys / kStep; ++i) {
+      const bool there = t0 + r0 + i * kStep < pc.end;
+      cp_async16(to + (uint32_t)(i * kStep * Stride) * 4, there ? from + i * kStep * D : base, there);
+    }
+  } else {
+#pragma unroll 4
+    for (int i = 0; i < kKeys / kStep; ++i) {
+      const int32_t t = t0 + r0 + i * kStep;
+      int64_t at = -1;
+      if (t < pc.end) {
+        const int32_t page = __ldg(p.kv.block_table + (int64_t)pc.b * p.kv.max_pages + t / p.kv.page_size);
+        if (page >= 0 && page < p.kv.num_pages)
+          at = ((int64_t)page * p.Hkv + pc.h) * p.kv.page_size + t % p.kv.page_size;
+        else
+          atomicOr(p.err, kErrBadIndex);
+      }
+      cp_async16(to + (uint32_t)(i * kStep * Stride) * 4, at < 0 ? base : base + at * D + c, at >= 0);
+    }
+  }
+  cp_async_commit();
+}
+
+// Row i of the tokens of a KV head, head by head, as a row of q and out: m of every n rows are tokens, the last.
+__device__ __forceinline__ int32_t tree_row(const TreeParams& p, int32_t m, int32_t i) {
+  return i / m * p.tree.n + (p.tree.n - m) + i % m;
+}
 
 template <int D>
-__global__ void __launch_bounds__(kCoreThreads, kTreeCtasCore) fd_tree_core_kernel(const TreeParams p) {
+__global__ void __launch_bounds__(kCoreThreads, tree_ctas(true, D)) fd_tree_core_kernel(const TreeParams p) {
   using S = CoreSmem<D>;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   S& s = *reinterpret_cast<S*>(smem_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int ty = tid / 16, tx = tid % 16;
-  const int32_t range = blockIdx.x / p.nsub, sub = blockIdx.x % p.nsub;
+  const int32_t range = blockIdx.x;
   constexpr int kCols = D / 64;  // float4 of output a row and thread
+  constexpr int kStep = kCoreThreads / (D / 4);  // rows side by side in a copy
+  const uint32_t to_q = smem_addr(s.q), to_k = smem_addr(s.k), to_v = smem_addr(s.v);
   pdl_launch_dependents();
   pdl_wait();
-  tree_no_rows<D, kRows>(p, range, sub, tid, kCoreThreads);  // thread 0 also says what its pieces leave to join
-  TreeWalk walk(p, range);  // every warp walks; the pieces that count are those of warp 0
+  tree_no_rows<D, kRows, kRows>(p, range, 0, tid, kCoreThreads);  // thread 0 also says what its pieces leave to join
+  TreeWalk<kRows> walk(p, range, warp == 0);
   for (;;) {
     if (warp == 0) {
       TreePiece pc;
@@ -49,169 +99,160 @@ __global__ void __launch_bounds__(kCoreThreads, kTreeCtasCore) fd_tree_core_kern
       if (lane == 0) {
         s.piece = pc;
         s.more = found;
-        if (found && sub == 0) walk.say(pc);
+        if (found) walk.say(pc);
       }
     }
     __syncthreads();
     if (!s.more) return;
     const TreePiece pc = s.piece;
-    const int64_t row0 = ((int64_t)pc.b * p.Hkv + pc.h) * p.rows + sub * kRows;  // of q and out
-    const int32_t live = p.rows - sub * kRows < kRows ? p.rows - sub * kRows : kRows;
-    for (int i = tid; i < kRows * (D / 4); i += kCoreThreads) {
-      const int r = i / (D / 4), c = i % (D / 4) * 4;
-      const float4 x = r < live ? load4(p.q + (row0 + r) * D + c) : make_float4(0.f, 0.f, 0.f, 0.f);
-      *reinterpret_cast<float4*>(s.q + r * S::kStride + c) = x;
+    const int64_t row0 = ((int64_t)pc.b * p.Hkv + pc.h) * p.rows;  // of q and out
+    const int32_t first = pc.sub * kRows, rows = p.g * pc.m - first;  // of the tokens' rows; how many there are from there
+#pragma unroll
+    for (int i = 0; i < kRows / kStep; ++i) {
+      const int r = tid / (D / 4) + i * kStep, c = tid % (D / 4) * 4;
+      const bool there = r < rows;
+      cp_async16(to_q + (uint32_t)(r * S::kStride + c) * 4, p.q + (there ? (row0 + tree_row(p, pc.m, first + r)) * D + c : 0), there);
     }
+    copy_tile<D, S::kStride>(p, pc, p.kv.k, pc.begin, to_k);  // (and q, which comes with it)
+    copy_tile<D, D>(p, pc, p.kv.v, pc.begin, to_v);
     const int32_t P = pc.len - pc.m;
     const Ancestors all = tree_ancestors(p.tree, pc.b, pc.m, p.err);
-    uint64_t anc[2];
-    float mx[2], l[2];
-    float4 o[2][kCols];
+    uint64_t anc[4];
+    float mx[4], l[4];
+    uint64_t o[4][kCols][2];  // pairs of channels
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      anc[i] = all.of((sub * kRows + 2 * ty + i) % p.tree.n - (p.tree.n - pc.m));
+    for (int i = 0; i < 4; ++i) {
+      anc[i] = all.of((first + 4 * ty + i) % pc.m);
       mx[i] = -INFINITY;
       l[i] = 0.f;
 #pragma unroll
-      for (int c = 0; c < kCols; ++c) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int c = 0; c < kCols; ++c) o[i][c][0] = o[i][c][1] = 0;
     }
     for (int32_t t0 = pc.begin; t0 < pc.end; t0 += kKeys) {
-      // rows past the piece's end hold nothing that counts: they come in as zeros
-      for (int i = tid; i < kKeys * (D / 4); i += kCoreThreads) {
-        const int r = i / (D / 4), c = i % (D / 4) * 4;
-        const int32_t t = t0 + r;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-        if (t < pc.end) {
-          int64_t at = -1;
-          if (p.kv.paged) {
-            const int32_t page = __ldg(p.kv.block_table + (int64_t)pc.b * p.kv.max_pages + t / p.kv.page_size);
-            if (page >= 0 && page < p.kv.num_pages)
-              at = ((int64_t)page * p.Hkv + pc.h) * p.kv.page_size + t % p.kv.page_size;
-            else
-              atomicOr(p.err, kErrBadIndex);
-          } else {
-            at = ((int64_t)pc.b * p.Hkv + pc.h) * p.kv.capacity + t;
-          }
-          if (at >= 0) {
-            x = load4(static_cast<const float*>(p.kv.k) + at * D + c);
-            y = load4(static_cast<const float*>(p.kv.v) + at * D + c);
-          }
-        }
-        *reinterpret_cast<float4*>(s.k + r * S::kStride + c) = x;
-        *reinterpret_cast<float4*>(s.v + r * D + c) = y;
-      }
-      __syncthreads();
-      // q . k of rows 2 ty, 2 ty + 1 and keys tx, tx + 16, tx + 32, tx + 48
-      float x[2][4] = {};
+      cp_async_wait_older();
+      __syncthreads();  // K's tile is there
+      // q . k of rows 4 ty .. 4 ty + 3 and keys tx, tx + 16, tx + 32, tx + 48
+      uint64_t y[4][4] = {};  // sums of the even and of the odd channels
 #pragma unroll 4
       for (int c = 0; c < D; c += 4) {
-        float4 a[2], k[4];
+        ulonglong2 a[4], k[4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) a[i] = *reinterpret_cast<const float4*>(s.q + (2 * ty + i) * S::kStride + c);
+        for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const ulonglong2*>(s.q + (4 * ty + i) * S::kStride + c);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) k[j] = *reinterpret_cast<const float4*>(s.k + (tx + 16 * j) * S::kStride + c);
+        for (int j = 0; j < 4; ++j) k[j] = *reinterpret_cast<const ulonglong2*>(s.k + (tx + 16 * j) * S::kStride + c);
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            x[i][j] = fmaf(a[i].x, k[j].x, x[i][j]);
-            x[i][j] = fmaf(a[i].y, k[j].y, x[i][j]);
-            x[i][j] = fmaf(a[i].z, k[j].z, x[i][j]);
-            x[i][j] = fmaf(a[i].w, k[j].w, x[i][j]);
-          }
+          for (int j = 0; j < 4; ++j) y[i][j] = fma2(a[i].y, k[j].y, fma2(a[i].x, k[j].x, y[i][j]));
       }
-      uint32_t w[2][2];  // what the two rows see of the tile
+      __syncthreads();  // K's tile is read
+      copy_tile<D, S::kStride>(p, pc, p.kv.k, t0 + kKeys, to_k);
+      uint32_t w[4][2];  // what the rows see of the tile
       bool all_seen = true;
+      float x[4][4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const TileMask mask = tile_mask(P, anc[i], t0);
-        w[i][0] = mask.w[0];
-        w[i][1] = mask.w[1];
+      for (int i = 0; i < 4; ++i) {
+        w[i][0] = w[i][1] = 0xffffffffu;
+        if (t0 + kKeys > P) {
+          const TileMask mask = tile_mask(P, anc[i], t0);
+          w[i][0] = mask.w[0];
+          w[i][1] = mask.w[1];
+        }
         all_seen = all_seen && (w[i][0] & w[i][1]) == 0xffffffffu;
         float top = -INFINITY;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          x[i][j] = w[i][j >> 1] >> (tx + 16 * (j & 1)) & 1u ? x[i][j] * p.qk_scale : -INFINITY;
+          float even, odd;
+          unpack2(y[i][j], even, odd);
+          x[i][j] = w[i][j >> 1] >> (tx + 16 * (j & 1)) & 1u ? (even + odd) * p.qk_scale : -INFINITY;
           top = fmaxf(top, x[i][j]);
         }
 #pragma unroll
         for (int d = 8; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
         const float mn = fmaxf(mx[i], top);
         const float base = mn == -INFINITY ? 0.f : mn;
-        const float alpha = mx[i] == -INFINITY ? 0.f : exp2f(mx[i] - base);
+        const float alpha = mx[i] == -INFINITY ? 0.f : ex2(mx[i] - base);
         float sum = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float e = exp2f(x[i][j] - base);
-          s.p[(2 * ty + i) * (kKeys + 4) + tx + 16 * j] = e;
-          sum += e;
+          x[i][j] = ex2(x[i][j] - base);
+          sum += x[i][j];
         }
         l[i] = fmaf(l[i], alpha, sum);
         mx[i] = mn;
+        const uint64_t a2 = pack2(alpha, alpha);
 #pragma unroll
         for (int c = 0; c < kCols; ++c) {
-          o[i][c].x *= alpha;
-          o[i][c].y *= alpha;
-          o[i][c].z *= alpha;
-          o[i][c].w *= alpha;
+          o[i][c][0] = mul2(o[i][c][0], a2);
+          o[i][c][1] = mul2(o[i][c][1], a2);
         }
       }
-      __syncwarp();  // a row's weights are written and read by one half of a warp
-      auto add = [&](int i, float e, int c, const float4& v) {
-        o[i][c].x = fmaf(e, v.x, o[i][c].x);
-        o[i][c].y = fmaf(e, v.y, o[i][c].y);
-        o[i][c].z = fmaf(e, v.z, o[i][c].z);
-        o[i][c].w = fmaf(e, v.w, o[i][c].w);
-      };
-      if (all_seen) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<float4*>(s.p + (tx + 16 * j) * S::kPStride + 4 * ty) = make_float4(x[0][j], x[1][j], x[2][j], x[3][j]);
+      cp_async_wait_older();
+      __syncthreads();  // V's tile is there, and the weights
+      if (__all_sync(0xffffffffu, all_seen)) {
 #pragma unroll 4
         for (int t = 0; t < kKeys; ++t) {
-          const float e0 = s.p[2 * ty * (kKeys + 4) + t], e1 = s.p[(2 * ty + 1) * (kKeys + 4) + t];
+          const float4 e = *reinterpret_cast<const float4*>(s.p + t * S::kPStride + 4 * ty);
+          const uint64_t weight[4] = {pack2(e.x, e.x), pack2(e.y, e.y), pack2(e.z, e.z), pack2(e.w, e.w)};
 #pragma unroll
           for (int c = 0; c < kCols; ++c) {
-            const float4 v = *reinterpret_cast<const float4*>(s.v + t * D + 64 * c + 4 * tx);
-            add(0, e0, c, v);
-            add(1, e1, c, v);
+            const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(s.v + t * D + 64 * c + 4 * tx);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              o[i][c][0] = fma2(weight[i], v.x, o[i][c][0]);
+              o[i][c][1] = fma2(weight[i], v.y, o[i][c][1]);
+            }
           }
         }
       } else {
         // a value that a row does not see may be anything: 0 * NaN is not 0
-#pragma unroll 1
+#pragma unroll 2
         for (int t = 0; t < kKeys; ++t) {
+          const float4 e = *reinterpret_cast<const float4*>(s.p + t * S::kPStride + 4 * ty);
+          const uint64_t weight[4] = {pack2(e.x, e.x), pack2(e.y, e.y), pack2(e.z, e.z), pack2(e.w, e.w)};
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if (!(w[i][t >> 5] >> (t & 31) & 1u)) continue;
-            const float e = s.p[(2 * ty + i) * (kKeys + 4) + t];
+          for (int c = 0; c < kCols; ++c) {
+            const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(s.v + t * D + 64 * c + 4 * tx);
 #pragma unroll
-            for (int c = 0; c < kCols; ++c) add(i, e, c, *reinterpret_cast<const float4*>(s.v + t * D + 64 * c + 4 * tx));
+            for (int i = 0; i < 4; ++i) {
+              const bool seen = (t < 32 ? w[i][0] : w[i][1]) >> (t & 31) & 1u;
+              o[i][c][0] = fma2(weight[i], seen ? v.x : 0, o[i][c][0]);
+              o[i][c][1] = fma2(weight[i], seen ? v.y : 0, o[i][c][1]);
+            }
           }
         }
       }
-      __syncthreads();
+      __syncthreads();  // V's tile is read
+      copy_tile<D, D>(p, pc, p.kv.v, t0 + kKeys, to_v);
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
 #pragma unroll
       for (int d = 8; d > 0; d >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
-      const int r = 2 * ty + i;
-      if (r >= live || (sub * kRows + r) % p.tree.n < p.tree.n - pc.m) continue;
-      const int64_t state = ((int64_t)pc.slot * p.nsub + sub) * kRows + r;
-      float* to = pc.slot < 0 ? p.out + (row0 + r) * D : p.o_part + state * D;
+      const int r = 4 * ty + i;
+      if (r >= rows) continue;
+      const int64_t row = row0 + tree_row(p, pc.m, first + r);
+      const int64_t state = (int64_t)pc.slot * kRows + r;
+      float* to = pc.slot < 0 ? p.out + row * D : p.o_part + state * D;
       const float f = pc.slot >= 0 ? 1.f : (l[i] == 0.f ? 0.f : 1.f / l[i]);
 #pragma unroll
-      for (int c = 0; c < kCols; ++c)
-        *reinterpret_cast<float4*>(to + 64 * c + 4 * tx) =
-            make_float4(o[i][c].x * f, o[i][c].y * f, o[i][c].z * f, o[i][c].w * f);
+      for (int c = 0; c < kCols; ++c) {
+        const uint64_t f2 = pack2(f, f);
+        *reinterpret_cast<ulonglong2*>(to + 64 * c + 4 * tx) = make_ulonglong2(mul2(o[i][c][0], f2), mul2(o[i][c][1], f2));
+      }
       if (tx == 0) {
         if (pc.slot >= 0) {
           p.m_part[state] = mx[i];
           p.l_part[state] = l[i];
         } else if (p.lse) {
-          p.lse[row0 + r] = l[i] == 0.f ? -INFINITY : (mx[i] + log2f(l[i])) * kTreeLn2;
+          p.lse[row] = l[i] == 0.f ? -INFINITY : (mx[i] + log2f(l[i])) * kTreeLn2;
         }
       }
     }
-    __syncthreads();  // s.piece and s.q are read
+    // (the last tile's barriers part this piece's reads of s.piece and s.q from the next one's writes)
   }
 }
 
@@ -229,10 +270,16 @@ __global__ void __launch_bounds__(256, 4) fd_tree_join_kernel(const TreeParams p
   const int32_t r = w % Rows, sub = w / Rows % p.nsub, f = w / Rows / p.nsub;
   if (f >= p.n_joins) return;
   const TreeJoin j = p.joins[f];
-  const int32_t row = sub * Rows + r;
+  int32_t row = (j.sub + sub) * Rows + r;
   // (a call that gave up may have left an entry of an earlier one)
-  if (j.b < 0 || j.b >= p.B || j.h < 0 || j.h >= p.Hkv || j.first < 0 || j.last < j.first || j.last >= p.ranges) return;
-  if (row >= p.rows || row % p.tree.n < p.tree.n - tree_tokens(p.tree, j.b)) return;
+  if (j.b < 0 || j.b >= p.B || j.h < 0 || j.h >= p.Hkv || j.sub < 0 || j.sub >= p.blocks || j.first < 0 || j.last < j.first || j.last >= p.ranges) return;
+  const int32_t m = tree_tokens(p.tree, j.b);
+  if (p.packed) {
+    if (row >= p.g * m) return;
+    row = tree_row(p, m, row);
+  } else if (row >= p.rows || row % p.tree.n < p.tree.n - m) {
+    return;
+  }
   const int32_t count = j.last - j.first + 1;
   auto state = [&](int32_t k) {
     return ((int64_t)(2 * (j.first + k) + (k == 0 ? 1 : 0)) * p.nsub + sub) * Rows + r;

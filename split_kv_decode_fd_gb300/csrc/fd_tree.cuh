@@ -9,6 +9,40 @@
 
 namespace fdk {
 
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
+  return d;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 // Cost units (kTileUnits = 4 a tile of 128 keys) that a piece costs a CTA besides its tiles.
 constexpr int kTreePieceUnits = 6;
 
@@ -89,7 +123,7 @@ __device__ __forceinline__ TileMask tile_mask(int32_t P, uint64_t anc, int32_t t
 
 // A run of keys of one (sequence, KV head).
 struct TreePiece {
-  int32_t b, h;
+  int32_t b, h, sub;
   int32_t begin, end;  // places, `end` clipped to the length
   int32_t len, m;      // the sequence's length and its tokens
   int32_t slot;        // -1: the piece is the whole pair
@@ -97,15 +131,24 @@ struct TreePiece {
   int64_t v;           // the pair's first cost unit
 };
 
+// Blocks of `Packed` rows of a KV head of a sequence of m tokens, each a pair of its own; 0: not packed.
+template <int Packed>
+__device__ __forceinline__ int32_t tree_blocks(const TreeParams& p, int32_t m) {
+  if constexpr (Packed == 0) return 1;
+  else return ceil_div(p.g * m, Packed);
+}
+
 // The pieces of one share, walked by one warp (all lanes alike).  Sequences
 // without keys or without tokens cost nothing and have no piece.  Lane l holds length and
 // tokens of sequence base + l.
+template <int Packed>
 struct TreeWalk {
   const TreeParams& p;
   int64_t units;
   int32_t used, range;
   int64_t pos, end;
-  int32_t b, h, len, m, tiles;
+  int32_t b, len, m, tiles;
+  int32_t i, heads;      // number of the pair in its sequence, and of those
   int64_t v;             // first unit of the pair
   int32_t u;             // units of a pair of its sequence
   int32_t base, my_len, my_m;
@@ -128,21 +171,23 @@ struct TreeWalk {
     m = uniform() ? p.tree.n : __shfl_sync(0xffffffffu, my_m, bb & 31);
     tiles = m > 0 ? ceil_div(len, kPlanTile) : 0;
     u = units_of(len, m);
+    heads = p.Hkv * tree_blocks<Packed>(p, m);
   }
 
-  __device__ __forceinline__ TreeWalk(const TreeParams& p_, int32_t range_) : p(p_), range(range_) {
+  __device__ __forceinline__ TreeWalk(const TreeParams& p_, int32_t range_, bool walks = true) : p(p_), range(range_) {
     const int lane = threadIdx.x & 31;
     pos = end = 0;
-    b = h = base = my_len = my_m = 0;
+    b = i = base = my_len = my_m = 0;
     v = 0;
+    if (!walks) return;
     if (uniform()) {
       load(0);
-      units = (int64_t)p.B * p.Hkv * u;
+      units = (int64_t)p.B * heads * u;
     } else {
       int64_t sum = 0;
-      for (int32_t i = (p.B - 1) & ~31; i >= 0; i -= 32) {  // the first block stays at hand
-        block(i);
-        sum += units_of(my_len, my_m);
+      for (int32_t b0 = (p.B - 1) & ~31; b0 >= 0; b0 -= 32) {  // the first block stays at hand
+        block(b0);
+        sum += (int64_t)units_of(my_len, my_m) * tree_blocks<Packed>(p, my_m);
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -154,16 +199,16 @@ struct TreeWalk {
     end = range_begin(units, used, range + 1);
     // the sequence that holds `pos`
     if (uniform()) {
-      const int64_t i = div_floor(pos, u);
-      b = (int32_t)div_floor(i, p.Hkv);
-      h = (int32_t)(i - (int64_t)b * p.Hkv);
-      v = i * u;
+      const int64_t pair = div_floor(pos, u);
+      b = (int32_t)div_floor(pair, heads);
+      i = (int32_t)(pair - (int64_t)b * heads);
+      v = pair * u;
       return;
     }
     int64_t before = 0;
     for (int32_t i0 = 0; i0 < p.B; i0 += 32) {
       if (i0 != base) block(i0);
-      const int64_t mine = units_of(my_len, my_m);
+      const int64_t mine = (int64_t)units_of(my_len, my_m) * tree_blocks<Packed>(p, my_m);
       int64_t incl = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -175,8 +220,8 @@ struct TreeWalk {
         const int l = __ffs(past) - 1;
         const int64_t start = (before + __shfl_sync(0xffffffffu, incl - mine, l)) * p.Hkv;
         load(i0 + l);
-        h = (int32_t)div_floor(pos - start, u);
-        v = start + (int64_t)h * u;
+        i = (int32_t)div_floor(pos - start, u);
+        v = start + (int64_t)i * u;
         return;
       }
       before += __shfl_sync(0xffffffffu, incl, 31);
@@ -195,7 +240,13 @@ struct TreeWalk {
       const bool found = hi > lo;
       if (found) {
         pc.b = b;
-        pc.h = h;
+        pc.h = i;
+        pc.sub = 0;
+        if constexpr (Packed > 0) {
+          const int32_t per = tree_blocks<Packed>(p, m);
+          pc.h = i / per;
+          pc.sub = i % per;
+        }
         pc.begin = lo * kPlanTile;
         pc.end = hi < tiles ? hi * kPlanTile : len;
         pc.len = len;
@@ -207,8 +258,8 @@ struct TreeWalk {
       pos = stop;
       if (pos == pend) {
         v = pend;
-        if (++h == p.Hkv) {
-          h = 0;
+        if (++i == heads) {
+          i = 0;
           if (uniform()) {
             ++b;
           } else if (pos < end) {  // the walk ends inside the units in all, so a sequence with units follows
@@ -226,27 +277,31 @@ struct TreeWalk {
   // Says of the pair that `pc` begins (if it does) whether it goes on, for the join; one lane.
   __device__ __forceinline__ void say(const TreePiece& pc) const {
     if (pc.begin != 0 || (pc.slot < 0 && !p.join_pairs)) return;
-    TreeJoin j{-1, pc.h, range, range};
+    TreeJoin j{-1, pc.h, pc.sub, range, range};
     if (pc.slot >= 0) {
       j.b = pc.b;
       j.last = cta_of_unit(units, used, pc.v + piece_units() + (int64_t)kTileUnits * (pc.tiles - 1));
     }
-    p.joins[p.join_pairs ? (int64_t)pc.b * p.Hkv + pc.h : range] = j;
+    p.joins[p.join_pairs ? ((int64_t)pc.b * p.Hkv + pc.h) * p.blocks + pc.sub : range] = j;
   }
 };
 
 // Sequences without keys or tokens: no share holds them.  The rows of their tokens get
 // out = 0, lse = -inf, and their pairs nothing to join, from the CTAs of share b % ranges.
-template <int D, int Rows>
+template <int D, int Rows, int Packed>
 __device__ __forceinline__ void tree_no_rows(const TreeParams& p, int32_t range, int32_t sub, int tid, int threads) {
   if (!p.join_pairs && sub == 0 && tid == 0) p.joins[range].b = -1;
   for (int32_t b = range; b < p.B; b += p.ranges) {
     const int32_t len = tree_len(p, b), m = tree_tokens(p.tree, b);
-    if (p.join_pairs && sub == 0 && (len == 0 || m == 0))
-      for (int32_t h = tid; h < p.Hkv; h += threads) p.joins[(int64_t)b * p.Hkv + h].b = -1;
+    if (p.join_pairs && sub == 0) {
+      const int32_t live = len == 0 || m == 0 ? 0 : tree_blocks<Packed>(p, m);
+      if (live < p.blocks)
+        for (int32_t i = tid; i < p.Hkv * p.blocks; i += threads)
+          if (i % p.blocks >= live) p.joins[(int64_t)b * p.Hkv * p.blocks + i].b = -1;
+    }
     if (len != 0) continue;
     const int32_t pad = p.tree.n - m;
-    const int32_t r0 = sub * Rows, r1 = r0 + Rows < p.rows ? r0 + Rows : p.rows;
+    const int32_t r0 = sub * Rows, r1 = Packed == 0 && r0 + Rows < p.rows ? r0 + Rows : p.rows;
     for (int64_t i = tid; i < (int64_t)p.Hkv * (r1 - r0); i += threads) {
       const int32_t row = r0 + (int32_t)(i % (r1 - r0));
       if (row % p.tree.n < pad) continue;

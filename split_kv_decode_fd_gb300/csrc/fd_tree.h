@@ -40,8 +40,12 @@ struct TreeView {
 // an earlier share (slot 2 r), and one that begins a pair (slot 2 r + 1).  Their number does not
 // grow with the batch.  Where a pair begins, joins says whether and how far it goes on: an
 // entry for each pair, or for each share where these are fewer.
+//
+// `packed` (fp32 caches): a block's rows are those of tokens alone, and each (b, KV head, block) is a pair of
+// its own, so that padded batches cost what their tokens need; nsub is 1 then, and `blocks` the
+// blocks of a KV head whose rows are all tokens.
 struct TreeJoin {
-  int32_t b, h;         // sequence (-1: nothing to join), KV head
+  int32_t b, h, sub;    // sequence (-1: nothing to join), KV head, block of its rows (packed)
   int32_t first, last;  // shares that hold the pair
 };
 
@@ -61,6 +65,7 @@ struct TreeParams {
   int32_t rows;                // g * n
   int32_t nsub, ranges;
   int32_t n_joins, join_pairs; // join_pairs: an entry for each pair
+  int32_t packed, blocks;
   int32_t max_len;
   int32_t box_rows;            // rows that a copy of K or V brings (bf16 caches)
   float qk_scale;              // scale * log2(e)
@@ -70,10 +75,10 @@ struct TreeParams {
 
 // Rows per CTA and CTAs per SM: fp32 caches on CUDA cores; bf16 ones on tensor cores, up to 64 rows of a KV head with the
 // keys on the rows of the products, more in blocks of 128 with the query rows there.
-constexpr int kTreeRowsCore = 32, kTreeCtasCore = 2;
+constexpr int kTreeRowsCore = 32;
 constexpr int kTreeRowsMma = 128;
 constexpr int tree_rows(bool f32, int rows) { return f32 || rows <= 32 ? 32 : rows <= 64 ? 64 : kTreeRowsMma; }
-constexpr int tree_ctas(bool f32) { return f32 ? kTreeCtasCore : 1; }
+constexpr int tree_ctas(bool f32, int D) { return !f32 ? 1 : D == 64 ? 3 : 2; }
 // Rows of a copy: as many of 64, 32, 16 as lie in a page.  A copy takes a warp some 100 cycles to start.
 constexpr int tree_box_rows(int page) { return page % 64 == 0 ? 64 : page % 32 == 0 ? 32 : 16; }
 

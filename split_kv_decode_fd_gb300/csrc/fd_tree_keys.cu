@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ pieces, q, K
     uint32_t u = 0, f = 0, skipped = 0xffffffffu;
     Ring<Lay::kK> r;
-    TreeWalk walk(p, range);
+    TreeWalk<0> walk(p, range);
     for (uint32_t e = 0;; ++e) {
       TreePiece pc;
       if (!walk.next(pc)) pc.b = -1;
@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int32_t channel = (warp & 3) * kLanes + lane % kLanes;
     const bool holds = lane < kLanes;
     const uint32_t at = tmem + 2 * kParts * N + ((uint32_t)((warp & 3) * 32) << 16);
-    tree_no_rows<D, N>(p, range, sub, tid - kSums * 32, 128);
+    tree_no_rows<D, N, 0>(p, range, sub, tid - kSums * 32, 128);
     uint32_t g = 0;
     TreePiece pc;
     for (uint32_t e = 0; take(e, pc); ++e) {

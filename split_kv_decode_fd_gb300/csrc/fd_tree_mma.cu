@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ pieces, q, K
     uint32_t u = 0, f = 0, skipped = 0xffffffffu;
     Ring<Lay::kK> r;
-    TreeWalk walk(p, range);
+    TreeWalk<0> walk(p, range);
     for (uint32_t e = 0;; ++e) {
       TreePiece pc;
       if (!walk.next(pc)) pc.b = -1;
@@ -481,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ sums
     const uint32_t at = tmem + kOCol + ((uint32_t)((warp - 4) * 32) << 16);
     const int32_t row = (warp - 4) * 32 + lane;
-    tree_no_rows<D, kRows>(p, range, sub, row, (int)warps * 32);
+    tree_no_rows<D, kRows, 0>(p, range, sub, row, (int)warps * 32);
     uint32_t g = 0;
     TreePiece pc;
     for (uint32_t e = 0; take(e, pc); ++e) {
