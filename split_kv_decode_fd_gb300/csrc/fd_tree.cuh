@@ -43,8 +43,9 @@ __device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
   return d;
 }
 
-// Cost units (kTileUnits = 4 a tile of 128 keys) that a piece costs a CTA besides its tiles.
-constexpr int kTreePieceUnits = 6;
+// Cost units (kTileUnits = 4 a tile of 128 keys) that a piece costs a CTA besides its tiles: q and the first tile's way
+// through the roles, some 5 us or three tiles of 64 rows (64 paged sequences of 512 to 16384 tokens: 271 us with 6, 255 with 12).
+constexpr int kTreePieceUnits = 12;
 
 __device__ __forceinline__ int32_t tree_len(const TreeParams& p, int32_t b) {
   return p.seq_lens ? clamp_len(__ldg(p.seq_lens + b), p.max_len) : p.max_len;
@@ -315,8 +316,9 @@ __device__ __forceinline__ void tree_no_rows(const TreeParams& p, int32_t range,
 
 constexpr float kTreeLn2 = 0.6931471805599453f;
 
-// Lets a kernel take `bytes` of dynamic shared memory, once per device.
-template <auto Kernel>
+// Lets a kernel take `bytes` of dynamic shared memory, once per device.  Regs: a kernel whose roles share its registers
+// out anew waits forever if it was not launched with as many a thread as the shares add up to: any other build of it is refused.
+template <auto Kernel, int Regs = 0>
 cudaError_t allow_smem(int bytes) {
   static std::atomic<uint64_t> done{0};
   int dev = 0;
@@ -324,6 +326,12 @@ cudaError_t allow_smem(int bytes) {
   if (e != cudaSuccess) return e;
   const uint64_t bit = dev < 64 ? 1ull << dev : 0;
   if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  if constexpr (Regs > 0) {
+    cudaFuncAttributes of;
+    e = cudaFuncGetAttributes(&of, Kernel);
+    if (e != cudaSuccess) return e;
+    if ((of.numRegs + 7) / 8 * 8 != Regs) return cudaErrorInvalidConfiguration;  // they are given out by eights
+  }
   e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
   return e;

@@ -30,7 +30,9 @@ namespace fdk {
 namespace {
 
 constexpr int kKeys = kPlanTile;
-constexpr int kThreads = 512;
+constexpr int kThreads = 512, kRegs = 128;  // registers a thread at launch
+constexpr int kSoftmaxRegs = 136, kSumsRegs = 152, kOtherRegs = 88;
+static_assert(256 * kSoftmaxRegs + 128 * kSumsRegs + 128 * kOtherRegs == kThreads * kRegs, "shares");
 constexpr int kSums = 8, kCopyK = 12, kCopyV = 13, kSWarp = 14;  // first of the sums' warps; S, and O: 15
 constexpr int kMoves = 4;              // tiles whose moves of the references are kept
 constexpr float kTau = 8.f;            // p stays below 2^kTau
@@ -104,6 +106,12 @@ __device__ __forceinline__ float across(float (&v)[R], F f) {
   return v[0];
 }
 
+// What does not fit the registers spills to L2, as shared memory leaves L1 nothing (64 paged sequences: 255 us with 128
+// for every thread, 239 with these shares).
+template <int N>
+__device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+__device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs)); }
+
 template <int D, int N>
 __global__ void __launch_bounds__(kThreads, 1)
     fd_tree_keys_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
@@ -174,6 +182,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const TileCopy copy(p);
 
   if (warp == kCopyK) {
+    give_registers();
     // ------------------------------------------------------------ pieces, q, K
     uint32_t u = 0, f = 0, skipped = 0xffffffffu;
     Ring<Lay::kK> r;
@@ -227,6 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == kCopyV) {
+    give_registers();
     // ------------------------------------------------------------ V
     uint32_t u = 0;
     Ring<Lay::kV> r;
@@ -251,6 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp >= kSWarp) {
+    give_registers();
     // ------------------------------------------------------------ products
     // Every branch and operand is uniform over the warp as the compiler sees it (votes and shuffles), so that the
     // products take their operands from uniform registers as they are.
@@ -329,6 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp < kSums) {
+    take_registers<kSoftmaxRegs>();
     // ------------------------------------------------------------ softmax
     // The four warps of a group meet at barriers: they stay together, whatever a wait of one of them says, and leave
     // together.
@@ -556,6 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       atomicOr(p.err, kErrTimeout);
     }
   } else {
+    take_registers<kSumsRegs>();
     // ------------------------------------------------------------ sums
     // D = 128: lane of tensor memory = channel; D = 64: a warp's lanes 0-15 hold sixteen channels.
     constexpr int kLanes = D / 4;
@@ -680,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D, int N>
 cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p, cudaStream_t stream) {
   constexpr uint32_t bytes = Layout<D, N>::kBytes;
-  const cudaError_t e = allow_smem<fd_tree_keys_kernel<D, N>>((int)bytes);
+  const cudaError_t e = allow_smem<fd_tree_keys_kernel<D, N>, kRegs>((int)bytes);
   if (e != cudaSuccess) return e;
   return launch_early(fd_tree_keys_kernel<D, N>, (unsigned)(p.ranges * p.nsub), kThreads, bytes, stream, tk, tv, p);
 }

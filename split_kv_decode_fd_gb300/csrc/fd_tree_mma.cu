@@ -1,10 +1,10 @@
 // fd_tree_mma.cu -- attention of a tree of drafted tokens over a bf16 cache on the
-// 5th-generation tensor cores.
+// 5th-generation tensor cores, for more than 64 rows a KV head.
 //
-// The rows of a KV head's group (heads x tokens, up to 128 a CTA) are the rows of
+// The rows of a KV head's group (heads x tokens, 128 a CTA) are the rows of
 // both products: S = Q K^T (128 x 128 keys, over D) and O = P V (128 x D, over the 128
-// keys of a tile).  The work is bound by reading the cache as long as the products
-// take less time than the tile's bytes, and the rows of one CTA come free with it.
+// keys of a tile).  Blocks of rows of a KV head run side by side on the same keys, which come from memory once
+// and from L2 for the others.
 //
 // Precision: K and V are exact in bf16.  q and p (fp32) are cut into three bf16
 // numbers of eight bits each by truncation, which is exact, so all products are, and
@@ -13,7 +13,7 @@
 // unit drop bits.  Six products of 8 k-steps make 3072 cycles a tile of 128 channels, and a
 // tile's 64 KB at an SM's share of the memory rate some 3000.
 //
-// Twelve warps:
+// Eleven warps:
 //   0-3  softmax, thread = row: reads S, masks, keeps the running max and sum, writes P
 //        over S; cuts q at the start of a piece.
 //   4-7  sums, thread = row: O of each tile times what the max has moved by; writes the
@@ -23,10 +23,8 @@
 //        be free: a barrier tells a phase from the one before, not from the one before that.  A warp starts a copy in
 //        some 100 cycles, so a copy brings up to 64 rows of a page and 64 channels (128-byte swizzle), and K and V have
 //        a warp each (with copies of 16 rows by one warp a tile took 4300 cycles);
-//   10, 11  products, one thread of each: S, and O.  While the softmax of a tile runs, the tensor
-//        core has the S of the next and the O of the one before.
-#include <atomic>
-
+//   10   products, one thread: S of the next tile, then O of this one.  While the softmax of a tile runs, the tensor
+//        core has the S of the next and the O of the one before.  (With a warp for S and one for O, 8 % slower.)
 #include "fd_tree_tc.cuh"
 
 namespace fdk {
@@ -34,24 +32,24 @@ namespace {
 
 constexpr int kRows = kTreeRowsMma;
 constexpr int kKeys = kPlanTile;
-constexpr int kThreads = 352;
-constexpr int kCopyK = 8, kCopyV = 9, kSWarp = 10;  // and O: 11
+constexpr int kThreads = 384, kRegs = 168;  // registers a thread at launch
+constexpr int kMoreRegs = 208, kLessRegs = 88;  // of the softmax and the sums, and of the other roles
+static_assert(256 * kMoreRegs + 128 * kLessRegs == kThreads * kRegs, "shares");
+constexpr int kCopyK = 8, kCopyV = 9, kProducts = 10;
 constexpr int kPBufs = 4;                // barriers of P and places for a tile's max
 // Tensor memory: two S / P buffers and O.  P takes 8 columns for each part of 16 keys, 192 in
 // all, and S the last 128 of them: a chunk of P never reaches an unread chunk of S.
 constexpr uint32_t kBuf = 192, kSOff = 64, kOCol = 384;
 
-// Rows: rows of q that are held, 64 or 128.  With 64, an operand's other rows are what follows in shared memory: the
-// products have rows that nobody reads, and the ring a slot more.
-template <int D, int Rows>
+template <int D>
 struct Layout {
   static constexpr int kNB = D / 64;                          // 128-byte column blocks of a row
   static constexpr uint32_t kBlock = 16384;                   // [128 rows][128 bytes]
   static constexpr uint32_t kTile = kNB * kBlock;             // a K or V tile
-  static constexpr uint32_t kQBlock = Rows * 128u;            // a column block of a part of q
+  static constexpr uint32_t kQBlock = kRows * 128u;           // a column block of a part of q
   static constexpr uint32_t kQPart = kNB * kQBlock;
   static constexpr uint32_t kRing = kParts * kQPart;          // q first
-  static constexpr uint32_t kK = D == 64 ? 4 : Rows == 64 ? 3 : 2, kV = D == 64 ? 4 : 2;  // slots
+  static constexpr uint32_t kK = D == 64 ? 4 : 2, kV = D == 64 ? 4 : 2;  // slots
   static constexpr uint32_t kVRing = kRing + kK * kTile;
   static constexpr uint32_t kMisc = kVRing + kV * kTile;
   static constexpr uint32_t kQRowsPerSlot = kTile / (D * 4);  // fp32 rows of q
@@ -65,7 +63,7 @@ struct Misc {
   uint64_t q_full[2][2];                               // of even and odd pieces, of each 64 rows
   uint64_t s_full[2], p_empty[2], o_empty[2], p_full[kPBufs];
   uint64_t piece_full[2], piece_empty[2];
-  uint64_t o_full, q_ready, fin_full, fin_empty, drain[2];
+  uint64_t o_full, q_ready, fin_full, fin_empty, drain;
   uint32_t tmem;
   volatile int abort;
   TreePiece piece[2];
@@ -75,11 +73,16 @@ struct Misc {
 };
 static_assert(sizeof(Misc) <= 3072, "Misc");
 
-template <int D, int Rows>
+// What does not fit the registers spills to L2, as shared memory leaves L1 nothing: 64 rows of 131072 keys took 8 heads
+// 316 us with 168 for every thread, 268 with 200 for those with much to hold, 241 with less code in the loops too.
+__device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kMoreRegs)); }
+__device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLessRegs)); }
+
+template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     fd_tree_mma_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                        const __grid_constant__ TreeParams p) {
-  using Lay = Layout<D, Rows>;
+  using Lay = Layout<D>;
   constexpr uint32_t kBlock = Lay::kBlock, kTile = Lay::kTile;
   extern __shared__ __align__(1024) uint8_t smem[];
   Misc& s = *reinterpret_cast<Misc*>(smem + Lay::kMisc);
@@ -109,10 +112,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(s.o_empty + i, warps);
       mbar_init(s.piece_full + i, 1);
       mbar_init(s.piece_empty + i, 2 + 2 * warps);
-      mbar_init(s.drain + i, 1);
     }
     for (int i = 0; i < kPBufs; ++i) mbar_init(s.p_full + i, warps);
     mbar_init(&s.o_full, 1);
+    mbar_init(&s.drain, 1);
     mbar_init(&s.q_ready, warps);
     mbar_init(&s.fin_full, warps);
     mbar_init(&s.fin_empty, warps);
@@ -121,8 +124,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == kCopyK && lane == 0) prefetch_tensormap(&tmap_k);
   if (warp == kCopyV && lane == 0) prefetch_tensormap(&tmap_v);
-  if (warp == kSWarp) tmem_alloc_all(smem_addr(&s.tmem));
-  if (warp < 4 && warp >= (int)warps && tid < Rows) {  // rows of q that are none are 0
+  if (warp == kProducts) tmem_alloc_all(smem_addr(&s.tmem));
+  if (warp < 4 && warp >= (int)warps) {  // rows of q that are none are 0
     for (uint32_t i = 0; i < kParts * Lay::kNB * 8u; ++i)
       sts128(sq + (i >> 3) * Lay::kQBlock + (uint32_t)tid * 128u + (i & 7u) * 16u, 0u, 0u, 0u, 0u);
     fence_async();
@@ -170,6 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp == kCopyK) {
+    give_registers();
     // ------------------------------------------------------------ pieces, q, K
     uint32_t u = 0, f = 0, skipped = 0xffffffffu;
     Ring<Lay::kK> r;
@@ -207,6 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     leave(s.k_full, u, Lay::kK, skipped, 0, f);
   } else if (warp == kCopyV) {
+    give_registers();
     // ------------------------------------------------------------ q, V
     uint32_t u = 0, f = 0;
     Ring<Lay::kV> r;
@@ -232,13 +237,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!w.ok) break;
     }
     leave(s.v_full, u, Lay::kV, 0xffffffffu, 1, f);
-  } else if (warp == kSWarp) {
+  } else if (warp == kProducts) {
+    give_registers();
     // ------------------------------------------------------------ products
     // Every branch and operand is uniform over the warp as the compiler sees it (votes and shuffles), so that the
     // products take their operands from uniform registers as they are.
     constexpr uint32_t idS = bf16_instr_desc(kRows, kKeys), idO = bf16_instr_desc(kRows, D, true);
     const uint32_t base = uniform(tmem), q0 = uniform(sq), k0 = uniform(k_ring), v0 = uniform(v_ring);
-    const bool is_s = uniform((uint32_t)warp) == kSWarp;
     Ring<Lay::kK> rk;
     Ring<Lay::kV> rv;
     uint32_t g = 0, f = 0;  // tiles and pieces so far
@@ -262,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_fence_after();
           if (elect_one()) {
             const uint32_t d = base + (t & 1) * kBuf + kSOff, k = k0 + rk.slot * kTile;
-#pragma unroll
+#pragma unroll 1
             for (int part = kParts - 1; part >= 0; --part) {
 #pragma unroll
               for (int i = 0; i < D / 16; ++i) {
@@ -286,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_fence_after();
           if (elect_one()) {
             const uint32_t a = base + (t & 1) * kBuf, v = v0 + rv.slot * kTile;
-#pragma unroll
+#pragma unroll 1
             for (int part = kParts - 1; part >= 0; --part) {
 #pragma unroll
               for (int i = 0; i < kKeys / 16; ++i)
@@ -311,12 +316,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // every product has completed before tensor memory is given back
     if (elect_one()) {
-      uint64_t* done = s.drain + (is_s ? 0 : 1);
-      mma_commit(smem_addr(done));
-      if (!mbar_wait_for(done, 0, w.limit)) atomicOr(p.err, kErrTimeout);
+      mma_commit(smem_addr(&s.drain));
+      if (!mbar_wait_for(&s.drain, 0, w.limit)) atomicOr(p.err, kErrTimeout);
     }
     __syncwarp();
-  } else if (warp < (int)warps) {
+  } else if (warp < 4) {
+    take_registers();
+    if (warp < (int)warps) {
     // ------------------------------------------------------------ softmax
     const uint32_t lanes = (uint32_t)(warp * 32) << 16;
     const int32_t row = warp * 32 + lane;  // of the block = lane of tensor memory
@@ -331,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // q: three bf16 parts of the row in the swizzled layout of an MMA operand.  The products of the piece before
       // have read theirs: its last S has been seen.  A lane starts at a 16-byte chunk of its own, off the others' banks.
       for (uint32_t i = 0; i < nq; ++i) w.on(&s.q_full[e & 1][i], (e >> 1) & 1);
-      if (row < live || (e == 0 && row < Rows)) {  // rows that are none stay 0
+      if (row < live || e == 0) {  // rows that are none stay 0
         constexpr uint32_t kC = D / 4, kStep = 8;  // fp32 chunks of a row, at a time
         const uint32_t from = (row < (int32_t)Lay::kQRowsPerSlot ? k_ring + uk % Lay::kK * kTile : v_ring + uv % Lay::kV * kTile) +
                               (uint32_t)row % Lay::kQRowsPerSlot * (D * 4);
@@ -477,7 +483,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       s.abort = 1;
       atomicOr(p.err, kErrTimeout);
     }
-  } else if (warp >= 4 && warp < 4 + (int)warps) {
+    }
+  } else if (warp < 8) {
+    take_registers();
+    if (warp < 4 + (int)warps) {
     // ------------------------------------------------------------ sums
     const uint32_t at = tmem + kOCol + ((uint32_t)((warp - 4) * 32) << 16);
     const int32_t row = (warp - 4) * 32 + lane;
@@ -566,29 +575,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       s.abort = 1;
       atomicOr(p.err, kErrTimeout);
     }
+    }
+  } else {
+    give_registers();
   }
   tmem_fence_before();
   cta_sync();
-  if (warp == kSWarp) {
+  if (warp == kProducts) {
     tmem_fence_after();
     tmem_free_all(tmem);
   }
 }
 
-template <int D, int Rows>
+template <int D>
 cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p, cudaStream_t stream) {
-  constexpr uint32_t bytes = Layout<D, Rows>::kBytes;
-  const cudaError_t e = allow_smem<fd_tree_mma_kernel<D, Rows>>((int)bytes);
+  constexpr uint32_t bytes = Layout<D>::kBytes;
+  const cudaError_t e = allow_smem<fd_tree_mma_kernel<D>, kRegs>((int)bytes);
   if (e != cudaSuccess) return e;
-  return launch_early(fd_tree_mma_kernel<D, Rows>, (unsigned)(p.ranges * p.nsub), kThreads, bytes, stream, tk, tv, p);
+  return launch_early(fd_tree_mma_kernel<D>, (unsigned)(p.ranges * p.nsub), kThreads, bytes, stream, tk, tv, p);
 }
 
 }  // namespace
 
 cudaError_t launch_tree_mma(int D, const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p,
                             cudaStream_t stream) {
-  if (D == 128) return launch<128, 128>(tk, tv, p, stream);
-  if (D == 64) return launch<64, 128>(tk, tv, p, stream);
+  if (D == 128) return launch<128>(tk, tv, p, stream);
+  if (D == 64) return launch<64>(tk, tv, p, stream);
   return cudaErrorInvalidValue;
 }
 
