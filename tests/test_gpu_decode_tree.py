@@ -209,6 +209,39 @@ def test_many_pieces_and_blocks_of_rows(D, page, g, n, most):
     assert norm < 2e-6, norm  # rounding errors of fp32 sums, unbiased: some 4e-7
 
 
+@pytest.mark.parametrize("D,page", [(64, 0), (128, 16)])
+@pytest.mark.parametrize("g,n", [(1, 5), (2, 33), (8, 64)])
+@pytest.mark.parametrize("most", [100, 700, 6000])
+@pytest.mark.parametrize("uniform", [False, True])
+def test_blocks_of_token_rows_over_an_fp32_cache(D, page, g, n, most, uniform):
+    """Blocks of rows that are pairs of their own, and that a sequence of few tokens does not have."""
+    r = np.random.default_rng(most + n)
+    B, Hkv = (150, 2) if most < 1000 else (10, 2)
+    lens = [most] * B if uniform else r.integers(0, most, B).tolist()
+    c = Case(B, g * Hkv, Hkv, D, n, lens, page=page, cache="f32", seed=most + n,
+             new_lens=None if uniform else [int(x) for x in r.integers(0, n + 1, B)])
+    out, lse = c.run(seq_lens=None, max_seq_len=most) if uniform else c.run()
+    assert fd.workspace_status() == 0
+    ro, rl = exact_on_the_gpu(c)
+    live = ~torch.isnan(rl)
+    # as above: the bound of the head of this file is below 1e-4 here
+    assert (out.double() - ro)[live].abs().max() < 1e-4
+    fin = live & torch.isfinite(rl)
+    assert torch.equal(torch.isneginf(lse[live]), torch.isneginf(rl[live])) and (lse.double() - rl)[fin].abs().max() < 1e-4
+    norm = (out.double() - ro)[live].norm() / ro[live].norm()
+    assert norm < 2e-6, norm
+
+
+@pytest.mark.parametrize("cache", ["bf16", "f32"])
+@pytest.mark.parametrize("Hq,n", [(4, 5), (8, 30), (8, 64)])
+def test_tokens_without_lengths_and_more_tokens_than_places(Hq, n, cache):
+    """new_lens without seq_lens: every sequence has max_seq_len places, here fewer than some have tokens."""
+    for T in (1, 40, 333):
+        c = Case(4, Hq, 2, 128, n, [T] * 4, new_lens=[0, 1, n // 2, n], cap=336, cache=cache, seed=T)
+        c.check(*c.run(seq_lens=None, max_seq_len=T))
+        assert fd.workspace_status() == 0
+
+
 @pytest.mark.parametrize("cache", ["bf16", "f32"])
 def test_a_large_batch_of_short_sequences(cache):
     r = np.random.default_rng(0)

@@ -69,6 +69,13 @@ def test_against_the_oracle(V, dtype, draft, shape):
     assert fd.workspace_status() == 0
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_a_large_vocabulary(dtype):
+    c = Case(2, 9, 300007, dtype=dtype, draft=dtype == "f32", shape="random", seed=1)
+    c.check(c.run())
+    assert fd.workspace_status() == 0
+
+
 @pytest.mark.parametrize("n", [1, 2, 31, 32, 33, 63, 64])
 @pytest.mark.parametrize("draft", [True, False])
 @pytest.mark.parametrize("agree", [0.0, 0.95, 1.0])
