@@ -65,7 +65,7 @@ typedef enum fd_status {
   FD_ERR_INVALID_ARG = 1,         /* null pointer, bad size, misalignment, Hq % Hkv != 0 ... */
   FD_ERR_UNSUPPORTED = 2,         /* head_dim, dtype or size outside what this build handles */
   FD_ERR_WORKSPACE_TOO_SMALL = 3, /* workspace_bytes < fd_workspace_bytes(...) */
-  FD_ERR_BAD_INDEX = 4,           /* a kernel met a block-table entry outside [0, num_pages) */
+  FD_ERR_BAD_INDEX = 4,           /* a kernel met a block-table entry outside [0, num_pages), or another index outside its range */
   FD_ERR_CUDA = 5,                /* a CUDA runtime/driver call failed (launch, copy, ...) */
   FD_ERR_TIMEOUT = 6              /* a kernel's internal wait gave up (never expected) */
 } fd_status;

@@ -307,7 +307,7 @@ const char* fd_status_string(fd_status s) {
     case FD_ERR_INVALID_ARG: return "invalid argument";
     case FD_ERR_UNSUPPORTED: return "unsupported shape or dtype";
     case FD_ERR_WORKSPACE_TOO_SMALL: return "workspace too small";
-    case FD_ERR_BAD_INDEX: return "block-table entry out of range";
+    case FD_ERR_BAD_INDEX: return "block-table entry or other index out of range";
     case FD_ERR_CUDA: return "CUDA error";
     case FD_ERR_TIMEOUT: return "kernel wait timed out";
   }
