@@ -18,9 +18,11 @@
 // walks the tree (when all sixteen did, 64 sequences of 131072 words took 131 us).
 //
 // Bound by the latency of the passes over a row (its sum when a child is refused, or at the end), one after
-// another: some 9 us each on a full device, of which the loads are a third and the exchange of sums and the walk another.
-// Measured: 64 sequences of 16 drafts, 131072 words in fp32, up to five passes, 44.5 us (reading the rows once takes 10); 32
-// sequences of 32 drafts, 65521 words in bf16, 14.3; one sequence of 8, 32000 words, 8.5.
+// another: some 6 us each once few sequences are left, two thirds of it the sum (its arithmetic in dependent steps, two warps a
+// scheduler), the rest the exchange of sums and the walk.
+// Measured: 64 sequences of 16 drafts, 131072 words in fp32, up to five passes, 43.7 us (reading the rows once takes 10); 32
+// sequences of 32 drafts, 65521 words in bf16, 11.6; one sequence of 8, 32000 words, 8.1.  (All refused words looked for in every
+// group of words 14.2 in place of 11.6; six groups in flight instead of four 45.6 in place of 43.7.)
 //
 // A cluster takes a sequence, each of its CTAs a part of the vocabulary; CTAs exchange
 // their sums through shared memory and decide alike.  The numbers that decide on a child
@@ -110,8 +112,17 @@ __device__ __forceinline__ void store_remote(Sum* at, uint32_t rank, const Sum& 
 
 template <class T>
 constexpr int kGroup = 16 / (int)sizeof(T);  // probabilities in 16 bytes
-template <class T>
-constexpr int kGroupsAhead = (int)sizeof(T);  // loads a thread has in flight, of each of p and q: 16 probabilities
+constexpr int kAhead = 4;                                  // groups of each of p and q that a thread has in flight
+constexpr int kRingBytes = 2 * kAhead * kThreads * 16;     // where they land
+
+// The probabilities of 16 bytes.
+__device__ __forceinline__ void widen(const uint4& w, float (&x)[4]) {
+  x[0] = __uint_as_float(w.x), x[1] = __uint_as_float(w.y), x[2] = __uint_as_float(w.z), x[3] = __uint_as_float(w.w);
+}
+__device__ __forceinline__ void widen(const uint4& w, float (&x)[8]) {
+  x[0] = bf16_lo(w.x), x[1] = bf16_hi(w.x), x[2] = bf16_lo(w.y), x[3] = bf16_hi(w.y);
+  x[4] = bf16_lo(w.z), x[5] = bf16_hi(w.z), x[6] = bf16_lo(w.w), x[7] = bf16_hi(w.w);
+}
 
 template <class T>
 __device__ __forceinline__ float at(const T* row, int32_t i);
@@ -129,13 +140,7 @@ __device__ __forceinline__ void load_group(const T* row, int32_t g, int32_t V, i
   constexpr int E = kGroup<T>;
   const int32_t first = g * E - off;
   if (vec && first >= 0 && first + E <= V) {
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>(row + first));
-    if constexpr (E == 4) {
-      x[0] = __uint_as_float(w.x), x[1] = __uint_as_float(w.y), x[2] = __uint_as_float(w.z), x[3] = __uint_as_float(w.w);
-    } else {
-      x[0] = bf16_lo(w.x), x[1] = bf16_hi(w.x), x[2] = bf16_lo(w.y), x[3] = bf16_hi(w.y);
-      x[4] = bf16_lo(w.z), x[5] = bf16_hi(w.z), x[6] = bf16_lo(w.w), x[7] = bf16_hi(w.w);
-    }
+    widen(__ldg(reinterpret_cast<const uint4*>(row + first)), x);
   } else {
 #pragma unroll
     for (int e = 0; e < E; ++e) x[e] = first + e >= 0 && first + e < V ? at(row, first + e) : 0.f;
@@ -149,8 +154,34 @@ struct Left {
   int32_t V, off;
   bool vec;                   // both rows are at the same place of 16 bytes
   float c_hi, c_lo;           // c as a sum of two floats
-  const int32_t* refused;     // without a draft: words that are out, those of this CTA's part
+  const int32_t* refused;     // without a draft: words that are out
   int32_t n_refused;
+  uint64_t near;              // those of them that lie in the groups at hand, by their number
+
+  // Before groups [g0, g1), a warp's, are looked at.
+  __device__ __forceinline__ void range(int32_t g0, int32_t g1) {
+    near = 0;
+    if constexpr (!kDraft) {
+      const int lane = threadIdx.x & 31;
+      const int32_t first = g0 * kGroup<T> - off, end = g1 * kGroup<T> - off;
+      uint32_t in[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int32_t x = lane + 32 * i < n_refused ? refused[lane + 32 * i] : -1;
+        in[i] = __ballot_sync(0xffffffffu, x >= 0 && x >= first && x < end);
+      }
+      near = (uint64_t)in[1] << 32 | in[0];
+    }
+  }
+  // Without the words of group g that are out.
+  __device__ __forceinline__ void refuse(float (&x)[kGroup<T>], int32_t g) const {
+    for (uint64_t some = near; some; some &= some - 1) {
+      const int32_t e = refused[__ffsll((long long)some) - 1] - (g * kGroup<T> - off);
+#pragma unroll
+      for (int k = 0; k < kGroup<T>; ++k)
+        if (k == e) x[k] = 0.f;
+    }
+  }
 
   // r of group g as sums hi + lo
   __device__ __forceinline__ void group(const float (&x)[kGroup<T>], const float (&y)[kGroup<T>], int32_t g,
@@ -169,48 +200,82 @@ struct Left {
       hi[e] = some ? d : 0.f;
       lo[e] = some ? t : 0.f;
     }
-    if constexpr (!kDraft) {
-      for (int32_t i = 0; i < n_refused; ++i) {
-        const int32_t e = refused[i] - (g * kGroup<T> - off);
-#pragma unroll
-        for (int k = 0; k < kGroup<T>; ++k)
-          if (k == e) hi[k] = 0.f;
-      }
-    }
+    if constexpr (!kDraft) refuse(hi, g);
   }
 
-  // The sum over groups [g0, g1), one warp; the same value in every lane.
-  __device__ __forceinline__ Sum sum(int32_t g0, int32_t g1) const {
-    constexpr int E = kGroup<T>, kAhead = kGroupsAhead<T>;
-    const int lane = threadIdx.x & 31;
-    Sum s{0.f, 0.f};
-    for (int32_t g = g0 + lane; g < g1; g += 32 * kAhead) {
-      float x[kAhead][E], y[kAhead][E] = {};
-#pragma unroll
-      for (int a = 0; a < kAhead; ++a) {
-        const int32_t ga = g + 32 * a;
-        if (ga < g1) {
-          load_group(p, ga, V, off, vec, x[a]);
-          if constexpr (kDraft) load_group(q, ga, V, off, vec, y[a]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < E; ++e) x[a][e] = 0.f;
-        }
-      }
-#pragma unroll
-      for (int a = 0; a < kAhead; ++a) {
-        float hi[E], lo[E];
-        group(x[a], y[a], g + 32 * a, hi, lo);
-#pragma unroll
-        for (int e = 0; e < E; ++e) add(s, hi[e], lo[e]);
-      }
+  // r of two words, added to two sums.
+  __device__ __forceinline__ void add_pair(uint64_t x, uint64_t y, uint64_t& s_hi, uint64_t& s_lo) const {
+    uint64_t d = x, t = 0;
+    if constexpr (kDraft) {
+      const uint64_t c = pack2(c_hi, c_hi), m = mul2(pack2(-c_hi, -c_hi), y);  // m: - c q
+      const uint64_t m_lo = fma2(pack2(c_lo, c_lo), y, fma2(c, y, m));
+      d = add2(x, m);
+      const uint64_t b = sub2(d, x);
+      t = sub2(sub2(sub2(x, sub2(d, b)), sub2(b, m)), m_lo);
     }
+    float d0, d1, t0, t1;
+    unpack2(d, d0, d1);
+    unpack2(t, t0, t1);
+    const bool some0 = d0 + t0 > 0.f, some1 = d1 + t1 > 0.f;  // NaN counts as nothing
+    d = pack2(some0 ? d0 : 0.f, some1 ? d1 : 0.f);
+    const uint64_t n = add2(s_hi, d), b = sub2(n, s_hi);
+    uint64_t e = add2(sub2(s_hi, sub2(n, b)), sub2(d, b));
+    if constexpr (kDraft) e = add2(e, pack2(some0 ? t0 : 0.f, some1 ? t1 : 0.f));
+    s_lo = add2(s_lo, e);
+    s_hi = n;
+  }
+
+  // The sum over groups [g0, g1), one warp; the same value in every lane.  mine: this thread's 16 bytes of the ring's first row.
+  __device__ __forceinline__ Sum sum(int32_t g0, int32_t g1, uint32_t mine) {
+    constexpr int E = kGroup<T>;
+    constexpr uint32_t kRow = kThreads * 16u;
+    const int32_t n = ceil_div(g1 - g0, 32), first = g0 + (int32_t)(threadIdx.x & 31);
+    range(g0, g1);
+    auto whole = [&](int32_t g) { return vec && g < g1 && g * E - off >= 0 && g * E - off + E <= V; };
+    auto load = [&](int32_t i) {
+      const int32_t g = first + 32 * i;
+      if (i < n && whole(g)) {
+        const uint32_t to = mine + (uint32_t)(i % kAhead) * (2 * kRow);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(p + (g * E - off)) : "memory");
+        if constexpr (kDraft)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + kRow), "l"(q + (g * E - off)) : "memory");
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    uint64_t s_hi = 0, s_lo = 0;
+#pragma unroll 1
+    for (int32_t i = 0; i < kAhead - 1; ++i) load(i);
+#pragma unroll 1
+    for (int32_t i = 0; i < n; ++i) {
+      load(i + kAhead - 1);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+      const int32_t g = first + 32 * i;
+      float x[E], y[E] = {};
+      if (whole(g)) {
+        const uint32_t from = mine + (uint32_t)(i % kAhead) * (2 * kRow);
+        widen(lds128u(from), x);
+        if constexpr (kDraft) widen(lds128u(from + kRow), y);
+      } else if (g < g1) {
+        load_group(p, g, V, off, vec, x);
+        if constexpr (kDraft) load_group(q, g, V, off, vec, y);
+      } else {
+        continue;
+      }
+      if constexpr (!kDraft) refuse(x, g);
+#pragma unroll
+      for (int e = 0; e < E; e += 2) add_pair(pack2(x[e], x[e + 1]), pack2(y[e], y[e + 1]), s_hi, s_lo);
+    }
+    Sum s, odd;
+    unpack2(s_hi, s.hi, odd.hi);
+    unpack2(s_lo, s.lo, odd.lo);
+    add(s, odd.hi, odd.lo);
     return warp_sum(s);
   }
 
   // The first word of groups [g0, g1) up to which the sum is over t; the last with r > 0 if rounding leaves none.
-  __device__ __forceinline__ int32_t find(int32_t g0, int32_t g1, Sum t) const {
+  __device__ __forceinline__ int32_t find(int32_t g0, int32_t g1, Sum t) {
     constexpr int E = kGroup<T>;
+    range(g0, g1);
     const int lane = threadIdx.x & 31;
     int32_t word = -1;
     for (int32_t gb = g0; gb < g1; gb += 32) {
@@ -264,7 +329,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) fd_verify_kernel(const Verify
   __shared__ Sum s_warp[kWarps], s_cta[2][kMaxCluster];
   __shared__ Order s_order;
   __shared__ Sum s_rest;
+  extern __shared__ __align__(16) uint8_t ring[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t own = smem_addr(ring) + (uint32_t)tid * 16u;
   uint32_t C;
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(C));
   const uint32_t rank = cluster_rank();
@@ -412,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) fd_verify_kernel(const Verify
     cta1 = min(groups, cta0 + per_cta);
     g0 = min(cta1, cta0 + warp * per_warp);
     g1 = min(cta1, g0 + per_warp);
-    const Sum mine = left.sum(g0, g1);
+    const Sum mine = left.sum(g0, g1, own);
     if (lane == 0) s_warp[warp] = mine;
     __syncthreads();
     buf ^= 1;
@@ -446,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) fd_verify_kernel(const Verify
     const int32_t h0 = min(cta1, cta0 + w * per_warp), h1 = min(cta1, h0 + per_warp);
     const int32_t per = ceil_div(h1 - h0, kWarps);
     const int32_t i0 = min(h1, h0 + warp * per), i1 = min(h1, i0 + per);
-    const Sum mine = left.sum(i0, i1);
+    const Sum mine = left.sum(i0, i1, own);
     if (lane == 0) s_warp[warp] = mine;
     __syncthreads();
     if (warp == 0) {
@@ -478,9 +545,12 @@ cudaError_t launch(const VerifyParams& v, cudaStream_t stream) {
   while (cluster < kMaxCluster && (int64_t)cluster * 1024 < v.V && 2 * (int64_t)v.B * cluster <= kCtas * (int64_t)sms)
     cluster *= 2;
   if ((int64_t)v.B * cluster > INT32_MAX) return cudaErrorInvalidValue;
+  e = allow_smem<fd_verify_kernel<T, kDraft>>(kRingBytes);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(v.B * cluster));
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kRingBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
