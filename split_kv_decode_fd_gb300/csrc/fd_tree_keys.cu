@@ -14,10 +14,11 @@
 // tile, 3100 cycles of its bandwidth.)  O is taken out of tensor memory every tile, since
 // the adds of the matrix unit drop bits.
 //
-// Bound by memory where the rows are few: with 32 rows 131072 keys stream at 6.4 to 6.7 TB/s; with 64 a tile takes 3060 cycles,
+// Bound by memory where the rows are few: with 32 rows 131072 keys stream at 6.4 to 6.7 TB/s; with 64 a tile takes some 2930 cycles,
 // S, softmax, P and O one after another through one place for P, against 2890 at an SM's share of the memory rate.  Measured: 64
-// rows, 131072 keys of 8 heads 99.6 us (5.4 TB/s); 64 paged sequences of 512 to 16384 tokens, 64 rows, 239 us (5.4 TB/s), of
-// which a piece's start and end are some 5 us each and a CTA has 4 of them.
+// rows, 131072 keys of 8 heads 95.6 us (5.6 TB/s; 99.4 with P's place given back as one, not the first two parts before the
+// third); 64 paged sequences of 512 to 16384 tokens, 64 rows, 238 us (5.4 TB/s), of
+// which a piece's start and end are some 5 us together and a CTA has 4 of them.
 //
 // A row's reference (what its scores are taken relative to) is the same for all keys, and moves only when a score of a
 // tile exceeds it by 2^kTau: a vote of the threads says so, and then the tile's maxima are found.
@@ -67,7 +68,7 @@ struct Misc {
   uint64_t q_full[2];                  // of even and odd pieces
   uint64_t s_full[2], s_empty[2], o_full, o_empty, moves_full[kMoves];
   uint64_t piece_full[2], piece_empty[2];
-  uint64_t p_full, p_empty, q_ready, fin_full, fin_empty, drain[2];
+  uint64_t p_full, p_empty[2], q_ready, fin_full, fin_empty, drain[2];
   uint32_t tmem;
   volatile int abort;
   TreePiece piece[2];
@@ -156,7 +157,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&s.o_full, 1);
     mbar_init(&s.o_empty, 4);
     mbar_init(&s.p_full, 8);
-    mbar_init(&s.p_empty, 1);
+    mbar_init(s.p_empty, 1);
+    mbar_init(s.p_empty + 1, 1);
     mbar_init(&s.q_ready, 8);
     mbar_init(&s.fin_full, 8);
     mbar_init(&s.fin_empty, 4);
@@ -318,12 +320,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < kKeys / 16; ++i)
               mma_ss(d, b_desc_rows(v + (uint32_t)i * 2048u, kTileBlock), b_desc_n<kKeys * 16>(p0 + (uint32_t)i * 256u), idO,
                      i != 0);
+            mma_commit(smem_addr(s.p_empty));  // the first two parts' places
 #pragma unroll
             for (int i = 0; i < kKeys / 16; ++i)
               mma_ss(d + N, b_desc_rows(v + (uint32_t)i * 2048u, kTileBlock),
                      b_desc_n<kKeys * 16>(p0 + 2 * Lay::kPPart + (uint32_t)i * 256u), idLast, 1);
             mma_commit(smem_addr(&s.o_full));
-            mma_commit(smem_addr(&s.p_empty));
+            mma_commit(smem_addr(s.p_empty + 1));
             mma_commit(smem_addr(s.v_empty + rv.slot));
           }
           __syncwarp();
@@ -503,15 +506,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < kParts; ++k) a[k][i] = part[k];
         }
-        // P's place is free once O of the tile before has read it
-        if (t > 0) w.on(&s.p_empty, (t - 1) & 1);
+        // P's places are free once O of the tile before has read them, the first two parts' before the third's
         const uint32_t to = sp + (uint32_t)(r0 / 8) * (kKeys * 16u) + (uint32_t)key * 16u;
 #pragma unroll
-        for (int k = 0; k < kParts; ++k)
+        for (int k = 0; k < kParts; ++k) {
+          if (k != 1 && t > 0) w.on(s.p_empty + k / 2, (t - 1) & 1);
 #pragma unroll
           for (int c = 0; c < kHalf / 8; ++c)
             sts128(to + (uint32_t)k * Lay::kPPart + (uint32_t)c * (kKeys * 16u), a[k][4 * c], a[k][4 * c + 1], a[k][4 * c + 2],
                    a[k][4 * c + 3]);
+        }
         if (some_hidden) {
           // V's rows at or past the length may hold anything, and so may those of the drafts, which not every
           // row sees: 0 * NaN is not 0.  Values that are no numbers become 0 here and are added to the rows that
