@@ -1088,7 +1088,8 @@ fd_status fd_decode_tree(const float* q, const fd_tree_desc* tree, const fd_kv_d
   int sms = 0;
   if (!sm_count(&sms)) return FD_ERR_CUDA;
   const bool f32 = kv->dtype == FD_F32;
-  const TreeSplit t = tree_split(Hq, Hkv, tree->n, D, f32, sms, (int64_t)B * Hkv * ceil_div(max_seq_len, kPlanTile));
+  const int tile = f32 ? kTreeTileCore : kPlanTile;
+  const TreeSplit t = tree_split(Hq, Hkv, tree->n, D, f32, sms, (int64_t)B * Hkv * ceil_div(max_seq_len, tile));
   const TreeLayout w = tree_layout(t, D);
   if (workspace_bytes < w.total) return FD_ERR_WORKSPACE_TOO_SMALL;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -1128,7 +1129,7 @@ fd_status fd_decode_tree(const float* q, const fd_tree_desc* tree, const fd_kv_d
     if (e != cudaSuccess) return FD_ERR_CUDA;
   }
   // a sequence of one tile lies within a share
-  if (t.ranges == 1 || max_seq_len <= kPlanTile) return FD_OK;
+  if (t.ranges == 1 || max_seq_len <= tile) return FD_OK;
   return launch_tree_join(D, t.block, p, s) == cudaSuccess ? FD_OK : FD_ERR_CUDA;
 }
 

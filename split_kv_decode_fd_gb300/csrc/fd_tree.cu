@@ -12,16 +12,16 @@
 // comes in under q . k, K's under p . V, and the other CTAs of the SM fill what is left.
 // Blocks of rows are made of tokens' rows alone and are pairs of their own in the shares: padding costs nothing.
 //
-// Measured: 6 sequences of 2099 to 3000 tokens, 12 heads on 4, D = 64, 2 to 10 tokens each: 32.9 us, of which the join has some 4,
+// Measured: 6 sequences of 2099 to 3000 tokens, 12 heads on 4, D = 64, 2 to 10 tokens each: 29.6 us, of which the join has some 4,
 // the start (walk, q, ancestors, first tile) 4 and a tile with three CTAs on the SM 5, where its 64 x 32 x 64 x 2 products could
-// take 1 at the rate of the fp32 units.  Two rows a thread, tiles loaded and then used, and padding's rows too: 58.
+// take 1 at the rate of the fp32 units (shares in tiles of 128 keys 33).  Two rows a thread, tiles loaded and then used, and padding's rows too: 58.
 #include "fd_tree.cuh"
 
 namespace fdk {
 namespace {
 
 constexpr int kRows = kTreeRowsCore;
-constexpr int kKeys = 64;
+constexpr int kKeys = kTreeTileCore;
 constexpr int kCoreThreads = 128;
 
 template <int D>

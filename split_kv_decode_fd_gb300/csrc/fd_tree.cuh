@@ -46,6 +46,8 @@ __device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
 // Cost units (kTileUnits = 4 a tile of 128 keys) that a piece costs a CTA besides its tiles: q and the first tile's way
 // through the roles, some 5 us or three tiles of 64 rows (64 paged sequences of 512 to 16384 tokens: 271 us with 6, 255 with 12).
 constexpr int kTreePieceUnits = 12;
+// The same of the fp32 kernel, in units of four a tile of 64 keys.
+constexpr int kTreePieceUnitsCore = 4;
 
 __device__ __forceinline__ int32_t tree_len(const TreeParams& p, int32_t b) {
   return p.seq_lens ? clamp_len(__ldg(p.seq_lens + b), p.max_len) : p.max_len;
@@ -144,6 +146,7 @@ __device__ __forceinline__ int32_t tree_blocks(const TreeParams& p, int32_t m) {
 // tokens of sequence base + l.
 template <int Packed>
 struct TreeWalk {
+  static constexpr int kTile = Packed > 0 ? kTreeTileCore : kPlanTile;
   const TreeParams& p;
   int64_t units;
   int32_t used, range;
@@ -155,9 +158,9 @@ struct TreeWalk {
   int32_t base, my_len, my_m;
 
   __device__ __forceinline__ bool uniform() const { return !p.seq_lens && !p.tree.new_lens; }
-  __device__ __forceinline__ int32_t piece_units() const { return p.seq_lens ? kTreePieceUnits : 0; }
+  __device__ __forceinline__ int32_t piece_units() const { return p.seq_lens ? (Packed > 0 ? kTreePieceUnitsCore : kTreePieceUnits) : 0; }
   __device__ __forceinline__ int32_t units_of(int32_t n, int32_t tokens) const {
-    return tokens > 0 ? (int32_t)pair_units(ceil_div(n, kPlanTile), piece_units()) : 0;
+    return tokens > 0 ? (int32_t)pair_units(ceil_div(n, kTile), piece_units()) : 0;
   }
   __device__ __forceinline__ void block(int32_t b0) {
     const int32_t i = b0 + (int32_t)(threadIdx.x & 31);
@@ -170,7 +173,7 @@ struct TreeWalk {
     b = bb;
     len = uniform() ? p.max_len : __shfl_sync(0xffffffffu, my_len, bb & 31);
     m = uniform() ? p.tree.n : __shfl_sync(0xffffffffu, my_m, bb & 31);
-    tiles = m > 0 ? ceil_div(len, kPlanTile) : 0;
+    tiles = m > 0 ? ceil_div(len, kTile) : 0;
     u = units_of(len, m);
     heads = p.Hkv * tree_blocks<Packed>(p, m);
   }
@@ -248,8 +251,8 @@ struct TreeWalk {
           pc.h = i / per;
           pc.sub = i % per;
         }
-        pc.begin = lo * kPlanTile;
-        pc.end = hi < tiles ? hi * kPlanTile : len;
+        pc.begin = lo * kTile;
+        pc.end = hi < tiles ? hi * kTile : len;
         pc.len = len;
         pc.m = m;
         pc.slot = lo == 0 && hi == tiles ? -1 : 2 * range + (lo == 0 ? 1 : 0);

@@ -76,7 +76,7 @@ struct TreeParams {
 // Rows per CTA and CTAs per SM: fp32 caches on CUDA cores; bf16 ones on tensor cores, up to 64 rows of a KV head with the
 // keys on the rows of the products, more in blocks of 128 with the query rows there.  Measured both ways, 131072 keys of 8
 // heads: 64 rows 100 us against 123 (64 paged sequences 238 against 287), 256 rows 334 us against 241.
-constexpr int kTreeRowsCore = 32;
+constexpr int kTreeRowsCore = 32, kTreeTileCore = 64;  // and keys of a tile
 constexpr int kTreeRowsMma = 128;
 constexpr int tree_rows(bool f32, int rows) { return f32 || rows <= 32 ? 32 : rows <= 64 ? 64 : kTreeRowsMma; }
 constexpr int tree_ctas(bool f32, int D) { return !f32 ? 1 : D == 64 ? 3 : 2; }
