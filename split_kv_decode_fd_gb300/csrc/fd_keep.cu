@@ -13,8 +13,8 @@
 // the last place that is written, as when the latest part of a sequence stays, no row is both read and written: the CTAs
 // of a (sequence, KV head) share the list and take whole rows.  Otherwise each takes the whole list
 // and a 32-byte slice of the rows, if there are fewer (sequence, KV head)s than SMs.
-// Measured, bf16, D = 128: the 5 rows of a step 1.7 us, 64 paths of up to 8 rows 4.4 us; 65536 rows of 8 heads 111 us (4.8 TB/s)
-// from behind what is written, 270 us (2.0 TB/s) where they overlap; 16 such lists of 4096 rows 97 us (5.5 TB/s).
+// Measured, bf16, D = 128: the 5 rows of a step 1.7 us, 64 paths of up to 8 rows 4.4 us; 65536 rows of 8 heads 99.8 us (5.4 TB/s)
+// from behind what is written, of which every CTA's look at the list is some 8, 250 us (2.1 TB/s) where they overlap; 16 such lists of 4096 rows 97 us (5.5 TB/s).
 #include "../../include/fdecode.h"
 #include "fd_tree.cuh"
 
@@ -196,30 +196,37 @@ __global__ void __launch_bounds__(kThreads) fd_keep_long_kernel(const KeepParams
   if (threadIdx.x == 0) s_stop = s_moves = count;
   __syncthreads();
   int32_t bad = count, moves = count;
+  const int64_t room = start < 0 ? 0 : (int64_t)p.max_len - start;  // entries from there on point past the end
   const int32_t lead = (int32_t)((reinterpret_cast<uintptr_t>(index) / 4) & 3);  // index - lead is at a 16-byte boundary
-  for (int64_t j0 = -lead; j0 < count; j0 += 4 * kScan * kThreads) {
-    int32_t at[kScan][4], before[kScan];
+  const int lane = threadIdx.x & 31;
+  for (int32_t j0 = -lead; j0 < count; j0 += 4 * kScan * kThreads) {
+    int4 at[kScan];
+    int32_t before[kScan];  // lane 0's first
 #pragma unroll
     for (int i = 0; i < kScan; ++i) {
-      const int64_t j = j0 + 4 * (i * kThreads + (int32_t)threadIdx.x);
-      before[i] = j > 0 && j < count ? __ldg(index + j - 1) : -1;
+      const int32_t j = j0 + 4 * (i * kThreads + (int32_t)threadIdx.x);
+      before[i] = lane == 0 && j > 0 && j < count ? __ldg(index + j - 1) : -1;
       if (j >= 0 && j + 4 <= count) {
-        const int4 w = __ldg(reinterpret_cast<const int4*>(index + j));
-        at[i][0] = w.x, at[i][1] = w.y, at[i][2] = w.z, at[i][3] = w.w;
+        at[i] = __ldg(reinterpret_cast<const int4*>(index + j));
       } else {
-#pragma unroll
-        for (int x = 0; x < 4; ++x) at[i][x] = j + x >= 0 && j + x < count ? __ldg(index + j + x) : -1;
+        auto one = [&](int32_t k) { return k >= 0 && k < count ? __ldg(index + k) : -1; };
+        at[i] = make_int4(one(j), one(j + 1), one(j + 2), one(j + 3));
       }
     }
 #pragma unroll
     for (int i = 0; i < kScan; ++i) {
-      const int64_t j = j0 + 4 * (i * kThreads + (int32_t)threadIdx.x);
+      const int32_t j = j0 + 4 * (i * kThreads + (int32_t)threadIdx.x);
+      const int4 a = at[i];
+      const int32_t up = __shfl_up_sync(0xffffffffu, a.w, 1), prev = lane == 0 ? before[i] : up;
+      const bool whole = j >= 0 && j + 4 <= count;
+      // four that rise, in range, and stay (as all before them do) or are behind one that moves: most are
+      if (whole && prev < a.x && a.x < a.y && a.y < a.z && a.z < a.w && a.w < room && (a.w == j + 3 || j >= moves)) continue;
+      const int32_t v[5] = {prev, a.x, a.y, a.z, a.w};
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         if (j + x < 0 || j + x >= count) continue;
-        const int32_t prev = x > 0 ? at[i][x > 0 ? x - 1 : 0] : before[i];
-        if (at[i][x] <= prev || prev < -1 || start < 0 || (int64_t)start + at[i][x] >= p.max_len) bad = min(bad, (int32_t)j + x);
-        if (at[i][x] != j + x) moves = min(moves, (int32_t)j + x);
+        if (v[x + 1] <= v[x] || v[x + 1] >= room) bad = min(bad, j + x);
+        if (v[x + 1] != j + x) moves = min(moves, j + x);
       }
     }
   }
