@@ -44,7 +44,7 @@ __device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
 }
 
 // Cost units (kTileUnits = 4 a tile of 128 keys) that a piece costs a CTA besides its tiles: q and the first tile's way
-// through the roles, some 5 us or three tiles of 64 rows (64 paged sequences of 512 to 16384 tokens: 271 us with 6, 255 with 12).
+// through the roles, some 4 us or three tiles of 64 rows (64 paged sequences of 512 to 16384 tokens: 252 us with 6, 226 with 12, 230 with 20).
 constexpr int kTreePieceUnits = 12;
 // The same of the fp32 kernel, in units of four a tile of 64 keys.
 constexpr int kTreePieceUnitsCore = 4;

@@ -17,8 +17,9 @@
 // Bound by memory where the rows are few: with 32 rows 131072 keys stream at 6.4 to 6.7 TB/s; with 64 a tile takes some 2930 cycles,
 // S, softmax, P and O one after another through one place for P, against 2890 at an SM's share of the memory rate.  Measured: 64
 // rows, 131072 keys of 8 heads 95.6 us (5.6 TB/s; 99.4 with P's place given back as one, not the first two parts before the
-// third); 64 paged sequences of 512 to 16384 tokens, 64 rows, 238 us (5.4 TB/s), of
-// which a piece's start and end are some 5 us together and a CTA has 4 of them.
+// third); 64 paged sequences of 512 to 16384 tokens, 64 rows, 227 us (5.7 TB/s), of
+// which a piece's start and end are some 4 us together and a CTA has 4 of them.  Code that a piece runs once is rolled: it comes from
+// behind the instruction cache (640 sequences of 512 tokens: 577 us with q's cut and the mask unrolled, 490 so).
 //
 // A row's reference (what its scores are taken relative to) is the same for all keys, and moves only when a score of a
 // tile exceeds it by 2^kTau: a vote of the threads says so, and then the tile's maxima are found.
@@ -372,18 +373,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int32_t row = tid % N;
         const uint32_t c0 = (uint32_t)(tid / N * kC);
         const uint32_t from = k_ring + uk % Lay::kK * kTile + (uint32_t)row * (D * 4);
-        uint4 x[kC];
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < kC; ++i) {  // a lane starts at a chunk of its own, off the others' banks
-          x[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (row < live) x[i] = lds128u(from + (c0 + (uint32_t)((i + lane) % kC)) * 16u);
-        }
-#pragma unroll
-        for (int i = 0; i < kC; ++i) {
           const uint32_t c = c0 + (uint32_t)((i + lane) % kC), c8 = c >> 1;  // c8: chunk of eight bf16
+          uint4 x = make_uint4(0u, 0u, 0u, 0u);
+          if (row < live) x = lds128u(from + c * 16u);
           uint32_t a[kParts], b[kParts];
-          cut3(__uint_as_float((x[i].x & keepq) ^ flip), __uint_as_float((x[i].y & keepq) ^ flip), a);
-          cut3(__uint_as_float((x[i].z & keepq) ^ flip), __uint_as_float((x[i].w & keepq) ^ flip), b);
+          cut3(__uint_as_float((x.x & keepq) ^ flip), __uint_as_float((x.y & keepq) ^ flip), a);
+          cut3(__uint_as_float((x.z & keepq) ^ flip), __uint_as_float((x.w & keepq) ^ flip), b);
           const uint32_t to = sq + (c8 >> 3) * Lay::kQBlock + (uint32_t)row * 128u + (((c8 ^ (uint32_t)row) & 7u) << 4) + (c & 1u) * 8u;
 #pragma unroll
           for (int part = 0; part < kParts; ++part) sts64(to + (uint32_t)part * Lay::kQPart, a[part], b[part]);
@@ -432,16 +429,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(s.s_empty + (t & 1));
         if (some_hidden) {
-          const int32_t a = t0 + key - P;  // the key's token
-          const bool drafted = a >= 0, none = a >= 64;
+          // the rows that see this key
+          const int32_t a = t0 + key - P;  // its token
+          uint32_t sees = a < 0 ? 0xffffffffu : 0u;
+          if (__any_sync(0xffffffffu, a >= 0 && a < 64)) {
+#pragma unroll 2
+            for (int i = 0; i < kHalf; ++i) {
+              const uint32_t low = __shfl_sync(0xffffffffu, (uint32_t)anc, i), high = __shfl_sync(0xffffffffu, (uint32_t)(anc >> 32), i);
+              if (a >= 0 && a < 64) sees |= ((a < 32 ? low : high) >> (a & 31) & 1u) << i;
+            }
+          }
 #pragma unroll
           for (int i = 0; i < kHalf; i += 2) {
             float x0, x1;
             unpack2(x[i / 2], x0, x1);
-            const uint64_t see0 = __shfl_sync(0xffffffffu, anc, i), see1 = __shfl_sync(0xffffffffu, anc, i + 1);
-            if (drafted && (none || !(see0 >> (a & 63) & 1))) x0 = -INFINITY;
-            if (drafted && (none || !(see1 >> (a & 63) & 1))) x1 = -INFINITY;
-            x[i / 2] = pack2(x0, x1);
+            x[i / 2] = pack2(sees >> i & 1 ? x0 : -INFINITY, sees >> (i + 1) & 1 ? x1 : -INFINITY);
           }
         }
         // relative to the references (kept with the other sign); a NaN does not vote
