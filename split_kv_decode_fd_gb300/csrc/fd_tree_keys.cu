@@ -41,6 +41,7 @@ constexpr int kThreads = 512, kRegs = 128;  // registers a thread at launch
 constexpr int kSoftmaxRegs = 136, kSumsRegs = 152, kOtherRegs = 88;
 static_assert(256 * kSoftmaxRegs + 128 * kSumsRegs + 128 * kOtherRegs == kThreads * kRegs, "shares");
 constexpr int kSums = 8, kCopyK = 12, kCopyV = 13, kSWarp = 14;  // first of the sums' warps; S, and O: 15
+constexpr uint32_t kMiscBytes = 3 * 1024;
 constexpr int kMoves = 4;              // tiles whose moves of the references are kept
 constexpr float kTau = 8.f;            // p stays below 2^kTau
 constexpr float kNoRef = -3.0e38f;     // the reference of a row that has seen no key
@@ -57,7 +58,7 @@ struct Layout {
   static constexpr uint32_t kK = D == 64 ? 4 : N == 32 ? 3 : 2, kV = D == 64 ? 4 : 2;  // slots
   static constexpr uint32_t kVRing = kRing + kK * kTile;
   static constexpr uint32_t kMisc = kVRing + kV * kTile;
-  static constexpr uint32_t kBytes = kMisc + 3072;
+  static constexpr uint32_t kBytes = kMisc + kMiscBytes;
   static_assert(kBytes <= 232448, "shared memory");
   static_assert(N * D * 4 <= kTile, "a slot holds the rows of q");
 };
@@ -126,7 +127,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using Lay = Layout<D, N>;
   constexpr uint32_t kTile = Lay::kTile;
   constexpr int kHalf = N / 2;  // rows of a softmax group
-  static_assert(sizeof(Misc<N>) <= 3072, "Misc");
+  static_assert(sizeof(Misc<N>) <= kMiscBytes, "Misc");
   extern __shared__ __align__(1024) uint8_t smem[];
   Misc<N>& s = *reinterpret_cast<Misc<N>*>(smem + Lay::kMisc);
   const uint32_t sq = smem_addr(smem), sp = sq + Lay::kP, k_ring = sq + Lay::kRing, v_ring = sq + Lay::kVRing;

@@ -10,7 +10,7 @@
 // numbers of eight bits each by truncation, which is exact, so all products are, and
 // fp32 sums are what rounds: S sums its small parts first, and O is taken out of
 // tensor memory every tile and added up in registers, since the adds of the matrix
-// unit drop bits.  Six products of 8 k-steps make 3072 cycles a tile of 128 channels, and a
+// unit drop bits.  Six products of 8 k-steps make some 3100 cycles a tile of 128 channels, and a
 // tile's 64 KB at an SM's share of the memory rate some 3000: the products bind.
 //
 // Measured: 256 rows a KV head on 131072 keys, 8 KV heads: 239 us, 1.72 PFLOP/s of exact products (the chip at its power limit, at
@@ -39,6 +39,7 @@ constexpr int kThreads = 384, kRegs = 168;  // registers a thread at launch
 constexpr int kMoreRegs = 208, kLessRegs = 88;  // of the softmax and the sums, and of the other roles
 static_assert(256 * kMoreRegs + 128 * kLessRegs == kThreads * kRegs, "shares");
 constexpr int kCopyK = 8, kCopyV = 9, kProducts = 10;
+constexpr uint32_t kMiscBytes = 3 * 1024;
 constexpr int kPBufs = 4;                // barriers of P and places for a tile's max
 // Tensor memory: two S / P buffers and O.  P takes 8 columns for each part of 16 keys, 192 in
 // all, and S the last 128 of them: a chunk of P never reaches an unread chunk of S.
@@ -56,7 +57,7 @@ struct Layout {
   static constexpr uint32_t kVRing = kRing + kK * kTile;
   static constexpr uint32_t kMisc = kVRing + kV * kTile;
   static constexpr uint32_t kQRowsPerSlot = kTile / (D * 4);  // fp32 rows of q
-  static constexpr uint32_t kBytes = kMisc + 3072;
+  static constexpr uint32_t kBytes = kMisc + kMiscBytes;
   static_assert(kBytes <= 232448, "shared memory");
 };
 
@@ -74,7 +75,7 @@ struct Misc {
   float l[kRows];         // a piece's sums
   uint64_t unfit[4];      // tokens whose values are not finite, as the softmax warps met them
 };
-static_assert(sizeof(Misc) <= 3072, "Misc");
+static_assert(sizeof(Misc) <= kMiscBytes, "Misc");
 
 // What does not fit the registers spills to L2, as shared memory leaves L1 nothing: 64 rows of 131072 keys took 8 heads
 // 316 us with 168 for every thread, 268 with 200 for those with much to hold, 241 with less code in the loops too.
