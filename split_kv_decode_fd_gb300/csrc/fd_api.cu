@@ -1120,7 +1120,7 @@ fd_status fd_decode_tree(const float* q, const fd_tree_desc* tree, const fd_kv_d
   p.stall_u = g_stall_it.load(std::memory_order_relaxed);
   cudaStream_t s = (cudaStream_t)stream;
   if (f32) {
-    if (launch_tree_core(D, p, s) != cudaSuccess) return FD_ERR_CUDA;
+    if (launch_tree_core(D, t.block, p, s) != cudaSuccess) return FD_ERR_CUDA;
   } else {
     CUtensorMap tk, tv;
     p.box_rows = tree_box_rows(p.kv.paged ? kv->page_size : 64);

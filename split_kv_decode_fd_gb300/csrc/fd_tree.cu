@@ -5,14 +5,14 @@
 //     out = sum_t exp(x_t - m) v_t / sum_t exp(x_t - m),   x_t = scale q . k_t,
 // over what it sees, with the running m and sum of an online softmax.
 //
-// A CTA of four warps serves 32 rows of a KV head from tiles of 64 keys in shared
-// memory; a thread has four rows, of which it takes four keys for q . k and D / 16
+// A CTA of four warps serves 32 rows of a KV head (16 where it has no more) from tiles of 64 keys in shared
+// memory; a thread has four rows (two), of which it takes four keys for q . k and D / 16
 // channels for p . V: sixteen products for eight values read, so that both keep the
 // arithmetic busy rather than shared memory.  K and V have one buffer each: V's next tile
 // comes in under q . k, K's under p . V, and the other CTAs of the SM fill what is left.
 // Blocks of rows are made of tokens' rows alone and are pairs of their own in the shares: padding costs nothing.
 //
-// Measured: 6 sequences of 2099 to 3000 tokens, 12 heads on 4, D = 64, 2 to 10 tokens each: 29.6 us, of which the join has some 4,
+// Measured: 6 sequences of 2099 to 3000 tokens, 12 heads on 4, D = 64, 2 to 10 tokens each: 28.6 us, of which the join has some 4,
 // the start (walk, q, ancestors, first tile) 4 and a tile with three CTAs on the SM 5, where its 64 x 32 x 64 x 2 products could
 // take 1 at the rate of the fp32 units (shares in tiles of 128 keys 33).  Two rows a thread, tiles loaded and then used, and padding's rows too: 58.
 #include "fd_tree.cuh"
@@ -20,12 +20,13 @@
 namespace fdk {
 namespace {
 
-constexpr int kRows = kTreeRowsCore;
 constexpr int kKeys = kTreeTileCore;
 constexpr int kCoreThreads = 128;
 
-template <int D>
+// R: rows a thread has, of those of its half warp; 8 R a CTA.
+template <int D, int R>
 struct CoreSmem {
+  static constexpr int kRows = 8 * R;
   static constexpr int kStride = D + 4;     // rows of q and k: eight rows in a row of banks
   static constexpr int kPStride = kRows + 4;
   float q[kRows * kStride];
@@ -82,9 +83,10 @@ __device__ __forceinline__ int32_t tree_row(const TreeParams& p, int32_t m, int3
   return i / m * p.tree.n + (p.tree.n - m) + i % m;
 }
 
-template <int D>
+template <int D, int R>
 __global__ void __launch_bounds__(kCoreThreads, tree_ctas(true, D)) fd_tree_core_kernel(const TreeParams p) {
-  using S = CoreSmem<D>;
+  using S = CoreSmem<D, R>;
+  constexpr int kRows = S::kRows;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   S& s = *reinterpret_cast<S*>(smem_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -122,12 +124,12 @@ __global__ void __launch_bounds__(kCoreThreads, tree_ctas(true, D)) fd_tree_core
     copy_tile<D, D>(p, pc, p.kv.v, pc.begin, to_v);
     const int32_t P = pc.len - pc.m;
     const Ancestors all = tree_ancestors(p.tree, pc.b, pc.m, p.err);
-    uint64_t anc[4];
-    float mx[4], l[4];
-    uint64_t o[4][kCols][2];  // pairs of channels
+    uint64_t anc[R];
+    float mx[R], l[R];
+    uint64_t o[R][kCols][2];  // pairs of channels
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      anc[i] = all.of((first + 4 * ty + i) % pc.m);
+    for (int i = 0; i < R; ++i) {
+      anc[i] = all.of((first + R * ty + i) % pc.m);
       mx[i] = -INFINITY;
       l[i] = 0.f;
 #pragma unroll
@@ -137,33 +139,32 @@ __global__ void __launch_bounds__(kCoreThreads, tree_ctas(true, D)) fd_tree_core
       cp_async_wait_older();
       __syncthreads();  // K's tile is there
       // q . k of rows 4 ty .. 4 ty + 3 and keys tx, tx + 16, tx + 32, tx + 48
-      uint64_t y[4][4] = {};  // sums of the even and of the odd channels
+      uint64_t y[R][4] = {};  // sums of the even and of the odd channels
 #pragma unroll 4
       for (int c = 0; c < D; c += 4) {
-        ulonglong2 a[4], k[4];
+        ulonglong2 a[R], k[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const ulonglong2*>(s.q + (4 * ty + i) * S::kStride + c);
+        for (int i = 0; i < R; ++i) a[i] = *reinterpret_cast<const ulonglong2*>(s.q + (R * ty + i) * S::kStride + c);
 #pragma unroll
         for (int j = 0; j < 4; ++j) k[j] = *reinterpret_cast<const ulonglong2*>(s.k + (tx + 16 * j) * S::kStride + c);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < R; ++i)
 #pragma unroll
           for (int j = 0; j < 4; ++j) y[i][j] = fma2(a[i].y, k[j].y, fma2(a[i].x, k[j].x, y[i][j]));
       }
       __syncthreads();  // K's tile is read
       copy_tile<D, S::kStride>(p, pc, p.kv.k, t0 + kKeys, to_k);
-      uint32_t w[4][2];  // what the rows see of the tile
-      bool all_seen = true;
-      float x[4][4];
+      const bool some_hidden = t0 + kKeys > P;
+      uint32_t w[R][2];  // what the rows see of the tile
+      float x[R][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < R; ++i) {
         w[i][0] = w[i][1] = 0xffffffffu;
-        if (t0 + kKeys > P) {
+        if (some_hidden) {
           const TileMask mask = tile_mask(P, anc[i], t0);
           w[i][0] = mask.w[0];
           w[i][1] = mask.w[1];
         }
-        all_seen = all_seen && (w[i][0] & w[i][1]) == 0xffffffffu;
         float top = -INFINITY;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -193,36 +194,62 @@ __global__ void __launch_bounds__(kCoreThreads, tree_ctas(true, D)) fd_tree_core
         }
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        *reinterpret_cast<float4*>(s.p + (tx + 16 * j) * S::kPStride + 4 * ty) = make_float4(x[0][j], x[1][j], x[2][j], x[3][j]);
+      for (int j = 0; j < 4; ++j) {
+        float* at = s.p + (tx + 16 * j) * S::kPStride + R * ty;
+        if constexpr (R == 4)
+          *reinterpret_cast<float4*>(at) = make_float4(x[0][j], x[1][j], x[2][j], x[3][j]);
+        else
+          *reinterpret_cast<float2*>(at) = make_float2(x[0][j], x[1][j]);
+      }
       cp_async_wait_older();
       __syncthreads();  // V's tile is there, and the weights
-      if (__all_sync(0xffffffffu, all_seen)) {
+      auto weights = [&](int t, uint64_t (&weight)[R]) {  // those of this thread's rows for key t
+        const float* at = s.p + t * S::kPStride + R * ty;
+        if constexpr (R == 4) {
+          const float4 e = *reinterpret_cast<const float4*>(at);
+          weight[0] = pack2(e.x, e.x), weight[1] = pack2(e.y, e.y), weight[2] = pack2(e.z, e.z), weight[3] = pack2(e.w, e.w);
+        } else {
+          const float2 e = *reinterpret_cast<const float2*>(at);
+          weight[0] = pack2(e.x, e.x), weight[1] = pack2(e.y, e.y);
+        }
+      };
+      // A value that a row does not see may be anything, and 0 * NaN is not 0: drafts whose values are no numbers take
+      // the second form.  (With that for every tile with drafts, 26 short sequences of 880 rows a head took 396 us in
+      // place of 329.)
+      bool odd = false;
+      if (some_hidden) {
+        const int32_t first = P > t0 ? P - t0 : 0, end = pc.end - t0 < kKeys ? pc.end - t0 : kKeys;
+        for (int32_t i = first * (D / 4) + tid; i < end * (D / 4); i += kCoreThreads) {
+          const float4 v = *reinterpret_cast<const float4*>(s.v + 4 * i);
+          odd = odd || !(fabsf(v.x) < INFINITY && fabsf(v.y) < INFINITY && fabsf(v.z) < INFINITY && fabsf(v.w) < INFINITY);
+        }
+        odd = __syncthreads_or(odd);
+      }
+      if (!odd) {
 #pragma unroll 4
         for (int t = 0; t < kKeys; ++t) {
-          const float4 e = *reinterpret_cast<const float4*>(s.p + t * S::kPStride + 4 * ty);
-          const uint64_t weight[4] = {pack2(e.x, e.x), pack2(e.y, e.y), pack2(e.z, e.z), pack2(e.w, e.w)};
+          uint64_t weight[R];
+          weights(t, weight);
 #pragma unroll
           for (int c = 0; c < kCols; ++c) {
             const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(s.v + t * D + 64 * c + 4 * tx);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < R; ++i) {
               o[i][c][0] = fma2(weight[i], v.x, o[i][c][0]);
               o[i][c][1] = fma2(weight[i], v.y, o[i][c][1]);
             }
           }
         }
       } else {
-        // a value that a row does not see may be anything: 0 * NaN is not 0
-#pragma unroll 2
+#pragma unroll 1
         for (int t = 0; t < kKeys; ++t) {
-          const float4 e = *reinterpret_cast<const float4*>(s.p + t * S::kPStride + 4 * ty);
-          const uint64_t weight[4] = {pack2(e.x, e.x), pack2(e.y, e.y), pack2(e.z, e.z), pack2(e.w, e.w)};
+          uint64_t weight[R];
+          weights(t, weight);
 #pragma unroll
           for (int c = 0; c < kCols; ++c) {
             const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(s.v + t * D + 64 * c + 4 * tx);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < R; ++i) {
               const bool seen = (t < 32 ? w[i][0] : w[i][1]) >> (t & 31) & 1u;
               o[i][c][0] = fma2(weight[i], seen ? v.x : 0, o[i][c][0]);
               o[i][c][1] = fma2(weight[i], seen ? v.y : 0, o[i][c][1]);
@@ -234,10 +261,10 @@ __global__ void __launch_bounds__(kCoreThreads, tree_ctas(true, D)) fd_tree_core
       copy_tile<D, D>(p, pc, p.kv.v, t0 + kKeys, to_v);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < R; ++i) {
 #pragma unroll
       for (int d = 8; d > 0; d >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
-      const int r = 4 * ty + i;
+      const int r = R * ty + i;
       if (r >= rows) continue;
       const int64_t row = row0 + tree_row(p, pc.m, first + r);
       const int64_t state = (int64_t)pc.slot * kRows + r;
@@ -341,11 +368,12 @@ __global__ void __launch_bounds__(256, 4) fd_tree_join_kernel(const TreeParams p
   if (p.lse && lane == 0) p.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * kTreeLn2;
 }
 
-template <int D>
+template <int D, int R>
 cudaError_t launch_core(const TreeParams& p, cudaStream_t stream) {
-  const cudaError_t e = allow_smem<fd_tree_core_kernel<D>>((int)sizeof(CoreSmem<D>));
+  using S = CoreSmem<D, R>;
+  const cudaError_t e = allow_smem<fd_tree_core_kernel<D, R>>((int)sizeof(S));
   if (e != cudaSuccess) return e;
-  return launch_early(fd_tree_core_kernel<D>, (unsigned)(p.ranges * p.nsub), kCoreThreads, sizeof(CoreSmem<D>), stream, p);
+  return launch_early(fd_tree_core_kernel<D, R>, (unsigned)(p.ranges * p.nsub), kCoreThreads, sizeof(S), stream, p);
 }
 
 template <int D, int Rows>
@@ -355,18 +383,22 @@ cudaError_t launch_join(const TreeParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_tree_core(int D, const TreeParams& p, cudaStream_t stream) {
-  if (D == 128) return launch_core<128>(p, stream);
-  if (D == 64) return launch_core<64>(p, stream);
+cudaError_t launch_tree_core(int D, int rows, const TreeParams& p, cudaStream_t stream) {
+  if (D == 128 && rows == 16) return launch_core<128, 2>(p, stream);
+  if (D == 128 && rows == 32) return launch_core<128, 4>(p, stream);
+  if (D == 64 && rows == 16) return launch_core<64, 2>(p, stream);
+  if (D == 64 && rows == 32) return launch_core<64, 4>(p, stream);
   return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_tree_join(int D, int rows, const TreeParams& p, cudaStream_t stream) {
   if (D == 128) {
+    if (rows == 16) return launch_join<128, 16>(p, stream);
     if (rows == 32) return launch_join<128, 32>(p, stream);
     if (rows == 64) return launch_join<128, 64>(p, stream);
     if (rows == 128) return launch_join<128, 128>(p, stream);
   } else if (D == 64) {
+    if (rows == 16) return launch_join<64, 16>(p, stream);
     if (rows == 32) return launch_join<64, 32>(p, stream);
     if (rows == 64) return launch_join<64, 64>(p, stream);
     if (rows == 128) return launch_join<64, 128>(p, stream);

@@ -75,15 +75,19 @@ struct TreeParams {
 
 // Rows per CTA and CTAs per SM: fp32 caches on CUDA cores; bf16 ones on tensor cores, up to 64 rows of a KV head with the
 // keys on the rows of the products, more in blocks of 128 with the query rows there.  Measured both ways, 131072 keys of 8
-// heads: 64 rows 100 us against 123 (64 paged sequences 238 against 287), 256 rows 334 us against 241.
-constexpr int kTreeRowsCore = 32, kTreeTileCore = 64;  // and keys of a tile
+// heads: 64 rows 100 us against 123 (64 paged sequences 238 against 287), 256 rows 334 us against 241.  fp32, 10 rows of 16 KV
+// heads on 2751 to 5502 keys, D = 128: blocks of 16 rows 53 us, of 32 61.
+constexpr int kTreeTileCore = 64;  // keys of a tile of the fp32 kernel
 constexpr int kTreeRowsMma = 128;
-constexpr int tree_rows(bool f32, int rows) { return f32 || rows <= 32 ? 32 : rows <= 64 ? 64 : kTreeRowsMma; }
+constexpr int tree_rows(bool f32, int rows) {
+  if (f32) return rows <= 16 ? 16 : 32;
+  return rows <= 32 ? 32 : rows <= 64 ? 64 : kTreeRowsMma;
+}
 constexpr int tree_ctas(bool f32, int D) { return !f32 ? 1 : D == 64 ? 3 : 2; }
 // Rows of a copy: as many of 64, 32, 16 as lie in a page.  A copy takes a warp some 100 cycles to start.
 constexpr int tree_box_rows(int page) { return page % 64 == 0 ? 64 : page % 32 == 0 ? 32 : 16; }
 
-cudaError_t launch_tree_core(int D, const TreeParams& p, cudaStream_t stream);
+cudaError_t launch_tree_core(int D, int rows, const TreeParams& p, cudaStream_t stream);
 cudaError_t launch_tree_mma(int D, const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p,
                             cudaStream_t stream);
 cudaError_t launch_tree_keys(int D, int rows, const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p,
