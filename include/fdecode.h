@@ -577,8 +577,7 @@ FD_API int64_t fd_plan_pieces(int32_t B, int32_t Hq, int32_t Hkv, int32_t kv_dty
  * kernels launched afterwards skip, in every CTA that reaches it, the copies of
  * stage number `stage` (split kernels: fd_decode and every call built on it,
  * fd_split_partial; fd_decode_kv4) or K/V tile copy number `stage` (fd_prefill, K and V
- * counted separately), or use number `stage` of K's slots (fd_decode_tree over a bf16 cache, where a
- * piece's first use brings q and is not skipped), so the waits for it run out; wait_limit_ns > 0 shortens
+ * counted separately), so the waits for it run out; wait_limit_ns > 0 shortens
  * every wait of those kernels to that many nanoseconds (0 keeps the default).  The
  * call's output is then undefined and fd_workspace_status (or
  * fd_static_status) reports FD_ERR_TIMEOUT; the workspace stays valid for the

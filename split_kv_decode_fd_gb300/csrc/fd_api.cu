@@ -1116,8 +1116,6 @@ fd_status fd_decode_tree(const float* q, const fd_tree_desc* tree, const fd_kv_d
   p.packed = f32;
   p.max_len = max_seq_len;
   p.qk_scale = (float)((double)scale * 1.4426950408889634);
-  p.wait_ns = (uint64_t)g_wait_ns.load(std::memory_order_relaxed);
-  p.stall_u = g_stall_it.load(std::memory_order_relaxed);
   cudaStream_t s = (cudaStream_t)stream;
   if (f32) {
     if (launch_tree_core(D, t.block, p, s) != cudaSuccess) return FD_ERR_CUDA;

@@ -69,8 +69,6 @@ struct TreeParams {
   int32_t max_len;
   int32_t box_rows;            // rows that a copy of K or V brings (bf16 caches)
   float qk_scale;              // scale * log2(e)
-  uint64_t wait_ns;            // limit of every wait (0: the default)
-  int32_t stall_u;             // testing hook: the copy that every CTA skips, or -1
 };
 
 // Rows per CTA and CTAs per SM: fp32 caches on CUDA cores; bf16 ones on tensor cores, up to 64 rows of a KV head with the

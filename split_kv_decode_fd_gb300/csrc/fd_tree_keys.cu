@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Tensor memory: two buffers of S^T of 3 N columns (with one, K's slot waited for the softmax), then O^T, 2 N columns.
   const uint32_t tmem = s.tmem;
   pdl_wait();
-  Waits w{&s.abort, p.wait_ns ? (unsigned long long)p.wait_ns : kWaitLimitNs};
+  Waits w{&s.abort, kWaitLimitNs};
 
   // The next piece, for a warp; false at the end.
   auto take = [&](uint32_t e, TreePiece& pc) -> bool {
@@ -190,165 +190,162 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   const TileCopy copy(p);
 
-  if (warp == kCopyK) {
-    give_registers();
-    // ------------------------------------------------------------ pieces, q, K
-    uint32_t u = 0, f = 0, skipped = 0xffffffffu;
-    Ring<Lay::kK> r;
-    TreeWalk<0> walk(p, range);
-    for (uint32_t e = 0;; ++e) {
-      TreePiece pc;
-      if (!walk.next(pc)) pc.b = -1;
-      if (e >= 2) w.on(s.piece_empty + (e & 1), ((e >> 1) - 1) & 1);
-      if (!w.all()) break;
-      if (lane == 0) {
-        s.piece[e & 1] = pc;
-        mbar_arrive(s.piece_full + (e & 1));
-      }
-      if (pc.b < 0) break;
-      const int32_t n = ceil_div(pc.end - pc.begin, kKeys);
-      int32_t page = copy.page_of(pc, 0);
-      w.on(s.k_empty + r.slot, r.phase ^ 1u);
-      if (!w.all()) break;
-      // The rows of q lie side by side.  They have barriers of their own, as the softmax waits for them without
-      // having waited for the slot's other uses; two, as q of the next piece may come before the softmax looks (not
-      // that of the one after: no ring has five slots).
-      if (lane == 0) {
-        mbar_arrive_expect_tx(s.q_full + (e & 1), (uint32_t)live * D * 4);
-        bulk_load(smem + Lay::kRing + r.slot * kTile, p.q + (((int64_t)pc.b * p.Hkv + pc.h) * p.rows + row0) * D,
-                  (uint32_t)live * D * 4, s.q_full + (e & 1));
-        mbar_arrive(s.k_full + r.slot);
-      }
-      __syncwarp();
-      ++f;
-      ++u;
-      r.next();
-      for (int32_t j = 0; j < n; ++j, ++u, r.next()) {
-        const int32_t next = copy.page_of(pc, j + 1);
+  if (warp >= kCopyK) {
+    give_registers();  // a warpgroup at one place, as the instruction wants it
+    if (warp == kCopyK) {
+      // ------------------------------------------------------------ pieces, q, K
+      uint32_t u = 0, f = 0;
+      Ring<Lay::kK> r;
+      TreeWalk<0> walk(p, range);
+      for (uint32_t e = 0;; ++e) {
+        TreePiece pc;
+        if (!walk.next(pc)) pc.b = -1;
+        if (e >= 2) w.on(s.piece_empty + (e & 1), ((e >> 1) - 1) & 1);
+        if (!w.all()) break;
+        if (lane == 0) {
+          s.piece[e & 1] = pc;
+          mbar_arrive(s.piece_full + (e & 1));
+        }
+        if (pc.b < 0) break;
+        const int32_t n = ceil_div(pc.end - pc.begin, kKeys);
+        int32_t page = copy.page_of(pc, 0);
         w.on(s.k_empty + r.slot, r.phase ^ 1u);
         if (!w.all()) break;
-        if (p.stall_u >= 0 && u == (uint32_t)p.stall_u)
-          skipped = u;  // testing hook
-        else
-          copy.start<Lay::kNB>(&tmap_k, pc, j, page, smem + Lay::kRing + r.slot * kTile, s.k_full + r.slot);
-        page = next;
-        if (j == 0 && lane == 0 && sub == 0) walk.say(pc);
-      }
-      if (!w.ok) break;
-    }
-    if (!w.ok) {
-      s.abort = 1;
-      if (lane == 0) {
-        atomicOr(p.err, kErrTimeout);
-        land(s.k_full, u, Lay::kK, skipped, w.limit);
-        for (uint32_t e = f > 2 ? f - 2 : 0; e < f; ++e) mbar_wait_for(s.q_full + (e & 1), (e >> 1) & 1, w.limit);
-      }
-    }
-  } else if (warp == kCopyV) {
-    give_registers();
-    // ------------------------------------------------------------ V
-    uint32_t u = 0;
-    Ring<Lay::kV> r;
-    TreePiece pc;
-    for (uint32_t e = 0; take(e, pc); ++e) {
-      const int32_t n = ceil_div(pc.end - pc.begin, kKeys);
-      int32_t page = copy.page_of(pc, 0);
-      for (int32_t j = 0; j < n; ++j, ++u, r.next()) {
-        const int32_t next = copy.page_of(pc, j + 1);
-        w.on(s.v_empty + r.slot, r.phase ^ 1u);
-        if (!w.all()) break;
-        copy.start<Lay::kNB>(&tmap_v, pc, j, page, smem + Lay::kVRing + r.slot * kTile, s.v_full + r.slot);
-        page = next;
-      }
-      if (!w.ok) break;
-    }
-    if (!w.ok) {
-      s.abort = 1;
-      if (lane == 0) {
-        atomicOr(p.err, kErrTimeout);
-        land(s.v_full, u, Lay::kV, 0xffffffffu, w.limit);
-      }
-    }
-  } else if (warp >= kSWarp) {
-    give_registers();
-    // ------------------------------------------------------------ products
-    // Every branch and operand is uniform over the warp as the compiler sees it (votes and shuffles), so that the
-    // products take their operands from uniform registers as they are.
-    constexpr uint32_t idS = bf16_instr_desc(kKeys, kParts * N), idO = bf16_instr_desc(D, 2 * N, true) | kAlongRows,
-                       idLast = bf16_instr_desc(D, N, true) | kAlongRows;
-    const uint32_t base = uniform(tmem), q0 = uniform(sq), p0 = uniform(sp), k0 = uniform(k_ring), v0 = uniform(v_ring);
-    const bool is_s = uniform((uint32_t)warp) == kSWarp;
-    Ring<Lay::kK> rk;
-    Ring<Lay::kV> rv;
-    uint32_t g = 0, f = 0;  // tiles and pieces so far
-    TreePiece pc;
-    for (uint32_t e = 0; take(e, pc); ++e) {
-      const uint32_t n = uniform((uint32_t)ceil_div(pc.end - pc.begin, kKeys));
-      if (is_s) {
-        w.on(&s.q_ready, f & 1);
-        if (!w.all()) break;
-        if (elect_one()) mbar_arrive(s.k_empty + rk.slot);  // the slot that q came in
+        // The rows of q lie side by side.  They have barriers of their own, as the softmax waits for them without
+        // having waited for the slot's other uses; two, as q of the next piece may come before the softmax looks (not
+        // that of the one after: no ring has five slots).
+        if (lane == 0) {
+          mbar_arrive_expect_tx(s.q_full + (e & 1), (uint32_t)live * D * 4);
+          bulk_load(smem + Lay::kRing + r.slot * kTile, p.q + (((int64_t)pc.b * p.Hkv + pc.h) * p.rows + row0) * D,
+                    (uint32_t)live * D * 4, s.q_full + (e & 1));
+          mbar_arrive(s.k_full + r.slot);
+        }
         __syncwarp();
-        rk.next();
-        for (uint32_t j = 0; j < n; ++j, rk.next()) {
-          const uint32_t t = g + j;
-          w.on(s.k_full + rk.slot, rk.phase);
-          if (t >= 2) w.on(s.s_empty + (t & 1), ((t - 2) >> 1) & 1);
+        ++f;
+        ++u;
+        r.next();
+        for (int32_t j = 0; j < n; ++j, ++u, r.next()) {
+          const int32_t next = copy.page_of(pc, j + 1);
+          w.on(s.k_empty + r.slot, r.phase ^ 1u);
           if (!w.all()) break;
-          tmem_fence_after();
-          if (elect_one()) {
-            const uint32_t d = base + (t & 1) * (kParts * N), k = k0 + rk.slot * kTile;
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-              const uint32_t block = (uint32_t)(i >> 2), off = (uint32_t)(i & 3) * 32u;
-              mma_ss(d, b_desc(k + block * kTileBlock + off), b_desc(q0 + block * Lay::kQBlock + off), idS, i != 0);
-            }
-            mma_commit(smem_addr(s.s_full + (t & 1)));
-            mma_commit(smem_addr(s.k_empty + rk.slot));
-          }
-          __syncwarp();
+          copy.start<Lay::kNB>(&tmap_k, pc, j, page, smem + Lay::kRing + r.slot * kTile, s.k_full + r.slot);
+          page = next;
+          if (j == 0 && lane == 0 && sub == 0) walk.say(pc);
         }
-      } else {
-        for (uint32_t j = 0; j < n; ++j, rv.next()) {
-          const uint32_t t = g + j;
-          w.on(s.v_full + rv.slot, rv.phase);
-          w.on(&s.p_full, t & 1);
-          if (t > 0) w.on(&s.o_empty, (t - 1) & 1);
-          if (!w.all()) break;
-          tmem_fence_after();
-          if (elect_one()) {
-            const uint32_t d = base + 2 * kParts * N, v = v0 + rv.slot * kTile;
-#pragma unroll
-            for (int i = 0; i < kKeys / 16; ++i)
-              mma_ss(d, b_desc_rows(v + (uint32_t)i * 2048u, kTileBlock), b_desc_n<kKeys * 16>(p0 + (uint32_t)i * 256u), idO,
-                     i != 0);
-            mma_commit(smem_addr(s.p_empty));  // the first two parts' places
-#pragma unroll
-            for (int i = 0; i < kKeys / 16; ++i)
-              mma_ss(d + N, b_desc_rows(v + (uint32_t)i * 2048u, kTileBlock),
-                     b_desc_n<kKeys * 16>(p0 + 2 * Lay::kPPart + (uint32_t)i * 256u), idLast, 1);
-            mma_commit(smem_addr(&s.o_full));
-            mma_commit(smem_addr(s.p_empty + 1));
-            mma_commit(smem_addr(s.v_empty + rv.slot));
-          }
-          __syncwarp();
+        if (!w.ok) break;
+      }
+      if (!w.ok) {
+        s.abort = 1;
+        if (lane == 0) {
+          atomicOr(p.err, kErrTimeout);
+          land(s.k_full, u, Lay::kK, w.limit);
+          for (uint32_t e = f > 2 ? f - 2 : 0; e < f; ++e) mbar_wait_for(s.q_full + (e & 1), (e >> 1) & 1, w.limit);
         }
       }
-      if (!w.ok) break;
-      g += n;
-      ++f;
+    } else if (warp == kCopyV) {
+      // ------------------------------------------------------------ V
+      uint32_t u = 0;
+      Ring<Lay::kV> r;
+      TreePiece pc;
+      for (uint32_t e = 0; take(e, pc); ++e) {
+        const int32_t n = ceil_div(pc.end - pc.begin, kKeys);
+        int32_t page = copy.page_of(pc, 0);
+        for (int32_t j = 0; j < n; ++j, ++u, r.next()) {
+          const int32_t next = copy.page_of(pc, j + 1);
+          w.on(s.v_empty + r.slot, r.phase ^ 1u);
+          if (!w.all()) break;
+          copy.start<Lay::kNB>(&tmap_v, pc, j, page, smem + Lay::kVRing + r.slot * kTile, s.v_full + r.slot);
+          page = next;
+        }
+        if (!w.ok) break;
+      }
+      if (!w.ok) {
+        s.abort = 1;
+        if (lane == 0) {
+          atomicOr(p.err, kErrTimeout);
+          land(s.v_full, u, Lay::kV, w.limit);
+        }
+      }
+    } else {
+      // ------------------------------------------------------------ products
+      // Every branch and operand is uniform over the warp as the compiler sees it (votes and shuffles), so that the
+      // products take their operands from uniform registers as they are.
+      constexpr uint32_t idS = bf16_instr_desc(kKeys, kParts * N), idO = bf16_instr_desc(D, 2 * N, true) | kAlongRows,
+                         idLast = bf16_instr_desc(D, N, true) | kAlongRows;
+      const uint32_t base = uniform(tmem), q0 = uniform(sq), p0 = uniform(sp), k0 = uniform(k_ring), v0 = uniform(v_ring);
+      const bool is_s = uniform((uint32_t)warp) == kSWarp;
+      Ring<Lay::kK> rk;
+      Ring<Lay::kV> rv;
+      uint32_t g = 0, f = 0;  // tiles and pieces so far
+      TreePiece pc;
+      for (uint32_t e = 0; take(e, pc); ++e) {
+        const uint32_t n = uniform((uint32_t)ceil_div(pc.end - pc.begin, kKeys));
+        if (is_s) {
+          w.on(&s.q_ready, f & 1);
+          if (!w.all()) break;
+          if (elect_one()) mbar_arrive(s.k_empty + rk.slot);  // the slot that q came in
+          __syncwarp();
+          rk.next();
+          for (uint32_t j = 0; j < n; ++j, rk.next()) {
+            const uint32_t t = g + j;
+            w.on(s.k_full + rk.slot, rk.phase);
+            if (t >= 2) w.on(s.s_empty + (t & 1), ((t - 2) >> 1) & 1);
+            if (!w.all()) break;
+            tmem_fence_after();
+            if (elect_one()) {
+              const uint32_t d = base + (t & 1) * (kParts * N), k = k0 + rk.slot * kTile;
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) {
+                const uint32_t block = (uint32_t)(i >> 2), off = (uint32_t)(i & 3) * 32u;
+                mma_ss(d, b_desc(k + block * kTileBlock + off), b_desc(q0 + block * Lay::kQBlock + off), idS, i != 0);
+              }
+              mma_commit(smem_addr(s.s_full + (t & 1)));
+              mma_commit(smem_addr(s.k_empty + rk.slot));
+            }
+            __syncwarp();
+          }
+        } else {
+          for (uint32_t j = 0; j < n; ++j, rv.next()) {
+            const uint32_t t = g + j;
+            w.on(s.v_full + rv.slot, rv.phase);
+            w.on(&s.p_full, t & 1);
+            if (t > 0) w.on(&s.o_empty, (t - 1) & 1);
+            if (!w.all()) break;
+            tmem_fence_after();
+            if (elect_one()) {
+              const uint32_t d = base + 2 * kParts * N, v = v0 + rv.slot * kTile;
+#pragma unroll
+              for (int i = 0; i < kKeys / 16; ++i)
+                mma_ss(d, b_desc_rows(v + (uint32_t)i * 2048u, kTileBlock), b_desc_n<kKeys * 16>(p0 + (uint32_t)i * 256u), idO,
+                       i != 0);
+              mma_commit(smem_addr(s.p_empty));  // the first two parts' places
+#pragma unroll
+              for (int i = 0; i < kKeys / 16; ++i)
+                mma_ss(d + N, b_desc_rows(v + (uint32_t)i * 2048u, kTileBlock),
+                       b_desc_n<kKeys * 16>(p0 + 2 * Lay::kPPart + (uint32_t)i * 256u), idLast, 1);
+              mma_commit(smem_addr(&s.o_full));
+              mma_commit(smem_addr(s.p_empty + 1));
+              mma_commit(smem_addr(s.v_empty + rv.slot));
+            }
+            __syncwarp();
+          }
+        }
+        if (!w.ok) break;
+        g += n;
+        ++f;
+      }
+      if (!w.ok) {
+        s.abort = 1;
+        atomicOr(p.err, kErrTimeout);
+      }
+      // every product has completed before tensor memory is given back
+      if (elect_one()) {
+        uint64_t* done = s.drain + (is_s ? 0 : 1);
+        mma_commit(smem_addr(done));
+        if (!mbar_wait_for(done, 0, w.limit)) atomicOr(p.err, kErrTimeout);
+      }
+      __syncwarp();
     }
-    if (!w.ok) {
-      s.abort = 1;
-      atomicOr(p.err, kErrTimeout);
-    }
-    // every product has completed before tensor memory is given back
-    if (elect_one()) {
-      uint64_t* done = s.drain + (is_s ? 0 : 1);
-      mma_commit(smem_addr(done));
-      if (!mbar_wait_for(done, 0, w.limit)) atomicOr(p.err, kErrTimeout);
-    }
-    __syncwarp();
   } else if (warp < kSums) {
     take_registers<kSoftmaxRegs>();
     // ------------------------------------------------------------ softmax
@@ -634,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < 8; ++i) unfit |= s.unfit[i];
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.fin_empty);
-      if (unfit) {
+      if (w.all() && unfit) {  // (of a piece that was given up it may be anything)
         const Ancestors all = tree_ancestors(p.tree, pc.b, pc.m, p.err);
         uint64_t anc[N / 32];
 #pragma unroll

@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tmem_fence_after();
   const uint32_t tmem = s.tmem;
   pdl_wait();
-  Waits w{&s.abort, p.wait_ns ? (unsigned long long)p.wait_ns : kWaitLimitNs};
+  Waits w{&s.abort, kWaitLimitNs};
 
   // The next piece, for a warp; false at the end.
   auto take = [&](uint32_t e, TreePiece& pc) -> bool {
@@ -167,163 +167,160 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   };
-  auto leave = [&](uint64_t* full, uint32_t u, uint32_t n, uint32_t skipped, uint32_t i, uint32_t f) {
+  auto leave = [&](uint64_t* full, uint32_t u, uint32_t n, uint32_t i, uint32_t f) {
     if (w.ok) return;
     s.abort = 1;
     if (lane != 0) return;
     atomicOr(p.err, kErrTimeout);
-    land(full, u, n, skipped, w.limit);
+    land(full, u, n, w.limit);
     for (uint32_t e = f > 2 ? f - 2 : 0; e < f; ++e) mbar_wait_for(&s.q_full[e & 1][i], (e >> 1) & 1, w.limit);
   };
 
-  if (warp == kCopyK) {
-    give_registers();
-    // ------------------------------------------------------------ pieces, q, K
-    uint32_t u = 0, f = 0, skipped = 0xffffffffu;
-    Ring<Lay::kK> r;
-    TreeWalk<0> walk(p, range);
-    for (uint32_t e = 0;; ++e) {
-      TreePiece pc;
-      if (!walk.next(pc)) pc.b = -1;
-      if (e >= 2) w.on(s.piece_empty + (e & 1), ((e >> 1) - 1) & 1);
-      if (!w.all()) break;
-      if (lane == 0) {
-        s.piece[e & 1] = pc;
-        mbar_arrive(s.piece_full + (e & 1));
-        if (pc.b >= 0 && sub == 0) walk.say(pc);
-      }
-      if (pc.b < 0) break;
-      const int32_t n = ceil_div(pc.end - pc.begin, kKeys);
-      int32_t page = copy.page_of(pc, 0);
-      w.on(s.k_empty + r.slot, r.phase ^ 1u);
-      if (!w.all()) break;
-      copy_q(pc, e, 0, smem + Lay::kRing + r.slot * kTile, s.k_full + r.slot);
-      ++f;
-      ++u;
-      r.next();
-      for (int32_t j = 0; j < n; ++j, ++u, r.next()) {
-        const int32_t next = copy.page_of(pc, j + 1);
+  if (warp >= kCopyK) {
+    give_registers();  // a warpgroup at one place, as the instruction wants it
+    if (warp == kCopyK) {
+      // ------------------------------------------------------------ pieces, q, K
+      uint32_t u = 0, f = 0;
+      Ring<Lay::kK> r;
+      TreeWalk<0> walk(p, range);
+      for (uint32_t e = 0;; ++e) {
+        TreePiece pc;
+        if (!walk.next(pc)) pc.b = -1;
+        if (e >= 2) w.on(s.piece_empty + (e & 1), ((e >> 1) - 1) & 1);
+        if (!w.all()) break;
+        if (lane == 0) {
+          s.piece[e & 1] = pc;
+          mbar_arrive(s.piece_full + (e & 1));
+          if (pc.b >= 0 && sub == 0) walk.say(pc);
+        }
+        if (pc.b < 0) break;
+        const int32_t n = ceil_div(pc.end - pc.begin, kKeys);
+        int32_t page = copy.page_of(pc, 0);
         w.on(s.k_empty + r.slot, r.phase ^ 1u);
         if (!w.all()) break;
-        if (p.stall_u >= 0 && u == (uint32_t)p.stall_u)
-          skipped = u;  // testing hook
-        else
-          copy.start<Lay::kNB>(&tmap_k, pc, j, page, smem + Lay::kRing + r.slot * kTile, s.k_full + r.slot);
-        page = next;
-      }
-      if (!w.ok) break;
-    }
-    leave(s.k_full, u, Lay::kK, skipped, 0, f);
-  } else if (warp == kCopyV) {
-    give_registers();
-    // ------------------------------------------------------------ q, V
-    uint32_t u = 0, f = 0;
-    Ring<Lay::kV> r;
-    TreePiece pc;
-    for (uint32_t e = 0; take(e, pc); ++e) {
-      const int32_t n = ceil_div(pc.end - pc.begin, kKeys);
-      int32_t page = copy.page_of(pc, 0);
-      if (nq == 2) {
-        w.on(s.v_empty + r.slot, r.phase ^ 1u);
-        if (!w.all()) break;
-        copy_q(pc, e, 1, smem + Lay::kVRing + r.slot * kTile, s.v_full + r.slot);
+        copy_q(pc, e, 0, smem + Lay::kRing + r.slot * kTile, s.k_full + r.slot);
         ++f;
         ++u;
         r.next();
+        for (int32_t j = 0; j < n; ++j, ++u, r.next()) {
+          const int32_t next = copy.page_of(pc, j + 1);
+          w.on(s.k_empty + r.slot, r.phase ^ 1u);
+          if (!w.all()) break;
+          copy.start<Lay::kNB>(&tmap_k, pc, j, page, smem + Lay::kRing + r.slot * kTile, s.k_full + r.slot);
+          page = next;
+        }
+        if (!w.ok) break;
       }
-      for (int32_t j = 0; j < n; ++j, ++u, r.next()) {
-        const int32_t next = copy.page_of(pc, j + 1);
-        w.on(s.v_empty + r.slot, r.phase ^ 1u);
+      leave(s.k_full, u, Lay::kK, 0, f);
+    } else if (warp == kCopyV) {
+      // ------------------------------------------------------------ q, V
+      uint32_t u = 0, f = 0;
+      Ring<Lay::kV> r;
+      TreePiece pc;
+      for (uint32_t e = 0; take(e, pc); ++e) {
+        const int32_t n = ceil_div(pc.end - pc.begin, kKeys);
+        int32_t page = copy.page_of(pc, 0);
+        if (nq == 2) {
+          w.on(s.v_empty + r.slot, r.phase ^ 1u);
+          if (!w.all()) break;
+          copy_q(pc, e, 1, smem + Lay::kVRing + r.slot * kTile, s.v_full + r.slot);
+          ++f;
+          ++u;
+          r.next();
+        }
+        for (int32_t j = 0; j < n; ++j, ++u, r.next()) {
+          const int32_t next = copy.page_of(pc, j + 1);
+          w.on(s.v_empty + r.slot, r.phase ^ 1u);
+          if (!w.all()) break;
+          copy.start<Lay::kNB>(&tmap_v, pc, j, page, smem + Lay::kVRing + r.slot * kTile, s.v_full + r.slot);
+          page = next;
+        }
+        if (!w.ok) break;
+      }
+      leave(s.v_full, u, Lay::kV, 1, f);
+    } else if (warp == kProducts) {
+      // ------------------------------------------------------------ products
+      // Every branch and operand is uniform over the warp as the compiler sees it (votes and shuffles), so that the
+      // products take their operands from uniform registers as they are.
+      constexpr uint32_t idS = bf16_instr_desc(kRows, kKeys), idO = bf16_instr_desc(kRows, D, true);
+      const uint32_t base = uniform(tmem), q0 = uniform(sq), k0 = uniform(k_ring), v0 = uniform(v_ring);
+      Ring<Lay::kK> rk;
+      Ring<Lay::kV> rv;
+      uint32_t g = 0, f = 0;  // tiles and pieces so far
+      TreePiece pc;
+      for (uint32_t e = 0; take(e, pc); ++e) {
+        const uint32_t n = uniform((uint32_t)ceil_div(pc.end - pc.begin, kKeys));
+        w.on(&s.q_ready, f & 1);
         if (!w.all()) break;
-        copy.start<Lay::kNB>(&tmap_v, pc, j, page, smem + Lay::kVRing + r.slot * kTile, s.v_full + r.slot);
-        page = next;
+        if (elect_one()) {  // the slots that q came in
+          mbar_arrive(s.k_empty + rk.slot);
+          if (nq == 2) mbar_arrive(s.v_empty + rv.slot);
+        }
+        __syncwarp();
+        rk.next();
+        if (nq == 2) rv.next();
+        for (uint32_t j = 0; j <= n; ++j) {
+          if (j < n) {
+            const uint32_t t = g + j;
+            w.on(s.k_full + rk.slot, rk.phase);
+            if (!w.all()) break;
+            tmem_fence_after();
+            if (elect_one()) {
+              const uint32_t d = base + (t & 1) * kBuf + kSOff, k = k0 + rk.slot * kTile;
+#pragma unroll 1
+              for (int part = kParts - 1; part >= 0; --part) {
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                  const uint32_t block = (uint32_t)(i >> 2), off = (uint32_t)(i & 3) * 32u;
+                  mma_ss(d, b_desc(q0 + (uint32_t)part * Lay::kQPart + block * Lay::kQBlock + off),
+                         b_desc(k + block * kBlock + off), idS, part != kParts - 1 || i != 0);
+                }
+              }
+              mma_commit(smem_addr(s.s_full + (t & 1)));
+              mma_commit(smem_addr(s.k_empty + rk.slot));
+            }
+            __syncwarp();
+            rk.next();
+          }
+          if (j > 0) {
+            const uint32_t t = g + j - 1;
+            w.on(s.v_full + rv.slot, rv.phase);
+            w.on(s.p_full + t % kPBufs, (t / kPBufs) & 1);
+            if (t > 0) w.on(s.o_empty + ((t - 1) & 1), ((t - 1) >> 1) & 1);
+            if (!w.all()) break;
+            tmem_fence_after();
+            if (elect_one()) {
+              const uint32_t a = base + (t & 1) * kBuf, v = v0 + rv.slot * kTile;
+#pragma unroll 1
+              for (int part = kParts - 1; part >= 0; --part) {
+#pragma unroll
+                for (int i = 0; i < kKeys / 16; ++i)
+                  mma_ts(base + kOCol, a + (uint32_t)i * (8u * kParts) + (uint32_t)part * 8u,
+                         b_desc_rows(v + (uint32_t)i * 2048u, kBlock), idO, part != kParts - 1 || i != 0);
+              }
+              mma_commit(smem_addr(&s.o_full));
+              mma_commit(smem_addr(s.p_empty + (t & 1)));
+              mma_commit(smem_addr(s.v_empty + rv.slot));
+            }
+            __syncwarp();
+            rv.next();
+          }
+        }
+        if (!w.ok) break;
+        g += n;
+        ++f;
       }
-      if (!w.ok) break;
-    }
-    leave(s.v_full, u, Lay::kV, 0xffffffffu, 1, f);
-  } else if (warp == kProducts) {
-    give_registers();
-    // ------------------------------------------------------------ products
-    // Every branch and operand is uniform over the warp as the compiler sees it (votes and shuffles), so that the
-    // products take their operands from uniform registers as they are.
-    constexpr uint32_t idS = bf16_instr_desc(kRows, kKeys), idO = bf16_instr_desc(kRows, D, true);
-    const uint32_t base = uniform(tmem), q0 = uniform(sq), k0 = uniform(k_ring), v0 = uniform(v_ring);
-    Ring<Lay::kK> rk;
-    Ring<Lay::kV> rv;
-    uint32_t g = 0, f = 0;  // tiles and pieces so far
-    TreePiece pc;
-    for (uint32_t e = 0; take(e, pc); ++e) {
-      const uint32_t n = uniform((uint32_t)ceil_div(pc.end - pc.begin, kKeys));
-      w.on(&s.q_ready, f & 1);
-      if (!w.all()) break;
-      if (elect_one()) {  // the slots that q came in
-        mbar_arrive(s.k_empty + rk.slot);
-        if (nq == 2) mbar_arrive(s.v_empty + rv.slot);
+      if (!w.ok) {
+        s.abort = 1;
+        atomicOr(p.err, kErrTimeout);
+      }
+      // every product has completed before tensor memory is given back
+      if (elect_one()) {
+        mma_commit(smem_addr(&s.drain));
+        if (!mbar_wait_for(&s.drain, 0, w.limit)) atomicOr(p.err, kErrTimeout);
       }
       __syncwarp();
-      rk.next();
-      if (nq == 2) rv.next();
-      for (uint32_t j = 0; j <= n; ++j) {
-        if (j < n) {
-          const uint32_t t = g + j;
-          w.on(s.k_full + rk.slot, rk.phase);
-          if (!w.all()) break;
-          tmem_fence_after();
-          if (elect_one()) {
-            const uint32_t d = base + (t & 1) * kBuf + kSOff, k = k0 + rk.slot * kTile;
-#pragma unroll 1
-            for (int part = kParts - 1; part >= 0; --part) {
-#pragma unroll
-              for (int i = 0; i < D / 16; ++i) {
-                const uint32_t block = (uint32_t)(i >> 2), off = (uint32_t)(i & 3) * 32u;
-                mma_ss(d, b_desc(q0 + (uint32_t)part * Lay::kQPart + block * Lay::kQBlock + off),
-                       b_desc(k + block * kBlock + off), idS, part != kParts - 1 || i != 0);
-              }
-            }
-            mma_commit(smem_addr(s.s_full + (t & 1)));
-            mma_commit(smem_addr(s.k_empty + rk.slot));
-          }
-          __syncwarp();
-          rk.next();
-        }
-        if (j > 0) {
-          const uint32_t t = g + j - 1;
-          w.on(s.v_full + rv.slot, rv.phase);
-          w.on(s.p_full + t % kPBufs, (t / kPBufs) & 1);
-          if (t > 0) w.on(s.o_empty + ((t - 1) & 1), ((t - 1) >> 1) & 1);
-          if (!w.all()) break;
-          tmem_fence_after();
-          if (elect_one()) {
-            const uint32_t a = base + (t & 1) * kBuf, v = v0 + rv.slot * kTile;
-#pragma unroll 1
-            for (int part = kParts - 1; part >= 0; --part) {
-#pragma unroll
-              for (int i = 0; i < kKeys / 16; ++i)
-                mma_ts(base + kOCol, a + (uint32_t)i * (8u * kParts) + (uint32_t)part * 8u,
-                       b_desc_rows(v + (uint32_t)i * 2048u, kBlock), idO, part != kParts - 1 || i != 0);
-            }
-            mma_commit(smem_addr(&s.o_full));
-            mma_commit(smem_addr(s.p_empty + (t & 1)));
-            mma_commit(smem_addr(s.v_empty + rv.slot));
-          }
-          __syncwarp();
-          rv.next();
-        }
-      }
-      if (!w.ok) break;
-      g += n;
-      ++f;
     }
-    if (!w.ok) {
-      s.abort = 1;
-      atomicOr(p.err, kErrTimeout);
-    }
-    // every product has completed before tensor memory is given back
-    if (elect_one()) {
-      mma_commit(smem_addr(&s.drain));
-      if (!mbar_wait_for(&s.drain, 0, w.limit)) atomicOr(p.err, kErrTimeout);
-    }
-    __syncwarp();
   } else if (warp < 4) {
     take_registers();
     if (warp < (int)warps) {
@@ -534,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float o[D];
 #pragma unroll
       for (int i = 0; i < D / 2; ++i) unpack2(acc[i], o[2 * i], o[2 * i + 1]);
-      if (unfit) {
+      if (w.all() && unfit) {  // (of a piece that was given up it may be anything)
         const Ancestors all = tree_ancestors(p.tree, pc.b, pc.m, p.err);
         unfit &= all.of((row0 + row) % p.tree.n - (p.tree.n - pc.m));
         while (unfit) {
@@ -580,8 +577,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       atomicOr(p.err, kErrTimeout);
     }
     }
-  } else {
-    give_registers();
   }
   tmem_fence_before();
   cta_sync();

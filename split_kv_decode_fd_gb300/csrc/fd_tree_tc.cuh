@@ -133,12 +133,10 @@ struct TileCopy {
   }
 };
 
-// Waits, in a CTA that gives up, for the last use of each of a ring's n slots (u uses so far; use `skipped` was not
-// started), so that it does not leave while a copy may still be landing.  At the end of the work the products have
+// Waits, in a CTA that gives up, for the last use of each of a ring's n slots (u uses so far), so that it does not leave while a copy may still be landing.  At the end of the work the products have
 // waited for every copy.
-__device__ __forceinline__ void land(uint64_t* full, uint32_t u, uint32_t n, uint32_t skipped, unsigned long long limit) {
-  for (uint32_t x = u > n ? u - n : 0; x < u; ++x)
-    if (x != skipped) mbar_wait_for(full + x % n, (x / n) & 1, limit);
+__device__ __forceinline__ void land(uint64_t* full, uint32_t u, uint32_t n, unsigned long long limit) {
+  for (uint32_t x = u > n ? u - n : 0; x < u; ++x) mbar_wait_for(full + x % n, (x / n) & 1, limit);
 }
 
 }  // namespace fdk
