@@ -73,7 +73,7 @@ struct TreeParams {
 
 // Rows per CTA and CTAs per SM: fp32 caches on CUDA cores; bf16 ones on tensor cores, up to 64 rows of a KV head with the
 // keys on the rows of the products, more in blocks of 128 with the query rows there.  Measured both ways, 131072 keys of 8
-// heads: 64 rows 100 us against 123 (64 paged sequences 238 against 287), 256 rows 334 us against 241.  fp32, 10 rows of 16 KV
+// heads: 64 rows 100 us against 123 (64 paged sequences 238 against 287), 256 rows 334 us against 250.  fp32, 10 rows of 16 KV
 // heads on 2751 to 5502 keys, D = 128: blocks of 16 rows 53 us, of 32 61.
 constexpr int kTreeTileCore = 64;  // keys of a tile of the fp32 kernel
 constexpr int kTreeRowsMma = 128;

@@ -13,7 +13,7 @@
 // unit drop bits.  Six products of 8 k-steps make some 3100 cycles a tile of 128 channels, and a
 // tile's 64 KB at an SM's share of the memory rate some 3000: the products bind.
 //
-// Measured: 256 rows a KV head on 131072 keys, 8 KV heads: 239 us, 1.72 PFLOP/s of exact products (the chip at its power limit, at
+// Measured: 256 rows a KV head on 131072 keys, 8 KV heads: 250 us, 1.65 PFLOP/s of exact products (the chip at its power limit, at
 // 1.87 GHz; a long run of large bf16 matrix products in a library reaches 1.73).
 //
 // Eleven warps:
@@ -36,7 +36,7 @@ namespace {
 constexpr int kRows = kTreeRowsMma;
 constexpr int kKeys = kPlanTile;
 constexpr int kThreads = 384, kRegs = 168;  // registers a thread at launch
-constexpr int kMoreRegs = 208, kLessRegs = 88;  // of the softmax and the sums, and of the other roles
+constexpr int kMoreRegs = 200, kLessRegs = 104;  // of the softmax and the sums, and of the other roles
 static_assert(256 * kMoreRegs + 128 * kLessRegs == kThreads * kRegs, "shares");
 constexpr int kCopyK = 8, kCopyV = 9, kProducts = 10;
 constexpr uint32_t kMiscBytes = 3 * 1024;
@@ -78,7 +78,7 @@ struct Misc {
 static_assert(sizeof(Misc) <= kMiscBytes, "Misc");
 
 // What does not fit the registers spills to L2, as shared memory leaves L1 nothing: 64 rows of 131072 keys took 8 heads
-// 316 us with 168 for every thread, 268 with 200 for those with much to hold, 241 with less code in the loops too.
+// 316 us with 168 for every thread, 268 with 200 for those with much to hold, 250 with less code in the loops and S read twice.
 __device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kMoreRegs)); }
 __device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLessRegs)); }
 
@@ -377,38 +377,56 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t at = tmem + buf * kBuf + lanes;
         w.on(s.s_full + buf, (t >> 1) & 1);
         tmem_fence_after();
-        float x[kKeys];
-        {
-          uint32_t* xr = reinterpret_cast<uint32_t*>(x);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) TmemRow<32>::load(at + kSOff + 32u * c, xr + 32 * c);
-          tmem_wait_loads();
-#pragma unroll
-          for (int c = 0; c < 4; ++c) TmemRow<32>::tie(xr + 32 * c);
-        }
-        if (t0 + kKeys > P) {
-          const TileMask mask = tile_mask(P, anc, t0);
-#pragma unroll
-          for (int c = 0; c < kKeys; ++c) x[c] = mask.w[c >> 5] >> (c & 31) & 1u ? x[c] : -INFINITY;
-        }
+        const bool some_hidden = t0 + kKeys > P;
+        TileMask mask;
+        if (some_hidden) mask = tile_mask(P, anc, t0);
+        // S twice: for its maximum, and for P a chunk at a time (held in registers it took all of them, 255 us for 250)
         float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          float x[64];
+          uint32_t* xr = reinterpret_cast<uint32_t*>(x);
+          TmemRow<32>::load(at + kSOff + 64u * h, xr);
+          TmemRow<32>::load(at + kSOff + 64u * h + 32u, xr + 32);
+          tmem_wait_loads();
+          TmemRow<32>::tie(xr);
+          TmemRow<32>::tie(xr + 32);
+          if (some_hidden) {
+            const uint32_t w0 = h ? mask.w[2] : mask.w[0], w1 = h ? mask.w[3] : mask.w[1];
 #pragma unroll
-        for (int c = 0; c < kKeys; c += 8)
+            for (int c = 0; c < 64; ++c) x[c] = (c < 32 ? w0 : w1) >> (c & 31) & 1u ? x[c] : -INFINITY;
+          }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) top4[i] = max3(top4[i], x[c + 2 * i], x[c + 2 * i + 1]);
+          for (int c = 0; c < 64; c += 8)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top4[i] = max3(top4[i], x[c + 2 * i], x[c + 2 * i + 1]);
+        }
         const float top = max3(fmaxf(top4[0], top4[1]), top4[2], top4[3]);
         const float mn = fmaxf(m, top == -INFINITY ? -INFINITY : top * f);
         const float alpha = m == mn ? 1.f : ex2(m - mn);  // 0 from -inf
         const float base = mn == -INFINITY ? 0.f : mn;
         const uint64_t base2 = pack2(-base, -base);
         uint64_t sum2[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
-#pragma unroll
+        uint32_t next[16];
+        TmemRow<16>::load(at + kSOff, next);
+#pragma unroll 2
         for (int c = 0; c < kKeys / 16; ++c) {
+          uint32_t x[16];
+          tmem_wait_loads();
+          TmemRow<16>::tie(next);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] = next[i];
+          if (c + 1 < kKeys / 16) TmemRow<16>::load(at + kSOff + 16u * (c + 1), next);
+          if (some_hidden) {
+            const uint32_t two = c < 4 ? (c < 2 ? mask.w[0] : mask.w[1]) : (c < 6 ? mask.w[2] : mask.w[3]), w16 = two >> (16 * (c & 1));
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = w16 >> i & 1u ? x[i] : 0xff800000u;
+          }
           uint32_t a[8 * kParts];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             float y0, y1;
-            unpack2(fma2(pack2(x[16 * c + 2 * i], x[16 * c + 2 * i + 1]), f2, base2), y0, y1);
+            unpack2(fma2(pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), f2, base2), y0, y1);
             y0 = ex2(y0);
             y1 = ex2(y1);
             sum2[i & 1] = add2(sum2[i & 1], pack2(y0, y1));
