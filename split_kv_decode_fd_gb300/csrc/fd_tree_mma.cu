@@ -16,7 +16,7 @@
 // Measured: 256 rows a KV head on 131072 keys, 8 KV heads: 250 us, 1.65 PFLOP/s of exact products (the chip at its power limit, at
 // 1.87 GHz; a long run of large bf16 matrix products in a library reaches 1.73).
 //
-// Eleven warps:
+// Twelve warps:
 //   0-3  softmax, thread = row: reads S, masks, keeps the running max and sum, writes P
 //        over S; cuts q at the start of a piece.
 //   4-7  sums, thread = row: O of each tile times what the max has moved by; writes the
@@ -28,6 +28,7 @@
 //        a warp each (with copies of 16 rows by one warp a tile took 4300 cycles);
 //   10   products, one thread: S of the next tile, then O of this one.  While the softmax of a tile runs, the tensor
 //        core has the S of the next and the O of the one before.  (With a warp for S and one for O, 8 % slower.)
+//   11   nothing: registers are given back by four warps together.
 #include "fd_tree_tc.cuh"
 
 namespace fdk {
