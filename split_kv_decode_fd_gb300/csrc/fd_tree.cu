@@ -97,8 +97,9 @@ __global__ void __launch_bounds__(kCoreThreads, tree_ctas(true, D)) fd_tree_core
   const uint32_t to_q = smem_addr(s.q), to_k = smem_addr(s.k), to_v = smem_addr(s.v);
   pdl_launch_dependents();
   pdl_wait();
-  tree_no_rows<D, kRows, kRows>(p, range, 0, tid, kCoreThreads);  // thread 0 also says what its pieces leave to join
+  tree_no_rows<D, kRows, kRows>(p, range, 0, tid, kCoreThreads);
   TreeWalk<kRows> walk(p, range, warp == 0);
+  if (tid == 0) walk.say_none();
   for (;;) {
     if (warp == 0) {
       TreePiece pc;

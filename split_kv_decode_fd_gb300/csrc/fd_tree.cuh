@@ -278,7 +278,12 @@ struct TreeWalk {
     return false;
   }
 
-  // Says of the pair that `pc` begins (if it does) whether it goes on, for the join; one lane.
+  // Before the first piece: the share begins no pair that goes on, for the join.  One lane, the one that says what its pieces
+  // leave: it writes the same entry, and nothing else orders the two stores.
+  __device__ __forceinline__ void say_none() const {
+    if (!p.join_pairs) p.joins[range].b = -1;
+  }
+  // Says of the pair that `pc` begins (if it does) whether it goes on.
   __device__ __forceinline__ void say(const TreePiece& pc) const {
     if (pc.begin != 0 || (pc.slot < 0 && !p.join_pairs)) return;
     TreeJoin j{-1, pc.h, pc.sub, range, range};
@@ -291,10 +296,10 @@ struct TreeWalk {
 };
 
 // Sequences without keys or tokens: no share holds them.  The rows of their tokens get
-// out = 0, lse = -inf, and their pairs nothing to join, from the CTAs of share b % ranges.
+// out = 0, lse = -inf, and their pairs nothing to join, from the CTAs of share b % ranges.  (Entries of pairs alone, which no
+// piece has: an entry of a share is written by the walk.)
 template <int D, int Rows, int Packed>
 __device__ __forceinline__ void tree_no_rows(const TreeParams& p, int32_t range, int32_t sub, int tid, int threads) {
-  if (!p.join_pairs && sub == 0 && tid == 0) p.joins[range].b = -1;
   for (int32_t b = range; b < p.B; b += p.ranges) {
     const int32_t len = tree_len(p, b), m = tree_tokens(p.tree, b);
     if (p.join_pairs && sub == 0) {

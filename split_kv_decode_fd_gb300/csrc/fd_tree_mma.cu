@@ -184,6 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t u = 0, f = 0;
       Ring<Lay::kK> r;
       TreeWalk<0> walk(p, range);
+      if (lane == 0 && sub == 0) walk.say_none();
       for (uint32_t e = 0;; ++e) {
         TreePiece pc;
         if (!walk.next(pc)) pc.b = -1;
