@@ -237,11 +237,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!w.ok) {
         s.abort = 1;
-        if (lane == 0) {
-          atomicOr(p.err, kErrTimeout);
-          land(s.k_full, u, Lay::kK, w.limit);
-          for (uint32_t e = f > 2 ? f - 2 : 0; e < f; ++e) mbar_wait_for(s.q_full + (e & 1), (e >> 1) & 1, w.limit);
-        }
+        atomicOr(p.err, kErrTimeout);
+      }
+      if (lane == 0) {
+        land(s.k_full, u, Lay::kK, w.limit);
+        for (uint32_t e = f > 2 ? f - 2 : 0; e < f; ++e) mbar_wait_for(s.q_full + (e & 1), (e >> 1) & 1, w.limit);
       }
     } else if (warp == kCopyV) {
       // ------------------------------------------------------------ V
@@ -262,11 +262,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!w.ok) {
         s.abort = 1;
-        if (lane == 0) {
-          atomicOr(p.err, kErrTimeout);
-          land(s.v_full, u, Lay::kV, w.limit);
-        }
+        atomicOr(p.err, kErrTimeout);
       }
+      if (lane == 0) land(s.v_full, u, Lay::kV, w.limit);
     } else {
       // ------------------------------------------------------------ products
       // Every branch and operand is uniform over the warp as the compiler sees it (votes and shuffles), so that the

@@ -169,10 +169,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   };
   auto leave = [&](uint64_t* full, uint32_t u, uint32_t n, uint32_t i, uint32_t f) {
-    if (w.ok) return;
-    s.abort = 1;
+    if (!w.ok) {
+      s.abort = 1;
+      atomicOr(p.err, kErrTimeout);
+    }
     if (lane != 0) return;
-    atomicOr(p.err, kErrTimeout);
     land(full, u, n, w.limit);
     for (uint32_t e = f > 2 ? f - 2 : 0; e < f; ++e) mbar_wait_for(&s.q_full[e & 1][i], (e >> 1) & 1, w.limit);
   };

@@ -133,8 +133,9 @@ struct TileCopy {
   }
 };
 
-// Waits, in a CTA that gives up, for the last use of each of a ring's n slots (u uses so far), so that it does not leave while a copy may still be landing.  At the end of the work the products have
-// waited for every copy.
+// Waits for the last use of each of a ring's n slots (u uses so far), so that the CTA does not leave while a copy may still be
+// landing.  A warp that copies does so at its end in any case: the products wait for every copy, but another role may give up
+// after this warp has ended well.
 __device__ __forceinline__ void land(uint64_t* full, uint32_t u, uint32_t n, unsigned long long limit) {
   for (uint32_t x = u > n ? u - n : 0; x < u; ++x) mbar_wait_for(full + x % n, (x / n) & 1, limit);
 }
