@@ -465,7 +465,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) fd_verify_kernel(const Verify
     const Order o = s_order;
     if (o.node < 0) break;
     left.p = target + o.node * v.ts[1];
-    left.q = kDraft ? draft + o.node * v.ds[1] : nullptr;
+    // Where nothing has been refused (c = 0) the draft's row is not read, as a leaf may have none: p, which is at hand, stands
+    // for it (64 sequences of 131072 words: 43.2 us; with q's loads left out by a branch 45.9).
+    left.q = kDraft && o.c_hi != 0.f ? draft + o.node * v.ds[1] : left.p;
     left.c_hi = o.c_hi;
     left.c_lo = o.c_lo;
     left.n_refused = o.n_refused;
