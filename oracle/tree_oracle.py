@@ -57,17 +57,17 @@ def verify(tokens, parents, target, uniforms, draft=None):
         return [], -1
     node, path = 0, [0]
     while True:
-        p = np.maximum(target[node].astype(np.float64), 0.0)
+        p, q = (None if x is None else np.where(x[node] > 0, x[node], 0).astype(np.float64) for x in (target, draft))  # NaN too
         left, mass = p.copy(), 1.0
         for child in [i for i in range(m) if parents[i] == node and i > node]:
             x, u = int(tokens[child]), float(uniforms[child])
-            share = float(draft[node, x]) if draft is not None else 1.0
+            share = float(q[x]) if draft is not None else 1.0
             if u * mass * share < left[x]:
                 path.append(child)
                 node = child
                 break
             if draft is not None:
-                left = np.maximum(left - mass * draft[node].astype(np.float64), 0.0)
+                left = np.maximum(left - mass * q, 0.0)
                 mass = left.sum()
             else:
                 mass -= left[x]

@@ -183,6 +183,14 @@ struct Left {
     }
   }
 
+  // What is not above 0 counts as 0 in the draft's row too (fmaxf gives 0 for NaN).
+  static __device__ __forceinline__ void clean(float (&y)[kGroup<T>]) {
+    if constexpr (kDraft) {
+#pragma unroll
+      for (int e = 0; e < kGroup<T>; ++e) y[e] = fmaxf(y[e], 0.f);
+    }
+  }
+
   // r of group g as sums hi + lo
   __device__ __forceinline__ void group(const float (&x)[kGroup<T>], const float (&y)[kGroup<T>], int32_t g,
                                         float (&hi)[kGroup<T>], float (&lo)[kGroup<T>]) const {
@@ -261,6 +269,7 @@ struct Left {
       } else {
         continue;
       }
+      clean(y);
       if constexpr (!kDraft) refuse(x, g);
 #pragma unroll
       for (int e = 0; e < E; e += 2) add_pair(pack2(x[e], x[e + 1]), pack2(y[e], y[e + 1]), s_hi, s_lo);
@@ -285,6 +294,7 @@ struct Left {
         load_group(p, g, V, off, vec, x);
         if constexpr (kDraft) load_group(q, g, V, off, vec, y);
       }
+      clean(y);
       group(x, y, g, hi, lo);
       Sum own{0.f, 0.f};
 #pragma unroll
@@ -355,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) fd_verify_kernel(const Verify
     s_parent[tid] = child ? up : -1;
     s_token[tid] = x;
     s_p[tid] = child ? fmaxf(at(target + up * v.ts[1], x), 0.f) : 0.f;
-    s_q[tid] = kDraft && child ? at(draft + up * v.ds[1], x) : 0.f;
+    s_q[tid] = kDraft && child ? fmaxf(at(draft + up * v.ds[1], x), 0.f) : 0.f;
   }
   int32_t* path = v.path + (int64_t)b * n;
   if (rank == 0 && tid < n) path[tid] = tid == 0 && m > 0 ? 0 : -1;

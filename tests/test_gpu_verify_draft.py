@@ -69,3 +69,21 @@ def test_the_row_of_a_token_whose_only_child_is_left_out():
     got = c.run(draft=draft)
     assert fd.workspace_status() == fd.fdecode.FD_ERR_BAD_INDEX
     assert all(torch.equal(g, w) for g, w in zip(got, want)) and (got[2] >= 0).all()
+
+
+@pytest.mark.parametrize("V", [3, 601, 5000, 40001])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", ["chain", "random", "wide"])
+@pytest.mark.parametrize("none", [math.nan, -math.inf, -1.0, -1e-30, -0.0])
+def test_what_is_no_draft_probability_counts_as_zero(V, dtype, shape, none):
+    """In a third of the words, those of some children among them."""
+    c = Case(6, 9, V, dtype=dtype, shape=shape, agree=0.7, new_lens=[9, 3, 9, 6, 2, 9], seed=V)
+    out = torch.from_numpy(np.random.default_rng(V).random(c.draft.shape) < 1 / 3).cuda()
+    c.draft[out] = 0.0
+    want = c.want()
+    clean = c.run()
+    c.draft[out] = none
+    got = c.run()
+    assert equal(clean, want) and equal(got, want)
+    c.check(got)  # and the oracle's own reading of such numbers
+    assert fd.workspace_status() == 0
