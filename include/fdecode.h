@@ -409,7 +409,11 @@ typedef struct fd_tree_desc {
  *        padding are not written.  A token that sees no place gives out = 0, lse = -inf.
  *   seq_lens / max_seq_len  L_b, the drafts included, as in fd_decode.
  *   workspace  zero-filled once, fd_tree_workspace_bytes(B, Hq, Hkv, D, n, 0) bytes.
- * Keys and values that a token does not see may be anything, NaN included.  A
+ * Keys and values that a token does not see may be anything, NaN included.  Over a bf16
+ * cache an infinite key that a token sees, or an infinite value before the drafts, may give NaN
+ * where the sums in fp32 give an infinity, or (a key that makes a score of -inf) a number: there q and
+ * the weights are sums of bf16 numbers, some of them 0, and 0 times an infinity is NaN.  It
+ * touches the rows of its sequence and KV head, a value its channel alone.  A
  * parent that is not below its token counts as -1 and is reported as FD_ERR_BAD_INDEX
  * by fd_workspace_status, and so is a page outside the pool, which leaves the
  * sequence's output undefined.  One launch, and a second one that joins the states

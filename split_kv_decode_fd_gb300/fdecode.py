@@ -1060,7 +1060,8 @@ def decode_tree(q, k, v, parents, *, new_lens=None, seq_lens=None, max_seq_len=N
     q ``[B, Hq, n, D]`` fp32, ``n`` up to 64; ``k``, ``v`` are the cache as in ``decode`` (bf16 or fp32).  ``parents``
     ``[B, n]`` int32 (or ``[n]``, one tree for all sequences) gives the number of each token's parent, below its own, or -1; a
     token sees what comes before the drafts, its ancestors and itself.  ``new_lens`` ``[B]``: only the last ``new_lens[b]`` of the
-    ``n`` rows are tokens, numbered from 0 there.  ``seq_lens`` count the drafts.  Calls that may run at the same time
+    ``n`` rows are tokens, numbered from 0 there.  ``seq_lens`` count the drafts.  Over a bf16 cache
+    an infinite key that a token sees, or an infinite value before the drafts, may come out as NaN.  Calls that may run at the same time
     need a ``workspace`` each; without one, each stream has its own (see ``Workspace``).  Returns ``(out [B, Hq, n, D], lse
     [B, Hq, n])``; padding rows keep what ``out`` and ``lse`` hold (zeros when they are made here).
     """
