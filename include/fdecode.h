@@ -417,7 +417,7 @@ typedef struct fd_tree_desc {
  * parent that is not below its token counts as -1 and is reported as FD_ERR_BAD_INDEX
  * by fd_workspace_status, and so is a page outside the pool, which leaves the
  * sequence's output undefined.  One launch, and a second one that joins the states
- * where a sequence may be longer than a tile of 128 keys.
+ * where a sequence may be longer than a tile of 128 keys (64 over an fp32 cache).
  */
 FD_API size_t fd_tree_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_t n, int32_t num_sms);
 FD_API fd_status fd_decode_tree(const float* q, const fd_tree_desc* tree, const fd_kv_desc* kv, float* out, float* lse,
@@ -446,8 +446,10 @@ FD_API fd_status fd_decode_tree(const float* q, const fd_tree_desc* tree, const 
  *   path       [B, n]: the numbers of the tokens that stay, token 0 first, then -1.
  *   count      [B]: how many they are.   next_token [B].  A sequence without tokens gets 0 and -1,
  *              and -1 stands for a target row without a positive probability.
- *   Sums are held to about 48 bits, so that a random number that decides between two words or
- *   on a child is one that is within some 2^-44 of the border before another outcome than that of exact sums is had.
+ *   Sums are pairs of fp32 numbers, of which an accumulator adds up to N = V / 512 + 8 words, in small batches
+ *   V / 4096 + 8.  They are off by at most (N^2 + 128 N + 2000) 2^-48 times the sum of p + c q, and as a rule by
+ *   2^-48 times that for V = 131072 and 2^-42 for 2^22: only a random number that close to the border
+ *   between two words, or to a child's, can have another outcome than exact sums give.
  *   workspace  at least 256 bytes, zero-filled once, of which only the error word is used.
  * A child whose word is outside [0, V), or a token whose parent is not below it, is left out
  * (FD_ERR_BAD_INDEX).  One launch.

@@ -44,9 +44,12 @@ __device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
 }
 
 // Cost units (kTileUnits = 4 a tile of 128 keys) that a piece costs a CTA besides its tiles: q and the first tile's way
-// through the roles, some 4 us or three tiles of 64 rows (64 paged sequences of 512 to 16384 tokens: 252 us with 6, 226 with 12, 230 with 20).
+// through the roles, some 4 us or three tiles of 64 rows.  64 paged sequences of 512 to 16384 tokens, with 6, 12 and 20: 64 rows of a
+// KV head 248, 229, 233 us; 32 rows 186, 189, 192; D = 64, 64 rows 230, 214, 217 and 32 rows 142, 132, 136; with the query rows on the products' rows,
+// 128 of them 312, 308, 316 and 256 626, 620, 655.  One value serves all but 128 rows of D = 64 (238, 254, 254), where a tile is short beside the piece.
 constexpr int kTreePieceUnits = 12;
-// The same of the fp32 kernel, in units of four a tile of 64 keys.
+// The same of the fp32 kernel, in units of four a tile of 64 keys (32 sequences of up to 4096 tokens, with 2, 4 and 8: 64 rows of D = 128
+// 586, 591, 603 us, 32 of D = 64 147, 150, 153).
 constexpr int kTreePieceUnitsCore = 4;
 
 __device__ __forceinline__ int32_t tree_len(const TreeParams& p, int32_t b) {

@@ -73,8 +73,10 @@ struct TreeParams {
 
 // Rows per CTA and CTAs per SM: fp32 caches on CUDA cores; bf16 ones on tensor cores, up to 64 rows of a KV head with the
 // keys on the rows of the products, more in blocks of 128 with the query rows there.  Measured both ways, 131072 keys of 8
-// heads: 64 rows 100 us against 123 (64 paged sequences 238 against 287), 256 rows 334 us against 250.  fp32, 10 rows of 16 KV
-// heads on 2751 to 5502 keys, D = 128: blocks of 16 rows 53 us, of 32 61.
+// heads: 32 rows 89 us against 130, 64 rows 97 against 131 (64 paged sequences 230 against 307), 80 rows 165 us against 136, 256 rows
+// 321 against 257.  A block of 128 costs the same however many of its rows there are: 65 to 128 rows 136 to 140 us, 129 to 256 rows 248 to
+// 257 (blocks of 64 would be even with that from 129 to 192).  fp32, 10 rows of 16 KV heads on 2751 to 5502 keys, D = 128: blocks of 16
+// rows 53 us, of 32 61.
 constexpr int kTreeTileCore = 64;  // keys of a tile of the fp32 kernel
 constexpr int kTreeRowsMma = 128;
 constexpr int tree_rows(bool f32, int rows) {

@@ -16,10 +16,10 @@
 //
 // Bound by memory where the rows are few: with 32 rows 131072 keys stream at 6.4 to 6.7 TB/s; with 64 a tile takes some 2930 cycles,
 // S, softmax, P and O one after another through one place for P, against 2890 at an SM's share of the memory rate.  Measured: 64
-// rows, 131072 keys of 8 heads 95.6 us (5.6 TB/s; 99.4 with P's place given back as one, not the first two parts before the
-// third); 64 paged sequences of 512 to 16384 tokens, 64 rows, 227 us (5.7 TB/s), of
+// rows, 131072 keys of 8 heads 96 us (5.6 TB/s; 4 more with P's place given back as one, not the first two parts before the
+// third); 64 paged sequences of 512 to 16384 tokens, 64 rows, 230 us (5.5 TB/s), of
 // which a piece's start and end are some 4 us together and a CTA has 4 of them.  Code that a piece runs once is rolled: it comes from
-// behind the instruction cache (640 sequences of 512 tokens: 577 us with q's cut and the mask unrolled, 490 so).
+// behind the instruction cache (with q's cut and the mask unrolled the paged sequences took 12 us more; 640 sequences of 512 tokens take 407).
 //
 // A row's reference (what its scores are taken relative to) is the same for all keys, and moves only when a score of a
 // tile exceeds it by 2^kTau: a vote of the threads says so, and then the tile's maxima are found.

@@ -78,7 +78,7 @@ struct Misc {
 };
 static_assert(sizeof(Misc) <= kMiscBytes, "Misc");
 
-// What does not fit the registers spills to L2, as shared memory leaves L1 nothing: 64 rows of 131072 keys took 8 heads
+// What does not fit the registers spills to L2, as shared memory leaves L1 nothing: 64 drafts (256 rows) on 131072 keys took 8 heads
 // 316 us with 168 for every thread, 268 with 200 for those with much to hold, 250 with less code in the loops and S read twice.
 __device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kMoreRegs)); }
 __device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLessRegs)); }

@@ -20,7 +20,7 @@
 // Bound by the latency of the passes over a row (its sum when a child is refused, or at the end), one after
 // another: some 6 us each once few sequences are left, two thirds of it the sum (its arithmetic in dependent steps, two warps a
 // scheduler), the rest the exchange of sums and the walk.
-// Measured: 64 sequences of 16 drafts, 131072 words in fp32, up to five passes, 43.7 us (reading the rows once takes 10); 32
+// Measured: 64 sequences of 16 drafts, 131072 words in fp32, up to five passes, 44 us (reading the rows once takes 10); 32
 // sequences of 32 drafts, 65521 words in bf16, 11.6; one sequence of 8, 32000 words, 8.1.  (All refused words looked for in every
 // group of words 14.2 in place of 11.6; six groups in flight instead of four 45.6 in place of 43.7.)
 //
